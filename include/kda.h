@@ -69,6 +69,8 @@ extern "C" {
 #define KDA_DEVICE_TIMEOUT 2u  /* a bounded wait inside a kernel gave up (a lost async completion); results are incomplete */
 #define KDA_DEVICE_BAD_COUNT 4u /* an accepted-token count was outside [0, T]; that request was skipped */
 #define KDA_DEVICE_BAD_INDEX 8u /* an output row index was outside [0, num_out_tokens); that row was not written */
+#define KDA_DEVICE_NO_PAGES 16u /* a request's new tokens found no page (free list or table row used up) */
+#define KDA_DEVICE_BAD_PAGE 32u /* a page id was outside [0, num_pages); its tokens were left out */
 
 /*
  * Slot id of a padding row.  A batch captured in a CUDA graph for a bucket of
@@ -424,6 +426,107 @@ KDA_API int kda_recurrent_verify_noalloc(const uint16_t *q, const uint16_t *k, c
                                  float scale, int B, int T, int H, const float *state_pool,
                                  int num_slots, const int32_t *slot_ids, uint16_t *out,
                                  int64_t out_token_stride, float *intermediate_states, void *stream);
+
+/* ======================================================================== *
+ * Beside the KDA layers of a hybrid model: the gated delta rule, attention  *
+ * of new tokens over a paged key-value cache, and the tables of a step.     *
+ * The conventions above hold (head_dim 128, caller-owned memory, host-side  *
+ * checks, one stream, the workspace's status word).                         *
+ * ======================================================================== */
+
+/*
+ * The gated delta rule: the delta-rule recurrence of the KDA calls with one
+ * unbounded log-decay per (token, value head) and key heads that value heads
+ * may share.  Per value head h, with key head h / (Hv / Hk):
+ *   q^ = q / sqrt(sum_c q_c^2 + 1e-6),  k^ likewise
+ *   beta = sigmoid(beta_logit),  lambda = -exp(A_log[h]) softplus(a + dt_bias[h])
+ *   S_t = (I - beta k^ k^T) e^lambda S_{t-1} + beta k^ v^T,  o_t = scale S_t^T q^
+ * States are those of the KDA calls ([.., Hv, 128, 128] fp32), so pools, slot
+ * ids, per-step records and kda_commit_accepted (with H = Hv) are shared.
+ *
+ *  q, k          [tokens, Hk, 128] bf16, one token stride qk_token_stride
+ *  v             [tokens, Hv, 128] bf16, token stride v_token_stride (q, k and v
+ *                may lie in one fused projection)
+ *  a, beta_logits [tokens, Hv] bf16, each with its token stride
+ *  A_log, dt_bias [Hv] fp32
+ *  Hv            a multiple of Hk, at most 4096
+ *  scale         finite (else KDA_ERR_UNSUPPORTED)
+ *
+ * kda_gdn_chunk_prefill: chunked varlen prefill; cu_seqlens, state_pool,
+ * slot_ids, flags (KDA_LOAD_INITIAL | KDA_FINAL_TO_POOL), out and final_state
+ * as in kda_chunk_prefill; workspace of kda_gdn_prefill_workspace_size bytes.
+ */
+KDA_API size_t kda_gdn_prefill_workspace_size(int64_t total_tokens, int num_seqs, int Hv);
+
+KDA_API int kda_gdn_chunk_prefill(const uint16_t *q, const uint16_t *k, int64_t qk_token_stride, const uint16_t *v,
+                          int64_t v_token_stride, const uint16_t *a, int64_t a_token_stride,
+                          const uint16_t *beta_logits, int64_t beta_token_stride, const float *A_log,
+                          const float *dt_bias, float scale, const int32_t *cu_seqlens_dev,
+                          const int32_t *cu_seqlens_host, int num_seqs, int Hk, int Hv, float *state_pool,
+                          int num_slots, const int32_t *slot_ids, int flags, uint16_t *out,
+                          int64_t out_token_stride, float *final_state, void *workspace,
+                          size_t workspace_bytes, void *stream);
+
+/*
+ * Speculative verify of the gated delta rule: as kda_recurrent_verify (the
+ * pool is only read, intermediate_states [B, T, Hv, 128, 128] receives the
+ * state after every draft token, KDA_PAD_SLOT_ID rows are skipped,
+ * 1 <= T <= 64).
+ */
+KDA_API int kda_gdn_recurrent_verify(const uint16_t *q, const uint16_t *k, int64_t qk_token_stride,
+                             const uint16_t *v, int64_t v_token_stride, const uint16_t *a, int64_t a_token_stride,
+                             const uint16_t *beta_logits, int64_t beta_token_stride, const float *A_log,
+                             const float *dt_bias, float scale, int B, int T, int Hk, int Hv,
+                             const float *state_pool, int num_slots, const int32_t *slot_ids, uint16_t *out,
+                             int64_t out_token_stride, float *intermediate_states, void *workspace,
+                             size_t workspace_bytes, void *stream);
+
+/*
+ * One token per request of the gated delta rule, the request's state updated
+ * in the pool: request b reads and writes state_pool[slot_ids[b]].  The slot
+ * ids are distinct (padding rows, KDA_PAD_SLOT_ID, excepted: they are skipped,
+ * their output rows left as they were).
+ */
+KDA_API int kda_gdn_decode(const uint16_t *q, const uint16_t *k, int64_t qk_token_stride, const uint16_t *v,
+                   int64_t v_token_stride, const uint16_t *a, int64_t a_token_stride,
+                   const uint16_t *beta_logits, int64_t beta_token_stride, const float *A_log,
+                   const float *dt_bias, float scale, int B, int Hk, int Hv, float *state_pool, int num_slots,
+                   const int32_t *slot_ids, uint16_t *out, int64_t out_token_stride, void *workspace,
+                   size_t workspace_bytes, void *stream);
+
+/*
+ * The tables of one step over a paged cache, built on the GPU from the
+ * requests' lengths.  Request r has seq_lens[r] tokens in the cache and brings
+ * new_lens[r] (any of them may be 0).
+ *
+ *  block_table   [B, table_width] int32, row stride table_row_stride: page ids
+ *                of each request.  The ids of the pages that the new tokens
+ *                begin are written behind those in use; all else is kept.
+ *  free_pages    [num_free] int32: pages are taken from its front, in request
+ *                order; *pages_used (int32) receives how many.
+ *  page_size     tokens per page, >= 1
+ *  max_tokens    rows of positions and slot_map
+ *  cu_seqlens    [B + 1] int32: request r's new tokens are rows
+ *                cu_seqlens[r] .. cu_seqlens[r + 1] - 1 (as the prefill calls take it)
+ *  kv_lens       [B] int32: seq_lens + new_lens (as kda_paged_attention takes it)
+ *  positions     [max_tokens] int32: the row's position in its request
+ *  slot_map      [max_tokens] int64: page id * page_size + position % page_size
+ * Rows behind the last request's (a captured bucket's padding) get position 0
+ * and slot -1.
+ *
+ * Device-side findings, each in the status word: a negative length, or lengths
+ * whose sum passes 2^31 - 1, counts as no new tokens (KDA_DEVICE_BAD_COUNT); new tokens beyond max_tokens
+ * rows have no row (KDA_DEVICE_BAD_COUNT); a request whose pages would not fit its table row, or that
+ * finds the free list used up by the requests before it, keeps its table row and
+ * its kv_lens = seq_lens, and its rows get slot -1 (KDA_DEVICE_NO_PAGES); a
+ * negative page id where a page in use is written to gives slot -1
+ * (KDA_DEVICE_BAD_SLOT).
+ */
+KDA_API int kda_step_tables(int32_t *block_table, int64_t table_row_stride, int table_width,
+                    const int32_t *seq_lens, const int32_t *new_lens, int B, const int32_t *free_pages,
+                    int num_free, int page_size, int64_t max_tokens, int32_t *cu_seqlens, int32_t *kv_lens,
+                    int32_t *positions, int64_t *slot_map, int32_t *pages_used, void *workspace,
+                    size_t workspace_bytes, void *stream);
 
 #ifdef __cplusplus
 }

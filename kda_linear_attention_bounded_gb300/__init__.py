@@ -15,6 +15,12 @@ Optional parts of a layer step, taken by the calls above:
   pool (``conv=``; verify records per-step windows, the commit copies the accepted one);
 * :data:`KDA_PAD_SLOT_ID` -- the slot id of a padding row in a batch captured in a CUDA graph per bucket.
 
+Beside the KDA layers of a hybrid model (the same pools, slot ids, workspaces and errors):
+
+* :func:`gdn_chunk_prefill`, :func:`gdn_recurrent_verify`, :func:`gdn_decode` -- the gated delta rule (one unbounded
+  decay per head, shared key heads): chunked prefill, speculative verify, one token in place;
+* :func:`step_tables` -- page tables and slot maps of a step, built on the GPU from the requests' lengths.
+
 Every call launches only on the given (or current) stream, allocates nothing beyond what the caller passes
 (the wrappers allocate missing outputs and workspaces through torch), and reports device-side problems
 through the workspace's status word (:func:`read_device_status`).
@@ -22,6 +28,7 @@ through the workspace's status word (:func:`read_device_status`).
 The binding is loaded on first use and raises if libkda has not been built.
 """
 from ._binding import (  # noqa: F401
-    KDA_DEVICE_BAD_COUNT, KDA_DEVICE_BAD_INDEX, KDA_DEVICE_BAD_SLOT, KDA_DEVICE_TIMEOUT, KDA_ERR_CUDA, KDA_ERR_INVALID_ARG, KDA_ERR_UNSUPPORTED, KDA_ERR_WORKSPACE,
+    KDA_DEVICE_BAD_COUNT, KDA_DEVICE_BAD_INDEX, KDA_DEVICE_BAD_PAGE, KDA_DEVICE_BAD_SLOT, KDA_DEVICE_NO_PAGES, KDA_DEVICE_TIMEOUT, KDA_ERR_CUDA, KDA_ERR_INVALID_ARG, KDA_ERR_UNSUPPORTED, KDA_ERR_WORKSPACE,
     KDA_FINAL_TO_POOL, KDA_LOAD_INITIAL, KDA_OK, KDA_TWO_PASS, KDA_FUSED, KDA_OVERLAP, KDA_CONV_NONE, KDA_CONV_SILU, KDA_PAD_SLOT_ID, KdaError, OutputNorm, ShortConv, chunk_prefill, commit_accepted, load, make_workspace,
     prefill_schedule, prefill_workspace_size, read_device_status, recurrent_verify, spec_step, status_string, workspace_size)
+from ._hybrid import gdn_chunk_prefill, gdn_decode, gdn_prefill_workspace_size, gdn_recurrent_verify, step_tables  # noqa: F401

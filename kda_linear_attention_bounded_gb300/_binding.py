@@ -26,6 +26,8 @@ KDA_DEVICE_BAD_SLOT = 1
 KDA_DEVICE_TIMEOUT = 2
 KDA_DEVICE_BAD_COUNT = 4
 KDA_DEVICE_BAD_INDEX = 8
+KDA_DEVICE_NO_PAGES = 16
+KDA_DEVICE_BAD_PAGE = 32
 KDA_LOAD_INITIAL = 1
 KDA_FINAL_TO_POOL = 2
 KDA_TWO_PASS = 4
@@ -41,7 +43,8 @@ KDA_SCHEDULE_SPLIT = 3
 #: exported symbols of include/kda.h
 EXPORTS = ("kda_status_string", "kda_workspace_size", "kda_prefill_workspace_size", "kda_workspace_reset",
            "kda_read_device_status", "kda_chunk_prefill", "kda_recurrent_verify", "kda_commit_accepted",
-           "kda_recurrent_verify_noalloc", "kda_spec_step", "kda_prefill_schedule")
+           "kda_recurrent_verify_noalloc", "kda_spec_step", "kda_prefill_schedule", "kda_gdn_prefill_workspace_size",
+           "kda_gdn_chunk_prefill", "kda_gdn_recurrent_verify", "kda_gdn_decode", "kda_step_tables")
 
 _lib = None
 
@@ -165,6 +168,15 @@ def load():
     lib.kda_spec_step.restype = I
     lib.kda_prefill_schedule.argtypes = [P, I, I, I, F, I, SZ, I, P]
     lib.kda_prefill_schedule.restype = I
+    GT = [P, P, I64, P, I64, P, I64, P, I64, P, P, F]   # q, k, v, a, beta_logits, head parameters, scale
+    lib.kda_gdn_prefill_workspace_size.argtypes = [I64, I, I]
+    lib.kda_gdn_prefill_workspace_size.restype = SZ
+    lib.kda_gdn_chunk_prefill.argtypes = GT + [P, P, I, I, I, P, I, P, I, P, I64, P, P, SZ, P]
+    lib.kda_gdn_recurrent_verify.argtypes = GT + [I, I, I, I, P, I, P, P, I64, P, P, SZ, P]
+    lib.kda_gdn_decode.argtypes = GT + [I, I, I, P, I, P, P, I64, P, SZ, P]
+    lib.kda_step_tables.argtypes = [P, I64, I, P, P, I, P, I, I, I64, P, P, P, P, P, P, SZ, P]
+    for name in ("kda_gdn_chunk_prefill", "kda_gdn_recurrent_verify", "kda_gdn_decode", "kda_step_tables"):
+        getattr(lib, name).restype = I
     _lib = lib
     return lib
 

@@ -5,27 +5,17 @@
 #include <cmath>
 #include <cstdint>
 
+#include "kda_checks.h"
 #include "kda_common.cuh"
 #include "kda_internal.h"
 #include "kda_prefill_block.h"
 
 namespace {
 
-constexpr size_t kWorkspaceBytes = 1024;
-static_assert(kda::kDoneCounterOffset + sizeof(uint32_t) <= kWorkspaceBytes,
-              "the spec step's CTA counter must sit in the cleared header");
-static_assert(kda::kSplitCounterOffset >= kda::kDoneCounterOffset + sizeof(uint32_t) &&
-                  kda::kSplitCounterOffset + kda::kMaxSplitCounters * sizeof(uint32_t) <= kWorkspaceBytes,
-              "the split schedule's counters lie in the part kda_workspace_reset clears");
-
-bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-bool good_stride(int64_t stride, int64_t min_elems) { return stride >= min_elems && stride % 8 == 0; }
-
-int check_workspace(const void *ws, size_t bytes) {
-  if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u) != 0 || bytes < kWorkspaceBytes) return KDA_ERR_WORKSPACE;
-  return KDA_OK;
-}
+using kda::aligned16;
+using kda::check_workspace;
+using kda::good_stride;
+using kda::kWorkspaceBytes;
 
 int check_gate(float lower_bound, float scale) {
   if (!std::isfinite(lower_bound) || !std::isfinite(scale)) return KDA_ERR_UNSUPPORTED;

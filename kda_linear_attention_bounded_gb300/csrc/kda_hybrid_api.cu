@@ -1,0 +1,173 @@
+// C ABI of the calls beside the KDA layers (declared in include/kda.h): the gated delta rule, attention over a paged
+// cache, and the step tables.  Host-side validation and launch planning only, by the rules of kda_api.cu: every check
+// that can be made on the host is made before anything is launched, nothing allocates device memory or synchronises.
+#include <climits>
+#include <cmath>
+#include <cstdint>
+
+#include "kda_checks.h"
+#include "kda_common.cuh"
+#include "kda_internal.h"
+
+namespace {
+
+using kda::aligned16;
+using kda::aligned_to;
+using kda::check_workspace;
+using kda::good_stride;
+
+// The tensors of a gated-delta-rule call over `tokens` tokens; fills the token part of `a`.  Without tokens (empty
+// sequences, whose final states are their initial ones) the token tensors may be NULL.
+int check_gdn(int64_t tokens, const uint16_t *q, const uint16_t *k, int64_t qk_stride, const uint16_t *v, int64_t v_stride,
+              const uint16_t *a_in, int64_t a_stride, const uint16_t *beta, int64_t beta_stride, const float *A_log,
+              const float *dt_bias, float scale, int Hk, int Hv, uint16_t *out, int64_t out_stride,
+              kda::GdnRecurrentArgs *a) {
+  if (Hk <= 0 || Hv <= 0 || Hv > 4096 || Hv % Hk != 0) return KDA_ERR_INVALID_ARG;
+  if (!A_log || !dt_bias) return KDA_ERR_INVALID_ARG;
+  if (tokens > 0 && (!q || !k || !v || !a_in || !beta || !out)) return KDA_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out)) return KDA_ERR_INVALID_ARG;
+  if (!aligned_to(a_in, 2) || !aligned_to(beta, 2) || !aligned_to(A_log, 4) || !aligned_to(dt_bias, 4))
+    return KDA_ERR_INVALID_ARG;
+  const int64_t krow = static_cast<int64_t>(Hk) * kda::kD, vrow = static_cast<int64_t>(Hv) * kda::kD;
+  if (!good_stride(qk_stride, krow) || !good_stride(v_stride, vrow) || !good_stride(out_stride, vrow))
+    return KDA_ERR_INVALID_ARG;
+  if (a_stride < Hv || beta_stride < Hv) return KDA_ERR_INVALID_ARG;
+  if (!std::isfinite(scale)) return KDA_ERR_UNSUPPORTED;
+  a->q = q; a->k = k; a->v = v; a->a = a_in; a->beta = beta;
+  a->qk_stride = qk_stride; a->v_stride = v_stride; a->a_stride = a_stride;
+  a->beta_stride = beta_stride; a->out_stride = out_stride;
+  a->A_log = A_log; a->dt_bias = dt_bias;
+  a->scale = scale;
+  a->Hv = Hv; a->group = Hv / Hk;
+  a->out = out;
+  return KDA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t kda_gdn_prefill_workspace_size(int64_t total_tokens, int num_seqs, int Hv) {
+  if (total_tokens < 0 || num_seqs < 0 || Hv <= 0) return 0;
+  return kda::kWorkspaceBytes;
+}
+
+int kda_gdn_chunk_prefill(const uint16_t *q, const uint16_t *k, int64_t qk_token_stride, const uint16_t *v,
+                          int64_t v_token_stride, const uint16_t *a, int64_t a_token_stride,
+                          const uint16_t *beta_logits, int64_t beta_token_stride, const float *A_log,
+                          const float *dt_bias, float scale, const int32_t *cu_seqlens_dev,
+                          const int32_t *cu_seqlens_host, int num_seqs, int Hk, int Hv, float *state_pool,
+                          int num_slots, const int32_t *slot_ids, int flags, uint16_t *out, int64_t out_token_stride,
+                          float *final_state, void *workspace, size_t workspace_bytes, void *stream) {
+  if (int rc = check_workspace(workspace, workspace_bytes)) return rc;
+  if (num_seqs < 0 || !cu_seqlens_dev || !cu_seqlens_host) return KDA_ERR_INVALID_ARG;
+  if (flags & ~(KDA_LOAD_INITIAL | KDA_FINAL_TO_POOL)) return KDA_ERR_INVALID_ARG;
+  if (cu_seqlens_host[0] != 0) return KDA_ERR_INVALID_ARG;
+  for (int n = 0; n < num_seqs; ++n)
+    if (cu_seqlens_host[n + 1] < cu_seqlens_host[n]) return KDA_ERR_INVALID_ARG;
+  if (num_seqs == 0) return KDA_OK;
+  kda::GdnRecurrentArgs r{};
+  if (int rc = check_gdn(cu_seqlens_host[num_seqs], q, k, qk_token_stride, v, v_token_stride, a, a_token_stride, beta_logits,
+                         beta_token_stride, A_log, dt_bias, scale, Hk, Hv, out, out_token_stride, &r))
+    return rc;
+  const bool use_pool = flags & (KDA_LOAD_INITIAL | KDA_FINAL_TO_POOL);
+  if (use_pool && (!state_pool || !slot_ids || num_slots <= 0 || !aligned16(state_pool))) return KDA_ERR_INVALID_ARG;
+  if (!(flags & KDA_FINAL_TO_POOL) && (!final_state || !aligned16(final_state))) return KDA_ERR_INVALID_ARG;
+  if (workspace_bytes < kda_gdn_prefill_workspace_size(cu_seqlens_host[num_seqs], num_seqs, Hv)) return KDA_ERR_WORKSPACE;
+  r.cu_seqlens = cu_seqlens_dev;
+  r.slot_ids = use_pool ? slot_ids : nullptr;
+  r.num_slots = num_slots;
+  r.state_in = (flags & KDA_LOAD_INITIAL) ? state_pool : nullptr;
+  r.state_out_pool = (flags & KDA_FINAL_TO_POOL) ? state_pool : nullptr;
+  r.state_out_dense = (flags & KDA_FINAL_TO_POOL) ? nullptr : final_state;
+  r.status = static_cast<uint32_t *>(workspace);
+  return kda::launch_gdn_recurrent(r, num_seqs, static_cast<cudaStream_t>(stream)) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}
+
+int kda_gdn_recurrent_verify(const uint16_t *q, const uint16_t *k, int64_t qk_token_stride, const uint16_t *v,
+                             int64_t v_token_stride, const uint16_t *a, int64_t a_token_stride,
+                             const uint16_t *beta_logits, int64_t beta_token_stride, const float *A_log,
+                             const float *dt_bias, float scale, int B, int T, int Hk, int Hv,
+                             const float *state_pool, int num_slots, const int32_t *slot_ids, uint16_t *out,
+                             int64_t out_token_stride, float *intermediate_states, void *workspace,
+                             size_t workspace_bytes, void *stream) {
+  if (int rc = check_workspace(workspace, workspace_bytes)) return rc;
+  if (B < 0 || T < 1 || T > 64) return KDA_ERR_INVALID_ARG;
+  if (B == 0) return KDA_OK;
+  kda::GdnRecurrentArgs r{};
+  if (int rc = check_gdn(B, q, k, qk_token_stride, v, v_token_stride, a, a_token_stride, beta_logits,
+                         beta_token_stride, A_log, dt_bias, scale, Hk, Hv, out, out_token_stride, &r))
+    return rc;
+  if (!state_pool || !aligned16(state_pool) || num_slots <= 0 || !slot_ids) return KDA_ERR_INVALID_ARG;
+  if (!intermediate_states || !aligned16(intermediate_states)) return KDA_ERR_INVALID_ARG;
+  r.T = T;
+  r.slot_ids = slot_ids;
+  r.num_slots = num_slots;
+  r.skip_padding = 1;
+  r.state_in = state_pool;
+  r.inter = intermediate_states;
+  r.status = static_cast<uint32_t *>(workspace);
+  return kda::launch_gdn_recurrent(r, B, static_cast<cudaStream_t>(stream)) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}
+
+int kda_gdn_decode(const uint16_t *q, const uint16_t *k, int64_t qk_token_stride, const uint16_t *v,
+                   int64_t v_token_stride, const uint16_t *a, int64_t a_token_stride, const uint16_t *beta_logits,
+                   int64_t beta_token_stride, const float *A_log, const float *dt_bias, float scale, int B, int Hk,
+                   int Hv, float *state_pool, int num_slots, const int32_t *slot_ids, uint16_t *out,
+                   int64_t out_token_stride, void *workspace, size_t workspace_bytes, void *stream) {
+  if (int rc = check_workspace(workspace, workspace_bytes)) return rc;
+  if (B < 0) return KDA_ERR_INVALID_ARG;
+  if (B == 0) return KDA_OK;
+  kda::GdnRecurrentArgs r{};
+  if (int rc = check_gdn(B, q, k, qk_token_stride, v, v_token_stride, a, a_token_stride, beta_logits,
+                         beta_token_stride, A_log, dt_bias, scale, Hk, Hv, out, out_token_stride, &r))
+    return rc;
+  if (!state_pool || !aligned16(state_pool) || num_slots <= 0 || !slot_ids) return KDA_ERR_INVALID_ARG;
+  r.T = 1;
+  r.slot_ids = slot_ids;
+  r.num_slots = num_slots;
+  r.skip_padding = 1;
+  r.state_in = state_pool;
+  r.state_out_pool = state_pool;
+  r.status = static_cast<uint32_t *>(workspace);
+  return kda::launch_gdn_recurrent(r, B, static_cast<cudaStream_t>(stream)) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}
+
+int kda_step_tables(int32_t *block_table, int64_t table_row_stride, int table_width, const int32_t *seq_lens,
+                    const int32_t *new_lens, int B, const int32_t *free_pages, int num_free, int page_size,
+                    int64_t max_tokens, int32_t *cu_seqlens, int32_t *kv_lens, int32_t *positions, int64_t *slot_map,
+                    int32_t *pages_used, void *workspace, size_t workspace_bytes, void *stream) {
+  if (int rc = check_workspace(workspace, workspace_bytes)) return rc;
+  if (B < 0 || num_free < 0 || page_size < 1 || max_tokens < 0 || max_tokens > INT_MAX || table_width < 0)
+    return KDA_ERR_INVALID_ARG;
+  if (B > 0 && (!seq_lens || !new_lens || !kv_lens || (table_width > 0 && !block_table) || table_row_stride < table_width))
+    return KDA_ERR_INVALID_ARG;
+  if (!cu_seqlens || !pages_used || (num_free > 0 && !free_pages)) return KDA_ERR_INVALID_ARG;
+  if (max_tokens > 0 && (!positions || !slot_map)) return KDA_ERR_INVALID_ARG;
+  for (const void *p : {static_cast<const void *>(block_table), static_cast<const void *>(seq_lens),
+                        static_cast<const void *>(new_lens), static_cast<const void *>(free_pages),
+                        static_cast<const void *>(cu_seqlens), static_cast<const void *>(kv_lens),
+                        static_cast<const void *>(positions), static_cast<const void *>(pages_used)})
+    if (!aligned_to(p, 4)) return KDA_ERR_INVALID_ARG;
+  if (!aligned_to(slot_map, 8)) return KDA_ERR_INVALID_ARG;
+  kda::StepTablesArgs t{};
+  t.table = block_table;
+  t.table_stride = table_row_stride;
+  t.width = table_width;
+  t.seq_lens = seq_lens;
+  t.new_lens = new_lens;
+  t.free_pages = free_pages;
+  t.num_free = num_free;
+  t.page = page_size;
+  t.B = B;
+  t.max_tokens = max_tokens;
+  t.cu_seqlens = cu_seqlens;
+  t.kv_lens = kv_lens;
+  t.positions = positions;
+  t.pages_used = pages_used;
+  t.slot_map = slot_map;
+  t.status = static_cast<uint32_t *>(workspace);
+  return kda::launch_step_tables(t, static_cast<cudaStream_t>(stream)) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}
+
+}  // extern "C"

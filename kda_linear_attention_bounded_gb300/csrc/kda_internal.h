@@ -278,4 +278,43 @@ cudaError_t launch_chunk_prefill(const ChunkArgs &args, const int32_t *cu_seqlen
 void describe_prefill_schedule(const ChunkArgs &args, const int32_t *cu_seqlens_host, size_t blocks_bytes, int sms,
                                int info[4]);
 
+// ---------------------------------------------------------------- gated delta rule
+// Arguments of the token-by-token gated delta rule.
+struct GdnRecurrentArgs {
+  const uint16_t *q, *k, *v, *a, *beta;
+  int64_t qk_stride, v_stride, a_stride, beta_stride, out_stride;
+  const float *A_log, *dt_bias;   // [Hv]
+  float scale;
+  int Hv, group;             // value heads; value heads per key head
+  const int32_t *cu_seqlens; // token ranges, or null: items of T tokens
+  int T;
+  const int32_t *slot_ids;   // non-null when a pool is read or written
+  int num_slots;
+  int skip_padding;          // KDA_PAD_SLOT_ID rows are skipped without a status bit
+  const float *state_in;     // pool, or null = zero
+  float *state_out_pool;     // pool, or null
+  float *state_out_dense;    // [items, Hv, D, D], or null
+  float *inter;              // [items, T, Hv, D, D], or null
+  uint16_t *out;
+  uint32_t *status;
+};
+
+cudaError_t launch_gdn_recurrent(const GdnRecurrentArgs &args, int num_items, cudaStream_t stream);
+
+// ---------------------------------------------------------------- step tables
+struct StepTablesArgs {
+  int32_t *table;            // [B, width], row stride table_stride
+  int64_t table_stride;
+  int width;
+  const int32_t *seq_lens, *new_lens;
+  const int32_t *free_pages;
+  int num_free, page, B;
+  int64_t max_tokens;
+  int32_t *cu_seqlens, *kv_lens, *positions, *pages_used;
+  int64_t *slot_map;
+  uint32_t *status;
+};
+
+cudaError_t launch_step_tables(const StepTablesArgs &args, cudaStream_t stream);
+
 }  // namespace kda

@@ -1,0 +1,274 @@
+"""Gated delta rule on the GPU against its 64-bit definition: prefill, verify, decode, and their use together."""
+import pytest
+import torch
+
+import kda_linear_attention_bounded_gb300 as kda
+from hybrid_refs import D, gdn_inputs, gdn_reference, rel_l2
+
+pytestmark = pytest.mark.gpu
+
+# Outputs are bf16: one rounding is at most 2^-8 of a value, so 2^-8 in rel-L2 at the most.  The recurrence runs in
+# fp32: sums of 128 products and a few factors per step, each step's roundings (below 150 x 2^-24 of the state)
+# contracted by the next ones.  The chunked form feeds the tensor cores with pairs of bf16 (a value's rounding is
+# 2^-18 of it): six such roundings meet in a state, 6 x 2^-18 at the most; its outputs take one bf16 rounding of P,
+# of U and of the result, 3 x 2^-8 at the most.
+OUT_STEP = 2.0 ** -8
+STATE_RECURRENT = 150 * 2.0 ** -24
+STATE_CHUNKED = 6 * 2.0 ** -18
+
+
+def _pool(slots, hv, seed):
+    g = torch.Generator().manual_seed(seed)
+    return (0.05 * torch.randn((slots, hv, D, D), generator=g)).cuda()
+
+
+def _i32(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+def _prefill(x, lens, **kw):
+    cu = [0]
+    for n in lens:
+        cu.append(cu[-1] + n)
+    return kda.gdn_chunk_prefill(*x, _i32(cu), torch.tensor(cu, dtype=torch.int32), **kw)
+
+
+@pytest.mark.parametrize("lens,hk,hv", [
+    ([1], 1, 1), ([2], 2, 2), ([63], 1, 2), ([64], 2, 2), ([65], 1, 4), ([128], 1, 1), ([200, 1, 0, 64, 130], 2, 4),
+    ([0, 3], 1, 1), ([517], 3, 3), ([33] * 9, 5, 5)])
+@pytest.mark.parametrize("initial", [False, True])
+def test_prefill(lens, hk, hv, initial):
+    x = gdn_inputs(sum(lens), hk, hv, seed=len(lens) + 100 * hv)
+    pool = _pool(len(lens) + 2, hv, 7)
+    slots = torch.arange(len(lens) + 1, 1, -1, dtype=torch.int32, device="cuda")[:len(lens)].contiguous()
+    before = pool.clone()
+    ws = kda.make_workspace(nbytes=kda.gdn_prefill_workspace_size(sum(lens), len(lens), hv))
+    out, final = _prefill(x, lens, state_pool=pool, slot_ids=slots, load_initial=initial, workspace=ws)
+    torch.cuda.synchronize()
+    assert kda.read_device_status(ws) == 0
+    assert torch.equal(pool, before)
+    ref, _, ref_S = gdn_reference(x, lens, before[slots.long()] if initial else None)
+    assert rel_l2(out, ref) <= 3 * OUT_STEP
+    for n in range(len(lens)):
+        for h in range(hv):
+            assert rel_l2(final[n, h], ref_S[n, h]) <= STATE_CHUNKED, (n, h)
+    # and the final states into the pool, every other slot kept
+    out2, none = _prefill(x, lens, state_pool=pool, slot_ids=slots, load_initial=initial, final_to_pool=True,
+                          workspace=ws)
+    assert none is None and torch.equal(out, out2)
+    assert torch.equal(pool[slots.long()], final)
+    rest = [i for i in range(pool.shape[0]) if i not in slots.tolist()]
+    assert torch.equal(pool[rest], before[rest])
+
+
+@pytest.mark.parametrize("a_mean", [-12.0, 3.0, 60.0, 3000.0])
+def test_prefill_decays(a_mean):
+    # from no decay at all to one that clears the state at every token; e^lambda underflows from about 60 on
+    lens = [150, 70]
+    x = gdn_inputs(sum(lens), 2, 2, seed=11, a_mean=a_mean)
+    pool = _pool(2, 2, 3)
+    out, final = _prefill(x, lens, state_pool=pool, slot_ids=_i32([1, 0]), load_initial=True)
+    ref, _, ref_S = gdn_reference(x, lens, pool[[1, 0]])
+    assert rel_l2(out, ref) <= 3 * OUT_STEP
+    assert rel_l2(final, ref_S) <= STATE_CHUNKED
+
+
+def test_prefill_one_strong_decay_among_weak_ones():
+    # a token that clears the state: pairs of tokens behind it keep their weak decays
+    x = gdn_inputs(190, 1, 2, seed=12, a_mean=-2.0)
+    x[3][20] = 500.0
+    x[3][100] = 80.0
+    out, final = _prefill(x, [190])
+    ref, _, ref_S = gdn_reference(x, [190])
+    assert rel_l2(out, ref) <= 3 * OUT_STEP
+    assert rel_l2(final, ref_S) <= STATE_CHUNKED
+
+
+def test_prefill_equal_keys():
+    # every key the same: the correction matrix is as far from the identity as it gets
+    x = gdn_inputs(256, 1, 1, seed=13, a_mean=-6.0)
+    x[1] = x[1][:1].expand(256, 1, D).contiguous()
+    x[4].fill_(3.0)
+    out, final = _prefill(x, [256])
+    ref, _, ref_S = gdn_reference(x, [256])
+    assert rel_l2(out, ref) <= 3 * OUT_STEP
+    assert rel_l2(final, ref_S) <= STATE_CHUNKED
+
+
+def test_prefill_in_place_from_a_fused_projection():
+    hk, hv, lens = 2, 4, [100, 37]
+    x = gdn_inputs(sum(lens), hk, hv, seed=14)
+    fused = torch.full((sum(lens), (2 * hk + hv) * D + 16), float("nan"), dtype=torch.bfloat16, device="cuda")
+    gates = torch.full((sum(lens), 2 * hv + 3), float("nan"), dtype=torch.bfloat16, device="cuda")
+    views = [fused[:, :hk * D].view(-1, hk, D), fused[:, hk * D:2 * hk * D].view(-1, hk, D),
+             fused[:, 2 * hk * D:(2 * hk + hv) * D].view(-1, hv, D), gates[:, 1:1 + hv], gates[:, 1 + hv:1 + 2 * hv]]
+    for view, src in zip(views, x):
+        view.copy_(src)
+    wide = torch.full((sum(lens), hv * D + 8), 7.0, dtype=torch.bfloat16, device="cuda")
+    out, final = _prefill(views + x[5:], lens, out=wide[:, :hv * D].view(-1, hv, D))
+    dense, final2 = _prefill(x, lens)
+    assert torch.equal(out, dense) and torch.equal(final, final2)
+    assert (wide[:, hv * D:] == 7.0).all()
+
+
+def test_prefill_sequences_do_not_meet():
+    # NaN and infinities in one sequence (and behind the last one) stay there
+    lens = [70, 50, 90]
+    x = gdn_inputs(sum(lens) + 30, 1, 2, seed=15)
+    clean = [t[70:120].clone() if t.shape[0] == sum(lens) + 30 else t for t in x]
+    for t in x[:5]:
+        t[:70] = float("nan")
+        t[120:] = float("inf")
+    out, final = _prefill(x, lens)
+    alone, final1 = _prefill(clean, [50])
+    assert torch.equal(out[70:120], alone) and torch.equal(final[1], final1[0])
+    assert torch.isnan(out[:70]).all() and torch.isnan(final[0]).all()
+
+
+def test_prefill_bad_slot_is_skipped():
+    lens = [20, 30]
+    x = gdn_inputs(50, 1, 1, seed=16)
+    pool = _pool(2, 1, 4)
+    ws = kda.make_workspace(nbytes=kda.gdn_prefill_workspace_size(50, 2, 1))
+    out = torch.full((50, 1, D), 5.0, dtype=torch.bfloat16, device="cuda")
+    final = torch.full((2, 1, D, D), 5.0, device="cuda")
+    _prefill(x, lens, state_pool=pool, slot_ids=_i32([2, 1]), load_initial=True, out=out, final_state=final, workspace=ws)
+    assert kda.read_device_status(ws) == kda.KDA_DEVICE_BAD_SLOT
+    assert (out[:20] == 5.0).all() and (final[0] == 5.0).all()
+    ref, _, ref_S = gdn_reference([t[20:] if t.shape[0] == 50 else t for t in x], [30], pool[1:])
+    assert rel_l2(out[20:], ref) <= 3 * OUT_STEP and rel_l2(final[1], ref_S[0]) <= STATE_CHUNKED
+
+
+@pytest.mark.parametrize("B,T,hk,hv", [(1, 1, 1, 1), (3, 4, 2, 4), (2, 7, 3, 3), (1, 64, 1, 2), (5, 2, 1, 8)])
+def test_verify(B, T, hk, hv):
+    x = gdn_inputs(B * T, hk, hv, seed=B + 10 * T)
+    pool = _pool(B + 1, hv, 5)
+    before = pool.clone()
+    slots = [(2 * b) % (B + 1) for b in range(B)]
+    ws = kda.make_workspace()
+    out, inter = kda.gdn_recurrent_verify(*x, pool, _i32(slots), T, workspace=ws)
+    assert kda.read_device_status(ws) == 0 and torch.equal(pool, before)
+    ref, steps, _ = gdn_reference(x, [T] * B, before[slots])
+    assert rel_l2(out, ref) <= OUT_STEP
+    for b in range(B):
+        assert rel_l2(inter[b], steps[b]) <= STATE_RECURRENT
+
+
+def test_verify_repeated_and_padding_slots():
+    B, T, hv = 5, 3, 2
+    x = gdn_inputs(B * T, 2, hv, seed=21)
+    pool = _pool(3, hv, 6)
+    ws = kda.make_workspace()
+    out = torch.full((B * T, hv, D), 5.0, dtype=torch.bfloat16, device="cuda")
+    inter = torch.full((B, T, hv, D, D), 5.0, device="cuda")
+    kda.gdn_recurrent_verify(*x, pool, _i32([1, -1, 1, 7, 2]), T, out=out, intermediate_states=inter, workspace=ws)
+    assert kda.read_device_status(ws) == kda.KDA_DEVICE_BAD_SLOT   # of the 7 alone
+    ref, steps, _ = gdn_reference(x, [T] * B, pool[[1, 0, 1, 0, 2]])
+    for b in (0, 2, 4):
+        assert rel_l2(out[b * T:(b + 1) * T], ref[b * T:(b + 1) * T]) <= OUT_STEP
+        assert rel_l2(inter[b], steps[b]) <= STATE_RECURRENT
+    for b in (1, 3):
+        assert (out[b * T:(b + 1) * T] == 5.0).all() and (inter[b] == 5.0).all()
+
+
+@pytest.mark.parametrize("B,hk,hv", [(1, 1, 1), (4, 2, 2), (7, 1, 4), (70, 8, 16)])
+def test_decode(B, hk, hv):
+    x = gdn_inputs(B, hk, hv, seed=30 + B)
+    pool = _pool(B + 2, hv, 8)
+    before = pool.clone()
+    slots = list(range(B + 1, 1, -1))
+    if B > 3:
+        slots[2] = -1
+    ws = kda.make_workspace()
+    out = torch.full((B, hv, D), 5.0, dtype=torch.bfloat16, device="cuda")
+    kda.gdn_decode(*x, pool, _i32(slots), out=out, workspace=ws)
+    assert kda.read_device_status(ws) == 0
+    ref, _, ref_S = gdn_reference(x, [1] * B, before[slots])
+    live = [b for b in range(B) if slots[b] >= 0]
+    assert rel_l2(out[live], ref[live]) <= OUT_STEP
+    assert rel_l2(pool[[slots[b] for b in live]], ref_S[live]) <= STATE_RECURRENT
+    rest = [i for i in range(B + 2) if i not in slots]
+    assert torch.equal(pool[rest], before[rest])
+    if B > 3:
+        assert (out[2] == 5.0).all()
+
+
+def test_prefill_decode_verify_commit_together():
+    """A prompt, two decoded tokens, a verified draft of which two tokens are accepted, and one more decoded token:
+    the states and outputs are those of the whole sequence."""
+    hk, hv, T = 1, 2, 4
+    lens = [150, 65]
+    total = [n + 2 + T + 1 for n in lens]
+    x = gdn_inputs(sum(total), hk, hv, seed=40)
+    first = [0, total[0]]
+
+    def rows(lo, hi):
+        idx = torch.cat([torch.arange(f + n + lo, f + n + hi) if lo >= 0 else torch.arange(f, f + n)
+                         for f, n in zip(first, lens)]).cuda()
+        return [t[idx] if t.shape[0] == sum(total) else t for t in x]
+
+    pool = torch.zeros((4, hv, D, D), device="cuda")
+    slots = _i32([3, 1])
+    ws = kda.make_workspace(nbytes=kda.gdn_prefill_workspace_size(sum(lens), 2, hv))
+    outs = [_prefill(rows(-1, 0), lens, state_pool=pool, slot_ids=slots, final_to_pool=True, workspace=ws)[0]]
+    for t in range(2):
+        outs.append(kda.gdn_decode(*rows(t, t + 1), pool, slots, workspace=ws))
+    vout, inter = kda.gdn_recurrent_verify(*rows(2, 2 + T), pool, slots, T, workspace=ws)
+    kda.commit_accepted(pool, slots, _i32([2, 2]), inter, workspace=ws)
+    after = [torch.arange(f + n + 4, f + n + 5) for f, n in zip(first, lens)]   # the token behind the accepted two
+    nxt = [t[torch.cat(after).cuda()] if t.shape[0] == sum(total) else t for t in x]
+    last = kda.gdn_decode(*nxt, pool, slots, workspace=ws)
+    assert kda.read_device_status(ws) == 0
+    ref, steps, _ = gdn_reference(x, total)
+    for i, (f, n) in enumerate(zip(first, lens)):
+        p0 = sum(lens[:i])
+        assert rel_l2(outs[0][p0:p0 + n], ref[f:f + n]) <= 3 * OUT_STEP
+        for t in range(2):
+            assert rel_l2(outs[1 + t][i], ref[f + n + t]) <= 2 * OUT_STEP
+        assert rel_l2(vout[i * T:(i + 1) * T], ref[f + n + 2:f + n + 2 + T]) <= 2 * OUT_STEP
+        assert rel_l2(last[i], ref[f + n + 4]) <= 2 * OUT_STEP
+        assert rel_l2(pool[int(slots[i])], steps[i][n + 4]) <= STATE_CHUNKED
+
+
+def test_graph_replay_and_other_stream():
+    lens, hv = [100, 30], 2
+    x = gdn_inputs(sum(lens), 1, hv, seed=50)
+    cu = [0, 100, 130]
+    cu_d, cu_h = _i32(cu), torch.tensor(cu, dtype=torch.int32)
+    ws = kda.make_workspace(nbytes=kda.gdn_prefill_workspace_size(130, 2, hv))
+    out = torch.zeros((130, hv, D), dtype=torch.bfloat16, device="cuda")
+    final = torch.zeros((2, hv, D, D), device="cuda")
+    pool, slots = _pool(4, hv, 9), _i32([2, 0])
+    dec = [t[:2].clone() if t.shape[0] == 130 else t for t in x]
+    dout = torch.zeros((2, hv, D), dtype=torch.bfloat16, device="cuda")
+
+    def step(stream=None):
+        kda.gdn_chunk_prefill(*x, cu_d, cu_h, out=out, final_state=final, workspace=ws, stream=stream)
+        kda.gdn_decode(*dec, pool, slots, out=dout, workspace=ws, stream=stream)
+
+    before = pool.clone()
+    step()
+    torch.cuda.synchronize()
+    want = [out.clone(), final.clone(), dout.clone(), pool.clone()]
+    pool.copy_(before)
+    graph = torch.cuda.CUDAGraph()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        step()   # once outside the capture on its stream
+        torch.cuda.synchronize()
+        with torch.cuda.graph(graph, stream=side):
+            step()
+    for _ in range(2):
+        for t in (out, final, dout):
+            t.zero_()
+        pool.copy_(before)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(want, (out, final, dout, pool)))
+    for t in (out, final, dout):
+        t.zero_()
+    pool.copy_(before)
+    side.wait_stream(torch.cuda.current_stream())
+    step(stream=side)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(want, (out, final, dout, pool)))

@@ -1,0 +1,120 @@
+"""Refusals of the calls beside the KDA layers, on the host (fake, aligned device addresses; never dereferenced) and
+in the Python wrappers (CPU tensors)."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+from kda_linear_attention_bounded_gb300 import build as kbuild
+
+FAKE = 0x10000000
+P = ctypes.c_void_p
+
+
+@pytest.fixture(scope="module")
+def lib():
+    kbuild.build()
+    from kda_linear_attention_bounded_gb300 import _binding
+    return _binding.load()
+
+
+def _head(hk=2, hv=4, q=FAKE, qs=None, v=FAKE, vs=None, a=FAKE, as_=None, beta=FAKE, A_log=FAKE, scale=0.1):
+    return [P(q), P(FAKE), hk * 128 if qs is None else qs, P(v), hv * 128 if vs is None else vs, P(a),
+            hv if as_ is None else as_, P(beta), hv, P(A_log), P(FAKE), scale], hk, hv
+
+
+def _prefill(lib, *, cu=(0, 70), pool=None, slots=None, nslots=0, flags=0, out=FAKE, os_=None, final=FAKE, ws=FAKE,
+             ws_bytes=None, **kw):
+    head, hk, hv = _head(**kw)
+    cu_host = np.array(cu, np.int32)
+    if ws_bytes is None:
+        ws_bytes = max(1024, lib.kda_gdn_prefill_workspace_size(max(int(cu[-1]), 0), len(cu) - 1, max(hv, 1)))
+    return lib.kda_gdn_chunk_prefill(*head, P(FAKE), cu_host.ctypes.data_as(P), len(cu) - 1, hk, hv, P(pool), nslots,
+                                     P(slots), flags, P(out), hv * 128 if os_ is None else os_, P(final), P(ws),
+                                     ws_bytes, None)
+
+
+BAD_TOKENS = [dict(hk=0), dict(hv=0), dict(hk=3), dict(hv=8192, hk=1), dict(q=None), dict(q=FAKE + 2),
+              dict(v=None), dict(v=FAKE + 8), dict(a=None), dict(a=FAKE + 1), dict(beta=None), dict(A_log=None),
+              dict(A_log=FAKE + 2), dict(qs=100), dict(qs=260), dict(qs=0), dict(vs=256), dict(vs=516), dict(as_=3)]
+
+
+def test_gdn_prefill_refusals(lib):
+    for bad in BAD_TOKENS:
+        assert _prefill(lib, **bad) == 1, bad
+    assert _prefill(lib, scale=float("nan")) == 2
+    assert _prefill(lib, scale=float("inf")) == 2
+    assert _prefill(lib, ws=None) == 3
+    assert _prefill(lib, ws=FAKE + 64) == 3
+    assert _prefill(lib, ws_bytes=1024 - 1) == 3
+    assert _prefill(lib, cu=(0, 70, 60)) == 1
+    assert _prefill(lib, cu=(2, 70)) == 1
+    assert _prefill(lib, flags=4) == 1                 # the KDA calls' execution paths are not this call's
+    assert _prefill(lib, flags=1) == 1                 # pool and slot ids required
+    assert _prefill(lib, flags=2, pool=FAKE, slots=FAKE, nslots=0) == 1
+    assert _prefill(lib, flags=2, pool=FAKE + 4, slots=FAKE, nslots=2) == 1
+    assert _prefill(lib, final=None) == 1
+    assert _prefill(lib, out=None) == 1
+    assert _prefill(lib, os_=500) == 1
+    assert _prefill(lib, cu=(0,)) == 0                 # no sequences: nothing to do
+
+
+def _verify(lib, *, B=2, T=4, pool=FAKE, nslots=4, slots=FAKE, out=FAKE, inter=FAKE, ws=FAKE, ws_bytes=1024, **kw):
+    head, hk, hv = _head(**kw)
+    return lib.kda_gdn_recurrent_verify(*head, B, T, hk, hv, P(pool), nslots, P(slots), P(out), hv * 128, P(inter),
+                                        P(ws), ws_bytes, None)
+
+
+def _decode(lib, *, B=2, pool=FAKE, nslots=4, slots=FAKE, out=FAKE, ws=FAKE, ws_bytes=1024, **kw):
+    head, hk, hv = _head(**kw)
+    return lib.kda_gdn_decode(*head, B, hk, hv, P(pool), nslots, P(slots), P(out), hv * 128, P(ws), ws_bytes, None)
+
+
+@pytest.mark.parametrize("call", [_verify, _decode])
+def test_gdn_recurrent_refusals(lib, call):
+    for bad in BAD_TOKENS:
+        assert call(lib, **bad) == 1, bad
+    assert call(lib, scale=float("nan")) == 2
+    for bad in (dict(B=-1), dict(pool=None), dict(pool=FAKE + 4), dict(nslots=0), dict(slots=None), dict(out=None),
+                dict(out=FAKE + 8)):
+        assert call(lib, **bad) == 1, bad
+    for bad in (dict(ws=None), dict(ws=FAKE + 16), dict(ws_bytes=512)):
+        assert call(lib, **bad) == 3, bad
+    assert call(lib, B=0) == 0
+    if call is _verify:
+        assert call(lib, T=0) == 1 and call(lib, T=65) == 1 and call(lib, inter=None) == 1
+
+
+def _tables(lib, *, table=FAKE, stride=8, width=8, old=FAKE, new=FAKE, B=4, free=FAKE, num_free=5, page=16, rows=10,
+            cu=FAKE, kv=FAKE, pos=FAKE, slot=FAKE, used=FAKE, ws=FAKE, ws_bytes=1024):
+    return lib.kda_step_tables(P(table), stride, width, P(old), P(new), B, P(free), num_free, page, rows, P(cu), P(kv),
+                               P(pos), P(slot), P(used), P(ws), ws_bytes, None)
+
+
+def test_step_tables_refusals(lib):
+    for bad in (dict(table=None), dict(stride=7), dict(old=None), dict(new=None), dict(B=-1), dict(free=None),
+                dict(num_free=-1), dict(page=0), dict(page=-16), dict(rows=-1), dict(rows=2 ** 31), dict(cu=None),
+                dict(kv=None), dict(pos=None), dict(slot=None), dict(used=None), dict(width=-1), dict(table=FAKE + 2),
+                dict(slot=FAKE + 4), dict(cu=FAKE + 1)):
+        assert _tables(lib, **bad) == 1, bad
+    for bad in (dict(ws=None), dict(ws=FAKE + 16), dict(ws_bytes=512)):
+        assert _tables(lib, **bad) == 3, bad
+
+
+def test_wrappers_refuse_host_tensors(lib):
+    import kda_linear_attention_bounded_gb300 as kda
+    q = torch.zeros((2, 1, 128), dtype=torch.bfloat16)
+    g = torch.zeros((2, 1), dtype=torch.bfloat16)
+    h = torch.zeros(1)
+    pool, slots = torch.zeros((2, 1, 128, 128)), torch.zeros(2, dtype=torch.int32)
+    with pytest.raises(ValueError, match="CUDA"):
+        kda.gdn_decode(q, q, q, g, g, h, h, pool, slots)
+    with pytest.raises(ValueError, match="CUDA"):
+        kda.gdn_recurrent_verify(q, q, q, g, g, h, h, pool, slots, 1)
+    with pytest.raises(ValueError, match="CUDA"):
+        kda.gdn_chunk_prefill(q, q, q, g, g, h, h, slots, slots)
+    z = torch.zeros(3, dtype=torch.int32)
+    with pytest.raises(ValueError, match="CUDA"):
+        kda.step_tables(z[:2].view(1, 2), z[:1], z[:1], z, 16, cu_seqlens=z[:2], kv_lens=z[:1], positions=z,
+                        slot_map=z.long(), pages_used=z[:1])

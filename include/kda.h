@@ -495,6 +495,43 @@ KDA_API int kda_gdn_decode(const uint16_t *q, const uint16_t *k, int64_t qk_toke
                    size_t workspace_bytes, void *stream);
 
 /*
+ * Attention of each request's T new tokens over its tokens in a paged cache
+ * (T = 1: plain decoding; T > 1: a verified draft, causal among its tokens).
+ * With n = seq_lens[b] tokens in the cache, the T new ones last, new token t
+ * of query head hq attends, in key head hq / (Hq / Hk), to tokens 0 .. n - T + t:
+ *   out = sum_j p_j v_j,  p = softmax(scale q . k_j),  lse = log sum_j e^(scale q . k_j)
+ *
+ *  q             [B*T, Hq, 128] bf16, token stride q_token_stride
+ *  k_pages, v_pages [num_pages, page_size, Hk, 128] bf16 with any page, token and
+ *                head strides (elements, >= 0, multiples of 8): pages of tokens or
+ *                of heads, K and V in one buffer or two
+ *  block_table   [B, table_width] int32, row stride table_row_stride; only the
+ *                ceil(n / page_size) ids in use are read
+ *  seq_lens      [B] int32, the new tokens included.  0 marks a padding row.  A row
+ *                that sees no token (n - T + t < 0) gets zeros and lse = -inf.
+ *  Hq            a multiple of Hk, at most 4096;  1 <= T <= 64;  page_size >= 1
+ *  out           [B*T, Hq, 128] bf16, token stride out_token_stride
+ *  lse           [B*T, Hq] fp32 (natural logarithm), or NULL
+ *  workspace     kda_paged_workspace_size(Hq, Hk, T) bytes; no part of it needs
+ *                clearing.  Concurrent calls need separate workspaces.
+ *
+ * Device-side findings: a length below 0 or above table_width * page_size counts
+ * as 0 (KDA_DEVICE_BAD_COUNT); a page id outside [0, num_pages) leaves its
+ * tokens out (KDA_DEVICE_BAD_PAGE).  Tokens a row does not see never reach it,
+ * whatever they hold.  Results do not depend on timing: the work is split by the
+ * lengths alone and joined in the order of the tokens.
+ */
+KDA_API size_t kda_paged_workspace_size(int Hq, int Hk, int T);
+
+KDA_API int kda_paged_attention(const uint16_t *q, int64_t q_token_stride, const uint16_t *k_pages,
+                        int64_t k_page_stride, int64_t k_token_stride, int64_t k_head_stride,
+                        const uint16_t *v_pages, int64_t v_page_stride, int64_t v_token_stride,
+                        int64_t v_head_stride, int num_pages, int page_size, const int32_t *block_table,
+                        int64_t table_row_stride, int table_width, const int32_t *seq_lens, int B, int T,
+                        int Hq, int Hk, float scale, uint16_t *out, int64_t out_token_stride, float *lse,
+                        void *workspace, size_t workspace_bytes, void *stream);
+
+/*
  * The tables of one step over a paged cache, built on the GPU from the
  * requests' lengths.  Request r has seq_lens[r] tokens in the cache and brings
  * new_lens[r] (any of them may be 0).

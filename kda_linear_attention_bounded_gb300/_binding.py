@@ -44,7 +44,8 @@ KDA_SCHEDULE_SPLIT = 3
 EXPORTS = ("kda_status_string", "kda_workspace_size", "kda_prefill_workspace_size", "kda_workspace_reset",
            "kda_read_device_status", "kda_chunk_prefill", "kda_recurrent_verify", "kda_commit_accepted",
            "kda_recurrent_verify_noalloc", "kda_spec_step", "kda_prefill_schedule", "kda_gdn_prefill_workspace_size",
-           "kda_gdn_chunk_prefill", "kda_gdn_recurrent_verify", "kda_gdn_decode", "kda_step_tables")
+           "kda_gdn_chunk_prefill", "kda_gdn_recurrent_verify", "kda_gdn_decode", "kda_step_tables",
+           "kda_paged_workspace_size", "kda_paged_attention")
 
 _lib = None
 
@@ -175,7 +176,12 @@ def load():
     lib.kda_gdn_recurrent_verify.argtypes = GT + [I, I, I, I, P, I, P, P, I64, P, P, SZ, P]
     lib.kda_gdn_decode.argtypes = GT + [I, I, I, P, I, P, P, I64, P, SZ, P]
     lib.kda_step_tables.argtypes = [P, I64, I, P, P, I, P, I, I, I64, P, P, P, P, P, P, SZ, P]
-    for name in ("kda_gdn_chunk_prefill", "kda_gdn_recurrent_verify", "kda_gdn_decode", "kda_step_tables"):
+    lib.kda_paged_workspace_size.argtypes = [I, I, I]
+    lib.kda_paged_workspace_size.restype = SZ
+    lib.kda_paged_attention.argtypes = [P, I64, P, I64, I64, I64, P, I64, I64, I64, I, I, P, I64, I, P, I, I, I, I, F, P,
+                                        I64, P, P, SZ, P]
+    for name in ("kda_gdn_chunk_prefill", "kda_gdn_recurrent_verify", "kda_gdn_decode", "kda_step_tables",
+                 "kda_paged_attention"):
         getattr(lib, name).restype = I
     _lib = lib
     return lib

@@ -192,6 +192,60 @@ def gdn_decode(q, k, v, a, beta_logits, A_log, dt_bias, state_pool, slot_ids, *,
     return out
 
 
+def paged_workspace_size(Hq: int, Hk: int, T: int = 1) -> int:
+    """Bytes of workspace ``paged_attention`` needs (whatever the batch and the lengths)."""
+    return int(_b.load().kda_paged_workspace_size(int(Hq), int(Hk), int(T)))
+
+
+def _pages(x, name, dev):
+    """bf16 ``[pages, page_size, Hk, 128]``, channels contiguous; returns its shape and strides."""
+    sh, st = x.shape, x.stride()
+    if x.dtype != _BF16 or x.device != dev or len(sh) != 4 or sh[3] != 128 or st[3] != 1:
+        raise ValueError(f"{name}: expected a bf16 tensor [pages, page_size, Hk, 128] on {dev}, channels contiguous")
+    return sh, [0 if n == 1 else x for n, x in zip(sh, st)]
+
+
+def paged_attention(q, k_pages, v_pages, block_table, seq_lens, T=1, *, scale=None, out=None, lse=None,
+                    workspace=None, stream=None):
+    """``kda_paged_attention``: every request's T new tokens over its tokens in the paged cache.
+
+    q: bf16 ``[B*T, Hq, 128]``; k_pages, v_pages: bf16 ``[pages, page_size, Hk, 128]`` with any page, token and head
+    strides; block_table: int32 ``[B, width]``; seq_lens: int32 ``[B]``, the new tokens included (0: a padding row).
+    lse: optional fp32 ``[B*T, Hq]`` to write.  Returns ``(out, lse)``."""
+    lib = _b.load()
+    dev = _cuda(q, "q")
+    T = int(T)
+    B = seq_lens.numel()
+    if q.dim() != 3:
+        raise ValueError("q: expected a bf16 tensor [B*T, Hq, 128]")
+    Hq = q.shape[1]
+    qs = _tokens(q, "q", dev, B * T, Hq)
+    sh, ks = _pages(k_pages, "k_pages", dev)
+    vsh, vs = _pages(v_pages, "v_pages", dev)
+    if sh != vsh:
+        raise ValueError("k_pages and v_pages must have one shape")
+    if block_table.dtype != _I32 or block_table.device != dev or block_table.dim() != 2 or block_table.shape[0] != B or \
+            (block_table.shape[1] > 1 and block_table.stride(1) != 1):
+        raise ValueError(f"block_table: expected an int32 tensor [{B}, width] on {dev} with contiguous rows")
+    width = block_table.shape[1]
+    lens = _check(seq_lens, "seq_lens", _I32, dev, (B,))
+    lse_ptr = None if lse is None else _check(lse, "lse", _F32, dev, (B * T, Hq))
+    with _device_guard(dev):
+        out, os_ = _out_rows(out, dev, B * T, Hq)
+        if workspace is None:
+            workspace = _b.make_workspace(dev, stream, paged_workspace_size(Hq, sh[2], T))
+        else:
+            _workspace(workspace, dev, stream, 0)
+        rc = lib.kda_paged_attention(
+            q.data_ptr(), qs, k_pages.data_ptr(), ks[0], ks[1], ks[2], v_pages.data_ptr(), vs[0], vs[1], vs[2], sh[0],
+            sh[1], block_table.data_ptr(), block_table.stride(0) if B > 1 else width, width, lens, B, T, Hq, sh[2],
+            _SCALE if scale is None else float(scale), out.data_ptr(), os_, lse_ptr, workspace.data_ptr(),
+            workspace.numel(), _stream(stream, dev))
+    if rc != KDA_OK:
+        raise KdaError(rc, "kda_paged_attention")
+    return out, lse
+
+
 def step_tables(block_table, seq_lens, new_lens, free_pages, page_size, *, cu_seqlens, kv_lens, positions, slot_map,
                 pages_used, workspace=None, stream=None):
     """``kda_step_tables``: page tables and slot maps of one step from the requests' lengths, all on the GPU.

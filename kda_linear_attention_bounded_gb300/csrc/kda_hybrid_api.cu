@@ -133,6 +133,61 @@ int kda_gdn_decode(const uint16_t *q, const uint16_t *k, int64_t qk_token_stride
   return kda::launch_gdn_recurrent(r, B, static_cast<cudaStream_t>(stream)) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 
+size_t kda_paged_workspace_size(int Hq, int Hk, int T) {
+  if (Hk <= 0 || Hq <= 0 || Hq % Hk != 0 || T < 1) return 0;
+  const int64_t rows = static_cast<int64_t>(Hq / Hk) * T;
+  const size_t per = kda::paged_rows_per_item(static_cast<int>(rows < 64 ? rows : 64));
+  const size_t joins = kda::kPagedMaxCtas * sizeof(int4);
+  return (kda::kWorkspaceBytes + joins + 2 * kda::kPagedMaxCtas * per * kda::kPagedPartFloats * sizeof(float) + 255) &
+         ~size_t(255);
+}
+
+int kda_paged_attention(const uint16_t *q, int64_t q_token_stride, const uint16_t *k_pages, int64_t k_page_stride,
+                        int64_t k_token_stride, int64_t k_head_stride, const uint16_t *v_pages, int64_t v_page_stride,
+                        int64_t v_token_stride, int64_t v_head_stride, int num_pages, int page_size,
+                        const int32_t *block_table, int64_t table_row_stride, int table_width,
+                        const int32_t *seq_lens, int B, int T, int Hq, int Hk, float scale, uint16_t *out,
+                        int64_t out_token_stride, float *lse, void *workspace, size_t workspace_bytes, void *stream) {
+  if (int rc = check_workspace(workspace, workspace_bytes)) return rc;
+  if (B < 0 || T < 1 || T > 64) return KDA_ERR_INVALID_ARG;
+  if (Hk <= 0 || Hq <= 0 || Hq > 4096 || Hq % Hk != 0) return KDA_ERR_INVALID_ARG;
+  if (page_size < 1 || num_pages < 0 || table_width < 0 || table_row_stride < table_width) return KDA_ERR_INVALID_ARG;
+  if (!std::isfinite(scale)) return KDA_ERR_UNSUPPORTED;
+  if (B == 0) return KDA_OK;
+  if (static_cast<int64_t>(B) * T > INT_MAX) return KDA_ERR_INVALID_ARG;
+  if (!q || !seq_lens || !out || !aligned16(q) || !aligned16(out) || !aligned_to(seq_lens, 4) || !aligned_to(lse, 4))
+    return KDA_ERR_INVALID_ARG;
+  if (table_width > 0 && (!block_table || !aligned_to(block_table, 4))) return KDA_ERR_INVALID_ARG;
+  if (num_pages > 0 && (!k_pages || !v_pages || !aligned16(k_pages) || !aligned16(v_pages))) return KDA_ERR_INVALID_ARG;
+  const int64_t row = static_cast<int64_t>(Hq) * kda::kD;
+  if (!good_stride(q_token_stride, row) || !good_stride(out_token_stride, row)) return KDA_ERR_INVALID_ARG;
+  for (int64_t s : {k_page_stride, k_token_stride, k_head_stride, v_page_stride, v_token_stride, v_head_stride})
+    if (!good_stride(s, 0)) return KDA_ERR_INVALID_ARG;
+  if (workspace_bytes < kda_paged_workspace_size(Hq, Hk, T)) return KDA_ERR_WORKSPACE;
+  kda::PagedArgs a{};
+  a.q = q; a.k = k_pages; a.v = v_pages;
+  a.q_stride = q_token_stride;
+  a.k_page_stride = k_page_stride; a.k_token_stride = k_token_stride; a.k_head_stride = k_head_stride;
+  a.v_page_stride = v_page_stride; a.v_token_stride = v_token_stride; a.v_head_stride = v_head_stride;
+  a.num_pages = num_pages;
+  a.page = page_size;
+  a.table = block_table;
+  a.table_stride = table_row_stride;
+  const int64_t most = static_cast<int64_t>(table_width) * page_size;
+  a.max_len = static_cast<int>(most < INT_MAX - 64 ? most : INT_MAX - 64);
+  a.seq_lens = seq_lens;
+  a.B = B; a.T = T; a.Hk = Hk; a.G = Hq / Hk;
+  a.scale = scale;
+  a.out = out;
+  a.out_stride = out_token_stride;
+  a.lse = lse;
+  uint8_t *ws = static_cast<uint8_t *>(workspace);
+  a.joins = reinterpret_cast<int4 *>(ws + kda::kWorkspaceBytes);
+  a.parts = reinterpret_cast<float *>(ws + kda::kWorkspaceBytes + kda::kPagedMaxCtas * sizeof(int4));
+  a.status = static_cast<uint32_t *>(workspace);
+  return kda::launch_paged_attention(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}
+
 int kda_step_tables(int32_t *block_table, int64_t table_row_stride, int table_width, const int32_t *seq_lens,
                     const int32_t *new_lens, int B, const int32_t *free_pages, int num_free, int page_size,
                     int64_t max_tokens, int32_t *cu_seqlens, int32_t *kv_lens, int32_t *positions, int64_t *slot_map,

@@ -301,6 +301,32 @@ struct GdnRecurrentArgs {
 
 cudaError_t launch_gdn_recurrent(const GdnRecurrentArgs &args, int num_items, cudaStream_t stream);
 
+// ---------------------------------------------------------------- paged attention
+constexpr int kPagedMaxCtas = 304;      // stretches of work at most (two CTAs on each of 152 SMs)
+constexpr int kPagedPartFloats = 132;   // a part of a row: 128 sums, the maximum, the sum of weights, padding
+struct PagedArgs {
+  const uint16_t *q, *k, *v;
+  int64_t q_stride;                                        // tokens of q (heads contiguous)
+  int64_t k_page_stride, k_token_stride, k_head_stride;    // elements
+  int64_t v_page_stride, v_token_stride, v_head_stride;
+  int num_pages, page;
+  const int32_t *table;
+  int64_t table_stride;
+  int max_len;                                             // tokens that a table row holds
+  const int32_t *seq_lens;
+  int B, T, Hk, G, row_blocks;                             // G: query heads per key head
+  float scale;
+  uint16_t *out;
+  int64_t out_stride;
+  float *lse;                                              // [B T, Hk G], or null
+  float *parts;
+  int4 *joins;                                             // one per CTA; null: no item can be cut
+  uint32_t *status;
+};
+// Rows (query heads x new tokens of a key head) that one CTA takes, for `rows` of them.
+int paged_rows_per_item(int rows);
+cudaError_t launch_paged_attention(const PagedArgs &args, cudaStream_t stream);
+
 // ---------------------------------------------------------------- step tables
 struct StepTablesArgs {
   int32_t *table;            // [B, width], row stride table_stride

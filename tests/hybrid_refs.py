@@ -49,3 +49,26 @@ def rel_l2(x, ref):
     x, ref = x.detach().double().cpu(), ref.double().cpu()
     den = ref.norm()
     return float((x - ref).norm() / den) if den > 0 else float((x - ref).norm())
+
+
+def paged_reference(q, k_pages, v_pages, table, lens, T, scale=D ** -0.5):
+    """(out [B*T, Hq, D], lse [B*T, Hq]) in fp64: request by request, row by row."""
+    q, k_pages, v_pages = (t.detach().double().cpu() for t in (q, k_pages, v_pages))
+    table, page, hk = table.cpu(), k_pages.shape[1], k_pages.shape[2]
+    hq = q.shape[1]
+    out = torch.zeros((q.shape[0], hq, D), dtype=torch.float64)
+    lse = torch.full((q.shape[0], hq), -math.inf, dtype=torch.float64)
+    for b, n in enumerate(lens):
+        pos = torch.arange(max(n, 0))
+        at = table[b].long()[pos // page] if n > 0 else pos
+        k, v = k_pages[at, pos % page], v_pages[at, pos % page]
+        for t in range(T):
+            seen = n - T + t + 1
+            if seen <= 0:
+                continue
+            for h in range(hk):
+                mine = slice(h * (hq // hk), (h + 1) * (hq // hk))
+                z = scale * (q[b * T + t, mine] @ k[:seen, h].T)
+                lse[b * T + t, mine] = torch.logsumexp(z, -1)
+                out[b * T + t, mine] = torch.softmax(z, -1) @ v[:seen, h]
+    return out, lse

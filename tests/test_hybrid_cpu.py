@@ -118,3 +118,34 @@ def test_wrappers_refuse_host_tensors(lib):
     with pytest.raises(ValueError, match="CUDA"):
         kda.step_tables(z[:2].view(1, 2), z[:1], z[:1], z, 16, cu_seqlens=z[:2], kv_lens=z[:1], positions=z,
                         slot_map=z.long(), pages_used=z[:1])
+
+
+def _paged(lib, *, q=FAKE, qs=1024, k=FAKE, kps=4096, kts=256, khs=128, v=FAKE, vps=4096, num_pages=9, page=16,
+           table=FAKE, ts=4, width=4, lens=FAKE, B=2, T=1, hq=8, hk=2, scale=0.1, out=FAKE, os_=1024, lse=None, ws=FAKE,
+           ws_bytes=None):
+    if ws_bytes is None:
+        ws_bytes = max(1024, lib.kda_paged_workspace_size(hq, hk, T))
+    return lib.kda_paged_attention(P(q), qs, P(k), kps, kts, khs, P(v), vps, kts, khs, num_pages, page, P(table), ts, width,
+                                   P(lens), B, T, hq, hk, scale, P(out), os_, P(lse), P(ws), ws_bytes, None)
+
+
+def test_paged_refusals(lib):
+    for bad in (dict(q=None), dict(q=FAKE + 8), dict(qs=1016), dict(qs=1028), dict(k=None), dict(v=None),
+                dict(k=FAKE + 4), dict(kps=-8), dict(kps=4), dict(kts=130), dict(khs=-128), dict(num_pages=-1),
+                dict(page=0), dict(table=None), dict(table=FAKE + 2), dict(ts=3), dict(width=-1), dict(lens=None),
+                dict(lens=FAKE + 2), dict(B=-1), dict(T=0), dict(T=65), dict(hk=0), dict(hk=3), dict(hq=0),
+                dict(hq=8192), dict(out=None), dict(out=FAKE + 4), dict(os_=1000), dict(lse=FAKE + 2)):
+        assert _paged(lib, **bad) == 1, bad
+    assert _paged(lib, scale=float("nan")) == 2
+    need = lib.kda_paged_workspace_size(8, 2, 1)
+    for bad in (dict(ws=None), dict(ws=FAKE + 16), dict(ws_bytes=need - 1)):
+        assert _paged(lib, **bad) == 3, bad
+    assert _paged(lib, B=0) == 0
+    assert lib.kda_paged_workspace_size(8, 3, 1) == 0 and lib.kda_paged_workspace_size(8, 2, 0) == 0
+
+
+def test_paged_wrapper_refusals(lib):
+    import kda_linear_attention_bounded_gb300 as kda
+    with pytest.raises(ValueError, match="CUDA"):
+        kda.paged_attention(torch.zeros((1, 2, 128), dtype=torch.bfloat16), None, None, None,
+                            torch.zeros(1, dtype=torch.int32))

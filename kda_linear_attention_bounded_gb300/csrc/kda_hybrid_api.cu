@@ -49,7 +49,7 @@ extern "C" {
 
 size_t kda_gdn_prefill_workspace_size(int64_t total_tokens, int num_seqs, int Hv) {
   if (total_tokens < 0 || num_seqs < 0 || Hv <= 0) return 0;
-  return kda::kWorkspaceBytes;
+  return kda::kWorkspaceBytes + kda::gdn_prefill_workspace_bytes(total_tokens, num_seqs, Hv);
 }
 
 int kda_gdn_chunk_prefill(const uint16_t *q, const uint16_t *k, int64_t qk_token_stride, const uint16_t *v,
@@ -81,7 +81,13 @@ int kda_gdn_chunk_prefill(const uint16_t *q, const uint16_t *k, int64_t qk_token
   r.state_out_pool = (flags & KDA_FINAL_TO_POOL) ? state_pool : nullptr;
   r.state_out_dense = (flags & KDA_FINAL_TO_POOL) ? nullptr : final_state;
   r.status = static_cast<uint32_t *>(workspace);
-  return kda::launch_gdn_recurrent(r, num_seqs, static_cast<cudaStream_t>(stream)) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  // without a token every final state is its initial one: the recurrence's copy
+  const cudaError_t e = cu_seqlens_host[num_seqs] == 0
+                            ? kda::launch_gdn_recurrent(r, num_seqs, st)
+                            : kda::launch_gdn_prefill(r, cu_seqlens_host, num_seqs,
+                                                      static_cast<uint8_t *>(workspace) + kda::kWorkspaceBytes, st);
+  return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 
 int kda_gdn_recurrent_verify(const uint16_t *q, const uint16_t *k, int64_t qk_token_stride, const uint16_t *v,

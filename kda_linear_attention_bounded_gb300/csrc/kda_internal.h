@@ -45,6 +45,11 @@ struct ShortConv {
   uint16_t *step_windows;     // verify: [B, T, 3, 3, H, 128]
 };
 
+// Tensor map of [tokens, H, 128] bf16 with the given token stride, box 64 channels x 1 head x 64 tokens, with the
+// 128-byte swizzle or without; false where the driver refuses it.
+bool make_token_map(CUtensorMap *map, const void *base, int H, int total_tokens, int64_t token_stride,
+                    bool swizzled = true);
+
 // Arguments of the token-by-token kernel (verify).
 struct RecurrentArgs {
   const uint16_t *q, *k, *v, *g, *beta;
@@ -300,6 +305,11 @@ struct GdnRecurrentArgs {
 };
 
 cudaError_t launch_gdn_recurrent(const GdnRecurrentArgs &args, int num_items, cudaStream_t stream);
+
+// Chunked prefill of the gated delta rule over the sequences of cu_host; blocks: gdn_prefill_workspace_bytes().
+size_t gdn_prefill_workspace_bytes(int64_t total_tokens, int num_seqs, int Hv);
+cudaError_t launch_gdn_prefill(const GdnRecurrentArgs &args, const int32_t *cu_host, int num_seqs, uint8_t *blocks,
+                               cudaStream_t stream);
 
 // ---------------------------------------------------------------- paged attention
 constexpr int kPagedMaxCtas = 304;      // stretches of work at most (two CTAs on each of 152 SMs)

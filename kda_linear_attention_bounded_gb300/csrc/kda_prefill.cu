@@ -38,11 +38,12 @@ EncodeTiledFn encode_fn() {
   return fn;
 }
 
+}  // namespace
+
 // [tokens, H, 128] bf16 with the given token stride; box = 64 channels x 1 head x 64 tokens, with the
 // 128-byte swizzle (the row-swizzled tile layout of the MMA operands and the output staging) or
 // unswizzled (tiles read only by CUDA cores); rows past the tensor's end read as zero
-bool make_token_map(CUtensorMap *map, const void *base, int H, int total_tokens, int64_t token_stride,
-                    bool swizzled = true) {
+bool make_token_map(CUtensorMap *map, const void *base, int H, int total_tokens, int64_t token_stride, bool swizzled) {
   EncodeTiledFn enc = encode_fn();
   if (!enc) return false;
   cuuint64_t dims[3] = {static_cast<cuuint64_t>(kD), static_cast<cuuint64_t>(H),
@@ -55,8 +56,6 @@ bool make_token_map(CUtensorMap *map, const void *base, int H, int total_tokens,
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
-
-}  // namespace
 
 size_t prefill_workspace_bytes(int64_t total_tokens, int num_seqs, int H) {
   // sum_n ceil(len_n / 64) <= floor(total / 64) + num_seqs

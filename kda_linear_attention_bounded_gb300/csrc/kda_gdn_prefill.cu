@@ -3,21 +3,28 @@
 // With chunks of C = 64 tokens, b_t the cumulative log-decay inside a chunk, k^, q^ the l2-normalised keys and
 // queries and S the state entering the chunk, the recurrence S_t = (I - beta k^ k^T) e^lambda S_{t-1} + beta k^ v^T is
 //
-//   A_ri = beta_r k^_r.k^_i e^(b_r - b_i)  (i < r),     T = (I + A)^-1 Diag(beta)
-//   P_ri = scale q^_r.k^_i e^(b_r - b_i)   (i <= r)
-//   R_i  = v_i - e^(b_i) S^T k^_i,   U = T R
-//   o_r  = scale e^(b_r) S^T q^_r + (P T R)_r,   S' = e^(b_63) S + sum_i e^(b_63 - b_i) k^_i U_i^T
+//   A_ri = beta_r k^_r.k^_i e^(b_r - b_i)  (i < r),     L = (I + A)^-1
+//   P_ri = q^_r.k^_i e^(b_r - b_i)         (i <= r)
+//   R_i  = beta_i (v_i - e^(b_i) S^T k^_i),   U = L R
+//   o_r  = scale (e^(b_r) S^T q^_r + (P L R)_r),   S' = e^(b_63) S + sum_i e^(b_63 - b_i) k^_i U_i^T
 //
 // The decay is one number per token, so every product runs on the caller's own bf16 keys and queries and the norms
 // and decays are fp32 factors of rows and columns: nothing is rounded that the caller did not round.
 //
-// Two kernels.  The intra-chunk kernel forms T and P T of every (chunk, value head) at once: 25 KB a block instead of
-// the keys' and queries' decayed copies.  The state pass walks a sequence's chunks with S in fp32 registers, three
-// products a chunk.  Where a product's operand is not the caller's data (S, T, R, the scaled U) it is a pair of bf16,
-// hi + lo (16 bits of mantissa): hi and lo stand side by side as one N = 128 operand, so the second half costs one
-// longer instruction and no second pass over the A operand.  A state then carries a relative error of a few 1e-6
-// (single bf16 operands: a few 1e-3), as fp32 storage of it deserves.
+// Two kernels.  The intra-chunk kernel forms L = (I + A)^-1 and P L of every (chunk, value head) at once: 25 KB a block
+// instead of the keys', queries' and values' products with them.  The state pass walks a sequence's chunks with S in
+// fp32 registers, three products a chunk.
+//
+// Operands that are not the caller's data are pairs.  S is two bf16 (its rounding, 2^-18, is contracted by the chunk).
+// L, R and U are two fp16, 22 bits: |L| <= 1 and |P L| <= 1, since (I - beta k^ k^T) contracts; R and U carry a power
+// of two per value channel that keeps them in fp16's range whatever the values are (from |v| and a bound on the
+// channel's state, |S_t|^2 <= |S_(t-1)|^2 + v_t^2); the keys they meet are the caller's, times a power of two per token
+// (exact down to 2^-17 of a key's norm).  Final states agree with the 64-bit recurrence to a few 1e-7, like an fp32
+// evaluation, where pairs of bf16 throughout leave 6e-6 and single bf16 operands a few 1e-3.  What only an output sees
+// is rounded once (P L to fp16, S to bf16).
 #include <cuda.h>
+
+#include <cuda_fp16.h>
 
 #include <algorithm>
 #include <numeric>
@@ -33,15 +40,16 @@ namespace {
 using namespace sm100;
 
 constexpr int kC = 64;
-// a block: [T hi ; P T] (128 rows x 64 tokens, bf16, 128-byte row swizzle) | T lo (64 rows) | factors
-constexpr uint32_t kBlkTlo = 16384, kBlkVec = 24576;
-constexpr uint32_t kGdnBlkBytes = 25600;
-// factors (fp32): e^(b_i) |k_i|^-1 | scale e^(b_r) |q_r|^-1 | e^(b_63 - b_i) |k_i|^-1 | e^(b_63)
-constexpr int kVecK = 0, kVecQ = 64, kVecS = 128, kVecGamma = 192;
+// a block: [L hi ; P L ; L lo] (192 rows x 64 tokens, fp16, 128-byte row swizzle) | factors
+constexpr uint32_t kBlkPL = 8192, kBlkL2 = 16384, kBlkVec = 24576;
+constexpr uint32_t kGdnBlkBytes = 26112;
+// factors (fp32): beta_i | beta_i e^(b_i) |k_i|^-1 | scale e^(b_r) |q_r|^-1 | 2^-x_i | 2^(x_i) e^(b_63 - b_i) |k_i|^-1 |
+// e^(b_63), with 2^(x_i) <= the norm of the raw key i < 2^(x_i + 1)
+constexpr int kVecB = 0, kVecK = 64, kVecQ = 128, kVecX = 192, kVecS = 256, kVecGamma = 320;
 constexpr int kGdnMaxSeqs = 1024;   // sequences per launch (longer batches are split on the host)
 
 struct GdnPrefillParams {
-  CUtensorMap tq, tk, tv;       // [tokens, H, 128] bf16, box 64 channels x 1 head x 64 tokens, 128-byte swizzle
+  CUtensorMap tq, tk, tv, tout; // [tokens, H, 128] bf16, box 64 channels x 1 head x 64 tokens, 128-byte swizzle
   const uint16_t *a, *beta;
   int64_t a_stride, beta_stride;
   const float *A_log, *dt_bias;
@@ -67,82 +75,118 @@ __host__ __device__ __forceinline__ int first_slot(const GdnPrefillParams &p, in
 
 __device__ __forceinline__ void wait_or_abort(uint64_t *bar, uint32_t parity, volatile uint32_t *abort_flag,
                                               uint32_t *status) {
-  if (*abort_flag) return;
+  if (mbar_try_wait(bar, parity) || *abort_flag) return;
   if (!mbar_wait(bar, parity)) {
     *abort_flag = 1;
     atomicOr(status, KDA_DEVICE_TIMEOUT);
   }
 }
 
-// x as a pair of bf16, hi + lo, of two neighbouring values
-__device__ __forceinline__ void split2(float x, float y, uint32_t &hi, uint32_t &lo) {
-  hi = pack_bf16x2(x, y);
-  const float2 h = unpack_bf16x2(hi);
-  lo = pack_bf16x2(x - h.x, y - h.y);
+__device__ __forceinline__ float2 sub2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 ra, rb, rd;\n\tmov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
+      "sub.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float2 x) {
+  const __half2 h = __floats2half2_rn(x.x, x.y);
+  return *reinterpret_cast<const uint32_t *>(&h);
+}
+__device__ __forceinline__ float2 unpack_f16x2(uint32_t w) { return __half22float2(*reinterpret_cast<const __half2 *>(&w)); }
+// Two values as sums of two fp16 each, to 2^-22 (and 2^-25 absolutely).
+__device__ __forceinline__ void split2h(float2 x, uint32_t &p1, uint32_t &p2) {
+  p1 = pack_f16x2(x);
+  p2 = pack_f16x2(sub2(x, unpack_f16x2(p1)));
+}
+// Two values as sums of two bf16 each, to 2^-18.
+__device__ __forceinline__ void split2(float2 x, uint32_t &p1, uint32_t &p2) {
+  p1 = pack_bf16x2(x.x, x.y);
+  const float2 r = sub2(x, unpack_bf16x2(p1));
+  p2 = pack_bf16x2(r.x, r.y);
 }
 
 // ================================================================ intra-chunk kernel
 namespace in {
 constexpr int kThreads = 256;   // 8 warps; three CTAs per SM
-constexpr uint32_t OFF_KQ = 0;  // [k ; q], 128 rows x 128 channels: consumed by the first product
 constexpr int kStride = 68;
-constexpr uint32_t OFF_A = 0;                          // A fp32 [64][68], turned into (I + A)^-1 in place
-constexpr uint32_t OFF_P = 64 * kStride * 4;           // P fp32 [64][68]
-constexpr uint32_t OFF_BLK = 35840;                    // the block's image
+constexpr uint32_t OFF_KQ = 0;           // [k ; q], 128 rows x 128 channels: consumed by the first product; then
+constexpr uint32_t OFF_A = 0;            // A fp32 [64][68], turned into (I + A)^-1 in place
+constexpr uint32_t OFF_P = 17408;        // P as two fp16 tiles (64 rows x 64, 128-byte row swizzle)
+constexpr uint32_t OFF_BLK = 33792;      // the block's image
 constexpr uint32_t OFF_SMALL = OFF_BLK + kGdnBlkBytes;
 constexpr uint32_t SM_NORM = 0 /* [128]: 1 / |k_r|, 1 / |q_r| */, SM_BETA = 512, SM_BI = 768, SM_BF = 1024 /* b, whole and
-                   fractional part */, SM_BAR = 1280, SM_TMEM = 1296, SM_ABORT = 1300, SM_END = 1312;
+                   fractional part */, SM_UP = 1280 /* 2^-b */, SM_POW = 1536 /* 2^-x */, SM_BAR = 1792, SM_TMEM = 1808, SM_ABORT = 1812,
+                   SM_END = 1824;
 constexpr uint32_t kSmemBytes = OFF_SMALL + SM_END + 1024;
-static_assert(OFF_BLK >= 2 * 64 * kStride * 4 && OFF_BLK >= 32768 && OFF_BLK % 1024 == 0, "shared memory map");
+static_assert(OFF_P == 64 * kStride * 4 && OFF_P % 1024 == 0 && OFF_BLK == OFF_P + 16384, "shared memory map");
 static_assert(3 * (kSmemBytes + 1024) <= 233472, "three CTAs per SM");
 constexpr uint32_t kTmemCols = 128;
+// Decays of a chunk down to 2^-kFactorRange are split into a row's and a column's factor (2^b_r and 2^-b_i stay far
+// inside fp32); beyond that each entry takes its own exponential.
+constexpr float kFactorRange = 60.f;
 }  // namespace in
 
-// 16 x 8 tile += X Y for X (16 x 8 ks), Y (8 ks x 8), fp32 with row stride in::kStride, on TF32 tensor cores; kExact: each
-// operand as a pair of TF32 (three products: the error falls from 2^-11 to about 2^-21)
-template <bool kExact>
-__device__ __forceinline__ void mm_tile(float (&d)[4], const float *X, const float *Y, int ks, int lane) {
+// 16 x 8 tile of X Y for X (16 x 8 KS), Y (8 KS x 8), fp32 with row stride in::kStride, on TF32 tensor cores.  Each operand
+// is a pair of TF32 (the hardware drops the bits below a TF32's): x1 y1 + x1 y2 + x2 y1 leaves about 2^-21.
+template <int KS>
+__device__ __forceinline__ void mm_tile(float (&d)[4], const float *X, const float *Y, int lane) {
   const int g = lane >> 2, t = lane & 3;
-  for (int k = 0; k < ks; ++k) {
+  float c[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int k = 0; k < KS; ++k) {
     const float *xa = X + g * in::kStride + 8 * k + t;
     const float *yb = Y + (8 * k + t) * in::kStride + g;
     const float x[4] = {xa[0], xa[8 * in::kStride], xa[4], xa[8 * in::kStride + 4]};
     const float y[2] = {yb[0], yb[4 * in::kStride]};
-    uint32_t xh[4], yh[2];
+    uint32_t xh[4], yh[2], xl[4], yl[2];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) xh[i] = to_tf32(x[i]);
+    for (int i = 0; i < 4; ++i) {
+      xh[i] = __float_as_uint(x[i]) & 0xFFFFE000u;
+      xl[i] = __float_as_uint(x[i] - __uint_as_float(xh[i]));
+    }
 #pragma unroll
-    for (int i = 0; i < 2; ++i) yh[i] = to_tf32(y[i]);
-    if constexpr (kExact) {
-      uint32_t xl[4], yl[2];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) xl[i] = to_tf32(x[i] - __uint_as_float(xh[i]));
-#pragma unroll
-      for (int i = 0; i < 2; ++i) yl[i] = to_tf32(y[i] - __uint_as_float(yh[i]));
-      mma_1688_tf32(d, xl[0], xl[1], xl[2], xl[3], yh[0], yh[1]);
-      mma_1688_tf32(d, xh[0], xh[1], xh[2], xh[3], yl[0], yl[1]);
+    for (int i = 0; i < 2; ++i) {
+      yh[i] = __float_as_uint(y[i]) & 0xFFFFE000u;
+      yl[i] = __float_as_uint(y[i] - __uint_as_float(yh[i]));
     }
     mma_1688_tf32(d, xh[0], xh[1], xh[2], xh[3], yh[0], yh[1]);
+    mma_1688_tf32(c, xh[0], xh[1], xh[2], xh[3], yl[0], yl[1]);
+    mma_1688_tf32(c, xl[0], xl[1], xl[2], xl[3], yh[0], yh[1]);
   }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) d[i] += c[i];
 }
 __device__ __forceinline__ void st_tile(float *D, const float (&d)[4], float sgn, int lane) {
   const int g = lane >> 2, t = lane & 3;
   *reinterpret_cast<float2 *>(D + g * in::kStride + 2 * t) = make_float2(sgn * d[0], sgn * d[1]);
   *reinterpret_cast<float2 *>(D + (g + 8) * in::kStride + 2 * t) = make_float2(sgn * d[2], sgn * d[3]);
 }
-// the same tile, times sgn and the column's beta, into T hi and T lo (rows row0.., columns col0..)
-__device__ __forceinline__ void st_tile_t(uint8_t *blk, int row0, int col0, const float (&d)[4], float sgn,
-                                          const float *s_beta, int lane) {
+// the same tile, times sgn, into the two parts of L (rows row0.., columns col0..)
+__device__ __forceinline__ void st_tile_l(uint8_t *blk, int row0, int col0, const float (&d)[4], float sgn, int lane) {
   const int g = lane >> 2, c = col0 + 2 * (lane & 3);
-  const float b0 = sgn * s_beta[c], b1 = sgn * s_beta[c + 1];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    uint32_t hi, lo;
-    split2(d[2 * i] * b0, d[2 * i + 1] * b1, hi, lo);
-    const uint32_t off = swz_offset(64, row0 + g + 8 * i, c);
-    *reinterpret_cast<uint32_t *>(blk + off) = hi;
-    *reinterpret_cast<uint32_t *>(blk + kBlkTlo + off) = lo;
+    uint32_t p1, p2;
+    split2h(make_float2(sgn * d[2 * i], sgn * d[2 * i + 1]), p1, p2);
+    uint8_t *at = blk + swz_offset(64, row0 + g + 8 * i, c);
+    *reinterpret_cast<uint32_t *>(at) = p1;
+    *reinterpret_cast<uint32_t *>(at + kBlkL2) = p2;
   }
+}
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+               : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
 // One CTA per (chunk slot, key head): the products of the chunk's keys and queries serve every value head of the group.
@@ -157,12 +201,14 @@ __global__ void __launch_bounds__(in::kThreads, 3) gdn_intra_kernel(const __grid
   float *s_beta = reinterpret_cast<float *>(small + SM_BETA);
   float *s_bi = reinterpret_cast<float *>(small + SM_BI);
   float *s_bf = reinterpret_cast<float *>(small + SM_BF);
+  float *s_up = reinterpret_cast<float *>(small + SM_UP);
+  float *s_pow = reinterpret_cast<float *>(small + SM_POW);
   uint64_t *bar_in = reinterpret_cast<uint64_t *>(small + SM_BAR);
   uint64_t *bar_mma = bar_in + 1;
   uint32_t *s_tmem = reinterpret_cast<uint32_t *>(small + SM_TMEM);
   volatile uint32_t *s_abort = reinterpret_cast<volatile uint32_t *>(small + SM_ABORT);
-  uint8_t *s_blk = sm + OFF_BLK;
-  float *sA = reinterpret_cast<float *>(sm + OFF_A), *sP = reinterpret_cast<float *>(sm + OFF_P);
+  uint8_t *s_blk = sm + OFF_BLK, *s_p = sm + OFF_P;
+  float *sA = reinterpret_cast<float *>(sm + OFF_A);
 
   grid_launch_dependents();   // the state pass may take SMs as this grid leaves them
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -228,8 +274,9 @@ __global__ void __launch_bounds__(in::kThreads, 3) gdn_intra_kernel(const __grid
           if (lam != lam) be = lam;   // a decay that is no number reaches everything behind it through beta
           lam = lam < -160.f ? -160.f : lam;
         }
-        b[e] = lam == lam ? static_cast<int64_t>(rintf(lam)) * 4294967296ll +
-                                static_cast<int64_t>((lam - rintf(lam)) * 4294967296.0f)
+        const float whole = rintf(lam);
+        b[e] = lam == lam ? static_cast<int64_t>(static_cast<int>(whole)) * 4294967296ll +
+                                static_cast<int64_t>((lam - whole) * 4294967296.0f)
                           : 0;
         s_beta[r] = be;
       }
@@ -242,8 +289,11 @@ __global__ void __launch_bounds__(in::kThreads, 3) gdn_intra_kernel(const __grid
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int64_t x = e ? sum : sum - b[1];
-        s_bi[2 * lane + e] = static_cast<float>(static_cast<int>(x >> 32));
-        s_bf[2 * lane + e] = static_cast<float>(static_cast<uint32_t>(x)) * 2.3283064365386963e-10f;
+        const float bi = static_cast<float>(static_cast<int>(x >> 32));
+        const float bf = static_cast<float>(static_cast<uint32_t>(x)) * 2.3283064365386963e-10f;
+        s_bi[2 * lane + e] = bi;
+        s_bf[2 * lane + e] = bf;
+        s_up[2 * lane + e] = fast_exp2(-(bi + bf));
       }
     }
     if (gh == 0) {
@@ -260,62 +310,94 @@ __global__ void __launch_bounds__(in::kThreads, 3) gdn_intra_kernel(const __grid
         for (int e = 0; e < 32; ++e) d = e == lane ? __uint_as_float(v[e]) : d;
         const int r = 32 * q4 + lane;
         s_norm[r] = (r & 63) < valid ? rsqrtf(d + kL2Eps) : 0.f;
+        // a power of two that brings the raw key's norm to [1/2, 1) or so (a zero key: any)
+        if (r < 64) s_pow[r] = r < valid ? __uint_as_float(__float_as_uint(rsqrtf(fmaxf(d, 1e-36f))) & 0x7F800000u) : 1.f;
+      } else {
+        // zeros above the diagonal of L's parts and of P L (the value heads of the group leave them): 6 blocks x 16
+        // rows x two 16-byte pieces of each
+        for (int x = tid - 128; x < 3 * 192; x += 128) {
+          const int which = x / 192, y = x % 192, b6 = y >> 5, rr = (y >> 1) & 15, hc = y & 1;
+          const int I = b6 < 3 ? 0 : b6 < 5 ? 1 : 2;
+          const int J = b6 < 3 ? b6 + 1 : b6 < 5 ? b6 - 1 : 3;
+          *reinterpret_cast<uint4 *>(s_blk + 8192 * which + swz_offset(64, 16 * I + rr, 16 * J + 8 * hc)) = make_uint4(0, 0, 0, 0);
+        }
       }
     }
     __syncthreads();
 
-    // ---- A and P (fp32) from TMEM; the block's factors
+    // ---- A (fp32) and P (fp16 pairs) from TMEM; the block's factors
     {
       const bool is_p = q4 >= 2;
       const int r = (q4 & 1) * 32 + lane;
       const float bi = s_bi[r], bf = s_bf[r];
-      const float rowf = is_p ? prm.scale * s_norm[64 + r] : s_beta[r] * s_norm[r];
-      float *dst = (is_p ? sP : sA) + r * kStride + 32 * ib;
-      if ((q4 & 1) < ib) {   // rows 0..31, columns 32..63: above the diagonal
-#pragma unroll
-        for (int e = 0; e < 32; e += 4) *reinterpret_cast<float4 *>(dst + e) = make_float4(0.f, 0.f, 0.f, 0.f);
-      } else {
+      const float rowf = is_p ? s_norm[64 + r] : s_beta[r] * s_norm[r];
+      const bool factors = s_bi[63] > -kFactorRange;   // (b falls along the chunk)
+      const float down = rowf * fast_exp2(bi + bf);
+      if ((q4 & 1) >= ib) {   // (rows 0..31, columns 32..63 lie above the diagonal)
         const int lim = r < valid ? r - 32 * ib + (is_p ? 1 : 0) : 0;   // kept: i < r (A), i <= r (P)
+        uint32_t v[32];
+        tmem_ld16_async(lanes + 32 * ib, v);
+        tmem_ld16_async(lanes + 32 * ib + 16, v + 16);
+        tmem_wait_ld();
+        tmem_tie<32>(v);
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          uint32_t v[16];
-          tmem_ld16_async(lanes + 32 * ib + 16 * half, v);
-          tmem_wait_ld();
-          tmem_tie<16>(v);
-          float x[16];
+        for (int e0 = 0; e0 < 32; e0 += 8) {
+          float x[8];
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const int i = 32 * ib + 16 * half + e;
-            const float dec = fast_exp2((bi - s_bi[i]) + (bf - s_bf[i]));
-            x[e] = 16 * half + e < lim ? __uint_as_float(v[e]) * (rowf * s_norm[i]) * dec : 0.f;
+          for (int e = 0; e < 8; e += 4) {
+            const int i = 32 * ib + e0 + e;
+            const float4 nk = *reinterpret_cast<const float4 *>(s_norm + i);
+            const float n4[4] = {nk.x, nk.y, nk.z, nk.w};
+            if (factors) {
+              const float4 up = *reinterpret_cast<const float4 *>(s_up + i);
+              const float u4[4] = {up.x, up.y, up.z, up.w};
+#pragma unroll
+              for (int z = 0; z < 4; ++z) x[e + z] = (__uint_as_float(v[e0 + e + z]) * down) * (n4[z] * u4[z]);
+            } else {
+#pragma unroll
+              for (int z = 0; z < 4; ++z)
+                x[e + z] = __uint_as_float(v[e0 + e + z]) * (rowf * n4[z]) * fast_exp2((bi - s_bi[i + z]) + (bf - s_bf[i + z]));
+            }
           }
 #pragma unroll
-          for (int e = 0; e < 16; e += 4)
-            *reinterpret_cast<float4 *>(dst + 16 * half + e) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
+          for (int e = 0; e < 8; ++e) x[e] = e0 + e < lim ? x[e] : 0.f;
+          if (is_p) {
+            uint4 p1, p2;
+            split2h(make_float2(x[0], x[1]), p1.x, p2.x);
+            split2h(make_float2(x[2], x[3]), p1.y, p2.y);
+            split2h(make_float2(x[4], x[5]), p1.z, p2.z);
+            split2h(make_float2(x[6], x[7]), p1.w, p2.w);
+            uint8_t *at = s_p + swz_offset(64, r, 32 * ib + e0);
+            *reinterpret_cast<uint4 *>(at) = p1;
+            *reinterpret_cast<uint4 *>(at + 8192) = p2;
+          } else {
+            float *dst = sA + r * kStride + 32 * ib + e0;
+            *reinterpret_cast<float4 *>(dst) = make_float4(x[0], x[1], x[2], x[3]);
+            *reinterpret_cast<float4 *>(dst + 4) = make_float4(x[4], x[5], x[6], x[7]);
+          }
+        }
+      } else {   // one of the two warps without entries: the block's factors, two rows a lane
+        if (!is_p) {
+          float *vec = reinterpret_cast<float *>(s_blk + kBlkVec);
+#pragma unroll
+          for (int e = 0; e < 64; e += 32) {
+            const int t = lane + e;
+            const float eb = fast_exp2(s_bi[t]) * fast_exp2(s_bf[t]);
+            vec[kVecB + t] = s_beta[t];
+            vec[kVecK + t] = s_beta[t] * s_norm[t] * eb;
+            vec[kVecQ + t] = prm.scale * s_norm[64 + t] * eb;
+            vec[kVecX + t] = s_pow[t];
+            vec[kVecS + t] = s_norm[t] / s_pow[t] * fast_exp2((s_bi[63] - s_bi[t]) + (s_bf[63] - s_bf[t]));
+            if (t == 63) vec[kVecGamma] = eb;
+          }
         }
       }
-      if (tid < 64) {
-        float *vec = reinterpret_cast<float *>(s_blk + kBlkVec);
-        const float eb = fast_exp2(s_bi[tid]) * fast_exp2(s_bf[tid]);
-        vec[kVecK + tid] = s_norm[tid] * eb;
-        vec[kVecQ + tid] = prm.scale * s_norm[64 + tid] * eb;
-        vec[kVecS + tid] = s_norm[tid] * fast_exp2((s_bi[63] - s_bi[tid]) + (s_bf[63] - s_bf[tid]));
-        if (tid == 63) vec[kVecGamma] = eb;
-      }
-    }
-    // zeros above the diagonal of T hi, T lo, P T: 6 blocks x 16 rows x two 16-byte pieces of each
-    for (int x = tid; x < 3 * 192; x += kThreads) {
-      const int which = x / 192, y = x % 192, b6 = y >> 5, rr = (y >> 1) & 15, hc = y & 1;
-      const int I = b6 < 3 ? 0 : b6 < 5 ? 1 : 2;
-      const int J = b6 < 3 ? b6 + 1 : b6 < 5 ? b6 - 1 : 3;
-      uint8_t *tile = s_blk + (which == 0 ? 0u : which == 1 ? kBlkTlo : 8192u);
-      *reinterpret_cast<uint4 *>(tile + swz_offset(64, 16 * I + rr, 16 * J + 8 * hc)) = make_uint4(0, 0, 0, 0);
     }
     __syncthreads();
 
-    // ---- T = (I + A)^-1 Diag(beta): 16 x 16 diagonal inverses D_R by substitution, then
+    // ---- L = (I + A)^-1: 16 x 16 diagonal inverses D_R by substitution, then
     //   L^-1_10 = -D_1 A_10 D_0,  L^-1_32 = -D_3 A_32 D_2,  L^-1 (rows 32.., cols ..31) = -I_2 A_(23,01) I_1
-    // in place in the A tile, temporaries in its unused upper part; every block goes to T hi / T lo as it is made.
+    // in place in the A tile, temporaries in its unused upper part; every block goes to L's parts as it is made.
     {
       // task (block R, column jc): lane q = lane % 4 of it carries rows q, q + 4, q + 8, q + 12
       const int q = lane & 3, jc = 8 * (warp & 1) + (lane >> 2), R = warp >> 1;
@@ -338,62 +420,82 @@ __global__ void __launch_bounds__(in::kThreads, 3) gdn_intra_kernel(const __grid
         case 2: named_bar_sync<3>(64); break;
         default: named_bar_sync<4>(64); break;
       }
-      const float bc = s_beta[16 * R + jc];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int r = 16 * R + 4 * i + q, c = 16 * R + jc;
         sA[r * kStride + c] = xs[i];
-        const float x = xs[i] * bc;
-        const uint16_t hi = f32_to_bf16_bits(x);
-        *reinterpret_cast<uint16_t *>(s_blk + swz_offset(64, r, c)) = hi;
-        *reinterpret_cast<uint16_t *>(s_blk + kBlkTlo + swz_offset(64, r, c)) = f32_to_bf16_bits(x - bf16_bits_to_f32(hi));
+        const __half hi = __float2half_rn(xs[i]);
+        uint8_t *at = s_blk + swz_offset(64, r, c);
+        *reinterpret_cast<__half *>(at) = hi;
+        *reinterpret_cast<__half *>(at + kBlkL2) = __float2half_rn(xs[i] - __half2float(hi));
       }
     }
     __syncthreads();
     if (warp < 4) {
       const int lo = warp < 2 ? 0 : 32, nj = warp & 1;
       float d[4] = {0.f, 0.f, 0.f, 0.f};
-      mm_tile<true>(d, sA + (lo + 16) * kStride + lo, sA + lo * kStride + lo + 8 * nj, 2, lane);
+      mm_tile<2>(d, sA + (lo + 16) * kStride + lo, sA + lo * kStride + lo + 8 * nj, lane);
       st_tile(sA + lo * kStride + lo + 16 + 8 * nj, d, 1.f, lane);
       if (warp < 2) named_bar_sync<5>(64); else named_bar_sync<6>(64);   // A_10 (A_32) has been read
       float e[4] = {0.f, 0.f, 0.f, 0.f};
-      mm_tile<true>(e, sA + (lo + 16) * kStride + lo + 16, sA + lo * kStride + lo + 16 + 8 * nj, 2, lane);
+      mm_tile<2>(e, sA + (lo + 16) * kStride + lo + 16, sA + lo * kStride + lo + 16 + 8 * nj, lane);
       st_tile(sA + (lo + 16) * kStride + lo + 8 * nj, e, -1.f, lane);
-      st_tile_t(s_blk, lo + 16, lo + 8 * nj, e, -1.f, s_beta, lane);
+      st_tile_l(s_blk, lo + 16, lo + 8 * nj, e, -1.f, lane);
     }
     __syncthreads();
     {   // Z = A_(23,01) I_1 -> rows 0..31, cols 32..63
-      const int mi = warp >> 2, nj = warp & 3, k0 = nj < 2 ? 0 : 16;
+      const int mi = warp >> 2, nj = warp & 3;
       float d[4] = {0.f, 0.f, 0.f, 0.f};
-      mm_tile<true>(d, sA + (32 + 16 * mi) * kStride + k0, sA + k0 * kStride + 8 * nj, (32 - k0) / 8, lane);
+      if (nj < 2) mm_tile<4>(d, sA + (32 + 16 * mi) * kStride, sA + 8 * nj, lane);
+      else mm_tile<2>(d, sA + (32 + 16 * mi) * kStride + 16, sA + 16 * kStride + 8 * nj, lane);
       st_tile(sA + (16 * mi) * kStride + 32 + 8 * nj, d, 1.f, lane);
     }
     __syncthreads();
     {
       const int mi = warp >> 2, nj = warp & 3;
       float d[4] = {0.f, 0.f, 0.f, 0.f};
-      mm_tile<true>(d, sA + (32 + 16 * mi) * kStride + 32, sA + 32 + 8 * nj, mi ? 4 : 2, lane);
-      st_tile(sA + (32 + 16 * mi) * kStride + 8 * nj, d, -1.f, lane);
-      st_tile_t(s_blk, 32 + 16 * mi, 8 * nj, d, -1.f, s_beta, lane);
+      if (mi) mm_tile<4>(d, sA + 48 * kStride + 32, sA + 32 + 8 * nj, lane);
+      else mm_tile<2>(d, sA + 32 * kStride + 32, sA + 32 + 8 * nj, lane);
+      st_tile_l(s_blk, 32 + 16 * mi, 8 * nj, d, -1.f, lane);
     }
     __syncthreads();
-    // ---- P T: 20 tiles of 16 x 8 on and below the diagonal, ten 8-deep steps a warp; an entry is rounded once, to
-    // bf16, like the output it goes into
+    // ---- P L: ten 16 x 16 tiles on and below the diagonal, at most four 16-deep steps a warp.  P and L enter as pairs
+    // (with keys that are alike the sums cancel far below their terms); the result, which only outputs see, is rounded
+    // once.
     {
-      // (row block, column tile) of each task, 3 bits each; 077: none
-      static constexpr uint16_t kTasks[8][4] = {{030, 012, 077, 077}, {031, 013, 077, 077}, {032, 022, 077, 077}, {033, 023, 077, 077},
-                                                {020, 034, 077, 077}, {021, 035, 077, 077}, {010, 036, 024, 000}, {011, 037, 025, 001}};
-#pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const int task = kTasks[warp][x];
-        if (task == 077) break;
-        const int I = task >> 3, cb = task & 7, k0 = 16 * (cb >> 1);
-        float d[4] = {0.f, 0.f, 0.f, 0.f};
-        mm_tile<false>(d, sP + 16 * I * kStride + k0, sA + k0 * kStride + 8 * cb, (16 * (I + 1) - k0) / 8, lane);
-        const int g = lane >> 2, c = 8 * cb + 2 * (lane & 3);
-        const float b0 = s_beta[c], b1 = s_beta[c + 1];
-        *reinterpret_cast<uint32_t *>(s_blk + 8192 + swz_offset(64, 16 * I + g, c)) = pack_bf16x2(d[0] * b0, d[1] * b1);
-        *reinterpret_cast<uint32_t *>(s_blk + 8192 + swz_offset(64, 16 * I + g + 8, c)) = pack_bf16x2(d[2] * b0, d[3] * b1);
+      auto tile = [&](int I, int J) {
+        float d0[4] = {0.f, 0.f, 0.f, 0.f}, d1[4] = {0.f, 0.f, 0.f, 0.f};
+        for (int kb = J; kb <= I; ++kb) {
+          uint32_t a[4], a2[4], b[4], b2[4];
+          const uint32_t at = smem_u32(s_p) + swz_offset(64, 16 * I + (lane & 15), 16 * kb + 8 * (lane >> 4));
+          const uint32_t bt = smem_u32(s_blk) + swz_offset(64, 16 * kb + (lane & 15), 16 * J + 8 * (lane >> 4));
+          ldsm4(a, at);
+          ldsm4_t(b, bt);
+          ldsm4(a2, at + 8192);
+          ldsm4_t(b2, bt + kBlkL2);
+          mma_16816(d0, a, b[0], b[1]);
+          mma_16816(d1, a, b[2], b[3]);
+          mma_16816(d0, a2, b[0], b[1]);
+          mma_16816(d1, a2, b[2], b[3]);
+          mma_16816(d0, a, b2[0], b2[1]);
+          mma_16816(d1, a, b2[2], b2[3]);
+        }
+        const int g = lane >> 2, c = 16 * J + 2 * (lane & 3);
+        uint8_t *pt = s_blk + kBlkPL;
+        *reinterpret_cast<uint32_t *>(pt + swz_offset(64, 16 * I + g, c)) = pack_f16x2(make_float2(d0[0], d0[1]));
+        *reinterpret_cast<uint32_t *>(pt + swz_offset(64, 16 * I + g + 8, c)) = pack_f16x2(make_float2(d0[2], d0[3]));
+        *reinterpret_cast<uint32_t *>(pt + swz_offset(64, 16 * I + g, c + 8)) = pack_f16x2(make_float2(d1[0], d1[1]));
+        *reinterpret_cast<uint32_t *>(pt + swz_offset(64, 16 * I + g + 8, c + 8)) = pack_f16x2(make_float2(d1[2], d1[3]));
+      };
+      switch (warp) {
+        case 0: tile(3, 0); break;
+        case 1: tile(2, 0); break;
+        case 2: tile(3, 1); break;
+        case 3: tile(1, 0); tile(0, 0); break;
+        case 4: tile(2, 1); tile(1, 1); break;
+        case 5: tile(3, 2); tile(2, 2); break;
+        case 6: tile(3, 3); break;
+        default: break;
       }
     }
     fence_async_smem();
@@ -414,54 +516,62 @@ __global__ void __launch_bounds__(in::kThreads, 3) gdn_intra_kernel(const __grid
 }
 
 // ================================================================ state pass
-// CTA = (sequence, value head) with kG groups, each owning 64 of the value channels, or (sequence, value head, half)
-// with one.  A group is 8 epilogue warps (warp w: TMEM lanes 32 (w % 4).., 32 of the 64 columns) and one issuing warp;
-// one more warp feeds both groups' chunks through two stages.  With [. | .] hi and lo side by side, a chunk is
-//   D  = [k ; q] [S | S]                       (M = 128: keys' and queries' rows; N = 128; K = 128)
-//   R  = v - e^b/|k| (k S)                     (warps of lanes 0..63; q S waits in the others' registers)
-//   D  = [T ; P T] [R | R],  X = T_lo R_hi     (N = 128 and 64, K = 64 tokens)
-//   U' = e^(b_63 - b)/|k| (T R), o = scale e^b/|q| (q S) + P T R
-//   D  = k^T [U' | U'],  S = e^(b_63) S + D    (M = 128 key channels; S in registers, 32 a thread)
-// The serial path of a chunk is three products and three short epilogues; two groups on an SM fill each other's gaps.
+// CTA = (sequence, value head).  Products run transposed (TMEM lane = value channel, M = 128), so that the operands a
+// chunk makes (S, R, U) go back to TMEM in the lanes they were read from and only the caller's tiles and the block come
+// from shared memory (N columns, K deep; a 16-deep step takes 48 cycles at N = 64 and 70 at N = 128):
+//   KU = S^T k^T                (S hi, S lo; N = 64 tokens, K = 128 channels)      QS = S^T q^T (S hi)
+//   R^T = beta (v^T - e^b/|k| KU)
+//   [U | OT] = R^T [L ; P L]^T  (R hi against [L hi ; P L], N = 128; R hi L lo, R lo L hi, N = 64; K = 64 tokens)
+//   U'^T = 2^x e^(b_63 - b)/|k| U,   o = scale e^b/|q| QS + scale OT
+//   D = U'^T (2^-x k)           (U' hi, U' lo; N = 128 channels, K = 64),          S = e^(b_63) S + D
+// Sixteen epilogue warps (warp w: lanes 32 (w % 4).., quarter w / 4 of the columns; 32 state entries a thread), one
+// issuing warp, one that feeds chunks through two stages and brings the next to L2.  The serial path of a chunk is
+// KU -> R -> U -> U' -> D -> S; what it does not need runs beside it: v^T and the fp16 keys under KU, QS under R's
+// epilogue, the output under D.
 namespace ch {
-template <int kG>
-struct Map {
-  static constexpr int kThreads = 32 * (8 * kG + kG + 1);
-  static constexpr uint32_t ST_BLK = 32768, ST_V = ST_BLK + kGdnBlkBytes, kStage = ST_V + 8192 * kG;
-  static constexpr uint32_t OFF_RLO = 2 * kStage, OFF_S = OFF_RLO + 8192 * kG, OFF_SMALL = OFF_S + 32768 * kG;
-  static constexpr uint32_t SM_BAR = 0 /* full[2], empty[2], then m1, m2, m3 of each group */, SM_TMEM = 96, SM_ABORT = 100,
-                            SM_END = 128;
-  static constexpr uint32_t kSmemBytes = OFF_SMALL + SM_END;
-  static constexpr uint32_t kTmemCols = 256 * kG;
-  static_assert(kSmemBytes <= 232448 && kStage % 1024 == 0 && OFF_S % 1024 == 0, "shared memory map");
-};
-constexpr uint32_t TM_X = 128;   // columns of a group: D (128), X (64)
+constexpr int kWorkers = 512, kThreads = kWorkers + 64;
+constexpr int kIssuer = 16, kProducer = 17;   // warps
+constexpr uint32_t ST_V = 32768, ST_BLK = 49152, kStage = 75776;   // [k ; q] | v | block, a multiple of 1024
+constexpr uint32_t OFF_K16 = 2 * kStage;          // the chunk's keys in fp16 (64 rows x 128 channels, two panels)
+constexpr uint32_t OFF_OUT = OFF_K16 + 16384;     // output rows on their way out (two panels of 64 channels)
+constexpr uint32_t OFF_SMALL = OFF_OUT + 16384;
+constexpr uint32_t SM_BAR = 0 /* full[2], empty[2], m1, m2, m3 */, SM_TMEM = 56, SM_ABORT = 60, SM_MAX = 64 /* [4][128] */,
+                   SM_END = 64 + 2048;
+constexpr uint32_t kSmemBytes = OFF_SMALL + SM_END + 1024;
+static_assert(kSmemBytes <= 232448 && kStage >= ST_BLK + kGdnBlkBytes && kStage % 1024 == 0, "shared memory map");
+constexpr uint32_t TM_KU = 0, TM_U = 64, TM_OT = 128, TM_QS = 192, TM_D = 0 /* 128 columns, over KU and U */,
+                   TM_S = 256 /* 2 x 64 */, TM_R = 384 /* 2 x 32 */, kTmemCols = 512;
+constexpr int kBarS = 1, kBarR = 2, kBarW = 3;   // named barriers: workers and issuer; workers alone
 }  // namespace ch
 
 __device__ __forceinline__ void bar_arrive(int id, int count) { asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(count) : "memory"); }
 __device__ __forceinline__ void bar_wait(int id, int count) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(count) : "memory"); }
+__device__ __forceinline__ void bulk_prefetch(const void *src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(reinterpret_cast<uint64_t>(src)), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t *v) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
+               ::"r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+// kind::f16 with fp16 operands
+__host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool a_mn_major, bool b_mn_major) {
+  return idesc_bf16(M, N, a_mn_major, b_mn_major) & ~((1u << 7) | (1u << 10));
+}
 
-template <int kG>
-__global__ void __launch_bounds__(ch::Map<kG>::kThreads, 1) gdn_chain_kernel(const __grid_constant__ GdnPrefillParams prm) {
-  using M = ch::Map<kG>;
-  extern __shared__ __align__(1024) uint8_t sm[];
-  uint8_t *small = sm + M::OFF_SMALL;
-  uint64_t *bar_full = reinterpret_cast<uint64_t *>(small + M::SM_BAR), *bar_empty = bar_full + 2, *bar_m = bar_full + 4;
-  uint32_t *s_tmem = reinterpret_cast<uint32_t *>(small + M::SM_TMEM);
-  volatile uint32_t *s_abort = reinterpret_cast<volatile uint32_t *>(small + M::SM_ABORT);
+__global__ void __launch_bounds__(ch::kThreads, 1) gdn_chain_kernel(const __grid_constant__ GdnPrefillParams prm) {
+  using namespace ch;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t *small = sm + OFF_SMALL;
+  uint64_t *bar_full = reinterpret_cast<uint64_t *>(small + SM_BAR), *bar_empty = bar_full + 2;
+  uint64_t *bar_m1 = bar_full + 4, *bar_m2 = bar_full + 5, *bar_m3 = bar_full + 6;
+  uint32_t *s_tmem = reinterpret_cast<uint32_t *>(small + SM_TMEM);
+  volatile uint32_t *s_abort = reinterpret_cast<volatile uint32_t *>(small + SM_ABORT);
+  float *s_max = reinterpret_cast<float *>(small + SM_MAX);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  constexpr int kIssuer0 = 8 * kG, kProducer = 9 * kG;   // warps
-  if (smem_u32(sm) & 1023u) {   // operand tiles need the alignment declared above
-    if (tid == 0) {
-      atomicOr(prm.status, KDA_DEVICE_TIMEOUT);
-      grid_dependency_wait();
-    }
-    return;
-  }
 
-  const int item = kG == 2 ? blockIdx.x : blockIdx.x >> 1;
-  const int half0 = kG == 2 ? 0 : blockIdx.x & 1;        // first 64-channel half of this CTA
-  const int h = item % prm.Hv, n = prm.order[item / prm.Hv], hk = h / prm.group;
+  const int h = blockIdx.x % prm.Hv, n = prm.order[blockIdx.x / prm.Hv], hk = h / prm.group;
   const int t0 = prm.cu[n], len = prm.cu[n + 1] - t0;
   const int nchunks = (len + kC - 1) / kC;
   int pool_slot = 0;
@@ -479,30 +589,22 @@ __global__ void __launch_bounds__(ch::Map<kG>::kThreads, 1) gdn_chain_kernel(con
   const float *src = prm.state_in ? prm.state_in + pool_at : nullptr;
   float *dst = prm.state_out_pool ? prm.state_out_pool + pool_at
                                   : prm.state_out_dense + (static_cast<size_t>(n) * prm.Hv + h) * kD * kD;
-  // epilogue thread: TMEM lane 32 quad + lane, columns cl .. cl + 31 of the group's 64
-  const int grp = warp >> 3, quad = warp & 3, cl = 32 * ((warp >> 2) & 1);
-  const bool worker = warp < kIssuer0;
-  const int row = 32 * quad + lane, v0 = 64 * (half0 + grp) + cl;   // state row (key channel), first value channel
+  // epilogue thread: value channel d (TMEM lane), key channels 32 cg .. + 31 of the state, tokens 16 cg .. + 15 of a chunk
+  const bool worker = warp < kIssuer;
+  const int quad = warp & 3, cg = warp >> 2, d = 32 * quad + lane;
   float S[32];
   if (worker) {
 #pragma unroll
-    for (int e = 0; e < 32; e += 4) {
-      const float4 x = src ? *reinterpret_cast<const float4 *>(src + row * kD + v0 + e) : make_float4(0.f, 0.f, 0.f, 0.f);
-      S[e] = x.x; S[e + 1] = x.y; S[e + 2] = x.z; S[e + 3] = x.w;
-    }
+    for (int e = 0; e < 32; ++e) S[e] = src ? src[(32 * cg + e) * kD + d] : 0.f;
   }
   if (nchunks > 0) {
     if (tid == 0) {
-      for (int i = 0; i < 2; ++i) {
-        mbar_init(&bar_full[i], 1);
-        mbar_init(&bar_empty[i], 8 * kG);
-      }
-      for (int i = 0; i < 3 * kG; ++i) mbar_init(&bar_m[i], 1);
+      for (int i = 0; i < 7; ++i) mbar_init(&bar_full[i], i == 2 || i == 3 ? 16 : 1);
       *s_abort = 0;
       fence_mbar_init();
     }
     if (warp == kProducer) {
-      tmem_alloc(s_tmem, M::kTmemCols);
+      tmem_alloc(s_tmem, kTmemCols);
       tmem_relinquish();
     }
     tc_fence_before();
@@ -516,232 +618,314 @@ __global__ void __launch_bounds__(ch::Map<kG>::kThreads, 1) gdn_chain_kernel(con
         const uint8_t *blk = prm.blocks + (static_cast<size_t>(first_slot(prm, n)) * prm.Hv + h) * kGdnBlkBytes;
         const size_t step = static_cast<size_t>(prm.Hv) * kGdnBlkBytes;
         int c = 0;
-        for (; c < nchunks && !*s_abort; ++c) {
+        for (; c < nchunks; ++c) {
           const int s = c & 1;
           if (c >= 2) wait_or_abort(&bar_empty[s], ((c >> 1) - 1) & 1, s_abort, prm.status);
           if (*s_abort) break;
-          uint8_t *st = sm + s * M::kStage;
-          mbar_arrive_expect_tx(&bar_full[s], M::kStage);
+          uint8_t *st = sm + s * kStage;
+          mbar_arrive_expect_tx(&bar_full[s], ST_BLK + kGdnBlkBytes);
           const int tok = t0 + c * kC;
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
             tma_load_3d(st + 16384 * x, &prm.tk, 64 * x, hk, tok, &bar_full[s]);
             tma_load_3d(st + 16384 * x + 8192, &prm.tq, 64 * x, hk, tok, &bar_full[s]);
+            tma_load_3d(st + ST_V + 8192 * x, &prm.tv, 64 * x, h, tok, &bar_full[s]);
           }
-#pragma unroll
-          for (int g = 0; g < kG; ++g) tma_load_3d(st + M::ST_V + 8192 * g, &prm.tv, 64 * (half0 + g), h, tok, &bar_full[s]);
           if (c == 0) grid_dependency_wait();   // the blocks are the intra-chunk grid's
-          bulk_load(st + M::ST_BLK, blk + c * step, kGdnBlkBytes, &bar_full[s]);
+          bulk_load(st + ST_BLK, blk + c * step, kGdnBlkBytes, &bar_full[s]);
+          if (c >= 1 && c + 1 < nchunks) {   // the next one to be fetched, into L2
+            const int tok1 = tok + kC;
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              tma_prefetch_3d(&prm.tk, 64 * x, hk, tok1);
+              tma_prefetch_3d(&prm.tq, 64 * x, hk, tok1);
+              tma_prefetch_3d(&prm.tv, 64 * x, h, tok1);
+            }
+            bulk_prefetch(blk + (c + 1) * step, kGdnBlkBytes);
+          }
         }
         // the copies that were issued last have landed before the CTA ends, whatever the others found
         for (int i = max(0, c - 2); i < c; ++i) mbar_wait(&bar_full[i & 1], (i >> 1) & 1);
       }
       __syncwarp();
     } else if (!worker) {
-      // ------------------------------------------------------------ products of one group
-      const int g = warp - kIssuer0, bar = 1 + g;
-      uint64_t *m = bar_m + 3 * g;
-      const uint32_t d = tmem + 256 * g, x = d + ch::TM_X;
-      const uint64_t s_desc = desc_mnmajor_base(smem_u32(sm + M::OFF_S + 32768 * g), 128);
-      const uint32_t rlo = smem_u32(sm + M::OFF_RLO + 8192 * g);
+      // ------------------------------------------------------------ products
+      constexpr uint32_t id1 = idesc_bf16(128, 64, false, false), id2w = idesc_f16(128, 128, false, false),
+                         id2 = idesc_f16(128, 64, false, false), id3 = idesc_f16(128, 128, false, true);
+      const uint64_t k16 = smem_desc(smem_u32(sm + OFF_K16), 8192, 1024);   // rows = tokens: two 64-channel panels
       for (int c = 0; c < nchunks; ++c) {
-        uint8_t *st = sm + (c & 1) * M::kStage;
-        const uint32_t rhi = smem_u32(st + M::ST_V + 8192 * g);
-        const uint64_t kq = desc_kmajor_base(smem_u32(st)), kt = desc_mnmajor_base(smem_u32(st), 128);
-        const uint64_t tp = desc_kmajor_base(smem_u32(st + M::ST_BLK)), tl = desc_kmajor_base(smem_u32(st + M::ST_BLK + kBlkTlo));
-        const uint64_t r2 = smem_desc(rhi, rlo - rhi, 1024);
-        bar_wait(bar, 288);   // S is in place
+        uint8_t *st = sm + (c & 1) * kStage;
+        const uint64_t kk = desc_kmajor_base(smem_u32(st)), qq = kk + desc_bytes(8192);
+        const uint64_t l1 = desc_kmajor_base(smem_u32(st + ST_BLK)), l2 = l1 + desc_bytes(kBlkL2);
+        bar_wait(kBarS, kWorkers + 32);   // S is in place, D has been read
         if (lane == 0) {
           wait_or_abort(&bar_full[c & 1], (c >> 1) & 1, s_abort, prm.status);
           tc_fence_after();
-          const uint32_t id = idesc_bf16(128, 128, false, true);
 #pragma unroll
-          for (int k = 0; k < 8; ++k) mma_bf16(d, kq + kmajor_step(128, k), s_desc + mnmajor_step(k), id, k > 0);
-          mma_commit(&m[0]);
+          for (int p = 0; p < 2; ++p)
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              mma_bf16_tmem_a(tmem + TM_KU, tmem + TM_S + 64 * p + 8 * k, kk + kmajor_step(128, k), id1, p + k > 0);
+          mma_commit(bar_m1);
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            mma_bf16_tmem_a(tmem + TM_QS, tmem + TM_S + 8 * k, qq + kmajor_step(128, k), id1, k > 0);
         }
         __syncwarp();
-        bar_wait(bar, 288);   // R is in place, D has been read
+        bar_wait(kBarR, kWorkers + 32);   // R is in place, KU has been read
         if (lane == 0) {
           tc_fence_after();
-          const uint32_t id = idesc_bf16(128, 128, false, true), id1 = idesc_bf16(128, 64, false, true);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) mma_bf16(d, tp + kmajor_step(128, k), r2 + mnmajor_step(k), id, k > 0);
+          for (int k = 0; k < 4; ++k)
+            mma_bf16_tmem_a(tmem + TM_U, tmem + TM_R + 8 * k, l1 + kmajor_step(64, k), id2w, k > 0);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) mma_bf16(x, tl + kmajor_step(128, k), r2 + mnmajor_step(k), id1, k > 0);
-          mma_commit(&m[1]);
+          for (int k = 0; k < 4; ++k) mma_bf16_tmem_a(tmem + TM_U, tmem + TM_R + 8 * k, l2 + kmajor_step(64, k), id2, 1);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) mma_bf16_tmem_a(tmem + TM_U, tmem + TM_R + 32 + 8 * k, l1 + kmajor_step(64, k), id2, 1);
+          mma_commit(bar_m2);
         }
         __syncwarp();
-        bar_wait(bar, 288);   // U' is in place, D has been read
+        bar_wait(kBarR, kWorkers + 32);   // U' and the fp16 keys are in place, U has been read
         if (lane == 0) {
           tc_fence_after();
-          const uint32_t id = idesc_bf16(128, 128, true, true);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) mma_bf16(d, kt + mnmajor_step(k), r2 + mnmajor_step(k), id, k > 0);
-          mma_commit(&m[2]);
+          for (int p = 0; p < 2; ++p)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              mma_bf16_tmem_a(tmem + TM_D, tmem + TM_R + 32 * p + 8 * k, k16 + mnmajor_step(k), id3, p + k > 0);
+          mma_commit(bar_m3);
         }
         __syncwarp();
       }
     } else {
-      // ------------------------------------------------------------ epilogues of one group
-      const int bar = 1 + grp;
-      uint64_t *m = bar_m + 3 * grp;
-      const uint32_t d = tmem + 256 * grp + (static_cast<uint32_t>(quad * 32) << 16) + cl, x = d + ch::TM_X;
-      uint8_t *s_tile = sm + M::OFF_S + 32768 * grp, *rlo = sm + M::OFF_RLO + 8192 * grp;
-      // 8 fp32 values -> 16 bytes of hi and of lo, columns c.. of row r (tiles of R rows)
-      auto put8 = [](uint8_t *hi_tile, uint8_t *lo_tile, uint32_t off, const float *f) {
-        uint4 hi, lo;
-        split2(f[0], f[1], hi.x, lo.x);
-        split2(f[2], f[3], hi.y, lo.y);
-        split2(f[4], f[5], hi.z, lo.z);
-        split2(f[6], f[7], hi.w, lo.w);
-        *reinterpret_cast<uint4 *>(hi_tile + off) = hi;
-        *reinterpret_cast<uint4 *>(lo_tile + off) = lo;
-      };
-      auto store_s = [&] {
+      // ------------------------------------------------------------ epilogues
+      const uint32_t lanes = tmem + (static_cast<uint32_t>(quad * 32) << 16);
+      auto store_s = [&] {   // this quarter of S -> its two parts
+        uint32_t p1[16], p2[16];
 #pragma unroll
-        for (int e = 0; e < 32; e += 8) put8(s_tile, s_tile + 16384, swz_offset(128, row, cl + e), S + e);
-        fence_async_smem();
+        for (int i = 0; i < 16; ++i) split2(make_float2(S[2 * i], S[2 * i + 1]), p1[i], p2[i]);
+        tmem_st16(lanes + TM_S + 16 * cg, p1);
+        tmem_st16(lanes + TM_S + 64 + 16 * cg, p2);
+        tmem_wait_st();
         tc_fence_before();
-        bar_arrive(bar, 288);
+        bar_arrive(kBarS, kWorkers + 32);
       };
-      // 16 columns of D, hi and lo part added
-      auto load16 = [&](int e, float *f) {
-        uint32_t a[16], b[16];
-        tmem_ld16_async(d + e, a);
-        tmem_ld16_async(d + 64 + e, b);
-        tmem_wait_ld();
-        tmem_tie<16>(a);
-        tmem_tie<16>(b);
+      auto store_r = [&](const float2 (&x)[8]) {   // 16 tokens of R or U' -> their two parts
+        uint32_t p1[8], p2[8];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) f[i] = __uint_as_float(a[i]) + __uint_as_float(b[i]);
+        for (int i = 0; i < 8; ++i) split2h(x[i], p1[i], p2[i]);
+        tmem_st8(lanes + TM_R + 8 * cg, p1);
+        tmem_st8(lanes + TM_R + 32 + 8 * cg, p2);
+        tmem_wait_st();
+        tc_fence_before();
+        bar_arrive(kBarR, kWorkers + 32);
+      };
+      // the four threads of a value channel share one number each
+      auto share = [&](float mine, float (&all)[4]) {
+        s_max[cg * 128 + d] = mine;
+        bar_wait(kBarW, kWorkers);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) all[i] = s_max[i * 128 + d];
       };
       store_s();
+      float bound;   // of the channel's state in 2-norm
+      {
+        float ss = 0.f, all[4];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) ss = fmaf(S[e], S[e], ss);
+        share(ss, all);
+        bound = sqrtf((all[0] + all[1]) + (all[2] + all[3]));
+        bar_wait(kBarW, kWorkers);   // read by all before the first chunk's maxima
+      }
       for (int c = 0; c < nchunks; ++c) {
-        uint8_t *st = sm + (c & 1) * M::kStage;
-        uint8_t *rhi = st + M::ST_V + 8192 * grp;
-        const float *vec = reinterpret_cast<const float *>(st + M::ST_BLK + kBlkVec);
+        uint8_t *st = sm + (c & 1) * kStage;
+        const float *vec = reinterpret_cast<const float *>(st + ST_BLK + kBlkVec);
         const int valid = min(kC, len - c * kC);
         wait_or_abort(&bar_full[c & 1], (c >> 1) & 1, s_abort, prm.status);
-        // keys behind the sequence's end may hold anything; their U' is 0, but 0 x NaN is not (each group clears them
-        // for its own last product; no other product's result there is used)
-        if (valid < kC)
-          for (int i = tid & 255; i < (kC - valid) * 16; i += 256)
-            *reinterpret_cast<uint4 *>(st + swz_offset(128, valid + (i >> 4), 8 * (i & 15))) = make_uint4(0, 0, 0, 0);
-        float qs[32];   // lanes 64..127: q S of token row - 64
-        wait_or_abort(&m[0], c & 1, s_abort, prm.status);
-        tc_fence_after();
-        if (quad < 2) {
-          const float f = -vec[kVecK + row];
-          const bool there = row < valid;
+        // ---- under the product: v^T (this thread's channel of 16 tokens) and the channel's scale
+        float2 x[8];
+        float vm = 0.f;
+        {
+          const uint8_t *vt = st + ST_V + 8192 * (d >> 6);
 #pragma unroll
-          for (int e = 0; e < 32; e += 16) {
-            float ks[16];
-            load16(e, ks);
+          for (int i = 0; i < 8; ++i) {
+            const int t = 16 * cg + 2 * i;
+            x[i].x = bf16_bits_to_f32(*reinterpret_cast<const uint16_t *>(vt + swz_offset(64, t, d & 63)));
+            x[i].y = bf16_bits_to_f32(*reinterpret_cast<const uint16_t *>(vt + swz_offset(64, t + 1, d & 63)));
+          }
+          if (valid < kC) {   // rows behind the end belong to others
 #pragma unroll
-            for (int y = 0; y < 16; y += 8) {
-              const uint32_t off = swz_offset(64, row, cl + e + y);
-              const uint4 w = *reinterpret_cast<const uint4 *>(rhi + off);
-              const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
-              float r[8];
-#pragma unroll
-              for (int z = 0; z < 4; ++z) {
-                const float2 v2 = unpack_bf16x2(ws[z]);
-                r[2 * z] = there ? fmaf(f, ks[y + 2 * z], v2.x) : 0.f;
-                r[2 * z + 1] = there ? fmaf(f, ks[y + 2 * z + 1], v2.y) : 0.f;
-              }
-              put8(rhi, rlo, off, r);
+            for (int i = 0; i < 8; ++i) {
+              if (16 * cg + 2 * i >= valid) x[i].x = 0.f;
+              if (16 * cg + 2 * i + 1 >= valid) x[i].y = 0.f;
             }
           }
-        } else {
-          load16(0, qs);
-          load16(16, qs + 16);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) vm = fmaxf(vm, fmaxf(fabsf(x[i].x), fabsf(x[i].y)));
+        }
+        // the chunk's keys times 2^-x as fp16 (thread: row tid / 8, 16 channels); rows behind the end are 0
+        {
+          const int r = tid >> 3, c0 = 16 * (tid & 7);
+          const float f = r < valid ? vec[kVecX + r] : 0.f;
+#pragma unroll
+          for (int y = 0; y < 16; y += 8) {
+            uint4 w = *reinterpret_cast<const uint4 *>(st + swz_offset(128, r, c0 + y));
+            const float2 f2 = make_float2(f, f);
+            w.x = pack_f16x2(mul2(unpack_bf16x2(w.x), f2));
+            w.y = pack_f16x2(mul2(unpack_bf16x2(w.y), f2));
+            w.z = pack_f16x2(mul2(unpack_bf16x2(w.z), f2));
+            w.w = pack_f16x2(mul2(unpack_bf16x2(w.w), f2));
+            if (r >= valid) w = make_uint4(0, 0, 0, 0);
+            *reinterpret_cast<uint4 *>(sm + OFF_K16 + swz_offset(64, r, c0 + y)) = w;
+          }
         }
         fence_async_smem();
-        tc_fence_before();
-        bar_arrive(bar, 288);
-
-        wait_or_abort(&m[1], c & 1, s_abort, prm.status);
-        tc_fence_after();
-        if (quad < 2) {
-          const float f = vec[kVecS + row];
+        // the channel's scale: |R|, |U| <= |v| + |S| within the chunk < 2^(e + 1) -> below 2^14 (U' below 2^15); at most
+        // 2^90, which keeps the factors finite where a channel is zero so far
+        float sig, inv;
+        const float gamma = vec[kVecGamma];
+        {
+          float all[4];
+          share(vm, all);
+          vm = fmaxf(fmaxf(all[0], all[1]), fmaxf(all[2], all[3]));
+          const float most = vm + sqrtf(fmaf(bound, bound, 64.f * vm * vm));
+          const int field = min(max(267 - static_cast<int>(__float_as_uint(most) >> 23 & 0xFF), 1), 217);
+          sig = __uint_as_float(static_cast<uint32_t>(field) << 23);
+          inv = __uint_as_float(static_cast<uint32_t>(254 - field) << 23);
+          bound = sqrtf(fmaf(gamma * bound, gamma * bound, 64.f * vm * vm));
+        }
+        const float2 sig2 = make_float2(sig, sig);
+        {   // R^T = beta (v^T - e^b/|k| (k S)^T)
+          uint32_t w[16];
+          float2 f1[8];
 #pragma unroll
-          for (int e = 0; e < 32; e += 16) {
-            float u[16];
-            uint32_t w[16];
-            tmem_ld16_async(x + e, w);
-            load16(e, u);
-            tmem_tie<16>(w);
+          for (int i = 0; i < 8; i += 2) {
+            const float4 b = *reinterpret_cast<const float4 *>(vec + kVecB + 16 * cg + 2 * i);
+            const float4 k = *reinterpret_cast<const float4 *>(vec + kVecK + 16 * cg + 2 * i);
+            x[i] = mul2(mul2(x[i], sig2), make_float2(b.x, b.y));
+            x[i + 1] = mul2(mul2(x[i + 1], sig2), make_float2(b.z, b.w));
+            f1[i] = mul2(make_float2(-k.x, -k.y), sig2);
+            f1[i + 1] = mul2(make_float2(-k.z, -k.w), sig2);
+          }
+          wait_or_abort(bar_m1, c & 1, s_abort, prm.status);
+          tc_fence_after();
+          tmem_ld16_async(lanes + TM_KU + 16 * cg, w);
+          tmem_wait_ld();
+          tmem_tie<16>(w);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) u[i] = f * (u[i] + __uint_as_float(w[i]));
-            put8(rhi, rlo, swz_offset(64, row, cl + e), u);
-            put8(rhi, rlo, swz_offset(64, row, cl + e + 8), u + 8);
+          for (int i = 0; i < 8; ++i)
+            x[i] = fma2(f1[i], make_float2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1])), x[i]);
+          if (valid < kC) {   // k S there may be anything
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              if (16 * cg + 2 * i >= valid) x[i].x = 0.f;
+              if (16 * cg + 2 * i + 1 >= valid) x[i].y = 0.f;
+            }
+          }
+          store_r(x);
+        }
+        {   // U'^T = 2^x e^(b_63 - b)/|k| (L R)^T
+          uint32_t w[16];
+          if (tid == 0) bulk_wait_read();   // the last chunk's output rows have left their tile
+          wait_or_abort(bar_m2, c & 1, s_abort, prm.status);
+          tc_fence_after();
+          tmem_ld16_async(lanes + TM_U + 16 * cg, w);
+#pragma unroll
+          for (int i = 0; i < 8; i += 2) {
+            const float4 f = *reinterpret_cast<const float4 *>(vec + kVecS + 16 * cg + 2 * i);
+            x[i] = make_float2(f.x, f.y);
+            x[i + 1] = make_float2(f.z, f.w);
+          }
+          tmem_wait_ld();
+          tmem_tie<16>(w);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) x[i] = mul2(x[i], make_float2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1])));
+          store_r(x);
+        }
+        {   // beside the state's product: o^T = scale e^b/|q| (q S)^T + scale (P L R)^T, one channel of 16 tokens
+          uint32_t w[16], y[16];
+          tmem_ld16_async(lanes + TM_QS + 16 * cg, w);
+          tmem_ld16_async(lanes + TM_OT + 16 * cg, y);
+          tmem_wait_ld();
+          tmem_tie<16>(w);
+          tmem_tie<16>(y);
+          const float so = prm.scale * inv;
+          bar_wait(kBarW, kWorkers);   // the tile is free (thread 0 waited for its last store above)
+          uint8_t *ot = sm + OFF_OUT + 8192 * (d >> 6);
+#pragma unroll
+          for (int i = 0; i < 16; i += 4) {
+            const float4 f = *reinterpret_cast<const float4 *>(vec + kVecQ + 16 * cg + i);
+            const float ff[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+            for (int z = 0; z < 4; ++z)
+              *reinterpret_cast<uint16_t *>(ot + swz_offset(64, 16 * cg + i + z, d & 63)) =
+                  f32_to_bf16_bits(fmaf(ff[z], __uint_as_float(w[i + z]), so * __uint_as_float(y[i + z])));
           }
           fence_async_smem();
-          tc_fence_before();
-          bar_arrive(bar, 288);
-        } else {
-          const float f = vec[kVecQ + row - 64];
-#pragma unroll
-          for (int e = 0; e < 32; e += 16) {
-            float u[16];
-            load16(e, u);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) qs[e + i] = fmaf(f, qs[e + i], u[i]);
-          }
-          tc_fence_before();
-          bar_arrive(bar, 288);
-          if (row - 64 < valid) {
-            uint16_t *o = prm.out + static_cast<int64_t>(t0 + c * kC + row - 64) * prm.out_stride + h * kD + v0;
-#pragma unroll
-            for (int e = 0; e < 32; e += 8)
-              *reinterpret_cast<uint4 *>(o + e) = make_uint4(pack_bf16x2(qs[e], qs[e + 1]), pack_bf16x2(qs[e + 2], qs[e + 3]),
-                                                             pack_bf16x2(qs[e + 4], qs[e + 5]), pack_bf16x2(qs[e + 6], qs[e + 7]));
+          bar_wait(kBarW, kWorkers);
+          if (valid == kC) {
+            if (tid == 0) {
+              tma_store_3d(&prm.tout, 0, h, t0 + c * kC, sm + OFF_OUT);
+              tma_store_3d(&prm.tout, 64, h, t0 + c * kC, sm + OFF_OUT + 8192);
+              bulk_commit();
+            }
+          } else {   // a ragged last chunk: its own rows alone
+            for (int i = tid; i < valid * 16; i += kWorkers) {
+              const int r = i >> 4, cc = i & 15;
+              *reinterpret_cast<uint4 *>(prm.out + static_cast<int64_t>(t0 + c * kC + r) * prm.out_stride + h * kD + 8 * cc) =
+                  *reinterpret_cast<const uint4 *>(sm + OFF_OUT + swz_offset(64, r, 8 * cc));
+            }
           }
         }
-
-        const float gamma = vec[kVecGamma];
-        wait_or_abort(&m[2], c & 1, s_abort, prm.status);
-        tc_fence_after();
+        {   // S = e^(b_63) S + D
+          uint32_t w[32];
+          wait_or_abort(bar_m3, c & 1, s_abort, prm.status);
+          tc_fence_after();
+          tmem_ld16_async(lanes + TM_D + 32 * cg, w);
+          tmem_ld16_async(lanes + TM_D + 32 * cg + 16, w + 16);
+          tmem_wait_ld();
+          tmem_tie<32>(w);
+          const float2 g2 = make_float2(gamma, gamma), i2 = make_float2(inv, inv);
 #pragma unroll
-        for (int e = 0; e < 32; e += 16) {
-          float u[16];
-          load16(e, u);
-#pragma unroll
-          for (int i = 0; i < 16; ++i) S[e + i] = fmaf(gamma, S[e + i], u[i]);
+          for (int i = 0; i < 32; i += 2) {
+            const float2 y = fma2(g2, make_float2(S[i], S[i + 1]),
+                                  mul2(i2, make_float2(__uint_as_float(w[i]), __uint_as_float(w[i + 1]))));
+            S[i] = y.x;
+            S[i + 1] = y.y;
+          }
+          if (c + 1 < nchunks) store_s();
         }
-        if (c + 1 < nchunks) store_s();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar_empty[c & 1]);
       }
+      if (tid == 0) bulk_wait_all();
     }
     tc_fence_before();
     __syncthreads();
     if (warp == kProducer) {
       tc_fence_after();
-      tmem_dealloc(tmem, M::kTmemCols);
+      tmem_dealloc(tmem, kTmemCols);
     }
   }
   if (nchunks == 0 && tid == 0) grid_dependency_wait();
   if (worker) {
 #pragma unroll
-    for (int e = 0; e < 32; e += 4)
-      *reinterpret_cast<float4 *>(dst + row * kD + v0 + e) = make_float4(S[e], S[e + 1], S[e + 2], S[e + 3]);
+    for (int e = 0; e < 32; ++e) dst[(32 * cg + e) * kD + d] = S[e];
   }
 }
 
-template <int kG>
 cudaError_t launch_chain(const GdnPrefillParams &p, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(p.num_seqs) * p.Hv * (kG == 2 ? 1 : 2));
-  cfg.blockDim = dim3(ch::Map<kG>::kThreads);
-  cfg.dynamicSmemBytes = ch::Map<kG>::kSmemBytes;
+  cfg.gridDim = dim3(static_cast<unsigned>(p.num_seqs) * p.Hv);
+  cfg.blockDim = dim3(ch::kThreads);
+  cfg.dynamicSmemBytes = ch::kSmemBytes;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, gdn_chain_kernel<kG>, p);
+  return cudaLaunchKernelEx(&cfg, gdn_chain_kernel, p);
 }
 
 }  // namespace
@@ -757,19 +941,14 @@ cudaError_t launch_gdn_prefill(const GdnRecurrentArgs &a, const int32_t *cu_host
   if (const cudaError_t e = set_attributes_once(mu, done, [] {
         cudaError_t r = cudaFuncSetAttribute(gdn_intra_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, in::kSmemBytes);
         if (r == cudaSuccess)
-          r = cudaFuncSetAttribute(gdn_chain_kernel<1>, cudaFuncAttributeMaxDynamicSharedMemorySize, ch::Map<1>::kSmemBytes);
-        if (r == cudaSuccess)
-          r = cudaFuncSetAttribute(gdn_chain_kernel<2>, cudaFuncAttributeMaxDynamicSharedMemorySize, ch::Map<2>::kSmemBytes);
+          r = cudaFuncSetAttribute(gdn_chain_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, ch::kSmemBytes);
         return r;
       }))
     return e;
-  int dev = 0, sms = 0;
-  if (const cudaError_t e = cudaGetDevice(&dev)) return e;
-  if (const cudaError_t e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) return e;
   GdnPrefillParams p;
   const int total = cu_host[num_seqs], Hk = a.Hv / a.group;
   if (!make_token_map(&p.tq, a.q, Hk, total, a.qk_stride) || !make_token_map(&p.tk, a.k, Hk, total, a.qk_stride) ||
-      !make_token_map(&p.tv, a.v, a.Hv, total, a.v_stride))
+      !make_token_map(&p.tv, a.v, a.Hv, total, a.v_stride) || !make_token_map(&p.tout, a.out, a.Hv, total, a.out_stride))
     return cudaErrorInvalidValue;
   p.a = a.a; p.beta = a.beta;
   p.a_stride = a.a_stride; p.beta_stride = a.beta_stride;
@@ -795,9 +974,7 @@ cudaError_t launch_gdn_prefill(const GdnRecurrentArgs &a, const int32_t *cu_host
     blocks += static_cast<size_t>(slots) * a.Hv * kGdnBlkBytes;
     gdn_intra_kernel<<<static_cast<unsigned>(slots) * Hk, in::kThreads, in::kSmemBytes, stream>>>(p);
     if (const cudaError_t e = cudaGetLastError()) return e;
-    // one half of the value channels per CTA while that many CTAs have an SM each
-    const cudaError_t e = 2ll * ns * a.Hv <= sms ? launch_chain<1>(p, stream) : launch_chain<2>(p, stream);
-    if (e != cudaSuccess) return e;
+    if (const cudaError_t e = launch_chain(p, stream)) return e;
   }
   return cudaSuccess;
 }

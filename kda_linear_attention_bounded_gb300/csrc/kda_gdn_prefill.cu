@@ -43,19 +43,23 @@ constexpr int kC = 64;
 // a block: [L hi ; P L ; L lo] (192 rows x 64 tokens, fp16, 128-byte row swizzle) | factors
 constexpr uint32_t kBlkPL = 8192, kBlkL2 = 16384, kBlkVec = 24576;
 constexpr uint32_t kGdnBlkBytes = 26112;
-// factors (fp32): beta_i | beta_i e^(b_i) |k_i|^-1 | scale e^(b_r) |q_r|^-1 | 2^-x_i | 2^(x_i) e^(b_63 - b_i) |k_i|^-1 |
-// e^(b_63), with 2^(x_i) <= the norm of the raw key i < 2^(x_i + 1)
-constexpr int kVecB = 0, kVecK = 64, kVecQ = 128, kVecX = 192, kVecS = 256, kVecGamma = 320;
+// a chunk's keys times 2^-x as fp16: 64 rows x 128 channels in two 64-channel panels, 128-byte row swizzle
+constexpr uint32_t kGdnKeyBytes = 16384;
+// factors (fp32): beta_i | -beta_i e^(b_i) |k_i|^-1 | scale e^(b_r) |q_r|^-1 | 2^(x_i) e^(b_63 - b_i) |k_i|^-1 |
+// e^(b_63), with 2^(x_i) the largest power of two not above the raw key's largest entry
+constexpr int kVecB = 0, kVecK = 64, kVecQ = 128, kVecS = 192, kVecGamma = 256;
 constexpr int kGdnMaxSeqs = 1024;   // sequences per launch (longer batches are split on the host)
 
 struct GdnPrefillParams {
-  CUtensorMap tq, tk, tv, tout; // [tokens, H, 128] bf16, box 64 channels x 1 head x 64 tokens, 128-byte swizzle
+  CUtensorMap tq, tk, tv;       // [tokens, H, 128] bf16, box 64 channels x 1 head x 64 tokens, 128-byte swizzle
+  CUtensorMap tout;             // the output: box 32 channels x 1 head x 16 tokens, unswizzled
   const uint16_t *a, *beta;
   int64_t a_stride, beta_stride;
   const float *A_log, *dt_bias;
   float scale;
   int Hk, Hv, group;
   uint8_t *blocks;              // block (slot g, value head h) at blocks + (g Hv + h) kGdnBlkBytes
+  uint8_t *keys;                // fp16 keys (slot g, key head hk) at keys + (g Hk + hk) kGdnKeyBytes
   const int32_t *slot_ids;      // indexed by the sequence of the launch
   int num_slots;
   const float *state_in;
@@ -117,7 +121,7 @@ constexpr uint32_t OFF_P = 17408;        // P as two fp16 tiles (64 rows x 64, 1
 constexpr uint32_t OFF_BLK = 33792;      // the block's image
 constexpr uint32_t OFF_SMALL = OFF_BLK + kGdnBlkBytes;
 constexpr uint32_t SM_NORM = 0 /* [128]: 1 / |k_r|, 1 / |q_r| */, SM_BETA = 512, SM_BI = 768, SM_BF = 1024 /* b, whole and
-                   fractional part */, SM_UP = 1280 /* 2^-b */, SM_POW = 1536 /* 2^-x */, SM_BAR = 1792, SM_TMEM = 1808, SM_ABORT = 1812,
+                   fractional part */, SM_UP = 1280 /* 2^-b */, SM_POW = 1536 /* 2^x */, SM_BAR = 1792, SM_TMEM = 1808, SM_ABORT = 1812,
                    SM_END = 1824;
 constexpr uint32_t kSmemBytes = OFF_SMALL + SM_END + 1024;
 static_assert(OFF_P == 64 * kStride * 4 && OFF_P % 1024 == 0 && OFF_BLK == OFF_P + 16384, "shared memory map");
@@ -253,6 +257,35 @@ __global__ void __launch_bounds__(in::kThreads, 3) gdn_intra_kernel(const __grid
     mma_commit(bar_mma);
   }
   __syncwarp();
+  // ---- under it: the keys over a power of two as fp16 (four lanes a row, each the pieces lane % 4, + 4, .. of it);
+  // rows behind the sequence's end are 0
+  {
+    wait_or_abort(bar_in, 0, s_abort, prm.status);
+    const int r = tid >> 2;
+    uint8_t *dst = prm.keys + (static_cast<size_t>(slot) * prm.Hk + hk) * kGdnKeyBytes;
+    uint4 w[4];
+    uint32_t top = 0;   // the largest entry's bits without its sign (bf16 order is integer order)
+#pragma unroll
+    for (int y = 0; y < 4; ++y) {
+      w[y] = *reinterpret_cast<const uint4 *>(sm + OFF_KQ + swz_offset(128, r, 32 * y + 8 * (tid & 3)));
+      const uint32_t ws[4] = {w[y].x, w[y].y, w[y].z, w[y].w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) top = max(top, max(ws[e] & 0x7FFFu, (ws[e] >> 16) & 0x7FFFu));
+    }
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    const int field = min(max(static_cast<int>(top >> 7), 1), 253);   // its exponent (a zero key: any)
+    if ((tid & 3) == 0) s_pow[r] = r < valid ? __uint_as_float(static_cast<uint32_t>(field) << 23) : 1.f;
+    const float f = __uint_as_float(static_cast<uint32_t>(254 - field) << 23);
+#pragma unroll
+    for (int y = 0; y < 4; ++y) {
+      uint32_t ws[4] = {w[y].x, w[y].y, w[y].z, w[y].w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) ws[e] = r < valid ? pack_f16x2(mul2(unpack_bf16x2(ws[e]), make_float2(f, f))) : 0u;
+      *reinterpret_cast<uint4 *>(dst + swz_offset(64, r, 32 * y + 8 * (tid & 3))) = make_uint4(ws[0], ws[1], ws[2], ws[3]);
+    }
+    asm volatile("fence.proxy.async.global;" ::: "memory");   // the state pass fetches them with bulk copies
+  }
   const int q4 = warp & 3, ib = warp >> 2;   // TMEM lane quadrant, half of the 64 key columns
   const uint32_t lanes = tmem + (static_cast<uint32_t>(q4 * 32) << 16);
 
@@ -310,8 +343,6 @@ __global__ void __launch_bounds__(in::kThreads, 3) gdn_intra_kernel(const __grid
         for (int e = 0; e < 32; ++e) d = e == lane ? __uint_as_float(v[e]) : d;
         const int r = 32 * q4 + lane;
         s_norm[r] = (r & 63) < valid ? rsqrtf(d + kL2Eps) : 0.f;
-        // a power of two that brings the raw key's norm to [1/2, 1) or so (a zero key: any)
-        if (r < 64) s_pow[r] = r < valid ? __uint_as_float(__float_as_uint(rsqrtf(fmaxf(d, 1e-36f))) & 0x7F800000u) : 1.f;
       } else {
         // zeros above the diagonal of L's parts and of P L (the value heads of the group leave them): 6 blocks x 16
         // rows x two 16-byte pieces of each
@@ -384,10 +415,9 @@ __global__ void __launch_bounds__(in::kThreads, 3) gdn_intra_kernel(const __grid
             const int t = lane + e;
             const float eb = fast_exp2(s_bi[t]) * fast_exp2(s_bf[t]);
             vec[kVecB + t] = s_beta[t];
-            vec[kVecK + t] = s_beta[t] * s_norm[t] * eb;
+            vec[kVecK + t] = -s_beta[t] * s_norm[t] * eb;
             vec[kVecQ + t] = prm.scale * s_norm[64 + t] * eb;
-            vec[kVecX + t] = s_pow[t];
-            vec[kVecS + t] = s_norm[t] / s_pow[t] * fast_exp2((s_bi[63] - s_bi[t]) + (s_bf[63] - s_bf[t]));
+            vec[kVecS + t] = s_norm[t] * s_pow[t] * fast_exp2((s_bi[63] - s_bi[t]) + (s_bf[63] - s_bf[t]));
             if (t == 63) vec[kVecGamma] = eb;
           }
         }
@@ -524,23 +554,25 @@ __global__ void __launch_bounds__(in::kThreads, 3) gdn_intra_kernel(const __grid
 //   [U | OT] = R^T [L ; P L]^T  (R hi against [L hi ; P L], N = 128; R hi L lo, R lo L hi, N = 64; K = 64 tokens)
 //   U'^T = 2^x e^(b_63 - b)/|k| U,   o = scale e^b/|q| QS + scale OT
 //   D = U'^T (2^-x k)           (U' hi, U' lo; N = 128 channels, K = 64),          S = e^(b_63) S + D
+//   VT = v^T 1                  (an identity as the other operand: v in the lanes that need it)
 // Sixteen epilogue warps (warp w: lanes 32 (w % 4).., quarter w / 4 of the columns; 32 state entries a thread), one
 // issuing warp, one that feeds chunks through two stages and brings the next to L2.  The serial path of a chunk is
-// KU -> R -> U -> U' -> D -> S; what it does not need runs beside it: v^T and the fp16 keys under KU, QS under R's
-// epilogue, the output under D.
+// KU -> R -> U -> U' -> D -> S; what it does not need runs beside it: VT under S's epilogue, the scales under KU, QS under
+// R's epilogue, the output under D.
 namespace ch {
 constexpr int kWorkers = 512, kThreads = kWorkers + 64;
 constexpr int kIssuer = 16, kProducer = 17;   // warps
-constexpr uint32_t ST_V = 32768, ST_BLK = 49152, kStage = 75776;   // [k ; q] | v | block, a multiple of 1024
-constexpr uint32_t OFF_K16 = 2 * kStage;          // the chunk's keys in fp16 (64 rows x 128 channels, two panels)
-constexpr uint32_t OFF_OUT = OFF_K16 + 16384;     // output rows on their way out (two panels of 64 channels)
+constexpr uint32_t ST_V = 32768, ST_K16 = 49152, ST_BLK = 65536, kStage = 92160;   // [k ; q] | v | fp16 keys | block
+constexpr uint32_t kStageLoad = ST_BLK + kGdnBlkBytes;
+constexpr uint32_t OFF_ONE = 2 * kStage;          // identity, 64 x 64 bf16
+constexpr uint32_t OFF_OUT = OFF_ONE + 8192;      // output on its way out: 16 tokens x 32 channels a warp
 constexpr uint32_t OFF_SMALL = OFF_OUT + 16384;
-constexpr uint32_t SM_BAR = 0 /* full[2], empty[2], m1, m2, m3 */, SM_TMEM = 56, SM_ABORT = 60, SM_MAX = 64 /* [4][128] */,
-                   SM_END = 64 + 2048;
+constexpr uint32_t SM_BAR = 0 /* full[2], empty[2], m1, m2, m3, v */, SM_TMEM = 64, SM_ABORT = 68, SM_MAX = 128 /* [4][128] */,
+                   SM_END = 128 + 2048;
 constexpr uint32_t kSmemBytes = OFF_SMALL + SM_END + 1024;
-static_assert(kSmemBytes <= 232448 && kStage >= ST_BLK + kGdnBlkBytes && kStage % 1024 == 0, "shared memory map");
+static_assert(kSmemBytes <= 232448 && kStage >= kStageLoad && kStage % 1024 == 0, "shared memory map");
 constexpr uint32_t TM_KU = 0, TM_U = 64, TM_OT = 128, TM_QS = 192, TM_D = 0 /* 128 columns, over KU and U */,
-                   TM_S = 256 /* 2 x 64 */, TM_R = 384 /* 2 x 32 */, kTmemCols = 512;
+                   TM_S = 256 /* 2 x 64 */, TM_R = 384 /* 2 x 32 */, TM_V = 448, kTmemCols = 512;
 constexpr int kBarS = 1, kBarR = 2, kBarW = 3;   // named barriers: workers and issuer; workers alone
 }  // namespace ch
 
@@ -559,13 +591,19 @@ __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool a_mn_major, 
   return idesc_bf16(M, N, a_mn_major, b_mn_major) & ~((1u << 7) | (1u << 10));
 }
 
+// wait_or_abort for a whole warp: one lane polls
+__device__ __forceinline__ void warp_wait(uint64_t *bar, uint32_t parity, volatile uint32_t *abort_flag, uint32_t *status) {
+  if ((threadIdx.x & 31) == 0) wait_or_abort(bar, parity, abort_flag, status);
+  __syncwarp();
+}
+
 __global__ void __launch_bounds__(ch::kThreads, 1) gdn_chain_kernel(const __grid_constant__ GdnPrefillParams prm) {
   using namespace ch;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t *small = sm + OFF_SMALL;
   uint64_t *bar_full = reinterpret_cast<uint64_t *>(small + SM_BAR), *bar_empty = bar_full + 2;
-  uint64_t *bar_m1 = bar_full + 4, *bar_m2 = bar_full + 5, *bar_m3 = bar_full + 6;
+  uint64_t *bar_m1 = bar_full + 4, *bar_m2 = bar_full + 5, *bar_m3 = bar_full + 6, *bar_v = bar_full + 7;
   uint32_t *s_tmem = reinterpret_cast<uint32_t *>(small + SM_TMEM);
   volatile uint32_t *s_abort = reinterpret_cast<volatile uint32_t *>(small + SM_ABORT);
   float *s_max = reinterpret_cast<float *>(small + SM_MAX);
@@ -599,13 +637,20 @@ __global__ void __launch_bounds__(ch::kThreads, 1) gdn_chain_kernel(const __grid
   }
   if (nchunks > 0) {
     if (tid == 0) {
-      for (int i = 0; i < 7; ++i) mbar_init(&bar_full[i], i == 2 || i == 3 ? 16 : 1);
+      for (int i = 0; i < 8; ++i) mbar_init(&bar_full[i], i == 2 || i == 3 ? 16 : 1);
       *s_abort = 0;
       fence_mbar_init();
     }
     if (warp == kProducer) {
       tmem_alloc(s_tmem, kTmemCols);
       tmem_relinquish();
+    }
+    if (worker) {   // the identity: row tid / 8, the 16 bytes with columns 8 (tid % 8) ..
+      const int r = tid >> 3, pc = tid & 7, w = (r & 7) >> 1;
+      const uint32_t one = (r >> 3) != pc ? 0u : (r & 1) ? 0x3F800000u : 0x00003F80u;
+      *reinterpret_cast<uint4 *>(sm + OFF_ONE + swz_offset(64, r, 8 * pc)) =
+          make_uint4(w == 0 ? one : 0u, w == 1 ? one : 0u, w == 2 ? one : 0u, w == 3 ? one : 0u);
+      fence_async_smem();
     }
     tc_fence_before();
     __syncthreads();
@@ -615,6 +660,8 @@ __global__ void __launch_bounds__(ch::kThreads, 1) gdn_chain_kernel(const __grid
     if (warp == kProducer) {
       // ------------------------------------------------------------ chunk c's keys, queries, values and block -> stage
       if (lane == 0) {
+        const uint8_t *key = prm.keys + (static_cast<size_t>(first_slot(prm, n)) * prm.Hk + hk) * kGdnKeyBytes;
+        const size_t kstep = static_cast<size_t>(prm.Hk) * kGdnKeyBytes;
         const uint8_t *blk = prm.blocks + (static_cast<size_t>(first_slot(prm, n)) * prm.Hv + h) * kGdnBlkBytes;
         const size_t step = static_cast<size_t>(prm.Hv) * kGdnBlkBytes;
         int c = 0;
@@ -623,7 +670,7 @@ __global__ void __launch_bounds__(ch::kThreads, 1) gdn_chain_kernel(const __grid
           if (c >= 2) wait_or_abort(&bar_empty[s], ((c >> 1) - 1) & 1, s_abort, prm.status);
           if (*s_abort) break;
           uint8_t *st = sm + s * kStage;
-          mbar_arrive_expect_tx(&bar_full[s], ST_BLK + kGdnBlkBytes);
+          mbar_arrive_expect_tx(&bar_full[s], kStageLoad);
           const int tok = t0 + c * kC;
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
@@ -631,7 +678,11 @@ __global__ void __launch_bounds__(ch::kThreads, 1) gdn_chain_kernel(const __grid
             tma_load_3d(st + 16384 * x + 8192, &prm.tq, 64 * x, hk, tok, &bar_full[s]);
             tma_load_3d(st + ST_V + 8192 * x, &prm.tv, 64 * x, h, tok, &bar_full[s]);
           }
-          if (c == 0) grid_dependency_wait();   // the blocks are the intra-chunk grid's
+          if (c == 0) {   // the blocks and fp16 keys are the intra-chunk grid's
+            grid_dependency_wait();
+            asm volatile("fence.proxy.async.global;" ::: "memory");
+          }
+          bulk_load(st + ST_K16, key + c * kstep, kGdnKeyBytes, &bar_full[s]);
           bulk_load(st + ST_BLK, blk + c * step, kGdnBlkBytes, &bar_full[s]);
           if (c >= 1 && c + 1 < nchunks) {   // the next one to be fetched, into L2
             const int tok1 = tok + kC;
@@ -641,6 +692,7 @@ __global__ void __launch_bounds__(ch::kThreads, 1) gdn_chain_kernel(const __grid
               tma_prefetch_3d(&prm.tq, 64 * x, hk, tok1);
               tma_prefetch_3d(&prm.tv, 64 * x, h, tok1);
             }
+            bulk_prefetch(key + (c + 1) * kstep, kGdnKeyBytes);
             bulk_prefetch(blk + (c + 1) * step, kGdnBlkBytes);
           }
         }
@@ -652,14 +704,27 @@ __global__ void __launch_bounds__(ch::kThreads, 1) gdn_chain_kernel(const __grid
       // ------------------------------------------------------------ products
       constexpr uint32_t id1 = idesc_bf16(128, 64, false, false), id2w = idesc_f16(128, 128, false, false),
                          id2 = idesc_f16(128, 64, false, false), id3 = idesc_f16(128, 128, false, true);
-      const uint64_t k16 = smem_desc(smem_u32(sm + OFF_K16), 8192, 1024);   // rows = tokens: two 64-channel panels
+      constexpr uint32_t idv = idesc_bf16(128, 64, true, false);
+      const uint64_t one = desc_kmajor_base(smem_u32(sm + OFF_ONE));
       for (int c = 0; c < nchunks; ++c) {
         uint8_t *st = sm + (c & 1) * kStage;
+        const uint64_t vt = desc_mnmajor_base(smem_u32(st + ST_V), 64), k16 = desc_mnmajor_base(smem_u32(st + ST_K16), 64);
+        auto values = [&] {
+          wait_or_abort(&bar_full[c & 1], (c >> 1) & 1, s_abort, prm.status);
+          tc_fence_after();
+#pragma unroll
+          for (int k = 0; k < 4; ++k) mma_bf16(tmem + TM_V, vt + mnmajor_step(k), one + kmajor_step(64, k), idv, k > 0);
+          mma_commit(bar_v);
+        };
+        // (a ragged chunk's rows behind the end are cleared before S is announced)
+        const bool ragged = len - c * kC < kC;
+        if (lane == 0 && !ragged) values();
+        __syncwarp();
         const uint64_t kk = desc_kmajor_base(smem_u32(st)), qq = kk + desc_bytes(8192);
         const uint64_t l1 = desc_kmajor_base(smem_u32(st + ST_BLK)), l2 = l1 + desc_bytes(kBlkL2);
         bar_wait(kBarS, kWorkers + 32);   // S is in place, D has been read
         if (lane == 0) {
-          wait_or_abort(&bar_full[c & 1], (c >> 1) & 1, s_abort, prm.status);
+          if (ragged) values();
           tc_fence_after();
 #pragma unroll
           for (int p = 0; p < 2; ++p)
@@ -685,7 +750,7 @@ __global__ void __launch_bounds__(ch::kThreads, 1) gdn_chain_kernel(const __grid
           mma_commit(bar_m2);
         }
         __syncwarp();
-        bar_wait(kBarR, kWorkers + 32);   // U' and the fp16 keys are in place, U has been read
+        bar_wait(kBarR, kWorkers + 32);   // U' is in place, U has been read
         if (lane == 0) {
           tc_fence_after();
 #pragma unroll
@@ -700,7 +765,17 @@ __global__ void __launch_bounds__(ch::kThreads, 1) gdn_chain_kernel(const __grid
     } else {
       // ------------------------------------------------------------ epilogues
       const uint32_t lanes = tmem + (static_cast<uint32_t>(quad * 32) << 16);
-      auto store_s = [&] {   // this quarter of S -> its two parts
+      // this quarter of S -> its two parts, ahead of chunk c; v's rows behind a ragged chunk's end, which may hold
+      // anything, are cleared (0 x NaN is not 0; the fp16 keys there are 0)
+      auto store_s = [&](int c) {
+        const int valid = len - c * kC;
+        if (valid < kC) {
+          warp_wait(&bar_full[c & 1], (c >> 1) & 1, s_abort, prm.status);
+          for (int i = tid; i < (kC - valid) * 16; i += kWorkers)
+            *reinterpret_cast<uint4 *>(sm + (c & 1) * kStage + ST_V + swz_offset(64, valid + (i >> 4), 8 * (i & 15))) =
+                make_uint4(0, 0, 0, 0);
+          fence_async_smem();
+        }
         uint32_t p1[16], p2[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) split2(make_float2(S[2 * i], S[2 * i + 1]), p1[i], p2[i]);
@@ -727,7 +802,7 @@ __global__ void __launch_bounds__(ch::kThreads, 1) gdn_chain_kernel(const __grid
 #pragma unroll
         for (int i = 0; i < 4; ++i) all[i] = s_max[i * 128 + d];
       };
-      store_s();
+      store_s(0);
       float bound;   // of the channel's state in 2-norm
       {
         float ss = 0.f, all[4];
@@ -741,58 +816,37 @@ __global__ void __launch_bounds__(ch::kThreads, 1) gdn_chain_kernel(const __grid
         uint8_t *st = sm + (c & 1) * kStage;
         const float *vec = reinterpret_cast<const float *>(st + ST_BLK + kBlkVec);
         const int valid = min(kC, len - c * kC);
-        wait_or_abort(&bar_full[c & 1], (c >> 1) & 1, s_abort, prm.status);
+        warp_wait(&bar_full[c & 1], (c >> 1) & 1, s_abort, prm.status);
         // ---- under the product: v^T (this thread's channel of 16 tokens) and the channel's scale
         float2 x[8];
         float vm = 0.f;
         {
-          const uint8_t *vt = st + ST_V + 8192 * (d >> 6);
+          uint32_t w[16];
+          warp_wait(bar_v, c & 1, s_abort, prm.status);
+          tc_fence_after();
+          tmem_ld16_async(lanes + TM_V + 16 * cg, w);
+          tmem_wait_ld();
+          tmem_tie<16>(w);
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            const int t = 16 * cg + 2 * i;
-            x[i].x = bf16_bits_to_f32(*reinterpret_cast<const uint16_t *>(vt + swz_offset(64, t, d & 63)));
-            x[i].y = bf16_bits_to_f32(*reinterpret_cast<const uint16_t *>(vt + swz_offset(64, t + 1, d & 63)));
-          }
-          if (valid < kC) {   // rows behind the end belong to others
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              if (16 * cg + 2 * i >= valid) x[i].x = 0.f;
-              if (16 * cg + 2 * i + 1 >= valid) x[i].y = 0.f;
-            }
-          }
-#pragma unroll
-          for (int i = 0; i < 8; ++i) vm = fmaxf(vm, fmaxf(fabsf(x[i].x), fabsf(x[i].y)));
-        }
-        // the chunk's keys times 2^-x as fp16 (thread: row tid / 8, 16 channels); rows behind the end are 0
-        {
-          const int r = tid >> 3, c0 = 16 * (tid & 7);
-          const float f = r < valid ? vec[kVecX + r] : 0.f;
-#pragma unroll
-          for (int y = 0; y < 16; y += 8) {
-            uint4 w = *reinterpret_cast<const uint4 *>(st + swz_offset(128, r, c0 + y));
-            const float2 f2 = make_float2(f, f);
-            w.x = pack_f16x2(mul2(unpack_bf16x2(w.x), f2));
-            w.y = pack_f16x2(mul2(unpack_bf16x2(w.y), f2));
-            w.z = pack_f16x2(mul2(unpack_bf16x2(w.z), f2));
-            w.w = pack_f16x2(mul2(unpack_bf16x2(w.w), f2));
-            if (r >= valid) w = make_uint4(0, 0, 0, 0);
-            *reinterpret_cast<uint4 *>(sm + OFF_K16 + swz_offset(64, r, c0 + y)) = w;
+            x[i] = make_float2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+            vm = fmaxf(vm, fmaxf(fabsf(x[i].x), fabsf(x[i].y)));
           }
         }
-        fence_async_smem();
-        // the channel's scale: |R|, |U| <= |v| + |S| within the chunk < 2^(e + 1) -> below 2^14 (U' below 2^15); at most
-        // 2^90, which keeps the factors finite where a channel is zero so far
+        // the channel's scale: |R|, |U| <= |v| + |S| within the chunk < 2^(e + 1) -> below 2^14; at most 2^90, which keeps
+        // the factors finite where a channel is zero so far.  (64 tokens of |v| <= vm add at most 8 vm to |S|; a loose
+        // bound costs nothing until it is 2^15 times too large.)
         float sig, inv;
         const float gamma = vec[kVecGamma];
         {
           float all[4];
           share(vm, all);
           vm = fmaxf(fmaxf(all[0], all[1]), fmaxf(all[2], all[3]));
-          const float most = vm + sqrtf(fmaf(bound, bound, 64.f * vm * vm));
+          const float most = fmaf(9.f, vm, bound);
           const int field = min(max(267 - static_cast<int>(__float_as_uint(most) >> 23 & 0xFF), 1), 217);
           sig = __uint_as_float(static_cast<uint32_t>(field) << 23);
           inv = __uint_as_float(static_cast<uint32_t>(254 - field) << 23);
-          bound = sqrtf(fmaf(gamma * bound, gamma * bound, 64.f * vm * vm));
+          bound = fmaf(gamma, bound, 8.f * vm);
         }
         const float2 sig2 = make_float2(sig, sig);
         {   // R^T = beta (v^T - e^b/|k| (k S)^T)
@@ -804,10 +858,10 @@ __global__ void __launch_bounds__(ch::kThreads, 1) gdn_chain_kernel(const __grid
             const float4 k = *reinterpret_cast<const float4 *>(vec + kVecK + 16 * cg + 2 * i);
             x[i] = mul2(mul2(x[i], sig2), make_float2(b.x, b.y));
             x[i + 1] = mul2(mul2(x[i + 1], sig2), make_float2(b.z, b.w));
-            f1[i] = mul2(make_float2(-k.x, -k.y), sig2);
-            f1[i + 1] = mul2(make_float2(-k.z, -k.w), sig2);
+            f1[i] = mul2(make_float2(k.x, k.y), sig2);
+            f1[i + 1] = mul2(make_float2(k.z, k.w), sig2);
           }
-          wait_or_abort(bar_m1, c & 1, s_abort, prm.status);
+          warp_wait(bar_m1, c & 1, s_abort, prm.status);
           tc_fence_after();
           tmem_ld16_async(lanes + TM_KU + 16 * cg, w);
           tmem_wait_ld();
@@ -826,8 +880,7 @@ __global__ void __launch_bounds__(ch::kThreads, 1) gdn_chain_kernel(const __grid
         }
         {   // U'^T = 2^x e^(b_63 - b)/|k| (L R)^T
           uint32_t w[16];
-          if (tid == 0) bulk_wait_read();   // the last chunk's output rows have left their tile
-          wait_or_abort(bar_m2, c & 1, s_abort, prm.status);
+          warp_wait(bar_m2, c & 1, s_abort, prm.status);
           tc_fence_after();
           tmem_ld16_async(lanes + TM_U + 16 * cg, w);
 #pragma unroll
@@ -849,56 +902,65 @@ __global__ void __launch_bounds__(ch::kThreads, 1) gdn_chain_kernel(const __grid
           tmem_wait_ld();
           tmem_tie<16>(w);
           tmem_tie<16>(y);
-          const float so = prm.scale * inv;
-          bar_wait(kBarW, kWorkers);   // the tile is free (thread 0 waited for its last store above)
-          uint8_t *ot = sm + OFF_OUT + 8192 * (d >> 6);
+          const float2 so = make_float2(prm.scale * inv, prm.scale * inv);
+          if (lane == 0) bulk_wait_read();   // the warp's last output has left its tile
+          __syncwarp();
+          uint16_t *ot = reinterpret_cast<uint16_t *>(sm + OFF_OUT + 1024 * warp) + lane;
 #pragma unroll
           for (int i = 0; i < 16; i += 4) {
             const float4 f = *reinterpret_cast<const float4 *>(vec + kVecQ + 16 * cg + i);
-            const float ff[4] = {f.x, f.y, f.z, f.w};
+            const float2 ff[2] = {make_float2(f.x, f.y), make_float2(f.z, f.w)};
 #pragma unroll
-            for (int z = 0; z < 4; ++z)
-              *reinterpret_cast<uint16_t *>(ot + swz_offset(64, 16 * cg + i + z, d & 63)) =
-                  f32_to_bf16_bits(fmaf(ff[z], __uint_as_float(w[i + z]), so * __uint_as_float(y[i + z])));
+            for (int z = 0; z < 4; z += 2) {
+              const uint32_t o2 = pack2(fma2(ff[z / 2], make_float2(__uint_as_float(w[i + z]), __uint_as_float(w[i + z + 1])),
+                                             mul2(so, make_float2(__uint_as_float(y[i + z]), __uint_as_float(y[i + z + 1])))));
+              ot[32 * (i + z)] = static_cast<uint16_t>(o2);
+              ot[32 * (i + z + 1)] = static_cast<uint16_t>(o2 >> 16);
+            }
           }
-          fence_async_smem();
-          bar_wait(kBarW, kWorkers);
-          if (valid == kC) {
-            if (tid == 0) {
-              tma_store_3d(&prm.tout, 0, h, t0 + c * kC, sm + OFF_OUT);
-              tma_store_3d(&prm.tout, 64, h, t0 + c * kC, sm + OFF_OUT + 8192);
+          const int rows = valid - 16 * cg;
+          if (rows >= 16) {
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              tma_store_3d(&prm.tout, 32 * quad, h, t0 + c * kC + 16 * cg, sm + OFF_OUT + 1024 * warp);
               bulk_commit();
             }
-          } else {   // a ragged last chunk: its own rows alone
-            for (int i = tid; i < valid * 16; i += kWorkers) {
-              const int r = i >> 4, cc = i & 15;
-              *reinterpret_cast<uint4 *>(prm.out + static_cast<int64_t>(t0 + c * kC + r) * prm.out_stride + h * kD + 8 * cc) =
-                  *reinterpret_cast<const uint4 *>(sm + OFF_OUT + swz_offset(64, r, 8 * cc));
-            }
+          } else {   // the end of a ragged chunk: its own rows alone
+            __syncwarp();
+            for (int i = lane; i < rows * 4; i += 32)
+              *reinterpret_cast<uint4 *>(prm.out + static_cast<int64_t>(t0 + c * kC + 16 * cg + (i >> 2)) * prm.out_stride +
+                                         h * kD + 32 * quad + 8 * (i & 3)) =
+                  *reinterpret_cast<const uint4 *>(sm + OFF_OUT + 1024 * warp + 64 * (i >> 2) + 16 * (i & 3));
           }
         }
         {   // S = e^(b_63) S + D
           uint32_t w[32];
-          wait_or_abort(bar_m3, c & 1, s_abort, prm.status);
+          const float2 g2 = make_float2(gamma, gamma), i2 = make_float2(inv, inv);
+#pragma unroll
+          for (int i = 0; i < 32; i += 2) {
+            const float2 y = mul2(g2, make_float2(S[i], S[i + 1]));
+            S[i] = y.x;
+            S[i + 1] = y.y;
+          }
+          warp_wait(bar_m3, c & 1, s_abort, prm.status);
           tc_fence_after();
           tmem_ld16_async(lanes + TM_D + 32 * cg, w);
           tmem_ld16_async(lanes + TM_D + 32 * cg + 16, w + 16);
           tmem_wait_ld();
           tmem_tie<32>(w);
-          const float2 g2 = make_float2(gamma, gamma), i2 = make_float2(inv, inv);
 #pragma unroll
           for (int i = 0; i < 32; i += 2) {
-            const float2 y = fma2(g2, make_float2(S[i], S[i + 1]),
-                                  mul2(i2, make_float2(__uint_as_float(w[i]), __uint_as_float(w[i + 1]))));
+            const float2 y = fma2(i2, make_float2(__uint_as_float(w[i]), __uint_as_float(w[i + 1])), make_float2(S[i], S[i + 1]));
             S[i] = y.x;
             S[i + 1] = y.y;
           }
-          if (c + 1 < nchunks) store_s();
+          if (c + 1 < nchunks) store_s(c + 1);
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar_empty[c & 1]);
       }
-      if (tid == 0) bulk_wait_all();
+      if (lane == 0) bulk_wait_all();
     }
     tc_fence_before();
     __syncthreads();
@@ -931,7 +993,8 @@ cudaError_t launch_chain(const GdnPrefillParams &p, cudaStream_t stream) {
 }  // namespace
 
 size_t gdn_prefill_workspace_bytes(int64_t total_tokens, int num_seqs, int Hv) {
-  return (total_tokens / kC + num_seqs) * static_cast<size_t>(Hv) * kGdnBlkBytes;
+  // (a key head for every value head at most)
+  return (total_tokens / kC + num_seqs) * static_cast<size_t>(Hv) * (kGdnBlkBytes + kGdnKeyBytes);
 }
 
 cudaError_t launch_gdn_prefill(const GdnRecurrentArgs &a, const int32_t *cu_host, int num_seqs, uint8_t *blocks,
@@ -948,7 +1011,7 @@ cudaError_t launch_gdn_prefill(const GdnRecurrentArgs &a, const int32_t *cu_host
   GdnPrefillParams p;
   const int total = cu_host[num_seqs], Hk = a.Hv / a.group;
   if (!make_token_map(&p.tq, a.q, Hk, total, a.qk_stride) || !make_token_map(&p.tk, a.k, Hk, total, a.qk_stride) ||
-      !make_token_map(&p.tv, a.v, a.Hv, total, a.v_stride) || !make_token_map(&p.tout, a.out, a.Hv, total, a.out_stride))
+      !make_token_map(&p.tv, a.v, a.Hv, total, a.v_stride) || !make_token_map(&p.tout, a.out, a.Hv, total, a.out_stride, false, 32, 16))
     return cudaErrorInvalidValue;
   p.a = a.a; p.beta = a.beta;
   p.a_stride = a.a_stride; p.beta_stride = a.beta_stride;
@@ -971,7 +1034,8 @@ cudaError_t launch_gdn_prefill(const GdnRecurrentArgs &a, const int32_t *cu_host
     std::stable_sort(p.order, p.order + ns, [&](int x, int y) { return p.cu[x + 1] - p.cu[x] > p.cu[y + 1] - p.cu[y]; });
     const int slots = (p.cu[ns] - p.cu[0]) / kC + ns;
     p.blocks = blocks;
-    blocks += static_cast<size_t>(slots) * a.Hv * kGdnBlkBytes;
+    p.keys = blocks + static_cast<size_t>(slots) * a.Hv * kGdnBlkBytes;
+    blocks = p.keys + static_cast<size_t>(slots) * Hk * kGdnKeyBytes;
     gdn_intra_kernel<<<static_cast<unsigned>(slots) * Hk, in::kThreads, in::kSmemBytes, stream>>>(p);
     if (const cudaError_t e = cudaGetLastError()) return e;
     if (const cudaError_t e = launch_chain(p, stream)) return e;

@@ -43,13 +43,14 @@ EncodeTiledFn encode_fn() {
 // [tokens, H, 128] bf16 with the given token stride; box = 64 channels x 1 head x 64 tokens, with the
 // 128-byte swizzle (the row-swizzled tile layout of the MMA operands and the output staging) or
 // unswizzled (tiles read only by CUDA cores); rows past the tensor's end read as zero
-bool make_token_map(CUtensorMap *map, const void *base, int H, int total_tokens, int64_t token_stride, bool swizzled) {
+bool make_token_map(CUtensorMap *map, const void *base, int H, int total_tokens, int64_t token_stride, bool swizzled,
+                    int box_channels, int box_tokens) {
   EncodeTiledFn enc = encode_fn();
   if (!enc) return false;
   cuuint64_t dims[3] = {static_cast<cuuint64_t>(kD), static_cast<cuuint64_t>(H),
                         static_cast<cuuint64_t>(std::max(total_tokens, 1))};
   cuuint64_t strides[2] = {static_cast<cuuint64_t>(kD * 2), static_cast<cuuint64_t>(token_stride * 2)};
-  cuuint32_t box[3] = {64, 1, static_cast<cuuint32_t>(kChunk)};
+  cuuint32_t box[3] = {static_cast<cuuint32_t>(box_channels), 1, static_cast<cuuint32_t>(box_tokens)};
   cuuint32_t estr[3] = {1, 1, 1};
   return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, estr,
              CU_TENSOR_MAP_INTERLEAVE_NONE, swizzled ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,

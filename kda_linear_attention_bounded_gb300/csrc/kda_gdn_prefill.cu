@@ -6,22 +6,22 @@
 //   A_ri = beta_r k^_r.k^_i e^(b_r - b_i)  (i < r),     L = (I + A)^-1
 //   P_ri = q^_r.k^_i e^(b_r - b_i)         (i <= r)
 //   R_i  = beta_i (v_i - e^(b_i) S^T k^_i),   U = L R
-//   o_r  = scale (e^(b_r) S^T q^_r + (P L R)_r),   S' = e^(b_63) S + sum_i e^(b_63 - b_i) k^_i U_i^T
+//   o_r  = scale (e^(b_r) S^T q^_r + (P U)_r),   S' = e^(b_63) S + sum_i e^(b_63 - b_i) k^_i U_i^T
 //
 // The decay is one number per token, so every product runs on the caller's own bf16 keys and queries and the norms
 // and decays are fp32 factors of rows and columns: nothing is rounded that the caller did not round.
 //
-// Two kernels.  The intra-chunk kernel forms L = (I + A)^-1 and P L of every (chunk, value head) at once: 25 KB a block
-// instead of the keys', queries' and values' products with them.  The state pass walks a sequence's chunks with S in
+// Two kernels.  The intra-chunk kernel forms L = (I + A)^-1 and P of every (chunk, value head) at once: 25 KB a block
+// instead of the keys', queries' and values' products with L.  The state pass walks a sequence's chunks with S in
 // fp32 registers, three products a chunk.
 //
 // Operands that are not the caller's data are pairs.  S is two bf16 (its rounding, 2^-18, is contracted by the chunk).
-// L, R and U are two fp16, 22 bits: |L| <= 1 and |P L| <= 1, since (I - beta k^ k^T) contracts; R and U carry a power
+// L, R and U are two fp16, 22 bits: |L| <= 1, since (I - beta k^ k^T) contracts, and |P| <= 1; R and U carry a power
 // of two per value channel that keeps them in fp16's range whatever the values are (from |v| and a bound on the
 // channel's state, |S_t|^2 <= |S_(t-1)|^2 + v_t^2); the keys they meet are the caller's, times a power of two per token
 // (exact down to 2^-17 of a key's norm).  Final states agree with the 64-bit recurrence to a few 1e-7, like an fp32
 // evaluation, where pairs of bf16 throughout leave 6e-6 and single bf16 operands a few 1e-3.  What only an output sees
-// is rounded once (P L to fp16, S to bf16).
+// is rounded once (P and its U to fp16, S to bf16).
 #include <cuda.h>
 
 #include <cuda_fp16.h>
@@ -40,26 +40,23 @@ namespace {
 using namespace sm100;
 
 constexpr int kC = 64;
-// a block: [L hi ; P L ; L lo] (192 rows x 64 tokens, fp16, 128-byte row swizzle) | factors
-constexpr uint32_t kBlkPL = 8192, kBlkL2 = 16384, kBlkVec = 24576;
+// a block: [L hi ; P ; L lo] (192 rows x 64 tokens, fp16, 128-byte row swizzle) | factors
+constexpr uint32_t kBlkP = 8192, kBlkL2 = 16384, kBlkVec = 24576;
 constexpr uint32_t kGdnBlkBytes = 26112;
-// a chunk's keys times 2^-x as fp16: 64 rows x 128 channels in two 64-channel panels, 128-byte row swizzle
-constexpr uint32_t kGdnKeyBytes = 16384;
-// factors (fp32): beta_i | -beta_i e^(b_i) |k_i|^-1 | scale e^(b_r) |q_r|^-1 | 2^(x_i) e^(b_63 - b_i) |k_i|^-1 |
-// e^(b_63), with 2^(x_i) the largest power of two not above the raw key's largest entry
-constexpr int kVecB = 0, kVecK = 64, kVecQ = 128, kVecS = 192, kVecGamma = 256;
+// factors (fp32): beta_i | -beta_i e^(b_i) |k_i|^-1 | scale e^(b_r) |q_r|^-1 | 2^-x_i | 2^(x_i) e^(b_63 - b_i) |k_i|^-1 |
+// e^(b_63), with 2^(x_i) the raw key's norm or up to twice that
+constexpr int kVecB = 0, kVecK = 64, kVecQ = 128, kVecX = 192, kVecS = 256, kVecGamma = 320;
 constexpr int kGdnMaxSeqs = 1024;   // sequences per launch (longer batches are split on the host)
 
 struct GdnPrefillParams {
   CUtensorMap tq, tk, tv;       // [tokens, H, 128] bf16, box 64 channels x 1 head x 64 tokens, 128-byte swizzle
-  CUtensorMap tout;             // the output: box 32 channels x 1 head x 16 tokens, unswizzled
+  CUtensorMap tout;             // the output: box 32 channels x 1 head x 16 tokens, 64-byte swizzle
   const uint16_t *a, *beta;
   int64_t a_stride, beta_stride;
   const float *A_log, *dt_bias;
   float scale;
   int Hk, Hv, group;
   uint8_t *blocks;              // block (slot g, value head h) at blocks + (g Hv + h) kGdnBlkBytes
-  uint8_t *keys;                // fp16 keys (slot g, key head hk) at keys + (g Hk + hk) kGdnKeyBytes
   const int32_t *slot_ids;      // indexed by the sequence of the launch
   int num_slots;
   const float *state_in;
@@ -77,19 +74,37 @@ static_assert(sizeof(GdnPrefillParams) <= 32764, "kernel parameters are limited 
 // each sequence its ceil(len / 64) slots whatever the lengths are.
 __host__ __device__ __forceinline__ int first_slot(const GdnPrefillParams &p, int n) { return (p.cu[n] - p.cu[0]) / kC + n; }
 
+// Waits for the phase; after about two seconds records the timeout in the status word and the CTA's abort flag, and later
+// waits return at once.  (The clock is read only after many tries: a wait that succeeds costs a handful of instructions.)
 __device__ __forceinline__ void wait_or_abort(uint64_t *bar, uint32_t parity, volatile uint32_t *abort_flag,
                                               uint32_t *status) {
-  if (mbar_try_wait(bar, parity) || *abort_flag) return;
-  if (!mbar_wait(bar, parity)) {
-    *abort_flag = 1;
-    atomicOr(status, KDA_DEVICE_TIMEOUT);
+  if (mbar_try_wait_suspend(bar, parity, 20000u)) return;
+  if (*abort_flag) return;
+  uint64_t t0 = 0;
+  for (uint32_t i = 1;; ++i) {
+    if (mbar_try_wait_suspend(bar, parity, 20000u)) return;
+    if ((i & 63u) == 0) {
+      const uint64_t t = globaltimer_ns();
+      if (t0 == 0) t0 = t;
+      if (t - t0 > 2000000000ull) break;
+    }
   }
+  *abort_flag = 1;
+  atomicOr(status, KDA_DEVICE_TIMEOUT);
 }
 
 __device__ __forceinline__ float2 sub2(float2 a, float2 b) {
   float2 d;
   asm("{\n\t.reg .b64 ra, rb, rd;\n\tmov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
       "sub.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 ra, rb, rd;\n\tmov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
+      "add.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
       : "=f"(d.x), "=f"(d.y)
       : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
   return d;
@@ -113,19 +128,18 @@ __device__ __forceinline__ void split2(float2 x, uint32_t &p1, uint32_t &p2) {
 
 // ================================================================ intra-chunk kernel
 namespace in {
-constexpr int kThreads = 256;   // 8 warps; three CTAs per SM
+constexpr int kThreads = 256;   // 8 warps; four CTAs per SM
 constexpr int kStride = 68;
 constexpr uint32_t OFF_KQ = 0;           // [k ; q], 128 rows x 128 channels: consumed by the first product; then
 constexpr uint32_t OFF_A = 0;            // A fp32 [64][68], turned into (I + A)^-1 in place
-constexpr uint32_t OFF_P = 17408;        // P as two fp16 tiles (64 rows x 64, 128-byte row swizzle)
-constexpr uint32_t OFF_BLK = 33792;      // the block's image
+constexpr uint32_t OFF_BLK = 17408;      // the block's image
 constexpr uint32_t OFF_SMALL = OFF_BLK + kGdnBlkBytes;
 constexpr uint32_t SM_NORM = 0 /* [128]: 1 / |k_r|, 1 / |q_r| */, SM_BETA = 512, SM_BI = 768, SM_BF = 1024 /* b, whole and
-                   fractional part */, SM_UP = 1280 /* 2^-b */, SM_POW = 1536 /* 2^x */, SM_BAR = 1792, SM_TMEM = 1808, SM_ABORT = 1812,
+                   fractional part */, SM_UP = 1280 /* 2^-b */, SM_POW = 1536 /* 2^-x */, SM_BAR = 1792, SM_TMEM = 1808, SM_ABORT = 1812,
                    SM_END = 1824;
 constexpr uint32_t kSmemBytes = OFF_SMALL + SM_END + 1024;
-static_assert(OFF_P == 64 * kStride * 4 && OFF_P % 1024 == 0 && OFF_BLK == OFF_P + 16384, "shared memory map");
-static_assert(3 * (kSmemBytes + 1024) <= 233472, "three CTAs per SM");
+static_assert(OFF_BLK == 64 * kStride * 4 && OFF_BLK % 1024 == 0 && OFF_SMALL >= 32768, "shared memory map");
+static_assert(4 * (kSmemBytes + 1024) <= 233472, "four CTAs per SM");
 constexpr uint32_t kTmemCols = 128;
 // Decays of a chunk down to 2^-kFactorRange are split into a row's and a column's factor (2^b_r and 2^-b_i stay far
 // inside fp32); beyond that each entry takes its own exponential.
@@ -179,27 +193,13 @@ __device__ __forceinline__ void st_tile_l(uint8_t *blk, int row0, int col0, cons
     *reinterpret_cast<uint32_t *>(at + kBlkL2) = p2;
   }
 }
-__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
-}
-__device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t addr) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
-}
-__device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-               : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
 // One CTA per (chunk slot, key head): the products of the chunk's keys and queries serve every value head of the group.
-// Bound by latency (short dependent phases on one chunk), hidden by three CTAs per SM; its traffic is the keys and
+// Bound by latency (short dependent phases on one chunk), hidden by four CTAs per SM; its traffic is the keys and
 // queries in and 25 KB a value head out.
-__global__ void __launch_bounds__(in::kThreads, 3) gdn_intra_kernel(const __grid_constant__ GdnPrefillParams prm) {
+__global__ void __launch_bounds__(in::kThreads, 4) gdn_intra_kernel(const __grid_constant__ GdnPrefillParams prm) {
   using namespace in;
   extern __shared__ uint8_t smem_raw[];
-  uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t *sm = smem_raw + (-smem_u32(smem_raw) & 1023u);   // (an offset, so that accesses stay shared-memory ones)
   uint8_t *small = sm + OFF_SMALL;
   float *s_norm = reinterpret_cast<float *>(small + SM_NORM);
   float *s_beta = reinterpret_cast<float *>(small + SM_BETA);
@@ -211,11 +211,11 @@ __global__ void __launch_bounds__(in::kThreads, 3) gdn_intra_kernel(const __grid
   uint64_t *bar_mma = bar_in + 1;
   uint32_t *s_tmem = reinterpret_cast<uint32_t *>(small + SM_TMEM);
   volatile uint32_t *s_abort = reinterpret_cast<volatile uint32_t *>(small + SM_ABORT);
-  uint8_t *s_blk = sm + OFF_BLK, *s_p = sm + OFF_P;
+  uint8_t *s_blk = sm + OFF_BLK;
   float *sA = reinterpret_cast<float *>(sm + OFF_A);
 
   grid_launch_dependents();   // the state pass may take SMs as this grid leaves them
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);   // (uniform in the warp)
   const int hk = blockIdx.x % prm.Hk, slot = blockIdx.x / prm.Hk;
   int n = 0;   // the slot's sequence: the last that starts at or before it
   for (int hi = prm.num_seqs - 1; n < hi;) {
@@ -257,35 +257,6 @@ __global__ void __launch_bounds__(in::kThreads, 3) gdn_intra_kernel(const __grid
     mma_commit(bar_mma);
   }
   __syncwarp();
-  // ---- under it: the keys over a power of two as fp16 (four lanes a row, each the pieces lane % 4, + 4, .. of it);
-  // rows behind the sequence's end are 0
-  {
-    wait_or_abort(bar_in, 0, s_abort, prm.status);
-    const int r = tid >> 2;
-    uint8_t *dst = prm.keys + (static_cast<size_t>(slot) * prm.Hk + hk) * kGdnKeyBytes;
-    uint4 w[4];
-    uint32_t top = 0;   // the largest entry's bits without its sign (bf16 order is integer order)
-#pragma unroll
-    for (int y = 0; y < 4; ++y) {
-      w[y] = *reinterpret_cast<const uint4 *>(sm + OFF_KQ + swz_offset(128, r, 32 * y + 8 * (tid & 3)));
-      const uint32_t ws[4] = {w[y].x, w[y].y, w[y].z, w[y].w};
-#pragma unroll
-      for (int e = 0; e < 4; ++e) top = max(top, max(ws[e] & 0x7FFFu, (ws[e] >> 16) & 0x7FFFu));
-    }
-    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-    top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-    const int field = min(max(static_cast<int>(top >> 7), 1), 253);   // its exponent (a zero key: any)
-    if ((tid & 3) == 0) s_pow[r] = r < valid ? __uint_as_float(static_cast<uint32_t>(field) << 23) : 1.f;
-    const float f = __uint_as_float(static_cast<uint32_t>(254 - field) << 23);
-#pragma unroll
-    for (int y = 0; y < 4; ++y) {
-      uint32_t ws[4] = {w[y].x, w[y].y, w[y].z, w[y].w};
-#pragma unroll
-      for (int e = 0; e < 4; ++e) ws[e] = r < valid ? pack_f16x2(mul2(unpack_bf16x2(ws[e]), make_float2(f, f))) : 0u;
-      *reinterpret_cast<uint4 *>(dst + swz_offset(64, r, 32 * y + 8 * (tid & 3))) = make_uint4(ws[0], ws[1], ws[2], ws[3]);
-    }
-    asm volatile("fence.proxy.async.global;" ::: "memory");   // the state pass fetches them with bulk copies
-  }
   const int q4 = warp & 3, ib = warp >> 2;   // TMEM lane quadrant, half of the 64 key columns
   const uint32_t lanes = tmem + (static_cast<uint32_t>(q4 * 32) << 16);
 
@@ -343,8 +314,10 @@ __global__ void __launch_bounds__(in::kThreads, 3) gdn_intra_kernel(const __grid
         for (int e = 0; e < 32; ++e) d = e == lane ? __uint_as_float(v[e]) : d;
         const int r = 32 * q4 + lane;
         s_norm[r] = (r & 63) < valid ? rsqrtf(d + kL2Eps) : 0.f;
+        // a power of two that brings the raw key's norm to (1/2, 1] (a zero key: any)
+        if (r < 64) s_pow[r] = r < valid ? __uint_as_float(__float_as_uint(rsqrtf(fmaxf(d, 1e-36f))) & 0x7F800000u) : 1.f;
       } else {
-        // zeros above the diagonal of L's parts and of P L (the value heads of the group leave them): 6 blocks x 16
+        // zeros above the diagonal of L's parts and of P (the value heads of the group leave them): 6 blocks x 16
         // rows x two 16-byte pieces of each
         for (int x = tid - 128; x < 3 * 192; x += 128) {
           const int which = x / 192, y = x % 192, b6 = y >> 5, rr = (y >> 1) & 15, hc = y & 1;
@@ -356,7 +329,7 @@ __global__ void __launch_bounds__(in::kThreads, 3) gdn_intra_kernel(const __grid
     }
     __syncthreads();
 
-    // ---- A (fp32) and P (fp16 pairs) from TMEM; the block's factors
+    // ---- A (fp32) and P (fp16) from TMEM; the block's factors
     {
       const bool is_p = q4 >= 2;
       const int r = (q4 & 1) * 32 + lane;
@@ -393,14 +366,9 @@ __global__ void __launch_bounds__(in::kThreads, 3) gdn_intra_kernel(const __grid
 #pragma unroll
           for (int e = 0; e < 8; ++e) x[e] = e0 + e < lim ? x[e] : 0.f;
           if (is_p) {
-            uint4 p1, p2;
-            split2h(make_float2(x[0], x[1]), p1.x, p2.x);
-            split2h(make_float2(x[2], x[3]), p1.y, p2.y);
-            split2h(make_float2(x[4], x[5]), p1.z, p2.z);
-            split2h(make_float2(x[6], x[7]), p1.w, p2.w);
-            uint8_t *at = s_p + swz_offset(64, r, 32 * ib + e0);
-            *reinterpret_cast<uint4 *>(at) = p1;
-            *reinterpret_cast<uint4 *>(at + 8192) = p2;
+            *reinterpret_cast<uint4 *>(s_blk + kBlkP + swz_offset(64, r, 32 * ib + e0)) =
+                make_uint4(pack_f16x2(make_float2(x[0], x[1])), pack_f16x2(make_float2(x[2], x[3])),
+                           pack_f16x2(make_float2(x[4], x[5])), pack_f16x2(make_float2(x[6], x[7])));
           } else {
             float *dst = sA + r * kStride + 32 * ib + e0;
             *reinterpret_cast<float4 *>(dst) = make_float4(x[0], x[1], x[2], x[3]);
@@ -417,7 +385,8 @@ __global__ void __launch_bounds__(in::kThreads, 3) gdn_intra_kernel(const __grid
             vec[kVecB + t] = s_beta[t];
             vec[kVecK + t] = -s_beta[t] * s_norm[t] * eb;
             vec[kVecQ + t] = prm.scale * s_norm[64 + t] * eb;
-            vec[kVecS + t] = s_norm[t] * s_pow[t] * fast_exp2((s_bi[63] - s_bi[t]) + (s_bf[63] - s_bf[t]));
+            vec[kVecX + t] = s_pow[t];
+            vec[kVecS + t] = s_norm[t] / s_pow[t] * fast_exp2((s_bi[63] - s_bi[t]) + (s_bf[63] - s_bf[t]));
             if (t == 63) vec[kVecGamma] = eb;
           }
         }
@@ -428,34 +397,29 @@ __global__ void __launch_bounds__(in::kThreads, 3) gdn_intra_kernel(const __grid
     // ---- L = (I + A)^-1: 16 x 16 diagonal inverses D_R by substitution, then
     //   L^-1_10 = -D_1 A_10 D_0,  L^-1_32 = -D_3 A_32 D_2,  L^-1 (rows 32.., cols ..31) = -I_2 A_(23,01) I_1
     // in place in the A tile, temporaries in its unused upper part; every block goes to L's parts as it is made.
-    {
-      // task (block R, column jc): lane q = lane % 4 of it carries rows q, q + 4, q + 8, q + 12
-      const int q = lane & 3, jc = 8 * (warp & 1) + (lane >> 2), R = warp >> 1;
-      const float *a = sA + (16 * R) * kStride + 16 * R;
-      float xs[4];
+    if (tid < 64) {   // thread = (block R, column jc)
+      const int R = tid >> 4, jc = tid & 15;
+      float *a = sA + (16 * R) * kStride + 16 * R;
+      float xs[16];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) xs[i] = 4 * i + q == jc ? 1.f : 0.f;
+      for (int r = 0; r < 16; ++r) {
+        float4 row[4];
 #pragma unroll
-      for (int m = 0; m < 15; ++m) {
-        const float xm = __shfl_sync(0xffffffffu, xs[m >> 2], (lane & ~3) | (m & 3));
+        for (int m = 0; m < r; m += 4) row[m / 4] = *reinterpret_cast<const float4 *>(a + r * kStride + m);
+        float acc[4] = {r == jc ? 1.f : 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int i = (m + 1) >> 2; i < 4; ++i) {
-          const int r = 4 * i + q;
-          if (r > m) xs[i] = fmaf(-a[r * kStride + m], xm, xs[i]);
+        for (int m = 0; m < r; ++m) {
+          const float am = m % 4 == 0 ? row[m / 4].x : m % 4 == 1 ? row[m / 4].y : m % 4 == 2 ? row[m / 4].z : row[m / 4].w;
+          acc[m & 3] = fmaf(-am, xs[m], acc[m & 3]);
         }
+        xs[r] = (acc[0] + acc[1]) + (acc[2] + acc[3]);
       }
-      switch (R) {   // both warps of the block have read its entries of A
-        case 0: named_bar_sync<1>(64); break;
-        case 1: named_bar_sync<2>(64); break;
-        case 2: named_bar_sync<3>(64); break;
-        default: named_bar_sync<4>(64); break;
-      }
+      __syncwarp();   // the block's entries of A have been read
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = 16 * R + 4 * i + q, c = 16 * R + jc;
-        sA[r * kStride + c] = xs[i];
+      for (int i = 0; i < 16; ++i) {
+        a[i * kStride + jc] = xs[i];
         const __half hi = __float2half_rn(xs[i]);
-        uint8_t *at = s_blk + swz_offset(64, r, c);
+        uint8_t *at = s_blk + swz_offset(64, 16 * R + i, 16 * R + jc);
         *reinterpret_cast<__half *>(at) = hi;
         *reinterpret_cast<__half *>(at + kBlkL2) = __float2half_rn(xs[i] - __half2float(hi));
       }
@@ -488,46 +452,6 @@ __global__ void __launch_bounds__(in::kThreads, 3) gdn_intra_kernel(const __grid
       else mm_tile<2>(d, sA + 32 * kStride + 32, sA + 32 + 8 * nj, lane);
       st_tile_l(s_blk, 32 + 16 * mi, 8 * nj, d, -1.f, lane);
     }
-    __syncthreads();
-    // ---- P L: ten 16 x 16 tiles on and below the diagonal, at most four 16-deep steps a warp.  P and L enter as pairs
-    // (with keys that are alike the sums cancel far below their terms); the result, which only outputs see, is rounded
-    // once.
-    {
-      auto tile = [&](int I, int J) {
-        float d0[4] = {0.f, 0.f, 0.f, 0.f}, d1[4] = {0.f, 0.f, 0.f, 0.f};
-        for (int kb = J; kb <= I; ++kb) {
-          uint32_t a[4], a2[4], b[4], b2[4];
-          const uint32_t at = smem_u32(s_p) + swz_offset(64, 16 * I + (lane & 15), 16 * kb + 8 * (lane >> 4));
-          const uint32_t bt = smem_u32(s_blk) + swz_offset(64, 16 * kb + (lane & 15), 16 * J + 8 * (lane >> 4));
-          ldsm4(a, at);
-          ldsm4_t(b, bt);
-          ldsm4(a2, at + 8192);
-          ldsm4_t(b2, bt + kBlkL2);
-          mma_16816(d0, a, b[0], b[1]);
-          mma_16816(d1, a, b[2], b[3]);
-          mma_16816(d0, a2, b[0], b[1]);
-          mma_16816(d1, a2, b[2], b[3]);
-          mma_16816(d0, a, b2[0], b2[1]);
-          mma_16816(d1, a, b2[2], b2[3]);
-        }
-        const int g = lane >> 2, c = 16 * J + 2 * (lane & 3);
-        uint8_t *pt = s_blk + kBlkPL;
-        *reinterpret_cast<uint32_t *>(pt + swz_offset(64, 16 * I + g, c)) = pack_f16x2(make_float2(d0[0], d0[1]));
-        *reinterpret_cast<uint32_t *>(pt + swz_offset(64, 16 * I + g + 8, c)) = pack_f16x2(make_float2(d0[2], d0[3]));
-        *reinterpret_cast<uint32_t *>(pt + swz_offset(64, 16 * I + g, c + 8)) = pack_f16x2(make_float2(d1[0], d1[1]));
-        *reinterpret_cast<uint32_t *>(pt + swz_offset(64, 16 * I + g + 8, c + 8)) = pack_f16x2(make_float2(d1[2], d1[3]));
-      };
-      switch (warp) {
-        case 0: tile(3, 0); break;
-        case 1: tile(2, 0); break;
-        case 2: tile(3, 1); break;
-        case 3: tile(1, 0); tile(0, 0); break;
-        case 4: tile(2, 1); tile(1, 1); break;
-        case 5: tile(3, 2); tile(2, 2); break;
-        case 6: tile(3, 3); break;
-        default: break;
-      }
-    }
     fence_async_smem();
     __syncthreads();
     if (tid == 0) {
@@ -548,32 +472,38 @@ __global__ void __launch_bounds__(in::kThreads, 3) gdn_intra_kernel(const __grid
 // ================================================================ state pass
 // CTA = (sequence, value head).  Products run transposed (TMEM lane = value channel, M = 128), so that the operands a
 // chunk makes (S, R, U) go back to TMEM in the lanes they were read from and only the caller's tiles and the block come
-// from shared memory (N columns, K deep; a 16-deep step takes 48 cycles at N = 64 and 70 at N = 128):
-//   KU = S^T k^T                (S hi, S lo; N = 64 tokens, K = 128 channels)      QS = S^T q^T (S hi)
+// from shared memory (a 16-deep step of N columns takes 32 cycles at N = 64 and 64 at N = 128, but one thread issues one
+// in 46: two warps issue, each to accumulators of its own that the epilogue adds):
+//   KU = S^T k^T                (S hi by one warp, S lo by the other; N = 64 tokens, K = 128 channels)
+//   QS = S^T q^T                (S hi)
 //   R^T = beta (v^T - e^b/|k| KU)
-//   [U | OT] = R^T [L ; P L]^T  (R hi against [L hi ; P L], N = 128; R hi L lo, R lo L hi, N = 64; K = 64 tokens)
-//   U'^T = 2^x e^(b_63 - b)/|k| U,   o = scale e^b/|q| QS + scale OT
+//   U = R^T L^T                 (R hi L hi, R hi L lo, R lo L hi; N = 64, K = 64 tokens)
+//   OT = U^T P^T                (U hi; N = 64, K = 64),   o = scale e^b/|q| QS + scale OT
+//   U'^T = 2^x e^(b_63 - b)/|k| U
 //   D = U'^T (2^-x k)           (U' hi, U' lo; N = 128 channels, K = 64),          S = e^(b_63) S + D
 //   VT = v^T 1                  (an identity as the other operand: v in the lanes that need it)
-// Sixteen epilogue warps (warp w: lanes 32 (w % 4).., quarter w / 4 of the columns; 32 state entries a thread), one
-// issuing warp, one that feeds chunks through two stages and brings the next to L2.  The serial path of a chunk is
-// KU -> R -> U -> U' -> D -> S; what it does not need runs beside it: VT under S's epilogue, the scales under KU, QS under
-// R's epilogue, the output under D.
+// Sixteen epilogue warps (warp w: lanes 32 (w % 4).., quarter w / 4 of the columns; 32 state entries a thread), the two
+// issuing warps, one that feeds chunks through two stages and brings the next to L2, and one that goes ahead of them all
+// over v for the channels' scales.  The serial path of a chunk is KU -> R -> U -> U' -> D -> S; what it does not need runs
+// beside it: VT under S's epilogue, QS under R's, the fp16 keys under U, OT and the output under D.
 namespace ch {
-constexpr int kWorkers = 512, kThreads = kWorkers + 64;
-constexpr int kIssuer = 16, kProducer = 17;   // warps
-constexpr uint32_t ST_V = 32768, ST_K16 = 49152, ST_BLK = 65536, kStage = 92160;   // [k ; q] | v | fp16 keys | block
+constexpr int kWorkers = 512, kThreads = kWorkers + 128;
+constexpr int kIssuer = 16, kProducer = 18, kScaler = 19;   // warps (two that issue)
+constexpr uint32_t ST_V = 32768, ST_BLK = 49152, kStage = 75776;   // [k ; q] | v | block, a multiple of 1024
 constexpr uint32_t kStageLoad = ST_BLK + kGdnBlkBytes;
 constexpr uint32_t OFF_ONE = 2 * kStage;          // identity, 64 x 64 bf16
-constexpr uint32_t OFF_OUT = OFF_ONE + 8192;      // output on its way out: 16 tokens x 32 channels a warp
+constexpr uint32_t OFF_K16 = OFF_ONE + 8192;      // the chunk's keys times 2^-x in fp16 (64 rows x 128 channels)
+constexpr uint32_t OFF_OUT = OFF_K16 + 16384;     // output on its way out: 16 tokens x 32 channels a warp, 64-byte swizzle
 constexpr uint32_t OFF_SMALL = OFF_OUT + 16384;
-constexpr uint32_t SM_BAR = 0 /* full[2], empty[2], m1, m2, m3, v */, SM_TMEM = 64, SM_ABORT = 68, SM_MAX = 128 /* [4][128] */,
-                   SM_END = 128 + 2048;
+constexpr uint32_t SM_BAR = 0 /* full[2], empty[2], scale[2], m1, m2, m3, v, o */, SM_TMEM = 96, SM_ABORT = 100,
+                   SM_SIG = 128 /* [2][128] */, SM_INV = 1152 /* [2][128] */, SM_END = 2176;
 constexpr uint32_t kSmemBytes = OFF_SMALL + SM_END + 1024;
 static_assert(kSmemBytes <= 232448 && kStage >= kStageLoad && kStage % 1024 == 0, "shared memory map");
-constexpr uint32_t TM_KU = 0, TM_U = 64, TM_OT = 128, TM_QS = 192, TM_D = 0 /* 128 columns, over KU and U */,
-                   TM_S = 256 /* 2 x 64 */, TM_R = 384 /* 2 x 32 */, TM_V = 448, kTmemCols = 512;
-constexpr int kBarS = 1, kBarR = 2, kBarW = 3;   // named barriers: workers and issuer; workers alone
+constexpr uint32_t TM_KU = 0 /* two of 64 */, TM_D = 0 /* 128, over KU */, TM_U = 128 /* two of 64 */, TM_OT = 128 /* over U */,
+                   TM_V = 192 /* over U */, TM_QS = 256, TM_S = 320 /* two of 64 */, TM_UH = 320 /* 32, over S */,
+                   TM_R = 448 /* two of 32 */, kTmemCols = 512;
+constexpr int kBarS = 1, kBarR = 2;   // named barriers of the workers and the issuing warps
+constexpr int kBarCount = kWorkers + 64;
 }  // namespace ch
 
 __device__ __forceinline__ void bar_arrive(int id, int count) { asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(count) : "memory"); }
@@ -586,28 +516,30 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t *v) {
                ::"r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
                : "memory");
 }
+// 16 lanes x 16 columns of 32 bits in the fragments of a 16 x 8 matrix product: registers 0, 1 and 2, 3 hold rows lane / 4
+// and lane / 4 + 8, columns 2 (lane % 4), + 1; registers 4 .. 7 the same of the next 8 columns
+__device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, uint32_t *r) {
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
+}
 // kind::f16 with fp16 operands
 __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool a_mn_major, bool b_mn_major) {
   return idesc_bf16(M, N, a_mn_major, b_mn_major) & ~((1u << 7) | (1u << 10));
 }
 
-// wait_or_abort for a whole warp: one lane polls
-__device__ __forceinline__ void warp_wait(uint64_t *bar, uint32_t parity, volatile uint32_t *abort_flag, uint32_t *status) {
-  if ((threadIdx.x & 31) == 0) wait_or_abort(bar, parity, abort_flag, status);
-  __syncwarp();
-}
-
 __global__ void __launch_bounds__(ch::kThreads, 1) gdn_chain_kernel(const __grid_constant__ GdnPrefillParams prm) {
   using namespace ch;
   extern __shared__ uint8_t smem_raw[];
-  uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t *sm = smem_raw + (-smem_u32(smem_raw) & 1023u);   // (an offset, so that accesses stay shared-memory ones)
   uint8_t *small = sm + OFF_SMALL;
   uint64_t *bar_full = reinterpret_cast<uint64_t *>(small + SM_BAR), *bar_empty = bar_full + 2;
-  uint64_t *bar_m1 = bar_full + 4, *bar_m2 = bar_full + 5, *bar_m3 = bar_full + 6, *bar_v = bar_full + 7;
+  uint64_t *bar_scale = bar_full + 4, *bar_m1 = bar_full + 6, *bar_m2 = bar_full + 7, *bar_m3 = bar_full + 8;
+  uint64_t *bar_v = bar_full + 9, *bar_o = bar_full + 10;
   uint32_t *s_tmem = reinterpret_cast<uint32_t *>(small + SM_TMEM);
   volatile uint32_t *s_abort = reinterpret_cast<volatile uint32_t *>(small + SM_ABORT);
-  float *s_max = reinterpret_cast<float *>(small + SM_MAX);
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  float *s_sig = reinterpret_cast<float *>(small + SM_SIG), *s_inv = reinterpret_cast<float *>(small + SM_INV);
+  const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);   // (uniform in the warp)
 
   const int h = blockIdx.x % prm.Hv, n = prm.order[blockIdx.x / prm.Hv], hk = h / prm.group;
   const int t0 = prm.cu[n], len = prm.cu[n + 1] - t0;
@@ -637,7 +569,8 @@ __global__ void __launch_bounds__(ch::kThreads, 1) gdn_chain_kernel(const __grid
   }
   if (nchunks > 0) {
     if (tid == 0) {
-      for (int i = 0; i < 8; ++i) mbar_init(&bar_full[i], i == 2 || i == 3 ? 16 : 1);
+      // (empty: the workers' warps and the scaler; the first two products: both issuing warps)
+      for (int i = 0; i < 11; ++i) mbar_init(&bar_full[i], i == 2 || i == 3 ? 17 : i == 6 || i == 7 ? 2 : 1);
       *s_abort = 0;
       fence_mbar_init();
     }
@@ -660,8 +593,6 @@ __global__ void __launch_bounds__(ch::kThreads, 1) gdn_chain_kernel(const __grid
     if (warp == kProducer) {
       // ------------------------------------------------------------ chunk c's keys, queries, values and block -> stage
       if (lane == 0) {
-        const uint8_t *key = prm.keys + (static_cast<size_t>(first_slot(prm, n)) * prm.Hk + hk) * kGdnKeyBytes;
-        const size_t kstep = static_cast<size_t>(prm.Hk) * kGdnKeyBytes;
         const uint8_t *blk = prm.blocks + (static_cast<size_t>(first_slot(prm, n)) * prm.Hv + h) * kGdnBlkBytes;
         const size_t step = static_cast<size_t>(prm.Hv) * kGdnBlkBytes;
         int c = 0;
@@ -678,11 +609,7 @@ __global__ void __launch_bounds__(ch::kThreads, 1) gdn_chain_kernel(const __grid
             tma_load_3d(st + 16384 * x + 8192, &prm.tq, 64 * x, hk, tok, &bar_full[s]);
             tma_load_3d(st + ST_V + 8192 * x, &prm.tv, 64 * x, h, tok, &bar_full[s]);
           }
-          if (c == 0) {   // the blocks and fp16 keys are the intra-chunk grid's
-            grid_dependency_wait();
-            asm volatile("fence.proxy.async.global;" ::: "memory");
-          }
-          bulk_load(st + ST_K16, key + c * kstep, kGdnKeyBytes, &bar_full[s]);
+          if (c == 0) grid_dependency_wait();   // the blocks are the intra-chunk grid's
           bulk_load(st + ST_BLK, blk + c * step, kGdnBlkBytes, &bar_full[s]);
           if (c >= 1 && c + 1 < nchunks) {   // the next one to be fetched, into L2
             const int tok1 = tok + kC;
@@ -692,7 +619,6 @@ __global__ void __launch_bounds__(ch::kThreads, 1) gdn_chain_kernel(const __grid
               tma_prefetch_3d(&prm.tq, 64 * x, hk, tok1);
               tma_prefetch_3d(&prm.tv, 64 * x, h, tok1);
             }
-            bulk_prefetch(key + (c + 1) * kstep, kGdnKeyBytes);
             bulk_prefetch(blk + (c + 1) * step, kGdnBlkBytes);
           }
         }
@@ -700,65 +626,125 @@ __global__ void __launch_bounds__(ch::kThreads, 1) gdn_chain_kernel(const __grid
         for (int i = max(0, c - 2); i < c; ++i) mbar_wait(&bar_full[i & 1], (i >> 1) & 1);
       }
       __syncwarp();
+    } else if (warp == kScaler) {
+      // ------------------------------------------------------------ the channels' scales, a chunk ahead
+      // |R|, |U| <= |v| + |S| within the chunk < 2^(e + 1) -> below 2^14 by a scale of at most 2^90 (which keeps the factors
+      // finite where a channel is zero so far).  64 tokens of |v| <= vm add at most 8 vm to |S|; a loose bound costs
+      // nothing until it is 2^15 times too large.  Lane: channels 2 lane, + 1, + 64, + 65.
+      float bound[4];   // of the channels' states in 2-norm
+      {
+        float ss[4] = {0.f, 0.f, 0.f, 0.f};
+        if (src)
+          for (int e = 0; e < kD; ++e) {
+            const float2 a = *reinterpret_cast<const float2 *>(src + e * kD + 2 * lane);
+            const float2 b = *reinterpret_cast<const float2 *>(src + e * kD + 64 + 2 * lane);
+            ss[0] = fmaf(a.x, a.x, ss[0]); ss[1] = fmaf(a.y, a.y, ss[1]);
+            ss[2] = fmaf(b.x, b.x, ss[2]); ss[3] = fmaf(b.y, b.y, ss[3]);
+          }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) bound[i] = sqrtf(ss[i]);
+      }
+      for (int c = 0; c < nchunks; ++c) {
+        const uint8_t *st = sm + (c & 1) * kStage;
+        const int valid = min(kC, len - c * kC);
+        wait_or_abort(&bar_full[c & 1], (c >> 1) & 1, s_abort, prm.status);
+        uint32_t top[2] = {0u, 0u};   // |v|'s bits (bf16 order is integer order)
+#pragma unroll 8
+        for (int t = 0; t < valid; ++t) {
+          const uint8_t *at = st + ST_V + swz_offset(64, t, 2 * lane);
+          top[0] = __vmaxu2(top[0], *reinterpret_cast<const uint32_t *>(at) & 0x7FFF7FFFu);
+          top[1] = __vmaxu2(top[1], *reinterpret_cast<const uint32_t *>(at + 8192) & 0x7FFF7FFFu);
+        }
+        const float gamma = reinterpret_cast<const float *>(st + ST_BLK + kBlkVec)[kVecGamma];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float vm = i & 1 ? __uint_as_float(top[i >> 1] & 0xFFFF0000u) : __uint_as_float(top[i >> 1] << 16);
+          const float most = fmaf(9.f, vm, bound[i]);
+          const int field = min(max(267 - static_cast<int>(__float_as_uint(most) >> 23 & 0xFF), 1), 217);
+          const int ch = 128 * (c & 1) + 64 * (i >> 1) + 2 * lane + (i & 1);
+          s_sig[ch] = __uint_as_float(static_cast<uint32_t>(field) << 23);
+          s_inv[ch] = __uint_as_float(static_cast<uint32_t>(254 - field) << 23);
+          bound[i] = fmaf(gamma, bound[i], 8.f * vm);
+        }
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&bar_scale[c & 1]);
+          mbar_arrive(&bar_empty[c & 1]);
+        }
+      }
     } else if (!worker) {
-      // ------------------------------------------------------------ products
-      constexpr uint32_t id1 = idesc_bf16(128, 64, false, false), id2w = idesc_f16(128, 128, false, false),
-                         id2 = idesc_f16(128, 64, false, false), id3 = idesc_f16(128, 128, false, true);
-      constexpr uint32_t idv = idesc_bf16(128, 64, true, false);
-      const uint64_t one = desc_kmajor_base(smem_u32(sm + OFF_ONE));
+      // ------------------------------------------------------------ products: this warp's accumulator of the pairs
+      const int me = warp - kIssuer;
+      constexpr uint32_t id1 = idesc_bf16(128, 64, false, false), id2 = idesc_f16(128, 64, false, false),
+                         id3 = idesc_f16(128, 128, false, true), idv = idesc_bf16(128, 64, true, false);
+      const uint64_t one = desc_kmajor_base(smem_u32(sm + OFF_ONE)), k16 = desc_mnmajor_base(smem_u32(sm + OFF_K16), 64);
+      const uint32_t ku = tmem + TM_KU + 64 * me, uu = tmem + TM_U + 64 * me, sp = tmem + TM_S + 64 * me;
       for (int c = 0; c < nchunks; ++c) {
         uint8_t *st = sm + (c & 1) * kStage;
-        const uint64_t vt = desc_mnmajor_base(smem_u32(st + ST_V), 64), k16 = desc_mnmajor_base(smem_u32(st + ST_K16), 64);
+        const uint64_t kk = desc_kmajor_base(smem_u32(st)), qq = kk + desc_bytes(8192), vt = desc_mnmajor_base(smem_u32(st + ST_V), 64);
+        const uint64_t l1 = desc_kmajor_base(smem_u32(st + ST_BLK)), pp = l1 + desc_bytes(kBlkP), l2 = l1 + desc_bytes(kBlkL2);
         auto values = [&] {
-          wait_or_abort(&bar_full[c & 1], (c >> 1) & 1, s_abort, prm.status);
-          tc_fence_after();
 #pragma unroll
           for (int k = 0; k < 4; ++k) mma_bf16(tmem + TM_V, vt + mnmajor_step(k), one + kmajor_step(64, k), idv, k > 0);
           mma_commit(bar_v);
         };
-        // (a ragged chunk's rows behind the end are cleared before S is announced)
+        // (a ragged chunk's rows behind the end are cleared before S is announced; D before, which values run behind)
         const bool ragged = len - c * kC < kC;
-        if (lane == 0 && !ragged) values();
-        __syncwarp();
-        const uint64_t kk = desc_kmajor_base(smem_u32(st)), qq = kk + desc_bytes(8192);
-        const uint64_t l1 = desc_kmajor_base(smem_u32(st + ST_BLK)), l2 = l1 + desc_bytes(kBlkL2);
-        bar_wait(kBarS, kWorkers + 32);   // S is in place, D has been read
         if (lane == 0) {
-          if (ragged) values();
-          tc_fence_after();
-#pragma unroll
-          for (int p = 0; p < 2; ++p)
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-              mma_bf16_tmem_a(tmem + TM_KU, tmem + TM_S + 64 * p + 8 * k, kk + kmajor_step(128, k), id1, p + k > 0);
-          mma_commit(bar_m1);
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-            mma_bf16_tmem_a(tmem + TM_QS, tmem + TM_S + 8 * k, qq + kmajor_step(128, k), id1, k > 0);
+          wait_or_abort(&bar_full[c & 1], (c >> 1) & 1, s_abort, prm.status);
+          if (me == 1 && !ragged) {
+            if (c > 0) wait_or_abort(bar_m3, (c - 1) & 1, s_abort, prm.status);
+            tc_fence_after();
+            values();
+          }
         }
         __syncwarp();
-        bar_wait(kBarR, kWorkers + 32);   // R is in place, KU has been read
+        bar_wait(kBarS, kBarCount);   // S is in place, D has been read
         if (lane == 0) {
           tc_fence_after();
+          if (me == 1 && ragged) values();
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            mma_bf16_tmem_a(tmem + TM_U, tmem + TM_R + 8 * k, l1 + kmajor_step(64, k), id2w, k > 0);
+          for (int k = 0; k < 8; ++k) mma_bf16_tmem_a(ku, sp + 8 * k, kk + kmajor_step(128, k), id1, k > 0);
+          mma_commit(bar_m1);
+          if (me == 1) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) mma_bf16_tmem_a(tmem + TM_U, tmem + TM_R + 8 * k, l2 + kmajor_step(64, k), id2, 1);
+            for (int k = 0; k < 8; ++k)
+              mma_bf16_tmem_a(tmem + TM_QS, tmem + TM_S + 8 * k, qq + kmajor_step(128, k), id1, k > 0);
+          }
+        }
+        __syncwarp();
+        bar_wait(kBarR, kBarCount);   // R is in place, KU and VT have been read
+        if (lane == 0) {
+          tc_fence_after();
+          if (me == 0) {   // R hi L hi, and half of R hi L lo
 #pragma unroll
-          for (int k = 0; k < 4; ++k) mma_bf16_tmem_a(tmem + TM_U, tmem + TM_R + 32 + 8 * k, l1 + kmajor_step(64, k), id2, 1);
+            for (int k = 0; k < 4; ++k) mma_bf16_tmem_a(uu, tmem + TM_R + 8 * k, l1 + kmajor_step(64, k), id2, k > 0);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) mma_bf16_tmem_a(uu, tmem + TM_R + 8 * k, l2 + kmajor_step(64, k), id2, 1);
+          } else {         // R lo L hi, and the other half
+#pragma unroll
+            for (int k = 0; k < 4; ++k) mma_bf16_tmem_a(uu, tmem + TM_R + 32 + 8 * k, l1 + kmajor_step(64, k), id2, k > 0);
+#pragma unroll
+            for (int k = 2; k < 4; ++k) mma_bf16_tmem_a(uu, tmem + TM_R + 8 * k, l2 + kmajor_step(64, k), id2, 1);
+          }
           mma_commit(bar_m2);
         }
         __syncwarp();
-        bar_wait(kBarR, kWorkers + 32);   // U' is in place, U has been read
+        bar_wait(kBarR, kBarCount);   // U, U' and the fp16 keys are in place, U's accumulators have been read
         if (lane == 0) {
           tc_fence_after();
+          if (me == 0) {
 #pragma unroll
-          for (int p = 0; p < 2; ++p)
+            for (int p = 0; p < 2; ++p)
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              mma_bf16_tmem_a(tmem + TM_D, tmem + TM_R + 32 * p + 8 * k, k16 + mnmajor_step(k), id3, p + k > 0);
-          mma_commit(bar_m3);
+              for (int k = 0; k < 4; ++k)
+                mma_bf16_tmem_a(tmem + TM_D, tmem + TM_R + 32 * p + 8 * k, k16 + mnmajor_step(k), id3, p + k > 0);
+            mma_commit(bar_m3);
+          } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) mma_bf16_tmem_a(tmem + TM_OT, tmem + TM_UH + 8 * k, pp + kmajor_step(64, k), id2, k > 0);
+            mma_commit(bar_o);
+          }
         }
         __syncwarp();
       }
@@ -766,11 +752,11 @@ __global__ void __launch_bounds__(ch::kThreads, 1) gdn_chain_kernel(const __grid
       // ------------------------------------------------------------ epilogues
       const uint32_t lanes = tmem + (static_cast<uint32_t>(quad * 32) << 16);
       // this quarter of S -> its two parts, ahead of chunk c; v's rows behind a ragged chunk's end, which may hold
-      // anything, are cleared (0 x NaN is not 0; the fp16 keys there are 0)
+      // anything, are cleared (0 x NaN is not 0; the fp16 keys there become 0)
       auto store_s = [&](int c) {
         const int valid = len - c * kC;
         if (valid < kC) {
-          warp_wait(&bar_full[c & 1], (c >> 1) & 1, s_abort, prm.status);
+          wait_or_abort(&bar_full[c & 1], (c >> 1) & 1, s_abort, prm.status);
           for (int i = tid; i < (kC - valid) * 16; i += kWorkers)
             *reinterpret_cast<uint4 *>(sm + (c & 1) * kStage + ST_V + swz_offset(64, valid + (i >> 4), 8 * (i & 15))) =
                 make_uint4(0, 0, 0, 0);
@@ -783,7 +769,7 @@ __global__ void __launch_bounds__(ch::kThreads, 1) gdn_chain_kernel(const __grid
         tmem_st16(lanes + TM_S + 64 + 16 * cg, p2);
         tmem_wait_st();
         tc_fence_before();
-        bar_arrive(kBarS, kWorkers + 32);
+        bar_arrive(kBarS, kBarCount);
       };
       auto store_r = [&](const float2 (&x)[8]) {   // 16 tokens of R or U' -> their two parts
         uint32_t p1[8], p2[8];
@@ -793,82 +779,50 @@ __global__ void __launch_bounds__(ch::kThreads, 1) gdn_chain_kernel(const __grid
         tmem_st8(lanes + TM_R + 32 + 8 * cg, p2);
         tmem_wait_st();
         tc_fence_before();
-        bar_arrive(kBarR, kWorkers + 32);
-      };
-      // the four threads of a value channel share one number each
-      auto share = [&](float mine, float (&all)[4]) {
-        s_max[cg * 128 + d] = mine;
-        bar_wait(kBarW, kWorkers);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) all[i] = s_max[i * 128 + d];
+        bar_arrive(kBarR, kBarCount);
       };
       store_s(0);
-      float bound;   // of the channel's state in 2-norm
-      {
-        float ss = 0.f, all[4];
-#pragma unroll
-        for (int e = 0; e < 32; ++e) ss = fmaf(S[e], S[e], ss);
-        share(ss, all);
-        bound = sqrtf((all[0] + all[1]) + (all[2] + all[3]));
-        bar_wait(kBarW, kWorkers);   // read by all before the first chunk's maxima
-      }
       for (int c = 0; c < nchunks; ++c) {
         uint8_t *st = sm + (c & 1) * kStage;
         const float *vec = reinterpret_cast<const float *>(st + ST_BLK + kBlkVec);
         const int valid = min(kC, len - c * kC);
-        warp_wait(&bar_full[c & 1], (c >> 1) & 1, s_abort, prm.status);
+        wait_or_abort(&bar_full[c & 1], (c >> 1) & 1, s_abort, prm.status);
         // ---- under the product: v^T (this thread's channel of 16 tokens) and the channel's scale
         float2 x[8];
-        float vm = 0.f;
-        {
-          uint32_t w[16];
-          warp_wait(bar_v, c & 1, s_abort, prm.status);
+        wait_or_abort(&bar_scale[c & 1], (c >> 1) & 1, s_abort, prm.status);
+        const float sig = s_sig[128 * (c & 1) + d], inv = s_inv[128 * (c & 1) + d], gamma = vec[kVecGamma];
+        const float2 sig2 = make_float2(sig, sig);
+        {   // R^T = beta (v^T - e^b/|k| (k S)^T)
+          uint32_t w[16], w2[16];
+          wait_or_abort(bar_v, c & 1, s_abort, prm.status);
           tc_fence_after();
           tmem_ld16_async(lanes + TM_V + 16 * cg, w);
           tmem_wait_ld();
           tmem_tie<16>(w);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            x[i] = make_float2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
-            vm = fmaxf(vm, fmaxf(fabsf(x[i].x), fabsf(x[i].y)));
-          }
-        }
-        // the channel's scale: |R|, |U| <= |v| + |S| within the chunk < 2^(e + 1) -> below 2^14; at most 2^90, which keeps
-        // the factors finite where a channel is zero so far.  (64 tokens of |v| <= vm add at most 8 vm to |S|; a loose
-        // bound costs nothing until it is 2^15 times too large.)
-        float sig, inv;
-        const float gamma = vec[kVecGamma];
-        {
-          float all[4];
-          share(vm, all);
-          vm = fmaxf(fmaxf(all[0], all[1]), fmaxf(all[2], all[3]));
-          const float most = fmaf(9.f, vm, bound);
-          const int field = min(max(267 - static_cast<int>(__float_as_uint(most) >> 23 & 0xFF), 1), 217);
-          sig = __uint_as_float(static_cast<uint32_t>(field) << 23);
-          inv = __uint_as_float(static_cast<uint32_t>(254 - field) << 23);
-          bound = fmaf(gamma, bound, 8.f * vm);
-        }
-        const float2 sig2 = make_float2(sig, sig);
-        {   // R^T = beta (v^T - e^b/|k| (k S)^T)
-          uint32_t w[16];
-          float2 f1[8];
-#pragma unroll
           for (int i = 0; i < 8; i += 2) {
             const float4 b = *reinterpret_cast<const float4 *>(vec + kVecB + 16 * cg + 2 * i);
-            const float4 k = *reinterpret_cast<const float4 *>(vec + kVecK + 16 * cg + 2 * i);
-            x[i] = mul2(mul2(x[i], sig2), make_float2(b.x, b.y));
-            x[i + 1] = mul2(mul2(x[i + 1], sig2), make_float2(b.z, b.w));
-            f1[i] = mul2(make_float2(k.x, k.y), sig2);
-            f1[i + 1] = mul2(make_float2(k.z, k.w), sig2);
+            x[i] = mul2(make_float2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1])), make_float2(b.x, b.y));
+            x[i + 1] = mul2(make_float2(__uint_as_float(w[2 * i + 2]), __uint_as_float(w[2 * i + 3])), make_float2(b.z, b.w));
           }
-          warp_wait(bar_m1, c & 1, s_abort, prm.status);
+          wait_or_abort(bar_m1, c & 1, s_abort, prm.status);
           tc_fence_after();
           tmem_ld16_async(lanes + TM_KU + 16 * cg, w);
+          tmem_ld16_async(lanes + TM_KU + 64 + 16 * cg, w2);
           tmem_wait_ld();
           tmem_tie<16>(w);
+          tmem_tie<16>(w2);
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            x[i] = fma2(f1[i], make_float2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1])), x[i]);
+          for (int i = 0; i < 8; i += 2) {
+            const float4 k = *reinterpret_cast<const float4 *>(vec + kVecK + 16 * cg + 2 * i);
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              const int j = i + y;
+              const float2 ku = add2(make_float2(__uint_as_float(w[2 * j]), __uint_as_float(w[2 * j + 1])),
+                                     make_float2(__uint_as_float(w2[2 * j]), __uint_as_float(w2[2 * j + 1])));
+              x[j] = mul2(fma2(y ? make_float2(k.z, k.w) : make_float2(k.x, k.y), ku, x[j]), sig2);
+            }
+          }
           if (valid < kC) {   // k S there may be anything
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
@@ -878,11 +832,30 @@ __global__ void __launch_bounds__(ch::kThreads, 1) gdn_chain_kernel(const __grid
           }
           store_r(x);
         }
-        {   // U'^T = 2^x e^(b_63 - b)/|k| (L R)^T
-          uint32_t w[16];
-          warp_wait(bar_m2, c & 1, s_abort, prm.status);
+        // ---- under U: the chunk's keys times 2^-x as fp16 (thread: row tid / 8, two pieces of 8 channels); rows behind
+        // the end are 0
+        {
+          const int r = tid >> 3, c0 = 8 * (tid & 7);
+          const float f = vec[kVecX + r];
+#pragma unroll
+          for (int y = 0; y < 128; y += 64) {
+            uint4 w = *reinterpret_cast<const uint4 *>(st + swz_offset(128, r, c0 + y));
+            const float2 f2 = make_float2(f, f);
+            w.x = pack_f16x2(mul2(unpack_bf16x2(w.x), f2));
+            w.y = pack_f16x2(mul2(unpack_bf16x2(w.y), f2));
+            w.z = pack_f16x2(mul2(unpack_bf16x2(w.z), f2));
+            w.w = pack_f16x2(mul2(unpack_bf16x2(w.w), f2));
+            if (r >= valid) w = make_uint4(0, 0, 0, 0);
+            *reinterpret_cast<uint4 *>(sm + OFF_K16 + swz_offset(64, r, c0 + y)) = w;
+          }
+          fence_async_smem();
+        }
+        {   // U^T = (L R)^T, its first part;  U'^T = 2^x e^(b_63 - b)/|k| U^T
+          uint32_t w[16], w2[16], uh[8];
+          wait_or_abort(bar_m2, c & 1, s_abort, prm.status);
           tc_fence_after();
           tmem_ld16_async(lanes + TM_U + 16 * cg, w);
+          tmem_ld16_async(lanes + TM_U + 64 + 16 * cg, w2);
 #pragma unroll
           for (int i = 0; i < 8; i += 2) {
             const float4 f = *reinterpret_cast<const float4 *>(vec + kVecS + 16 * cg + 2 * i);
@@ -891,32 +864,51 @@ __global__ void __launch_bounds__(ch::kThreads, 1) gdn_chain_kernel(const __grid
           }
           tmem_wait_ld();
           tmem_tie<16>(w);
+          tmem_tie<16>(w2);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) x[i] = mul2(x[i], make_float2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1])));
+          for (int i = 0; i < 8; ++i) {
+            const float2 u = add2(make_float2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1])),
+                                  make_float2(__uint_as_float(w2[2 * i]), __uint_as_float(w2[2 * i + 1])));
+            uh[i] = pack_f16x2(u);
+            x[i] = mul2(x[i], u);
+          }
+          tmem_st8(lanes + TM_UH + 8 * cg, uh);
           store_r(x);
         }
-        {   // beside the state's product: o^T = scale e^b/|q| (q S)^T + scale (P L R)^T, one channel of 16 tokens
+        {   // beside the state's product: o^T = scale e^b/|q| (q S)^T + scale (P U)^T.  Here a thread holds the fragments
+            // that stmatrix transposes: channels lane / 4 + 8 i, tokens 2 (lane % 4), + 1 (+ 8) of the warp's 32 x 16
+          if (lane == 0) bulk_wait_read();   // the warp's last output has left its tile
+          wait_or_abort(bar_o, c & 1, s_abort, prm.status);
+          tc_fence_after();
+          const uint32_t ot = smem_u32(sm + OFF_OUT + 1024 * warp);
+          const float2 f0 = *reinterpret_cast<const float2 *>(vec + kVecQ + 16 * cg + 2 * (lane & 3));
+          const float2 f1 = *reinterpret_cast<const float2 *>(vec + kVecQ + 16 * cg + 2 * (lane & 3) + 8);
           uint32_t w[16], y[16];
-          tmem_ld16_async(lanes + TM_QS + 16 * cg, w);
-          tmem_ld16_async(lanes + TM_OT + 16 * cg, y);
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf) {
+            tmem_ld_frag(lanes + (static_cast<uint32_t>(16 * hf) << 16) + TM_QS + 16 * cg, w + 8 * hf);
+            tmem_ld_frag(lanes + (static_cast<uint32_t>(16 * hf) << 16) + TM_OT + 16 * cg, y + 8 * hf);
+          }
           tmem_wait_ld();
           tmem_tie<16>(w);
           tmem_tie<16>(y);
-          const float2 so = make_float2(prm.scale * inv, prm.scale * inv);
-          if (lane == 0) bulk_wait_read();   // the warp's last output has left its tile
-          __syncwarp();
-          uint16_t *ot = reinterpret_cast<uint16_t *>(sm + OFF_OUT + 1024 * warp) + lane;
 #pragma unroll
-          for (int i = 0; i < 16; i += 4) {
-            const float4 f = *reinterpret_cast<const float4 *>(vec + kVecQ + 16 * cg + i);
-            const float2 ff[2] = {make_float2(f.x, f.y), make_float2(f.z, f.w)};
+          for (int hf = 0; hf < 2; ++hf) {   // 16 channels
+            const float *si = s_inv + 128 * (c & 1) + 32 * quad + 16 * hf + (lane >> 2);
+            const float s0 = prm.scale * si[0], s1 = prm.scale * si[8];
+            uint32_t p[4];   // (channels 0..7, tokens 0..7), (8..15, 0..7), (0..7, 8..15), (8..15, 8..15)
 #pragma unroll
-            for (int z = 0; z < 4; z += 2) {
-              const uint32_t o2 = pack2(fma2(ff[z / 2], make_float2(__uint_as_float(w[i + z]), __uint_as_float(w[i + z + 1])),
-                                             mul2(so, make_float2(__uint_as_float(y[i + z]), __uint_as_float(y[i + z + 1])))));
-              ot[32 * (i + z)] = static_cast<uint16_t>(o2);
-              ot[32 * (i + z + 1)] = static_cast<uint16_t>(o2 >> 16);
+            for (int i = 0; i < 4; ++i) {
+              const float2 q = make_float2(__uint_as_float(w[8 * hf + 2 * i]), __uint_as_float(w[8 * hf + 2 * i + 1]));
+              const float2 u = make_float2(__uint_as_float(y[8 * hf + 2 * i]), __uint_as_float(y[8 * hf + 2 * i + 1]));
+              const float ss = i & 1 ? s1 : s0;
+              p[i] = pack2(fma2(i & 2 ? f1 : f0, q, mul2(make_float2(ss, ss), u)));
             }
+            // lane: the address of token (lane & 7) + 8 (lane >> 4), channels 16 hf + 8 ((lane >> 3) & 1) ..
+            const int tk = (lane & 7) + 8 * (lane >> 4), ch = 2 * hf + ((lane >> 3) & 1);
+            asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};"
+                         ::"r"(ot + 64 * tk + ((ch ^ ((tk >> 1) & 3)) << 4)), "r"(p[0]), "r"(p[1]), "r"(p[2]), "r"(p[3])
+                         : "memory");
           }
           const int rows = valid - 16 * cg;
           if (rows >= 16) {
@@ -928,10 +920,12 @@ __global__ void __launch_bounds__(ch::kThreads, 1) gdn_chain_kernel(const __grid
             }
           } else {   // the end of a ragged chunk: its own rows alone
             __syncwarp();
-            for (int i = lane; i < rows * 4; i += 32)
-              *reinterpret_cast<uint4 *>(prm.out + static_cast<int64_t>(t0 + c * kC + 16 * cg + (i >> 2)) * prm.out_stride +
-                                         h * kD + 32 * quad + 8 * (i & 3)) =
-                  *reinterpret_cast<const uint4 *>(sm + OFF_OUT + 1024 * warp + 64 * (i >> 2) + 16 * (i & 3));
+            for (int i = lane; i < rows * 4; i += 32) {
+              const int tk = i >> 2, ch = i & 3;
+              *reinterpret_cast<uint4 *>(prm.out + static_cast<int64_t>(t0 + c * kC + 16 * cg + tk) * prm.out_stride + h * kD +
+                                         32 * quad + 8 * ch) =
+                  *reinterpret_cast<const uint4 *>(sm + OFF_OUT + 1024 * warp + 64 * tk + ((ch ^ ((tk >> 1) & 3)) << 4));
+            }
           }
         }
         {   // S = e^(b_63) S + D
@@ -943,7 +937,7 @@ __global__ void __launch_bounds__(ch::kThreads, 1) gdn_chain_kernel(const __grid
             S[i] = y.x;
             S[i + 1] = y.y;
           }
-          warp_wait(bar_m3, c & 1, s_abort, prm.status);
+          wait_or_abort(bar_m3, c & 1, s_abort, prm.status);
           tc_fence_after();
           tmem_ld16_async(lanes + TM_D + 32 * cg, w);
           tmem_ld16_async(lanes + TM_D + 32 * cg + 16, w + 16);
@@ -993,8 +987,7 @@ cudaError_t launch_chain(const GdnPrefillParams &p, cudaStream_t stream) {
 }  // namespace
 
 size_t gdn_prefill_workspace_bytes(int64_t total_tokens, int num_seqs, int Hv) {
-  // (a key head for every value head at most)
-  return (total_tokens / kC + num_seqs) * static_cast<size_t>(Hv) * (kGdnBlkBytes + kGdnKeyBytes);
+  return (total_tokens / kC + num_seqs) * static_cast<size_t>(Hv) * kGdnBlkBytes;
 }
 
 cudaError_t launch_gdn_prefill(const GdnRecurrentArgs &a, const int32_t *cu_host, int num_seqs, uint8_t *blocks,
@@ -1010,8 +1003,8 @@ cudaError_t launch_gdn_prefill(const GdnRecurrentArgs &a, const int32_t *cu_host
     return e;
   GdnPrefillParams p;
   const int total = cu_host[num_seqs], Hk = a.Hv / a.group;
-  if (!make_token_map(&p.tq, a.q, Hk, total, a.qk_stride) || !make_token_map(&p.tk, a.k, Hk, total, a.qk_stride) ||
-      !make_token_map(&p.tv, a.v, a.Hv, total, a.v_stride) || !make_token_map(&p.tout, a.out, a.Hv, total, a.out_stride, false, 32, 16))
+  if (!make_token_map(&p.tq, a.q, Hk, total, a.qk_stride, 128) || !make_token_map(&p.tk, a.k, Hk, total, a.qk_stride, 128) ||
+      !make_token_map(&p.tv, a.v, a.Hv, total, a.v_stride, 128) || !make_token_map(&p.tout, a.out, a.Hv, total, a.out_stride, 64, 32, 16))
     return cudaErrorInvalidValue;
   p.a = a.a; p.beta = a.beta;
   p.a_stride = a.a_stride; p.beta_stride = a.beta_stride;
@@ -1034,8 +1027,7 @@ cudaError_t launch_gdn_prefill(const GdnRecurrentArgs &a, const int32_t *cu_host
     std::stable_sort(p.order, p.order + ns, [&](int x, int y) { return p.cu[x + 1] - p.cu[x] > p.cu[y + 1] - p.cu[y]; });
     const int slots = (p.cu[ns] - p.cu[0]) / kC + ns;
     p.blocks = blocks;
-    p.keys = blocks + static_cast<size_t>(slots) * a.Hv * kGdnBlkBytes;
-    blocks = p.keys + static_cast<size_t>(slots) * Hk * kGdnKeyBytes;
+    blocks += static_cast<size_t>(slots) * a.Hv * kGdnBlkBytes;
     gdn_intra_kernel<<<static_cast<unsigned>(slots) * Hk, in::kThreads, in::kSmemBytes, stream>>>(p);
     if (const cudaError_t e = cudaGetLastError()) return e;
     if (const cudaError_t e = launch_chain(p, stream)) return e;

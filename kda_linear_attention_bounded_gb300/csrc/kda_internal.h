@@ -46,9 +46,9 @@ struct ShortConv {
 };
 
 // Tensor map of [tokens, H, 128] bf16 with the given token stride, box 64 channels (or fewer) x 1 head x 64 tokens (or
-// fewer), with the 128-byte swizzle (64 channels) or without; false where the driver refuses it.
+// fewer), swizzled by 128 or 64 bytes or not (0); false where the driver refuses it.
 bool make_token_map(CUtensorMap *map, const void *base, int H, int total_tokens, int64_t token_stride,
-                    bool swizzled = true, int box_channels = 64, int box_tokens = 64);
+                    int swizzle = 128, int box_channels = 64, int box_tokens = 64);
 
 // Arguments of the token-by-token kernel (verify).
 struct RecurrentArgs {

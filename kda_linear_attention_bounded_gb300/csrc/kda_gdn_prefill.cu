@@ -49,8 +49,7 @@ constexpr int kVecB = 0, kVecK = 64, kVecQ = 128, kVecX = 192, kVecS = 256, kVec
 constexpr int kGdnMaxSeqs = 1024;   // sequences per launch (longer batches are split on the host)
 
 struct GdnPrefillParams {
-  CUtensorMap tq, tk, tv;       // [tokens, H, 128] bf16, box 64 channels x 1 head x 64 tokens, 128-byte swizzle
-  CUtensorMap tout;             // the output: box 32 channels x 1 head x 16 tokens, 64-byte swizzle
+  CUtensorMap tq, tk, tv, tout; // [tokens, H, 128] bf16, box 64 channels x 1 head x 64 tokens, 128-byte swizzle
   const uint16_t *a, *beta;
   int64_t a_stride, beta_stride;
   const float *A_log, *dt_bias;
@@ -75,15 +74,16 @@ static_assert(sizeof(GdnPrefillParams) <= 32764, "kernel parameters are limited 
 __host__ __device__ __forceinline__ int first_slot(const GdnPrefillParams &p, int n) { return (p.cu[n] - p.cu[0]) / kC + n; }
 
 // Waits for the phase; after about two seconds records the timeout in the status word and the CTA's abort flag, and later
-// waits return at once.  (The clock is read only after many tries: a wait that succeeds costs a handful of instructions.)
+// waits return at once.  (The clock is read only after many tries.  All lanes of a warp wait: measured, a warp is back 70
+// cycles after the arrival so, 290 where one lane polls and the others wait for it.)
 __device__ __forceinline__ void wait_or_abort(uint64_t *bar, uint32_t parity, volatile uint32_t *abort_flag,
                                               uint32_t *status) {
-  if (mbar_try_wait_suspend(bar, parity, 20000u)) return;
+  if (mbar_try_wait(bar, parity)) return;
   if (*abort_flag) return;
   uint64_t t0 = 0;
   for (uint32_t i = 1;; ++i) {
-    if (mbar_try_wait_suspend(bar, parity, 20000u)) return;
-    if ((i & 63u) == 0) {
+    if (mbar_try_wait(bar, parity)) return;
+    if ((i & 255u) == 0) {
       const uint64_t t = globaltimer_ns();
       if (t0 == 0) t0 = t;
       if (t - t0 > 2000000000ull) break;
@@ -483,8 +483,8 @@ __global__ void __launch_bounds__(in::kThreads, 4) gdn_intra_kernel(const __grid
 //   D = U'^T (2^-x k)           (U' hi, U' lo; N = 128 channels, K = 64),          S = e^(b_63) S + D
 //   VT = v^T 1                  (an identity as the other operand: v in the lanes that need it)
 // Sixteen epilogue warps (warp w: lanes 32 (w % 4).., quarter w / 4 of the columns; 32 state entries a thread), the two
-// issuing warps, one that feeds chunks through two stages and brings the next to L2, and one that goes ahead of them all
-// over v for the channels' scales.  The serial path of a chunk is KU -> R -> U -> U' -> D -> S; what it does not need runs
+// issuing warps, one that feeds chunks through two stages, brings the next to L2 and stores the output, and one that goes
+// ahead of them all over v for the channels' scales.  The serial path of a chunk is KU -> R -> U -> U' -> D -> S; what it does not need runs
 // beside it: VT under S's epilogue, QS under R's, the fp16 keys under U, OT and the output under D.
 namespace ch {
 constexpr int kWorkers = 512, kThreads = kWorkers + 128;
@@ -493,23 +493,31 @@ constexpr uint32_t ST_V = 32768, ST_BLK = 49152, kStage = 75776;   // [k ; q] | 
 constexpr uint32_t kStageLoad = ST_BLK + kGdnBlkBytes;
 constexpr uint32_t OFF_ONE = 2 * kStage;          // identity, 64 x 64 bf16
 constexpr uint32_t OFF_K16 = OFF_ONE + 8192;      // the chunk's keys times 2^-x in fp16 (64 rows x 128 channels)
-constexpr uint32_t OFF_OUT = OFF_K16 + 16384;     // output on its way out: 16 tokens x 32 channels a warp, 64-byte swizzle
+constexpr uint32_t OFF_OUT = OFF_K16 + 16384;     // output on its way out (64 rows x 128 channels)
 constexpr uint32_t OFF_SMALL = OFF_OUT + 16384;
-constexpr uint32_t SM_BAR = 0 /* full[2], empty[2], scale[2], m1, m2, m3, v, o */, SM_TMEM = 96, SM_ABORT = 100,
-                   SM_SIG = 128 /* [2][128] */, SM_INV = 1152 /* [2][128] */, SM_END = 2176;
+constexpr uint32_t SM_BAR = 0 /* the barriers below */, SM_TMEM = 128, SM_ABORT = 132, SM_SIG = 256 /* [2][128] */, SM_INV = 1280 /* [2][128] */, SM_END = 2304;
+// mbarriers: landed in stage 0, 1; scales of even, odd chunks; products done (first, second, state's, v's, output's); output
+// tile free | the workers' warps: S, R, U' in place, stage done with, output in its tile
+enum { B_FULL = 0, B_SCALE = 2, B_M1 = 4, B_M2, B_M3, B_V, B_O, B_OUT, B_S, B_R, B_U, B_FREE, B_TILE, kBarriers };
 constexpr uint32_t kSmemBytes = OFF_SMALL + SM_END + 1024;
 static_assert(kSmemBytes <= 232448 && kStage >= kStageLoad && kStage % 1024 == 0, "shared memory map");
 constexpr uint32_t TM_KU = 0 /* two of 64 */, TM_D = 0 /* 128, over KU */, TM_U = 128 /* two of 64 */, TM_OT = 128 /* over U */,
                    TM_V = 192 /* over U */, TM_QS = 256, TM_S = 320 /* two of 64 */, TM_UH = 320 /* 32, over S */,
                    TM_R = 448 /* two of 32 */, kTmemCols = 512;
-constexpr int kBarS = 1, kBarR = 2;   // named barriers of the workers and the issuing warps
-constexpr int kBarCount = kWorkers + 64;
 }  // namespace ch
 
-__device__ __forceinline__ void bar_arrive(int id, int count) { asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(count) : "memory"); }
-__device__ __forceinline__ void bar_wait(int id, int count) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(count) : "memory"); }
 __device__ __forceinline__ void bulk_prefetch(const void *src, uint32_t bytes) {
   asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(reinterpret_cast<uint64_t>(src)), "r"(bytes) : "memory");
+}
+// one arrival for the warp, once its lanes' writes are done (no branch)
+__device__ __forceinline__ void warp_arrive(uint64_t *bar) {
+  __syncwarp();
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.eq.u32 p, %1, 0;\n\t"
+      "@p mbarrier.arrive.shared::cta.b64 _, [%0];\n\t}"
+      ::"r"(smem_u32(bar)), "r"(threadIdx.x & 31)
+      : "memory");
 }
 __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t *v) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
@@ -533,9 +541,7 @@ __global__ void __launch_bounds__(ch::kThreads, 1) gdn_chain_kernel(const __grid
   extern __shared__ uint8_t smem_raw[];
   uint8_t *sm = smem_raw + (-smem_u32(smem_raw) & 1023u);   // (an offset, so that accesses stay shared-memory ones)
   uint8_t *small = sm + OFF_SMALL;
-  uint64_t *bar_full = reinterpret_cast<uint64_t *>(small + SM_BAR), *bar_empty = bar_full + 2;
-  uint64_t *bar_scale = bar_full + 4, *bar_m1 = bar_full + 6, *bar_m2 = bar_full + 7, *bar_m3 = bar_full + 8;
-  uint64_t *bar_v = bar_full + 9, *bar_o = bar_full + 10;
+  uint64_t *bar = reinterpret_cast<uint64_t *>(small + SM_BAR);
   uint32_t *s_tmem = reinterpret_cast<uint32_t *>(small + SM_TMEM);
   volatile uint32_t *s_abort = reinterpret_cast<volatile uint32_t *>(small + SM_ABORT);
   float *s_sig = reinterpret_cast<float *>(small + SM_SIG), *s_inv = reinterpret_cast<float *>(small + SM_INV);
@@ -569,8 +575,7 @@ __global__ void __launch_bounds__(ch::kThreads, 1) gdn_chain_kernel(const __grid
   }
   if (nchunks > 0) {
     if (tid == 0) {
-      // (empty: the workers' warps and the scaler; the first two products: both issuing warps)
-      for (int i = 0; i < 11; ++i) mbar_init(&bar_full[i], i == 2 || i == 3 ? 17 : i == 6 || i == 7 ? 2 : 1);
+      for (int i = 0; i < kBarriers; ++i) mbar_init(&bar[i], i >= B_S ? 16 : i == B_M1 || i == B_M2 ? 2 : 1);   // (two issuers)
       *s_abort = 0;
       fence_mbar_init();
     }
@@ -591,39 +596,70 @@ __global__ void __launch_bounds__(ch::kThreads, 1) gdn_chain_kernel(const __grid
     const uint32_t tmem = *s_tmem;
 
     if (warp == kProducer) {
-      // ------------------------------------------------------------ chunk c's keys, queries, values and block -> stage
+      // ------------------------------------------------------------ chunks -> stages, output tiles -> the caller's rows
+      const uint8_t *blk = prm.blocks + (static_cast<size_t>(first_slot(prm, n)) * prm.Hv + h) * kGdnBlkBytes;
+      const size_t step = static_cast<size_t>(prm.Hv) * kGdnBlkBytes;
+      auto load = [&](int c) {
+        uint8_t *st = sm + (c & 1) * kStage;
+        uint64_t *full = &bar[B_FULL + (c & 1)];
+        mbar_arrive_expect_tx(full, kStageLoad);
+        const int tok = t0 + c * kC;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          tma_load_3d(st + 16384 * x, &prm.tk, 64 * x, hk, tok, full);
+          tma_load_3d(st + 16384 * x + 8192, &prm.tq, 64 * x, hk, tok, full);
+          tma_load_3d(st + ST_V + 8192 * x, &prm.tv, 64 * x, h, tok, full);
+        }
+        if (c == 0) grid_dependency_wait();   // the blocks are the intra-chunk grid's
+        bulk_load(st + ST_BLK, blk + c * step, kGdnBlkBytes, full);
+      };
       if (lane == 0) {
-        const uint8_t *blk = prm.blocks + (static_cast<size_t>(first_slot(prm, n)) * prm.Hv + h) * kGdnBlkBytes;
-        const size_t step = static_cast<size_t>(prm.Hv) * kGdnBlkBytes;
-        int c = 0;
-        for (; c < nchunks; ++c) {
-          const int s = c & 1;
-          if (c >= 2) wait_or_abort(&bar_empty[s], ((c >> 1) - 1) & 1, s_abort, prm.status);
-          if (*s_abort) break;
-          uint8_t *st = sm + s * kStage;
-          mbar_arrive_expect_tx(&bar_full[s], kStageLoad);
-          const int tok = t0 + c * kC;
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            tma_load_3d(st + 16384 * x, &prm.tk, 64 * x, hk, tok, &bar_full[s]);
-            tma_load_3d(st + 16384 * x + 8192, &prm.tq, 64 * x, hk, tok, &bar_full[s]);
-            tma_load_3d(st + ST_V + 8192 * x, &prm.tv, 64 * x, h, tok, &bar_full[s]);
+        load(0);
+        if (nchunks > 1) load(1);
+      }
+      __syncwarp();
+      for (int c = 0; c < nchunks; ++c) {
+        const int valid = min(kC, len - c * kC), tok = t0 + c * kC;
+        wait_or_abort(&bar[B_TILE], c & 1, s_abort, prm.status);   // chunk c's output is in its tile
+        if (valid == kC) {
+          if (lane == 0) {
+            tma_store_3d(&prm.tout, 0, h, tok, sm + OFF_OUT);
+            tma_store_3d(&prm.tout, 64, h, tok, sm + OFF_OUT + 8192);
+            bulk_commit();
           }
-          if (c == 0) grid_dependency_wait();   // the blocks are the intra-chunk grid's
-          bulk_load(st + ST_BLK, blk + c * step, kGdnBlkBytes, &bar_full[s]);
-          if (c >= 1 && c + 1 < nchunks) {   // the next one to be fetched, into L2
-            const int tok1 = tok + kC;
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              tma_prefetch_3d(&prm.tk, 64 * x, hk, tok1);
-              tma_prefetch_3d(&prm.tq, 64 * x, hk, tok1);
-              tma_prefetch_3d(&prm.tv, 64 * x, h, tok1);
-            }
-            bulk_prefetch(blk + (c + 1) * step, kGdnBlkBytes);
+        } else {   // a ragged last chunk: its own rows alone
+          for (int i = lane; i < valid * 16; i += 32) {
+            const int r = i >> 4, cc = i & 15;
+            *reinterpret_cast<uint4 *>(prm.out + static_cast<int64_t>(tok + r) * prm.out_stride + h * kD + 8 * cc) =
+                *reinterpret_cast<const uint4 *>(sm + OFF_OUT + swz_offset(64, r, 8 * cc));
           }
         }
-        // the copies that were issued last have landed before the CTA ends, whatever the others found
-        for (int i = max(0, c - 2); i < c; ++i) mbar_wait(&bar_full[i & 1], (i >> 1) & 1);
+        __syncwarp();
+        wait_or_abort(&bar[B_FREE], c & 1, s_abort, prm.status);   // chunk c is done with its stage
+        if (lane == 0) {
+          if (c + 2 < nchunks && !*s_abort) load(c + 2);
+          if (c + 3 < nchunks) {   // the one behind it, into L2
+            const int tok3 = tok + 3 * kC;
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              tma_prefetch_3d(&prm.tk, 64 * x, hk, tok3);
+              tma_prefetch_3d(&prm.tq, 64 * x, hk, tok3);
+              tma_prefetch_3d(&prm.tv, 64 * x, h, tok3);
+            }
+            bulk_prefetch(blk + (c + 3) * step, kGdnBlkBytes);
+          }
+          bulk_wait_read();
+          mbar_arrive(&bar[B_OUT]);   // the output tile is free
+        }
+        __syncwarp();
+      }
+      if (lane == 0) bulk_wait_all();
+      // (every chunk was waited for by the issuing warps; after a timeout the copies in flight are waited for here)
+      if (*s_abort) {
+        mbar_wait(&bar[B_FULL], 0);
+        mbar_wait(&bar[B_FULL + 1], 0);
+        mbar_wait(&bar[B_FULL], 1);
+        mbar_wait(&bar[B_FULL + 1], 1);
       }
       __syncwarp();
     } else if (warp == kScaler) {
@@ -632,6 +668,7 @@ __global__ void __launch_bounds__(ch::kThreads, 1) gdn_chain_kernel(const __grid
       // finite where a channel is zero so far).  64 tokens of |v| <= vm add at most 8 vm to |S|; a loose bound costs
       // nothing until it is 2^15 times too large.  Lane: channels 2 lane, + 1, + 64, + 65.
       float bound[4];   // of the channels' states in 2-norm
+      int field[4] = {300, 300, 300, 300};   // the scales' exponent fields
       {
         float ss[4] = {0.f, 0.f, 0.f, 0.f};
         if (src)
@@ -647,7 +684,7 @@ __global__ void __launch_bounds__(ch::kThreads, 1) gdn_chain_kernel(const __grid
       for (int c = 0; c < nchunks; ++c) {
         const uint8_t *st = sm + (c & 1) * kStage;
         const int valid = min(kC, len - c * kC);
-        wait_or_abort(&bar_full[c & 1], (c >> 1) & 1, s_abort, prm.status);
+        wait_or_abort(&bar[B_FULL + (c & 1)], (c >> 1) & 1, s_abort, prm.status);
         uint32_t top[2] = {0u, 0u};   // |v|'s bits (bf16 order is integer order)
 #pragma unroll 8
         for (int t = 0; t < valid; ++t) {
@@ -660,17 +697,17 @@ __global__ void __launch_bounds__(ch::kThreads, 1) gdn_chain_kernel(const __grid
         for (int i = 0; i < 4; ++i) {
           const float vm = i & 1 ? __uint_as_float(top[i >> 1] & 0xFFFF0000u) : __uint_as_float(top[i >> 1] << 16);
           const float most = fmaf(9.f, vm, bound[i]);
-          const int field = min(max(267 - static_cast<int>(__float_as_uint(most) >> 23 & 0xFF), 1), 217);
+          // (kept until it is too large, or 2^10 too small)
+          const int want = min(max(267 - static_cast<int>(__float_as_uint(most) >> 23 & 0xFF), 1), 217);
+          if (want < field[i] || want > field[i] + 10) field[i] = want;
           const int ch = 128 * (c & 1) + 64 * (i >> 1) + 2 * lane + (i & 1);
-          s_sig[ch] = __uint_as_float(static_cast<uint32_t>(field) << 23);
-          s_inv[ch] = __uint_as_float(static_cast<uint32_t>(254 - field) << 23);
+          s_sig[ch] = __uint_as_float(static_cast<uint32_t>(field[i]) << 23);
+          s_inv[ch] = __uint_as_float(static_cast<uint32_t>(254 - field[i]) << 23);
           bound[i] = fmaf(gamma, bound[i], 8.f * vm);
         }
         __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&bar_scale[c & 1]);
-          mbar_arrive(&bar_empty[c & 1]);
-        }
+        if (lane == 0) mbar_arrive(&bar[B_SCALE + (c & 1)]);   // (the workers wait for it, so their word that the stage is free
+                                                         // is this warp's too)
       }
     } else if (!worker) {
       // ------------------------------------------------------------ products: this warp's accumulator of the pairs
@@ -686,26 +723,24 @@ __global__ void __launch_bounds__(ch::kThreads, 1) gdn_chain_kernel(const __grid
         auto values = [&] {
 #pragma unroll
           for (int k = 0; k < 4; ++k) mma_bf16(tmem + TM_V, vt + mnmajor_step(k), one + kmajor_step(64, k), idv, k > 0);
-          mma_commit(bar_v);
+          mma_commit(&bar[B_V]);
         };
         // (a ragged chunk's rows behind the end are cleared before S is announced; D before, which values run behind)
         const bool ragged = len - c * kC < kC;
-        if (lane == 0) {
-          wait_or_abort(&bar_full[c & 1], (c >> 1) & 1, s_abort, prm.status);
-          if (me == 1 && !ragged) {
-            if (c > 0) wait_or_abort(bar_m3, (c - 1) & 1, s_abort, prm.status);
-            tc_fence_after();
-            values();
-          }
-        }
-        __syncwarp();
-        bar_wait(kBarS, kBarCount);   // S is in place, D has been read
-        if (lane == 0) {
+        wait_or_abort(&bar[B_FULL + (c & 1)], (c >> 1) & 1, s_abort, prm.status);
+        if (me == 1 && !ragged) {
+          if (c > 0) wait_or_abort(&bar[B_M3], (c - 1) & 1, s_abort, prm.status);
           tc_fence_after();
+          if (lane == 0) values();
+          __syncwarp();
+        }
+        wait_or_abort(&bar[B_S], c & 1, s_abort, prm.status);   // S is in place, D has been read
+        tc_fence_after();
+        if (lane == 0) {
           if (me == 1 && ragged) values();
 #pragma unroll
           for (int k = 0; k < 8; ++k) mma_bf16_tmem_a(ku, sp + 8 * k, kk + kmajor_step(128, k), id1, k > 0);
-          mma_commit(bar_m1);
+          mma_commit(&bar[B_M1]);
           if (me == 1) {
 #pragma unroll
             for (int k = 0; k < 8; ++k)
@@ -713,9 +748,9 @@ __global__ void __launch_bounds__(ch::kThreads, 1) gdn_chain_kernel(const __grid
           }
         }
         __syncwarp();
-        bar_wait(kBarR, kBarCount);   // R is in place, KU and VT have been read
+        wait_or_abort(&bar[B_R], c & 1, s_abort, prm.status);   // R is in place, KU and VT have been read
+        tc_fence_after();
         if (lane == 0) {
-          tc_fence_after();
           if (me == 0) {   // R hi L hi, and half of R hi L lo
 #pragma unroll
             for (int k = 0; k < 4; ++k) mma_bf16_tmem_a(uu, tmem + TM_R + 8 * k, l1 + kmajor_step(64, k), id2, k > 0);
@@ -727,24 +762,21 @@ __global__ void __launch_bounds__(ch::kThreads, 1) gdn_chain_kernel(const __grid
 #pragma unroll
             for (int k = 2; k < 4; ++k) mma_bf16_tmem_a(uu, tmem + TM_R + 8 * k, l2 + kmajor_step(64, k), id2, 1);
           }
-          mma_commit(bar_m2);
+          mma_commit(&bar[B_M2]);
         }
         __syncwarp();
-        bar_wait(kBarR, kBarCount);   // U, U' and the fp16 keys are in place, U's accumulators have been read
-        if (lane == 0) {
-          tc_fence_after();
-          if (me == 0) {
+        wait_or_abort(&bar[B_U], c & 1, s_abort, prm.status);   // U, U', the fp16 keys are in place, the accumulators read
+        tc_fence_after();
+        if (me == 0 && lane == 0) {
 #pragma unroll
-            for (int p = 0; p < 2; ++p)
+          for (int k = 0; k < 4; ++k) mma_bf16_tmem_a(tmem + TM_OT, tmem + TM_UH + 8 * k, pp + kmajor_step(64, k), id2, k > 0);
+          mma_commit(&bar[B_O]);
 #pragma unroll
-              for (int k = 0; k < 4; ++k)
-                mma_bf16_tmem_a(tmem + TM_D, tmem + TM_R + 32 * p + 8 * k, k16 + mnmajor_step(k), id3, p + k > 0);
-            mma_commit(bar_m3);
-          } else {
+          for (int p = 0; p < 2; ++p)
 #pragma unroll
-            for (int k = 0; k < 4; ++k) mma_bf16_tmem_a(tmem + TM_OT, tmem + TM_UH + 8 * k, pp + kmajor_step(64, k), id2, k > 0);
-            mma_commit(bar_o);
-          }
+            for (int k = 0; k < 4; ++k)
+              mma_bf16_tmem_a(tmem + TM_D, tmem + TM_R + 32 * p + 8 * k, k16 + mnmajor_step(k), id3, p + k > 0);
+          mma_commit(&bar[B_M3]);
         }
         __syncwarp();
       }
@@ -756,7 +788,7 @@ __global__ void __launch_bounds__(ch::kThreads, 1) gdn_chain_kernel(const __grid
       auto store_s = [&](int c) {
         const int valid = len - c * kC;
         if (valid < kC) {
-          wait_or_abort(&bar_full[c & 1], (c >> 1) & 1, s_abort, prm.status);
+          wait_or_abort(&bar[B_FULL + (c & 1)], (c >> 1) & 1, s_abort, prm.status);
           for (int i = tid; i < (kC - valid) * 16; i += kWorkers)
             *reinterpret_cast<uint4 *>(sm + (c & 1) * kStage + ST_V + swz_offset(64, valid + (i >> 4), 8 * (i & 15))) =
                 make_uint4(0, 0, 0, 0);
@@ -769,9 +801,9 @@ __global__ void __launch_bounds__(ch::kThreads, 1) gdn_chain_kernel(const __grid
         tmem_st16(lanes + TM_S + 64 + 16 * cg, p2);
         tmem_wait_st();
         tc_fence_before();
-        bar_arrive(kBarS, kBarCount);
+        warp_arrive(&bar[B_S]);
       };
-      auto store_r = [&](const float2 (&x)[8]) {   // 16 tokens of R or U' -> their two parts
+      auto store_r = [&](const float2 (&x)[8], int which) {   // 16 tokens of R or U' -> their two parts
         uint32_t p1[8], p2[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) split2h(x[i], p1[i], p2[i]);
@@ -779,22 +811,26 @@ __global__ void __launch_bounds__(ch::kThreads, 1) gdn_chain_kernel(const __grid
         tmem_st8(lanes + TM_R + 32 + 8 * cg, p2);
         tmem_wait_st();
         tc_fence_before();
-        bar_arrive(kBarR, kBarCount);
+        warp_arrive(&bar[which]);
       };
+      // S is kept times its channel's scale: announced with chunk 0's, and brought to the next chunk's where that differs
+      wait_or_abort(&bar[B_SCALE], 0, s_abort, prm.status);
+      float sig = s_sig[d];
+#pragma unroll
+      for (int e = 0; e < 32; ++e) S[e] *= sig;
       store_s(0);
       for (int c = 0; c < nchunks; ++c) {
         uint8_t *st = sm + (c & 1) * kStage;
         const float *vec = reinterpret_cast<const float *>(st + ST_BLK + kBlkVec);
         const int valid = min(kC, len - c * kC);
-        wait_or_abort(&bar_full[c & 1], (c >> 1) & 1, s_abort, prm.status);
-        // ---- under the product: v^T (this thread's channel of 16 tokens) and the channel's scale
+        wait_or_abort(&bar[B_FULL + (c & 1)], (c >> 1) & 1, s_abort, prm.status);
+        // ---- under the product: v^T (this thread's channel of 16 tokens)
         float2 x[8];
-        wait_or_abort(&bar_scale[c & 1], (c >> 1) & 1, s_abort, prm.status);
-        const float sig = s_sig[128 * (c & 1) + d], inv = s_inv[128 * (c & 1) + d], gamma = vec[kVecGamma];
+        const float gamma = vec[kVecGamma];
         const float2 sig2 = make_float2(sig, sig);
         {   // R^T = beta (v^T - e^b/|k| (k S)^T)
           uint32_t w[16], w2[16];
-          wait_or_abort(bar_v, c & 1, s_abort, prm.status);
+          wait_or_abort(&bar[B_V], c & 1, s_abort, prm.status);
           tc_fence_after();
           tmem_ld16_async(lanes + TM_V + 16 * cg, w);
           tmem_wait_ld();
@@ -802,10 +838,10 @@ __global__ void __launch_bounds__(ch::kThreads, 1) gdn_chain_kernel(const __grid
 #pragma unroll
           for (int i = 0; i < 8; i += 2) {
             const float4 b = *reinterpret_cast<const float4 *>(vec + kVecB + 16 * cg + 2 * i);
-            x[i] = mul2(make_float2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1])), make_float2(b.x, b.y));
-            x[i + 1] = mul2(make_float2(__uint_as_float(w[2 * i + 2]), __uint_as_float(w[2 * i + 3])), make_float2(b.z, b.w));
+            x[i] = mul2(mul2(make_float2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1])), sig2), make_float2(b.x, b.y));
+            x[i + 1] = mul2(mul2(make_float2(__uint_as_float(w[2 * i + 2]), __uint_as_float(w[2 * i + 3])), sig2), make_float2(b.z, b.w));
           }
-          wait_or_abort(bar_m1, c & 1, s_abort, prm.status);
+          wait_or_abort(&bar[B_M1], c & 1, s_abort, prm.status);
           tc_fence_after();
           tmem_ld16_async(lanes + TM_KU + 16 * cg, w);
           tmem_ld16_async(lanes + TM_KU + 64 + 16 * cg, w2);
@@ -820,7 +856,7 @@ __global__ void __launch_bounds__(ch::kThreads, 1) gdn_chain_kernel(const __grid
               const int j = i + y;
               const float2 ku = add2(make_float2(__uint_as_float(w[2 * j]), __uint_as_float(w[2 * j + 1])),
                                      make_float2(__uint_as_float(w2[2 * j]), __uint_as_float(w2[2 * j + 1])));
-              x[j] = mul2(fma2(y ? make_float2(k.z, k.w) : make_float2(k.x, k.y), ku, x[j]), sig2);
+              x[j] = fma2(y ? make_float2(k.z, k.w) : make_float2(k.x, k.y), ku, x[j]);
             }
           }
           if (valid < kC) {   // k S there may be anything
@@ -830,7 +866,7 @@ __global__ void __launch_bounds__(ch::kThreads, 1) gdn_chain_kernel(const __grid
               if (16 * cg + 2 * i + 1 >= valid) x[i].y = 0.f;
             }
           }
-          store_r(x);
+          store_r(x, B_R);
         }
         // ---- under U: the chunk's keys times 2^-x as fp16 (thread: row tid / 8, two pieces of 8 channels); rows behind
         // the end are 0
@@ -852,7 +888,7 @@ __global__ void __launch_bounds__(ch::kThreads, 1) gdn_chain_kernel(const __grid
         }
         {   // U^T = (L R)^T, its first part;  U'^T = 2^x e^(b_63 - b)/|k| U^T
           uint32_t w[16], w2[16], uh[8];
-          wait_or_abort(bar_m2, c & 1, s_abort, prm.status);
+          wait_or_abort(&bar[B_M2], c & 1, s_abort, prm.status);
           tc_fence_after();
           tmem_ld16_async(lanes + TM_U + 16 * cg, w);
           tmem_ld16_async(lanes + TM_U + 64 + 16 * cg, w2);
@@ -873,14 +909,13 @@ __global__ void __launch_bounds__(ch::kThreads, 1) gdn_chain_kernel(const __grid
             x[i] = mul2(x[i], u);
           }
           tmem_st8(lanes + TM_UH + 8 * cg, uh);
-          store_r(x);
+          store_r(x, B_U);
         }
         {   // beside the state's product: o^T = scale e^b/|q| (q S)^T + scale (P U)^T.  Here a thread holds the fragments
             // that stmatrix transposes: channels lane / 4 + 8 i, tokens 2 (lane % 4), + 1 (+ 8) of the warp's 32 x 16
-          if (lane == 0) bulk_wait_read();   // the warp's last output has left its tile
-          wait_or_abort(bar_o, c & 1, s_abort, prm.status);
+          wait_or_abort(&bar[B_O], c & 1, s_abort, prm.status);
           tc_fence_after();
-          const uint32_t ot = smem_u32(sm + OFF_OUT + 1024 * warp);
+          const uint32_t ot = smem_u32(sm + OFF_OUT + 8192 * (quad >> 1));
           const float2 f0 = *reinterpret_cast<const float2 *>(vec + kVecQ + 16 * cg + 2 * (lane & 3));
           const float2 f1 = *reinterpret_cast<const float2 *>(vec + kVecQ + 16 * cg + 2 * (lane & 3) + 8);
           uint32_t w[16], y[16];
@@ -895,49 +930,35 @@ __global__ void __launch_bounds__(ch::kThreads, 1) gdn_chain_kernel(const __grid
 #pragma unroll
           for (int hf = 0; hf < 2; ++hf) {   // 16 channels
             const float *si = s_inv + 128 * (c & 1) + 32 * quad + 16 * hf + (lane >> 2);
-            const float s0 = prm.scale * si[0], s1 = prm.scale * si[8];
+            const float2 s0 = make_float2(si[0], si[0]), s1 = make_float2(si[8], si[8]);
             uint32_t p[4];   // (channels 0..7, tokens 0..7), (8..15, 0..7), (0..7, 8..15), (8..15, 8..15)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               const float2 q = make_float2(__uint_as_float(w[8 * hf + 2 * i]), __uint_as_float(w[8 * hf + 2 * i + 1]));
               const float2 u = make_float2(__uint_as_float(y[8 * hf + 2 * i]), __uint_as_float(y[8 * hf + 2 * i + 1]));
-              const float ss = i & 1 ? s1 : s0;
-              p[i] = pack2(fma2(i & 2 ? f1 : f0, q, mul2(make_float2(ss, ss), u)));
+              p[i] = pack2(mul2(i & 1 ? s1 : s0, fma2(i & 2 ? f1 : f0, q, mul2(make_float2(prm.scale, prm.scale), u))));
             }
             // lane: the address of token (lane & 7) + 8 (lane >> 4), channels 16 hf + 8 ((lane >> 3) & 1) ..
-            const int tk = (lane & 7) + 8 * (lane >> 4), ch = 2 * hf + ((lane >> 3) & 1);
+            const int tk = 16 * cg + (lane & 7) + 8 * (lane >> 4), ch = 32 * (quad & 1) + 16 * hf + (lane & 8);
+            if (hf == 0 && c > 0) wait_or_abort(&bar[B_OUT], (c - 1) & 1, s_abort, prm.status);   // the tile is free
             asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};"
-                         ::"r"(ot + 64 * tk + ((ch ^ ((tk >> 1) & 3)) << 4)), "r"(p[0]), "r"(p[1]), "r"(p[2]), "r"(p[3])
+                         ::"r"(ot + swz_offset(64, tk, ch)), "r"(p[0]), "r"(p[1]), "r"(p[2]), "r"(p[3])
                          : "memory");
           }
-          const int rows = valid - 16 * cg;
-          if (rows >= 16) {
-            fence_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-              tma_store_3d(&prm.tout, 32 * quad, h, t0 + c * kC + 16 * cg, sm + OFF_OUT + 1024 * warp);
-              bulk_commit();
-            }
-          } else {   // the end of a ragged chunk: its own rows alone
-            __syncwarp();
-            for (int i = lane; i < rows * 4; i += 32) {
-              const int tk = i >> 2, ch = i & 3;
-              *reinterpret_cast<uint4 *>(prm.out + static_cast<int64_t>(t0 + c * kC + 16 * cg + tk) * prm.out_stride + h * kD +
-                                         32 * quad + 8 * ch) =
-                  *reinterpret_cast<const uint4 *>(sm + OFF_OUT + 1024 * warp + 64 * tk + ((ch ^ ((tk >> 1) & 3)) << 4));
-            }
-          }
+          fence_async_smem();
+          warp_arrive(&bar[B_TILE]);
         }
-        {   // S = e^(b_63) S + D
+        {   // S = e^(b_63) S + D, ready for the next chunk's scale
           uint32_t w[32];
-          const float2 g2 = make_float2(gamma, gamma), i2 = make_float2(inv, inv);
-#pragma unroll
-          for (int i = 0; i < 32; i += 2) {
-            const float2 y = mul2(g2, make_float2(S[i], S[i + 1]));
-            S[i] = y.x;
-            S[i + 1] = y.y;
+          const float2 g2 = make_float2(gamma, gamma);
+          float ratio = 1.f;
+          if (c + 1 < nchunks) {
+            wait_or_abort(&bar[B_SCALE + ((c + 1) & 1)], ((c + 1) >> 1) & 1, s_abort, prm.status);
+            const float next = s_sig[128 * ((c + 1) & 1) + d];
+            ratio = next * s_inv[128 * (c & 1) + d];   // a power of two, nearly always 1
+            sig = next;
           }
-          wait_or_abort(bar_m3, c & 1, s_abort, prm.status);
+          wait_or_abort(&bar[B_M3], c & 1, s_abort, prm.status);
           tc_fence_after();
           tmem_ld16_async(lanes + TM_D + 32 * cg, w);
           tmem_ld16_async(lanes + TM_D + 32 * cg + 16, w + 16);
@@ -945,16 +966,21 @@ __global__ void __launch_bounds__(ch::kThreads, 1) gdn_chain_kernel(const __grid
           tmem_tie<32>(w);
 #pragma unroll
           for (int i = 0; i < 32; i += 2) {
-            const float2 y = fma2(i2, make_float2(__uint_as_float(w[i]), __uint_as_float(w[i + 1])), make_float2(S[i], S[i + 1]));
+            const float2 y = fma2(g2, make_float2(S[i], S[i + 1]), make_float2(__uint_as_float(w[i]), __uint_as_float(w[i + 1])));
             S[i] = y.x;
             S[i + 1] = y.y;
           }
+          if (__any_sync(0xffffffffu, ratio != 1.f)) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) S[i] *= ratio;
+          }
           if (c + 1 < nchunks) store_s(c + 1);
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bar_empty[c & 1]);
+        warp_arrive(&bar[B_FREE]);   // the last read of the stage is behind
       }
-      if (lane == 0) bulk_wait_all();
+      const float inv = s_inv[128 * ((nchunks - 1) & 1) + d];
+#pragma unroll
+      for (int e = 0; e < 32; ++e) S[e] *= inv;
     }
     tc_fence_before();
     __syncthreads();
@@ -1003,8 +1029,8 @@ cudaError_t launch_gdn_prefill(const GdnRecurrentArgs &a, const int32_t *cu_host
     return e;
   GdnPrefillParams p;
   const int total = cu_host[num_seqs], Hk = a.Hv / a.group;
-  if (!make_token_map(&p.tq, a.q, Hk, total, a.qk_stride, 128) || !make_token_map(&p.tk, a.k, Hk, total, a.qk_stride, 128) ||
-      !make_token_map(&p.tv, a.v, a.Hv, total, a.v_stride, 128) || !make_token_map(&p.tout, a.out, a.Hv, total, a.out_stride, 64, 32, 16))
+  if (!make_token_map(&p.tq, a.q, Hk, total, a.qk_stride) || !make_token_map(&p.tk, a.k, Hk, total, a.qk_stride) ||
+      !make_token_map(&p.tv, a.v, a.Hv, total, a.v_stride) || !make_token_map(&p.tout, a.out, a.Hv, total, a.out_stride))
     return cudaErrorInvalidValue;
   p.a = a.a; p.beta = a.beta;
   p.a_stride = a.a_stride; p.beta_stride = a.beta_stride;

@@ -45,10 +45,10 @@ struct ShortConv {
   uint16_t *step_windows;     // verify: [B, T, 3, 3, H, 128]
 };
 
-// Tensor map of [tokens, H, 128] bf16 with the given token stride, box 64 channels (or fewer) x 1 head x 64 tokens (or
-// fewer), swizzled by 128 or 64 bytes or not (0); false where the driver refuses it.
+// Tensor map of [tokens, H, 128] bf16 with the given token stride, box 64 channels x 1 head x 64 tokens, with the
+// 128-byte swizzle or without; false where the driver refuses it.
 bool make_token_map(CUtensorMap *map, const void *base, int H, int total_tokens, int64_t token_stride,
-                    int swizzle = 128, int box_channels = 64, int box_tokens = 64);
+                    bool swizzled = true);
 
 // Arguments of the token-by-token kernel (verify).
 struct RecurrentArgs {

@@ -496,9 +496,9 @@ constexpr uint32_t OFF_K16 = OFF_ONE + 8192;      // the chunk's keys times 2^-x
 constexpr uint32_t OFF_OUT = OFF_K16 + 16384;     // output on its way out (64 rows x 128 channels)
 constexpr uint32_t OFF_SMALL = OFF_OUT + 16384;
 constexpr uint32_t SM_BAR = 0 /* the barriers below */, SM_TMEM = 128, SM_ABORT = 132, SM_SIG = 256 /* [2][128] */, SM_INV = 1280 /* [2][128] */, SM_END = 2304;
-// mbarriers: landed in stage 0, 1; scales of even, odd chunks; products done (first, second, state's, v's, output's); output
+// mbarriers: landed in stage 0, 1: all but v, v (which goes first, for the scales); scales of even, odd chunks; products done (first, second, state's, v's, output's); output
 // tile free | the workers' warps: S, R, U' in place, stage done with, output in its tile
-enum { B_FULL = 0, B_SCALE = 2, B_M1 = 4, B_M2, B_M3, B_V, B_O, B_OUT, B_S, B_R, B_U, B_FREE, B_TILE, kBarriers };
+enum { B_FULL = 0, B_VAL = 2, B_SCALE = 4, B_M1 = 6, B_M2, B_M3, B_V, B_O, B_OUT, B_S, B_R, B_U, B_FREE, B_TILE, kBarriers };
 constexpr uint32_t kSmemBytes = OFF_SMALL + SM_END + 1024;
 static_assert(kSmemBytes <= 232448 && kStage >= kStageLoad && kStage % 1024 == 0, "shared memory map");
 constexpr uint32_t TM_KU = 0 /* two of 64 */, TM_D = 0 /* 128, over KU */, TM_U = 128 /* two of 64 */, TM_OT = 128 /* over U */,
@@ -601,14 +601,16 @@ __global__ void __launch_bounds__(ch::kThreads, 1) gdn_chain_kernel(const __grid
       const size_t step = static_cast<size_t>(prm.Hv) * kGdnBlkBytes;
       auto load = [&](int c) {
         uint8_t *st = sm + (c & 1) * kStage;
-        uint64_t *full = &bar[B_FULL + (c & 1)];
-        mbar_arrive_expect_tx(full, kStageLoad);
+        uint64_t *full = &bar[B_FULL + (c & 1)], *val = &bar[B_VAL + (c & 1)];
         const int tok = t0 + c * kC;
+        mbar_arrive_expect_tx(val, 16384);
+#pragma unroll
+        for (int x = 0; x < 2; ++x) tma_load_3d(st + ST_V + 8192 * x, &prm.tv, 64 * x, h, tok, val);
+        mbar_arrive_expect_tx(full, kStageLoad - 16384);
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           tma_load_3d(st + 16384 * x, &prm.tk, 64 * x, hk, tok, full);
           tma_load_3d(st + 16384 * x + 8192, &prm.tq, 64 * x, hk, tok, full);
-          tma_load_3d(st + ST_V + 8192 * x, &prm.tv, 64 * x, h, tok, full);
         }
         if (c == 0) grid_dependency_wait();   // the blocks are the intra-chunk grid's
         bulk_load(st + ST_BLK, blk + c * step, kGdnBlkBytes, full);
@@ -656,10 +658,10 @@ __global__ void __launch_bounds__(ch::kThreads, 1) gdn_chain_kernel(const __grid
       if (lane == 0) bulk_wait_all();
       // (every chunk was waited for by the issuing warps; after a timeout the copies in flight are waited for here)
       if (*s_abort) {
-        mbar_wait(&bar[B_FULL], 0);
-        mbar_wait(&bar[B_FULL + 1], 0);
-        mbar_wait(&bar[B_FULL], 1);
-        mbar_wait(&bar[B_FULL + 1], 1);
+        for (int i = 0; i < 4; ++i) {
+          mbar_wait(&bar[B_FULL + i], 0);
+          mbar_wait(&bar[B_FULL + i], 1);
+        }
       }
       __syncwarp();
     } else if (warp == kScaler) {
@@ -669,6 +671,7 @@ __global__ void __launch_bounds__(ch::kThreads, 1) gdn_chain_kernel(const __grid
       // nothing until it is 2^15 times too large.  Lane: channels 2 lane, + 1, + 64, + 65.
       float bound[4];   // of the channels' states in 2-norm
       int field[4] = {300, 300, 300, 300};   // the scales' exponent fields
+      float last[4] = {0.f, 0.f, 0.f, 0.f};  // the last chunk's largest |v|
       {
         float ss[4] = {0.f, 0.f, 0.f, 0.f};
         if (src)
@@ -684,7 +687,7 @@ __global__ void __launch_bounds__(ch::kThreads, 1) gdn_chain_kernel(const __grid
       for (int c = 0; c < nchunks; ++c) {
         const uint8_t *st = sm + (c & 1) * kStage;
         const int valid = min(kC, len - c * kC);
-        wait_or_abort(&bar[B_FULL + (c & 1)], (c >> 1) & 1, s_abort, prm.status);
+        wait_or_abort(&bar[B_VAL + (c & 1)], (c >> 1) & 1, s_abort, prm.status);
         uint32_t top[2] = {0u, 0u};   // |v|'s bits (bf16 order is integer order)
 #pragma unroll 8
         for (int t = 0; t < valid; ++t) {
@@ -692,10 +695,17 @@ __global__ void __launch_bounds__(ch::kThreads, 1) gdn_chain_kernel(const __grid
           top[0] = __vmaxu2(top[0], *reinterpret_cast<const uint32_t *>(at) & 0x7FFF7FFFu);
           top[1] = __vmaxu2(top[1], *reinterpret_cast<const uint32_t *>(at + 8192) & 0x7FFF7FFFu);
         }
-        const float gamma = reinterpret_cast<const float *>(st + ST_BLK + kBlkVec)[kVecGamma];
+        // the last chunk's decay and growth (its block has long landed, and its stage is held until these scales are out)
+        float gamma = 1.f;
+        if (c > 0) {
+          wait_or_abort(&bar[B_FULL + ((c - 1) & 1)], ((c - 1) >> 1) & 1, s_abort, prm.status);
+          gamma = reinterpret_cast<const float *>(sm + ((c - 1) & 1) * kStage + ST_BLK + kBlkVec)[kVecGamma];
+        }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const float vm = i & 1 ? __uint_as_float(top[i >> 1] & 0xFFFF0000u) : __uint_as_float(top[i >> 1] << 16);
+          bound[i] = fmaf(gamma, bound[i], 8.f * last[i]);
+          last[i] = vm;
           const float most = fmaf(9.f, vm, bound[i]);
           // (kept until it is too large, or 2^10 too small)
           const int want = min(max(267 - static_cast<int>(__float_as_uint(most) >> 23 & 0xFF), 1), 217);
@@ -703,7 +713,6 @@ __global__ void __launch_bounds__(ch::kThreads, 1) gdn_chain_kernel(const __grid
           const int ch = 128 * (c & 1) + 64 * (i >> 1) + 2 * lane + (i & 1);
           s_sig[ch] = __uint_as_float(static_cast<uint32_t>(field[i]) << 23);
           s_inv[ch] = __uint_as_float(static_cast<uint32_t>(254 - field[i]) << 23);
-          bound[i] = fmaf(gamma, bound[i], 8.f * vm);
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar[B_SCALE + (c & 1)]);   // (the workers wait for it, so their word that the stage is free
@@ -727,13 +736,15 @@ __global__ void __launch_bounds__(ch::kThreads, 1) gdn_chain_kernel(const __grid
         };
         // (a ragged chunk's rows behind the end are cleared before S is announced; D before, which values run behind)
         const bool ragged = len - c * kC < kC;
-        wait_or_abort(&bar[B_FULL + (c & 1)], (c >> 1) & 1, s_abort, prm.status);
         if (me == 1 && !ragged) {
+          wait_or_abort(&bar[B_VAL + (c & 1)], (c >> 1) & 1, s_abort, prm.status);
           if (c > 0) wait_or_abort(&bar[B_M3], (c - 1) & 1, s_abort, prm.status);
           tc_fence_after();
           if (lane == 0) values();
           __syncwarp();
         }
+        wait_or_abort(&bar[B_VAL + (c & 1)], (c >> 1) & 1, s_abort, prm.status);
+        wait_or_abort(&bar[B_FULL + (c & 1)], (c >> 1) & 1, s_abort, prm.status);
         wait_or_abort(&bar[B_S], c & 1, s_abort, prm.status);   // S is in place, D has been read
         tc_fence_after();
         if (lane == 0) {
@@ -788,7 +799,7 @@ __global__ void __launch_bounds__(ch::kThreads, 1) gdn_chain_kernel(const __grid
       auto store_s = [&](int c) {
         const int valid = len - c * kC;
         if (valid < kC) {
-          wait_or_abort(&bar[B_FULL + (c & 1)], (c >> 1) & 1, s_abort, prm.status);
+          wait_or_abort(&bar[B_VAL + (c & 1)], (c >> 1) & 1, s_abort, prm.status);
           for (int i = tid; i < (kC - valid) * 16; i += kWorkers)
             *reinterpret_cast<uint4 *>(sm + (c & 1) * kStage + ST_V + swz_offset(64, valid + (i >> 4), 8 * (i & 15))) =
                 make_uint4(0, 0, 0, 0);
@@ -913,11 +924,14 @@ __global__ void __launch_bounds__(ch::kThreads, 1) gdn_chain_kernel(const __grid
         }
         {   // beside the state's product: o^T = scale e^b/|q| (q S)^T + scale (P U)^T.  Here a thread holds the fragments
             // that stmatrix transposes: channels lane / 4 + 8 i, tokens 2 (lane % 4), + 1 (+ 8) of the warp's 32 x 16
-          wait_or_abort(&bar[B_O], c & 1, s_abort, prm.status);
-          tc_fence_after();
+          if (c > 0) wait_or_abort(&bar[B_OUT], (c - 1) & 1, s_abort, prm.status);   // the tile is free
+          const float *si = s_inv + 128 * (c & 1) + 32 * quad + (lane >> 2);
+          const float inv4[4] = {si[0], si[8], si[16], si[24]};
           const uint32_t ot = smem_u32(sm + OFF_OUT + 8192 * (quad >> 1));
           const float2 f0 = *reinterpret_cast<const float2 *>(vec + kVecQ + 16 * cg + 2 * (lane & 3));
           const float2 f1 = *reinterpret_cast<const float2 *>(vec + kVecQ + 16 * cg + 2 * (lane & 3) + 8);
+          wait_or_abort(&bar[B_O], c & 1, s_abort, prm.status);
+          tc_fence_after();
           uint32_t w[16], y[16];
 #pragma unroll
           for (int hf = 0; hf < 2; ++hf) {
@@ -929,8 +943,7 @@ __global__ void __launch_bounds__(ch::kThreads, 1) gdn_chain_kernel(const __grid
           tmem_tie<16>(y);
 #pragma unroll
           for (int hf = 0; hf < 2; ++hf) {   // 16 channels
-            const float *si = s_inv + 128 * (c & 1) + 32 * quad + 16 * hf + (lane >> 2);
-            const float2 s0 = make_float2(si[0], si[0]), s1 = make_float2(si[8], si[8]);
+            const float2 s0 = make_float2(inv4[2 * hf], inv4[2 * hf]), s1 = make_float2(inv4[2 * hf + 1], inv4[2 * hf + 1]);
             uint32_t p[4];   // (channels 0..7, tokens 0..7), (8..15, 0..7), (0..7, 8..15), (8..15, 8..15)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -940,7 +953,6 @@ __global__ void __launch_bounds__(ch::kThreads, 1) gdn_chain_kernel(const __grid
             }
             // lane: the address of token (lane & 7) + 8 (lane >> 4), channels 16 hf + 8 ((lane >> 3) & 1) ..
             const int tk = 16 * cg + (lane & 7) + 8 * (lane >> 4), ch = 32 * (quad & 1) + 16 * hf + (lane & 8);
-            if (hf == 0 && c > 0) wait_or_abort(&bar[B_OUT], (c - 1) & 1, s_abort, prm.status);   // the tile is free
             asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};"
                          ::"r"(ot + swz_offset(64, tk, ch)), "r"(p[0]), "r"(p[1]), "r"(p[2]), "r"(p[3])
                          : "memory");

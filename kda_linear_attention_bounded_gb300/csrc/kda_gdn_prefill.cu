@@ -28,7 +28,6 @@
 
 #include <algorithm>
 #include <numeric>
-#include <vector>
 
 #include "kda_common.cuh"
 #include "kda_internal.h"
@@ -48,6 +47,21 @@ constexpr uint32_t kGdnBlkBytes = 26112;
 constexpr int kVecB = 0, kVecK = 64, kVecQ = 128, kVecX = 192, kVecS = 256, kVecGamma = 320;
 constexpr int kGdnMaxSeqs = 1024;   // sequences per launch (longer batches are split on the host)
 
+// A state pass is serial in a sequence's chunks, so few long sequences leave most of the GPU idle.  They are cut into
+// segments of seg chunks.  Within a segment the state is affine in the state S that enters it, S_end = F S + B, and F and
+// B are states of the same pass: F is what becomes of the identity without values, B of a zero state with them.  One
+// grid runs first segments (as usual: their state is known) and F and B of the inner ones, a small kernel forms
+// S_(j+1) = F_j S_j + B_j in fp32, and a second grid runs the segments behind the first from those states.
+// A segment job: sequence | segment | F | first of the sequence's matrices among the launch's.  A sequence of m segments
+// has 2 m - 3 matrices: the states entering segments 1 .. m - 1, then F of segments 1 .. m - 2.
+constexpr int kGdnMaxJobs = 256, kGdnMaxSegs = 16;   // jobs per grid, segments per sequence
+constexpr int kGdnMaxMats = 304;                     // matrices times heads (64 KB each)
+constexpr int kSegmentMin = 4, kSegmentExtra = 8;    // chunks of the shortest segment; what cutting costs, in chunks' time
+struct GdnJob {
+  uint16_t seq, mat;
+  uint8_t seg, segs, map, pad;   // map: this job is F
+};
+
 struct GdnPrefillParams {
   CUtensorMap tq, tk, tv, tout; // [tokens, H, 128] bf16, box 64 channels x 1 head x 64 tokens, 128-byte swizzle
   const uint16_t *a, *beta;
@@ -66,6 +80,10 @@ struct GdnPrefillParams {
   int num_seqs;
   int32_t cu[kGdnMaxSeqs + 1];  // first token of each sequence of the launch, and the end of the last
   uint16_t order[kGdnMaxSeqs];  // sequences, longest first
+  // segments
+  int first_pass, seg_chunks;
+  float *mats;                  // matrix m of head h at mats + (m Hv + h) 128 128
+  GdnJob job[kGdnMaxJobs];
 };
 static_assert(sizeof(GdnPrefillParams) <= 32764, "kernel parameters are limited to 32764 bytes");
 
@@ -536,6 +554,7 @@ __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool a_mn_major, 
   return idesc_bf16(M, N, a_mn_major, b_mn_major) & ~((1u << 7) | (1u << 10));
 }
 
+template <bool SEGMENTS>
 __global__ void __launch_bounds__(ch::kThreads, 1) gdn_chain_kernel(const __grid_constant__ GdnPrefillParams prm) {
   using namespace ch;
   extern __shared__ uint8_t smem_raw[];
@@ -547,9 +566,21 @@ __global__ void __launch_bounds__(ch::kThreads, 1) gdn_chain_kernel(const __grid
   float *s_sig = reinterpret_cast<float *>(small + SM_SIG), *s_inv = reinterpret_cast<float *>(small + SM_INV);
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);   // (uniform in the warp)
 
-  const int h = blockIdx.x % prm.Hv, n = prm.order[blockIdx.x / prm.Hv], hk = h / prm.group;
-  const int t0 = prm.cu[n], len = prm.cu[n + 1] - t0;
+  const int h = blockIdx.x % prm.Hv, hk = h / prm.group;
+  GdnJob job = {};
+  if (SEGMENTS) job = prm.job[blockIdx.x / prm.Hv];
+  const int n = SEGMENTS ? job.seq : prm.order[blockIdx.x / prm.Hv];
+  const bool map = SEGMENTS && job.map;
+  int t0 = prm.cu[n], len = prm.cu[n + 1] - t0, chunk0 = 0;
+  if (SEGMENTS && job.segs > 1) {
+    chunk0 = job.seg * prm.seg_chunks;
+    t0 += chunk0 * kC;
+    len -= chunk0 * kC;
+    if (job.seg + 1 < job.segs) len = min(len, prm.seg_chunks * kC);
+  }
   const int nchunks = (len + kC - 1) / kC;
+  // a segment whose entering state is known has outputs; the others' F and B do not
+  const bool known = !SEGMENTS || !prm.first_pass || job.seg == 0;
   int pool_slot = 0;
   if (prm.slot_ids) {
     pool_slot = prm.slot_ids[n];
@@ -565,13 +596,24 @@ __global__ void __launch_bounds__(ch::kThreads, 1) gdn_chain_kernel(const __grid
   const float *src = prm.state_in ? prm.state_in + pool_at : nullptr;
   float *dst = prm.state_out_pool ? prm.state_out_pool + pool_at
                                   : prm.state_out_dense + (static_cast<size_t>(n) * prm.Hv + h) * kD * kD;
+  if (SEGMENTS && job.segs > 1) {
+    const auto mat = [&](int m) { return prm.mats + (static_cast<size_t>(job.mat + m) * prm.Hv + h) * kD * kD; };
+    if (job.seg > 0) src = known ? mat(job.seg - 1) : nullptr;
+    if (map)
+      dst = mat(job.segs - 1 + job.seg - 1);
+    else if (job.seg + 1 < job.segs && prm.first_pass)
+      dst = mat(job.seg);
+    else if (job.seg + 1 < job.segs)
+      dst = nullptr;   // (the next segment's state is there already)
+  }
+  if (SEGMENTS && !prm.first_pass) grid_dependency_wait();   // the entering states
   // epilogue thread: value channel d (TMEM lane), key channels 32 cg .. + 31 of the state, tokens 16 cg .. + 15 of a chunk
   const bool worker = warp < kIssuer;
   const int quad = warp & 3, cg = warp >> 2, d = 32 * quad + lane;
   float S[32];
   if (worker) {
 #pragma unroll
-    for (int e = 0; e < 32; ++e) S[e] = src ? src[(32 * cg + e) * kD + d] : 0.f;
+    for (int e = 0; e < 32; ++e) S[e] = src ? src[(32 * cg + e) * kD + d] : map && 32 * cg + e == d ? 1.f : 0.f;
   }
   if (nchunks > 0) {
     if (tid == 0) {
@@ -588,6 +630,10 @@ __global__ void __launch_bounds__(ch::kThreads, 1) gdn_chain_kernel(const __grid
       const uint32_t one = (r >> 3) != pc ? 0u : (r & 1) ? 0x3F800000u : 0x00003F80u;
       *reinterpret_cast<uint4 *>(sm + OFF_ONE + swz_offset(64, r, 8 * pc)) =
           make_uint4(w == 0 ? one : 0u, w == 1 ? one : 0u, w == 2 ? one : 0u, w == 3 ? one : 0u);
+      if (map) {   // no values
+        for (int i = tid; i < 2048; i += kWorkers)
+          *reinterpret_cast<uint4 *>(sm + (i >> 10) * kStage + ST_V + 16 * (i & 1023)) = make_uint4(0, 0, 0, 0);
+      }
       fence_async_smem();
     }
     tc_fence_before();
@@ -597,15 +643,19 @@ __global__ void __launch_bounds__(ch::kThreads, 1) gdn_chain_kernel(const __grid
 
     if (warp == kProducer) {
       // ------------------------------------------------------------ chunks -> stages, output tiles -> the caller's rows
-      const uint8_t *blk = prm.blocks + (static_cast<size_t>(first_slot(prm, n)) * prm.Hv + h) * kGdnBlkBytes;
+      const uint8_t *blk = prm.blocks + (static_cast<size_t>(first_slot(prm, n) + chunk0) * prm.Hv + h) * kGdnBlkBytes;
       const size_t step = static_cast<size_t>(prm.Hv) * kGdnBlkBytes;
       auto load = [&](int c) {
         uint8_t *st = sm + (c & 1) * kStage;
         uint64_t *full = &bar[B_FULL + (c & 1)], *val = &bar[B_VAL + (c & 1)];
         const int tok = t0 + c * kC;
-        mbar_arrive_expect_tx(val, 16384);
+        if (map) {
+          mbar_arrive(val);
+        } else {
+          mbar_arrive_expect_tx(val, 16384);
 #pragma unroll
-        for (int x = 0; x < 2; ++x) tma_load_3d(st + ST_V + 8192 * x, &prm.tv, 64 * x, h, tok, val);
+          for (int x = 0; x < 2; ++x) tma_load_3d(st + ST_V + 8192 * x, &prm.tv, 64 * x, h, tok, val);
+        }
         mbar_arrive_expect_tx(full, kStageLoad - 16384);
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
@@ -622,8 +672,9 @@ __global__ void __launch_bounds__(ch::kThreads, 1) gdn_chain_kernel(const __grid
       __syncwarp();
       for (int c = 0; c < nchunks; ++c) {
         const int valid = min(kC, len - c * kC), tok = t0 + c * kC;
-        wait_or_abort(&bar[B_TILE], c & 1, s_abort, prm.status);   // chunk c's output is in its tile
-        if (valid == kC) {
+        if (known) wait_or_abort(&bar[B_TILE], c & 1, s_abort, prm.status);   // chunk c's output is in its tile
+        if (!known) {
+        } else if (valid == kC) {
           if (lane == 0) {
             tma_store_3d(&prm.tout, 0, h, tok, sm + OFF_OUT);
             tma_store_3d(&prm.tout, 64, h, tok, sm + OFF_OUT + 8192);
@@ -650,8 +701,10 @@ __global__ void __launch_bounds__(ch::kThreads, 1) gdn_chain_kernel(const __grid
             }
             bulk_prefetch(blk + (c + 3) * step, kGdnBlkBytes);
           }
-          bulk_wait_read();
-          mbar_arrive(&bar[B_OUT]);   // the output tile is free
+          if (known) {
+            bulk_wait_read();
+            mbar_arrive(&bar[B_OUT]);   // the output tile is free
+          }
         }
         __syncwarp();
       }
@@ -682,7 +735,7 @@ __global__ void __launch_bounds__(ch::kThreads, 1) gdn_chain_kernel(const __grid
             ss[2] = fmaf(b.x, b.x, ss[2]); ss[3] = fmaf(b.y, b.y, ss[3]);
           }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) bound[i] = sqrtf(ss[i]);
+        for (int i = 0; i < 4; ++i) bound[i] = map ? 1.f : sqrtf(ss[i]);
       }
       for (int c = 0; c < nchunks; ++c) {
         const uint8_t *st = sm + (c & 1) * kStage;
@@ -752,7 +805,7 @@ __global__ void __launch_bounds__(ch::kThreads, 1) gdn_chain_kernel(const __grid
 #pragma unroll
           for (int k = 0; k < 8; ++k) mma_bf16_tmem_a(ku, sp + 8 * k, kk + kmajor_step(128, k), id1, k > 0);
           mma_commit(&bar[B_M1]);
-          if (me == 1) {
+          if (me == 1 && known) {
 #pragma unroll
             for (int k = 0; k < 8; ++k)
               mma_bf16_tmem_a(tmem + TM_QS, tmem + TM_S + 8 * k, qq + kmajor_step(128, k), id1, k > 0);
@@ -779,9 +832,11 @@ __global__ void __launch_bounds__(ch::kThreads, 1) gdn_chain_kernel(const __grid
         wait_or_abort(&bar[B_U], c & 1, s_abort, prm.status);   // U, U', the fp16 keys are in place, the accumulators read
         tc_fence_after();
         if (me == 0 && lane == 0) {
+          if (known) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) mma_bf16_tmem_a(tmem + TM_OT, tmem + TM_UH + 8 * k, pp + kmajor_step(64, k), id2, k > 0);
-          mma_commit(&bar[B_O]);
+            for (int k = 0; k < 4; ++k) mma_bf16_tmem_a(tmem + TM_OT, tmem + TM_UH + 8 * k, pp + kmajor_step(64, k), id2, k > 0);
+            mma_commit(&bar[B_O]);
+          }
 #pragma unroll
           for (int p = 0; p < 2; ++p)
 #pragma unroll
@@ -919,10 +974,10 @@ __global__ void __launch_bounds__(ch::kThreads, 1) gdn_chain_kernel(const __grid
             uh[i] = pack_f16x2(u);
             x[i] = mul2(x[i], u);
           }
-          tmem_st8(lanes + TM_UH + 8 * cg, uh);
+          if (known) tmem_st8(lanes + TM_UH + 8 * cg, uh);
           store_r(x, B_U);
         }
-        {   // beside the state's product: o^T = scale e^b/|q| (q S)^T + scale (P U)^T.  Here a thread holds the fragments
+        if (known) {   // beside the state's product: o^T = scale e^b/|q| (q S)^T + scale (P U)^T.  Here a thread holds the fragments
             // that stmatrix transposes: channels lane / 4 + 8 i, tokens 2 (lane % 4), + 1 (+ 8) of the warp's 32 x 16
           if (c > 0) wait_or_abort(&bar[B_OUT], (c - 1) & 1, s_abort, prm.status);   // the tile is free
           const float *si = s_inv + 128 * (c & 1) + 32 * quad + (lane >> 2);
@@ -1002,30 +1057,201 @@ __global__ void __launch_bounds__(ch::kThreads, 1) gdn_chain_kernel(const __grid
     }
   }
   if (nchunks == 0 && tid == 0) grid_dependency_wait();
-  if (worker) {
+  if (worker && dst) {
 #pragma unroll
     for (int e = 0; e < 32; ++e) dst[(32 * cg + e) * kD + d] = S[e];
   }
 }
 
-cudaError_t launch_chain(const GdnPrefillParams &p, cudaStream_t stream) {
+// The states entering a sequence's segments, S_(j+1) = F_j S_j + B_j (B_j is where S_(j+1) goes), in fp32: a CTA per
+// sequence, head and 16 value channels, a warp per 16 key channels.  A lane holds four columns of F's rows, which a warp
+// reads as whole rows, and the four rows of S that they meet; the lanes' sums meet in a halving exchange, at whose end
+// each lane holds one.  Bound by the latency of its few steps; the next F and B are on their way during a step.
+constexpr int kJoinParts = 8, kJoinStride = 68;
+__global__ void __launch_bounds__(256, 1) gdn_join_kernel(const __grid_constant__ GdnPrefillParams prm) {
+  __shared__ __align__(16) float s_state[2][32 * kJoinStride];   // rows 4 l .. + 3 at kJoinStride l
+  const int part = blockIdx.x % kJoinParts, h = blockIdx.x / kJoinParts % prm.Hv, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const GdnJob job = prm.job[blockIdx.x / kJoinParts / prm.Hv];
+  const auto mat = [&](int m) { return prm.mats + (static_cast<size_t>(job.mat + m) * prm.Hv + h) * kD * kD; };
+  // this lane's entry of rows 2 i, 2 i + 1 of the warp's: row 2 i + lane / 16, value channel lane % 16
+  const size_t at = static_cast<size_t>(16 * warp + (lane >> 4)) * kD + 16 * part + (lane & 15);
+  const auto put = [&](int buf, int i, float y) {
+    const int row = 16 * warp + 2 * i + (lane >> 4);
+    s_state[buf][(row >> 2) * kJoinStride + (row & 3) * 16 + (lane & 15)] = y;
+  };
+  float4 f[16];
+  float b[8];
+  const auto fetch = [&](int j) {
+    const float4 *src = reinterpret_cast<const float4 *>(mat(job.segs + j - 2) + static_cast<size_t>(16 * warp) * kD);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) f[i] = src[32 * i + lane];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) b[i] = mat(j)[at + 2 * i * kD];
+  };
+  grid_dependency_wait();
+  fetch(1);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) put(0, i, mat(0)[at + 2 * i * kD]);
+  __syncthreads();
+  for (int j = 1; j + 1 < job.segs; ++j) {
+    float st[4][16];
+#pragma unroll
+    for (int x = 0; x < 16; ++x)
+      *reinterpret_cast<float4 *>(&st[x >> 2][4 * (x & 3)]) =
+          *reinterpret_cast<const float4 *>(&s_state[(j - 1) & 1][kJoinStride * lane + 4 * x]);
+    float y[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      float v[32];
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const float4 w = f[2 * i + r];
+#pragma unroll
+        for (int c = 0; c < 16; ++c) v[16 * r + c] = fmaf(w.w, st[3][c], fmaf(w.z, st[2][c], fmaf(w.y, st[1][c], w.x * st[0][c])));
+      }
+#pragma unroll
+      for (int half = 16; half > 0; half >>= 1) {
+        const bool up = lane & half;
+#pragma unroll
+        for (int x = 0; x < half; ++x) {
+          const float send = up ? v[x] : v[x + half];
+          v[x] = (up ? v[x + half] : v[x]) + __shfl_xor_sync(0xffffffffu, send, half);
+        }
+      }
+      y[i] = v[0] + b[i];
+    }
+    if (j + 2 < job.segs) fetch(j + 1);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      put(j & 1, i, y[i]);
+      mat(j)[at + 2 * i * kD] = y[i];
+    }
+    __syncthreads();
+  }
+}
+
+template <typename K>
+cudaError_t launch_behind(K kernel, int ctas, int threads, uint32_t smem, const GdnPrefillParams &p, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(p.num_seqs) * p.Hv);
-  cfg.blockDim = dim3(ch::kThreads);
-  cfg.dynamicSmemBytes = ch::kSmemBytes;
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas));
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, gdn_chain_kernel, p);
+  return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+template <bool SEGMENTS>
+cudaError_t launch_chain(const GdnPrefillParams &p, int ctas, cudaStream_t stream) {
+  return launch_behind(gdn_chain_kernel<SEGMENTS>, ctas, ch::kThreads, ch::kSmemBytes, p, stream);
+}
+
+int chunks_of(const GdnPrefillParams &p, int n) { return (p.cu[n + 1] - p.cu[n] + kC - 1) / kC; }
+
+// Chunks per segment, or 0 to leave the sequences whole: the estimates of both in chunks' time.  A grid of at most one
+// CTA per SM takes its longest; others are bounded (from below for whole sequences, from above for segments).
+int segment_chunks(const GdnPrefillParams &p, int max_mats) {
+  const int longest = chunks_of(p, p.order[0]);
+  int64_t sum = 0;
+  if (longest < kSegmentExtra + 2 * kSegmentMin) return 0;
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
+      sms <= 0)
+    sms = 152;
+  for (int n = 0; n < p.num_seqs; ++n) sum += chunks_of(p, n);
+  int64_t best = std::max<int64_t>(longest, sum * p.Hv / sms);
+  int seg = 0, tried = 0;
+  for (int m = 2; m <= kGdnMaxSegs; ++m) {
+    const int g = (longest + m - 1) / m;
+    if (g < kSegmentMin) break;
+    if (g == tried) continue;
+    tried = g;
+    int64_t jobs1 = 0, jobs2 = 0, work1 = 0, mats = 0, work2 = 0;
+    for (int n = 0; n < p.num_seqs; ++n) {
+      const int chunks = chunks_of(p, n), segs = (chunks + g - 1) / g;
+      if (segs <= 1) {
+        jobs1 += 1;
+        work1 += chunks;
+        continue;
+      }
+      jobs1 += 2 * segs - 3;
+      work1 += static_cast<int64_t>(2 * segs - 3) * g;
+      jobs2 += segs - 1;
+      work2 += chunks - g;
+      mats += 2 * segs - 3;
+    }
+    if (jobs1 > kGdnMaxJobs || mats * p.Hv > max_mats) break;
+    const int64_t est = (jobs1 * p.Hv <= sms ? g : work1 * p.Hv / sms + g) + (jobs2 * p.Hv <= sms ? g : work2 * p.Hv / sms + g) +
+                        kSegmentExtra;
+    if (est < best) {
+      best = est;
+      seg = g;
+    }
+  }
+  return seg;
+}
+
+cudaError_t launch_segments(GdnPrefillParams &p, int g, float *mats, cudaStream_t stream) {
+  p.seg_chunks = g;
+  p.mats = mats;
+  // first segments, then the inner ones, then the sequences that stay whole (sequences come longest first, so those with
+  // inner segments are ahead of the others)
+  int jobs = 0, mat = 0, joined = 0;
+  const auto segments = [&](int i) { return std::max(1, (chunks_of(p, p.order[i]) + g - 1) / g); };
+  const auto add = [&](int i, int seg, bool map) {
+    const int segs = segments(i);
+    p.job[jobs++] = {p.order[i], static_cast<uint16_t>(mat), static_cast<uint8_t>(seg), static_cast<uint8_t>(segs),
+                     static_cast<uint8_t>(map), 0};
+    return 2 * segs - 3;
+  };
+  for (int i = 0; i < p.num_seqs && segments(i) > 1; ++i) {
+    joined += segments(i) > 2;
+    mat += add(i, 0, false);
+  }
+  mat = 0;
+  for (int i = 0; i < joined; ++i) {
+    for (int s = 1; s + 1 < segments(i); ++s) {
+      add(i, s, false);
+      add(i, s, true);
+    }
+    mat += 2 * segments(i) - 3;
+  }
+  mat = 0;
+  for (int i = 0; i < p.num_seqs; ++i)
+    if (segments(i) == 1) add(i, 0, false);
+  p.first_pass = 1;
+  cudaError_t e = launch_chain<true>(p, jobs * p.Hv, stream);
+  if (e == cudaSuccess && joined) e = launch_behind(gdn_join_kernel, joined * p.Hv * kJoinParts, 256, 0, p, stream);
+  if (e != cudaSuccess) return e;
+  jobs = mat = 0;
+  for (int i = 0; i < p.num_seqs && segments(i) > 1; ++i) {
+    for (int s = 1; s < segments(i); ++s) add(i, s, false);
+    mat += 2 * segments(i) - 3;
+  }
+  p.first_pass = 0;
+  return launch_chain<true>(p, jobs * p.Hv, stream);
 }
 
 }  // namespace
 
-size_t gdn_prefill_workspace_bytes(int64_t total_tokens, int num_seqs, int Hv) {
+namespace {
+// matrices (times heads) that a batch of so many tokens has room for: a segment has kSegmentMin chunks or more, and a
+// sequence of m segments 2 m - 3 matrices; none where no sequence can be long enough
+int64_t matrix_room(int64_t total_tokens, int Hv) {
+  const int64_t chunks = total_tokens / kC + 1;
+  if (chunks < kSegmentExtra + 2 * kSegmentMin) return 0;
+  return std::min<int64_t>(kGdnMaxMats, 2 * chunks / kSegmentMin * Hv);
+}
+size_t block_bytes(int64_t total_tokens, int num_seqs, int Hv) {
   return (total_tokens / kC + num_seqs) * static_cast<size_t>(Hv) * kGdnBlkBytes;
+}
+}  // namespace
+
+size_t gdn_prefill_workspace_bytes(int64_t total_tokens, int num_seqs, int Hv) {
+  return block_bytes(total_tokens, num_seqs, Hv) + matrix_room(total_tokens, Hv) * sizeof(float) * kD * kD;
 }
 
 cudaError_t launch_gdn_prefill(const GdnRecurrentArgs &a, const int32_t *cu_host, int num_seqs, uint8_t *blocks,
@@ -1035,12 +1261,16 @@ cudaError_t launch_gdn_prefill(const GdnRecurrentArgs &a, const int32_t *cu_host
   if (const cudaError_t e = set_attributes_once(mu, done, [] {
         cudaError_t r = cudaFuncSetAttribute(gdn_intra_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, in::kSmemBytes);
         if (r == cudaSuccess)
-          r = cudaFuncSetAttribute(gdn_chain_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, ch::kSmemBytes);
+          r = cudaFuncSetAttribute(gdn_chain_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, ch::kSmemBytes);
+        if (r == cudaSuccess)
+          r = cudaFuncSetAttribute(gdn_chain_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, ch::kSmemBytes);
         return r;
       }))
     return e;
   GdnPrefillParams p;
   const int total = cu_host[num_seqs], Hk = a.Hv / a.group;
+  const int room = static_cast<int>(matrix_room(total, a.Hv));
+  float *mats = reinterpret_cast<float *>(blocks + block_bytes(total, num_seqs, a.Hv));
   if (!make_token_map(&p.tq, a.q, Hk, total, a.qk_stride) || !make_token_map(&p.tk, a.k, Hk, total, a.qk_stride) ||
       !make_token_map(&p.tv, a.v, a.Hv, total, a.v_stride) || !make_token_map(&p.tout, a.out, a.Hv, total, a.out_stride))
     return cudaErrorInvalidValue;
@@ -1068,7 +1298,8 @@ cudaError_t launch_gdn_prefill(const GdnRecurrentArgs &a, const int32_t *cu_host
     blocks += static_cast<size_t>(slots) * a.Hv * kGdnBlkBytes;
     gdn_intra_kernel<<<static_cast<unsigned>(slots) * Hk, in::kThreads, in::kSmemBytes, stream>>>(p);
     if (const cudaError_t e = cudaGetLastError()) return e;
-    if (const cudaError_t e = launch_chain(p, stream)) return e;
+    const int seg = segment_chunks(p, room);
+    if (const cudaError_t e = seg ? launch_segments(p, seg, mats, stream) : launch_chain<false>(p, ns * a.Hv, stream)) return e;
   }
   return cudaSuccess;
 }

@@ -19,8 +19,8 @@ def gdn_inputs(tokens, hk, hv, seed, a_mean=0.0, device="cuda"):
     return [q, k, v, a, beta, A_log, (dt + torch.log(-torch.expm1(-dt))).to(device)]
 
 
-def gdn_reference(x, lens, S0=None, scale=D ** -0.5):
-    """(out [tokens, Hv, D], states after every token: list per sequence of [len, Hv, D, D], final [N, Hv, D, D])."""
+def gdn_reference(x, lens, S0=None, scale=D ** -0.5, keep=True):
+    """(out [tokens, Hv, D], states after every token: list per sequence of [len, Hv, D, D] if keep, final [N, Hv, D, D])."""
     q, k, v, a, beta, A_log, dt_bias = (t.detach().double().cpu() for t in x)
     hv = v.shape[1]
     group = hv // q.shape[1]
@@ -38,7 +38,8 @@ def gdn_reference(x, lens, S0=None, scale=D ** -0.5):
             u = beta[t][:, None] * (v[t] - torch.einsum("hkv,hk->hv", S, k[t]))
             S = S + k[t][:, :, None] * u[:, None, :]
             out[t] = scale * torch.einsum("hkv,hk->hv", S, q[t])
-            rec.append(S)
+            if keep:
+                rec.append(S)
             t += 1
         steps.append(torch.stack(rec) if rec else torch.zeros((0, hv, D, D), dtype=torch.float64))
         final.append(S)

@@ -61,6 +61,42 @@ def test_prefill(lens, hk, hv, initial):
     assert torch.equal(pool[rest], before[rest])
 
 
+@pytest.mark.parametrize("lens,hk,hv,a_mean", [
+    ([64 * 16], 1, 1, -4.0), ([1537], 1, 1, -6.0), ([2048 + 63], 2, 4, -6.0), ([4033, 0, 130, 64, 1], 1, 2, -6.0),
+    ([700, 3000, 2100], 2, 2, -4.0), ([2600], 1, 1, 3.0), ([2600], 1, 1, 3000.0), ([64 * 40], 4, 16, -8.0)])
+def test_prefill_long_sequences(lens, hk, hv, a_mean):
+    # few sequences, long enough to be cut into segments: the entering states come from products of 128 x 128 matrices,
+    # whose pass and whose product add a rounding each per segment (16 at the most) to the state's; with |F| <= 1 and
+    # |B| bounded as a state is, each is at most as large as a chunk pass's own
+    x = gdn_inputs(sum(lens), hk, hv, seed=sum(lens), a_mean=a_mean)
+    pool = _pool(len(lens) + 1, hv, 8)
+    before = pool.clone()
+    slots = torch.arange(len(lens), 0, -1, dtype=torch.int32, device="cuda")
+    ws = kda.make_workspace(nbytes=kda.gdn_prefill_workspace_size(sum(lens), len(lens), hv))
+    out, final = _prefill(x, lens, state_pool=pool, slot_ids=slots, load_initial=True, workspace=ws)
+    out2, _ = _prefill(x, lens, state_pool=pool, slot_ids=slots, load_initial=True, final_to_pool=True, workspace=ws)
+    torch.cuda.synchronize()
+    assert kda.read_device_status(ws) == 0
+    ref, _, ref_S = gdn_reference(x, lens, before[slots.long()], keep=False)
+    assert rel_l2(out, ref) <= 3 * OUT_STEP
+    for n in range(len(lens)):
+        for h in range(hv):
+            assert rel_l2(final[n, h], ref_S[n, h]) <= STATE_CHUNKED, (n, h)
+    assert torch.equal(out, out2) and torch.equal(pool[slots.long()], final) and torch.equal(pool[0], before[0])
+
+
+def test_prefill_long_sequence_keeps_channels_apart():
+    # a NaN among one value channel's values of an early segment reaches that channel alone, from its 64-token chunk's
+    # first token on (the chunk's tokens meet in one product, where 0 x NaN is NaN)
+    x = gdn_inputs(2500, 1, 2, seed=21)
+    clean, _ = _prefill(x, [2500])
+    x[2][700, 1, 5] = float("nan")
+    out, final = _prefill(x, [2500])
+    assert torch.isnan(out[700:, 1, 5]).all() and torch.isnan(final[0, 1, :, 5]).all()
+    out[640:, 1, 5] = clean[640:, 1, 5]
+    assert torch.equal(out, clean)
+
+
 @pytest.mark.parametrize("a_mean", [-12.0, 3.0, 60.0, 3000.0])
 def test_prefill_decays(a_mean):
     # from no decay at all to one that clears the state at every token; e^lambda underflows from about 60 on

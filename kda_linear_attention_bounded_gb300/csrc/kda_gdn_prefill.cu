@@ -56,7 +56,10 @@ constexpr int kGdnMaxSeqs = 1024;   // sequences per launch (longer batches are 
 // has 2 m - 3 matrices: the states entering segments 1 .. m - 1, then F of segments 1 .. m - 2.
 constexpr int kGdnMaxJobs = 256, kGdnMaxSegs = 16;   // jobs per grid, segments per sequence
 constexpr int kGdnMaxMats = 304;                     // matrices times heads (64 KB each)
-constexpr int kSegmentMin = 4, kSegmentExtra = 8;    // chunks of the shortest segment; what cutting costs, in chunks' time
+// Chunks of the shortest segment, and what cutting costs (two more grids, their states) in chunks' time.  Measured, whole
+// against cut, 16 heads: one sequence of 768 tokens 41 against 44 us, of 1024 53 against 51, 2048 95 against 70, 16384 686
+// against 297; two of 1024 56 against 63, two of 2048 103 against 96.
+constexpr int kSegmentMin = 4, kSegmentExtra = 7;
 struct GdnJob {
   uint16_t seq, mat;
   uint8_t seg, segs, map, pad;   // map: this job is F

@@ -49,6 +49,9 @@ struct ShortConv {
 // 128-byte swizzle or without; false where the driver refuses it.
 bool make_token_map(CUtensorMap *map, const void *base, int H, int total_tokens, int64_t token_stride,
                     bool swizzled = true);
+// A bf16 tensor of `rank` dimensions (dims and box innermost first, strides in bytes from the second on), 128-byte swizzle.
+bool make_bf16_map(CUtensorMap *map, const void *base, int rank, const uint64_t *dims, const uint64_t *strides,
+                   const uint32_t *box);
 
 // Arguments of the token-by-token kernel (verify).
 struct RecurrentArgs {

@@ -8,15 +8,21 @@
 //
 // Bound by HBM: each token costs 512 bytes per key head and only 4 Hq / Hk T 128 operations.  So the work is cut by
 // bytes: the tiles of 64 tokens of every (request, key head, row block) stand in one line, of which each CTA (two per
-// SM, a fixed grid) takes an equal stretch, whatever the lengths are.  A stretch that begins or ends inside an item
+// SM, a fixed grid) takes an equal stretch, whatever the lengths are.  In the line an item takes kItemCost units, for its
+// queries and its end, and one for each tile; a tile is the stretch's that its unit is in.  (Measured: 64 requests of 1
+// to 8192 tokens 61 us without, 55 us with 2 to 6, where stretches of many short requests had come last.)  A stretch that begins or ends inside an item
 // leaves its part (m, l, o) in the workspace; a second kernel, launched as a programmatic dependent, joins an item's
 // parts in the order of its tokens, so results do not depend on timing.
 //
-// Tiles come through three 32 KB stages of 16-byte asynchronous copies (any page size and strides; page ids are
-// looked up a tile earlier), rows swizzled for ldmatrix.  A CTA's rows (16, 32 or 64 of them: query heads of the key
-// head x new tokens) share every key and value; with 16 rows the four warps split a tile's tokens, with 64 its rows.
-// Products are mma.sync m16n8k16 (bf16, fp32 sums): even 64 rows need 64 operations per byte, which it sustains at
-// HBM speed.  e^(s - m) is rounded to bf16 for the second product (the cache's own precision), l sums the unrounded.
+// One warp brings tiles through three 32 KB stages (page ids are looked up a tile earlier), four compute on them, and
+// they meet at mbarriers only.  Pages whose size has a power of two of 8 or more in it come by TMA, in boxes of so many
+// rows (up to 64); other sizes by 16-byte asynchronous copies, a row's pair at a time.  A CTA's rows (16, 32 or 64 of
+// them: query heads of the key head x new tokens) share every key and value; with 16 rows the four warps split a tile's
+// tokens, with 64 its rows.  Products are mma.sync m16n8k16 (bf16, fp32 sums): even 64 rows need 64 operations per
+// byte, which it sustains at HBM speed.  e^(s - m) is rounded to bf16 for the second product (the cache's own
+// precision), l sums the unrounded.
+#include <cuda.h>
+
 #include <algorithm>
 
 #include "kda_common.cuh"
@@ -26,21 +32,46 @@
 namespace kda {
 namespace {
 
-constexpr int kThreads = 128;
+constexpr int kThreads = 160, kComputeWarps = 4;   // and a loading warp
 constexpr int kTile = 64;        // tokens per tile
 constexpr int kStages = 3;
 constexpr uint32_t kStageBytes = 2 * kTile * kD * 2;   // K rows, then V rows
-constexpr uint32_t OFF_ROW = kStages * kStageBytes;    // [2][64]: element offsets of a tile's key and value rows (-1: none)
-constexpr uint32_t OFF_MASK = OFF_ROW + 2 * kTile * 16; // uint32 [4][2]: which tokens of a tile are there
-constexpr uint32_t OFF_ML = OFF_MASK + 32;              // float [4 warps][16 rows][2]
+constexpr uint32_t kHalf = kTile * 128;                // 64 channels of a tile's rows (128-byte swizzle); K: 2, V: 2
+constexpr uint32_t OFF_INFO = kStages * kStageBytes;   // int4 per stage: request, head and row block, tile, length
+constexpr uint32_t OFF_MASK = OFF_INFO + 64;           // uint64 per stage: which tokens of the tile are there
+constexpr uint32_t OFF_ML = OFF_MASK + 32;             // float [4 warps][16 rows][2]
 constexpr uint32_t OFF_SCAN = OFF_ML + 512;
-constexpr uint32_t kSmemBytes = OFF_SCAN + 64;
+constexpr uint32_t OFF_BAR = OFF_SCAN + 64;            // landed [3], free [3], readers met, abort flag
+constexpr uint32_t kSmemBytes = OFF_BAR + 64 + 1024;
 static_assert(4 * 16 * kD * 4 <= kStageBytes, "the warps' sums fit one stage");
 
-__device__ __forceinline__ uint32_t row_chunk(int row, int chunk) { return row * 256 + ((chunk ^ (row & 7)) << 4); }
+// 16 bytes (8 channels) `chunk` of a tile's row
+__device__ __forceinline__ uint32_t row_chunk(int row, int chunk) {
+  return (chunk >> 3) * kHalf + row * 128 + (((chunk ^ row) & 7) << 4);
+}
 
-__device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool there) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+struct PagedMaps {
+  CUtensorMap k, v;   // [page, token, head, 128], boxes of 64 channels x `box` tokens, 128-byte swizzle
+  int box;            // 0: none, rows come by asynchronous copies
+};
+
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map, int c0, int c1, int c2, int c3,
+                                            uint64_t *bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];"
+      ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(sm100::smem_u32(bar))
+      : "memory");
+}
+__device__ __forceinline__ void cp16(uint32_t dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+// The two of a word's bf16 that bits 0 and 1 ask for.
+__device__ __forceinline__ uint32_t pick2(uint32_t bits) {
+  return (bits & 1 ? 0x0000FFFFu : 0u) | (bits & 2 ? 0xFFFF0000u : 0u);
+}
+// Tokens 0 .. n - 1 of a tile.
+__device__ __forceinline__ uint64_t first_tokens(int n) {
+  return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1;
 }
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -60,7 +91,11 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4],
 // A place in the line of tiles: tile `tile` of item (request b, key head and row block hr).
 struct Cursor {
   int b, hr, tile, ntiles, len;
+  int cost;       // units of an item besides its tiles'
+  int64_t unit;   // of the tile
 };
+constexpr int kItemCost = 4;   // (0 where there is a CTA for every tile)
+constexpr int kLastTile = 1 << 30;   // with the head and row block: the stretch ends here
 
 // Tokens of request b; a length that is none, or that its table row cannot hold, counts as 0.
 __device__ __forceinline__ int request_len(const PagedArgs &p, int b) {
@@ -75,8 +110,10 @@ __device__ __forceinline__ int request_len(const PagedArgs &p, int b) {
 __device__ __forceinline__ int tile_count(int len) { return max(1, (len + kTile - 1) / kTile); }
 
 __device__ __forceinline__ void advance(const PagedArgs &p, Cursor &c, int items_per_request) {
+  ++c.unit;
   if (++c.tile < c.ntiles) return;
   c.tile = 0;
+  c.unit += c.cost;
   if (++c.hr < items_per_request) return;
   c.hr = 0;
   if (++c.b < p.B) {
@@ -96,23 +133,39 @@ __device__ __forceinline__ void paged_store_row(const PagedArgs &p, int b, int t
 }
 
 template <int WR>   // row groups of 16; the other 4 / WR warps of a row group split the tile's tokens
-__global__ void __launch_bounds__(kThreads, 2) paged_attention_kernel(PagedArgs p) {
+__global__ void __launch_bounds__(kThreads, 2) paged_attention_kernel(PagedArgs p, const __grid_constant__ PagedMaps maps) {
   constexpr int WT = 4 / WR, kTok = kTile / WT, kNT = kTok / 8;
   constexpr int kRows = 16 * WR;
-  extern __shared__ __align__(128) uint8_t sm[];
-  longlong2 *s_row = reinterpret_cast<longlong2 *>(sm + OFF_ROW);
-  uint32_t *s_mask = reinterpret_cast<uint32_t *>(sm + OFF_MASK);
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *sm = smem_raw + (-sm100::smem_u32(smem_raw) & 1023u);
+  int4 *s_info = reinterpret_cast<int4 *>(sm + OFF_INFO);
+  uint64_t *s_mask = reinterpret_cast<uint64_t *>(sm + OFF_MASK);
   float *s_ml = reinterpret_cast<float *>(sm + OFF_ML);
+  uint64_t *landed = reinterpret_cast<uint64_t *>(sm + OFF_BAR), *freed = landed + kStages, *met = freed + kStages;
+  volatile uint32_t *s_abort = reinterpret_cast<volatile uint32_t *>(sm + OFF_BAR + 56);
   const uint32_t smem = sm100::smem_u32(sm);
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   const int wr = warp % WR, wt = warp / WR;
   const int ipr = p.Hk * p.row_blocks;   // items per request
   sm100::grid_launch_dependents();
+  if (maps.box && tid == kThreads - 32) {
+    sm100::prefetch_tensormap(&maps.k);
+    sm100::prefetch_tensormap(&maps.v);
+  }
+  if (tid == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      sm100::mbar_init(&landed[i], maps.box ? 1 : 33);
+      sm100::mbar_init(&freed[i], kComputeWarps);
+    }
+    sm100::mbar_init(met, kComputeWarps);
+    *s_abort = 0;
+    sm100::fence_mbar_init();
+  }
 
   // ---- this CTA's stretch of the line of tiles
-  int64_t *s_scan = reinterpret_cast<int64_t *>(sm + OFF_SCAN);   // [4] warp sums, then the start's request
+  int64_t *s_scan = reinterpret_cast<int64_t *>(sm + OFF_SCAN);   // [5] warp sums, then the start's request and tile
   int64_t first = 0, last = 0, total = 0;
-  int stretches;   // CTAs with tiles: every one of them has at least one
+  int stretches;   // CTAs with units: every one of them has at least one
   Cursor cur;
   {
     const int per = (p.B + kThreads - 1) / kThreads;
@@ -129,47 +182,51 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attention_kernel(PagedArgs 
     __syncthreads();
     int64_t before = inc - sum;
 #pragma unroll
-    for (int w = 0; w < 4; ++w) {
+    for (int w = 0; w < kThreads / 32; ++w) {
       if (w < warp) before += s_scan[w];
       total += s_scan[w];
     }
-    total *= ipr;
-    before *= ipr;
+    cur.cost = total * ipr > gridDim.x ? kItemCost : 0;
+    total = (total + static_cast<int64_t>(cur.cost) * p.B) * ipr;
+    before = (before + static_cast<int64_t>(cur.cost) * b0) * ipr;
+    sum = (sum + static_cast<int64_t>(cur.cost) * (b1 - b0)) * ipr;
     stretches = static_cast<int>(min(total, static_cast<int64_t>(gridDim.x)));
     if (blockIdx.x < stretches) {
       first = total * blockIdx.x / stretches;
       last = total * (blockIdx.x + 1) / stretches;
     }
     // the thread whose requests hold the first tile walks to it
-    if (first < last && first >= before && first < before + sum * ipr) {
+    if (first < last && first >= before && first < before + sum) {
       int b = b0;
       int64_t at = before;
       while (true) {
-        const int64_t n = static_cast<int64_t>(tile_count(request_len(p, b))) * ipr;
+        const int64_t n = static_cast<int64_t>(cur.cost + tile_count(request_len(p, b))) * ipr;
         if (first < at + n) break;
         at += n;
         ++b;
       }
-      s_scan[4] = b;
-      s_scan[5] = first - at;
+      s_scan[6] = b;
+      s_scan[7] = first - at;
     }
     __syncthreads();
   }
-  if (first >= last) {
-    if (tid == 0 && p.joins) p.joins[blockIdx.x] = make_int4(0, 0, 0, 0);
-    return;
+  bool none = first >= last;
+  if (!none) {
+    cur.b = static_cast<int>(s_scan[6]);
+    cur.len = request_len(p, cur.b);
+    cur.ntiles = tile_count(cur.len);
+    const int per_item = cur.cost + cur.ntiles;
+    cur.hr = static_cast<int>(s_scan[7] / per_item);
+    const int u = static_cast<int>(s_scan[7] - static_cast<int64_t>(cur.hr) * per_item);
+    cur.tile = max(0, u - cur.cost);
+    cur.unit = first - u + cur.cost + cur.tile;
+    none = cur.unit >= last;   // (a stretch of an item's first units alone)
   }
-  cur.b = static_cast<int>(s_scan[4]);
-  cur.len = request_len(p, cur.b);
-  cur.ntiles = tile_count(cur.len);
-  cur.hr = static_cast<int>(s_scan[5] / cur.ntiles);
-  cur.tile = static_cast<int>(s_scan[5] - static_cast<int64_t>(cur.hr) * cur.ntiles);
-  const int ntiles_here = static_cast<int>(last - first);
   // an item that an earlier CTA began: the CTA at the first cut inside it describes the join
   if (tid == 0 && p.joins) {
     int4 j = make_int4(0, 0, 0, 0);
-    if (cur.tile > 0) {
-      const int64_t begin = first - cur.tile, end = begin + cur.ntiles;   // the item's tiles in the line
+    if (!none && cur.tile > 0) {
+      const int64_t begin = cur.unit - cur.tile, end = begin + cur.ntiles;   // the units of the item's tiles
       if (total * (blockIdx.x - 1) / stretches <= begin) {
         int n = 1;   // stretches behind the first that begin before the item's end
         while (blockIdx.x + n < stretches && total * (blockIdx.x + n) / stretches < end) ++n;
@@ -178,104 +235,155 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attention_kernel(PagedArgs 
     }
     p.joins[blockIdx.x] = j;
   }
+  if (none) return;
 
-  // ---- loads: tile i of the stretch at the cursor `ld` (three tiles ahead of the products)
-  Cursor ld = cur;
-  int loaded = 0;   // tiles whose page ids have been asked for
-  int id = 0;       // threads 0..63: the page of token `tid` of that tile
-  int id_pos = 0;
-  bool id_there = false;
-  int id_h = 0;
-  auto ask = [&] {
-    id_there = false;
-    if (loaded < ntiles_here) {
-      if (tid < kTile) {
-        id_pos = ld.tile * kTile + tid;
-        id_h = ld.hr / p.row_blocks;
-        if (id_pos < ld.len) {
-          id = p.table[static_cast<int64_t>(ld.b) * p.table_stride + id_pos / p.page];
-          id_there = true;
-        }
-      }
-      advance(p, ld, ipr);
-    }
-    ++loaded;
-  };
-  auto place = [&] {   // the rows of tile `loaded - 1` (asked for last)
-    const int i = loaded - 1;
-    if (tid < kTile) {
-      bool ok = id_there;
-      if (ok && (id < 0 || id >= p.num_pages)) {
-        atomicOr(p.status, KDA_DEVICE_BAD_PAGE);
-        ok = false;
-      }
-      const int64_t pg = ok ? id : 0, tok = id_pos % p.page;
-      s_row[(i & 1) * kTile + tid] =
-          ok ? make_longlong2(pg * p.k_page_stride + tok * p.k_token_stride + id_h * p.k_head_stride,
-                              pg * p.v_page_stride + tok * p.v_token_stride + id_h * p.v_head_stride)
-             : make_longlong2(-1, -1);
-      const uint32_t m = __ballot_sync(0xffffffffu, ok);
-      if (lane == 0) s_mask[(i & 3) * 2 + warp] = m;
-    }
-  };
-  const int lrow = tid >> 4, lchunk = tid & 15;
-  auto load = [&](int i) {
-    if (i < ntiles_here) {
-      const uint32_t st = smem + (i % kStages) * kStageBytes;
+  if (warp == kComputeWarps) {
+    // ---------------------------------------------------------------- loads
+    const int box = maps.box ? maps.box : 1, boxes = kTile / box;   // TMA: a box a lane; copies: rows lane, lane + 32
+    int id[2];
+    bool there[2];
+    auto ask = [&] {   // the pages of the tile at the cursor
 #pragma unroll
-      for (int r = 0; r < kTile; r += 8) {
-        const longlong2 at = s_row[(i & 1) * kTile + r + lrow];
-        const bool there = at.x >= 0;
-        const uint16_t *ks = p.k + (there ? at.x : 0), *vs = p.v + (there ? at.y : 0);
-        cp16(st + row_chunk(r + lrow, lchunk), ks + lchunk * 8, there);
-        cp16(st + kTile * 256 + row_chunk(r + lrow, lchunk), vs + lchunk * 8, there);
+      for (int x = 0; x < 2; ++x) {
+        const int at = lane + 32 * x, pos = cur.tile * kTile + at * box;
+        there[x] = at < boxes && pos < cur.len;
+        id[x] = there[x] ? p.table[static_cast<int64_t>(cur.b) * p.table_stride + pos / p.page] : 0;
       }
+    };
+    ask();
+    for (int i = 0; ; ++i) {
+      const int st = i % kStages, pos0 = cur.tile * kTile, h = cur.hr / p.row_blocks;
+      const uint32_t dst = smem + st * kStageBytes;
+      int4 info = make_int4(cur.b, cur.hr, cur.tile, cur.len);
+      bool ok[2];
+      int pg[2];
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        pg[x] = id[x];
+        ok[x] = there[x] && id[x] >= 0 && id[x] < p.num_pages;
+        if (there[x] && !ok[x]) atomicOr(p.status, KDA_DEVICE_BAD_PAGE);
+      }
+      advance(p, cur, ipr);
+      const bool more = cur.unit < last;
+      if (more)
+        ask();
+      else
+        info.y |= kLastTile;
+      const uint32_t on[2] = {__ballot_sync(0xffffffffu, ok[0]), __ballot_sync(0xffffffffu, ok[1])};
+      if (i >= kStages) sm100::wait_or_abort(&freed[st], (i / kStages - 1) & 1, s_abort, p.status);
+      if (*s_abort) break;   // (what was asked for lands below)
+      if (lane == 0) {
+        uint64_t mask = (static_cast<uint64_t>(on[1]) << 32) | on[0];
+        if (box > 1) {
+          mask = 0;
+          for (int x = 0; x < boxes; ++x)
+            if (on[0] >> x & 1) mask |= first_tokens(box) << (x * box);
+          mask &= first_tokens(info.w - pos0);
+        }
+        s_info[st] = info;
+        s_mask[st] = mask;
+        if (maps.box)
+          sm100::mbar_arrive_expect_tx(&landed[st], __popc(on[0]) * box * 512);
+        else
+          sm100::mbar_arrive(&landed[st]);
+      }
+      __syncwarp();
+      if (maps.box) {
+        if (ok[0]) {
+          const int tok = (pos0 + lane * box) % p.page;
+          const uint32_t at = dst + lane * box * 128;
+          tma_load_4d(at, &maps.k, 0, h, tok, pg[0], &landed[st]);
+          tma_load_4d(at + kHalf, &maps.k, 64, h, tok, pg[0], &landed[st]);
+          tma_load_4d(at + 2 * kHalf, &maps.v, 0, h, tok, pg[0], &landed[st]);
+          tma_load_4d(at + 3 * kHalf, &maps.v, 64, h, tok, pg[0], &landed[st]);
+        }
+        __syncwarp();
+      } else {
+        int64_t ka[2], va[2];   // this lane's two rows (-1: not there)
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const int64_t tok = (pos0 + lane + 32 * x) % p.page;
+          ka[x] = ok[x] ? pg[x] * p.k_page_stride + tok * p.k_token_stride + h * p.k_head_stride : -1;
+          va[x] = pg[x] * p.v_page_stride + tok * p.v_token_stride + h * p.v_head_stride;
+        }
+        const int chunk = lane & 15;
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+#pragma unroll 4
+          for (int r = 0; r < 32; r += 2) {
+            const int from = r + (lane >> 4);
+            const int64_t k = __shfl_sync(0xffffffffu, ka[x], from), v = __shfl_sync(0xffffffffu, va[x], from);
+            if (k >= 0) {
+              const uint32_t at = dst + row_chunk(32 * x + from, chunk);
+              cp16(at, p.k + k + chunk * 8);
+              cp16(at + 2 * kHalf, p.v + v + chunk * 8);
+            }
+          }
+        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(sm100::smem_u32(&landed[st])) : "memory");
+      }
+      if (!more) break;
     }
-    asm volatile("cp.async.commit_group;" ::: "memory");
-  };
-  ask(); place();
-  __syncthreads();
-  load(0);
-  ask(); place();
-  __syncthreads();
-  load(1);
-  ask(); place();   // tile 2's rows: read behind the first barrier of the loop
+    // (after a timeout the copies in flight are waited for here; otherwise the readers have waited for them)
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    if (*s_abort)
+      for (int i = 0; i < kStages; ++i) {
+        sm100::mbar_wait(&landed[i], 0);
+        sm100::mbar_wait(&landed[i], 1);
+      }
+    return;
+  }
 
+  // ------------------------------------------------------------------ products
   const float sl2 = p.scale * kLog2e;
   uint32_t qf[8][4];
   float o[16][4], m2[2], l2[2];   // rows g and g + 8 of the warp's group
   int lim[2];                     // tokens each row sees
   const int g = lane >> 2, t4 = lane & 3;
   bool fresh = true;              // an item begins
+  int begun = 0;                  // the stretch's first tile of the item
+  uint32_t meetings = 0;
+  // the readers wait for each other (bounded like every wait: after a timeout nobody is waited for)
+  const auto meet = [&] {
+    __syncwarp();
+    if (lane == 0) sm100::mbar_arrive(met);
+    sm100::wait_or_abort(met, meetings++ & 1, s_abort, p.status);
+  };
 
-  for (int i = 0; i < ntiles_here; ++i) {
-    asm volatile("cp.async.wait_group 1;" ::: "memory");
-    __syncthreads();   // tile i has landed; tile i - 1's stage is free; tile i + 2's rows are placed
-    load(i + 2);
-    ask();             // tile i + 3
+  const auto begin_item = [&] {
+    const int rb = cur.hr % p.row_blocks, h = cur.hr / p.row_blocks;
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      const int row = rb * kRows + 16 * wr + g + 8 * s;   // row of the key head: new token row / G, head row % G
+      const int t = row / p.G;
+      lim[s] = t < p.T ? min(max(cur.len - p.T + t + 1, 0), cur.len) : 0;
+      const uint16_t *src = p.q + (static_cast<int64_t>(cur.b) * p.T + t) * p.q_stride + (h * p.G + row % p.G) * kD + t4 * 2;
+#pragma unroll
+      for (int kk = 0; kk < 8; ++kk) {
+        qf[kk][s] = t < p.T ? *reinterpret_cast<const uint32_t *>(src + kk * 16) : 0u;
+        qf[kk][s + 2] = t < p.T ? *reinterpret_cast<const uint32_t *>(src + kk * 16 + 8) : 0u;
+      }
+      m2[s] = -INFINITY;
+      l2[s] = 0.f;
+    }
+#pragma unroll
+    for (int n = 0; n < 16; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[n][e] = 0.f;
+  };
+  begin_item();   // (the first one's queries come beside its first tile)
+  for (int i = 0;; ++i) {
+    const int st = i % kStages;
+    sm100::wait_or_abort(&landed[st], (i / kStages) & 1, s_abort, p.status);
+    const int4 info = s_info[st];
+    if (*s_abort) break;
+    cur.b = info.x; cur.hr = info.y & (kLastTile - 1); cur.tile = info.z; cur.len = info.w;
+    const bool stretch_ends = info.y & kLastTile;
     if (fresh) {
       fresh = false;
-      const int rb = cur.hr % p.row_blocks, h = cur.hr / p.row_blocks;
-#pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        const int row = rb * kRows + 16 * wr + g + 8 * s;   // row of the key head: new token row / G, head row % G
-        const int t = row / p.G;
-        lim[s] = t < p.T ? min(max(cur.len - p.T + t + 1, 0), cur.len) : 0;
-        const uint16_t *src = p.q + (static_cast<int64_t>(cur.b) * p.T + t) * p.q_stride + (h * p.G + row % p.G) * kD + t4 * 2;
-#pragma unroll
-        for (int kk = 0; kk < 8; ++kk) {
-          qf[kk][s] = t < p.T ? *reinterpret_cast<const uint32_t *>(src + kk * 16) : 0u;
-          qf[kk][s + 2] = t < p.T ? *reinterpret_cast<const uint32_t *>(src + kk * 16 + 8) : 0u;
-        }
-        m2[s] = -INFINITY;
-        l2[s] = 0.f;
-      }
-#pragma unroll
-      for (int n = 0; n < 16; ++n)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[n][e] = 0.f;
+      begun = i;
+      if (i > 0) begin_item();
     }
-    const uint32_t kt = smem + (i % kStages) * kStageBytes, vt = kt + kTile * 256;
+    const uint32_t kt = smem + st * kStageBytes, vt = kt + 2 * kHalf;
     const int tok0 = wt * kTok;   // the warp's tokens of the tile
 
     // ---- scores
@@ -293,19 +401,27 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attention_kernel(PagedArgs 
         mma_16816(s[n], qf[kk], b[0], b[1]);
         mma_16816(s[n + 1], qf[kk], b[2], b[3]);
       }
-    // ---- masks, running maximum
-    const uint64_t mask = (static_cast<uint64_t>(s_mask[(i & 3) * 2 + 1]) << 32) | s_mask[(i & 3) * 2];
+    // ---- masks (tiles that every row sees whole need none), running maximum
+    const uint64_t mask = s_mask[st];
     const int pos0 = cur.tile * kTile;
+    const bool edge = mask != ~0ull || pos0 + kTile > cur.len - p.T + 1;
     float mx[2] = {m2[0], m2[1]};
 #pragma unroll
     for (int n = 0; n < kNT; ++n)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int tk = tok0 + n * 8 + t4 * 2 + (e & 1);
-        const bool seen = ((mask >> tk) & 1) && pos0 + tk < lim[e >> 1];
-        s[n][e] = seen ? s[n][e] * sl2 : -INFINITY;
-        mx[e >> 1] = fmaxf(mx[e >> 1], s[n][e]);
-      }
+      for (int e = 0; e < 4; ++e) s[n][e] *= sl2;
+    if (edge) {
+      const uint64_t seen[2] = {mask & first_tokens(lim[0] - pos0), mask & first_tokens(lim[1] - pos0)};
+#pragma unroll
+      for (int n = 0; n < kNT; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (!(seen[e >> 1] >> (tok0 + n * 8 + t4 * 2 + (e & 1)) & 1)) s[n][e] = -INFINITY;
+    }
+#pragma unroll
+    for (int n = 0; n < kNT; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) mx[e >> 1] = fmaxf(mx[e >> 1], s[n][e]);
     float base[2];
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
@@ -335,74 +451,82 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attention_kernel(PagedArgs 
       pf[n >> 1][(n & 1) * 2] = pack_bf16x2(e0, e1);
       pf[n >> 1][(n & 1) * 2 + 1] = pack_bf16x2(e2, e3);
     }
-    // ---- values.  A new token's value row that an earlier new token must not see would still meet its zero weight
-    // in the product, where NaN and infinities survive: such rows (they are looked for among the last T - 1 tokens
-    // only) take the second form, one new token at a time, with the rows behind it zeroed.
-    bool poisoned = false;
-    if (p.T > 1 && pos0 + kTile > cur.len - p.T + 1) {
-      bool bad = false;
-      for (int x = tid; x < kTile * 16; x += kThreads) {
-        const int r = x >> 4;
-        if (pos0 + r > cur.len - p.T && pos0 + r < cur.len) {
-          const uint4 w = *reinterpret_cast<const uint4 *>(sm + (vt - smem) + row_chunk(r, x & 15));
-          const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            bad |= (ws[e] & 0x7F80u) == 0x7F80u || (ws[e] & 0x7F800000u) == 0x7F800000u;
-        }
-      }
-      poisoned = __syncthreads_or(bad);
-    }
-    if (!poisoned) {
+    // ---- values
+    auto value_pair = [&](uint32_t (&b)[4], int k, int n) {   // tokens k*16 .. +15, channels n*8 .. +15
+      ldsm4_t(b, vt + row_chunk(tok0 + k * 16 + (lane & 15), n + (lane >> 4)));
+    };
+    if (!edge) {
 #pragma unroll
       for (int k = 0; k < kNT / 2; ++k)
 #pragma unroll
         for (int n = 0; n < 16; n += 2) {
-          uint32_t b[4];   // tokens k*16 .. +15, channels n*8 .. +15
-          ldsm4_t(b, vt + row_chunk(tok0 + k * 16 + (lane & 15), n + (lane >> 4)));
+          uint32_t b[4];
+          value_pair(b, k, n);
           mma_16816(o[n], pf[k], b[0], b[1]);
           mma_16816(o[n + 1], pf[k], b[2], b[3]);
         }
     } else {
-      for (int t = p.T - 1; t >= 0; --t) {
-        const int n_t = min(max(cur.len - p.T + t + 1, 0), cur.len);
-        for (int x = tid; x < kTile * 16; x += kThreads)
-          if (pos0 + (x >> 4) >= n_t)
-            *reinterpret_cast<uint4 *>(sm + (vt - smem) + row_chunk(x >> 4, x & 15)) = make_uint4(0u, 0u, 0u, 0u);
-        __syncthreads();
-        const int row0 = (cur.hr % p.row_blocks) * kRows + 16 * wr + g;
-        const bool on0 = row0 / p.G == t, on1 = (row0 + 8) / p.G == t;
+      // Rows that are not there hold anything, and NaN and infinities would survive their zero weights: they are cleared
+      // on the way.  So would a new token's value row that earlier new tokens must not see: where one is not finite the
+      // new tokens take their products one at a time, with the rows behind them cleared.
+      const auto cleared = [&](uint32_t (&b)[4], int k, uint64_t rows) {
+        const uint32_t r = static_cast<uint32_t>(rows >> (tok0 + k * 16 + 2 * t4));
+        const uint32_t lo = pick2(r), hi = pick2(r >> 8);
+        b[0] &= lo; b[2] &= lo;
+        b[1] &= hi; b[3] &= hi;
+      };
+      bool bad = false;
+      const uint64_t later = mask & ~first_tokens(cur.len - p.T + 1 - pos0);
+      if (later) {
 #pragma unroll
         for (int k = 0; k < kNT / 2; ++k)
 #pragma unroll
           for (int n = 0; n < 16; n += 2) {
             uint32_t b[4];
-            ldsm4_t(b, vt + row_chunk(tok0 + k * 16 + (lane & 15), n + (lane >> 4)));
-            float x[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+            value_pair(b, k, n);
+            cleared(b, k, later);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) bad |= (b[e] & 0x7F80u) == 0x7F80u || (b[e] & 0x7F800000u) == 0x7F800000u;
+          }
+        bad = __any_sync(0xffffffffu, bad);
+      }
+      const int row0 = (cur.hr % p.row_blocks) * kRows + 16 * wr + g;
+#pragma unroll 1
+      for (int t = bad ? p.T - 1 : 0; t >= 0; --t) {
+        const uint64_t rows = bad ? mask & first_tokens(cur.len - p.T + t + 1 - pos0) : mask;
+        const bool on0 = !bad || row0 / p.G == t, on1 = !bad || (row0 + 8) / p.G == t;
+#pragma unroll
+        for (int n = 0; n < 16; n += 2) {
+          float x[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+#pragma unroll
+          for (int k = 0; k < kNT / 2; ++k) {
+            uint32_t b[4];
+            value_pair(b, k, n);
+            cleared(b, k, rows);
             mma_16816(x[0], pf[k], b[0], b[1]);
             mma_16816(x[1], pf[k], b[2], b[3]);
-#pragma unroll
-            for (int y = 0; y < 2; ++y) {
-              if (on0) { o[n + y][0] += x[y][0]; o[n + y][1] += x[y][1]; }
-              if (on1) { o[n + y][2] += x[y][2]; o[n + y][3] += x[y][3]; }
-            }
           }
-        __syncthreads();
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            if (on0) { o[n + y][0] += x[y][0]; o[n + y][1] += x[y][1]; }
+            if (on1) { o[n + y][2] += x[y][2]; o[n + y][3] += x[y][3]; }
+          }
+        }
       }
     }
-    place();   // tile i + 3's rows, by the page ids asked for before the products
 
     // ---- the item's (or the stretch's) end: join the warps of each row group, write the rows or the part
-    const bool item_ends = cur.tile + 1 == cur.ntiles;
-    if (item_ends || i + 1 == ntiles_here) {
-      const bool whole = item_ends && cur.tile - i <= 0;   // the item began in this stretch, too
+    const bool item_ends = cur.tile + 1 == tile_count(cur.len);
+    if (item_ends || stretch_ends) {
+      const bool from_start = cur.tile == i - begun;   // the item began in this stretch, too
+      const bool whole = item_ends && from_start;
       float l0 = l2[0], l1 = l2[1];
       l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
       l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
       l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
       l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
-      __syncthreads();   // tile i has been read: its stage takes the sums
-      float *so = reinterpret_cast<float *>(sm + (i % kStages) * kStageBytes);
+      meet();   // tile i has been read: its stage takes the sums
+      float *so = reinterpret_cast<float *>(sm + st * kStageBytes);
 #pragma unroll
       for (int n = 0; n < 16; ++n) {
         const int c = (n * 8 + t4 * 2) ^ (g << 3);
@@ -415,10 +539,10 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attention_kernel(PagedArgs 
         s_ml[(warp * 16 + g + 8) * 2] = m2[1];
         s_ml[(warp * 16 + g + 8) * 2 + 1] = l1;
       }
-      __syncthreads();
+      meet();
       const int rb = cur.hr % p.row_blocks, h = cur.hr / p.row_blocks;
-      const int slot = 2 * blockIdx.x + (cur.tile - i <= 0 ? 1 : 0);
-      for (int r = warp; r < kRows; r += 4) {
+      const int slot = 2 * blockIdx.x + (from_start ? 1 : 0);
+      for (int r = warp; r < kRows; r += kComputeWarps) {
         const int row = rb * kRows + r, t = row / p.G;
         if (t >= p.T) break;
         const int gr = r >> 4, rr = r & 15;
@@ -445,44 +569,125 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attention_kernel(PagedArgs 
         }
       }
       fresh = true;
+      sm100::fence_async_smem();   // (the stage's next tile comes behind these accesses)
     }
-    advance(p, cur, ipr);
+    __syncwarp();
+    if (lane == 0) sm100::mbar_arrive(&freed[st]);
+    if (stretch_ends) break;
   }
-  asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
-// Joins the parts of the items that the stretches cut: CTA (cut i, group of 4 rows), a warp per row.
-__global__ void __launch_bounds__(kThreads) paged_join_kernel(PagedArgs p, int rows_per_item) {
+// Joins the parts of the items that the stretches cut.  Every CTA lists the joins (few places hold one) and takes rows of
+// them in turn, with 2, 4, 8 or 16 warps a row (`split`), each with every split-th part, four of them under way together.
+// Bound by the latency of three dependent loads (the list, the parts, the row), so all rows go at once where they can.
+constexpr int kJoinThreads = 512, kJoinWarps = kJoinThreads / 32, kJoinCtas = 304;
+static_assert(kPagedMaxCtas <= kJoinThreads, "a place a thread");
+__global__ void __launch_bounds__(kJoinThreads, 2) paged_join_kernel(PagedArgs p, int rows_per_item, int places) {
+  __shared__ int4 s_join[kPagedMaxCtas];
+  __shared__ int s_count[kJoinWarps];
+  __shared__ float4 s_acc[kJoinWarps][32];
+  __shared__ float2 s_ml[kJoinWarps];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   sm100::grid_dependency_wait();
-  const int cut = blockIdx.x;
-  const int4 j = p.joins[cut];
-  const int r = blockIdx.y * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  if (j.x == 0) return;
-  const int rb = j.z % p.row_blocks, h = j.z / p.row_blocks;
-  const int row = rb * rows_per_item + r, t = row / p.G;
-  if (t >= p.T) return;
-  // part 0: the stretch before the cut, in its last slot; part n: the n-th stretch from the cut on, in its first
-  auto part = [&](int n) {
-    const int slot = n == 0 ? 2 * (cut - 1) + 1 : 2 * (cut + n - 1);
-    return p.parts + (static_cast<size_t>(slot) * rows_per_item + r) * kPagedPartFloats;
-  };
-  float mm = -INFINITY;
-  for (int n = lane; n < j.x; n += 32) mm = fmaxf(mm, part(n)[kD]);
+  int4 mine = static_cast<int>(threadIdx.x) < places ? p.joins[threadIdx.x] : make_int4(0, 0, 0, 0);
+  mine.w = threadIdx.x;
+  const uint32_t on = __ballot_sync(0xffffffffu, mine.x != 0);
+  if (lane == 0) s_count[warp] = __popc(on);
+  __syncthreads();
+  int joins = 0;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, o));
-  const float bs = mm == -INFINITY ? 0.f : mm;
-  float ll = 0.f;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int n = 0; n < j.x; ++n) {
-    const float *q = part(n);
-    const float2 ml = *reinterpret_cast<const float2 *>(q + kD);
-    const float4 x = *reinterpret_cast<const float4 *>(q + lane * 4);
-    const float c = fast_exp2(ml.x - bs);
-    ll += c * ml.y;
-    acc.x += c * x.x; acc.y += c * x.y; acc.z += c * x.z; acc.w += c * x.w;
+  for (int i = 0; i < kJoinWarps; ++i) {
+    if (i == warp && mine.x != 0) s_join[joins + __popc(on & ((1u << lane) - 1))] = mine;
+    joins += s_count[i];
   }
-  paged_store_row(p, j.y, t, h * p.G + row % p.G, lane, acc, mm, ll);
+  __syncthreads();
+  const int rows = min(rows_per_item, p.T * p.G);   // (a last row block may have fewer)
+  const int units = joins * rows, most = gridDim.x * kJoinWarps;
+  int split = kJoinWarps;
+  while (split > 2 && units * split > most) split >>= 1;
+  const int w = warp & (split - 1), per_cta = kJoinWarps / split;
+  for (int at0 = per_cta * blockIdx.x; at0 < units; at0 += per_cta * gridDim.x) {
+    const int at = at0 + warp / split;
+    const int4 j = s_join[min(at, units - 1) / rows];
+    const int cut = j.w, r = at % rows;
+    const int rb = j.z % p.row_blocks, h = j.z / p.row_blocks;
+    const int row = rb * rows_per_item + r, t = row / p.G;
+    const bool there = at < units && t < p.T;
+    float m = -INFINITY, l = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (there) {
+      // part 0: the stretch before the cut, in its last slot; part n: the n-th stretch from the cut on, in its first
+      auto part = [&](int n) {
+        const int slot = n == 0 ? 2 * (cut - 1) + 1 : 2 * (cut + n - 1);
+        return p.parts + (static_cast<size_t>(slot) * rows_per_item + r) * kPagedPartFloats;
+      };
+      for (int n0 = w; n0 < j.x; n0 += 4 * split) {
+        float2 ml[4];
+        float4 x[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int n = n0 + i * split;
+          ml[i] = make_float2(-INFINITY, 0.f);
+          x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (n < j.x) {
+            const float *q = part(n);
+            ml[i] = *reinterpret_cast<const float2 *>(q + kD);
+            x[i] = *reinterpret_cast<const float4 *>(q + lane * 4);
+          }
+        }
+        float top = m;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) top = fmaxf(top, ml[i].x);
+        const float base = top == -INFINITY ? 0.f : top, c0 = fast_exp2(m - base);
+        l *= c0;
+        acc = make_float4(c0 * acc.x, c0 * acc.y, c0 * acc.z, c0 * acc.w);
+        m = top;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float c = fast_exp2(ml[i].x - base);
+          l += c * ml[i].y;
+          acc.x += c * x[i].x; acc.y += c * x[i].y; acc.z += c * x[i].z; acc.w += c * x[i].w;
+        }
+      }
+      s_acc[warp][lane] = acc;
+      if (lane == 0) s_ml[warp] = make_float2(m, l);
+    }
+    __syncthreads();
+    if (there && w == 0) {
+      float top = m;
+      for (int i = 1; i < split; ++i) top = fmaxf(top, s_ml[warp + i].x);
+      const float base = top == -INFINITY ? 0.f : top, c0 = fast_exp2(m - base);
+      l *= c0;
+      acc = make_float4(c0 * acc.x, c0 * acc.y, c0 * acc.z, c0 * acc.w);
+      for (int i = 1; i < split; ++i) {
+        const float2 ml = s_ml[warp + i];
+        const float4 x = s_acc[warp + i][lane];
+        const float c = fast_exp2(ml.x - base);
+        l += c * ml.y;
+        acc.x += c * x.x; acc.y += c * x.y; acc.z += c * x.z; acc.w += c * x.w;
+      }
+      paged_store_row(p, j.y, t, h * p.G + row % p.G, lane, acc, top, l);
+    }
+    __syncthreads();
+  }
+}
+
+// Boxes of fewer rows are not worth a TMA copy each (four a box).  Measured over 64 x 8192 tokens, 2 key heads: boxes of 8
+// 115 us against 132 us by asynchronous copies, of 4 171 us against 132 (of 16 and more 93 us).
+constexpr int kLeastBox = 8;
+
+// false: the strides or sizes are none that a tensor map takes
+bool make_page_map(CUtensorMap *map, const uint16_t *pages, int64_t page_stride, int64_t token_stride, int64_t head_stride,
+                   const PagedArgs &a, int box) {
+  const int64_t most = (int64_t(1) << 39) / 2;
+  if (a.num_pages < 1 || page_stride <= 0 || token_stride <= 0 || head_stride <= 0 || page_stride >= most ||
+      token_stride >= most || head_stride >= most)
+    return false;
+  const uint64_t dims[4] = {kD, static_cast<uint64_t>(a.Hk), static_cast<uint64_t>(a.page), static_cast<uint64_t>(a.num_pages)};
+  const uint64_t strides[3] = {static_cast<uint64_t>(head_stride) * 2, static_cast<uint64_t>(token_stride) * 2,
+                               static_cast<uint64_t>(page_stride) * 2};
+  const uint32_t boxes[4] = {64, 1, static_cast<uint32_t>(box), 1};
+  return make_bf16_map(map, pages, 4, dims, strides, boxes);
 }
 
 template <int WR>
@@ -501,18 +706,24 @@ cudaError_t launch_paged(PagedArgs a, cudaStream_t stream) {
   const int64_t most = items * std::max<int64_t>(1, (a.max_len + kTile - 1) / kTile);   // tiles there can be
   if (most == items) a.joins = nullptr;   // one tile an item: nothing is cut
   const unsigned grid = static_cast<unsigned>(std::min<int64_t>(most, std::min(2 * sms, kPagedMaxCtas)));
-  paged_attention_kernel<WR><<<grid, kThreads, kSmemBytes, stream>>>(a);
+  PagedMaps maps;
+  maps.box = 1;
+  while (maps.box < kTile && a.page % (2 * maps.box) == 0) maps.box *= 2;
+  if (maps.box < kLeastBox || !make_page_map(&maps.k, a.k, a.k_page_stride, a.k_token_stride, a.k_head_stride, a, maps.box) ||
+      !make_page_map(&maps.v, a.v, a.v_page_stride, a.v_token_stride, a.v_head_stride, a, maps.box))
+    maps.box = 0;
+  paged_attention_kernel<WR><<<grid, kThreads, kSmemBytes, stream>>>(a, maps);
   if (const cudaError_t e = cudaGetLastError()) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid, 4 * WR);
-  cfg.blockDim = dim3(kThreads);
+  cfg.gridDim = dim3(std::min(grid * 16 * WR, static_cast<unsigned>(kJoinCtas)));
+  cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return a.joins ? cudaLaunchKernelEx(&cfg, paged_join_kernel, a, 16 * WR) : cudaSuccess;
+  return a.joins ? cudaLaunchKernelEx(&cfg, paged_join_kernel, a, 16 * WR, static_cast<int>(grid)) : cudaSuccess;
 }
 
 }  // namespace

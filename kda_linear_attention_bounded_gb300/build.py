@@ -1,8 +1,9 @@
 """Build libkda (the CUDA path) in-tree with nvcc for sm_103a.
 
 Translation units are compiled in parallel and linked into
-``kda_linear_attention_bounded_gb300/_build/libkda.so``.  The CUDA runtime is
-linked statically and the driver API (tensor-map encoding) is resolved at run
+``kda_linear_attention_bounded_gb300/_build/libkda.so``; ``csrc/kda_torch.cpp``
+(torch tensors' argument checks, for the running interpreter) becomes
+``_build/_kda_torch.so`` beside it.  The CUDA runtime is linked statically and the driver API (tensor-map encoding) is resolved at run
 time, so the library loads on a machine without a GPU driver.
 """
 from __future__ import annotations
@@ -18,6 +19,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libkda.so")
+TORCH_SRC = os.path.join(CSRC, "kda_torch.cpp")
+TORCH_EXT = os.path.join(BUILD, "_kda_torch.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
@@ -37,14 +40,27 @@ def sources():
 
 def _deps():
     return sources() + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cuh")) + \
-        [os.path.join(INCLUDE, "kda.h"), os.path.abspath(__file__)]
+        [os.path.join(INCLUDE, "kda.h"), TORCH_SRC, os.path.abspath(__file__)]
+
+
+def _torch_ext_command(out):
+    import sysconfig
+
+    import torch
+
+    root = os.path.dirname(os.path.abspath(torch.__file__))
+    cuda = os.path.dirname(os.path.dirname(_nvcc())) or "/usr/local/cuda"
+    return [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-shared",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", f"-I{INCLUDE}", f"-I{root}/include",
+            f"-I{root}/include/torch/csrc/api/include", f"-I{cuda}/include", f"-I{sysconfig.get_paths()['include']}",
+            TORCH_SRC, "-o", out, f"-L{root}/lib", "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"]
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     os.makedirs(BUILD, exist_ok=True)
-    if not force and os.path.exists(LIB):
+    if not force and os.path.exists(LIB) and os.path.exists(TORCH_EXT):
         newest = max(os.path.getmtime(p) for p in _deps())
-        if os.path.getmtime(LIB) >= newest:
+        if min(os.path.getmtime(LIB), os.path.getmtime(TORCH_EXT)) >= newest:
             return LIB
     nvcc = _nvcc()
     procs = []
@@ -56,6 +72,11 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
             print(" ".join(cmd), file=sys.stderr)
         procs.append((src, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)))
         objs.append(obj)
+    ext_tmp = TORCH_EXT + f".tmp{os.getpid()}"
+    cmd = _torch_ext_command(ext_tmp)
+    if verbose:
+        print(" ".join(cmd), file=sys.stderr)
+    procs.append((TORCH_SRC, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)))
     failed = []
     for src, p in procs:
         out, _ = p.communicate()
@@ -64,10 +85,11 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         elif verbose and out:
             print(out, file=sys.stderr)
     if failed:
-        raise RuntimeError("nvcc failed:\n" + "\n".join(failed))
+        raise RuntimeError("compilation failed:\n" + "\n".join(failed))
     tmp = LIB + f".tmp{os.getpid()}"
     subprocess.run([nvcc, *ARCH, "-shared", "-o", tmp, *objs], check=True)
     os.replace(tmp, LIB)
+    os.replace(ext_tmp, TORCH_EXT)
     return LIB
 
 

@@ -120,6 +120,17 @@ def test_wrappers_refuse_host_tensors(lib):
                         slot_map=z.long(), pages_used=z[:1])
 
 
+def test_wrappers_refuse_what_is_no_tensor(lib):
+    import kda_linear_attention_bounded_gb300 as kda
+    z = torch.zeros(3, dtype=torch.int32)
+    with pytest.raises(TypeError, match="q: expected a tensor"):
+        kda.gdn_decode(1, z, z, z, z, z, z, z, z, out=z, workspace=z)
+    with pytest.raises(TypeError, match="block_table: expected a tensor"):
+        kda.step_tables([[1]], z, z, z, 16, cu_seqlens=z, kv_lens=z, positions=z, slot_map=z, pages_used=z, workspace=z)
+    with pytest.raises(ValueError, match="strided"):
+        kda.gdn_decode(torch.eye(3).to_sparse(), z, z, z, z, z, z, z, z, out=z, workspace=z)
+
+
 def _paged(lib, *, q=FAKE, qs=1024, k=FAKE, kps=4096, kts=256, khs=128, v=FAKE, vps=4096, num_pages=9, page=16,
            table=FAKE, ts=4, width=4, lens=FAKE, B=2, T=1, hq=8, hk=2, scale=0.1, out=FAKE, os_=1024, lse=None, ws=FAKE,
            ws_bytes=None):

@@ -136,6 +136,33 @@ def test_what_is_not_seen_does_not_matter():
         assert torch.isnan(out[b * 3 + 2]).all()
 
 
+@pytest.mark.parametrize("bad", [0, 1, 77, 149, 399])
+@pytest.mark.parametrize("longest", [40, 700])
+def test_a_bad_length_is_recorded_wherever_it_is(bad, longest):
+    # with items cut and whole, whichever CTA has it
+    B = 150 if bad < 150 else 400
+    q, k, v, table, lens = make([1 + 37 * i % longest for i in range(B)], 1, 8, 1, 16, seed=12)
+    good, _ = check(q, k, v, table, lens, 1)
+    for n in (-1, 16 * table.shape[1] + 1):
+        wrong = lens.clone()
+        wrong[bad] = n
+        ws = kda.make_workspace(nbytes=kda.paged_workspace_size(8, 1, 1))
+        out, _ = kda.paged_attention(q, k, v, table, wrong, 1, workspace=ws)
+        assert kda.read_device_status(ws) == kda.KDA_DEVICE_BAD_COUNT
+        assert (out[bad] == 0).all()
+        rest = [b for b in range(B) if b != bad]
+        assert rel_l2(out[rest], good[rest].cpu()) <= 2 * OUT_TOL
+
+
+@pytest.mark.parametrize("hk,page,pages", [(1, 16, 30), (1, 64, 30), (3, 512, 1), (1, 512, 1)])
+def test_strides_of_one_head_or_page_do_not_matter(hk, page, pages):
+    q, k, v, table, lens = make([page * pages - 3], 1, 4 * hk, hk, page, seed=13, spare=0)
+    out, _ = check(q, k, v, table, lens, 1)
+    st = [0 if n == 1 else s for n, s in zip(k.shape, k.stride())]
+    k0, v0 = (t.as_strided(t.shape, st) for t in (k, v))
+    assert torch.equal(check(q, k0, v0, table, lens, 1)[0], out)
+
+
 def test_bad_pages_and_lengths_are_left_out():
     q, k, v, table, lens = make([100, 200, 50], 1, 8, 2, 16, seed=11)
     table[1, 4], table[1, 7] = k.shape[0], -1

@@ -215,7 +215,9 @@ __global__ void __launch_bounds__(in::kThreads, 4) gdn_intra_kernel(const __grid
   uint8_t *s_blk = sm + OFF_BLK;
   float *sA = reinterpret_cast<float *>(sm + OFF_A);
 
-  grid_launch_dependents();   // the state pass may take SMs as this grid leaves them
+  // (TMEM is taken behind the wait: a grid before this one may still be taking its own)
+  grid_dependency_wait();
+  grid_launch_dependents();   // the state pass may take SMs as this grid leaves them, and read the caller's tensors
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);   // (uniform in the warp)
   const int hk = blockIdx.x % prm.Hk, slot = blockIdx.x / prm.Hk;
   int n = 0;   // the slot's sequence: the last that starts at or before it
@@ -506,6 +508,8 @@ constexpr uint32_t TM_KU = 0 /* two of 64 */, TM_D = 0 /* 128, over KU */, TM_U 
                    TM_V = 192 /* over U */, TM_QS = 256, TM_S = 320 /* two of 64 */, TM_UH = 320 /* 32, over S */,
                    TM_R = 448 /* two of 32 */, kTmemCols = 512;
 }  // namespace ch
+// A CTA of the state pass takes all of an SM's TMEM, possibly before the intra-chunk grid is done: the two never share one.
+static_assert(ch::kSmemBytes + in::kSmemBytes + 2048 > 233472, "no SM holds CTAs of both");
 
 __device__ __forceinline__ void bulk_prefetch(const void *src, uint32_t bytes) {
   asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(reinterpret_cast<uint64_t>(src)), "r"(bytes) : "memory");
@@ -1113,25 +1117,6 @@ __global__ void __launch_bounds__(256, 1) gdn_join_kernel(const __grid_constant_
   }
 }
 
-template <typename K>
-cudaError_t launch_behind(K kernel, int ctas, int threads, uint32_t smem, const GdnPrefillParams &p, cudaStream_t stream) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(ctas));
-  cfg.blockDim = dim3(static_cast<unsigned>(threads));
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, p);
-}
-template <bool SEGMENTS>
-cudaError_t launch_chain(const GdnPrefillParams &p, int ctas, cudaStream_t stream) {
-  return launch_behind(gdn_chain_kernel<SEGMENTS>, ctas, ch::kThreads, ch::kSmemBytes, p, stream);
-}
-
 int chunks_of(const GdnPrefillParams &p, int n) { return (p.cu[n + 1] - p.cu[n] + kC - 1) / kC; }
 
 // Chunks per segment, or 0 to leave the sequences whole: the estimates of both in chunks' time.  A grid of at most one
@@ -1206,8 +1191,8 @@ cudaError_t launch_segments(GdnPrefillParams &p, int g, float *mats, cudaStream_
   for (int i = 0; i < p.num_seqs; ++i)
     if (segments(i) == 1) add(i, 0, false);
   p.first_pass = 1;
-  cudaError_t e = launch_chain<true>(p, jobs * p.Hv, stream);
-  if (e == cudaSuccess && joined) e = launch_behind(gdn_join_kernel, joined * p.Hv * kJoinParts, 256, 0, p, stream);
+  cudaError_t e = launch_dependent(gdn_chain_kernel<true>, jobs * p.Hv, ch::kThreads, ch::kSmemBytes, stream, p);
+  if (e == cudaSuccess && joined) e = launch_dependent(gdn_join_kernel, joined * p.Hv * kJoinParts, 256, 0, stream, p);
   if (e != cudaSuccess) return e;
   jobs = mat = 0;
   for (int i = 0; i < p.num_seqs && segments(i) > 1; ++i) {
@@ -1215,7 +1200,7 @@ cudaError_t launch_segments(GdnPrefillParams &p, int g, float *mats, cudaStream_
     mat += 2 * segments(i) - 3;
   }
   p.first_pass = 0;
-  return launch_chain<true>(p, jobs * p.Hv, stream);
+  return launch_dependent(gdn_chain_kernel<true>, jobs * p.Hv, ch::kThreads, ch::kSmemBytes, stream, p);
 }
 
 }  // namespace
@@ -1279,10 +1264,11 @@ cudaError_t launch_gdn_prefill(const GdnRecurrentArgs &a, const int32_t *cu_host
     const int slots = (p.cu[ns] - p.cu[0]) / kC + ns;
     p.blocks = blocks;
     blocks += static_cast<size_t>(slots) * a.Hv * kGdnBlkBytes;
-    gdn_intra_kernel<<<static_cast<unsigned>(slots) * Hk, in::kThreads, in::kSmemBytes, stream>>>(p);
-    if (const cudaError_t e = cudaGetLastError()) return e;
+    if (const cudaError_t e = launch_dependent(gdn_intra_kernel, static_cast<unsigned>(slots) * Hk, in::kThreads, in::kSmemBytes,
+                                               stream, p))
+      return e;
     const int seg = segment_chunks(p, room);
-    if (const cudaError_t e = seg ? launch_segments(p, seg, mats, stream) : launch_chain<false>(p, ns * a.Hv, stream)) return e;
+    if (const cudaError_t e = seg ? launch_segments(p, seg, mats, stream) : launch_dependent(gdn_chain_kernel<false>, ns * a.Hv, ch::kThreads, ch::kSmemBytes, stream, p)) return e;
   }
   return cudaSuccess;
 }

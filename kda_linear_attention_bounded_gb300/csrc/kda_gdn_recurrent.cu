@@ -14,6 +14,7 @@
 // run under the stores of another and the last wave is short.
 #include "kda_common.cuh"
 #include "kda_internal.h"
+#include "kda_sm100.cuh"
 
 namespace kda {
 namespace {
@@ -34,6 +35,8 @@ __global__ void __launch_bounds__(kThreads) gdn_recurrent_kernel(GdnRecurrentArg
   __shared__ float s_alpha[kTile], s_beta[kTile], s_kq[kTile];
   __shared__ __align__(16) float s_red[2][kWarps][2][kCols];   // [token parity][warp][k | q][column]
 
+  sm100::grid_dependency_wait();
+  sm100::grid_launch_dependents();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int part = blockIdx.x % kP;
   const int h = (blockIdx.x / kP) % p.Hv;
@@ -163,8 +166,7 @@ cudaError_t launch_gdn_recurrent(const GdnRecurrentArgs &args, int num_items, cu
   if (num_items <= 0) return cudaSuccess;
   const int64_t grid = static_cast<int64_t>(num_items) * args.Hv * 4;
   if (grid > 0x7fffffff) return cudaErrorInvalidValue;
-  gdn_recurrent_kernel<4><<<static_cast<unsigned>(grid), kThreads, 0, stream>>>(args);
-  return cudaGetLastError();
+  return launch_dependent(gdn_recurrent_kernel<4>, static_cast<unsigned>(grid), kThreads, 0, stream, args);
 }
 
 }  // namespace kda

@@ -26,6 +26,24 @@ cudaError_t set_attributes_once(std::mutex &mu, uint64_t &done, Set set) {
   return e;
 }
 
+// Launches a kernel as a programmatic dependent of what precedes it on the stream: its launch overlaps the end of that.
+// The kernel reads and writes nothing before its grid_dependency_wait, or only what the call's caller may not have
+// pending in the grid directly before it.
+template <typename... P, typename... A>
+cudaError_t launch_dependent(void (*kernel)(P...), unsigned grid, unsigned threads, size_t smem, cudaStream_t stream, const A &...args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // Sigmoid-gated RMSNorm of the output rows (gate == nullptr: none).
 struct OutNorm {
   const uint16_t *gate;   // [rows, H, 128] bf16, indexed by the output row

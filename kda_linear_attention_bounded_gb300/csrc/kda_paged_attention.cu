@@ -149,7 +149,6 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attention_kernel(PagedArgs 
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   const int wr = warp % WR, wt = warp / WR;
   const int ipr = p.Hk * p.row_blocks;   // items per request
-  sm100::grid_launch_dependents();
   if (maps.box && tid == kThreads - 32) {
     sm100::prefetch_tensormap(&maps.k);
     sm100::prefetch_tensormap(&maps.v);
@@ -163,6 +162,8 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attention_kernel(PagedArgs 
     *s_abort = 0;
     sm100::fence_mbar_init();
   }
+  sm100::grid_dependency_wait();
+  sm100::grid_launch_dependents();
 
   // ---- this CTA's stretch of the line of tiles
   int64_t *s_scan = reinterpret_cast<int64_t *>(sm + OFF_SCAN);   // [5] warp sums, then the start's request and tile
@@ -732,18 +733,10 @@ cudaError_t launch_paged(PagedArgs a, cudaStream_t stream) {
   if (maps.box < kLeastBox || !make_page_map(&maps.k, a.k, a.k_page_stride, a.k_token_stride, a.k_head_stride, a, maps.box) ||
       !make_page_map(&maps.v, a.v, a.v_page_stride, a.v_token_stride, a.v_head_stride, a, maps.box))
     maps.box = 0;
-  paged_attention_kernel<WR><<<grid, kThreads, kSmemBytes, stream>>>(a, maps);
-  if (const cudaError_t e = cudaGetLastError()) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(std::min(grid * 16 * WR, static_cast<unsigned>(kJoinCtas)));
-  cfg.blockDim = dim3(kJoinThreads);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return a.joins ? cudaLaunchKernelEx(&cfg, paged_join_kernel, a, 16 * WR, static_cast<int>(grid)) : cudaSuccess;
+  const cudaError_t e = launch_dependent(paged_attention_kernel<WR>, grid, kThreads, kSmemBytes, stream, a, maps);
+  if (e != cudaSuccess || !a.joins) return e;
+  return launch_dependent(paged_join_kernel, std::min(grid * 16 * WR, static_cast<unsigned>(kJoinCtas)), kJoinThreads, 0, stream, a,
+                          16 * WR, static_cast<int>(grid));
 }
 
 }  // namespace

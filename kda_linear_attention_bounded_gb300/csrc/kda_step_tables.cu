@@ -12,6 +12,7 @@
 // from the free list, never from the table, so no CTA waits for another's table writes.
 #include "kda_common.cuh"
 #include "kda_internal.h"
+#include "kda_sm100.cuh"
 
 namespace kda {
 namespace {
@@ -24,6 +25,8 @@ __global__ void __launch_bounds__(kThreads) step_tables_kernel(StepTablesArgs p)
   __shared__ bool s_refused[kThreads];
   __shared__ int64_t s_warp[2][kWarps];
 
+  sm100::grid_dependency_wait();
+  sm100::grid_launch_dependents();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t stride = static_cast<int64_t>(gridDim.x) * kThreads, mine = static_cast<int64_t>(blockIdx.x) * kThreads + tid;
   int64_t rows = 0, pages = 0, granted = 0;   // sums before the window; pages handed out
@@ -153,12 +156,12 @@ __global__ void __launch_bounds__(kThreads) step_tables_kernel(StepTablesArgs p)
 }  // namespace
 
 cudaError_t launch_step_tables(const StepTablesArgs &a, cudaStream_t stream) {
-  const int threads = a.B <= 256 ? 256 : 1024;
+  // a window holds the whole batch where it can (512 requests: 6.0 us with 512 threads, 7.8 with 1024)
+  const int threads = a.B <= 256 ? 256 : a.B <= 512 ? 512 : 1024;
   const int64_t want = (a.max_tokens + threads - 1) / threads;
   const unsigned grid = static_cast<unsigned>(want < 1 ? 1 : want > 608 ? 608 : want);
-  if (threads == 256) step_tables_kernel<256><<<grid, 256, 0, stream>>>(a);
-  else step_tables_kernel<1024><<<grid, 1024, 0, stream>>>(a);
-  return cudaGetLastError();
+  const auto kernel = threads == 256 ? step_tables_kernel<256> : threads == 512 ? step_tables_kernel<512> : step_tables_kernel<1024>;
+  return launch_dependent(kernel, grid, threads, 0, stream, a);
 }
 
 }  // namespace kda

@@ -24,7 +24,7 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kTile = kWarps;   // tokens prepared per prologue pass (one per warp)
 
 template <int kP>
-__global__ void __launch_bounds__(kThreads) gdn_recurrent_kernel(GdnRecurrentArgs p) {
+__global__ void __launch_bounds__(kThreads, 8) gdn_recurrent_kernel(GdnRecurrentArgs p) {
   constexpr int kCols = kD / kP;              // value channels of the CTA
   constexpr int kQuads = kCols / 4;           // threads along a row
   constexpr int kGroups = kThreads / kQuads;  // row groups; group g owns rows g, g + kGroups, ...

@@ -319,3 +319,57 @@ def test_graph_replay_and_other_stream():
     step(stream=side)
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(want, (out, final, dout, pool)))
+
+
+@pytest.mark.parametrize("before", ["memset", "copy", "two streams", "kernel"])
+def test_captured_behind_other_work(before):
+    # the first launch of a call joins whatever the captured stream waits for: a memset, a copy, another stream's work
+    hv, tokens = 2, 3
+    x = gdn_inputs(tokens, 1, hv, seed=31)
+    pool0 = _pool(4, hv, 9)
+    pool, slots = torch.empty_like(pool0), _i32([2, 0, 3])
+    long = gdn_inputs(130, 1, hv, seed=32)
+    cu_h = torch.tensor([0, 100, 130], dtype=torch.int32)
+    cu_d = cu_h.cuda()
+    ws = kda.make_workspace(nbytes=kda.gdn_prefill_workspace_size(130, 2, hv))
+    ws2 = kda.make_workspace()
+    out, out2 = torch.empty((tokens, hv, D), dtype=torch.bfloat16, device="cuda"), torch.empty((130, hv, D), dtype=torch.bfloat16, device="cuda")
+    final = torch.empty((2, hv, D, D), device="cuda")
+    side, main = torch.cuda.Stream(), torch.cuda.Stream()
+
+    def work():
+        s = torch.cuda.current_stream()
+        if before == "two streams":
+            side.wait_stream(s)
+            with torch.cuda.stream(side):
+                pool.copy_(pool0)
+            out.zero_()
+            s.wait_stream(side)
+        elif before == "kernel":
+            torch.add(pool0, 0.0, out=pool)
+        elif before == "memset":
+            pool.copy_(pool0)
+            out.view(torch.uint8).zero_()
+        else:
+            pool.copy_(pool0)
+        kda.gdn_decode(*x, pool, slots, out=out, workspace=ws2)
+        if before == "two streams":
+            side.wait_stream(s)
+            with torch.cuda.stream(side):
+                out2.zero_()
+            s.wait_stream(side)
+        kda.gdn_chunk_prefill(*long, cu_d, cu_h, out=out2, final_state=final, workspace=ws)
+
+    with torch.cuda.stream(main):
+        work()
+        torch.cuda.synchronize()
+        want = [t.clone() for t in (pool, out, out2, final)]
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=main):
+            work()
+    for _ in range(3):
+        for t in (pool, out, out2, final):
+            t.fill_(7.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip((pool, out, out2, final), want))

@@ -30,18 +30,26 @@ cudaError_t set_attributes_once(std::mutex &mu, uint64_t &done, Set set) {
 // The kernel reads and writes nothing before its grid_dependency_wait, or only what the call's caller may not have
 // pending in the grid directly before it.
 template <typename... P, typename... A>
-cudaError_t launch_dependent(void (*kernel)(P...), unsigned grid, unsigned threads, size_t smem, cudaStream_t stream, const A &...args) {
+cudaError_t launch_dependent_clusters(void (*kernel)(P...), unsigned cluster, unsigned grid, unsigned threads, size_t smem,
+                                      cudaStream_t stream, const A &...args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+template <typename... P, typename... A>
+cudaError_t launch_dependent(void (*kernel)(P...), unsigned grid, unsigned threads, size_t smem, cudaStream_t stream, const A &...args) {
+  return launch_dependent_clusters(kernel, 1, grid, threads, smem, stream, args...);
 }
 
 // Sigmoid-gated RMSNorm of the output rows (gate == nullptr: none).
@@ -351,7 +359,8 @@ struct PagedArgs {
   int64_t out_stride;
   float *lse;                                              // [B T, Hk G], or null
   float *parts;
-  int4 *joins;                                             // one per CTA; null: no item can be cut
+  int4 *joins;                                             // one per CTA (stretches)
+  int cluster;                                             // CTAs of an item's cluster (clusters)
   uint32_t *status;
 };
 // Rows (query heads x new tokens of a key head) that one CTA takes, for `rows` of them.

@@ -12,7 +12,8 @@
 // queries and its end, and one for each tile; a tile is the stretch's that its unit is in.  (Measured: 64 requests of 1
 // to 8192 tokens 61 us without, 55 us with 2 to 6, where stretches of many short requests had come last.)  A stretch that begins or ends inside an item
 // leaves its part (m, l, o) in the workspace; a second kernel, launched as a programmatic dependent, joins an item's
-// parts in the order of its tokens, so results do not depend on timing.
+// parts in the order of its tokens, so results do not depend on timing.  Few short items go to a cluster of CTAs each
+// instead, which join in shared memory.
 //
 // One warp brings tiles through three 32 KB stages (page ids are looked up a tile earlier), four compute on them, and
 // they meet at mbarriers only.  Pages whose size has a power of two of 8 or more in it come by TMA, in boxes of so many
@@ -40,7 +41,8 @@ constexpr uint32_t kHalf = kTile * 128;                // 64 channels of a tile'
 constexpr uint32_t OFF_INFO = kStages * kStageBytes;   // int4 per stage: request, head and row block, tile, length
 constexpr uint32_t OFF_MASK = OFF_INFO + 64;           // uint64 per stage: which tokens of the tile are there
 constexpr uint32_t OFF_ML = OFF_MASK + 32;             // float [4 warps][16 rows][2]
-constexpr uint32_t OFF_SCAN = OFF_ML + 512;
+constexpr uint32_t OFF_CML = OFF_ML + 512;             // float2 [64]: a cluster CTA's rows' maximum and sum of weights
+constexpr uint32_t OFF_SCAN = OFF_CML + 512;
 constexpr uint32_t OFF_BAR = OFF_SCAN + 64;            // landed [3], free [3], readers met, abort flag
 constexpr uint32_t kSmemBytes = OFF_BAR + 64 + 1024;
 static_assert(4 * 16 * kD * 4 <= kStageBytes, "the warps' sums fit one stage");
@@ -64,6 +66,26 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map
 }
 __device__ __forceinline__ void cp16(uint32_t dst, const void *src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// A shared-memory address of this CTA, in the cluster's CTA `rank`
+__device__ __forceinline__ uint32_t peer(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ float2 peer_f2(uint32_t addr) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ float4 peer_f4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
+  return v;
 }
 // The two of a word's bf16 that bits 0 and 1 ask for.
 __device__ __forceinline__ uint32_t pick2(uint32_t bits) {
@@ -95,6 +117,7 @@ struct Cursor {
   int cost;       // units of an item besides its tiles'
   int64_t unit;   // of the tile
 };
+constexpr uint32_t kMostRanks = 8;   // CTAs of a cluster
 constexpr int kItemCost = 4;   // (0 where there is a CTA for every tile)
 constexpr int kLastTile = 1 << 30;   // with the head and row block: the stretch ends here
 
@@ -134,7 +157,9 @@ __device__ __forceinline__ void paged_store_row(const PagedArgs &p, int b, int t
   if (p.lse && lane == 0) p.lse[row * p.Hk * p.G + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
 }
 
-template <int WR>   // row groups of 16; the other 4 / WR warps of a row group split the tile's tokens
+// WR: row groups of 16; the other 4 / WR warps of a row group split the tile's tokens.  kCluster: a cluster an item (no
+// joins), else stretches of the line.
+template <int WR, bool kCluster>
 __global__ void __launch_bounds__(kThreads, 2) paged_attention_kernel(PagedArgs p, const __grid_constant__ PagedMaps maps) {
   constexpr int WT = 4 / WR, kTok = kTile / WT, kNT = kTok / 8;
   constexpr int kRows = 16 * WR;
@@ -168,16 +193,20 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attention_kernel(PagedArgs 
   // ---- this CTA's stretch of the line of tiles
   int64_t *s_scan = reinterpret_cast<int64_t *>(sm + OFF_SCAN);   // [5] warp sums, then the start's request and tile
   int64_t first = 0, last = 0, total = 0;
-  int stretches;   // CTAs with units: every one of them has at least one
+  int stretches = 0;   // CTAs with units: every one of them has at least one
   Cursor cur;
-  if (!p.joins) {   // a CTA an item
-    cur.b = blockIdx.x / ipr;
-    cur.hr = blockIdx.x % ipr;
+  const uint32_t ranks = kCluster ? p.cluster : 1, rank = blockIdx.x % ranks;
+  if constexpr (kCluster) {
+    const int item = blockIdx.x / ranks;
+    cur.b = item / ipr;
+    cur.hr = item % ipr;
     cur.len = request_len(p, cur.b, tid == 0);
     cur.ntiles = tile_count(cur.len);
-    cur.tile = cur.cost = 0;
-    cur.unit = 0;
-    last = cur.ntiles;
+    cur.cost = 0;
+    first = static_cast<int64_t>(cur.ntiles) * rank / ranks;
+    last = static_cast<int64_t>(cur.ntiles) * (rank + 1) / ranks;
+    cur.unit = first;
+    cur.tile = static_cast<int>(first);
     __syncthreads();
   } else {
     const int per = (p.B + kThreads - 1) / kThreads;
@@ -223,7 +252,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attention_kernel(PagedArgs 
     __syncthreads();
   }
   bool none = first >= last;
-  if (!none && p.joins) {
+  if (!kCluster && !none) {
     cur.b = static_cast<int>(s_scan[6]);
     cur.len = request_len(p, cur.b);
     cur.ntiles = tile_count(cur.len);
@@ -235,7 +264,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attention_kernel(PagedArgs 
     none = cur.unit >= last;   // (a stretch of an item's first units alone)
   }
   // an item that an earlier CTA began: the CTA at the first cut inside it describes the join
-  if (tid == 0 && p.joins) {
+  if (!kCluster && tid == 0) {
     int4 j = make_int4(0, 0, 0, 0);
     if (!none && cur.tile > 0) {
       const int64_t begin = cur.unit - cur.tile, end = begin + cur.ntiles;   // the units of the item's tiles
@@ -247,7 +276,48 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attention_kernel(PagedArgs 
     }
     p.joins[blockIdx.x] = j;
   }
-  if (none) return;
+  // A cluster's end: its CTAs' rows (channels in stage 0, maximum and weights beside) are joined in the order of their
+  // tokens, each CTA taking every ranks-th row.  All threads of the cluster come here.
+  const uint32_t c_rows = smem, c_ml = smem + OFF_CML;
+  const auto finish = [&] {
+    if (!kCluster || ranks == 1) return;
+    if (none && tid < kRows) *reinterpret_cast<float2 *>(sm + OFF_CML + 8 * tid) = make_float2(-INFINITY, 0.f);
+    cluster_sync();
+    if (warp < kComputeWarps) {
+      const int rb = cur.hr % p.row_blocks, h = cur.hr / p.row_blocks;
+      for (int r = rank + ranks * warp; r < kRows; r += ranks * kComputeWarps) {
+        const int row = rb * kRows + r, t = row / p.G;
+        if (t >= p.T) break;
+        float2 ml[kMostRanks];
+        float4 x[kMostRanks];
+        float mm = -INFINITY, ll = 0.f;
+#pragma unroll
+        for (uint32_t q = 0; q < kMostRanks; ++q) {
+          ml[q] = make_float2(-INFINITY, 0.f);
+          if (q < ranks) {
+            ml[q] = peer_f2(peer(c_ml + 8 * r, q));
+            x[q] = peer_f4(peer(c_rows + (r * kD + lane * 4) * 4, q));
+          }
+          mm = fmaxf(mm, ml[q].x);
+        }
+        const float bs = mm == -INFINITY ? 0.f : mm;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (uint32_t q = 0; q < kMostRanks; ++q)
+          if (ml[q].x != -INFINITY) {   // (a CTA without tokens has written no channels)
+            const float c = fast_exp2(ml[q].x - bs);
+            ll += c * ml[q].y;
+            acc.x += c * x[q].x; acc.y += c * x[q].y; acc.z += c * x[q].z; acc.w += c * x[q].w;
+          }
+        paged_store_row(p, cur.b, t, h * p.G + row % p.G, lane, acc, mm, ll);
+      }
+    }
+    cluster_sync();   // (a CTA's shared memory stays while others read it)
+  };
+  if (none) {
+    finish();
+    return;
+  }
 
   if (warp == kComputeWarps) {
     // ---------------------------------------------------------------- loads
@@ -343,6 +413,8 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attention_kernel(PagedArgs 
         sm100::mbar_wait(&landed[i], 0);
         sm100::mbar_wait(&landed[i], 1);
       }
+    __syncwarp();
+    finish();
     return;
   }
 
@@ -539,7 +611,8 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attention_kernel(PagedArgs 
       l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
       l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
       meet();   // tile i has been read: its stage takes the sums
-      float *so = reinterpret_cast<float *>(sm + st * kStageBytes);
+      // (a cluster's CTA ends here: no stage is in use any more)
+      float *so = reinterpret_cast<float *>(sm + (ranks > 1 ? 1 : st) * kStageBytes);
 #pragma unroll
       for (int n = 0; n < 16; ++n) {
         const int c = (n * 8 + t4 * 2) ^ (g << 3);
@@ -573,7 +646,10 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attention_kernel(PagedArgs 
           ll += c * s_ml[wi * 2 + 1];
           acc.x += c * x.x; acc.y += c * x.y; acc.z += c * x.z; acc.w += c * x.w;
         }
-        if (whole) {
+        if (ranks > 1) {
+          *reinterpret_cast<float4 *>(sm + (r * kD + lane * 4) * 4) = acc;
+          if (lane == 0) *reinterpret_cast<float2 *>(sm + OFF_CML + 8 * r) = make_float2(mm, ll);
+        } else if (whole) {
           paged_store_row(p, cur.b, t, h * p.G + row % p.G, lane, acc, mm, ll);
         } else {
           float *part = p.parts + (static_cast<size_t>(slot) * kRows + r) * kPagedPartFloats;
@@ -588,6 +664,8 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attention_kernel(PagedArgs 
     if (lane == 0) sm100::mbar_arrive(&freed[st]);
     if (stretch_ends) break;
   }
+  __syncwarp();
+  finish();
 }
 
 // Joins the parts of the items that the stretches cut.  Every CTA lists the joins (few places hold one) and takes rows of
@@ -685,8 +763,10 @@ __global__ void __launch_bounds__(kJoinThreads, 2) paged_join_kernel(PagedArgs p
   }
 }
 
-// Measured (16 query, 2 key heads; cut against whole): one request of 128 tokens 8.6 and 5.9 us, of 257 8.7 and 10.0; 16
-// of 128 9.7 and 6.2 us, of 257 10.4 and 10.4; 120 of 128 11.9 and 7.0 us.  (A CTA alone takes 1.0 to 1.3 us a tile.)
+// Tiles for each CTA of a cluster, at most.  Measured (16 query, 2 key heads, requests of one length; cut against clusters):
+// one request of 257 tokens 8.9 and 6.3 us, of 2048 11.5 and 9.9, of 4096 (8 tiles a CTA) 15.6 and 15.0; 16 of 2048 (4
+// tiles) 14.5 and 11.4; 120 of 257 (5 tiles) 16.1 and 11.8, of 4096 (64 tiles) 85 and 91.  A CTA takes 1.3 us a tile, and
+// where one request is much longer than the others only stretches share it out, hence not more.
 constexpr int kWholeTiles = 4;
 // Boxes of fewer rows are not worth a TMA copy each (four a box).  Measured over 64 x 8192 tokens, 2 key heads: boxes of 8
 // 115 us against 132 us by asynchronous copies, of 4 171 us against 132 (of 16 and more 93 us).
@@ -713,7 +793,10 @@ cudaError_t launch_paged(PagedArgs a, cudaStream_t stream) {
   static std::mutex mu;
   static uint64_t done = 0;
   if (const cudaError_t e = set_attributes_once(mu, done, [] {
-        return cudaFuncSetAttribute(paged_attention_kernel<WR>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+        cudaError_t r = cudaFuncSetAttribute(paged_attention_kernel<WR, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+        if (r == cudaSuccess)
+          r = cudaFuncSetAttribute(paged_attention_kernel<WR, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+        return r;
       }))
     return e;
   int dev = 0, sms = 0;
@@ -723,18 +806,24 @@ cudaError_t launch_paged(PagedArgs a, cudaStream_t stream) {
   const int64_t items = static_cast<int64_t>(a.B) * a.Hk * a.row_blocks;
   const int64_t most = items * std::max<int64_t>(1, (a.max_len + kTile - 1) / kTile);   // tiles there can be
   const int64_t ctas = std::min(2 * sms, kPagedMaxCtas);
-  // Nothing is cut where items are short and all of them run at once: the scan and the join cost more than the tiles.
-  const bool whole = items <= ctas && most <= items * kWholeTiles;
-  if (whole) a.joins = nullptr;
-  const unsigned grid = static_cast<unsigned>(whole ? items : std::min(most, ctas));
+  // Items that all run at once and are short go to a cluster each, whose CTAs join through shared memory: the scan and the
+  // join kernel cost more than the tiles.
+  int ranks = kMostRanks;
+  while (ranks > 1 && items * ranks > ctas) ranks >>= 1;
+  const bool whole = items * ranks <= ctas && most <= items * ranks * kWholeTiles;
+  while (ranks > 1 && most <= items * (ranks >> 1)) ranks >>= 1;   // no more of them than tiles
+  a.cluster = ranks;
+  const unsigned grid = static_cast<unsigned>(whole ? items * ranks : std::min(most, ctas));
   PagedMaps maps;
   maps.box = 1;
   while (maps.box < kTile && a.page % (2 * maps.box) == 0) maps.box *= 2;
   if (maps.box < kLeastBox || !make_page_map(&maps.k, a.k, a.k_page_stride, a.k_token_stride, a.k_head_stride, a, maps.box) ||
       !make_page_map(&maps.v, a.v, a.v_page_stride, a.v_token_stride, a.v_head_stride, a, maps.box))
     maps.box = 0;
-  const cudaError_t e = launch_dependent(paged_attention_kernel<WR>, grid, kThreads, kSmemBytes, stream, a, maps);
-  if (e != cudaSuccess || !a.joins) return e;
+  if (whole)
+    return launch_dependent_clusters(paged_attention_kernel<WR, true>, a.cluster, grid, kThreads, kSmemBytes, stream, a, maps);
+  const cudaError_t e = launch_dependent(paged_attention_kernel<WR, false>, grid, kThreads, kSmemBytes, stream, a, maps);
+  if (e != cudaSuccess) return e;
   return launch_dependent(paged_join_kernel, std::min(grid * 16 * WR, static_cast<unsigned>(kJoinCtas)), kJoinThreads, 0, stream, a,
                           16 * WR, static_cast<int>(grid));
 }

@@ -67,6 +67,22 @@ def test_paged(lens, T, hq, hk, page):
     check(*make(lens, T, hq, hk, page, seed=len(lens) + T), T)
 
 
+@pytest.mark.parametrize("lens,T,hq,hk,page", [
+    ([1], 1, 16, 2, 16), ([0, 1, 64, 65], 1, 8, 2, 16), ([257], 1, 16, 2, 16), ([129, 2000], 1, 16, 2, 64),
+    ([500, 3, 0, 1000, 64], 4, 8, 1, 16), ([1500], 8, 32, 4, 24), ([700, 20], 16, 8, 2, 5), ([130] * 40, 1, 16, 2, 16),
+    ([90] * 160, 1, 8, 1, 64), ([2000, 1900], 2, 48, 2, 16), ([1, 2, 3], 3, 4, 4, 1)])
+def test_clusters_and_stretches(lens, T, hq, hk, page):
+    # a narrow table's items go to a cluster each, a wide one's (with no more tokens) are cut
+    q, k, v, table, lens_d = make(lens, T, hq, hk, page, seed=len(lens) + 10 * T)
+    out, lse = check(q, k, v, table, lens_d, T)
+    wide = torch.full((len(lens), table.shape[1] + 40000 // page), -7, dtype=torch.int32, device="cuda")
+    wide[:, :table.shape[1]] = table
+    out2, lse2 = check(q, k, v, wide, lens_d, T)
+    assert rel_l2(out2, out.cpu()) <= 2 * OUT_TOL or not out.any()
+    # and the same bits again
+    assert torch.equal(check(q, k, v, table, lens_d, T)[0], out) and torch.equal(check(q, k, v, wide, lens_d, T)[0], out2)
+
+
 def test_more_requests_than_threads():
     g = torch.Generator().manual_seed(3)
     lens = torch.randint(0, 90, (700,), generator=g).tolist()
@@ -115,9 +131,10 @@ def test_strides_and_interleaved_cache():
     assert (dst[:, 8 * D:] == 4.0).all()
 
 
-def test_what_is_not_seen_does_not_matter():
+@pytest.mark.parametrize("width", [None, 4000])
+def test_what_is_not_seen_does_not_matter(width):
     # NaN and infinities in other pages, behind the last token of the last page, and in later new tokens
-    q, k, v, table, lens = make([70, 131], 3, 8, 2, 16, seed=10)
+    q, k, v, table, lens = make([70, 131], 3, 8, 2, 16, seed=10, width=width)
     clean = check(q, k, v, table, lens, 3)[0].clone()
     used = torch.zeros((k.shape[0], 16), dtype=torch.bool)
     for b, n in enumerate([70, 131]):
@@ -163,8 +180,9 @@ def test_strides_of_one_head_or_page_do_not_matter(hk, page, pages):
     assert torch.equal(check(q, k0, v0, table, lens, 1)[0], out)
 
 
-def test_bad_pages_and_lengths_are_left_out():
-    q, k, v, table, lens = make([100, 200, 50], 1, 8, 2, 16, seed=11)
+@pytest.mark.parametrize("width", [None, 4000])
+def test_bad_pages_and_lengths_are_left_out(width):
+    q, k, v, table, lens = make([100, 200, 50], 1, 8, 2, 16, seed=11, width=width)
     table[1, 4], table[1, 7] = k.shape[0], -1
     lens[2] = 16 * table.shape[1] + 1
     ws = kda.make_workspace(nbytes=kda.paged_workspace_size(8, 2, 1))

@@ -51,19 +51,26 @@ constexpr int kGdnMaxSeqs = 1024;   // sequences per launch (longer batches are 
 // segments of seg chunks.  Within a segment the state is affine in the state S that enters it, S_end = F S + B, and F and
 // B are states of the same pass: F is what becomes of the identity without values, B of a zero state with them.  One
 // grid runs first segments (as usual: their state is known) and F and B of the inner ones, a small kernel forms
-// S_(j+1) = F_j S_j + B_j in fp32, and a second grid runs the segments behind the first from those states.
-// A segment job: sequence | segment | F | first of the sequence's matrices among the launch's.  A sequence of m segments
-// has 2 m - 3 matrices: the states entering segments 1 .. m - 1, then F of segments 1 .. m - 2.
+// S_(j+1) = F_j S_j + B_j in fp32, and a second grid runs the segments behind the first from those states.  Where it
+// pays, F and B are also kept half way: the second grid then runs inner segments as halves, from S_j and the half-way
+// state that the same kernel forms from it, and the last segment is about half as long.
 constexpr int kGdnMaxJobs = 256, kGdnMaxSegs = 16;   // jobs per grid, segments per sequence
-constexpr int kGdnMaxMats = 304;                     // matrices times heads (64 KB each)
+constexpr int kGdnMaxMats = 400;                     // matrices times heads (64 KB each)
 // Chunks of the shortest segment, and what cutting costs (two more grids, their states) in chunks' time.  Measured, whole
 // against cut, 16 heads: one sequence of 768 tokens 41 against 44 us, of 1024 53 against 51, 2048 95 against 70, 16384 686
-// against 297; two of 1024 56 against 63, two of 2048 103 against 96.
-constexpr int kSegmentMin = 4, kSegmentExtra = 7;
+// against 297; two of 1024 56 against 63, two of 2048 103 against 96.  Half-way states cost another kernel (14 us with
+// 4 segments of 16 heads): 4096 tokens 101 us without against 111 with them, 16384 297 against 286, 16384 x 32 heads 545 against 516.
+constexpr int kSegmentMin = 4, kSegmentExtra = 7, kHalvesExtra = 8;
+// A piece of a sequence's state pass.  Matrices are numbered per launch; those of a sequence with k inner segments are S_1 ..
+// S_(k+1), F_1 .. F_k, and half way B (then the state) and F of each.
 struct GdnJob {
-  uint16_t seq, mat;
-  uint8_t seg, segs, map, pad;   // map: this job is F
+  uint16_t seq;
+  int16_t src;         // entering state: a matrix, or one of the below
+  int16_t dst;         // end: a matrix, or one of the below
+  int16_t mid;         // half way, before chunk mid_chunk: a matrix, or none
+  int32_t chunk0, chunks, mid_chunk;
 };
+enum { kFromCaller = -1, kFromZero = -2, kFromIdentity = -3, kToCaller = -1, kToNothing = -2 };
 
 struct GdnPrefillParams {
   CUtensorMap tq, tk, tv, tout; // [tokens, H, 128] bf16, box 64 channels x 1 head x 64 tokens, 128-byte swizzle
@@ -84,7 +91,7 @@ struct GdnPrefillParams {
   int32_t cu[kGdnMaxSeqs + 1];  // first token of each sequence of the launch, and the end of the last
   uint16_t order[kGdnMaxSeqs];  // sequences, longest first
   // segments
-  int first_pass, seg_chunks;
+  int behind;                   // the entering states come from the grid before
   float *mats;                  // matrix m of head h at mats + (m Hv + h) 128 128
   GdnJob job[kGdnMaxJobs];
 };
@@ -560,17 +567,16 @@ __global__ void __launch_bounds__(ch::kThreads, 1) gdn_chain_kernel(const __grid
   GdnJob job = {};
   if (SEGMENTS) job = prm.job[blockIdx.x / prm.Hv];
   const int n = SEGMENTS ? job.seq : prm.order[blockIdx.x / prm.Hv];
-  const bool map = SEGMENTS && job.map;
+  const bool map = SEGMENTS && job.src == kFromIdentity;   // (F: no values)
   int t0 = prm.cu[n], len = prm.cu[n + 1] - t0, chunk0 = 0;
-  if (SEGMENTS && job.segs > 1) {
-    chunk0 = job.seg * prm.seg_chunks;
+  if (SEGMENTS) {
+    chunk0 = job.chunk0;
     t0 += chunk0 * kC;
-    len -= chunk0 * kC;
-    if (job.seg + 1 < job.segs) len = min(len, prm.seg_chunks * kC);
+    len = min(len - chunk0 * kC, job.chunks * kC);
   }
   const int nchunks = (len + kC - 1) / kC;
   // a segment whose entering state is known has outputs; the others' F and B do not
-  const bool known = !SEGMENTS || !prm.first_pass || job.seg == 0;
+  const bool known = !SEGMENTS || job.src >= kFromCaller;
   int pool_slot = 0;
   if (prm.slot_ids) {
     pool_slot = prm.slot_ids[n];
@@ -586,17 +592,14 @@ __global__ void __launch_bounds__(ch::kThreads, 1) gdn_chain_kernel(const __grid
   const float *src = prm.state_in ? prm.state_in + pool_at : nullptr;
   float *dst = prm.state_out_pool ? prm.state_out_pool + pool_at
                                   : prm.state_out_dense + (static_cast<size_t>(n) * prm.Hv + h) * kD * kD;
-  if (SEGMENTS && job.segs > 1) {
-    const auto mat = [&](int m) { return prm.mats + (static_cast<size_t>(job.mat + m) * prm.Hv + h) * kD * kD; };
-    if (job.seg > 0) src = known ? mat(job.seg - 1) : nullptr;
-    if (map)
-      dst = mat(job.segs - 1 + job.seg - 1);
-    else if (job.seg + 1 < job.segs && prm.first_pass)
-      dst = mat(job.seg);
-    else if (job.seg + 1 < job.segs)
-      dst = nullptr;   // (the next segment's state is there already)
+  float *mid = nullptr;
+  if (SEGMENTS) {
+    const auto mat = [&](int m) { return prm.mats + (static_cast<size_t>(m) * prm.Hv + h) * kD * kD; };
+    if (job.src != kFromCaller) src = job.src >= 0 ? mat(job.src) : nullptr;
+    if (job.dst != kToCaller) dst = job.dst >= 0 ? mat(job.dst) : nullptr;
+    if (job.mid >= 0) mid = mat(job.mid);
   }
-  if (SEGMENTS && !prm.first_pass) grid_dependency_wait();   // the entering states
+  if (SEGMENTS && prm.behind) grid_dependency_wait();
   // epilogue thread: value channel d (TMEM lane), key channels 32 cg .. + 31 of the state, tokens 16 cg .. + 15 of a chunk
   const bool worker = warp < kIssuer;
   const int quad = warp & 3, cg = warp >> 2, d = 32 * quad + lane;
@@ -1032,6 +1035,11 @@ __global__ void __launch_bounds__(ch::kThreads, 1) gdn_chain_kernel(const __grid
             for (int i = 0; i < 32; ++i) S[i] *= ratio;
           }
           if (c + 1 < nchunks) store_s(c + 1);
+          if (SEGMENTS && mid && c + 1 == job.mid_chunk && c + 1 < nchunks) {
+            const float inv = s_inv[128 * ((c + 1) & 1) + d];
+#pragma unroll
+            for (int e = 0; e < 32; ++e) mid[(32 * cg + e) * kD + d] = S[e] * inv;
+          }
         }
         warp_arrive(&bar[B_FREE]);   // the last read of the stage is behind
       }
@@ -1053,8 +1061,8 @@ __global__ void __launch_bounds__(ch::kThreads, 1) gdn_chain_kernel(const __grid
   }
 }
 
-// The states entering a sequence's segments, S_(j+1) = F_j S_j + B_j (B_j is where S_(j+1) goes), in fp32: a CTA per
-// sequence, head and 16 value channels, a warp per 16 key channels.  A lane holds four columns of F's rows, which a warp
+// Entering states, S' = F S + B (S' goes where B is), in fp32, a sequence's (`chunks` of them) one behind the other from S
+// (matrix src; F: mid .., B: dst ..), or alone: a CTA per job, head and 16 value channels, a warp per 16 key channels.  A lane holds four columns of F's rows, which a warp
 // reads as whole rows, and the four rows of S that they meet; the lanes' sums meet in a halving exchange, at whose end
 // each lane holds one.  Bound by the latency of its few steps; the next F and B are on their way during a step.
 constexpr int kJoinParts = 8, kJoinStride = 68;
@@ -1062,7 +1070,7 @@ __global__ void __launch_bounds__(256, 1) gdn_join_kernel(const __grid_constant_
   __shared__ __align__(16) float s_state[2][32 * kJoinStride];   // rows 4 l .. + 3 at kJoinStride l
   const int part = blockIdx.x % kJoinParts, h = blockIdx.x / kJoinParts % prm.Hv, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const GdnJob job = prm.job[blockIdx.x / kJoinParts / prm.Hv];
-  const auto mat = [&](int m) { return prm.mats + (static_cast<size_t>(job.mat + m) * prm.Hv + h) * kD * kD; };
+  const auto mat = [&](int m) { return prm.mats + (static_cast<size_t>(m) * prm.Hv + h) * kD * kD; };
   // this lane's entry of rows 2 i, 2 i + 1 of the warp's: row 2 i + lane / 16, value channel lane % 16
   const size_t at = static_cast<size_t>(16 * warp + (lane >> 4)) * kD + 16 * part + (lane & 15);
   const auto put = [&](int buf, int i, float y) {
@@ -1072,23 +1080,23 @@ __global__ void __launch_bounds__(256, 1) gdn_join_kernel(const __grid_constant_
   float4 f[16];
   float b[8];
   const auto fetch = [&](int j) {
-    const float4 *src = reinterpret_cast<const float4 *>(mat(job.segs + j - 2) + static_cast<size_t>(16 * warp) * kD);
+    const float4 *src = reinterpret_cast<const float4 *>(mat(job.mid + j) + static_cast<size_t>(16 * warp) * kD);
 #pragma unroll
     for (int i = 0; i < 16; ++i) f[i] = src[32 * i + lane];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) b[i] = mat(j)[at + 2 * i * kD];
+    for (int i = 0; i < 8; ++i) b[i] = mat(job.dst + j)[at + 2 * i * kD];
   };
   grid_dependency_wait();
-  fetch(1);
+  fetch(0);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) put(0, i, mat(0)[at + 2 * i * kD]);
+  for (int i = 0; i < 8; ++i) put(0, i, mat(job.src)[at + 2 * i * kD]);
   __syncthreads();
-  for (int j = 1; j + 1 < job.segs; ++j) {
+  for (int j = 0; j < job.chunks; ++j) {
     float st[4][16];
 #pragma unroll
     for (int x = 0; x < 16; ++x)
       *reinterpret_cast<float4 *>(&st[x >> 2][4 * (x & 3)]) =
-          *reinterpret_cast<const float4 *>(&s_state[(j - 1) & 1][kJoinStride * lane + 4 * x]);
+          *reinterpret_cast<const float4 *>(&s_state[j & 1][kJoinStride * lane + 4 * x]);
     float y[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -1110,11 +1118,11 @@ __global__ void __launch_bounds__(256, 1) gdn_join_kernel(const __grid_constant_
       }
       y[i] = v[0] + b[i];
     }
-    if (j + 2 < job.segs) fetch(j + 1);
+    if (j + 1 < job.chunks) fetch(j + 1);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      put(j & 1, i, y[i]);
-      mat(j)[at + 2 * i * kD] = y[i];
+      put((j + 1) & 1, i, y[i]);
+      mat(job.dst + j)[at + 2 * i * kD] = y[i];
     }
     __syncthreads();
   }
@@ -1122,95 +1130,125 @@ __global__ void __launch_bounds__(256, 1) gdn_join_kernel(const __grid_constant_
 
 int chunks_of(const GdnPrefillParams &p, int n) { return (p.cu[n + 1] - p.cu[n] + kC - 1) / kC; }
 
-// Chunks per segment, or 0 to leave the sequences whole: the estimates of both in chunks' time.  A grid of at most one
-// CTA per SM takes its longest; others are bounded (from below for whole sequences, from above for segments).
-int segment_chunks(const GdnPrefillParams &p, int max_mats) {
+// Segments of a sequence: a first one of g chunks, inner ones of as many, and a last one of 1 to g.
+struct Cut {
+  int g = 0, halves = 1;   // chunks of a segment (0: sequences stay whole), pieces of an inner one in the second grid
+  bool whole(int chunks) const { return chunks <= g; }
+  int half() const { return (g + 1) / 2; }
+  int inner(int chunks) const { return (chunks + g - 1) / g - 2; }
+  int last(int chunks) const { return chunks - (inner(chunks) + 1) * g; }
+  int matrices(int chunks) const { return 1 + (halves == 2 ? 4 : 2) * inner(chunks); }
+};
+
+// How to cut, by estimates in chunks' time.  A grid of at most one CTA per SM takes its longest piece; others are bounded
+// (from below for whole sequences, from above for segments).
+Cut choose_cut(const GdnPrefillParams &p, int max_mats) {
   const int longest = chunks_of(p, p.order[0]);
   int64_t sum = 0;
-  if (longest < kSegmentExtra + 2 * kSegmentMin) return 0;
+  Cut best_cut;
+  if (longest < kSegmentExtra + 2 * kSegmentMin) return best_cut;
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
       sms <= 0)
     sms = 152;
   for (int n = 0; n < p.num_seqs; ++n) sum += chunks_of(p, n);
   int64_t best = std::max<int64_t>(longest, sum * p.Hv / sms);
-  int seg = 0, tried = 0;
-  for (int m = 2; m <= kGdnMaxSegs; ++m) {
-    const int g = (longest + m - 1) / m;
-    if (g < kSegmentMin) break;
-    if (g == tried) continue;
-    tried = g;
-    int64_t jobs1 = 0, jobs2 = 0, work1 = 0, mats = 0, work2 = 0;
-    for (int n = 0; n < p.num_seqs; ++n) {
-      const int chunks = chunks_of(p, n), segs = (chunks + g - 1) / g;
-      if (segs <= 1) {
-        jobs1 += 1;
-        work1 += chunks;
-        continue;
+  for (int m = 2; m <= kGdnMaxSegs; ++m)
+    for (int halves = 1; halves <= 2; ++halves) {
+      Cut cut;
+      cut.halves = halves;
+      cut.g = halves == 1 ? (longest + m - 1) / m : (2 * longest + 2 * m - 2) / (2 * m - 1);
+      if (cut.g < kSegmentMin * halves) continue;
+      int64_t jobs1 = 0, jobs2 = 0, work1 = 0, work2 = 0, mats = 0;
+      int piece = 0;
+      for (int n = 0; n < p.num_seqs; ++n) {
+        const int chunks = chunks_of(p, n);
+        if (cut.whole(chunks)) {
+          jobs1 += 1;
+          work1 += chunks;
+          continue;
+        }
+        const int k = cut.inner(chunks);
+        jobs1 += 1 + 2 * k;
+        work1 += static_cast<int64_t>(1 + 2 * k) * cut.g;
+        jobs2 += 1 + k * halves;
+        work2 += chunks - cut.g;
+        mats += cut.matrices(chunks);
+        piece = std::max({piece, cut.last(chunks), k == 0 ? 0 : halves == 2 ? cut.half() : cut.g});
       }
-      jobs1 += 2 * segs - 3;
-      work1 += static_cast<int64_t>(2 * segs - 3) * g;
-      jobs2 += segs - 1;
-      work2 += chunks - g;
-      mats += 2 * segs - 3;
+      if (jobs1 > kGdnMaxJobs || jobs2 > kGdnMaxJobs || mats * p.Hv > max_mats) continue;
+      const int64_t est = (jobs1 * p.Hv <= sms ? cut.g : work1 * p.Hv / sms + cut.g) +
+                          (jobs2 * p.Hv <= sms ? piece : work2 * p.Hv / sms + piece) + kSegmentExtra + (halves == 2 ? kHalvesExtra : 0);
+      if (est < best) {
+        best = est;
+        best_cut = cut;
+      }
     }
-    if (jobs1 > kGdnMaxJobs || mats * p.Hv > max_mats) break;
-    const int64_t est = (jobs1 * p.Hv <= sms ? g : work1 * p.Hv / sms + g) + (jobs2 * p.Hv <= sms ? g : work2 * p.Hv / sms + g) +
-                        kSegmentExtra;
-    if (est < best) {
-      best = est;
-      seg = g;
-    }
-  }
-  return seg;
+  return best_cut;
 }
 
-cudaError_t launch_segments(GdnPrefillParams &p, int g, float *mats, cudaStream_t stream) {
-  p.seg_chunks = g;
+cudaError_t launch_segments(GdnPrefillParams &p, const Cut &cut, float *mats, cudaStream_t stream) {
+  const int g = cut.g, half = cut.half();
   p.mats = mats;
-  // first segments, then the inner ones, then the sequences that stay whole (sequences come longest first, so those with
-  // inner segments are ahead of the others)
-  int jobs = 0, mat = 0, joined = 0;
-  const auto segments = [&](int i) { return std::max(1, (chunks_of(p, p.order[i]) + g - 1) / g); };
-  const auto add = [&](int i, int seg, bool map) {
-    const int segs = segments(i);
-    p.job[jobs++] = {p.order[i], static_cast<uint16_t>(mat), static_cast<uint8_t>(seg), static_cast<uint8_t>(segs),
-                     static_cast<uint8_t>(map), 0};
-    return 2 * segs - 3;
+  int jobs = 0;
+  const auto add = [&](int i, int src, int dst, int chunk0, int chunks, int mid = -1) {
+    p.job[jobs++] = {p.order[i], static_cast<int16_t>(src), static_cast<int16_t>(dst), static_cast<int16_t>(mid), chunk0, chunks, half};
   };
-  for (int i = 0; i < p.num_seqs && segments(i) > 1; ++i) {
-    joined += segments(i) > 2;
-    mat += add(i, 0, false);
-  }
-  mat = 0;
-  for (int i = 0; i < joined; ++i) {
-    for (int s = 1; s + 1 < segments(i); ++s) {
-      add(i, s, false);
-      add(i, s, true);
+  // every sequence that is cut (they come longest first), with its inner segments and its first matrix
+  const auto each = [&](auto body) {
+    int base = 0;
+    for (int i = 0; i < p.num_seqs && !cut.whole(chunks_of(p, p.order[i])); ++i) {
+      const int chunks = chunks_of(p, p.order[i]), k = cut.inner(chunks);
+      body(i, chunks, k, base, base + k + 1 /* F */, base + 2 * k + 1 /* half way: B, S */, base + 3 * k + 1 /* F */);
+      base += cut.matrices(chunks);
     }
-    mat += 2 * segments(i) - 3;
+  };
+  const auto run = [&](auto kernel, int per_head, int threads, size_t smem) {
+    const int n = jobs;
+    jobs = 0;
+    return n ? launch_dependent(kernel, n * p.Hv * per_head, threads, smem, stream, p) : cudaSuccess;
+  };
+  // first segments, F and B of the inner ones, then the sequences that stay whole
+  each([&](int i, int, int, int base, int, int, int) { add(i, kFromCaller, base, 0, g); });
+  each([&](int i, int, int k, int base, int f, int mb, int mf) {
+    for (int j = 0; j < k; ++j) {
+      add(i, kFromZero, base + 1 + j, (1 + j) * g, g, cut.halves == 2 ? mb + j : -1);
+      add(i, kFromIdentity, f + j, (1 + j) * g, g, cut.halves == 2 ? mf + j : -1);
+    }
+  });
+  for (int i = 0; i < p.num_seqs; ++i) {
+    const int chunks = chunks_of(p, p.order[i]);
+    if (cut.whole(chunks)) add(i, kFromCaller, kToCaller, 0, chunks);
   }
-  mat = 0;
-  for (int i = 0; i < p.num_seqs; ++i)
-    if (segments(i) == 1) add(i, 0, false);
-  p.first_pass = 1;
-  cudaError_t e = launch_dependent(gdn_chain_kernel<true>, jobs * p.Hv, ch::kThreads, ch::kSmemBytes, stream, p);
-  if (e == cudaSuccess && joined) e = launch_dependent(gdn_join_kernel, joined * p.Hv * kJoinParts, 256, 0, stream, p);
-  if (e != cudaSuccess) return e;
-  jobs = mat = 0;
-  for (int i = 0; i < p.num_seqs && segments(i) > 1; ++i) {
-    for (int s = 1; s < segments(i); ++s) add(i, s, false);
-    mat += 2 * segments(i) - 3;
+  p.behind = 0;
+  if (const cudaError_t e = run(gdn_chain_kernel<true>, 1, ch::kThreads, ch::kSmemBytes)) return e;
+  // entering states, then the half-way ones from them
+  each([&](int i, int, int k, int base, int f, int, int) {
+    if (k) add(i, base, base + 1, 0, k, f);
+  });
+  if (const cudaError_t e = run(gdn_join_kernel, kJoinParts, 256, 0)) return e;
+  if (cut.halves == 2) {
+    each([&](int i, int, int k, int base, int, int mb, int mf) {
+      for (int j = 0; j < k; ++j) add(i, base + j, mb + j, 0, 1, mf + j);
+    });
+    if (const cudaError_t e = run(gdn_join_kernel, kJoinParts, 256, 0)) return e;
   }
-  p.first_pass = 0;
-  return launch_dependent(gdn_chain_kernel<true>, jobs * p.Hv, ch::kThreads, ch::kSmemBytes, stream, p);
+  each([&](int i, int chunks, int k, int base, int, int mb, int) {
+    add(i, base + k, kToCaller, (1 + k) * g, chunks - (1 + k) * g);
+    for (int j = 0; j < k; ++j) {
+      add(i, base + j, kToNothing, (1 + j) * g, cut.halves == 2 ? half : g);
+      if (cut.halves == 2) add(i, mb + j, kToNothing, (1 + j) * g + half, g - half);
+    }
+  });
+  p.behind = 1;
+  return run(gdn_chain_kernel<true>, 1, ch::kThreads, ch::kSmemBytes);
 }
 
 }  // namespace
 
 namespace {
-// matrices (times heads) that a batch of so many tokens has room for: a segment has kSegmentMin chunks or more, and a
-// sequence of m segments 2 m - 3 matrices; none where no sequence can be long enough
+// matrices (times heads) that a batch of so many tokens has room for: a segment has kSegmentMin chunks or more, in halves
+// twice as many, and 2 matrices, in halves 4; none where no sequence can be long enough
 int64_t matrix_room(int64_t total_tokens, int Hv) {
   const int64_t chunks = total_tokens / kC + 1;
   if (chunks < kSegmentExtra + 2 * kSegmentMin) return 0;
@@ -1270,8 +1308,8 @@ cudaError_t launch_gdn_prefill(const GdnRecurrentArgs &a, const int32_t *cu_host
     if (const cudaError_t e = launch_dependent(gdn_intra_kernel, static_cast<unsigned>(slots) * Hk, in::kThreads, in::kSmemBytes,
                                                stream, p))
       return e;
-    const int seg = segment_chunks(p, room);
-    if (const cudaError_t e = seg ? launch_segments(p, seg, mats, stream) : launch_dependent(gdn_chain_kernel<false>, ns * a.Hv, ch::kThreads, ch::kSmemBytes, stream, p)) return e;
+    const Cut cut = choose_cut(p, room);
+    if (const cudaError_t e = cut.g ? launch_segments(p, cut, mats, stream) : launch_dependent(gdn_chain_kernel<false>, ns * a.Hv, ch::kThreads, ch::kSmemBytes, stream, p)) return e;
   }
   return cudaSuccess;
 }

@@ -85,6 +85,26 @@ def test_prefill_long_sequences(lens, hk, hv, a_mean):
     assert torch.equal(out, out2) and torch.equal(pool[slots.long()], final) and torch.equal(pool[0], before[0])
 
 
+@pytest.mark.parametrize("lens,hk,hv", [([13000], 8, 16), ([13000, 130], 5, 15), ([12800], 19, 38)])
+def test_prefill_cut_against_pieces(lens, hk, hv):
+    # long enough for half-way states; the same tokens in calls too short to be cut, the state handed on.  Either is
+    # within the tolerances of the definition (the pieces' calls are compared with it above), so both together are within twice
+    x = gdn_inputs(sum(lens), hk, hv, seed=61, a_mean=-7.0)
+    pool = _pool(len(lens) + 1, hv, 62)
+    slots = _i32(list(range(1, len(lens) + 1)))
+    out, final = _prefill(x, lens, state_pool=pool, slot_ids=slots, load_initial=True)
+    at = 0
+    for n, length in enumerate(lens):
+        for t in range(0, length, 900):
+            some = slice(at + t, at + min(t + 900, length))
+            part = [y[some] if y.shape[0] == sum(lens) else y for y in x]
+            o, _ = _prefill(part, [part[0].shape[0]], state_pool=pool, slot_ids=slots[n:n + 1], load_initial=True, final_to_pool=True)
+            assert rel_l2(out[some], o.cpu()) <= 2 * 3 * OUT_STEP
+        at += length
+        for h in range(hv):
+            assert rel_l2(final[n, h], pool[n + 1, h].cpu()) <= 2 * STATE_CHUNKED, (n, h)
+
+
 def test_prefill_long_sequence_keeps_channels_apart():
     # a NaN among one value channel's values of an early segment reaches that channel alone, from its 64-token chunk's
     # first token on (the chunk's tokens meet in one product, where 0 x NaN is NaN)

@@ -58,9 +58,9 @@ constexpr int kGdnMaxJobs = 256, kGdnMaxSegs = 16;   // jobs per grid, segments 
 constexpr int kGdnMaxMats = 400;                     // matrices times heads (64 KB each)
 // Chunks of the shortest segment, and what cutting costs (two more grids, their states) in chunks' time.  Measured, whole
 // against cut, 16 heads: one sequence of 768 tokens 41 against 44 us, of 1024 53 against 51, 2048 95 against 70, 16384 686
-// against 297; two of 1024 56 against 63, two of 2048 103 against 96.  Half-way states cost another kernel (14 us with
-// 4 segments of 16 heads): 4096 tokens 101 us without against 111 with them, 16384 297 against 286, 16384 x 32 heads 545 against 516.
-constexpr int kSegmentMin = 4, kSegmentExtra = 7, kHalvesExtra = 8;
+// against 297; two of 1024 56 against 63, two of 2048 103 against 96.  Half-way states cost another small grid; without
+// and with them, 16 heads: 4096 tokens 98 and 102 us, 6000 132 and 134, 8192 170 and 165, 13000 246 and 235, 16384 288 and 277.
+constexpr int kSegmentMin = 4, kSegmentExtra = 7, kHalvesExtra = 6;
 // A piece of a sequence's state pass.  Matrices are numbered per launch; those of a sequence with k inner segments are S_1 ..
 // S_(k+1), F_1 .. F_k, and half way B (then the state) and F of each.
 struct GdnJob {
@@ -1062,69 +1062,99 @@ __global__ void __launch_bounds__(ch::kThreads, 1) gdn_chain_kernel(const __grid
 }
 
 // Entering states, S' = F S + B (S' goes where B is), in fp32, a sequence's (`chunks` of them) one behind the other from S
-// (matrix src; F: mid .., B: dst ..), or alone: a CTA per job, head and 16 value channels, a warp per 16 key channels.  A lane holds four columns of F's rows, which a warp
-// reads as whole rows, and the four rows of S that they meet; the lanes' sums meet in a halving exchange, at whose end
-// each lane holds one.  Bound by the latency of its few steps; the next F and B are on their way during a step.
-constexpr int kJoinParts = 8, kJoinStride = 68;
-__global__ void __launch_bounds__(256, 1) gdn_join_kernel(const __grid_constant__ GdnPrefillParams prm) {
-  __shared__ __align__(16) float s_state[2][32 * kJoinStride];   // rows 4 l .. + 3 at kJoinStride l
-  const int part = blockIdx.x % kJoinParts, h = blockIdx.x / kJoinParts % prm.Hv, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const GdnJob job = prm.job[blockIdx.x / kJoinParts / prm.Hv];
+// (matrix src; F: mid .., B: dst ..), or alone: a CTA per job, head and 16 value channels.  F comes to shared memory, the
+// next one during a step (where there is one).  A thread sums half of the key channels for two rows and 8 value channels,
+// two products an instruction; the halves meet in shared memory.  Bound by the issue of a step's products and operand
+// reads (1400 cycles) and the latency around them.
+namespace jn {
+constexpr int kParts = 8, kThreads = 256, kStride = 132;   // value channels / 16; floats of a row of F
+constexpr uint32_t kF = kD * kStride * 4, OFF_S = 0, OFF_SUM = 2 * kD * 64, OFF_F = 3 * kD * 64;   // S: two of [128][16]
+constexpr uint32_t smem_bytes(int steps) { return OFF_F + (steps > 1 ? 2 : 1) * kF; }
+}  // namespace jn
+__global__ void __launch_bounds__(jn::kThreads) gdn_join_kernel(const __grid_constant__ GdnPrefillParams prm) {
+  using namespace jn;
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  const int tid = threadIdx.x, part = blockIdx.x % kParts, h = blockIdx.x / kParts % prm.Hv;
+  const GdnJob job = prm.job[blockIdx.x / kParts / prm.Hv];
   const auto mat = [&](int m) { return prm.mats + (static_cast<size_t>(m) * prm.Hv + h) * kD * kD; };
-  // this lane's entry of rows 2 i, 2 i + 1 of the warp's: row 2 i + lane / 16, value channel lane % 16
-  const size_t at = static_cast<size_t>(16 * warp + (lane >> 4)) * kD + 16 * part + (lane & 15);
-  const auto put = [&](int buf, int i, float y) {
-    const int row = 16 * warp + 2 * i + (lane >> 4);
-    s_state[buf][(row >> 2) * kJoinStride + (row & 3) * 16 + (lane & 15)] = y;
-  };
-  float4 f[16];
-  float b[8];
+  float *const s_state = reinterpret_cast<float *>(smem_raw + OFF_S), *const s_sum = reinterpret_cast<float *>(smem_raw + OFF_SUM);
   const auto fetch = [&](int j) {
-    const float4 *src = reinterpret_cast<const float4 *>(mat(job.mid + j) + static_cast<size_t>(16 * warp) * kD);
+    const float *src = mat(job.mid + j);
+    const uint32_t dst = smem_u32(smem_raw) + OFF_F + (j & 1) * kF;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) f[i] = src[32 * i + lane];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) b[i] = mat(job.dst + j)[at + 2 * i * kD];
+    for (int i = 0; i < 16; ++i) {
+      const int x = i * kThreads + tid;   // 16 bytes: row x / 32, piece x % 32
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + (x >> 5) * kStride * 4 + (x & 31) * 16), "l"(src + 4 * x) : "memory");
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
   };
   grid_dependency_wait();
   fetch(0);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) put(0, i, mat(job.src)[at + 2 * i * kD]);
-  __syncthreads();
+  for (int i = 0; i < 2; ++i) {
+    const int x = i * kThreads + tid;     // 16 bytes: row x / 4, piece x % 4
+    *reinterpret_cast<float4 *>(s_state + 4 * x) = *reinterpret_cast<const float4 *>(mat(job.src) + (x >> 2) * kD + 16 * part + 4 * (x & 3));
+  }
+  const int k0 = tid >> 7 ? kD / 2 : 0, c0 = 8 * (tid & 1), row = (tid & 127) >> 1;   // and row + 64
   for (int j = 0; j < job.chunks; ++j) {
-    float st[4][16];
+    const bool more = j + 1 < job.chunks;
+    if (more) fetch(j + 1);
+    float *out = mat(job.dst + j) + row * kD + 16 * part + c0;
+    float4 b[2][2];
+    if (k0 == 0) {
 #pragma unroll
-    for (int x = 0; x < 16; ++x)
-      *reinterpret_cast<float4 *>(&st[x >> 2][4 * (x & 3)]) =
-          *reinterpret_cast<const float4 *>(&s_state[j & 1][kJoinStride * lane + 4 * x]);
-    float y[8];
+      for (int r = 0; r < 2; ++r)
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      float v[32];
+        for (int x = 0; x < 2; ++x) b[r][x] = *reinterpret_cast<const float4 *>(out + r * 64 * kD + 4 * x);
+    }
+    if (more) asm volatile("cp.async.wait_group 1;" ::: "memory");
+    else asm volatile("cp.async.wait_group 0;" ::: "memory");
+    __syncthreads();
+    const float *f = reinterpret_cast<const float *>(smem_raw + OFF_F + (j & 1) * kF) + row * kStride + k0;
+    const float *st = s_state + (j & 1) * kD * 16 + k0 * 16 + c0;
+    float2 acc[2][4];
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const float4 w = f[2 * i + r];
+    for (int r = 0; r < 2; ++r)
 #pragma unroll
-        for (int c = 0; c < 16; ++c) v[16 * r + c] = fmaf(w.w, st[3][c], fmaf(w.z, st[2][c], fmaf(w.y, st[1][c], w.x * st[0][c])));
-      }
+      for (int x = 0; x < 4; ++x) acc[r][x] = make_float2(0.f, 0.f);
+#pragma unroll 4
+    for (int k = 0; k < kD / 2; k += 4) {
+      const float4 fa = *reinterpret_cast<const float4 *>(f + k), fb = *reinterpret_cast<const float4 *>(f + 64 * kStride + k);
+      const float a4[4] = {fa.x, fa.y, fa.z, fa.w}, b4[4] = {fb.x, fb.y, fb.z, fb.w};
 #pragma unroll
-      for (int half = 16; half > 0; half >>= 1) {
-        const bool up = lane & half;
+      for (int kk = 0; kk < 4; ++kk) {
+        const float4 s0 = *reinterpret_cast<const float4 *>(st + (k + kk) * 16), s1 = *reinterpret_cast<const float4 *>(st + (k + kk) * 16 + 4);
+        const float2 s2[4] = {make_float2(s0.x, s0.y), make_float2(s0.z, s0.w), make_float2(s1.x, s1.y), make_float2(s1.z, s1.w)};
 #pragma unroll
-        for (int x = 0; x < half; ++x) {
-          const float send = up ? v[x] : v[x + half];
-          v[x] = (up ? v[x + half] : v[x]) + __shfl_xor_sync(0xffffffffu, send, half);
+        for (int x = 0; x < 4; ++x) {
+          acc[0][x] = fma2(make_float2(a4[kk], a4[kk]), s2[x], acc[0][x]);
+          acc[1][x] = fma2(make_float2(b4[kk], b4[kk]), s2[x], acc[1][x]);
         }
       }
-      y[i] = v[0] + b[i];
     }
-    if (j + 1 < job.chunks) fetch(j + 1);
+    float *sum = s_sum + row * 16 + c0;
+    if (k0 != 0) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      put((j + 1) & 1, i, y[i]);
-      mat(job.dst + j)[at + 2 * i * kD] = y[i];
+      for (int r = 0; r < 2; ++r)
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+          *reinterpret_cast<float4 *>(sum + r * 64 * 16 + 4 * x) = make_float4(acc[r][2 * x].x, acc[r][2 * x].y, acc[r][2 * x + 1].x, acc[r][2 * x + 1].y);
     }
     __syncthreads();
+    if (k0 == 0) {
+      float *next = s_state + ((j + 1) & 1) * kD * 16 + row * 16 + c0;
+#pragma unroll
+      for (int r = 0; r < 2; ++r)
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const float4 u = *reinterpret_cast<const float4 *>(sum + r * 64 * 16 + 4 * x);
+          const float4 y = make_float4(acc[r][2 * x].x + u.x + b[r][x].x, acc[r][2 * x].y + u.y + b[r][x].y,
+                                       acc[r][2 * x + 1].x + u.z + b[r][x].z, acc[r][2 * x + 1].y + u.w + b[r][x].w);
+          *reinterpret_cast<float4 *>(next + r * 64 * 16 + 4 * x) = y;
+          *reinterpret_cast<float4 *>(out + r * 64 * kD + 4 * x) = y;
+        }
+    }
+    __syncthreads();   // (F's buffer and the sums are free, the next state is in place)
   }
 }
 
@@ -1226,12 +1256,12 @@ cudaError_t launch_segments(GdnPrefillParams &p, const Cut &cut, float *mats, cu
   each([&](int i, int, int k, int base, int f, int, int) {
     if (k) add(i, base, base + 1, 0, k, f);
   });
-  if (const cudaError_t e = run(gdn_join_kernel, kJoinParts, 256, 0)) return e;
+  if (const cudaError_t e = run(gdn_join_kernel, jn::kParts, jn::kThreads, jn::smem_bytes(2))) return e;
   if (cut.halves == 2) {
     each([&](int i, int, int k, int base, int, int mb, int mf) {
       for (int j = 0; j < k; ++j) add(i, base + j, mb + j, 0, 1, mf + j);
     });
-    if (const cudaError_t e = run(gdn_join_kernel, kJoinParts, 256, 0)) return e;
+    if (const cudaError_t e = run(gdn_join_kernel, jn::kParts, jn::kThreads, jn::smem_bytes(1))) return e;
   }
   each([&](int i, int chunks, int k, int base, int, int mb, int) {
     add(i, base + k, kToCaller, (1 + k) * g, chunks - (1 + k) * g);
@@ -1273,6 +1303,8 @@ cudaError_t launch_gdn_prefill(const GdnRecurrentArgs &a, const int32_t *cu_host
           r = cudaFuncSetAttribute(gdn_chain_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, ch::kSmemBytes);
         if (r == cudaSuccess)
           r = cudaFuncSetAttribute(gdn_chain_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, ch::kSmemBytes);
+        if (r == cudaSuccess)
+          r = cudaFuncSetAttribute(gdn_join_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, jn::smem_bytes(2));
         return r;
       }))
     return e;

@@ -304,7 +304,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attention_kernel(PagedArgs 
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (uint32_t q = 0; q < kMostRanks; ++q)
-          if (ml[q].x != -INFINITY) {   // (a CTA without tokens has written no channels)
+          if (ml[q].x != -INFINITY || ml[q].y != 0.f) {   // (a CTA without tokens has written no channels)
             const float c = fast_exp2(ml[q].x - bs);
             ll += c * ml[q].y;
             acc.x += c * x[q].x; acc.y += c * x[q].y; acc.z += c * x[q].z; acc.w += c * x[q].w;
@@ -354,7 +354,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attention_kernel(PagedArgs 
         info.y |= kLastTile;
       const uint32_t on[2] = {__ballot_sync(0xffffffffu, ok[0]), __ballot_sync(0xffffffffu, ok[1])};
       if (i >= kStages) sm100::wait_or_abort(&freed[st], (i / kStages - 1) & 1, s_abort, p.status);
-      if (*s_abort) break;   // (what was asked for lands below)
+      if (__any_sync(0xffffffffu, *s_abort != 0)) break;   // (what was asked for lands below)
       if (lane == 0) {
         uint64_t mask = (static_cast<uint64_t>(on[1]) << 32) | on[0];
         if (box > 1) {
@@ -460,7 +460,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attention_kernel(PagedArgs 
     const int st = i % kStages;
     sm100::wait_or_abort(&landed[st], (i / kStages) & 1, s_abort, p.status);
     const int4 info = s_info[st];
-    if (*s_abort) break;
+    if (__any_sync(0xffffffffu, *s_abort != 0)) break;
     cur.b = info.x; cur.hr = info.y & (kLastTile - 1); cur.tile = info.z; cur.len = info.w;
     const bool stretch_ends = info.y & kLastTile;
     if (fresh) {

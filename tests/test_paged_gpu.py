@@ -153,6 +153,19 @@ def test_what_is_not_seen_does_not_matter(width):
         assert torch.isnan(out[b * 3 + 2]).all()
 
 
+@pytest.mark.parametrize("width", [None, 4000])
+@pytest.mark.parametrize("tile", [0, 2, 6])
+def test_nan_of_seen_tokens_is_kept(tile, width):
+    # also where it is all that one CTA of an item sees
+    q, k, v, table, lens = make([500, 130], 1, 8, 2, 16, seed=14, width=width)
+    clean = check(q, k, v, table, lens, 1)[0]
+    for j in range(64 * tile, min(64 * tile + 64, 500)):
+        k[int(table[0, j // 16]), j % 16, 1] = float("nan")
+    out, _ = kda.paged_attention(q, k, v, table, lens, 1)
+    assert torch.isnan(out[0, 4:]).all()
+    assert torch.equal(out[0, :4], clean[0, :4]) and torch.equal(out[1], clean[1])
+
+
 @pytest.mark.parametrize("bad", [0, 1, 77, 149, 399])
 @pytest.mark.parametrize("longest", [40, 700])
 def test_a_bad_length_is_recorded_wherever_it_is(bad, longest):

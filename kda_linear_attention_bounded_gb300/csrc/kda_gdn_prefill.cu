@@ -715,7 +715,7 @@ __global__ void __launch_bounds__(ch::kThreads, 1) gdn_chain_kernel(const __grid
       // |R|, |U| <= |v| + |S| within the chunk < 2^(e + 1) -> below 2^14 by a scale of at most 2^90 (which keeps the factors
       // finite where a channel is zero so far).  64 tokens of |v| <= vm add at most 8 vm to |S|; a loose bound costs
       // nothing until it is 2^15 times too large.  Lane: channels 2 lane, + 1, + 64, + 65.
-      float bound[4];   // of the channels' states in 2-norm
+      float bound[4];   // of the channels' states in 2-norm (the entering one's 1-norm: its squares may leave fp32)
       int field[4] = {300, 300, 300, 300};   // the scales' exponent fields
       float last[4] = {0.f, 0.f, 0.f, 0.f};  // the last chunk's largest |v|
       {
@@ -724,11 +724,11 @@ __global__ void __launch_bounds__(ch::kThreads, 1) gdn_chain_kernel(const __grid
           for (int e = 0; e < kD; ++e) {
             const float2 a = *reinterpret_cast<const float2 *>(src + e * kD + 2 * lane);
             const float2 b = *reinterpret_cast<const float2 *>(src + e * kD + 64 + 2 * lane);
-            ss[0] = fmaf(a.x, a.x, ss[0]); ss[1] = fmaf(a.y, a.y, ss[1]);
-            ss[2] = fmaf(b.x, b.x, ss[2]); ss[3] = fmaf(b.y, b.y, ss[3]);
+            ss[0] += fabsf(a.x); ss[1] += fabsf(a.y);
+            ss[2] += fabsf(b.x); ss[3] += fabsf(b.y);
           }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) bound[i] = map ? 1.f : sqrtf(ss[i]);
+        for (int i = 0; i < 4; ++i) bound[i] = map ? 1.f : ss[i];
       }
       for (int c = 0; c < nchunks; ++c) {
         const uint8_t *st = sm + (c & 1) * kStage;

@@ -129,6 +129,43 @@ def test_prefill_decays(a_mean):
     assert rel_l2(final, ref_S) <= STATE_CHUNKED
 
 
+@pytest.mark.parametrize("lens", [[150], [2100]])
+@pytest.mark.parametrize("initial", [False, True])
+def test_prefill_channels_of_any_size(lens, initial):
+    # value channels from 10^-20 to 10^20, some of them growing on the way, some zero for a while: each is as accurate as
+    # if it were alone
+    x = gdn_inputs(sum(lens), 1, 2, seed=70, a_mean=-5.0)
+    g = torch.Generator().manual_seed(71)
+    size = (10.0 ** (40 * torch.rand((1, 2, D), generator=g) - 20)).cuda()
+    size = size.repeat(sum(lens), 1, 1)
+    size[40:, :, 3] *= 1e8
+    size[100:, :, 4] *= 1e-8
+    size[:90, :, 5] = 0.0
+    x[2] = (x[2].float() * size).bfloat16()
+    x[2][130:, :, 6] = 0.0
+    pool = _pool(1, 2, 72) * size[0][None, :, None, :] if initial else None
+    kw = dict(state_pool=pool.contiguous(), slot_ids=_i32([0]), load_initial=True) if initial else {}
+    out, final = _prefill(x, lens, **kw)
+    ref, _, ref_S = gdn_reference(x, lens, pool, keep=False)
+    for h in range(2):
+        for c in range(D):
+            assert rel_l2(final[0, h, :, c], ref_S[0, h, :, c]) <= STATE_CHUNKED, (h, c)
+            assert rel_l2(out[:, h, c], ref[:, h, c]) <= 3 * OUT_STEP, (h, c)
+
+
+def test_prefill_keys_of_any_size_and_none():
+    # keys from 10^-12 to 10^12 (the norm's 1e-6 counts for the small ones), queries likewise, some of them zero
+    x = gdn_inputs(200, 1, 2, seed=73, a_mean=-5.0)
+    g = torch.Generator().manual_seed(74)
+    for i in (0, 1):
+        x[i] = (x[i].float() * (10.0 ** (24 * torch.rand((200, 1, 1), generator=g) - 12)).cuda()).bfloat16()
+        x[i][20 + i:200:7] = 0.0
+    out, final = _prefill(x, [200])
+    ref, _, ref_S = gdn_reference(x, [200])
+    assert rel_l2(out, ref) <= 3 * OUT_STEP
+    assert rel_l2(final, ref_S) <= STATE_CHUNKED
+
+
 def test_prefill_one_strong_decay_among_weak_ones():
     # a token that clears the state: pairs of tokens behind it keep their weak decays
     x = gdn_inputs(190, 1, 2, seed=12, a_mean=-2.0)

@@ -320,9 +320,13 @@ __global__ void __launch_bounds__(in::kThreads, 4) gdn_intra_kernel(const __grid
         tmem_ld16_async(lanes + 32 * q4 + 16, v + 16);
         tmem_wait_ld();
         tmem_tie<32>(v);
-        float d = 0.f;
 #pragma unroll
-        for (int e = 0; e < 32; ++e) d = e == lane ? __uint_as_float(v[e]) : d;
+        for (int half = 16; half > 0; half >>= 1) {   // entry `lane`: a bit of it at a time
+          const bool up = lane & half;
+#pragma unroll
+          for (int e = 0; e < half; ++e) v[e] = up ? v[e + half] : v[e];
+        }
+        const float d = __uint_as_float(v[0]);
         const int r = 32 * q4 + lane;
         s_norm[r] = (r & 63) < valid ? rsqrtf(d + kL2Eps) : 0.f;
         // a power of two that brings the raw key's norm to (1/2, 1] (a zero key: any)
@@ -350,6 +354,7 @@ __global__ void __launch_bounds__(in::kThreads, 4) gdn_intra_kernel(const __grid
       const float down = rowf * fast_exp2(bi + bf);
       if ((q4 & 1) >= ib) {   // (rows 0..31, columns 32..63 lie above the diagonal)
         const int lim = r < valid ? r - 32 * ib + (is_p ? 1 : 0) : 0;   // kept: i < r (A), i <= r (P)
+        const bool masked = __any_sync(0xffffffffu, lim < 32);   // (not below the diagonal in a full chunk)
         uint32_t v[32];
         tmem_ld16_async(lanes + 32 * ib, v);
         tmem_ld16_async(lanes + 32 * ib + 16, v + 16);
@@ -374,8 +379,10 @@ __global__ void __launch_bounds__(in::kThreads, 4) gdn_intra_kernel(const __grid
                 x[e + z] = __uint_as_float(v[e0 + e + z]) * (rowf * n4[z]) * fast_exp2((bi - s_bi[i + z]) + (bf - s_bf[i + z]));
             }
           }
+          if (masked) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) x[e] = e0 + e < lim ? x[e] : 0.f;
+            for (int e = 0; e < 8; ++e) x[e] = e0 + e < lim ? x[e] : 0.f;
+          }
           if (is_p) {
             *reinterpret_cast<uint4 *>(s_blk + kBlkP + swz_offset(64, r, 32 * ib + e0)) =
                 make_uint4(pack_f16x2(make_float2(x[0], x[1])), pack_f16x2(make_float2(x[2], x[3])),

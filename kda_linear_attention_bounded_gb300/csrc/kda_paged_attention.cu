@@ -15,9 +15,9 @@
 // parts in the order of its tokens, so results do not depend on timing.  Few short items go to a cluster of CTAs each
 // instead, which join in shared memory.
 //
-// One warp brings tiles through three 32 KB stages (page ids are looked up a tile earlier), four compute on them, and
-// they meet at mbarriers only.  Pages whose size has a power of two of 8 or more in it come by TMA, in boxes of so many
-// rows (up to 64); other sizes by 16-byte asynchronous copies, a row's pair at a time.  A CTA's rows (16, 32 or 64 of
+// One warp, or two, bring tiles through three 32 KB stages (page ids are looked up a tile earlier), four compute on them,
+// and they meet at mbarriers only.  Pages whose size has a power of two of 16 or more in it come by TMA, in boxes of so many
+// rows (up to 64); other sizes by 16-byte asynchronous copies, by two warps.  A CTA's rows (16, 32 or 64 of
 // them: query heads of the key head x new tokens) share every key and value; with 16 rows the four warps split a tile's
 // tokens, with 64 its rows.  Products are mma.sync m16n8k16 (bf16, fp32 sums): even 64 rows need 64 operations per
 // byte, which it sustains at HBM speed.  e^(s - m) is rounded to bf16 for the second product (the cache's own
@@ -33,7 +33,7 @@
 namespace kda {
 namespace {
 
-constexpr int kThreads = 160, kComputeWarps = 4;   // and a loading warp
+constexpr int kThreads = 192, kComputeWarps = 4;   // and two loading warps (the second for copies only)
 constexpr int kTile = 64;        // tokens per tile
 constexpr int kStages = 3;
 constexpr uint32_t kStageBytes = 2 * kTile * kD * 2;   // K rows, then V rows
@@ -174,13 +174,13 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attention_kernel(PagedArgs 
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   const int wr = warp % WR, wt = warp / WR;
   const int ipr = p.Hk * p.row_blocks;   // items per request
-  if (maps.box && tid == kThreads - 32) {
+  if (maps.box && tid == 32 * kComputeWarps) {
     sm100::prefetch_tensormap(&maps.k);
     sm100::prefetch_tensormap(&maps.v);
   }
   if (tid == 0) {
     for (int i = 0; i < kStages; ++i) {
-      sm100::mbar_init(&landed[i], maps.box ? 1 : 33);
+      sm100::mbar_init(&landed[i], maps.box ? 1 : 66);
       sm100::mbar_init(&freed[i], kComputeWarps);
     }
     sm100::mbar_init(met, kComputeWarps);
@@ -191,7 +191,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attention_kernel(PagedArgs 
   sm100::grid_launch_dependents();
 
   // ---- this CTA's stretch of the line of tiles
-  int64_t *s_scan = reinterpret_cast<int64_t *>(sm + OFF_SCAN);   // [5] warp sums, then the start's request and tile
+  int64_t *s_scan = reinterpret_cast<int64_t *>(sm + OFF_SCAN);   // [6] warp sums, then the start's request and tile
   int64_t first = 0, last = 0, total = 0;
   int stretches = 0;   // CTAs with units: every one of them has at least one
   Cursor cur;
@@ -319,89 +319,79 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attention_kernel(PagedArgs 
     return;
   }
 
-  if (warp == kComputeWarps) {
+  if (warp >= kComputeWarps) {
     // ---------------------------------------------------------------- loads
-    const int box = maps.box ? maps.box : 1, boxes = kTile / box;   // TMA: a box a lane; copies: rows lane, lane + 32
+    const int box = maps.box ? maps.box : 1, boxes = kTile / box;
+    const int half = warp - kComputeWarps;   // copies: rows 32 half + lane; TMA: the first warp's lanes have a box each
+    if (half && maps.box) {
+      finish();
+      return;
+    }
     cur.next = cur.b + 1 < p.B ? request_len(p, cur.b + 1) : 0;
-    int id[2];
-    bool there[2];
+    const int at = lane + 32 * half;
+    int id = 0;
+    bool there = false;
     auto ask = [&] {   // the pages of the tile at the cursor
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const int at = lane + 32 * x, pos = cur.tile * kTile + at * box;
-        there[x] = at < boxes && pos < cur.len;
-        id[x] = there[x] ? p.table[static_cast<int64_t>(cur.b) * p.table_stride + pos / p.page] : 0;
-      }
+      const int pos = cur.tile * kTile + at * box;
+      there = at < boxes && pos < cur.len;
+      id = there ? p.table[static_cast<int64_t>(cur.b) * p.table_stride + pos / p.page] : 0;
     };
     ask();
     for (int i = 0; ; ++i) {
       const int st = i % kStages, pos0 = cur.tile * kTile, h = cur.hr / p.row_blocks;
       const uint32_t dst = smem + st * kStageBytes;
       int4 info = make_int4(cur.b, cur.hr, cur.tile, cur.len);
-      bool ok[2];
-      int pg[2];
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        pg[x] = id[x];
-        ok[x] = there[x] && id[x] >= 0 && id[x] < p.num_pages;
-        if (there[x] && !ok[x]) atomicOr(p.status, KDA_DEVICE_BAD_PAGE);
-      }
+      const int pg = id;
+      const bool ok = there && pg >= 0 && pg < p.num_pages;
+      if (there && !ok) atomicOr(p.status, KDA_DEVICE_BAD_PAGE);
       advance(p, cur, ipr);
       const bool more = cur.unit < last;
       if (more)
         ask();
       else
         info.y |= kLastTile;
-      const uint32_t on[2] = {__ballot_sync(0xffffffffu, ok[0]), __ballot_sync(0xffffffffu, ok[1])};
+      const uint32_t on = __ballot_sync(0xffffffffu, ok);
       if (i >= kStages) sm100::wait_or_abort(&freed[st], (i / kStages - 1) & 1, s_abort, p.status);
       if (__any_sync(0xffffffffu, *s_abort != 0)) break;   // (what was asked for lands below)
       if (lane == 0) {
-        uint64_t mask = (static_cast<uint64_t>(on[1]) << 32) | on[0];
-        if (box > 1) {
-          mask = 0;
+        if (half == 0) s_info[st] = info;
+        if (maps.box) {
+          uint64_t mask = 0;
           for (int x = 0; x < boxes; ++x)
-            if (on[0] >> x & 1) mask |= first_tokens(box) << (x * box);
-          mask &= first_tokens(info.w - pos0);
-        }
-        s_info[st] = info;
-        s_mask[st] = mask;
-        if (maps.box)
-          sm100::mbar_arrive_expect_tx(&landed[st], __popc(on[0]) * box * 512);
-        else
+            if (on >> x & 1) mask |= first_tokens(box) << (x * box);
+          s_mask[st] = mask & first_tokens(info.w - pos0);
+          sm100::mbar_arrive_expect_tx(&landed[st], __popc(on) * box * 512);
+        } else {
+          reinterpret_cast<uint32_t *>(&s_mask[st])[half] = on;
           sm100::mbar_arrive(&landed[st]);
+        }
       }
       __syncwarp();
       if (maps.box) {
-        if (ok[0]) {
+        if (ok) {
           const int tok = (pos0 + lane * box) % p.page;
-          const uint32_t at = dst + lane * box * 128;
-          tma_load_4d(at, &maps.k, 0, h, tok, pg[0], &landed[st]);
-          tma_load_4d(at + kHalf, &maps.k, 64, h, tok, pg[0], &landed[st]);
-          tma_load_4d(at + 2 * kHalf, &maps.v, 0, h, tok, pg[0], &landed[st]);
-          tma_load_4d(at + 3 * kHalf, &maps.v, 64, h, tok, pg[0], &landed[st]);
+          const uint32_t to = dst + lane * box * 128;
+          tma_load_4d(to, &maps.k, 0, h, tok, pg, &landed[st]);
+          tma_load_4d(to + kHalf, &maps.k, 64, h, tok, pg, &landed[st]);
+          tma_load_4d(to + 2 * kHalf, &maps.v, 0, h, tok, pg, &landed[st]);
+          tma_load_4d(to + 3 * kHalf, &maps.v, 64, h, tok, pg, &landed[st]);
         }
         __syncwarp();
       } else {
-        int64_t ka[2], va[2];   // this lane's two rows (-1: not there)
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const int64_t tok = (pos0 + lane + 32 * x) % p.page;
-          ka[x] = ok[x] ? pg[x] * p.k_page_stride + tok * p.k_token_stride + h * p.k_head_stride : -1;
-          va[x] = pg[x] * p.v_page_stride + tok * p.v_token_stride + h * p.v_head_stride;
-        }
+        const int64_t tok = (pos0 + at) % p.page;   // this lane's row (-1: not there)
+        const int64_t ka = ok ? pg * p.k_page_stride + tok * p.k_token_stride + h * p.k_head_stride : -1;
+        const int64_t va = pg * p.v_page_stride + tok * p.v_token_stride + h * p.v_head_stride;
         const int chunk = lane & 15;
-#pragma unroll
-        for (int x = 0; x < 2; ++x)
 #pragma unroll 4
-          for (int r = 0; r < 32; r += 2) {
-            const int from = r + (lane >> 4);
-            const int64_t k = __shfl_sync(0xffffffffu, ka[x], from), v = __shfl_sync(0xffffffffu, va[x], from);
-            if (k >= 0) {
-              const uint32_t at = dst + row_chunk(32 * x + from, chunk);
-              cp16(at, p.k + k + chunk * 8);
-              cp16(at + 2 * kHalf, p.v + v + chunk * 8);
-            }
+        for (int r = 0; r < 32; r += 2) {
+          const int from = r + (lane >> 4);
+          const int64_t k = __shfl_sync(0xffffffffu, ka, from), v = __shfl_sync(0xffffffffu, va, from);
+          if (k >= 0) {
+            const uint32_t to = dst + row_chunk(32 * half + from, chunk);
+            cp16(to, p.k + k + chunk * 8);
+            cp16(to + 2 * kHalf, p.v + v + chunk * 8);
           }
+        }
         asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(sm100::smem_u32(&landed[st])) : "memory");
       }
       if (!more) break;
@@ -769,8 +759,8 @@ __global__ void __launch_bounds__(kJoinThreads, 2) paged_join_kernel(PagedArgs p
 // where one request is much longer than the others only stretches share it out, hence not more.
 constexpr int kWholeTiles = 4;
 // Boxes of fewer rows are not worth a TMA copy each (four a box).  Measured over 64 x 8192 tokens, 2 key heads: boxes of 8
-// 115 us against 132 us by asynchronous copies, of 4 171 us against 132 (of 16 and more 93 us).
-constexpr int kLeastBox = 8;
+// 109 us against 95 us by asynchronous copies, of 16 and more 90 to 92 us (copies by one warp instead of two: 133 us).
+constexpr int kLeastBox = 16;
 
 // false: the strides or sizes are none that a tensor map takes
 bool make_page_map(CUtensorMap *map, const uint16_t *pages, int64_t page_stride, int64_t token_stride, int64_t head_stride,

@@ -430,3 +430,43 @@ def test_captured_behind_other_work(before):
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip((pool, out, out2, final), want))
+
+
+def test_two_streams_at_once():
+    # prefills of different shapes (cut and whole), decodes beside them, each stream with its own workspace and pool
+    shapes = [([300, 64, 500], 2, 4), ([2500], 1, 2)]
+    runs = []
+    for i, (lens, hk, hv) in enumerate(shapes):
+        x = gdn_inputs(sum(lens), hk, hv, seed=80 + i, a_mean=-5.0)
+        cu = [0]
+        for n in lens:
+            cu.append(cu[-1] + n)
+        dec = [t[:3].contiguous() if t.shape[0] == sum(lens) else t for t in x]
+        runs.append(dict(x=x, cu=_i32(cu), cu_h=torch.tensor(cu, dtype=torch.int32), dec=dec, pool=_pool(4, hv, 82 + i),
+                         slots=_i32([3, 0, 1]), ws=kda.make_workspace(nbytes=kda.gdn_prefill_workspace_size(sum(lens), len(lens), hv)),
+                         out=torch.empty((sum(lens), hv, D), dtype=torch.bfloat16, device="cuda"),
+                         final=torch.empty((len(lens), hv, D, D), device="cuda"),
+                         dout=torch.empty((3, hv, D), dtype=torch.bfloat16, device="cuda")))
+
+    def step(r, stream):
+        kda.gdn_chunk_prefill(*r["x"], r["cu"], r["cu_h"], out=r["out"], final_state=r["final"], workspace=r["ws"], stream=stream)
+        kda.gdn_decode(*r["dec"], r["pool"], r["slots"], out=r["dout"], workspace=r["ws"], stream=stream)
+
+    want = []
+    for r in runs:
+        pool = r["pool"].clone()
+        for _ in range(8):
+            step(r, None)
+        want.append([r[k].clone() for k in ("out", "final", "dout", "pool")])
+        r["pool"].copy_(pool)
+        for k in ("out", "final", "dout"):
+            r[k].zero_()
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(8):
+        for r, s in zip(runs, streams):
+            step(r, s)
+    torch.cuda.synchronize()
+    for r, w in zip(runs, want):
+        assert kda.read_device_status(r["ws"]) == 0
+        assert all(torch.equal(a, r[k]) for a, k in zip(w, ("out", "final", "dout", "pool")))

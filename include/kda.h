@@ -457,8 +457,9 @@ KDA_API int kda_recurrent_verify_noalloc(const uint16_t *q, const uint16_t *k, c
  * as in kda_chunk_prefill; workspace of kda_gdn_prefill_workspace_size bytes
  * (which grows with each of its arguments; separate ones for concurrent calls).
  * Final states carry an fp32 evaluation's error.  Few long sequences are cut
- * into segments, so a sequence's last bits depend on what it is batched with
- * (not on timing).  A NaN or infinity among a token's inputs reaches the
+ * into segments and batches of sequences of at most 10 tokens go token by
+ * token, so a sequence's last bits depend on what it is batched with (not on
+ * timing).  A NaN or infinity among a token's inputs reaches the
  * outputs of its 64-token chunk and of those behind it, in its own sequence.
  */
 KDA_API size_t kda_gdn_prefill_workspace_size(int64_t total_tokens, int num_seqs, int Hv);

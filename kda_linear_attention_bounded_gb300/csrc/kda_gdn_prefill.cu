@@ -625,6 +625,12 @@ __global__ void __launch_bounds__(ch::kThreads, 1) gdn_chain_kernel(const __grid
       tmem_alloc(s_tmem, kTmemCols);
       tmem_relinquish();
     }
+    if (worker && src) {   // the entering state's 1-norms, a quarter of the key channels each
+      float sum = 0.f;
+#pragma unroll
+      for (int e = 0; e < 32; ++e) sum += fabsf(S[e]);
+      reinterpret_cast<float *>(sm + OFF_OUT)[128 * cg + d] = sum;
+    }
     if (worker) {   // the identity: row tid / 8, the 16 bytes with columns 8 (tid % 8) ..
       const int r = tid >> 3, pc = tid & 7, w = (r & 7) >> 1;
       const uint32_t one = (r >> 3) != pc ? 0u : (r & 1) ? 0x3F800000u : 0x00003F80u;
@@ -726,16 +732,12 @@ __global__ void __launch_bounds__(ch::kThreads, 1) gdn_chain_kernel(const __grid
       int field[4] = {300, 300, 300, 300};   // the scales' exponent fields
       float last[4] = {0.f, 0.f, 0.f, 0.f};  // the last chunk's largest |v|
       {
-        float ss[4] = {0.f, 0.f, 0.f, 0.f};
-        if (src)
-          for (int e = 0; e < kD; ++e) {
-            const float2 a = *reinterpret_cast<const float2 *>(src + e * kD + 2 * lane);
-            const float2 b = *reinterpret_cast<const float2 *>(src + e * kD + 64 + 2 * lane);
-            ss[0] += fabsf(a.x); ss[1] += fabsf(a.y);
-            ss[2] += fabsf(b.x); ss[3] += fabsf(b.y);
-          }
+        const float *sums = reinterpret_cast<const float *>(sm + OFF_OUT);   // (until the first output)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) bound[i] = map ? 1.f : ss[i];
+        for (int i = 0; i < 4; ++i) {
+          const int ch = 64 * (i >> 1) + 2 * lane + (i & 1);
+          bound[i] = map ? 1.f : src ? (sums[ch] + sums[128 + ch]) + (sums[256 + ch] + sums[384 + ch]) : 0.f;
+        }
       }
       for (int c = 0; c < nchunks; ++c) {
         const uint8_t *st = sm + (c & 1) * kStage;

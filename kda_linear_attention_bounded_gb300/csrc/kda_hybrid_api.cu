@@ -1,6 +1,7 @@
 // C ABI of the calls beside the KDA layers (declared in include/kda.h): the gated delta rule, attention over a paged
 // cache, and the step tables.  Host-side validation and launch planning only, by the rules of kda_api.cu: every check
 // that can be made on the host is made before anything is launched, nothing allocates device memory or synchronises.
+#include <algorithm>
 #include <climits>
 #include <cmath>
 #include <cstdint>
@@ -43,6 +44,10 @@ int check_gdn(int64_t tokens, const uint16_t *q, const uint16_t *k, int64_t qk_s
   return KDA_OK;
 }
 
+// Batches whose sequences have so many tokens at most take the recurrence token by token.  Measured, chunks against
+// tokens: 1 sequence x 2 heads of 8 tokens 11.1 and 6.7 us, of 12 11.1 and 9.0; 64 x 16 heads of 8 66 and 52 us, of 12 68 and 75.
+constexpr int kRecurrentTokens = 10;
+
 }  // namespace
 
 extern "C" {
@@ -82,8 +87,9 @@ int kda_gdn_chunk_prefill(const uint16_t *q, const uint16_t *k, int64_t qk_token
   r.state_out_dense = (flags & KDA_FINAL_TO_POOL) ? nullptr : final_state;
   r.status = static_cast<uint32_t *>(workspace);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  // without a token every final state is its initial one: the recurrence's copy
-  const cudaError_t e = cu_seqlens_host[num_seqs] == 0
+  int longest = 0;
+  for (int n = 0; n < num_seqs; ++n) longest = std::max(longest, cu_seqlens_host[n + 1] - cu_seqlens_host[n]);
+  const cudaError_t e = longest <= kRecurrentTokens
                             ? kda::launch_gdn_recurrent(r, num_seqs, st)
                             : kda::launch_gdn_prefill(r, cu_seqlens_host, num_seqs,
                                                       static_cast<uint8_t *>(workspace) + kda::kWorkspaceBytes, st);

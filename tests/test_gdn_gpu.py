@@ -117,6 +117,28 @@ def test_prefill_long_sequence_keeps_channels_apart():
     assert torch.equal(out, clean)
 
 
+@pytest.mark.parametrize("lens,hk,hv", [([10], 1, 2), ([11], 1, 2), ([3, 0, 10, 1], 2, 4), ([3, 0, 11, 1], 2, 4), ([8] * 30, 1, 1)])
+@pytest.mark.parametrize("initial", [False, True])
+def test_prefill_few_tokens(lens, hk, hv, initial):
+    # around the length up to which a batch is taken token by token; a bad slot is skipped on either side
+    x = gdn_inputs(sum(lens), hk, hv, seed=90)
+    pool = _pool(len(lens) + 1, hv, 91)
+    before = pool.clone()
+    slots = torch.arange(len(lens), 0, -1, dtype=torch.int32, device="cuda")
+    out, final = _prefill(x, lens, state_pool=pool, slot_ids=slots, load_initial=initial)
+    ref, _, ref_S = gdn_reference(x, lens, before[slots.long()] if initial else None)
+    assert rel_l2(out, ref) <= 3 * OUT_STEP
+    for n in range(len(lens)):
+        assert rel_l2(final[n], ref_S[n]) <= STATE_CHUNKED
+    slots[0] = -1
+    ws = kda.make_workspace(nbytes=kda.gdn_prefill_workspace_size(sum(lens), len(lens), hv))
+    _, none = _prefill(x, lens, state_pool=pool, slot_ids=slots, load_initial=initial, final_to_pool=True, workspace=ws)
+    assert none is None and kda.read_device_status(ws) == kda.KDA_DEVICE_BAD_SLOT
+    assert torch.equal(pool[0], before[0]) and torch.equal(pool[len(lens)], before[len(lens)])
+    for n in range(1, len(lens)):
+        assert torch.equal(pool[int(slots[n])], final[n])
+
+
 @pytest.mark.parametrize("a_mean", [-12.0, 3.0, 60.0, 3000.0])
 def test_prefill_decays(a_mean):
     # from no decay at all to one that clears the state at every token; e^lambda underflows from about 60 on

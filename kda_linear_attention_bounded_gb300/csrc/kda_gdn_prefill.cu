@@ -1185,13 +1185,14 @@ Cut choose_cut(const GdnPrefillParams &p, int max_mats) {
   const int longest = chunks_of(p, p.order[0]);
   int64_t sum = 0;
   Cut best_cut;
-  if (longest < kSegmentExtra + 2 * kSegmentMin) return best_cut;
+  if (longest < kSegmentExtra + 2 * kSegmentMin || p.num_seqs > kGdnMaxJobs) return best_cut;
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
       sms <= 0)
     sms = 152;
   for (int n = 0; n < p.num_seqs; ++n) sum += chunks_of(p, n);
   int64_t best = std::max<int64_t>(longest, sum * p.Hv / sms);
+  if (sum * p.Hv / sms + kSegmentExtra >= longest) return best_cut;   // the work alone takes as long
   for (int m = 2; m <= kGdnMaxSegs; ++m)
     for (int halves = 1; halves <= 2; ++halves) {
       Cut cut;

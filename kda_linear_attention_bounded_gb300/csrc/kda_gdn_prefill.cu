@@ -56,11 +56,12 @@ constexpr int kGdnMaxSeqs = 1024;   // sequences per launch (longer batches are 
 // state that the same kernel forms from it, and the last segment is about half as long.
 constexpr int kGdnMaxJobs = 256, kGdnMaxSegs = 16;   // jobs per grid, segments per sequence
 constexpr int kGdnMaxMats = 400;                     // matrices times heads (64 KB each)
-// Chunks of the shortest segment, and what cutting costs (two more grids, their states) in chunks' time.  Measured, whole
-// against cut, 16 heads: one sequence of 768 tokens 41 against 44 us, of 1024 53 against 51, 2048 95 against 70, 16384 686
-// against 297; two of 1024 56 against 63, two of 2048 103 against 96.  Half-way states cost another small grid; without
-// and with them, 16 heads: 4096 tokens 98 and 102 us, 6000 132 and 134, 8192 170 and 165, 13000 246 and 235, 16384 288 and 277.
-constexpr int kSegmentMin = 4, kSegmentExtra = 7, kHalvesExtra = 6;
+// Chunks of the shortest segment, and what costs in chunks' time: cutting (two more grids, their states), half-way states
+// (another grid), a CTA behind another on an SM.  Measured, whole against cut, 16 heads: one sequence of 768 tokens 41 and
+// 41 us, of 896 46 and 43, of 1024 51 and 44, 2048 95 and 61, 16384 686 and 285; two of 1024 54 and 57, of 1280 67 and 75 (two
+// CTAs per SM), of 1536 78 and 73, of 2048 101 and 90.  Without half-way states and with them: 4096 tokens 98 and 102 us,
+// 6000 132 and 134, 8192 170 and 165, 13000 246 and 235, 16384 285 and 266.
+constexpr int kSegmentMin = 4, kSegmentExtra = 5, kHalvesExtra = 6, kWaveExtra = 3;
 // A piece of a sequence's state pass.  Matrices are numbered per launch; those of a sequence with k inner segments are S_1 ..
 // S_(k+1), F_1 .. F_k, and half way B (then the state) and F of each.
 struct GdnJob {
@@ -1217,8 +1218,10 @@ Cut choose_cut(const GdnPrefillParams &p, int max_mats) {
         piece = std::max({piece, cut.last(chunks), k == 0 ? 0 : halves == 2 ? cut.half() : cut.g});
       }
       if (jobs1 > kGdnMaxJobs || jobs2 > kGdnMaxJobs || mats * p.Hv > max_mats) continue;
-      const int64_t est = (jobs1 * p.Hv <= sms ? cut.g : work1 * p.Hv / sms + cut.g) +
-                          (jobs2 * p.Hv <= sms ? piece : work2 * p.Hv / sms + piece) + kSegmentExtra + (halves == 2 ? kHalvesExtra : 0);
+      const auto grid = [&](int64_t jobs, int64_t work, int longest_piece) {
+        return jobs * p.Hv <= sms ? longest_piece : work * p.Hv / sms + longest_piece + kWaveExtra * (jobs * p.Hv / sms);
+      };
+      const int64_t est = grid(jobs1, work1, cut.g) + grid(jobs2, work2, piece) + kSegmentExtra + (halves == 2 ? kHalvesExtra : 0);
       if (est < best) {
         best = est;
         best_cut = cut;

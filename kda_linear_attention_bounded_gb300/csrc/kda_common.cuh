@@ -47,9 +47,6 @@ __device__ __forceinline__ float sigmoid_f(float x) {
   return fast_rcp(1.0f + fast_exp2(-x * kLog2e));
 }
 
-// log(1 + e^x), without overflow for large x
-__device__ __forceinline__ float softplus(float x) { return fmaxf(x, 0.f) + log1pf(expf(-fabsf(x))); }
-
 __device__ __forceinline__ float2 unpack_bf16x2(uint32_t v) {
   return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xFFFF0000u));
 }

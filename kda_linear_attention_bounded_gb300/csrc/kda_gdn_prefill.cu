@@ -29,9 +29,7 @@
 #include <algorithm>
 #include <numeric>
 
-#include "kda_common.cuh"
-#include "kda_internal.h"
-#include "kda_sm100.cuh"
+#include "kda_hybrid.cuh"
 
 namespace kda {
 namespace {
@@ -1325,8 +1323,8 @@ cudaError_t launch_gdn_prefill(const GdnRecurrentArgs &a, const int32_t *cu_host
   const int total = cu_host[num_seqs], Hk = a.Hv / a.group;
   const int room = static_cast<int>(matrix_room(total, a.Hv));
   float *mats = reinterpret_cast<float *>(blocks + block_bytes(total, num_seqs, a.Hv));
-  if (!make_token_map(&p.tq, a.q, Hk, total, a.qk_stride) || !make_token_map(&p.tk, a.k, Hk, total, a.qk_stride) ||
-      !make_token_map(&p.tv, a.v, a.Hv, total, a.v_stride) || !make_token_map(&p.tout, a.out, a.Hv, total, a.out_stride))
+  if (!make_tokens_map(&p.tq, a.q, Hk, total, a.qk_stride) || !make_tokens_map(&p.tk, a.k, Hk, total, a.qk_stride) ||
+      !make_tokens_map(&p.tv, a.v, a.Hv, total, a.v_stride) || !make_tokens_map(&p.tout, a.out, a.Hv, total, a.out_stride))
     return cudaErrorInvalidValue;
   p.a = a.a; p.beta = a.beta;
   p.a_stride = a.a_stride; p.beta_stride = a.beta_stride;

@@ -14,9 +14,7 @@
 // run under the stores of another and the last wave is short.  Measured (16 heads): quarters of the channels, eight CTAs
 // per SM 24.8 us for 64 x 1 tokens (5.4 TB/s) and 53.2 us for 64 x 4 (6.4 TB/s); halves 25.6 and 54.7, eighths 29 to 31
 // and 61 us (their rows are half lines).
-#include "kda_common.cuh"
-#include "kda_internal.h"
-#include "kda_sm100.cuh"
+#include "kda_hybrid.cuh"
 
 namespace kda {
 namespace {

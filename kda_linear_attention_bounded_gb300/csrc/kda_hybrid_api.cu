@@ -8,7 +8,7 @@
 
 #include "kda_checks.h"
 #include "kda_common.cuh"
-#include "kda_internal.h"
+#include "kda_hybrid.h"
 
 namespace {
 

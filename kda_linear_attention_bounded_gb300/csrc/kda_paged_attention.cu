@@ -26,9 +26,7 @@
 
 #include <algorithm>
 
-#include "kda_common.cuh"
-#include "kda_internal.h"
-#include "kda_sm100.cuh"
+#include "kda_hybrid.cuh"
 
 namespace kda {
 namespace {

@@ -38,12 +38,11 @@ EncodeTiledFn encode_fn() {
   return fn;
 }
 
-}  // namespace
-
 // [tokens, H, 128] bf16 with the given token stride; box = 64 channels x 1 head x 64 tokens, with the
 // 128-byte swizzle (the row-swizzled tile layout of the MMA operands and the output staging) or
 // unswizzled (tiles read only by CUDA cores); rows past the tensor's end read as zero
-bool make_token_map(CUtensorMap *map, const void *base, int H, int total_tokens, int64_t token_stride, bool swizzled) {
+bool make_token_map(CUtensorMap *map, const void *base, int H, int total_tokens, int64_t token_stride,
+                    bool swizzled = true) {
   EncodeTiledFn enc = encode_fn();
   if (!enc) return false;
   cuuint64_t dims[3] = {static_cast<cuuint64_t>(kD), static_cast<cuuint64_t>(H),
@@ -57,21 +56,7 @@ bool make_token_map(CUtensorMap *map, const void *base, int H, int total_tokens,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-bool make_bf16_map(CUtensorMap *map, const void *base, int rank, const uint64_t *dims, const uint64_t *strides,
-                   const uint32_t *box) {
-  EncodeTiledFn enc = encode_fn();
-  if (!enc || rank > 5) return false;
-  cuuint64_t d[5], st[4];
-  cuuint32_t bx[5], estr[5] = {1, 1, 1, 1, 1};
-  for (int i = 0; i < rank; ++i) {
-    d[i] = dims[i];
-    bx[i] = box[i];
-    if (i + 1 < rank) st[i] = strides[i];
-  }
-  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, static_cast<cuuint32_t>(rank), const_cast<void *>(base), d, st, bx, estr,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
+}  // namespace
 
 size_t prefill_workspace_bytes(int64_t total_tokens, int num_seqs, int H) {
   // sum_n ceil(len_n / 64) <= floor(total / 64) + num_seqs

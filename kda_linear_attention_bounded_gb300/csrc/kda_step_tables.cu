@@ -10,9 +10,7 @@
 // and of the new pages of the window, both found by binary search in the window's sums, so that one long prompt
 // spreads over the grid as evenly as many short ones.  A token of a page handed out in this call reads the page id
 // from the free list, never from the table, so no CTA waits for another's table writes.
-#include "kda_common.cuh"
-#include "kda_internal.h"
-#include "kda_sm100.cuh"
+#include "kda_hybrid.cuh"
 
 namespace kda {
 namespace {

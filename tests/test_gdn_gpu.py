@@ -85,6 +85,31 @@ def test_prefill_long_sequences(lens, hk, hv, a_mean):
     assert torch.equal(out, out2) and torch.equal(pool[slots.long()], final) and torch.equal(pool[0], before[0])
 
 
+def test_prefill_more_sequences_than_a_launch_takes():
+    # 1024 sequences a launch; the second launch's long one is cut into segments
+    g = torch.Generator().manual_seed(95)
+    lens = torch.randint(0, 40, (1029,), generator=g).tolist() + [1500, 7]
+    x = gdn_inputs(sum(lens), 1, 1, seed=96)
+    pool = _pool(len(lens), 1, 97)
+    before = pool.clone()
+    slots = torch.randperm(len(lens), generator=g).to(torch.int32).cuda()
+    ws = kda.make_workspace(nbytes=kda.gdn_prefill_workspace_size(sum(lens), len(lens), 1))
+    out, none = _prefill(x, lens, state_pool=pool, slot_ids=slots, load_initial=True, final_to_pool=True, workspace=ws)
+    assert none is None and kda.read_device_status(ws) == 0
+    ref, _, ref_S = gdn_reference(x, lens, before[slots.long()], keep=False)
+    assert rel_l2(out, ref) <= 3 * OUT_STEP
+    final = pool[slots.long()]
+    for n in range(len(lens)):
+        assert rel_l2(final[n], ref_S[n]) <= STATE_CHUNKED, n
+
+
+def test_prefill_workspace_one_byte_short_is_refused():
+    x = gdn_inputs(1600, 1, 2, seed=98)
+    need = kda.gdn_prefill_workspace_size(1600, 1, 2)
+    with pytest.raises(kda.KdaError):
+        _prefill(x, [1600], workspace=kda.make_workspace(nbytes=need)[:need - 1])
+
+
 @pytest.mark.parametrize("lens,hk,hv", [([13000], 8, 16), ([13000, 130], 5, 15), ([12800], 19, 38)])
 def test_prefill_cut_against_pieces(lens, hk, hv):
     # long enough for half-way states; the same tokens in calls too short to be cut, the state handed on.  Either is

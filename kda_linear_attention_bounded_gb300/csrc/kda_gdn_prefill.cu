@@ -146,6 +146,8 @@ constexpr uint32_t SM_NORM = 0 /* [128]: 1 / |k_r|, 1 / |q_r| */, SM_BETA = 512,
                    SM_END = 1824;
 constexpr uint32_t kSmemBytes = OFF_SMALL + SM_END + 1024;
 static_assert(OFF_BLK == 64 * kStride * 4 && OFF_BLK % 1024 == 0 && OFF_SMALL >= 32768, "shared memory map");
+static_assert(SM_POW + 256 <= SM_BAR && SM_BAR + 2 * 8 <= SM_TMEM && SM_TMEM + 4 <= SM_ABORT && SM_ABORT + 4 <= SM_END,
+              "small part of the shared memory map");
 static_assert(4 * (kSmemBytes + 1024) <= 233472, "four CTAs per SM");
 constexpr uint32_t kTmemCols = 128;
 // Decays of a chunk down to 2^-kFactorRange are split into a row's and a column's factor (2^b_r and 2^-b_i stay far
@@ -514,12 +516,15 @@ constexpr uint32_t OFF_ONE = 2 * kStage;          // identity, 64 x 64 bf16
 constexpr uint32_t OFF_K16 = OFF_ONE + 8192;      // the chunk's keys times 2^-x in fp16 (64 rows x 128 channels)
 constexpr uint32_t OFF_OUT = OFF_K16 + 16384;     // output on its way out (64 rows x 128 channels)
 constexpr uint32_t OFF_SMALL = OFF_OUT + 16384;
-constexpr uint32_t SM_BAR = 0 /* the barriers below */, SM_TMEM = 128, SM_ABORT = 132, SM_SIG = 256 /* [2][128] */, SM_INV = 1280 /* [2][128] */, SM_END = 2304;
+constexpr uint32_t SM_BAR = 0 /* the barriers below */, SM_TMEM = 144, SM_ABORT = 148, SM_SIG = 256 /* [2][128] */, SM_INV = 1280 /* [2][128] */, SM_END = 2304;
 // mbarriers: landed in stage 0, 1: all but v, v (which goes first, for the scales); scales of even, odd chunks; products done (first, second, state's, v's, output's); output
 // tile free | the workers' warps: S, R, U' in place, stage done with, output in its tile
 enum { B_FULL = 0, B_VAL = 2, B_SCALE = 4, B_M1 = 6, B_M2, B_M3, B_V, B_O, B_OUT, B_S, B_R, B_U, B_FREE, B_TILE, kBarriers };
 constexpr uint32_t kSmemBytes = OFF_SMALL + SM_END + 1024;
 static_assert(kSmemBytes <= 232448 && kStage >= kStageLoad && kStage % 1024 == 0, "shared memory map");
+static_assert(SM_BAR + 8 * kBarriers <= SM_TMEM && SM_TMEM + 4 <= SM_ABORT && SM_ABORT + 4 <= SM_SIG &&
+                  SM_SIG + 1024 <= SM_INV && SM_INV + 1024 <= SM_END,
+              "small part of the shared memory map");
 constexpr uint32_t TM_KU = 0 /* two of 64 */, TM_D = 0 /* 128, over KU */, TM_U = 128 /* two of 64 */, TM_OT = 128 /* over U */,
                    TM_V = 192 /* over U */, TM_QS = 256, TM_S = 320 /* two of 64 */, TM_UH = 320 /* 32, over S */,
                    TM_R = 448 /* two of 32 */, kTmemCols = 512;

@@ -44,6 +44,7 @@ constexpr uint32_t OFF_SCAN = OFF_CML + 512;
 constexpr uint32_t OFF_BAR = OFF_SCAN + 64;            // landed [3], free [3], readers met, abort flag
 constexpr uint32_t kSmemBytes = OFF_BAR + 64 + 1024;
 static_assert(4 * 16 * kD * 4 <= kStageBytes, "the warps' sums fit one stage");
+static_assert(16 * kStages <= 64 && 8 * kStages <= 32 && (2 * kStages + 1) * 8 <= 56, "small parts of the shared memory map");
 
 // 16 bytes (8 channels) `chunk` of a tile's row
 __device__ __forceinline__ uint32_t row_chunk(int row, int chunk) {

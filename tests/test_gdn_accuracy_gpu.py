@@ -1,0 +1,44 @@
+"""Final states of the gated delta rule's prefill to the accuracy of an fp32 evaluation, whatever the inputs' sizes."""
+import pytest
+import torch
+
+import kda_linear_attention_bounded_gb300 as kda
+from gdn_rounding import final_states
+from hybrid_refs import D, gdn_inputs, gdn_reference, rel_l2
+
+# Outputs: a bf16 rounding of P, of U and of the result, 2^-8 each at most.
+OUT = 3 * 2.0 ** -8
+# A state is a sum of terms k^ u.  Besides S's own rounding a term carries eight relative errors of at most 2^-22 each: beta,
+# the key's norm, the decay's two factors (approximate exponentials and reciprocal roots are good to 2^-22), L, R and U
+# as pairs of fp16 (2^-23 each, with their products' sums 2^-22), and the sum of the terms.
+TERM = 8 * 2.0 ** -22
+# lengths and the mean of `a` (how weak the decays are): one chunk, a few, a ragged batch, long ones that are cut into segments
+STATES = [([64], 0.0), ([200], 0.0), ([200], -6.0), ([64, 130, 11], -3.0), ([1100], -6.0)]
+
+
+def state_bound(x, lens, S0=None):
+    """Per sequence and head: the terms' errors and what S's rounding (two bf16) costs alone, both in rel-L2."""
+    _, _, ref = gdn_reference(x, lens, S0, keep=False)
+    got = final_states(x, lens, of_s=torch.bfloat16, S0=S0)
+    return [[TERM + rel_l2(got[n, h], ref[n, h]) for h in range(ref.shape[1])] for n in range(len(lens))]
+
+
+def _prefill(x, lens, **kw):
+    cu = [0]
+    for n in lens:
+        cu.append(cu[-1] + n)
+    cu = torch.tensor(cu, dtype=torch.int32)
+    return kda.gdn_chunk_prefill(*x, cu.cuda(), cu, **kw)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("lens,a_mean", STATES)
+def test_states_are_an_fp32_evaluations(lens, a_mean):
+    x = gdn_inputs(sum(lens), 2, 4, seed=len(lens) + sum(lens), a_mean=a_mean)
+    out, final = _prefill(x, lens)
+    ref, _, ref_S = gdn_reference(x, lens, keep=False)
+    assert rel_l2(out, ref) <= OUT
+    bound = state_bound(x, lens)
+    for n in range(len(lens)):
+        for h in range(4):
+            assert rel_l2(final[n, h], ref_S[n, h]) <= bound[n][h], (n, h)

@@ -309,7 +309,7 @@ __global__ void __launch_bounds__(in::kThreads, 4) gdn_intra_kernel(const __grid
         const float bf = static_cast<float>(static_cast<uint32_t>(x)) * 2.3283064365386963e-10f;
         s_bi[2 * lane + e] = bi;
         s_bf[2 * lane + e] = bf;
-        s_up[2 * lane + e] = fast_exp2(-(bi + bf));
+        s_up[2 * lane + e] = fast_exp2(-bi) * fast_exp2(-bf);   // (their sum would lose bits of bf)
       }
     }
     if (gh == 0) {
@@ -352,7 +352,7 @@ __global__ void __launch_bounds__(in::kThreads, 4) gdn_intra_kernel(const __grid
       const float bi = s_bi[r], bf = s_bf[r];
       const float rowf = is_p ? s_norm[64 + r] : s_beta[r] * s_norm[r];
       const bool factors = s_bi[63] > -kFactorRange;   // (b falls along the chunk)
-      const float down = rowf * fast_exp2(bi + bf);
+      const float down = rowf * (fast_exp2(bi) * fast_exp2(bf));
       if ((q4 & 1) >= ib) {   // (rows 0..31, columns 32..63 lie above the diagonal)
         const int lim = r < valid ? r - 32 * ib + (is_p ? 1 : 0) : 0;   // kept: i < r (A), i <= r (P)
         const bool masked = __any_sync(0xffffffffu, lim < 32);   // (not below the diagonal in a full chunk)

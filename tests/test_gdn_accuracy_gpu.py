@@ -42,3 +42,31 @@ def test_states_are_an_fp32_evaluations(lens, a_mean):
     for n in range(len(lens)):
         for h in range(4):
             assert rel_l2(final[n, h], ref_S[n, h]) <= bound[n][h], (n, h)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("tokens", [2, 64])
+def test_weak_decays_behind_a_strong_one(tokens):
+    # A chunk's decays sum to 2^-45 or so after its first token, where an fp32 sum is good to 2^-19 and no more; the pairs
+    # behind it differ by 2^-14 to 2^-3.  Equal keys and values, beta next to 1: a token's u is v minus what the state
+    # holds already, so an error of A's entries is one of the state.
+    # Two tokens: s = e^lambda u_0 + u_1 with u_1 = beta (v - e^lambda s_0), and s is v.  A's entry has two exponentials, the
+    # first term one; beta and the norms (2^-23 each), the pairs of fp16 (2^-23 each) and the sums are not more than three
+    # errors of 2^-22 besides.  Six errors of at most 2^-22 that do not know of each other have a root mean square of at most
+    # (6 / 3)^(1/2) 2^-22 over many heads, below 2 x 2^-22.  With more tokens every u is such a difference, and they add up.
+    hv = 64
+    x = gdn_inputs(64, 1, hv, seed=5)
+    for i in (0, 1, 2):
+        x[i] = x[i][:1].expand_as(x[i])
+    x[4].fill_(8.0)
+    x[3][1:] = -3.0
+    x[3][0] = (45 * 0.6931 / torch.exp(x[5]) - x[6]).bfloat16()
+    x = [t[:tokens].contiguous() if i < 5 else t for i, t in enumerate(x)]
+    # (padded by a sequence that is long enough for chunks)
+    more = gdn_inputs(20, 1, hv, seed=6)
+    x = [torch.cat([t, m]) if i < 5 else t for i, (t, m) in enumerate(zip(x, more))]
+    out, final = _prefill(x, [tokens, 20])
+    ref, _, ref_S = gdn_reference(x, [tokens, 20], keep=False)
+    assert rel_l2(out, ref) <= OUT
+    rms = (sum(rel_l2(final[0, h], ref_S[0, h]) ** 2 for h in range(hv)) / hv) ** 0.5
+    assert rms <= tokens * 2.0 ** -22, rms

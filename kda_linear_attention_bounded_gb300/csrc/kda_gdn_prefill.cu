@@ -763,7 +763,7 @@ __global__ void __launch_bounds__(ch::kThreads, 1) gdn_chain_kernel(const __grid
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const float vm = i & 1 ? __uint_as_float(top[i >> 1] & 0xFFFF0000u) : __uint_as_float(top[i >> 1] << 16);
-          bound[i] = fmaf(gamma, bound[i], 8.f * last[i]);
+          bound[i] = fminf(fmaf(gamma, bound[i], 8.f * last[i]), 3.4e38f);   // (an infinite one would never fall again)
           last[i] = vm;
           const float most = fmaf(9.f, vm, bound[i]);
           // (kept until it is too large, or 2^10 too small)

@@ -70,3 +70,26 @@ def test_weak_decays_behind_a_strong_one(tokens):
     assert rel_l2(out, ref) <= OUT
     rms = (sum(rel_l2(final[0, h], ref_S[0, h]) ** 2 for h in range(hv)) / hv) ** 0.5
     assert rms <= tokens * 2.0 ** -22, rms
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("initial", [False, True])
+def test_values_next_to_the_largest_fade(initial):
+    # a channel's value of 10^38 (or an entering state whose 1-norm passes fp32) decays by 2^-64 a chunk: four chunks later it
+    # is nothing, and the channel is as accurate as any
+    lens = [500]
+    x = gdn_inputs(500, 1, 2, seed=6)
+    x[3][:] = ((torch.log(torch.expm1(torch.tensor(0.6931, device="cuda") / torch.exp(x[5]))) - x[6])[None]).bfloat16()
+    kw, S0 = {}, None
+    if initial:
+        S0 = torch.full((1, 2, D, D), 0.01, device="cuda")
+        S0[..., 5] = 1e37
+        kw = dict(state_pool=S0, slot_ids=torch.zeros(1, dtype=torch.int32, device="cuda"), load_initial=True)
+    else:
+        x[2][:20, :, 5] = 1e38
+    out, final = _prefill(x, lens, **kw)
+    ref, _, ref_S = gdn_reference(x, lens, S0, keep=False)
+    for h in range(2):
+        assert rel_l2(out[320:, h, 5], ref[320:, h, 5]) <= OUT
+        assert rel_l2(final[0, h, :, 5], ref_S[0, h, :, 5]) <= TERM
+        assert rel_l2(final[0, h], ref_S[0, h]) <= TERM

@@ -41,8 +41,12 @@ constexpr int kC = 64;
 constexpr uint32_t kBlkP = 8192, kBlkL2 = 16384, kBlkVec = 24576;
 constexpr uint32_t kGdnBlkBytes = 26112;
 // factors (fp32): beta_i | -beta_i e^(b_i) |k_i|^-1 | scale e^(b_r) |q_r|^-1 | 2^-x_i | 2^(x_i) e^(b_63 - b_i) |k_i|^-1 |
-// e^(b_63), with 2^(x_i) the raw key's norm or up to twice that
-constexpr int kVecB = 0, kVecK = 64, kVecQ = 128, kVecX = 192, kVecS = 256, kVecGamma = 320;
+// e^(b_63), with 2^(x_i) the raw key's norm or up to twice that | which rows are taken times kRowScale (k, q: 64 bits each)
+constexpr int kVecB = 0, kVecK = 64, kVecQ = 128, kVecX = 192, kVecS = 256, kVecGamma = 320, kVecLong = 324;
+static_assert(kBlkVec + 4 * (kVecLong + 4) <= kGdnBlkBytes && (kBlkVec + 4 * kVecLong) % 16 == 0, "block map");
+// Keys and queries meet as they are, and products of rows with squares below kRowMost stay inside fp32.  Longer rows (finite
+// in bf16 all the same) are taken times a power of two, exactly, wherever they are loaded: their norm takes it back.
+constexpr float kRowMost = 1e38f, kRowScale = 8.271806125530277e-25f /* 2^-80 */;
 constexpr int kGdnMaxSeqs = 1024;   // sequences per launch (longer batches are split on the host)
 
 // A state pass is serial in a sequence's chunks, so few long sequences leave most of the GPU idle.  They are cut into
@@ -133,6 +137,17 @@ __device__ __forceinline__ void split2(float2 x, uint32_t &p1, uint32_t &p2) {
   p2 = pack_bf16x2(r.x, r.y);
 }
 
+// 16 bytes of a row, times kRowScale
+__device__ __forceinline__ void scale_piece(uint8_t *at) {
+  uint4 w = *reinterpret_cast<const uint4 *>(at);
+  const float2 f = make_float2(kRowScale, kRowScale);
+  w.x = pack2(mul2(unpack_bf16x2(w.x), f));
+  w.y = pack2(mul2(unpack_bf16x2(w.y), f));
+  w.z = pack2(mul2(unpack_bf16x2(w.z), f));
+  w.w = pack2(mul2(unpack_bf16x2(w.w), f));
+  *reinterpret_cast<uint4 *>(at) = w;
+}
+
 // ================================================================ intra-chunk kernel
 namespace in {
 constexpr int kThreads = 256;   // 8 warps; four CTAs per SM
@@ -143,10 +158,11 @@ constexpr uint32_t OFF_BLK = 17408;      // the block's image
 constexpr uint32_t OFF_SMALL = OFF_BLK + kGdnBlkBytes;
 constexpr uint32_t SM_NORM = 0 /* [128]: 1 / |k_r|, 1 / |q_r| */, SM_BETA = 512, SM_BI = 768, SM_BF = 1024 /* b, whole and
                    fractional part */, SM_UP = 1280 /* 2^-b */, SM_POW = 1536 /* 2^-x */, SM_BAR = 1792, SM_TMEM = 1808, SM_ABORT = 1812,
-                   SM_END = 1824;
+                   SM_LONG = 1824 /* a bit a row of [k ; q]: its squares pass kRowMost */, SM_END = 1840;
 constexpr uint32_t kSmemBytes = OFF_SMALL + SM_END + 1024;
 static_assert(OFF_BLK == 64 * kStride * 4 && OFF_BLK % 1024 == 0 && OFF_SMALL >= 32768, "shared memory map");
-static_assert(SM_POW + 256 <= SM_BAR && SM_BAR + 2 * 8 <= SM_TMEM && SM_TMEM + 4 <= SM_ABORT && SM_ABORT + 4 <= SM_END,
+static_assert(SM_POW + 256 <= SM_BAR && SM_BAR + 2 * 8 <= SM_TMEM && SM_TMEM + 4 <= SM_ABORT && SM_ABORT + 4 <= SM_LONG &&
+                  SM_LONG + 16 <= SM_END,
               "small part of the shared memory map");
 static_assert(4 * (kSmemBytes + 1024) <= 233472, "four CTAs per SM");
 constexpr uint32_t kTmemCols = 128;
@@ -221,6 +237,7 @@ __global__ void __launch_bounds__(in::kThreads, 4) gdn_intra_kernel(const __grid
   uint64_t *bar_mma = bar_in + 1;
   uint32_t *s_tmem = reinterpret_cast<uint32_t *>(small + SM_TMEM);
   volatile uint32_t *s_abort = reinterpret_cast<volatile uint32_t *>(small + SM_ABORT);
+  uint32_t *s_long = reinterpret_cast<uint32_t *>(small + SM_LONG);
   uint8_t *s_blk = sm + OFF_BLK;
   float *sA = reinterpret_cast<float *>(sm + OFF_A);
 
@@ -238,17 +255,20 @@ __global__ void __launch_bounds__(in::kThreads, 4) gdn_intra_kernel(const __grid
   const int valid = min(kC, prm.cu[n + 1] - tok0);
   if (valid <= 0) return;   // a slot between two sequences
 
-  if (tid == 0) {
-    mbar_init(bar_in, 1);
-    mbar_init(bar_mma, 1);
-    *s_abort = 0;
-    fence_mbar_init();
+  const auto fetch = [&] {
     mbar_arrive_expect_tx(bar_in, 32768);
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
       tma_load_3d(sm + OFF_KQ + 16384 * x, &prm.tk, 64 * x, hk, tok0, bar_in);
       tma_load_3d(sm + OFF_KQ + 16384 * x + 8192, &prm.tq, 64 * x, hk, tok0, bar_in);
     }
+  };
+  if (tid == 0) {
+    mbar_init(bar_in, 1);
+    mbar_init(bar_mma, 1);
+    *s_abort = 0;
+    fence_mbar_init();
+    fetch();
   }
   if (warp == 1) {
     tmem_alloc(s_tmem, kTmemCols);
@@ -260,17 +280,59 @@ __global__ void __launch_bounds__(in::kThreads, 4) gdn_intra_kernel(const __grid
   const uint32_t tmem = *s_tmem;
 
   // ---- [k ; q] [k ; q]^T: rows 0..63 k.k, rows 64..127 q.k; its diagonal holds the squared norms
-  if (tid == 0) {
-    wait_or_abort(bar_in, 0, s_abort, prm.status);
+  const auto multiply = [&] {
     const uint64_t kq = desc_kmajor_base(smem_u32(sm + OFF_KQ));
     const uint32_t id = idesc_bf16(128, 128, false, false);
 #pragma unroll
     for (int s = 0; s < 8; ++s) mma_bf16(tmem, kq + kmajor_step(128, s), kq + kmajor_step(128, s), id, s > 0);
     mma_commit(bar_mma);
+  };
+  if (tid == 0) {
+    wait_or_abort(bar_in, 0, s_abort, prm.status);
+    multiply();
   }
   __syncwarp();
   const int q4 = warp & 3, ib = warp >> 2;   // TMEM lane quadrant, half of the 64 key columns
   const uint32_t lanes = tmem + (static_cast<uint32_t>(q4 * 32) << 16);
+
+  // ---- the rows' norms (again: once long rows have been scaled), and what stays zero in the blocks
+  const auto norms = [&](bool again) {
+    wait_or_abort(bar_mma, again, s_abort, prm.status);
+    tc_fence_after();
+    if (warp < 4) {   // row 32 q4 + lane: its diagonal entry
+      uint32_t v[32];
+      tmem_ld16_async(lanes + 32 * q4, v);
+      tmem_ld16_async(lanes + 32 * q4 + 16, v + 16);
+      tmem_wait_ld();
+      tmem_tie<32>(v);
+#pragma unroll
+      for (int half = 16; half > 0; half >>= 1) {   // entry `lane`: a bit of it at a time
+        const bool up = lane & half;
+#pragma unroll
+        for (int e = 0; e < half; ++e) v[e] = up ? v[e + half] : v[e];
+      }
+      const float d = __uint_as_float(v[0]);
+      const int r = 32 * q4 + lane;
+      const bool in = (r & 63) < valid;
+      // (a row that has been scaled leaves the 1e-6 far below its squares)
+      s_norm[r] = in ? rsqrtf(again && s_long[q4] >> lane & 1 ? d : d + kL2Eps) : 0.f;
+      // a power of two that brings the raw key's norm to (1/2, 1] (a zero key: any)
+      if (r < 64) s_pow[r] = in ? __uint_as_float(__float_as_uint(rsqrtf(fmaxf(d, 1e-36f))) & 0x7F800000u) : 1.f;
+      if (!again) {
+        const uint32_t mine = __ballot_sync(0xffffffffu, in && !(d <= kRowMost));
+        if (lane == 0) s_long[q4] = mine;
+      }
+    } else {
+      // zeros above the diagonal of L's parts and of P (the value heads of the group leave them): 6 blocks x 16
+      // rows x two 16-byte pieces of each
+      for (int x = tid - 128; x < 3 * 192; x += 128) {
+        const int which = x / 192, y = x % 192, b6 = y >> 5, rr = (y >> 1) & 15, hc = y & 1;
+        const int I = b6 < 3 ? 0 : b6 < 5 ? 1 : 2;
+        const int J = b6 < 3 ? b6 + 1 : b6 < 5 ? b6 - 1 : 3;
+        *reinterpret_cast<uint4 *>(s_blk + 8192 * which + swz_offset(64, 16 * I + rr, 16 * J + 8 * hc)) = make_uint4(0, 0, 0, 0);
+      }
+    }
+  };
 
   for (int gh = 0; gh < prm.group; ++gh) {
     const int h = hk * prm.group + gh;
@@ -312,38 +374,31 @@ __global__ void __launch_bounds__(in::kThreads, 4) gdn_intra_kernel(const __grid
         s_up[2 * lane + e] = fast_exp2(-bi) * fast_exp2(-bf);   // (their sum would lose bits of bf)
       }
     }
+    if (gh == 0) norms(false);
+    __syncthreads();
     if (gh == 0) {
-      wait_or_abort(bar_mma, 0, s_abort, prm.status);
-      tc_fence_after();
-      if (warp < 4) {   // row 32 q4 + lane: its diagonal entry
-        uint32_t v[32];
-        tmem_ld16_async(lanes + 32 * q4, v);
-        tmem_ld16_async(lanes + 32 * q4 + 16, v + 16);
-        tmem_wait_ld();
-        tmem_tie<32>(v);
-#pragma unroll
-        for (int half = 16; half > 0; half >>= 1) {   // entry `lane`: a bit of it at a time
-          const bool up = lane & half;
-#pragma unroll
-          for (int e = 0; e < half; ++e) v[e] = up ? v[e + half] : v[e];
+      const uint4 rows4 = *reinterpret_cast<const uint4 *>(s_long);
+      if (rows4.x | rows4.y | rows4.z | rows4.w) {   // the tiles once more (the zeros are over them), long rows scaled
+        fence_async_smem();
+        tc_fence_before();
+        __syncthreads();
+        if (tid == 0) fetch();
+        __syncwarp();
+        wait_or_abort(bar_in, 1, s_abort, prm.status);
+        const int r = tid >> 1;
+        if (s_long[r >> 5] >> (r & 31) & 1)
+          for (int c = 0; c < 64; c += 8) scale_piece(sm + OFF_KQ + swz_offset(128, r, 64 * (tid & 1) + c));
+        fence_async_smem();
+        __syncthreads();
+        if (tid == 0) {
+          tc_fence_after();
+          multiply();
         }
-        const float d = __uint_as_float(v[0]);
-        const int r = 32 * q4 + lane;
-        s_norm[r] = (r & 63) < valid ? rsqrtf(d + kL2Eps) : 0.f;
-        // a power of two that brings the raw key's norm to (1/2, 1] (a zero key: any)
-        if (r < 64) s_pow[r] = r < valid ? __uint_as_float(__float_as_uint(rsqrtf(fmaxf(d, 1e-36f))) & 0x7F800000u) : 1.f;
-      } else {
-        // zeros above the diagonal of L's parts and of P (the value heads of the group leave them): 6 blocks x 16
-        // rows x two 16-byte pieces of each
-        for (int x = tid - 128; x < 3 * 192; x += 128) {
-          const int which = x / 192, y = x % 192, b6 = y >> 5, rr = (y >> 1) & 15, hc = y & 1;
-          const int I = b6 < 3 ? 0 : b6 < 5 ? 1 : 2;
-          const int J = b6 < 3 ? b6 + 1 : b6 < 5 ? b6 - 1 : 3;
-          *reinterpret_cast<uint4 *>(s_blk + 8192 * which + swz_offset(64, 16 * I + rr, 16 * J + 8 * hc)) = make_uint4(0, 0, 0, 0);
-        }
+        __syncwarp();
+        norms(true);
+        __syncthreads();
       }
     }
-    __syncthreads();
 
     // ---- A (fp32) and P (fp16) from TMEM; the block's factors
     {
@@ -407,6 +462,7 @@ __global__ void __launch_bounds__(in::kThreads, 4) gdn_intra_kernel(const __grid
             vec[kVecX + t] = s_pow[t];
             vec[kVecS + t] = s_norm[t] / s_pow[t] * fast_exp2((s_bi[63] - s_bi[t]) + (s_bf[63] - s_bf[t]));
             if (t == 63) vec[kVecGamma] = eb;
+            if (t < 4) reinterpret_cast<uint32_t *>(vec)[kVecLong + t] = s_long[t];
           }
         }
       }
@@ -518,8 +574,8 @@ constexpr uint32_t OFF_OUT = OFF_K16 + 16384;     // output on its way out (64 r
 constexpr uint32_t OFF_SMALL = OFF_OUT + 16384;
 constexpr uint32_t SM_BAR = 0 /* the barriers below */, SM_TMEM = 144, SM_ABORT = 148, SM_SIG = 256 /* [2][128] */, SM_INV = 1280 /* [2][128] */, SM_END = 2304;
 // mbarriers: landed in stage 0, 1: all but v, v (which goes first, for the scales); scales of even, odd chunks; products done (first, second, state's, v's, output's); output
-// tile free | the workers' warps: S, R, U' in place, stage done with, output in its tile
-enum { B_FULL = 0, B_VAL = 2, B_SCALE = 4, B_M1 = 6, B_M2, B_M3, B_V, B_O, B_OUT, B_S, B_R, B_U, B_FREE, B_TILE, kBarriers };
+// tile free; long rows scaled (both issuing warps) | the workers' warps: S, R, U' in place, stage done with, output in its tile
+enum { B_FULL = 0, B_VAL = 2, B_SCALE = 4, B_M1 = 6, B_M2, B_M3, B_V, B_O, B_OUT, B_LONG, B_S, B_R, B_U, B_FREE, B_TILE, kBarriers };
 constexpr uint32_t kSmemBytes = OFF_SMALL + SM_END + 1024;
 static_assert(kSmemBytes <= 232448 && kStage >= kStageLoad && kStage % 1024 == 0, "shared memory map");
 static_assert(SM_BAR + 8 * kBarriers <= SM_TMEM && SM_TMEM + 4 <= SM_ABORT && SM_ABORT + 4 <= SM_SIG &&
@@ -621,7 +677,7 @@ __global__ void __launch_bounds__(ch::kThreads, 1) gdn_chain_kernel(const __grid
   }
   if (nchunks > 0) {
     if (tid == 0) {
-      for (int i = 0; i < kBarriers; ++i) mbar_init(&bar[i], i >= B_S ? 16 : i == B_M1 || i == B_M2 ? 2 : 1);   // (two issuers)
+      for (int i = 0; i < kBarriers; ++i) mbar_init(&bar[i], i >= B_S ? 16 : i == B_M1 || i == B_M2 || i == B_LONG ? 2 : 1);   // (two issuers)
       *s_abort = 0;
       fence_mbar_init();
     }
@@ -783,6 +839,7 @@ __global__ void __launch_bounds__(ch::kThreads, 1) gdn_chain_kernel(const __grid
       constexpr uint32_t id1 = idesc_bf16(128, 64, false, false), id2 = idesc_f16(128, 64, false, false),
                          id3 = idesc_f16(128, 128, false, true), idv = idesc_bf16(128, 64, true, false);
       const uint64_t one = desc_kmajor_base(smem_u32(sm + OFF_ONE)), k16 = desc_mnmajor_base(smem_u32(sm + OFF_K16), 64);
+      uint32_t longs = 0;   // chunks with long rows so far
       const uint32_t ku = tmem + TM_KU + 64 * me, uu = tmem + TM_U + 64 * me, sp = tmem + TM_S + 64 * me;
       for (int c = 0; c < nchunks; ++c) {
         uint8_t *st = sm + (c & 1) * kStage;
@@ -804,6 +861,18 @@ __global__ void __launch_bounds__(ch::kThreads, 1) gdn_chain_kernel(const __grid
         }
         wait_or_abort(&bar[B_VAL + (c & 1)], (c >> 1) & 1, s_abort, prm.status);
         wait_or_abort(&bar[B_FULL + (c & 1)], (c >> 1) & 1, s_abort, prm.status);
+        {   // long rows, scaled as they were for the block (this warp's: keys or queries; both warps' products read both)
+          const uint32_t *rows = reinterpret_cast<const uint32_t *>(st + ST_BLK + kBlkVec) + kVecLong;
+          const uint4 rows4 = *reinterpret_cast<const uint4 *>(rows);
+          if (rows4.x | rows4.y | rows4.z | rows4.w) {
+            for (int half = 0; half < 2; ++half)
+              if (rows[2 * me + half] >> lane & 1)
+                for (int ch = 0; ch < kD; ch += 8) scale_piece(st + swz_offset(128, 64 * me + 32 * half + lane, ch));
+            fence_async_smem();
+            warp_arrive(&bar[B_LONG]);
+            wait_or_abort(&bar[B_LONG], longs++ & 1, s_abort, prm.status);
+          }
+        }
         wait_or_abort(&bar[B_S], c & 1, s_abort, prm.status);   // S is in place, D has been read
         tc_fence_after();
         if (lane == 0) {

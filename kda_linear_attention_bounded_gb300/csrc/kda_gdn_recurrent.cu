@@ -23,6 +23,19 @@ constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
 constexpr int kTile = kWarps;   // tokens prepared per prologue pass (one per warp)
 
+// A warp's row over its norm.  Where the squares pass fp32 they are taken of the row times 2^-80 (and the 1e-6 is nothing).
+__device__ __forceinline__ float4 unit_row(float4 x) {
+  float sq = warp_sum(x.x * x.x + x.y * x.y + x.z * x.z + x.w * x.w), eps = kL2Eps;
+  if (sq == INFINITY) {
+    constexpr float f = 8.271806125530277e-25f;
+    x = make_float4(f * x.x, f * x.y, f * x.z, f * x.w);
+    sq = warp_sum(x.x * x.x + x.y * x.y + x.z * x.z + x.w * x.w);
+    eps = 0.f;
+  }
+  const float n = rsqrtf(sq + eps);
+  return make_float4(x.x * n, x.y * n, x.z * n, x.w * n);
+}
+
 template <int kP>
 __global__ void __launch_bounds__(kThreads, 8) gdn_recurrent_kernel(GdnRecurrentArgs p) {
   constexpr int kCols = kD / kP;              // value channels of the CTA
@@ -77,11 +90,7 @@ __global__ void __launch_bounds__(kThreads, 8) gdn_recurrent_kernel(GdnRecurrent
       const float2 k01 = unpack_bf16x2(kr.x), k23 = unpack_bf16x2(kr.y);
       const uint16_t *vp = p.v + t * p.v_stride + h * kD + part * kCols;
       for (int c = lane; c < kCols; c += 32) s_v[warp][c] = bf16_bits_to_f32(vp[c]);
-      const float qq = warp_sum(q01.x * q01.x + q01.y * q01.y + q23.x * q23.x + q23.y * q23.y);
-      const float kk = warp_sum(k01.x * k01.x + k01.y * k01.y + k23.x * k23.x + k23.y * k23.y);
-      const float nq = rsqrtf(qq + kL2Eps), nk = rsqrtf(kk + kL2Eps);
-      const float4 qh = make_float4(q01.x * nq, q01.y * nq, q23.x * nq, q23.y * nq);
-      const float4 kh = make_float4(k01.x * nk, k01.y * nk, k23.x * nk, k23.y * nk);
+      const float4 qh = unit_row(make_float4(q01.x, q01.y, q23.x, q23.y)), kh = unit_row(make_float4(k01.x, k01.y, k23.x, k23.y));
       const float kq = warp_sum(qh.x * kh.x + qh.y * kh.y + qh.z * kh.z + qh.w * kh.w);
       *reinterpret_cast<float4 *>(&s_q[warp][lane * 4]) = qh;
       *reinterpret_cast<float4 *>(&s_k[warp][lane * 4]) = kh;

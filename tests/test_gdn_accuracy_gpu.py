@@ -93,3 +93,59 @@ def test_values_next_to_the_largest_fade(initial):
         assert rel_l2(out[320:, h, 5], ref[320:, h, 5]) <= OUT
         assert rel_l2(final[0, h, :, 5], ref_S[0, h, :, 5]) <= TERM
         assert rel_l2(final[0, h], ref_S[0, h]) <= TERM
+
+
+def _huge_rows(x, tokens):
+    """Some keys and queries so long that their squares pass fp32 (and products with others, too)."""
+    for i, (first, step) in ((0, (1, 5)), (1, (0, 4))):
+        size = torch.ones((tokens, 1, 1), device="cuda")
+        size[first::step] = 1e20
+        size[first + 2::2 * step] = 1e30
+        size[first + 3::3 * step] = 1e-18
+        x[i] = (x[i].float() * size).bfloat16()
+    x[1][2, 0] = 0.0
+    x[1][2, 0, 7] = 3.3e38
+    return x
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("lens", [[200], [64], [9, 10], [9, 11], [70, 0, 3, 64, 1], [1100]])
+@pytest.mark.parametrize("hk,hv", [(1, 2), (2, 2)])
+def test_keys_whose_squares_pass_fp32(lens, hk, hv):
+    x = _huge_rows(gdn_inputs(sum(lens), hk, hv, seed=8, a_mean=-4.0), sum(lens))
+    out, final = _prefill(x, lens)
+    ref, _, ref_S = gdn_reference(x, lens, keep=False)
+    assert rel_l2(out, ref) <= OUT
+    bound = state_bound(x, lens)
+    for n in range(len(lens)):
+        for h in range(hv):
+            assert rel_l2(final[n, h], ref_S[n, h]) <= bound[n][h], (n, h)
+
+
+@pytest.mark.gpu
+def test_keys_whose_squares_pass_fp32_token_by_token():
+    B, T, hv = 3, 4, 2
+    x = _huge_rows(gdn_inputs(B * T, 1, hv, seed=9), B * T)
+    g = torch.Generator().manual_seed(10)
+    pool = (0.05 * torch.randn((B, hv, D, D), generator=g)).cuda()
+    slots = torch.arange(B, dtype=torch.int32, device="cuda")
+    out, inter = kda.gdn_recurrent_verify(*x, pool, slots, T)
+    ref, steps, _ = gdn_reference(x, [T] * B, pool)
+    assert rel_l2(out, ref) <= OUT
+    for b in range(B):
+        assert rel_l2(inter[b], steps[b]) <= 150 * 2.0 ** -24
+    first = [t[::T].contiguous() if t.shape[0] == B * T else t for t in x]
+    out1 = kda.gdn_decode(*first, pool, slots)
+    assert torch.equal(out1, out[::T]) and torch.equal(pool, inter[:, 0])
+
+
+@pytest.mark.gpu
+def test_infinite_keys_still_spread():
+    # an infinity among the keys is no number's norm: its chunk and what is behind it, in its own sequence, as it says
+    lens = [100, 70]
+    x = gdn_inputs(170, 1, 2, seed=11)
+    clean = _prefill(x, lens)
+    x[1][80, 0, 3] = float("inf")
+    out, final = _prefill(x, lens)
+    assert torch.equal(out[:64], clean[0][:64]) and torch.equal(out[100:], clean[0][100:])
+    assert torch.isnan(out[80:100]).all() and torch.isnan(final[0]).all() and torch.equal(final[1], clean[1][1])

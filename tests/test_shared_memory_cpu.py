@@ -41,7 +41,7 @@ CASES = {
     # source, where the map stands, what it holds (name of the offset: bytes), and its end
     "gated delta rule, intra-chunk": ("kda_gdn_prefill.cu", "namespace in {", "SM_END", {
         "SM_NORM": 128 * F32, "SM_BETA": 64 * F32, "SM_BI": 64 * F32, "SM_BF": 64 * F32, "SM_UP": 64 * F32,
-        "SM_POW": 64 * F32, "SM_BAR": 2 * 8, "SM_TMEM": 4, "SM_ABORT": 4}),
+        "SM_POW": 64 * F32, "SM_BAR": 2 * 8, "SM_TMEM": 4, "SM_ABORT": 4, "SM_LONG": 16}),
     "gated delta rule, state pass": ("kda_gdn_prefill.cu", "namespace ch {", "SM_END", {
         "SM_BAR": "8 * kBarriers", "SM_TMEM": 4, "SM_ABORT": 4, "SM_SIG": 2 * 128 * F32, "SM_INV": 2 * 128 * F32}),
     "gated delta rule, state pass, tiles": ("kda_gdn_prefill.cu", "namespace ch {", "kSmemBytes", {

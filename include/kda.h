@@ -556,6 +556,10 @@ KDA_API int kda_paged_attention(const uint16_t *q, int64_t q_token_stride, const
  *  slot_map      [max_tokens] int64: page id * page_size + position % page_size
  * Rows behind the last request's (a captured bucket's padding) get position 0
  * and slot -1.
+ * What is written may overlap neither an input nor each other
+ * (KDA_ERR_INVALID_ARG), except that kv_lens may be seq_lens itself: the lengths
+ * move forward in place, for the next step (by one CTA, so large steps take
+ * longer).
  *
  * Device-side findings, each in the status word: a negative length, or lengths
  * whose sum passes 2^31 - 1, counts as no new tokens (KDA_DEVICE_BAD_COUNT); new tokens beyond max_tokens

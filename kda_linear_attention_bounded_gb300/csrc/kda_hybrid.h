@@ -103,6 +103,7 @@ struct StepTablesArgs {
   int64_t max_tokens;
   int32_t *cu_seqlens, *kv_lens, *positions, *pages_used;
   int64_t *slot_map;
+  int one_cta;               // kv_lens is seq_lens: no second CTA may read it
   uint32_t *status;
 };
 

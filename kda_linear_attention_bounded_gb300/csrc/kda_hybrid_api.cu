@@ -5,6 +5,7 @@
 #include <climits>
 #include <cmath>
 #include <cstdint>
+#include <iterator>
 
 #include "kda_checks.h"
 #include "kda_common.cuh"
@@ -43,6 +44,16 @@ int check_gdn(int64_t tokens, const uint16_t *q, const uint16_t *k, int64_t qk_s
   a->out = out;
   return KDA_OK;
 }
+
+// A piece of memory (bytes; of none, nothing meets it).
+struct Span {
+  const void *at;
+  int64_t bytes;
+  bool meets(const Span &o) const {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(at), b = reinterpret_cast<uintptr_t>(o.at);
+    return bytes > 0 && o.bytes > 0 && a < b + static_cast<uintptr_t>(o.bytes) && b < a + static_cast<uintptr_t>(bytes);
+  }
+};
 
 // Batches whose sequences have so many tokens at most take the recurrence token by token.  Measured, chunks against
 // tokens: 1 sequence x 2 heads of 8 tokens 11.1 and 6.7 us, of 12 11.1 and 9.0; 64 x 16 heads of 8 66 and 52 us, of 12 68 and 75.
@@ -217,7 +228,22 @@ int kda_step_tables(int32_t *block_table, int64_t table_row_stride, int table_wi
                         static_cast<const void *>(positions), static_cast<const void *>(pages_used)})
     if (!aligned_to(p, 4)) return KDA_ERR_INVALID_ARG;
   if (!aligned_to(slot_map, 8)) return KDA_ERR_INVALID_ARG;
+  // What is written lies apart from all else: every CTA reads the inputs for itself, at its own time.  The lengths may be
+  // brought forward in place (kv_lens is seq_lens): one CTA then takes the call.
+  const bool in_place = B > 0 && kv_lens == seq_lens;
+  const auto ints = [](const int32_t *at, int64_t n) { return Span{at, n * 4}; };
+  const Span inputs[] = {in_place ? Span{nullptr, 0} : ints(seq_lens, B), ints(new_lens, B), ints(free_pages, num_free)};
+  const Span written[] = {ints(block_table, B > 0 && table_width > 0 ? (B - 1) * table_row_stride + table_width : 0),
+                          ints(cu_seqlens, static_cast<int64_t>(B) + 1), ints(kv_lens, B), ints(positions, max_tokens),
+                          Span{slot_map, max_tokens * 8}, ints(pages_used, 1)};
+  for (size_t i = 0; i < std::size(written); ++i) {
+    for (const Span &x : inputs)
+      if (written[i].meets(x)) return KDA_ERR_INVALID_ARG;
+    for (size_t j = 0; j < i; ++j)
+      if (written[i].meets(written[j])) return KDA_ERR_INVALID_ARG;
+  }
   kda::StepTablesArgs t{};
+  t.one_cta = in_place;
   t.table = block_table;
   t.table_stride = table_row_stride;
   t.width = table_width;

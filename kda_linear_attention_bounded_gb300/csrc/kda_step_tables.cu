@@ -9,7 +9,8 @@
 // in windows of one request per thread, instead of waiting for a scan kernel: it then takes its share of the rows
 // and of the new pages of the window, both found by binary search in the window's sums, so that one long prompt
 // spreads over the grid as evenly as many short ones.  A token of a page handed out in this call reads the page id
-// from the free list, never from the table, so no CTA waits for another's table writes.
+// from the free list, never from the table, so no CTA waits for another's table writes.  The lengths in place (kv_lens is
+// seq_lens) are one CTA's work: each is read once, by the thread that then writes it.
 #include "kda_hybrid.cuh"
 
 namespace kda {
@@ -157,7 +158,7 @@ cudaError_t launch_step_tables(const StepTablesArgs &a, cudaStream_t stream) {
   // a window holds the whole batch where it can (512 requests: 6.0 us with 512 threads, 7.8 with 1024)
   const int threads = a.B <= 256 ? 256 : a.B <= 512 ? 512 : 1024;
   const int64_t want = (a.max_tokens + threads - 1) / threads;
-  const unsigned grid = static_cast<unsigned>(want < 1 ? 1 : want > 608 ? 608 : want);
+  const unsigned grid = static_cast<unsigned>(want < 1 || a.one_cta ? 1 : want > 608 ? 608 : want);
   const auto kernel = threads == 256 ? step_tables_kernel<256> : threads == 512 ? step_tables_kernel<512> : step_tables_kernel<1024>;
   return launch_dependent(kernel, grid, threads, 0, stream, a);
 }

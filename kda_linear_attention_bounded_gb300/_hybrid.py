@@ -9,6 +9,7 @@ from __future__ import annotations
 import ctypes
 import importlib.machinery
 import importlib.util
+import operator
 import os
 
 import torch
@@ -109,7 +110,7 @@ def gdn_recurrent_verify(q, k, v, a, beta_logits, A_log, dt_bias, state_pool, sl
         if out is None:
             out = _rows_like(v, "v")
         if intermediate_states is None:
-            intermediate_states = torch.empty((slot_ids.numel(), max(int(T), 0), v.shape[1], 128, 128), dtype=_F32, device=dev)
+            intermediate_states = torch.empty((slot_ids.numel(), max(operator.index(T), 0), v.shape[1], 128, 128), dtype=_F32, device=dev)
         if workspace is None:
             workspace = _new_workspace(dev, stream)
     rc = _ext.gdn_recurrent_verify(q, k, v, a, beta_logits, A_log, dt_bias, scale, state_pool, slot_ids, T, out,
@@ -138,7 +139,7 @@ def gdn_decode(q, k, v, a, beta_logits, A_log, dt_bias, state_pool, slot_ids, *,
 
 def paged_workspace_size(Hq: int, Hk: int, T: int = 1) -> int:
     """Bytes of workspace ``paged_attention`` needs (whatever the batch and the lengths)."""
-    return int(_b.load().kda_paged_workspace_size(int(Hq), int(Hk), int(T)))
+    return int(_b.load().kda_paged_workspace_size(*map(operator.index, (Hq, Hk, T))))
 
 
 def paged_attention(q, k_pages, v_pages, block_table, seq_lens, T=1, *, scale=None, out=None, lse=None,

@@ -49,8 +49,11 @@ int cuda_device(const at::Tensor &t, const char *name) {
 bool on(const at::Tensor &t, int dev) { return t.is_cuda() && t.get_device() == dev; }
 
 int64_t integer(PyObject *o, const char *name) {
-  PyObject *i = PyNumber_Long(o);
-  if (!i) throw Refused{};
+  PyObject *i = PyNumber_Index(o);   // (whole numbers alone: not 2.9, not "16")
+  if (!i) {
+    PyErr_Format(PyExc_TypeError, "%s: expected a whole number", name);
+    throw Refused{};
+  }
   const int64_t x = PyLong_AsLongLong(i);
   Py_DECREF(i);
   if (x == -1 && PyErr_Occurred()) {
@@ -239,8 +242,8 @@ PyObject *gdn_chunk_prefill(PyObject *, PyObject *const *x, Py_ssize_t argc) {
 // q, k, v, a, beta_logits, A_log, dt_bias, scale, state_pool, slot_ids, T, out, intermediate_states, workspace, stream
 PyObject *gdn_recurrent_verify(PyObject *, PyObject *const *x, Py_ssize_t argc) {
   return guarded(argc, 15, [&] {
-    const GdnTokens g = gdn_tokens(x, x[7]);
     const int T = int32(x[10], "T");
+    const GdnTokens g = gdn_tokens(x, x[7]);
     const int64_t B = count_of(x[9], "slot_ids");
     if (g.tokens != B * T) refuse("q: " + n(g.tokens) + " tokens for " + n(B) + " requests x " + n(T));
     const Pool pool = pool_of(x[8], g.dev, g.Hv);
@@ -305,9 +308,10 @@ Table table_of(const at::Tensor &t, int dev) {
 // q, k_pages, v_pages, block_table, seq_lens, T, scale, out, lse, workspace, stream
 PyObject *paged_attention(PyObject *, PyObject *const *x, Py_ssize_t argc) {
   return guarded(argc, 11, [&] {
+    const int T = int32(x[5], "T");
+    const float scale = scale_of(x[6]);
     const at::Tensor &q = tensor(x[0], "q");
     const int dev = cuda_device(q, "q");
-    const int T = int32(x[5], "T");
     const int64_t B = count_of(x[4], "seq_lens");
     if (q.dim() != 3) refuse("q: expected a bf16 tensor [B*T, Hq, 128]");
     const int64_t Hq = q.size(1);
@@ -322,7 +326,6 @@ PyObject *paged_attention(PyObject *, PyObject *const *x, Py_ssize_t argc) {
     float *lse = x[8] == Py_None ? nullptr : static_cast<float *>(exact(x[8], "lse", at::kFloat, dev, {B * T, Hq}));
     const Workspace ws = workspace_of(x[9], dev);
     void *stream = stream_of(x[10], dev);
-    const float scale = scale_of(x[6]);
     const int num_pages = int32(kt.size(0), "k_pages"), page = int32(kt.size(1), "k_pages"), Hk = int32(kt.size(2), "k_pages"),
               heads = int32(Hq, "q"), requests = int32(B, "seq_lens");
     return call(dev, [&] {
@@ -337,6 +340,7 @@ PyObject *paged_attention(PyObject *, PyObject *const *x, Py_ssize_t argc) {
 // workspace, stream
 PyObject *step_tables(PyObject *, PyObject *const *x, Py_ssize_t argc) {
   return guarded(argc, 12, [&] {
+    const int page = int32(x[4], "page_size");
     const at::Tensor &t = tensor(x[0], "block_table");
     const int dev = cuda_device(t, "block_table");
     const Table table = table_of(t, dev);
@@ -348,7 +352,7 @@ PyObject *step_tables(PyObject *, PyObject *const *x, Py_ssize_t argc) {
     auto *map = static_cast<int64_t *>(exact(x[8], "slot_map", at::kLong, dev, {rows}));
     int32_t *used = ints(9, "pages_used", 1), *old = ints(1, "seq_lens", B), *fresh = ints(2, "new_lens", B),
             *pages = ints(3, "free_pages", free);
-    const int page = int32(x[4], "page_size"), num_free = int32(free, "free_pages");
+    const int num_free = int32(free, "free_pages");
     const Workspace ws = workspace_of(x[10], dev);
     void *stream = stream_of(x[11], dev);
     return call(dev, [&] {

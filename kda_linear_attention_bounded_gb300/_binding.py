@@ -230,12 +230,23 @@ def _stream_ptr(stream, device):
     return stream.cuda_stream
 
 
+def _empty(shape, dtype, device, stream):
+    """A new tensor for a call on ``stream``.  On a given stream its memory is that stream's: the current one may still be
+    at work on what has been given back to it.  (The caller reads it on the current stream, later.)"""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        x = torch.empty(shape, dtype=dtype, device=device)
+    x.record_stream(torch.cuda.current_stream(x.device))
+    return x
+
+
 def make_workspace(device=None, stream=None, nbytes=None) -> torch.Tensor:
     """Allocate (through torch) and clear a workspace for the calls: at least
     ``workspace_size()`` bytes, or ``nbytes`` if larger (a prefill needs
     ``prefill_workspace_size(...)``)."""
     n = max(workspace_size(), int(nbytes or 0))
-    ws = torch.empty(n, dtype=torch.uint8, device=device or "cuda")
+    ws = _empty(n, torch.uint8, device or "cuda", stream)
     rc = load().kda_workspace_reset(_ptr(ws), ws.numel(), _stream_ptr(stream, ws.device))
     if rc != KDA_OK:
         raise KdaError(rc, "kda_workspace_reset")
@@ -291,10 +302,10 @@ def chunk_prefill(q, k, v, g, beta_logits, A_log, dt_bias, cu_seqlens, cu_seqlen
     T_total = q.shape[0]
     dev = q.device
     if out is None:
-        out = torch.empty((T_total, H, 128), dtype=torch.bfloat16, device=dev)
+        out = _empty((T_total, H, 128), torch.bfloat16, dev, stream)
     os_ = _token_tensor(out, "out", H)
     if not final_to_pool and final_state is None:
-        final_state = torch.empty((N, H, 128, 128), dtype=torch.float32, device=dev)
+        final_state = _empty((N, H, 128, 128), torch.float32, dev, stream)
     if workspace is None:
         workspace = make_workspace(dev, stream, prefill_workspace_size(T_total, N, H))
     flags = (KDA_LOAD_INITIAL if load_initial else 0) | (KDA_FINAL_TO_POOL if final_to_pool else 0) | \
@@ -327,10 +338,10 @@ def recurrent_verify(q, k, v, g, beta_logits, A_log, dt_bias, state_pool, slot_i
     B = slot_ids.numel()
     dev = q.device
     if out is None:
-        out = torch.empty((B * T, H, 128), dtype=torch.bfloat16, device=dev)
+        out = _empty((B * T, H, 128), torch.bfloat16, dev, stream)
     os_ = _token_tensor(out, "out", H)
     if intermediate_states is None:
-        intermediate_states = torch.empty((B, T, H, 128, 128), dtype=torch.float32, device=dev)
+        intermediate_states = _empty((B, T, H, 128, 128), torch.float32, dev, stream)
     if workspace is None:
         workspace = make_workspace(dev, stream)
     if scale is None:
@@ -404,14 +415,14 @@ def spec_step(prefill, cu_seqlens, cu_seqlens_host, spec, T, A_log, dt_bias, sta
             raise ValueError("cu_seqlens_host must be in host memory")
         N = cu_host.numel() - 1
         if not final_to_pool and final_state is None:
-            final_state = torch.empty((N, H, 128, 128), dtype=torch.float32, device=dev)
+            final_state = _empty((N, H, 128, 128), torch.float32, dev, stream)
     if spec is not None:
         spc, Bt = _token_struct(spec, H)
         if Bt % T:
             raise ValueError("spec segment: tokens must be a multiple of T")
         B = Bt // T
         if intermediate_states is None:
-            intermediate_states = torch.empty((B, T, H, 128, 128), dtype=torch.float32, device=dev)
+            intermediate_states = _empty((B, T, H, 128, 128), torch.float32, dev, stream)
     for name, idx, n in (("non_spec_token_indx", non_spec_token_indx, Tp), ("spec_token_indx", spec_token_indx, B * T)):
         if n and (idx is None or idx.dtype != torch.int32 or not idx.is_cuda or idx.numel() != n or not idx.is_contiguous()):
             raise ValueError(f"{name}: expected a contiguous CUDA int32 tensor of {n} entries")

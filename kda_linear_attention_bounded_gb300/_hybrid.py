@@ -56,17 +56,14 @@ def _raw(stream, x):
     return stream.cuda_stream
 
 
-def _rows_like(x, name):
+def _rows_like(x, name, stream):
     """A new output for the tokens of x."""
-    return torch.empty(x.shape, dtype=_BF16, device=_cuda(x, name))
+    return _b._empty(x.shape, _BF16, _cuda(x, name), stream)
 
 
 def _new_workspace(dev, stream, nbytes=None):
     with torch.cuda.device(dev):
-        ws = _b.make_workspace(dev, stream, nbytes)
-    if stream is not None:   # (its memory is not handed out again before the call on that stream is done)
-        ws.record_stream(stream)
-    return ws
+        return _b.make_workspace(dev, stream, nbytes)
 
 
 def gdn_prefill_workspace_size(total_tokens: int, num_seqs: int, Hv: int) -> int:
@@ -88,9 +85,9 @@ def gdn_chunk_prefill(q, k, v, a, beta_logits, A_log, dt_bias, cu_seqlens, cu_se
         dev = _cuda(q, "q")
         N, Hv = max(cu.numel() - 1, 0), v.shape[1]
         if out is None:
-            out = _rows_like(v, "v")
+            out = _rows_like(v, "v", stream)
         if final_state is None and not final_to_pool:
-            final_state = torch.empty((N, Hv, 128, 128), dtype=_F32, device=dev)
+            final_state = _b._empty((N, Hv, 128, 128), _F32, dev, stream)
         if workspace is None:
             workspace = _new_workspace(dev, stream, gdn_prefill_workspace_size(q.shape[0], N, Hv))
     flags = (KDA_LOAD_INITIAL if load_initial else 0) | (KDA_FINAL_TO_POOL if final_to_pool else 0)
@@ -108,9 +105,10 @@ def gdn_recurrent_verify(q, k, v, a, beta_logits, A_log, dt_bias, state_pool, sl
     if out is None or intermediate_states is None or workspace is None:
         dev = _cuda(q, "q")
         if out is None:
-            out = _rows_like(v, "v")
+            out = _rows_like(v, "v", stream)
         if intermediate_states is None:
-            intermediate_states = torch.empty((slot_ids.numel(), max(operator.index(T), 0), v.shape[1], 128, 128), dtype=_F32, device=dev)
+            intermediate_states = _b._empty((slot_ids.numel(), max(operator.index(T), 0), v.shape[1], 128, 128), _F32, dev,
+                                            stream)
         if workspace is None:
             workspace = _new_workspace(dev, stream)
     rc = _ext.gdn_recurrent_verify(q, k, v, a, beta_logits, A_log, dt_bias, scale, state_pool, slot_ids, T, out,
@@ -127,7 +125,7 @@ def gdn_decode(q, k, v, a, beta_logits, A_log, dt_bias, state_pool, slot_ids, *,
     if out is None or workspace is None:
         dev = _cuda(q, "q")
         if out is None:
-            out = _rows_like(v, "v")
+            out = _rows_like(v, "v", stream)
         if workspace is None:
             workspace = _new_workspace(dev, stream)
     rc = _ext.gdn_decode(q, k, v, a, beta_logits, A_log, dt_bias, scale, state_pool, slot_ids, out, workspace,
@@ -152,7 +150,7 @@ def paged_attention(q, k_pages, v_pages, block_table, seq_lens, T=1, *, scale=No
     if out is None or workspace is None:
         dev = _cuda(q, "q")
         if out is None:
-            out = _rows_like(q, "q")
+            out = _rows_like(q, "q", stream)
         if workspace is None:
             workspace = _new_workspace(dev, stream, paged_workspace_size(q.shape[1], k_pages.shape[2], T))
     rc = _ext.paged_attention(q, k_pages, v_pages, block_table, seq_lens, T, scale, out, lse, workspace,

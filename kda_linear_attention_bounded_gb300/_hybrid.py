@@ -25,11 +25,13 @@ class _Unloaded:
 
     def __getattr__(self, name):
         global _ext
+        from . import build
+
         lib = _b.load()
-        path = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_build", "_kda_torch.so")
+        path = build.torch_ext()
         if not os.path.exists(path):
-            raise RuntimeError(f"the torch binding is not built ({path} missing): run __graft_entry__.build() "
-                               "or `python -m kda_linear_attention_bounded_gb300.build`")
+            raise RuntimeError(f"the torch binding is not built for this interpreter and torch ({path} missing): run "
+                               "__graft_entry__.build() or `python -m kda_linear_attention_bounded_gb300.build`")
         loader = importlib.machinery.ExtensionFileLoader("_kda_torch", path)
         ext = importlib.util.module_from_spec(importlib.util.spec_from_loader("_kda_torch", loader))
         loader.exec_module(ext)

@@ -456,7 +456,16 @@ KDA_API int kda_recurrent_verify_noalloc(const uint16_t *q, const uint16_t *k, c
  * slot_ids, flags (KDA_LOAD_INITIAL | KDA_FINAL_TO_POOL), out and final_state
  * as in kda_chunk_prefill; workspace of kda_gdn_prefill_workspace_size bytes
  * (which grows with each of its arguments; separate ones for concurrent calls).
- * Final states carry an fp32 evaluation's error.  Few long sequences are cut
+ * Final states carry an fp32 evaluation's error (measured: a few 1e-7 in the
+ * norm of a head's state, to 2e-6 where decays are so weak that hundreds of
+ * tokens add up, 6e-6 where all keys of a chunk are the same); for a value
+ * channel it is relative to the largest that its values and its state have been
+ * within the last 64 tokens, and keys shorter than 1e-8 (far below the root of
+ * the 1e-6 in their norm) count with fewer bits.  Outputs are rounded to bf16;
+ * the chunked form rounds the weights of a chunk's own tokens and their values
+ * (fp16) and, for the output alone, the entering state (bf16) before that: they
+ * are off by about 1.9e-3 in the norm, where bf16 alone leaves 1.7e-3.
+ * Keys and queries may have any finite length.  Few long sequences are cut
  * into segments and batches of sequences of at most 10 tokens go token by
  * token, so a sequence's last bits depend on what it is batched with (not on
  * timing).  A NaN or infinity among a token's inputs reaches the
@@ -517,6 +526,9 @@ KDA_API int kda_gdn_decode(const uint16_t *q, const uint16_t *k, int64_t qk_toke
  *                that sees no token (n - T + t < 0) gets zeros and lse = -inf.
  *  Hq            a multiple of Hk, at most 4096;  1 <= T <= 64;  page_size >= 1
  *  out           [B*T, Hq, 128] bf16, token stride out_token_stride
+ *                Sums, maxima and weights' sums are fp32; a weight is rounded to
+ *                bf16 where it meets its value (out is off by about 2e-3 in the
+ *                norm, where its own bf16 leaves 1.7e-3); lse is of unrounded weights.
  *  lse           [B*T, Hq] fp32 (natural logarithm), or NULL
  *  workspace     kda_paged_workspace_size(Hq, Hk, T) bytes; no part of it needs
  *                clearing.  Concurrent calls need separate workspaces.

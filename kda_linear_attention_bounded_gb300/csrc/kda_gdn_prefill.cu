@@ -15,12 +15,13 @@
 // instead of the keys', queries' and values' products with L.  The state pass walks a sequence's chunks with S in
 // fp32 registers, three products a chunk.
 //
-// Operands that are not the caller's data are pairs.  S is two bf16 (its rounding, 2^-18, is contracted by the chunk).
+// Operands that are not the caller's data are pairs.  S is two bf16 (its rounding, at most 2^-17, is contracted by the chunk).
 // L, R and U are two fp16, 22 bits: |L| <= 1, since (I - beta k^ k^T) contracts, and |P| <= 1; R and U carry a power
 // of two per value channel that keeps them in fp16's range whatever the values are (from |v| and a bound on the
 // channel's state, |S_t|^2 <= |S_(t-1)|^2 + v_t^2); the keys they meet are the caller's, times a power of two per token
-// (exact down to 2^-17 of a key's norm).  Final states agree with the 64-bit recurrence to a few 1e-7, like an fp32
-// evaluation, where pairs of bf16 throughout leave 6e-6 and single bf16 operands a few 1e-3.  What only an output sees
+// (exact down to 2^-17 of a key's norm).  Final states agree with the 64-bit recurrence to a few 1e-7 (1 to 2e-6 where decays
+// are so weak that S's rounding counts), like an fp32 evaluation, where pairs of bf16 throughout leave 3 to 6e-6 and single
+// bf16 operands a few 1e-3.  What only an output sees
 // is rounded once (P and its U to fp16, S to bf16).
 #include <cuda.h>
 
@@ -220,8 +221,9 @@ __device__ __forceinline__ void st_tile_l(uint8_t *blk, int row0, int col0, cons
 }
 // One CTA per (chunk slot, key head): the products of the chunk's keys and queries serve every value head of the group.
 // Short dependent phases on one chunk, hidden by four CTAs per SM (TMEM and shared memory hold no fifth); its traffic is
-// the keys and queries in and 25 KB a value head out.  Measured: 2048 x 8 tokens, 16 heads 58 us (issue slots 52 % busy,
-// 3.4 TB/s); the phases in parallel warps with two barriers fewer took 61 us, so it is the instructions that bind.
+// the keys and queries in and 25 KB a value head out.  Measured: 2048 x 8 tokens, 16 heads 59 us (issue slots 50 % busy,
+// 3.3 TB/s).  Neither issue nor memory is full: what binds has not been measured phase by phase (phases in which two or
+// four of the eight warps work, seven barriers a value head).  Phases in parallel warps with two barriers fewer took 61 us.
 __global__ void __launch_bounds__(in::kThreads, 4) gdn_intra_kernel(const __grid_constant__ GdnPrefillParams prm) {
   using namespace in;
   extern __shared__ uint8_t smem_raw[];
@@ -561,7 +563,7 @@ __global__ void __launch_bounds__(in::kThreads, 4) gdn_intra_kernel(const __grid
 // issuing warps, one that feeds chunks through two stages, brings the next to L2 and stores the output, and one that goes
 // ahead of them all over v for the channels' scales.  The serial path of a chunk is KU -> R -> U -> U' -> D -> S; what it does not need runs
 // beside it: VT under S's epilogue, QS under R's, the fp16 keys under U, OT and the output under D.  Bound by that path:
-// 2.6 us a chunk on one long sequence, 3.0 with every SM at work (2048 x 8 tokens, 16 heads: 96 us; tensor pipe 35 %, DRAM
+// 2.6 us a chunk on one long sequence, 3.0 with every SM at work (2048 x 8 tokens, 16 heads: 96 us; tensor pipe 35 %, issue 46 %, DRAM
 // 48 % busy).  Fetching tokens a chunk earlier, with more scales in flight, took 100 us.
 namespace ch {
 constexpr int kWorkers = 512, kThreads = kWorkers + 128;

@@ -754,8 +754,10 @@ __global__ void __launch_bounds__(kJoinThreads, 2) paged_join_kernel(PagedArgs p
 
 // Tiles for each CTA of a cluster, at most.  Measured (16 query, 2 key heads, requests of one length; cut against clusters):
 // one request of 257 tokens 8.9 and 6.3 us, of 2048 11.5 and 9.9, of 4096 (8 tiles a CTA) 15.6 and 15.0; 16 of 2048 (4
-// tiles) 14.5 and 11.4; 120 of 257 (5 tiles) 16.1 and 11.8, of 4096 (64 tiles) 85 and 91.  A CTA takes 1.3 us a tile, and
-// where one request is much longer than the others only stretches share it out, hence not more.
+// tiles) 14.5 and 11.4; 120 of 257 (5 tiles) 16.1 and 11.8, of 4096 (64 tiles) 85 and 91.  The host knows no lengths, only how
+// many tokens the table's rows hold, so this is a limit on the table; a CTA takes 1.3 us a tile, and where one request is
+// much longer than the others only stretches share it out.  By these figures the limit could be higher for requests of one
+// length (5 tiles gain 4.3 us), and short requests in a wide table take the cut and its join all the same.
 constexpr int kWholeTiles = 4;
 // Boxes of fewer rows are not worth a TMA copy each (four a box).  Measured over 64 x 8192 tokens, 2 key heads: boxes of 8
 // 109 us against 95 us by asynchronous copies, of 16 and more 90 to 92 us (copies by one warp instead of two: 133 us).

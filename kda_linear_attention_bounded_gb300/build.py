@@ -112,12 +112,11 @@ def build(force: bool = False, verbose: bool = False, extra_flags=(), binding: b
     ext_tmp = f"{ext}.tmp{os.getpid()}"
     if need_ext:
         module.append((TORCH_SRC, _start(_torch_ext_command(ext_tmp), verbose)))
-    failed = _finish(units, verbose)
+    failed, module_failed = _finish(units, verbose), _finish(module, verbose)
     if need_lib and not failed:
         tmp = LIB + f".tmp{os.getpid()}"
         subprocess.run([_nvcc(), *ARCH, "-shared", "-o", tmp, *objs], check=True)
         os.replace(tmp, LIB)
-    module_failed = _finish(module, verbose)
     if need_ext and not module_failed:
         os.replace(ext_tmp, ext)
     if failed or module_failed:

@@ -45,13 +45,16 @@ int check_gdn(int64_t tokens, const uint16_t *q, const uint16_t *k, int64_t qk_s
   return KDA_OK;
 }
 
-// A piece of memory (bytes; of none, nothing meets it).
+// A piece of memory (bytes; of none, nothing meets it), or rows of it a stride apart (what lies between them is others').
 struct Span {
   const void *at;
-  int64_t bytes;
-  bool meets(const Span &o) const {
-    const uintptr_t a = reinterpret_cast<uintptr_t>(at), b = reinterpret_cast<uintptr_t>(o.at);
-    return bytes > 0 && o.bytes > 0 && a < b + static_cast<uintptr_t>(o.bytes) && b < a + static_cast<uintptr_t>(bytes);
+  int64_t bytes, rows = 1, stride = 0;
+  bool meets(const Span &o) const {   // (o is in one piece)
+    if (bytes <= 0 || rows <= 0 || o.bytes <= 0) return false;
+    const int64_t from = static_cast<int64_t>(reinterpret_cast<uintptr_t>(o.at) - reinterpret_cast<uintptr_t>(at));
+    const int64_t first = rows > 1 && from > 0 ? std::min(from / stride, rows - 1) : 0;   // the last row at or before it
+    const auto row = [&](int64_t r) { return r < rows && r * stride < from + o.bytes && from < r * stride + bytes; };
+    return row(first) || row(first + 1);
   }
 };
 
@@ -234,13 +237,13 @@ int kda_step_tables(int32_t *block_table, int64_t table_row_stride, int table_wi
   const bool in_place = B > 0 && kv_lens == seq_lens;
   const auto ints = [](const int32_t *at, int64_t n) { return Span{at, n * 4}; };
   const Span inputs[] = {in_place ? Span{nullptr, 0} : ints(seq_lens, B), ints(new_lens, B), ints(free_pages, num_free)};
-  const Span written[] = {ints(block_table, B > 0 && table_width > 0 ? (B - 1) * table_row_stride + table_width : 0),
+  const Span written[] = {Span{block_table, int64_t(4) * table_width, B, 4 * table_row_stride},
                           ints(cu_seqlens, static_cast<int64_t>(B) + 1), ints(kv_lens, B), ints(positions, max_tokens),
                           Span{slot_map, max_tokens * 8}, ints(pages_used, 1)};
   for (size_t i = 0; i < std::size(written); ++i) {
     for (const Span &x : inputs)
       if (written[i].meets(x)) return KDA_ERR_INVALID_ARG;
-    for (size_t j = 0; j < i; ++j)
+    for (size_t j = i + 1; j < std::size(written); ++j)
       if (written[i].meets(written[j])) return KDA_ERR_INVALID_ARG;
   }
   kda::StepTablesArgs t{};

@@ -66,3 +66,22 @@ def test_overlapping_buffers_are_refused():
                  dict(kv_lens=table.view(-1)[:3])):
         with pytest.raises(kda.KdaError):
             kda.step_tables(table, lens, new, free, 16, **{**o, **args})
+
+
+def test_what_lies_between_the_tables_rows():
+    # the lengths, their sums and the count in the gaps of a table with wide rows
+    table, old, new, free = case(6, 90, 40, 16, seed=7)
+    width, rows = len(table[0]), sum(new) + 3
+    want = reference(table, old, new, free, 16, rows)
+    room = torch.full((6, width + 8), -9, dtype=torch.int32, device="cuda")
+    room[:, :width] = _i32(table)
+    gap = lambda r, n: room[r, width:width + n]  # noqa: E731
+    lens, kv, cu, used, fresh = gap(0, 6), gap(1, 6), gap(2, 7), gap(5, 1), gap(3, 6)
+    lens.copy_(_i32(old))
+    fresh.copy_(_i32(new))
+    o, ws = _outs(6, rows), kda.make_workspace()
+    o.update(cu_seqlens=cu, pages_used=used)
+    kda.step_tables(room[:, :width], lens, fresh, _i32(free), 16, kv_lens=kv, workspace=ws, **o)
+    got = (room[:, :width].tolist(), cu.tolist(), kv.tolist(), o["positions"].tolist(), o["slot_map"].tolist(), int(used),
+           kda.read_device_status(ws))
+    assert got == want

@@ -80,7 +80,7 @@ int kda_gdn_chunk_prefill(const uint16_t *q, const uint16_t *k, int64_t qk_token
                           int num_slots, const int32_t *slot_ids, int flags, uint16_t *out, int64_t out_token_stride,
                           float *final_state, void *workspace, size_t workspace_bytes, void *stream) {
   if (int rc = check_workspace(workspace, workspace_bytes)) return rc;
-  if (num_seqs < 0 || !cu_seqlens_dev || !cu_seqlens_host) return KDA_ERR_INVALID_ARG;
+  if (num_seqs < 0 || !cu_seqlens_dev || !cu_seqlens_host || !aligned_to(cu_seqlens_dev, 4)) return KDA_ERR_INVALID_ARG;
   if (flags & ~(KDA_LOAD_INITIAL | KDA_FINAL_TO_POOL)) return KDA_ERR_INVALID_ARG;
   if (cu_seqlens_host[0] != 0) return KDA_ERR_INVALID_ARG;
   for (int n = 0; n < num_seqs; ++n)
@@ -91,7 +91,8 @@ int kda_gdn_chunk_prefill(const uint16_t *q, const uint16_t *k, int64_t qk_token
                          beta_token_stride, A_log, dt_bias, scale, Hk, Hv, out, out_token_stride, &r))
     return rc;
   const bool use_pool = flags & (KDA_LOAD_INITIAL | KDA_FINAL_TO_POOL);
-  if (use_pool && (!state_pool || !slot_ids || num_slots <= 0 || !aligned16(state_pool))) return KDA_ERR_INVALID_ARG;
+  if (use_pool && (!state_pool || !slot_ids || num_slots <= 0 || !aligned16(state_pool) || !aligned_to(slot_ids, 4)))
+    return KDA_ERR_INVALID_ARG;
   if (!(flags & KDA_FINAL_TO_POOL) && (!final_state || !aligned16(final_state))) return KDA_ERR_INVALID_ARG;
   if (workspace_bytes < kda_gdn_prefill_workspace_size(cu_seqlens_host[num_seqs], num_seqs, Hv)) return KDA_ERR_WORKSPACE;
   r.cu_seqlens = cu_seqlens_dev;
@@ -125,7 +126,7 @@ int kda_gdn_recurrent_verify(const uint16_t *q, const uint16_t *k, int64_t qk_to
   if (int rc = check_gdn(B, q, k, qk_token_stride, v, v_token_stride, a, a_token_stride, beta_logits,
                          beta_token_stride, A_log, dt_bias, scale, Hk, Hv, out, out_token_stride, &r))
     return rc;
-  if (!state_pool || !aligned16(state_pool) || num_slots <= 0 || !slot_ids) return KDA_ERR_INVALID_ARG;
+  if (!state_pool || !aligned16(state_pool) || num_slots <= 0 || !slot_ids || !aligned_to(slot_ids, 4)) return KDA_ERR_INVALID_ARG;
   if (!intermediate_states || !aligned16(intermediate_states)) return KDA_ERR_INVALID_ARG;
   r.T = T;
   r.slot_ids = slot_ids;
@@ -149,7 +150,7 @@ int kda_gdn_decode(const uint16_t *q, const uint16_t *k, int64_t qk_token_stride
   if (int rc = check_gdn(B, q, k, qk_token_stride, v, v_token_stride, a, a_token_stride, beta_logits,
                          beta_token_stride, A_log, dt_bias, scale, Hk, Hv, out, out_token_stride, &r))
     return rc;
-  if (!state_pool || !aligned16(state_pool) || num_slots <= 0 || !slot_ids) return KDA_ERR_INVALID_ARG;
+  if (!state_pool || !aligned16(state_pool) || num_slots <= 0 || !slot_ids || !aligned_to(slot_ids, 4)) return KDA_ERR_INVALID_ARG;
   r.T = 1;
   r.slot_ids = slot_ids;
   r.num_slots = num_slots;

@@ -68,7 +68,7 @@ extern "C" {
 #define KDA_DEVICE_BAD_SLOT 1u /* a slot id was outside [0, num_slots); that work item was skipped */
 #define KDA_DEVICE_TIMEOUT 2u  /* a bounded wait inside a kernel gave up (a lost async completion); results are incomplete */
 #define KDA_DEVICE_BAD_COUNT 4u /* an accepted-token count was outside [0, T]; that request was skipped */
-#define KDA_DEVICE_BAD_INDEX 8u /* an output row index was outside [0, num_out_tokens); that row was not written */
+#define KDA_DEVICE_BAD_INDEX 8u /* an output row index (a request, a group's bounds) was outside its range; that row was not written, that entry skipped */
 #define KDA_DEVICE_NO_PAGES 16u /* a request's new tokens found no page (free list or table row used up) */
 #define KDA_DEVICE_BAD_PAGE 32u /* a page id was outside [0, num_pages); its tokens were left out */
 
@@ -586,6 +586,170 @@ KDA_API int kda_step_tables(int32_t *block_table, int64_t table_row_stride, int 
                     int num_free, int page_size, int64_t max_tokens, int32_t *cu_seqlens, int32_t *kv_lens,
                     int32_t *positions, int64_t *slot_map, int32_t *pages_used, void *workspace,
                     size_t workspace_bytes, void *stream);
+
+/* ======================================================================== *
+ * Around the paged cache: rotary positions and the store of a step's keys   *
+ * and values, attention over prefixes that requests share, and the pages'   *
+ * own operations.  Pages in use are those the block table names: there are  *
+ * no reference counts, and each call leaves the same result when run again. *
+ * ======================================================================== */
+
+/*
+ * Rotary positions of a step's tokens: the queries turned, the keys turned and
+ * stored into the cache with the values.  Frequency f (of R / 2) of token i
+ * turns by theta = positions[axes[f]][i] * inv_freq[f], and with m = mscale
+ *   (a, b) -> m (a cos theta - b sin theta, b cos theta + a sin theta)
+ * on the channels (f, f + R / 2), or (2 f, 2 f + 1) with interleaved != 0;
+ * channels R .. 127 are kept.  Values are stored as they are.
+ *
+ *  q             [tokens, Hq, 128] bf16, token stride q_token_stride
+ *  k, v          [tokens, Hk, 128] bf16, each with its token stride
+ *  positions     [num_axes, tokens] int32, any value, a row each
+ *                position_row_stride (elements); 1 <= num_axes <= 4
+ *  slot_map      [tokens] int64: page id * page_size + row in the page (as
+ *                kda_step_tables writes it), distinct.  -1 marks a padding
+ *                token: nothing of it is read or written.  Any other slot
+ *                outside the cache leaves the token out, too
+ *                (KDA_DEVICE_BAD_SLOT).
+ *  inv_freq      [R / 2] fp32; below 2^24 in size (others turn to NaN)
+ *  axes          HOST, [R / 2] bytes below num_axes; NULL: axis 0 throughout
+ *  R             a multiple of 16, 16 .. 128 (else KDA_ERR_UNSUPPORTED)
+ *  mscale        finite (else KDA_ERR_UNSUPPORTED)
+ *  k_pages, v_pages [num_pages, page_size, Hk, 128] bf16 with any page, token
+ *                and head strides (elements, multiples of 8) that keep rows apart
+ *  out           [tokens, Hq, 128] bf16, token stride out_token_stride; may be
+ *                q itself (same stride)
+ * What is written may overlap no input (KDA_ERR_INVALID_ARG), except that out may
+ * be q; q, k, v and out may lie in one buffer with one token stride.
+ * The angle is reduced exactly (the position times the frequency in turns as a
+ * 64-bit fraction), so far positions lose nothing: cos and sin are off by about
+ * 2^-22, and the result is rounded to bf16 once.
+ */
+KDA_API int kda_rotary_to_pages(const uint16_t *q, int64_t q_token_stride, const uint16_t *k, int64_t k_token_stride,
+                        const uint16_t *v, int64_t v_token_stride, int tokens, int Hq, int Hk,
+                        const int32_t *positions, int64_t position_row_stride, int num_axes,
+                        const int64_t *slot_map, const float *inv_freq, int R, const uint8_t *axes, int interleaved,
+                        float mscale, uint16_t *k_pages, int64_t k_page_stride, int64_t k_page_token_stride,
+                        int64_t k_head_stride, uint16_t *v_pages, int64_t v_page_stride, int64_t v_page_token_stride,
+                        int64_t v_head_stride, int num_pages, int page_size, uint16_t *out, int64_t out_token_stride,
+                        void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Forks requests of a paged cache: row children[i] becomes a copy of row
+ * parents[i].  With n = seq_lens[parent], the child takes the parent's
+ * floor(n / page_size) whole pages as they are (both read them, nobody writes
+ * them again) and, where n is no multiple of page_size, a page of its own from
+ * free_pages for the rest; seq_lens[child] = n.  The pages' contents are
+ * kda_copy_pages' part, from the lists that this call writes.
+ *
+ *  block_table   [B, table_width] int32, row stride table_row_stride
+ *  seq_lens      [B] int32
+ *  parents, children [forks] int32 rows.  The children are distinct, and none
+ *                is a parent of this call.  A negative one marks a padding
+ *                entry; one of B and above, or a child that is its parent,
+ *                skips the fork (KDA_DEVICE_BAD_INDEX).
+ *  free_pages    [num_free] int32: pages are taken from its front, in the order
+ *                of the forks; *pages_used (int32) receives how many
+ *  copy_src, copy_dst [forks] int32: the page to copy and where to, -1 where
+ *                there is none
+ * A parent's length that is negative or that its row cannot hold skips the fork
+ * (KDA_DEVICE_BAD_COUNT), and so does a free list used up by the forks before
+ * (KDA_DEVICE_NO_PAGES).  A fork that is skipped leaves the child's row and length
+ * as they were.  What is written may overlap neither another input nor each other.
+ */
+KDA_API int kda_fork_requests(int32_t *block_table, int64_t table_row_stride, int table_width, int32_t *seq_lens, int B,
+                      const int32_t *parents, const int32_t *children, int forks, const int32_t *free_pages,
+                      int num_free, int page_size, int32_t *copy_src, int32_t *copy_dst, int32_t *pages_used,
+                      void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Ends requests: seq_lens[rows[i]] = 0 (rows may repeat; a negative one marks a
+ * padding entry, one of B and above is KDA_DEVICE_BAD_INDEX).  Then the free list
+ * is written anew: the ids below num_pages that no row of the table holds in its
+ * first ceil(seq_lens / page_size) places, ascending, -1 behind them, and how many
+ * in *num_free (int32).  A page that several rows hold is free when the last of
+ * them ends.  Pages held for another reason (a prompt kept for later) need a row
+ * of their own.
+ *
+ *  free_pages    [num_pages] int32
+ * A length that is negative or that its row cannot hold counts as 0
+ * (KDA_DEVICE_BAD_COUNT); an id outside [0, num_pages) is passed over
+ * (KDA_DEVICE_BAD_PAGE).
+ */
+KDA_API int kda_release_requests(const int32_t *block_table, int64_t table_row_stride, int table_width, int32_t *seq_lens,
+                         int B, const int32_t *rows, int num_rows, int page_size, int32_t *free_pages, int num_pages,
+                         int32_t *num_free, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Brings the pages in use to the ids 0 .. n - 1, n their number: the i-th page in
+ * use of id n or above goes to the i-th id below n that is free.  Writes the
+ * table's places in use with the new ids, the copies to make (kda_copy_pages), and
+ * the free list n .. num_pages - 1 (-1 behind it) with its length.  No page is both
+ * copied from and copied to.
+ *
+ *  new_table     [B, table_width] int32, row stride new_row_stride; may be
+ *                block_table itself (same stride).  Other places are kept.
+ *  copy_src, copy_dst [room] int32, room >= num_pages / 2: -1 behind the copies
+ *  free_pages    [num_pages] int32;  num_free: int32
+ * Bad lengths and ids as in kda_release_requests (a bad id is kept as it is).
+ */
+KDA_API int kda_compact_pages(const int32_t *block_table, int64_t table_row_stride, int table_width,
+                      const int32_t *seq_lens, int B, int page_size, int num_pages, int32_t *new_table,
+                      int64_t new_row_stride, int32_t *copy_src, int32_t *copy_dst, int room, int32_t *free_pages,
+                      int32_t *num_free, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * A buffer of pages: num_pages pieces of `bytes` contiguous bytes, each
+ * page_stride bytes behind the one before.  Any type: keys or values of one
+ * layer, or the recurrent states or convolution windows of forked requests
+ * (a slot is a page then).
+ */
+typedef struct kda_page_buffer {
+  void *base;
+  int64_t page_stride; /* bytes, a multiple of 16, at least `bytes` */
+  int64_t bytes;       /* a multiple of 16 */
+} kda_page_buffer;
+
+/*
+ * Copies pages copy_src[i] -> copy_dst[i] (i < count) of every buffer.  A negative
+ * id marks an entry without a copy; an id of num_pages or above skips it
+ * (KDA_DEVICE_BAD_PAGE), and a page is not copied onto itself.  The destinations
+ * are distinct, and none is a source.  `buffers` is a HOST array; the buffers may
+ * not overlap.
+ */
+KDA_API int kda_copy_pages(const kda_page_buffer *buffers, int num_buffers, int num_pages, const int32_t *copy_src,
+                   const int32_t *copy_dst, int count, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * kda_paged_attention for batches whose requests share long prefixes: each group's
+ * prefix is read once for all its requests.  Group g is the requests
+ * group_starts[g] .. group_starts[g + 1] - 1, whose first prefix_lens[g] tokens are
+ * the same: they are read through the group's first request with a length above 0.
+ * Requests in no group attend alone.  The result is that of kda_paged_attention.
+ *
+ *  prefix_lens   [num_groups] int32, >= 0, any length (pages need not end with the
+ *                prefix; the requests' own tables hold all of their tokens).  Tokens
+ *                that one of the group's new tokens does not see, or that a table row
+ *                has no room for, are not counted in.
+ *  group_starts  [num_groups + 1] int32, ascending, within 0 .. B
+ *  the rest      as in kda_paged_attention
+ *  workspace     kda_shared_prefix_workspace_size(B, T, Hq, Hk, num_groups) bytes; no
+ *                part of it needs clearing.  Concurrent calls need separate ones.
+ *
+ * Device-side findings as in kda_paged_attention; starts that do not ascend or
+ * leave 0 .. B, or a negative prefix length, make every request attend alone
+ * (KDA_DEVICE_BAD_INDEX).  Results do not depend on timing.
+ */
+KDA_API size_t kda_shared_prefix_workspace_size(int B, int T, int Hq, int Hk, int num_groups);
+
+KDA_API int kda_shared_prefix_attention(const uint16_t *q, int64_t q_token_stride, const uint16_t *k_pages,
+                                int64_t k_page_stride, int64_t k_token_stride, int64_t k_head_stride,
+                                const uint16_t *v_pages, int64_t v_page_stride, int64_t v_token_stride,
+                                int64_t v_head_stride, int num_pages, int page_size, const int32_t *block_table,
+                                int64_t table_row_stride, int table_width, const int32_t *seq_lens, int B, int T,
+                                const int32_t *prefix_lens, const int32_t *group_starts, int num_groups, int Hq, int Hk,
+                                float scale, uint16_t *out, int64_t out_token_stride, float *lse, void *workspace,
+                                size_t workspace_bytes, void *stream);
 
 #ifdef __cplusplus
 }

@@ -20,7 +20,11 @@ Beside the KDA layers of a hybrid model (the same pools, slot ids, workspaces an
 * :func:`gdn_chunk_prefill`, :func:`gdn_recurrent_verify`, :func:`gdn_decode` -- the gated delta rule (one unbounded
   decay per head, shared key heads): chunked prefill, speculative verify, one token in place;
 * :func:`paged_attention` -- one or several new tokens per request over a paged key-value cache;
-* :func:`step_tables` -- page tables and slot maps of a step, built on the GPU from the requests' lengths.
+* :func:`step_tables` -- page tables and slot maps of a step, built on the GPU from the requests' lengths;
+* :func:`rotary_to_pages` -- rotary positions of one or several axes, the step's keys and values stored into their pages;
+* :func:`shared_prefix_attention` -- attention for batches whose requests share long prefixes, read once for all;
+* :func:`fork_requests`, :func:`release_requests`, :func:`compact_pages`, :func:`copy_pages` -- the pages' own operations,
+  the last over every layer's pages or the pooled states.
 
 Every call launches only on the given (or current) stream, allocates nothing beyond what the caller passes
 (the wrappers allocate missing outputs and workspaces through torch), and reports device-side problems
@@ -35,3 +39,6 @@ from ._binding import (  # noqa: F401
 from ._hybrid import (  # noqa: F401
     gdn_chunk_prefill, gdn_decode, gdn_prefill_workspace_size, gdn_recurrent_verify, paged_attention, paged_workspace_size,
     step_tables)
+from ._cache import (  # noqa: F401
+    compact_pages, copy_pages, fork_requests, release_requests, rotary_to_pages, shared_prefix_attention,
+    shared_prefix_workspace_size)

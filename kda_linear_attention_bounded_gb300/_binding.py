@@ -45,7 +45,9 @@ EXPORTS = ("kda_status_string", "kda_workspace_size", "kda_prefill_workspace_siz
            "kda_read_device_status", "kda_chunk_prefill", "kda_recurrent_verify", "kda_commit_accepted",
            "kda_recurrent_verify_noalloc", "kda_spec_step", "kda_prefill_schedule", "kda_gdn_prefill_workspace_size",
            "kda_gdn_chunk_prefill", "kda_gdn_recurrent_verify", "kda_gdn_decode", "kda_step_tables",
-           "kda_paged_workspace_size", "kda_paged_attention")
+           "kda_paged_workspace_size", "kda_paged_attention", "kda_rotary_to_pages", "kda_fork_requests",
+           "kda_release_requests", "kda_compact_pages", "kda_copy_pages", "kda_shared_prefix_workspace_size",
+           "kda_shared_prefix_attention")
 
 _lib = None
 
@@ -55,6 +57,11 @@ class TokenTensors(ctypes.Structure):
     _fields_ = [("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
                 ("qkv_token_stride", ctypes.c_int64), ("g", ctypes.c_void_p), ("g_token_stride", ctypes.c_int64),
                 ("beta_logits", ctypes.c_void_p), ("beta_token_stride", ctypes.c_int64)]
+
+
+class PageBuffer(ctypes.Structure):
+    """``kda_page_buffer``: pages of contiguous bytes, a stride apart."""
+    _fields_ = [("base", ctypes.c_void_p), ("page_stride", ctypes.c_int64), ("bytes", ctypes.c_int64)]
 
 
 class _OutputNormC(ctypes.Structure):
@@ -180,8 +187,20 @@ def load():
     lib.kda_paged_workspace_size.restype = SZ
     lib.kda_paged_attention.argtypes = [P, I64, P, I64, I64, I64, P, I64, I64, I64, I, I, P, I64, I, P, I, I, I, I, F, P,
                                         I64, P, P, SZ, P]
+    S3 = [I64, I64, I64]   # page, token and head strides
+    lib.kda_rotary_to_pages.argtypes = [P, I64, P, I64, P, I64, I, I, I, P, I64, I, P, P, I, P, I, F, P, *S3, P, *S3, I, I,
+                                        P, I64, P, SZ, P]
+    lib.kda_fork_requests.argtypes = [P, I64, I, P, I, P, P, I, P, I, I, P, P, P, P, SZ, P]
+    lib.kda_release_requests.argtypes = [P, I64, I, P, I, P, I, I, P, I, P, P, SZ, P]
+    lib.kda_compact_pages.argtypes = [P, I64, I, P, I, I, I, P, I64, P, P, I, P, P, P, SZ, P]
+    lib.kda_copy_pages.argtypes = [ctypes.POINTER(PageBuffer), I, I, P, P, I, P, SZ, P]
+    lib.kda_shared_prefix_workspace_size.argtypes = [I, I, I, I, I]
+    lib.kda_shared_prefix_workspace_size.restype = SZ
+    lib.kda_shared_prefix_attention.argtypes = [P, I64, P, *S3, P, *S3, I, I, P, I64, I, P, I, I, P, P, I, I, I, F, P, I64, P,
+                                                P, SZ, P]
     for name in ("kda_gdn_chunk_prefill", "kda_gdn_recurrent_verify", "kda_gdn_decode", "kda_step_tables",
-                 "kda_paged_attention"):
+                 "kda_paged_attention", "kda_rotary_to_pages", "kda_fork_requests", "kda_release_requests",
+                 "kda_compact_pages", "kda_copy_pages", "kda_shared_prefix_attention"):
         getattr(lib, name).restype = I
     _lib = lib
     return lib

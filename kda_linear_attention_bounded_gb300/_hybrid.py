@@ -37,7 +37,8 @@ class _Unloaded:
         loader.exec_module(ext)
         ext.bind(*(ctypes.cast(getattr(lib, f), ctypes.c_void_p).value
                    for f in ("kda_gdn_chunk_prefill", "kda_gdn_recurrent_verify", "kda_gdn_decode", "kda_paged_attention",
-                             "kda_step_tables")))
+                             "kda_step_tables", "kda_rotary_to_pages", "kda_fork_requests", "kda_release_requests",
+                             "kda_compact_pages", "kda_copy_pages", "kda_shared_prefix_attention")))
         _ext = ext
         return getattr(ext, name)
 

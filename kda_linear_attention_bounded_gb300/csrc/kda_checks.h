@@ -4,6 +4,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "kda.h"
 #include "kda_internal.h"
 
@@ -26,5 +28,18 @@ inline int check_workspace(const void *ws, size_t bytes) {
   if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u) != 0 || bytes < kWorkspaceBytes) return KDA_ERR_WORKSPACE;
   return KDA_OK;
 }
+
+// A piece of memory (bytes; of none, nothing meets it), or rows of it a stride apart (what lies between them is others').
+struct Span {
+  const void *at;
+  int64_t bytes, rows = 1, stride = 0;
+  bool meets(const Span &o) const {   // (o is in one piece)
+    if (bytes <= 0 || rows <= 0 || o.bytes <= 0) return false;
+    const int64_t from = static_cast<int64_t>(reinterpret_cast<uintptr_t>(o.at) - reinterpret_cast<uintptr_t>(at));
+    const int64_t first = rows > 1 && from > 0 ? std::min(from / stride, rows - 1) : 0;   // the last row at or before it
+    const auto row = [&](int64_t r) { return r < rows && r * stride < from + o.bytes && from < r * stride + bytes; };
+    return row(first) || row(first + 1);
+  }
+};
 
 }  // namespace kda

@@ -91,6 +91,12 @@ struct PagedArgs {
 // Rows (query heads x new tokens of a key head) that one CTA takes, for `rows` of them.
 int paged_rows_per_item(int rows);
 cudaError_t launch_paged_attention(const PagedArgs &args, cudaStream_t stream);
+// Checks what kda_paged_attention is given and fills its arguments (with B == 0 it leaves them without the tensors).
+int check_paged(const uint16_t *q, int64_t q_token_stride, const uint16_t *k_pages, int64_t k_page_stride, int64_t k_token_stride,
+                int64_t k_head_stride, const uint16_t *v_pages, int64_t v_page_stride, int64_t v_token_stride,
+                int64_t v_head_stride, int num_pages, int page_size, const int32_t *block_table, int64_t table_row_stride,
+                int table_width, const int32_t *seq_lens, int B, int T, int Hq, int Hk, float scale, uint16_t *out,
+                int64_t out_token_stride, float *lse, void *workspace, size_t workspace_bytes, PagedArgs *args);
 
 // ---------------------------------------------------------------- step tables
 struct StepTablesArgs {

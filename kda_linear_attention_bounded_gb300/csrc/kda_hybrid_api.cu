@@ -17,6 +17,7 @@ using kda::aligned16;
 using kda::aligned_to;
 using kda::check_workspace;
 using kda::good_stride;
+using kda::Span;
 
 // The tensors of a gated-delta-rule call over `tokens` tokens; fills the token part of `a`.  Without tokens (empty
 // sequences, whose final states are their initial ones) the token tensors may be NULL.
@@ -45,25 +46,62 @@ int check_gdn(int64_t tokens, const uint16_t *q, const uint16_t *k, int64_t qk_s
   return KDA_OK;
 }
 
-// A piece of memory (bytes; of none, nothing meets it), or rows of it a stride apart (what lies between them is others').
-struct Span {
-  const void *at;
-  int64_t bytes, rows = 1, stride = 0;
-  bool meets(const Span &o) const {   // (o is in one piece)
-    if (bytes <= 0 || rows <= 0 || o.bytes <= 0) return false;
-    const int64_t from = static_cast<int64_t>(reinterpret_cast<uintptr_t>(o.at) - reinterpret_cast<uintptr_t>(at));
-    const int64_t first = rows > 1 && from > 0 ? std::min(from / stride, rows - 1) : 0;   // the last row at or before it
-    const auto row = [&](int64_t r) { return r < rows && r * stride < from + o.bytes && from < r * stride + bytes; };
-    return row(first) || row(first + 1);
-  }
-};
-
 // Batches whose sequences have so many tokens at most take the recurrence token by token.  Measured, chunks against
 // tokens: 1 sequence x 2 heads of 8 tokens 11.1 and 6.7 us, of 12 11.1 and 9.0; 64 x 16 heads of 8 66 and 52 us, of 12 68 and 75.
 // So a full GPU crosses between 8 and 12 and a single sequence later; 10 is right for both, at 11 and 12 a small batch loses 2 us.
 constexpr int kRecurrentTokens = 10;
 
 }  // namespace
+
+namespace kda {
+
+int check_paged(const uint16_t *q, int64_t q_token_stride, const uint16_t *k_pages, int64_t k_page_stride,
+                int64_t k_token_stride, int64_t k_head_stride, const uint16_t *v_pages, int64_t v_page_stride,
+                int64_t v_token_stride, int64_t v_head_stride, int num_pages, int page_size,
+                const int32_t *block_table, int64_t table_row_stride, int table_width,
+                const int32_t *seq_lens, int B, int T, int Hq, int Hk, float scale, uint16_t *out,
+                int64_t out_token_stride, float *lse, void *workspace, size_t workspace_bytes, PagedArgs *args) {
+  if (int rc = check_workspace(workspace, workspace_bytes)) return rc;
+  if (B < 0 || T < 1 || T > 64) return KDA_ERR_INVALID_ARG;
+  if (Hk <= 0 || Hq <= 0 || Hq > 4096 || Hq % Hk != 0) return KDA_ERR_INVALID_ARG;
+  if (page_size < 1 || num_pages < 0 || table_width < 0 || table_row_stride < table_width) return KDA_ERR_INVALID_ARG;
+  if (!std::isfinite(scale)) return KDA_ERR_UNSUPPORTED;
+  if (B == 0) return KDA_OK;
+  if (static_cast<int64_t>(B) * T > INT_MAX) return KDA_ERR_INVALID_ARG;
+  if (!q || !seq_lens || !out || !aligned16(q) || !aligned16(out) || !aligned_to(seq_lens, 4) || !aligned_to(lse, 4))
+    return KDA_ERR_INVALID_ARG;
+  if (table_width > 0 && (!block_table || !aligned_to(block_table, 4))) return KDA_ERR_INVALID_ARG;
+  if (num_pages > 0 && (!k_pages || !v_pages || !aligned16(k_pages) || !aligned16(v_pages))) return KDA_ERR_INVALID_ARG;
+  const int64_t row = static_cast<int64_t>(Hq) * kD;
+  if (!good_stride(q_token_stride, row) || !good_stride(out_token_stride, row)) return KDA_ERR_INVALID_ARG;
+  for (int64_t s : {k_page_stride, k_token_stride, k_head_stride, v_page_stride, v_token_stride, v_head_stride})
+    if (!good_stride(s, 0)) return KDA_ERR_INVALID_ARG;
+  if (workspace_bytes < kda_paged_workspace_size(Hq, Hk, T)) return KDA_ERR_WORKSPACE;
+  PagedArgs &a = *args;
+  a.q = q; a.k = k_pages; a.v = v_pages;
+  a.q_stride = q_token_stride;
+  a.k_page_stride = k_page_stride; a.k_token_stride = k_token_stride; a.k_head_stride = k_head_stride;
+  a.v_page_stride = v_page_stride; a.v_token_stride = v_token_stride; a.v_head_stride = v_head_stride;
+  a.num_pages = num_pages;
+  a.page = page_size;
+  a.table = block_table;
+  a.table_stride = table_row_stride;
+  const int64_t most = static_cast<int64_t>(table_width) * page_size;
+  a.max_len = static_cast<int>(most < INT_MAX - 64 ? most : INT_MAX - 64);
+  a.seq_lens = seq_lens;
+  a.B = B; a.T = T; a.Hk = Hk; a.G = Hq / Hk;
+  a.scale = scale;
+  a.out = out;
+  a.out_stride = out_token_stride;
+  a.lse = lse;
+  uint8_t *ws = static_cast<uint8_t *>(workspace);
+  a.joins = reinterpret_cast<int4 *>(ws + kWorkspaceBytes);
+  a.parts = reinterpret_cast<float *>(ws + kWorkspaceBytes + kPagedMaxCtas * sizeof(int4));
+  a.status = static_cast<uint32_t *>(workspace);
+  return KDA_OK;
+}
+
+}  // namespace kda
 
 extern "C" {
 
@@ -176,43 +214,11 @@ int kda_paged_attention(const uint16_t *q, int64_t q_token_stride, const uint16_
                         const int32_t *block_table, int64_t table_row_stride, int table_width,
                         const int32_t *seq_lens, int B, int T, int Hq, int Hk, float scale, uint16_t *out,
                         int64_t out_token_stride, float *lse, void *workspace, size_t workspace_bytes, void *stream) {
-  if (int rc = check_workspace(workspace, workspace_bytes)) return rc;
-  if (B < 0 || T < 1 || T > 64) return KDA_ERR_INVALID_ARG;
-  if (Hk <= 0 || Hq <= 0 || Hq > 4096 || Hq % Hk != 0) return KDA_ERR_INVALID_ARG;
-  if (page_size < 1 || num_pages < 0 || table_width < 0 || table_row_stride < table_width) return KDA_ERR_INVALID_ARG;
-  if (!std::isfinite(scale)) return KDA_ERR_UNSUPPORTED;
-  if (B == 0) return KDA_OK;
-  if (static_cast<int64_t>(B) * T > INT_MAX) return KDA_ERR_INVALID_ARG;
-  if (!q || !seq_lens || !out || !aligned16(q) || !aligned16(out) || !aligned_to(seq_lens, 4) || !aligned_to(lse, 4))
-    return KDA_ERR_INVALID_ARG;
-  if (table_width > 0 && (!block_table || !aligned_to(block_table, 4))) return KDA_ERR_INVALID_ARG;
-  if (num_pages > 0 && (!k_pages || !v_pages || !aligned16(k_pages) || !aligned16(v_pages))) return KDA_ERR_INVALID_ARG;
-  const int64_t row = static_cast<int64_t>(Hq) * kda::kD;
-  if (!good_stride(q_token_stride, row) || !good_stride(out_token_stride, row)) return KDA_ERR_INVALID_ARG;
-  for (int64_t s : {k_page_stride, k_token_stride, k_head_stride, v_page_stride, v_token_stride, v_head_stride})
-    if (!good_stride(s, 0)) return KDA_ERR_INVALID_ARG;
-  if (workspace_bytes < kda_paged_workspace_size(Hq, Hk, T)) return KDA_ERR_WORKSPACE;
   kda::PagedArgs a{};
-  a.q = q; a.k = k_pages; a.v = v_pages;
-  a.q_stride = q_token_stride;
-  a.k_page_stride = k_page_stride; a.k_token_stride = k_token_stride; a.k_head_stride = k_head_stride;
-  a.v_page_stride = v_page_stride; a.v_token_stride = v_token_stride; a.v_head_stride = v_head_stride;
-  a.num_pages = num_pages;
-  a.page = page_size;
-  a.table = block_table;
-  a.table_stride = table_row_stride;
-  const int64_t most = static_cast<int64_t>(table_width) * page_size;
-  a.max_len = static_cast<int>(most < INT_MAX - 64 ? most : INT_MAX - 64);
-  a.seq_lens = seq_lens;
-  a.B = B; a.T = T; a.Hk = Hk; a.G = Hq / Hk;
-  a.scale = scale;
-  a.out = out;
-  a.out_stride = out_token_stride;
-  a.lse = lse;
-  uint8_t *ws = static_cast<uint8_t *>(workspace);
-  a.joins = reinterpret_cast<int4 *>(ws + kda::kWorkspaceBytes);
-  a.parts = reinterpret_cast<float *>(ws + kda::kWorkspaceBytes + kda::kPagedMaxCtas * sizeof(int4));
-  a.status = static_cast<uint32_t *>(workspace);
+  if (int rc = kda::check_paged(q, q_token_stride, k_pages, k_page_stride, k_token_stride, k_head_stride, v_pages, v_page_stride,
+                                v_token_stride, v_head_stride, num_pages, page_size, block_table, table_row_stride, table_width,
+                                seq_lens, B, T, Hq, Hk, scale, out, out_token_stride, lse, workspace, workspace_bytes, &a))
+    return rc;
   return kda::launch_paged_attention(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 

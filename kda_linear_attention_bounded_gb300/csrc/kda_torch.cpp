@@ -12,6 +12,7 @@
 #include <cmath>
 #include <exception>
 #include <string>
+#include <vector>
 
 #include "kda.h"
 
@@ -22,6 +23,12 @@ decltype(&kda_gdn_recurrent_verify) g_verify = nullptr;
 decltype(&kda_gdn_decode) g_decode = nullptr;
 decltype(&kda_paged_attention) g_paged = nullptr;
 decltype(&kda_step_tables) g_tables = nullptr;
+decltype(&kda_rotary_to_pages) g_rotary = nullptr;
+decltype(&kda_fork_requests) g_fork = nullptr;
+decltype(&kda_release_requests) g_release = nullptr;
+decltype(&kda_compact_pages) g_compact = nullptr;
+decltype(&kda_copy_pages) g_copy = nullptr;
+decltype(&kda_shared_prefix_attention) g_prefix = nullptr;
 
 constexpr int64_t kD = 128;
 
@@ -180,7 +187,7 @@ PyObject *guarded(Py_ssize_t have, Py_ssize_t want, F body) {
       PyErr_SetString(PyExc_TypeError, "wrong number of arguments");
       return nullptr;
     }
-    if (!g_tables) {
+    if (!g_prefix) {
       PyErr_SetString(PyExc_RuntimeError, "the library has not been bound");
       return nullptr;
     }
@@ -305,34 +312,231 @@ Table table_of(const at::Tensor &t, int dev) {
   return b;
 }
 
+// The tensors of an attention over pages: q, k_pages, v_pages, block_table, seq_lens, then T, scale, out, lse
+struct PagedCall {
+  int dev, T, num_pages, page, Hq, Hk, requests;
+  float scale;
+  Rows q, out;
+  Pages k, v;
+  Table table;
+  const int32_t *lens;
+  float *lse;
+};
+PagedCall paged_call(PyObject *const *x, PyObject *T, PyObject *scale, PyObject *out, PyObject *lse) {
+  PagedCall c;
+  c.T = int32(T, "T");
+  c.scale = scale_of(scale);
+  const at::Tensor &q = tensor(x[0], "q");
+  c.dev = cuda_device(q, "q");
+  const int64_t B = count_of(x[4], "seq_lens");
+  if (q.dim() != 3) refuse("q: expected a bf16 tensor [B*T, Hq, 128]");
+  const int64_t Hq = q.size(1);
+  c.q = rows3(x[0], "q", c.dev, B * c.T, Hq);
+  const at::Tensor &kt = tensor(x[1], "k_pages"), &vt = tensor(x[2], "v_pages");
+  c.k = pages_of(kt, "k_pages", c.dev);
+  c.v = pages_of(vt, "v_pages", c.dev);
+  if (kt.sizes() != vt.sizes()) refuse("k_pages and v_pages must have one shape");
+  c.table = table_of(tensor(x[3], "block_table"), c.dev);
+  if (c.table.requests != B) refuse("block_table: " + n(c.table.requests) + " rows for " + n(B) + " requests");
+  c.lens = static_cast<const int32_t *>(exact(x[4], "seq_lens", at::kInt, c.dev, {B}));
+  c.out = rows3(out, "out", c.dev, B * c.T, Hq);
+  c.lse = lse == Py_None ? nullptr : static_cast<float *>(exact(lse, "lse", at::kFloat, c.dev, {B * c.T, Hq}));
+  c.num_pages = int32(kt.size(0), "k_pages");
+  c.page = int32(kt.size(1), "k_pages");
+  c.Hk = int32(kt.size(2), "k_pages");
+  c.Hq = int32(Hq, "q");
+  c.requests = int32(B, "seq_lens");
+  return c;
+}
+
 // q, k_pages, v_pages, block_table, seq_lens, T, scale, out, lse, workspace, stream
 PyObject *paged_attention(PyObject *, PyObject *const *x, Py_ssize_t argc) {
   return guarded(argc, 11, [&] {
-    const int T = int32(x[5], "T");
-    const float scale = scale_of(x[6]);
-    const at::Tensor &q = tensor(x[0], "q");
+    const PagedCall c = paged_call(x, x[5], x[6], x[7], x[8]);
+    const Workspace ws = workspace_of(x[9], c.dev);
+    void *stream = stream_of(x[10], c.dev);
+    return call(c.dev, [&] {
+      return g_paged(c.q.at, c.q.stride, c.k.at, c.k.stride[0], c.k.stride[1], c.k.stride[2], c.v.at, c.v.stride[0],
+                     c.v.stride[1], c.v.stride[2], c.num_pages, c.page, c.table.at, c.table.stride, c.table.width, c.lens,
+                     c.requests, c.T, c.Hq, c.Hk, c.scale, c.out.at, c.out.stride, c.lse, ws.at, ws.bytes, stream);
+    });
+  });
+}
+
+// q, k_pages, v_pages, block_table, seq_lens, prefix_lens, group_starts, T, scale, out, lse, workspace, stream
+PyObject *shared_prefix_attention(PyObject *, PyObject *const *x, Py_ssize_t argc) {
+  return guarded(argc, 13, [&] {
+    const PagedCall c = paged_call(x, x[7], x[8], x[9], x[10]);
+    const int64_t G = count_of(x[5], "prefix_lens");
+    const auto *prefix = static_cast<const int32_t *>(exact(x[5], "prefix_lens", at::kInt, c.dev, {G}));
+    const auto *starts = static_cast<const int32_t *>(exact(x[6], "group_starts", at::kInt, c.dev, {G + 1}));
+    const Workspace ws = workspace_of(x[11], c.dev);
+    void *stream = stream_of(x[12], c.dev);
+    const int groups = int32(G, "prefix_lens");
+    return call(c.dev, [&] {
+      return g_prefix(c.q.at, c.q.stride, c.k.at, c.k.stride[0], c.k.stride[1], c.k.stride[2], c.v.at, c.v.stride[0],
+                      c.v.stride[1], c.v.stride[2], c.num_pages, c.page, c.table.at, c.table.stride, c.table.width, c.lens,
+                      c.requests, c.T, prefix, starts, groups, c.Hq, c.Hk, c.scale, c.out.at, c.out.stride, c.lse, ws.at,
+                      ws.bytes, stream);
+    });
+  });
+}
+
+// q, k, v, positions, slot_map, inv_freq, k_pages, v_pages, axes, interleaved, mscale, out, workspace, stream
+PyObject *rotary_to_pages(PyObject *, PyObject *const *x, Py_ssize_t argc) {
+  return guarded(argc, 14, [&] {
+    const int interleaved = int32(x[9], "interleaved");
+    const double mscale = PyFloat_AsDouble(x[10]);
+    if (mscale == -1.0 && PyErr_Occurred()) throw Refused{};
+    const at::Tensor &q = tensor(x[0], "q"), &kt = tensor(x[6], "k_pages"), &vt = tensor(x[7], "v_pages"),
+                     &pos = tensor(x[3], "positions");
     const int dev = cuda_device(q, "q");
-    const int64_t B = count_of(x[4], "seq_lens");
-    if (q.dim() != 3) refuse("q: expected a bf16 tensor [B*T, Hq, 128]");
-    const int64_t Hq = q.size(1);
-    const Rows rows = rows3(x[0], "q", dev, B * T, Hq);
-    const at::Tensor &kt = tensor(x[1], "k_pages"), &vt = tensor(x[2], "v_pages");
-    const Pages k = pages_of(kt, "k_pages", dev), v = pages_of(vt, "v_pages", dev);
+    if (q.dim() != 3) refuse("q: expected a bf16 tensor [tokens, Hq, 128]");
+    const int64_t tokens = q.size(0), Hq = q.size(1), half = count_of(x[5], "inv_freq");
+    const Pages kp = pages_of(kt, "k_pages", dev), vp = pages_of(vt, "v_pages", dev);
     if (kt.sizes() != vt.sizes()) refuse("k_pages and v_pages must have one shape");
-    const Table table = table_of(tensor(x[3], "block_table"), dev);
-    if (table.requests != B) refuse("block_table: " + n(table.requests) + " rows for " + n(B) + " requests");
-    const auto *lens = static_cast<const int32_t *>(exact(x[4], "seq_lens", at::kInt, dev, {B}));
-    const Rows out = rows3(x[7], "out", dev, B * T, Hq);
-    float *lse = x[8] == Py_None ? nullptr : static_cast<float *>(exact(x[8], "lse", at::kFloat, dev, {B * T, Hq}));
+    const int64_t Hk = kt.size(2);
+    const Rows qr = rows3(x[0], "q", dev, tokens, Hq), kr = rows3(x[1], "k", dev, tokens, Hk), vr = rows3(x[2], "v", dev, tokens, Hk);
+    if (pos.scalar_type() != at::kInt || !on(pos, dev) || pos.dim() < 1 || pos.dim() > 2 || pos.size(-1) != tokens ||
+        (tokens > 1 && pos.stride(-1) != 1))
+      refuse("positions: expected an int32 tensor [" + n(tokens) + "] or [axes, " + n(tokens) + "] on cuda:" + n(dev) +
+             " with contiguous rows");
+    const int64_t rows = pos.dim() == 2 ? pos.size(0) : 1, row_stride = rows > 1 ? pos.stride(0) : tokens;
+    const auto *slots = static_cast<const int64_t *>(exact(x[4], "slot_map", at::kLong, dev, {tokens}));
+    const auto *freq = static_cast<const float *>(exact(x[5], "inv_freq", at::kFloat, dev, {half}));
+    const uint8_t *axes = nullptr;
+    if (x[8] != Py_None) {
+      if (!PyBytes_Check(x[8])) {
+        PyErr_SetString(PyExc_TypeError, "axes: expected bytes");
+        throw Refused{};
+      }
+      if (PyBytes_GET_SIZE(x[8]) != half)
+        refuse("axes: expected one for each of the " + n(half) + " frequencies, got " + n(PyBytes_GET_SIZE(x[8])));
+      axes = reinterpret_cast<const uint8_t *>(PyBytes_AS_STRING(x[8]));
+    }
+    const Rows out = rows3(x[11], "out", dev, tokens, Hq);
+    const Workspace ws = workspace_of(x[12], dev);
+    void *stream = stream_of(x[13], dev);
+    const int count = int32(tokens, "q"), hq = int32(Hq, "q"), hk = int32(Hk, "k_pages"), num_axes = int32(rows, "positions"),
+              R = int32(2 * half, "inv_freq"), num_pages = int32(kt.size(0), "k_pages"), page = int32(kt.size(1), "k_pages");
+    return call(dev, [&] {
+      return g_rotary(qr.at, qr.stride, kr.at, kr.stride, vr.at, vr.stride, count, hq, hk, static_cast<const int32_t *>(pos.data_ptr()),
+                      row_stride, num_axes, slots, freq, R, axes, interleaved, static_cast<float>(mscale),
+                      const_cast<uint16_t *>(kp.at), kp.stride[0], kp.stride[1], kp.stride[2], const_cast<uint16_t *>(vp.at),
+                      vp.stride[0], vp.stride[1], vp.stride[2], num_pages, page, out.at, out.stride, ws.at, ws.bytes, stream);
+    });
+  });
+}
+
+// block_table, seq_lens, parents, children, free_pages, page_size, copy_src, copy_dst, pages_used, workspace, stream
+PyObject *fork_requests(PyObject *, PyObject *const *x, Py_ssize_t argc) {
+  return guarded(argc, 11, [&] {
+    const int page = int32(x[5], "page_size");
+    const at::Tensor &t = tensor(x[0], "block_table");
+    const int dev = cuda_device(t, "block_table");
+    const Table table = table_of(t, dev);
+    auto ints = [&](int i, const char *name, int64_t count) {
+      return static_cast<int32_t *>(exact(x[i], name, at::kInt, dev, {count}));
+    };
+    const int64_t forks = count_of(x[2], "parents"), free = count_of(x[4], "free_pages");
+    int32_t *lens = ints(1, "seq_lens", table.requests), *parents = ints(2, "parents", forks), *children = ints(3, "children", forks),
+            *pages = ints(4, "free_pages", free), *src = ints(6, "copy_src", forks), *dst = ints(7, "copy_dst", forks),
+            *used = ints(8, "pages_used", 1);
     const Workspace ws = workspace_of(x[9], dev);
     void *stream = stream_of(x[10], dev);
-    const int num_pages = int32(kt.size(0), "k_pages"), page = int32(kt.size(1), "k_pages"), Hk = int32(kt.size(2), "k_pages"),
-              heads = int32(Hq, "q"), requests = int32(B, "seq_lens");
+    const int count = int32(forks, "parents"), num_free = int32(free, "free_pages");
     return call(dev, [&] {
-      return g_paged(rows.at, rows.stride, k.at, k.stride[0], k.stride[1], k.stride[2], v.at, v.stride[0], v.stride[1],
-                     v.stride[2], num_pages, page, table.at, table.stride, table.width, lens, requests, T, heads, Hk, scale,
-                     out.at, out.stride, lse, ws.at, ws.bytes, stream);
+      return g_fork(table.at, table.stride, table.width, lens, table.requests, parents, children, count, pages, num_free, page,
+                    src, dst, used, ws.at, ws.bytes, stream);
     });
+  });
+}
+
+// block_table, seq_lens, rows, page_size, free_pages, num_free, workspace, stream
+PyObject *release_requests(PyObject *, PyObject *const *x, Py_ssize_t argc) {
+  return guarded(argc, 8, [&] {
+    const int page = int32(x[3], "page_size");
+    const at::Tensor &t = tensor(x[0], "block_table");
+    const int dev = cuda_device(t, "block_table");
+    const Table table = table_of(t, dev);
+    const int64_t rows = count_of(x[2], "rows"), pages = count_of(x[4], "free_pages");
+    auto ints = [&](int i, const char *name, int64_t count) {
+      return static_cast<int32_t *>(exact(x[i], name, at::kInt, dev, {count}));
+    };
+    int32_t *lens = ints(1, "seq_lens", table.requests), *ended = ints(2, "rows", rows), *list = ints(4, "free_pages", pages),
+            *num = ints(5, "num_free", 1);
+    const Workspace ws = workspace_of(x[6], dev);
+    void *stream = stream_of(x[7], dev);
+    const int num_rows = int32(rows, "rows"), num_pages = int32(pages, "free_pages");
+    return call(dev, [&] {
+      return g_release(table.at, table.stride, table.width, lens, table.requests, ended, num_rows, page, list, num_pages, num,
+                       ws.at, ws.bytes, stream);
+    });
+  });
+}
+
+// block_table, seq_lens, page_size, new_table, copy_src, copy_dst, free_pages, num_free, workspace, stream
+PyObject *compact_pages(PyObject *, PyObject *const *x, Py_ssize_t argc) {
+  return guarded(argc, 10, [&] {
+    const int page = int32(x[2], "page_size");
+    const at::Tensor &t = tensor(x[0], "block_table"), &nt = tensor(x[3], "new_table");
+    const int dev = cuda_device(t, "block_table");
+    const Table table = table_of(t, dev);
+    if (nt.sizes() != t.sizes()) refuse("block_table and new_table must have one shape");
+    if (nt.scalar_type() != at::kInt || !on(nt, dev) || (nt.size(1) > 1 && nt.stride(1) != 1))
+      refuse("new_table: expected an int32 tensor [requests, width] on cuda:" + n(dev) + " with contiguous rows");
+    const int64_t new_stride = nt.size(0) > 1 ? nt.stride(0) : nt.size(1);
+    if (new_stride < table.width) refuse("new_table: its rows overlap");
+    const int64_t pages = count_of(x[6], "free_pages"), room = count_of(x[4], "copy_src");
+    auto ints = [&](int i, const char *name, int64_t count) {
+      return static_cast<int32_t *>(exact(x[i], name, at::kInt, dev, {count}));
+    };
+    if (room < pages / 2) refuse("copy_src: " + n(room) + " places for up to " + n(pages / 2) + " copies");
+    int32_t *lens = ints(1, "seq_lens", table.requests), *src = ints(4, "copy_src", room), *dst = ints(5, "copy_dst", room),
+            *list = ints(6, "free_pages", pages), *num = ints(7, "num_free", 1);
+    const Workspace ws = workspace_of(x[8], dev);
+    void *stream = stream_of(x[9], dev);
+    const int num_pages = int32(pages, "free_pages"), places = int32(room, "copy_src");
+    return call(dev, [&] {
+      return g_compact(table.at, table.stride, table.width, lens, table.requests, page, num_pages,
+                       static_cast<int32_t *>(nt.data_ptr()), new_stride, src, dst, places, list, num, ws.at, ws.bytes, stream);
+    });
+  });
+}
+
+// buffers (list or tuple), copy_src, copy_dst, workspace, stream
+PyObject *copy_pages(PyObject *, PyObject *const *x, Py_ssize_t argc) {
+  return guarded(argc, 5, [&] {
+    if (!PyList_Check(x[0]) && !PyTuple_Check(x[0])) {
+      PyErr_SetString(PyExc_TypeError, "buffers: expected a list or a tuple of tensors");
+      throw Refused{};
+    }
+    const Py_ssize_t many = PySequence_Fast_GET_SIZE(x[0]);
+    if (many < 1) refuse("buffers: expected at least one tensor");
+    std::vector<kda_page_buffer> buffers(static_cast<size_t>(many));
+    int dev = 0;
+    int64_t pages = 0;
+    for (Py_ssize_t i = 0; i < many; ++i) {
+      const at::Tensor &t = tensor(PySequence_Fast_GET_ITEM(x[0], i), "buffers");
+      if (i == 0) dev = cuda_device(t, "buffers");
+      if (!on(t, dev) || t.dim() < 1) refuse("buffers: expected tensors [pages, ...] on cuda:" + n(dev));
+      if (i == 0) pages = t.size(0);
+      if (t.size(0) != pages) refuse("buffers: " + n(t.size(0)) + " pages beside " + n(pages));
+      int64_t inner = 1;
+      for (int64_t d = t.dim() - 1; d >= 1; --d) {
+        if (t.size(d) > 1 && t.stride(d) != inner) refuse("buffers: a page has to be contiguous");
+        inner *= t.size(d);
+      }
+      const int64_t bytes = inner * t.element_size();
+      buffers[static_cast<size_t>(i)] = {t.data_ptr(), pages > 1 ? t.stride(0) * static_cast<int64_t>(t.element_size()) : bytes, bytes};
+    }
+    const int64_t count = count_of(x[1], "copy_src");
+    const auto *src = static_cast<const int32_t *>(exact(x[1], "copy_src", at::kInt, dev, {count}));
+    const auto *dst = static_cast<const int32_t *>(exact(x[2], "copy_dst", at::kInt, dev, {count}));
+    const Workspace ws = workspace_of(x[3], dev);
+    void *stream = stream_of(x[4], dev);
+    const int num_pages = int32(pages, "buffers"), copies = int32(count, "copy_src"), num = int32(many, "buffers");
+    return call(dev, [&] { return g_copy(buffers.data(), num, num_pages, src, dst, copies, ws.at, ws.bytes, stream); });
   });
 }
 
@@ -362,14 +566,15 @@ PyObject *step_tables(PyObject *, PyObject *const *x, Py_ssize_t argc) {
   });
 }
 
-// bind(addresses of kda_gdn_chunk_prefill, kda_gdn_recurrent_verify, kda_gdn_decode, kda_paged_attention, kda_step_tables)
+// bind(addresses of the C entry points, in the order below)
 PyObject *bind(PyObject *, PyObject *const *x, Py_ssize_t argc) {
-  if (argc != 5) {
-    PyErr_SetString(PyExc_TypeError, "bind: five addresses");
+  constexpr int kCalls = 11;
+  if (argc != kCalls) {
+    PyErr_SetString(PyExc_TypeError, "bind: eleven addresses");
     return nullptr;
   }
-  void *at[5];
-  for (int i = 0; i < 5; ++i) {
+  void *at[kCalls];
+  for (int i = 0; i < kCalls; ++i) {
     at[i] = PyLong_AsVoidPtr(x[i]);
     if (!at[i]) {
       if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "bind: a null address");
@@ -381,6 +586,12 @@ PyObject *bind(PyObject *, PyObject *const *x, Py_ssize_t argc) {
   g_decode = reinterpret_cast<decltype(g_decode)>(at[2]);
   g_paged = reinterpret_cast<decltype(g_paged)>(at[3]);
   g_tables = reinterpret_cast<decltype(g_tables)>(at[4]);
+  g_rotary = reinterpret_cast<decltype(g_rotary)>(at[5]);
+  g_fork = reinterpret_cast<decltype(g_fork)>(at[6]);
+  g_release = reinterpret_cast<decltype(g_release)>(at[7]);
+  g_compact = reinterpret_cast<decltype(g_compact)>(at[8]);
+  g_copy = reinterpret_cast<decltype(g_copy)>(at[9]);
+  g_prefix = reinterpret_cast<decltype(g_prefix)>(at[10]);
   Py_RETURN_NONE;
 }
 
@@ -394,6 +605,12 @@ PyMethodDef methods[] = {{"bind", fast<bind>(), METH_FASTCALL, nullptr},
                          {"gdn_decode", fast<gdn_decode>(), METH_FASTCALL, nullptr},
                          {"paged_attention", fast<paged_attention>(), METH_FASTCALL, nullptr},
                          {"step_tables", fast<step_tables>(), METH_FASTCALL, nullptr},
+                         {"rotary_to_pages", fast<rotary_to_pages>(), METH_FASTCALL, nullptr},
+                         {"fork_requests", fast<fork_requests>(), METH_FASTCALL, nullptr},
+                         {"release_requests", fast<release_requests>(), METH_FASTCALL, nullptr},
+                         {"compact_pages", fast<compact_pages>(), METH_FASTCALL, nullptr},
+                         {"copy_pages", fast<copy_pages>(), METH_FASTCALL, nullptr},
+                         {"shared_prefix_attention", fast<shared_prefix_attention>(), METH_FASTCALL, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_kda_torch", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

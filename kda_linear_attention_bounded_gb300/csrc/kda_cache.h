@@ -66,12 +66,28 @@ cudaError_t launch_copy_pages(const kda_page_buffer *buffers, int num_buffers, i
                               const int32_t *dst, int count, uint32_t *status, cudaStream_t stream);
 
 // ---------------------------------------------------------------- attention over shared prefixes
+struct PrefixGroup {         // of the plan: a group's place in the line of work
+  int64_t unit;              // its first
+  int64_t piece;             // rows of pieces before its
+  int b0, rows, tiles, len;  // first request, rows of a key head, tiles and tokens that are shared (0: none)
+  int table_row, pad[3];     // the request whose table row is read
+};
+struct PrefixPlan {
+  int64_t units;
+  int stretches, pad;
+};
 struct PrefixArgs {
-  PagedArgs a;
+  PagedArgs a;               // own, rows: for the requests' own tokens
   const int32_t *prefix_lens, *group_starts;
   int groups;
-  uint8_t *scratch;          // shared_prefix_bytes() behind what the paged attention itself needs
+  int2 *own;                 // [B]: a request's first own token, its group (-1: nothing is shared)
+  PrefixPlan *plan;
+  PrefixGroup *group;        // [groups]
+  float *pieces;             // rows of kPagedPartFloats
 };
+// Bytes that the plan, the rows of own tokens and the pieces take behind the paged attention's workspace; with args and base the
+// pointers are set, too.
+size_t shared_prefix_bytes(int B, int T, int Hq, int Hk, int groups, uint8_t *base, PrefixArgs *args);
 cudaError_t launch_shared_prefix(const PrefixArgs &args, cudaStream_t stream);
 
 }  // namespace kda

@@ -248,7 +248,7 @@ int kda_copy_pages(const kda_page_buffer *buffers, int num_buffers, int num_page
 size_t kda_shared_prefix_workspace_size(int B, int T, int Hq, int Hk, int num_groups) {
   const size_t base = kda_paged_workspace_size(Hq, Hk, T);
   if (B < 0 || num_groups < 0 || base == 0) return 0;
-  return base;
+  return base + kda::shared_prefix_bytes(B, T, Hq, Hk, num_groups, nullptr, nullptr);
 }
 
 int kda_shared_prefix_attention(const uint16_t *q, int64_t q_token_stride, const uint16_t *k_pages, int64_t k_page_stride,
@@ -270,7 +270,8 @@ int kda_shared_prefix_attention(const uint16_t *q, int64_t q_token_stride, const
   p.prefix_lens = prefix_lens;
   p.group_starts = group_starts;
   p.groups = num_groups;
-  return status_of(kda::launch_paged_attention(p.a, static_cast<cudaStream_t>(stream)));
+  kda::shared_prefix_bytes(B, T, Hq, Hk, num_groups, static_cast<uint8_t *>(workspace) + kda_paged_workspace_size(Hq, Hk, T), &p);
+  return status_of(kda::launch_shared_prefix(p, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -113,6 +113,7 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4],
 struct Cursor {
   int b, hr, tile, ntiles, len;
   int next;       // length of the next request (looked up early)
+  int start, next_start;   // the first of the tokens that count (0: all do), and the next request's
   int cost;       // units of an item besides its tiles'
   int64_t unit;   // of the tile
 };
@@ -130,9 +131,15 @@ __device__ __forceinline__ int request_len(const PagedArgs &p, int b, bool recor
   }
   return len;
 }
+// The first own token of request b; tiles begin at multiples of their size all the same.
+template <bool kOwn>
+__device__ __forceinline__ int request_start(const PagedArgs &p, int b) {
+  return kOwn ? p.own[b].x : 0;
+}
 // Tiles of an item: an empty request keeps one (its rows are written as empty)
-__device__ __forceinline__ int tile_count(int len) { return max(1, (len + kTile - 1) / kTile); }
+__device__ __forceinline__ int tile_count(int len, int start = 0) { return max(1, (len + kTile - 1) / kTile - start / kTile); }
 
+template <bool kOwn>
 __device__ __forceinline__ void advance(const PagedArgs &p, Cursor &c, int items_per_request) {
   ++c.unit;
   if (++c.tile < c.ntiles) return;
@@ -142,14 +149,25 @@ __device__ __forceinline__ void advance(const PagedArgs &p, Cursor &c, int items
   c.hr = 0;
   ++c.b;
   c.len = c.next;
-  c.ntiles = tile_count(c.len);
-  if (c.b + 1 < p.B) c.next = request_len(p, c.b + 1);
+  c.start = c.next_start;
+  c.ntiles = tile_count(c.len, c.start);
+  if (c.b + 1 < p.B) {
+    c.next = request_len(p, c.b + 1);
+    c.next_start = request_start<kOwn>(p, c.b + 1);
+  }
 }
 
 // One output row (a new token's query head) by a warp, four channels a lane, from its sums.
+template <bool kOwn = false>
 __device__ __forceinline__ void paged_store_row(const PagedArgs &p, int b, int t, int head, int lane, float4 acc, float m,
                                                 float l) {
   const int64_t row = static_cast<int64_t>(b) * p.T + t;
+  if constexpr (kOwn) {   // (for the join with what is shared)
+    float *part = p.rows + (row * p.Hk * p.G + head) * kPagedPartFloats;
+    *reinterpret_cast<float4 *>(part + lane * 4) = acc;
+    if (lane == 0) *reinterpret_cast<float2 *>(part + kD) = make_float2(m, l);
+    return;
+  }
   const float inv = l == 0.f ? 0.f : 1.0f / l;   // a row that sees nothing: zeros
   *reinterpret_cast<uint2 *>(p.out + row * p.out_stride + static_cast<int64_t>(head) * kD + lane * 4) =
       make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
@@ -157,8 +175,8 @@ __device__ __forceinline__ void paged_store_row(const PagedArgs &p, int b, int t
 }
 
 // WR: row groups of 16; the other 4 / WR warps of a row group split the tile's tokens.  kCluster: a cluster an item (no
-// joins), else stretches of the line.
-template <int WR, bool kCluster>
+// joins), else stretches of the line.  kOwn: only tokens from own[b].x on, sums left for a join.
+template <int WR, bool kCluster, bool kOwn>
 __global__ void __launch_bounds__(kThreads, 2) paged_attention_kernel(PagedArgs p, const __grid_constant__ PagedMaps maps) {
   constexpr int WT = 4 / WR, kTok = kTile / WT, kNT = kTok / 8;
   constexpr int kRows = 16 * WR;
@@ -200,7 +218,8 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attention_kernel(PagedArgs 
     cur.b = item / ipr;
     cur.hr = item % ipr;
     cur.len = request_len(p, cur.b, tid == 0);
-    cur.ntiles = tile_count(cur.len);
+    cur.start = request_start<kOwn>(p, cur.b);
+    cur.ntiles = tile_count(cur.len, cur.start);
     cur.cost = 0;
     first = static_cast<int64_t>(cur.ntiles) * rank / ranks;
     last = static_cast<int64_t>(cur.ntiles) * (rank + 1) / ranks;
@@ -211,7 +230,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attention_kernel(PagedArgs 
     const int per = (p.B + kThreads - 1) / kThreads;
     const int b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
     int64_t sum = 0;
-    for (int b = b0; b < b1; ++b) sum += tile_count(request_len(p, b, true));
+    for (int b = b0; b < b1; ++b) sum += tile_count(request_len(p, b, true), request_start<kOwn>(p, b));
     int64_t inc = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -240,7 +259,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attention_kernel(PagedArgs 
       int b = b0;
       int64_t at = before;
       while (true) {
-        const int64_t n = static_cast<int64_t>(cur.cost + tile_count(request_len(p, b))) * ipr;
+        const int64_t n = static_cast<int64_t>(cur.cost + tile_count(request_len(p, b), request_start<kOwn>(p, b))) * ipr;
         if (first < at + n) break;
         at += n;
         ++b;
@@ -254,7 +273,8 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attention_kernel(PagedArgs 
   if (!kCluster && !none) {
     cur.b = static_cast<int>(s_scan[6]);
     cur.len = request_len(p, cur.b);
-    cur.ntiles = tile_count(cur.len);
+    cur.start = request_start<kOwn>(p, cur.b);
+    cur.ntiles = tile_count(cur.len, cur.start);
     const int per_item = cur.cost + cur.ntiles;
     cur.hr = static_cast<int>(s_scan[7] / per_item);
     const int u = static_cast<int>(s_scan[7] - static_cast<int64_t>(cur.hr) * per_item);
@@ -308,7 +328,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attention_kernel(PagedArgs 
             ll += c * ml[q].y;
             acc.x += c * x[q].x; acc.y += c * x[q].y; acc.z += c * x[q].z; acc.w += c * x[q].w;
           }
-        paged_store_row(p, cur.b, t, h * p.G + row % p.G, lane, acc, mm, ll);
+        paged_store_row<kOwn>(p, cur.b, t, h * p.G + row % p.G, lane, acc, mm, ll);
       }
     }
     cluster_sync();   // (a CTA's shared memory stays while others read it)
@@ -327,23 +347,25 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attention_kernel(PagedArgs 
       return;
     }
     cur.next = cur.b + 1 < p.B ? request_len(p, cur.b + 1) : 0;
+    cur.next_start = cur.b + 1 < p.B ? request_start<kOwn>(p, cur.b + 1) : 0;
     const int at = lane + 32 * half;
     int id = 0;
     bool there = false;
     auto ask = [&] {   // the pages of the tile at the cursor
-      const int pos = cur.tile * kTile + at * box;
+      const int pos = (cur.start / kTile + cur.tile) * kTile + at * box;
       there = at < boxes && pos < cur.len;
       id = there ? p.table[static_cast<int64_t>(cur.b) * p.table_stride + pos / p.page] : 0;
     };
     ask();
     for (int i = 0; ; ++i) {
-      const int st = i % kStages, pos0 = cur.tile * kTile, h = cur.hr / p.row_blocks;
+      const int st = i % kStages, pos0 = (cur.start / kTile + cur.tile) * kTile, h = cur.hr / p.row_blocks;
+      const uint64_t before = kOwn ? first_tokens(cur.start - pos0) : 0;   // tokens of the tile that are not own
       const uint32_t dst = smem + st * kStageBytes;
       int4 info = make_int4(cur.b, cur.hr, cur.tile, cur.len);
       const int pg = id;
       const bool ok = there && pg >= 0 && pg < p.num_pages;
       if (there && !ok) atomicOr(p.status, KDA_DEVICE_BAD_PAGE);
-      advance(p, cur, ipr);
+      advance<kOwn>(p, cur, ipr);
       const bool more = cur.unit < last;
       if (more)
         ask();
@@ -358,10 +380,10 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attention_kernel(PagedArgs 
           uint64_t mask = 0;
           for (int x = 0; x < boxes; ++x)
             if (on >> x & 1) mask |= first_tokens(box) << (x * box);
-          s_mask[st] = mask & first_tokens(info.w - pos0);
+          s_mask[st] = mask & first_tokens(info.w - pos0) & ~before;
           sm100::mbar_arrive_expect_tx(&landed[st], __popc(on) * box * 512);
         } else {
-          reinterpret_cast<uint32_t *>(&s_mask[st])[half] = on;
+          reinterpret_cast<uint32_t *>(&s_mask[st])[half] = on & ~static_cast<uint32_t>(before >> (32 * half));
           sm100::mbar_arrive(&landed[st]);
         }
       }
@@ -477,7 +499,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attention_kernel(PagedArgs 
       }
     // ---- masks (tiles that every row sees whole need none), running maximum
     const uint64_t mask = s_mask[st];
-    const int pos0 = cur.tile * kTile;
+    const int start = request_start<kOwn>(p, cur.b), pos0 = (start / kTile + cur.tile) * kTile;
     const bool edge = mask != ~0ull || pos0 + kTile > cur.len - p.T + 1;
     float mx[2] = {m2[0], m2[1]};
 #pragma unroll
@@ -590,7 +612,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attention_kernel(PagedArgs 
     }
 
     // ---- the item's (or the stretch's) end: join the warps of each row group, write the rows or the part
-    const bool item_ends = cur.tile + 1 == tile_count(cur.len);
+    const bool item_ends = cur.tile + 1 == tile_count(cur.len, start);
     if (item_ends || stretch_ends) {
       const bool from_start = cur.tile == i - begun;   // the item began in this stretch, too
       const bool whole = item_ends && from_start;
@@ -639,7 +661,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attention_kernel(PagedArgs 
           *reinterpret_cast<float4 *>(sm + (r * kD + lane * 4) * 4) = acc;
           if (lane == 0) *reinterpret_cast<float2 *>(sm + OFF_CML + 8 * r) = make_float2(mm, ll);
         } else if (whole) {
-          paged_store_row(p, cur.b, t, h * p.G + row % p.G, lane, acc, mm, ll);
+          paged_store_row<kOwn>(p, cur.b, t, h * p.G + row % p.G, lane, acc, mm, ll);
         } else {
           float *part = p.parts + (static_cast<size_t>(slot) * kRows + r) * kPagedPartFloats;
           *reinterpret_cast<float4 *>(part + lane * 4) = acc;
@@ -763,30 +785,15 @@ constexpr int kWholeTiles = 4;
 // 109 us against 95 us by asynchronous copies, of 16 and more 90 to 92 us (copies by one warp instead of two: 133 us).
 constexpr int kLeastBox = 16;
 
-// false: the strides or sizes are none that a tensor map takes
-bool make_page_map(CUtensorMap *map, const uint16_t *pages, int64_t page_stride, int64_t token_stride, int64_t head_stride,
-                   const PagedArgs &a, int box) {
-  const int64_t most = (int64_t(1) << 39) / 2;
-  if (a.Hk == 1) head_stride = kD;   // (of one alone the stride may be anything)
-  if (a.num_pages == 1) page_stride = kD;
-  if (a.num_pages < 1 || page_stride <= 0 || token_stride <= 0 || head_stride <= 0 || page_stride >= most ||
-      token_stride >= most || head_stride >= most)
-    return false;
-  const uint64_t dims[4] = {kD, static_cast<uint64_t>(a.Hk), static_cast<uint64_t>(a.page), static_cast<uint64_t>(a.num_pages)};
-  const uint64_t strides[3] = {static_cast<uint64_t>(head_stride) * 2, static_cast<uint64_t>(token_stride) * 2,
-                               static_cast<uint64_t>(page_stride) * 2};
-  const uint32_t boxes[4] = {64, 1, static_cast<uint32_t>(box), 1};
-  return make_bf16_map(map, pages, 4, dims, strides, boxes);
-}
-
-template <int WR>
-cudaError_t launch_paged(PagedArgs a, cudaStream_t stream) {
+// places: of the joins that the caller has to make (kOwn)
+template <int WR, bool kOwn>
+cudaError_t launch_paged(PagedArgs a, cudaStream_t stream, int *places = nullptr) {
   static std::mutex mu;
   static uint64_t done = 0;
   if (const cudaError_t e = set_attributes_once(mu, done, [] {
-        cudaError_t r = cudaFuncSetAttribute(paged_attention_kernel<WR, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+        cudaError_t r = cudaFuncSetAttribute(paged_attention_kernel<WR, false, kOwn>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
         if (r == cudaSuccess)
-          r = cudaFuncSetAttribute(paged_attention_kernel<WR, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+          r = cudaFuncSetAttribute(paged_attention_kernel<WR, true, kOwn>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
         return r;
       }))
     return e;
@@ -811,24 +818,48 @@ cudaError_t launch_paged(PagedArgs a, cudaStream_t stream) {
   if (maps.box < kLeastBox || !make_page_map(&maps.k, a.k, a.k_page_stride, a.k_token_stride, a.k_head_stride, a, maps.box) ||
       !make_page_map(&maps.v, a.v, a.v_page_stride, a.v_token_stride, a.v_head_stride, a, maps.box))
     maps.box = 0;
+  if (kOwn) *places = whole ? 0 : static_cast<int>(grid);
   if (whole)
-    return launch_dependent_clusters(paged_attention_kernel<WR, true>, a.cluster, grid, kThreads, kSmemBytes, stream, a, maps);
-  const cudaError_t e = launch_dependent(paged_attention_kernel<WR, false>, grid, kThreads, kSmemBytes, stream, a, maps);
-  if (e != cudaSuccess) return e;
+    return launch_dependent_clusters(paged_attention_kernel<WR, true, kOwn>, a.cluster, grid, kThreads, kSmemBytes, stream, a, maps);
+  const cudaError_t e = launch_dependent(paged_attention_kernel<WR, false, kOwn>, grid, kThreads, kSmemBytes, stream, a, maps);
+  if (e != cudaSuccess || kOwn) return e;
   return launch_dependent(paged_join_kernel, std::min(grid * 16 * WR, static_cast<unsigned>(kJoinCtas)), kJoinThreads, 0, stream, a,
                           16 * WR, static_cast<int>(grid));
 }
 
 }  // namespace
 
+bool make_page_map(CUtensorMap *map, const uint16_t *pages, int64_t page_stride, int64_t token_stride, int64_t head_stride,
+                   const PagedArgs &a, int box) {
+  const int64_t most = (int64_t(1) << 39) / 2;
+  if (a.Hk == 1) head_stride = kD;   // (of one alone the stride may be anything)
+  if (a.num_pages == 1) page_stride = kD;
+  if (a.num_pages < 1 || page_stride <= 0 || token_stride <= 0 || head_stride <= 0 || page_stride >= most ||
+      token_stride >= most || head_stride >= most)
+    return false;
+  const uint64_t dims[4] = {kD, static_cast<uint64_t>(a.Hk), static_cast<uint64_t>(a.page), static_cast<uint64_t>(a.num_pages)};
+  const uint64_t strides[3] = {static_cast<uint64_t>(head_stride) * 2, static_cast<uint64_t>(token_stride) * 2,
+                               static_cast<uint64_t>(page_stride) * 2};
+  const uint32_t boxes[4] = {64, 1, static_cast<uint32_t>(box), 1};
+  return make_bf16_map(map, pages, 4, dims, strides, boxes);
+}
+
 int paged_rows_per_item(int rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
 
 cudaError_t launch_paged_attention(const PagedArgs &a, cudaStream_t stream) {
   if (a.B <= 0) return cudaSuccess;
   switch (paged_rows_per_item(a.T * a.G)) {
-    case 16: return launch_paged<1>(a, stream);
-    case 32: return launch_paged<2>(a, stream);
-    default: return launch_paged<4>(a, stream);
+    case 16: return launch_paged<1, false>(a, stream);
+    case 32: return launch_paged<2, false>(a, stream);
+    default: return launch_paged<4, false>(a, stream);
+  }
+}
+
+cudaError_t launch_paged_own(const PagedArgs &a, int *places, cudaStream_t stream) {
+  switch (paged_rows_per_item(a.T * a.G)) {
+    case 16: return launch_paged<1, true>(a, stream, places);
+    case 32: return launch_paged<2, true>(a, stream, places);
+    default: return launch_paged<4, true>(a, stream, places);
   }
 }
 

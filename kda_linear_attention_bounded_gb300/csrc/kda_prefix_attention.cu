@@ -9,9 +9,9 @@
 //   4. the join of a row's parts, in the order of a fixed list.
 // Each is a programmatic dependent of the one before.  Results do not depend on timing.
 //
-// 2. Bound by the products where a prefix meets more than about 280 rows, else by HBM.  A block is 256 rows, two groups of 128
-// threads with a row each, against tiles of 128 tokens, or 128 rows (where there are no more) of which the groups take the tiles in
-// turn.  So either way a step is two S = Q K^T and two O += P V of 128 x 128 x 128, and while one group turns its S into P the tensor
+// 2. Bound by the products where a prefix meets more than about 280 rows, else by HBM.  A block is 256 rows, for two groups of 256
+// threads with half a row each, against tiles of 128 tokens, or 128 rows (where there are no more) of which the groups take the
+// tiles in turn.  So either way a step is two S = Q K^T and two O += P V of 128 x 128 x 128, and while one group turns its S into P the tensor
 // cores work for the other: with P written over S in TMEM (S, O: 4 x 128 columns) nothing of them passes through shared memory.
 // One warp issues the products, one brings tiles (K and V in turn, five of 32 KB, TMA boxes of as many rows as the page's size has
 // powers of two, 8 to 64; pages without a factor of 8: asynchronous copies by two warps).  Steps of all blocks stand in one line of
@@ -22,6 +22,7 @@
 
 #include <algorithm>
 #include <climits>
+#include <type_traits>
 
 #include "kda_cache.h"
 #include "kda_hybrid.cuh"
@@ -29,7 +30,8 @@
 namespace kda {
 namespace {
 
-constexpr int kThreads = 384;                      // two groups of softmax warps, products, loads, loads (copies), spare
+constexpr int kSoftWarps = 16;                     // two groups of eight: each four lots of 32 rows, two warps a lot with half the tokens each
+constexpr int kThreads = 32 * (kSoftWarps + 4);    // and two for products, two for loads
 constexpr int kTile = 128;                         // tokens
 constexpr int kBlock = 256;                        // rows
 constexpr int kSlots = 5;
@@ -38,13 +40,16 @@ constexpr uint32_t OFF_Q = kSlots * kTileBytes;    // two tiles of 128 rows
 constexpr int kRing = 8;                           // masks of tiles: the loads are at most five tiles ahead of their readers
 constexpr uint32_t OFF_MASK = OFF_Q + 2 * kTileBytes;
 constexpr uint32_t OFF_BAR = OFF_MASK + kRing * 16;
-// landed [5], freed [5], scores [2], weights [2], sums [2], queries, cleared, drained
-constexpr int kBarriers = 2 * kSlots + 9;
-constexpr uint32_t OFF_TMEM = OFF_BAR + 8 * kBarriers;
+// landed [5], freed [5], scores [2], weights [2], sums [2], queries, cleared, drained [2], turn [2]
+constexpr int kBarriers = 2 * kSlots + 12;
+constexpr uint32_t OFF_ROWS = OFF_BAR + 8 * kBarriers;   // float [2][128]: what the two halves of a row tell each other
+constexpr uint32_t OFF_TMEM = OFF_ROWS + 4 * 256;
 constexpr uint32_t OFF_ABORT = OFF_TMEM + 4;
 constexpr uint32_t kSmemBytes = OFF_ABORT + 4 + 1024;
+static_assert(kSmemBytes <= 227 * 1024, "one CTA's shared memory");
 constexpr int kMostCtas = 152;
 constexpr int kCost = 2;                           // units of a block besides its steps': queries and sums
+constexpr int kPieceFloats = 136;                  // a row of a piece: 128 sums, the maximum, the sum of weights, padding to 32 bytes
 constexpr float kFollow = 8.f;                     // powers of two that the maximum may be too low
 constexpr int kLeastBox = 8;
 
@@ -77,6 +82,39 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map
 __device__ __forceinline__ void cp16(uint32_t dst, const void *src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 ra, rb, rd;\n\tmov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
+      "add.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+// 32 bytes, aligned
+__device__ __forceinline__ void st_global32(float *to, const uint32_t *x) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]),
+               "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
+               : "memory");
+}
+// Among the 64 threads of two warps: a barrier, and whether any says so.
+__device__ __forceinline__ void lot_sync(uint32_t id) { asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory"); }
+__device__ __forceinline__ bool lot_any(uint32_t id, bool x) {
+  uint32_t y;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %1, 0;\n\tbar.red.or.pred p, %2, 64, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(y)
+      : "r"(static_cast<uint32_t>(x)), "r"(id)
+      : "memory");
+  return y != 0;
+}
+// One lane of the warp, in a way that the compiler knows to be one: what it issues then takes its operands from uniform registers.
+__device__ __forceinline__ bool elect() {
+  uint32_t on;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(on));
+  return on != 0;
+}
+template <typename T>
+__device__ __forceinline__ T uniform(T x) { return __shfl_sync(0xffffffffu, x, 0); }
 __device__ __forceinline__ void st_zero16(uint32_t dst) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(dst), "r"(0) : "memory");
 }
@@ -105,6 +143,24 @@ __device__ __forceinline__ Blocks blocks_of(int rows, int tiles) {
   x.rows = static_cast<int64_t>(x.count - 1) * kBlock + (x.split ? 2 : 1) * x.last_rows;
   return x;
 }
+
+// of numbers that are not negative (a 64-bit division costs four of 32)
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+  return (a | b) >> 32 ? a / b : static_cast<int64_t>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b));
+}
+
+// Where a step's keys and values stand in the order of a block's tiles.  A block of more than 128 rows: K0 V0 K1 V1 ..; else the
+// first keys of both groups, then one's values and next keys, the other's values and next keys, as far as each has them.
+struct Order {
+  bool split;
+  int first, second;   // steps of the two groups, split
+  __device__ Order(bool split, int tiles) : split(split), first((tiles + 1) / 2), second(tiles / 2) {}
+  __device__ int steps(int s, int tiles) const { return !split ? tiles : s ? second : first; }
+  __device__ int keys(int s, int j) const { return !split ? 2 * j : j == 0 ? s : 4 * j - 1 + 2 * s; }
+  __device__ int values(int s, int j) const {
+    return !split ? 2 * j + 1 : s == 0 ? 4 * j + (j < second ? 2 : 1) : 4 * j + (j + 1 < second || first > second ? 4 : 3);
+  }
+};
 
 constexpr int kPlanThreads = 1024;
 __global__ void __launch_bounds__(kPlanThreads) shared_prefix_plan_kernel(PrefixArgs p, int ctas) {
@@ -213,9 +269,9 @@ __device__ __forceinline__ bool walk(const PrefixArgs &p, Walk &w) {
     const int tiles = x.tiles;
     const Blocks y = blocks_of(x.rows, tiles);
     int64_t v = w.at - x.unit;
-    w.h = static_cast<int>(v / y.units);
+    w.h = static_cast<int>(quotient(v, y.units));
     v -= w.h * y.units;
-    const int mb = static_cast<int>(min(static_cast<int64_t>(y.count - 1), v / (tiles + kCost)));
+    const int mb = static_cast<int>(min(static_cast<int64_t>(y.count - 1), quotient(v, tiles + kCost)));
     v -= static_cast<int64_t>(mb) * (tiles + kCost);
     const bool end = mb == y.count - 1;
     const int steps = end ? y.last_steps : tiles;
@@ -249,7 +305,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(PrefixArgs p
   uint8_t *sm = smem_raw + (-sm100::smem_u32(smem_raw) & 1023u);
   const uint32_t smem = sm100::smem_u32(sm);
   uint64_t *landed = reinterpret_cast<uint64_t *>(sm + OFF_BAR), *freed = landed + kSlots, *scores = freed + kSlots,
-           *weights = scores + 2, *sums = weights + 2, *queries = sums + 2, *cleared = queries + 1, *drained = cleared + 1;
+           *weights = scores + 2, *sums = weights + 2, *queries = sums + 2, *cleared = queries + 1, *drained = cleared + 1, *turn = drained + 2;
   volatile uint32_t *s_abort = reinterpret_cast<volatile uint32_t *>(sm + OFF_ABORT);
   uint32_t *s_tmem = reinterpret_cast<uint32_t *>(sm + OFF_TMEM);
   uint4 *s_mask = reinterpret_cast<uint4 *>(sm + OFF_MASK);
@@ -257,17 +313,18 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(PrefixArgs p
   uint32_t *status = p.a.status;
   if (tid == 0) {
     for (int i = 0; i < kSlots; ++i) {
-      sm100::mbar_init(&landed[i], maps.box ? 1 : 2);
-      sm100::mbar_init(&freed[i], 1);
+      sm100::mbar_init(&landed[i], 1);
+      sm100::mbar_init(&freed[i], 2);
     }
     for (int i = 0; i < 2; ++i) {
       sm100::mbar_init(&scores[i], 1);
-      sm100::mbar_init(&weights[i], 128);
+      sm100::mbar_init(&weights[i], 8);
+      sm100::mbar_init(&drained[i], 1);
+      sm100::mbar_init(&turn[i], 1);
       sm100::mbar_init(&sums[i], 1);
     }
-    sm100::mbar_init(queries, 256);
+    sm100::mbar_init(queries, kSoftWarps);
     sm100::mbar_init(cleared, 1);
-    sm100::mbar_init(drained, 1);
     *s_abort = 0;
     sm100::fence_mbar_init();
     if (maps.box) {
@@ -292,351 +349,380 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(PrefixArgs p
     }
     w.g = lo;
   }
-  if (warp == 8) {
+  if (warp == kSoftWarps) {
     sm100::tmem_alloc(s_tmem, 512);
     sm100::tmem_relinquish();
   }
   sm100::tc_fence_before();
   __syncthreads();
   sm100::tc_fence_after();
-  const uint32_t tmem = *s_tmem;   // scores (and weights) of a group of threads at 128 s, sums at 256 + 128 s
+  const uint32_t tmem = uniform(*s_tmem);   // scores (and weights) of a group of threads at 128 s, sums at 256 + 128 s
 
-  if (warp < 8) {
-    // ------------------------------------------------------------------ softmax: a row a thread
-    const int s = warp >> 2, r = tid & 127;
+  if (warp < kSoftWarps) {
+    // ------------------------------------------------------------------ softmax: half a row a thread
+    const int s = warp >> 3, hf = (warp >> 2) & 1, r = (warp & 3) * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t t_s = tmem + lanes + 128 * s, t_o = tmem + lanes + 256 + 128 * s;
+    const uint32_t t_s = tmem + lanes + 128 * s, t_o = tmem + lanes + 256 + 128 * s + 64 * hf;
+    const uint32_t lot = 1 + 4 * s + (warp & 3);   // the barrier of the two warps of these rows
+    volatile float *told = reinterpret_cast<volatile float *>(sm + OFF_ROWS) + 128 * s + r;
     // (a negative scale's sign goes to the queries, and so does a scale of 0: masked scores are infinite before they are scaled)
     const float sl2 = (p.a.scale == 0.f ? 1.f : fabsf(p.a.scale)) * kLog2e;
     const uint32_t flip = p.a.scale < 0.f ? 0x80008000u : 0u, keep = p.a.scale == 0.f ? 0u : ~0u;
-    uint32_t phase = 0;   // steps done
+    // the larger (the sum) of what the two halves of a row have
+    const auto both = [&](float x, auto join) {
+      if (hf == 0) *told = x;
+      lot_sync(lot);
+      if (hf) *told = x = join(*told, x);
+      lot_sync(lot);
+      return hf ? x : *told;
+    };
+    uint32_t done = 0;    // steps
     int ring = 0;         // tiles of the blocks before
     while (walk(p, w)) {
       const int row = (w.split ? 0 : 128 * s) + r;   // of the block
       const bool mine = row < w.rows;
       if (!(w.split && s)) {
-        const int rr = w.row0 + row;
+        // 16 rows a warp, two at a time
+        const int r0 = 16 * (warp & 7), q_row = (w.split ? 0 : 128 * s) + r0 + (lane & 15), rr = w.row0 + q_row;
         const int64_t tok = static_cast<int64_t>(w.b0) * p.a.T + rr / p.a.G;
-        const uint16_t *src = p.a.q + tok * p.a.q_stride + (w.h * p.a.G + rr % p.a.G) * kD;
+        const int64_t at = q_row < w.rows ? tok * p.a.q_stride + (w.h * p.a.G + rr % p.a.G) * kD : -1;
         const uint32_t to = smem + OFF_Q + s * kTileBytes;
-#pragma unroll 8
-        for (int c = 0; c < 16; ++c) {
-          uint4 x = make_uint4(0, 0, 0, 0);
-          if (mine) x = *reinterpret_cast<const uint4 *>(src + 8 * c);
-          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to + sm100::swz_offset(128, r, 8 * c)), "r"((x.x ^ flip) & keep),
-                       "r"((x.y ^ flip) & keep), "r"((x.z ^ flip) & keep), "r"((x.w ^ flip) & keep)
-                       : "memory");
+        const int chunk = lane & 15;
+        uint4 x[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int64_t from = __shfl_sync(0xffffffffu, at, 2 * i + (lane >> 4));
+          x[i] = from >= 0 ? *reinterpret_cast<const uint4 *>(p.a.q + from + 8 * chunk) : make_uint4(0, 0, 0, 0);
         }
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to + sm100::swz_offset(128, r0 + 2 * i + (lane >> 4), 8 * chunk)),
+                       "r"((x[i].x ^ flip) & keep), "r"((x[i].y ^ flip) & keep), "r"((x[i].z ^ flip) & keep), "r"((x[i].w ^ flip) & keep)
+                       : "memory");
         sm100::fence_async_smem();
       }
-      sm100::mbar_arrive(queries);
+      __syncwarp();
+      if (lane == 0) sm100::mbar_arrive(queries);
       const int steps = w.split ? (w.tiles + 1 - s) / 2 : w.tiles;
       float m = -INFINITY, l = 0.f;
 #pragma unroll 1
-      for (int j = 0; j < steps; ++j, ++phase) {
-        sm100::wait_or_abort(&scores[s], phase & 1, s_abort, status);
+      for (int j = 0; j < steps; ++j, ++done) {
+        sm100::wait_or_abort(&scores[s], done & 1, s_abort, status);
         sm100::tc_fence_after();
-        uint32_t x[128];
+        const uint2 mask = reinterpret_cast<const uint2 *>(&s_mask[(ring + (w.split ? 2 * j + s : j)) % kRing])[hf];
+        // 64 tokens' scores, their maximum, and with weigh their weights relative to m
+        uint32_t w2[32];
+        float2 sum;
+        const auto pass = [&](auto weigh) {
+          constexpr bool kWeigh = decltype(weigh)::value;
+          const float base = m == -INFINITY ? 0.f : m;   // nothing seen yet: every weight is 2^-inf = 0
+          const float2 k2 = make_float2(sl2, sl2), b2 = make_float2(-base, -base);
+          float top[2] = {-INFINITY, -INFINITY};
+          sum = make_float2(0.f, 0.f);
+          uint32_t x[2][16];
+          sm100::tmem_ld16_async(t_s + 64 * hf, x[0]);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32(t_s + 32 * c, x + 32 * c);
-        const uint4 mask = s_mask[(ring + (w.split ? 2 * j + s : j)) % kRing];
-        sm100::tmem_wait_ld();
-        sm100::tmem_tie<128>(x);
-        if ((mask.x & mask.y & mask.z & mask.w) != ~0u) {
-          const uint32_t word[4] = {mask.x, mask.y, mask.z, mask.w};
+          for (int c = 0; c < 4; ++c) {
+            uint32_t *const y = x[c & 1];
+            sm100::tmem_wait_ld();
+            sm100::tmem_tie<16>(y);
+            if (c < 3) sm100::tmem_ld16_async(t_s + 64 * hf + 16 * (c + 1), x[(c + 1) & 1]);
+            if ((mask.x & mask.y) != ~0u) {
+              const uint32_t word = (c < 2 ? mask.x : mask.y) >> (16 * (c & 1));
 #pragma unroll
-          for (int c = 0; c < 128; ++c)
-            if (!(word[c >> 5] >> (c & 31) & 1)) x[c] = __float_as_uint(-INFINITY);
-        }
-        float top[4];
+              for (int i = 0; i < 16; ++i)
+                if (!(word >> i & 1)) y[i] = __float_as_uint(-INFINITY);
+            }
 #pragma unroll
-        for (int c = 0; c < 4; ++c) top[c] = __uint_as_float(x[c]);
-#pragma unroll
-        for (int c = 4; c < 128; c += 8)
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            top[i] = fmaxf(top[i], c + 4 + i < 128 ? fmaxf(__uint_as_float(x[c + i]), __uint_as_float(x[c + 4 + i]))
-                                                    : __uint_as_float(x[c + i]));
-        const float high = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * sl2;
-        if (j == 0) {
-          m = high;
-        } else {
-          const bool up = high > m + kFollow;
-          if (__any_sync(0xffffffffu, up)) {
-            sm100::wait_or_abort(&sums[s], (phase - 1) & 1, s_abort, status);
-            sm100::tc_fence_after();
-            const float to = up ? high : m, f = m == to ? 1.f : fast_exp2(m - to);
-            l *= f;
-            m = to;
-#pragma unroll 1
-            for (int c = 0; c < 128; c += 16) {
-              float o[16];
-              sm100::tmem_ld16(t_o + c, o);
-#pragma unroll
-              for (int i = 0; i < 16; ++i) o[i] *= f;
-              sm100::tmem_st16(t_o + c, o);
+            for (int i = 0; i < 8; ++i) {
+              const float2 v = make_float2(__uint_as_float(y[2 * i]), __uint_as_float(y[2 * i + 1]));
+              top[i & 1] = fmaxf(top[i & 1], fmaxf(v.x, v.y));
+              if constexpr (kWeigh) {
+                const float2 e = exp2_2(fma2(v, k2, b2));
+                sum = add2(sum, e);
+                w2[8 * c + i] = pack2(e);
+              }
             }
           }
-        }
-        const float base = m == -INFINITY ? 0.f : m;   // nothing seen yet: every weight is 2^-inf = 0
-        float2 part[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-        const float2 k2 = make_float2(sl2, sl2), b2 = make_float2(-base, -base);
-        uint32_t w2[64];
+          return fmaxf(top[0], top[1]) * sl2;
+        };
+        if (j == 0) m = both(pass(std::false_type{}), [](float a, float b) { return fmaxf(a, b); });
+        const float high = pass(std::true_type{});
+        if (lot_any(lot, high > m + kFollow)) {
+          const float top = both(high, [](float a, float b) { return fmaxf(a, b); });
+          const float to = top > m + kFollow ? top : m, f = m == to ? 1.f : fast_exp2(m - to);
+          sm100::wait_or_abort(&sums[s], (done - 1) & 1, s_abort, status);
+          sm100::tc_fence_after();
+          l *= f;
+          m = to;
+#pragma unroll 1
+          for (int c = 0; c < 64; c += 16) {
+            float o[16];
+            sm100::tmem_ld16(t_o + c, o);
 #pragma unroll
-        for (int c = 0; c < 64; ++c) {
-          const float2 e = exp2_2(fma2(make_float2(__uint_as_float(x[2 * c]), __uint_as_float(x[2 * c + 1])), k2, b2));
-          part[c & 1].x += e.x;
-          part[c & 1].y += e.y;
-          w2[c] = pack2(e);
+            for (int i = 0; i < 16; ++i) o[i] *= f;
+            sm100::tmem_st16(t_o + c, o);
+          }
+          pass(std::true_type{});
+          lot_sync(lot);
         }
-        tmem_st32(t_s, w2);
-        tmem_st32(t_s + 32, w2 + 32);
-        l += (part[0].x + part[0].y) + (part[1].x + part[1].y);
+        // (weights go where scores of both halves were: both have read theirs at the barrier above)
+        tmem_st32(t_s + 32 * hf, w2);
+        l += sum.x + sum.y;
         sm100::tmem_wait_st();
         sm100::tc_fence_before();
-        sm100::mbar_arrive(&weights[s]);
+        __syncwarp();
+        if (lane == 0) sm100::mbar_arrive(&weights[s]);
       }
       ring += w.tiles;
       // the piece
-      float *to = p.pieces + (w.piece + (w.split ? s * w.rows : 0) + row) * kPagedPartFloats;
+      l = both(l, [](float a, float b) { return a + b; });
+      float *to = p.pieces + (w.piece + (w.split ? s * w.rows : 0) + row) * kPieceFloats;
       if (steps > 0) {
-        sm100::wait_or_abort(&sums[s], (phase - 1) & 1, s_abort, status);
+        sm100::wait_or_abort(&sums[s], (done - 1) & 1, s_abort, status);
         sm100::tc_fence_after();
-#pragma unroll 1
-        for (int c = 0; c < 128; c += 32) {
-          uint32_t o[32];
+      }
+#pragma unroll
+      for (int c = 0; c < 64; c += 32) {
+        uint32_t o[32];
+        if (steps > 0) {
           tmem_ld32(t_o + c, o);
           sm100::tmem_wait_ld();
           sm100::tmem_tie<32>(o);
-          if (mine)
+        } else {
 #pragma unroll
-            for (int i = 0; i < 32; i += 4)
-              *reinterpret_cast<uint4 *>(to + c + i) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+          for (int i = 0; i < 32; ++i) o[i] = 0;
         }
-      } else if (mine) {
-        for (int c = 0; c < 128; c += 4) *reinterpret_cast<uint4 *>(to + c) = make_uint4(0, 0, 0, 0);
+        if (mine)
+#pragma unroll
+          for (int i = 0; i < 32; i += 8) st_global32(to + 64 * hf + c + i, o + i);
       }
-      if (mine) *reinterpret_cast<float2 *>(to + kD) = make_float2(m, l);
+      if (mine && hf == 0) *reinterpret_cast<float2 *>(to + kD) = make_float2(m, l);
       sm100::tc_fence_before();
-      named_bar_sync<1>(256);   // (the other group's products have read the queries)
+      named_bar_sync<15>(32 * kSoftWarps);   // (the other group's products have read the queries)
     }
-  } else if (warp == 8) {
-    // ------------------------------------------------------------------ products
+  } else if (warp < kSoftWarps + 2) {
+    // ------------------------------------------------------------------ products: a warp for each group
     constexpr uint32_t kIdescS = sm100::idesc_bf16(128, 128, false, false), kIdescO = sm100::idesc_bf16(128, 128, false, true);
-    uint32_t n = 0, items = 0, done[2] = {0, 0};
-    const auto take = [&] {   // the next tile's slot, once it is there
-      const uint32_t slot = n % kSlots;
-      sm100::wait_or_abort(&landed[slot], n / kSlots & 1, s_abort, status);
-      ++n;
-      return slot;
-    };
-    while (walk(p, w)) {
+    const int s = warp - kSoftWarps;
+    const uint32_t t_s = tmem + 128 * s, t_o = tmem + 256 + 128 * s;
+    uint32_t n = 0, items = 0, done = 0, turns = 0;   // tiles of the blocks before; blocks; steps; turns
+    while (uniform(static_cast<int>(walk(p, w)))) {
+      const bool split = uniform(static_cast<int>(w.split));
+      const int tiles = uniform(w.tiles);
+      const Order order(split, tiles);
+      const int steps = order.steps(s, tiles);
+      const uint64_t q = sm100::desc_kmajor_base(smem + OFF_Q + (split ? 0 : s) * kTileBytes);
       sm100::wait_or_abort(queries, items++ & 1, s_abort, status);
-      const int steps[2] = {w.split ? (w.tiles + 1) / 2 : w.tiles, w.split ? w.tiles / 2 : w.tiles};
-      const auto product_s = [&](int s, uint32_t slot) {
-        if (lane == 0) {
-          sm100::tc_fence_after();
-          const uint64_t a = sm100::desc_kmajor_base(smem + OFF_Q + (w.split ? 0 : s) * kTileBytes),
-                         b = sm100::desc_kmajor_base(smem + slot * kTileBytes);
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-            sm100::mma_bf16(tmem + 128 * s, a + sm100::kmajor_step(128, k), b + sm100::kmajor_step(128, k), kIdescS, k > 0);
-          sm100::mma_commit(&scores[s]);
-          if (w.split || s) sm100::mma_commit(&freed[slot]);
-        }
-        __syncwarp();
+      const auto landing = [&](int x) {   // the slot of the block's x-th tile, once it is there
+        const uint32_t i = n + x, slot = i % kSlots;
+        sm100::wait_or_abort(&landed[slot], i / kSlots & 1, s_abort, status);
+        return slot;
       };
-      const auto product_o = [&](int s, uint32_t slot, bool more) {
-        if (lane == 0) {
-          sm100::tc_fence_after();
-          const uint64_t b = sm100::desc_mnmajor_base(smem + slot * kTileBytes, 128);
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-            sm100::mma_bf16_tmem_a(tmem + 256 + 128 * s, tmem + 128 * s + 8 * k, b + sm100::mnmajor_step(k), kIdescO, more || k > 0);
-          sm100::mma_commit(&sums[s]);
-          if (w.split || s) sm100::mma_commit(&freed[slot]);
-        }
-        __syncwarp();
+      const auto free = [&](uint32_t slot) {   // (two arrivals: both groups', or twice the one's that alone has the tile)
+        sm100::mma_commit(&freed[slot]);
+        if (split) sm100::mma_commit(&freed[slot]);
       };
-      uint32_t k = take(), v = 0;
-      product_s(0, k);
-      if (steps[1] > 0) {
-        if (w.split) k = take();
-        product_s(1, k);
-      }
+      // The groups' products go in turn, a sum of the last step's and the scores of the next together: then one's softmax falls
+      // into the other's products.  (Issued side by side both groups wait for their products and for their softmax at once.)
 #pragma unroll 1
-      for (int j = 0; j < steps[0]; ++j) {
-        sm100::wait_or_abort(&weights[0], done[0]++ & 1, s_abort, status);
-        v = take();
-        product_o(0, v, j > 0);
-        if (j + 1 < steps[0]) {
-          k = take();
-          product_s(0, k);
+      for (int j = 0; j <= (split ? order.first : tiles); ++j) {
+        uint32_t k = 0, v = 0;
+        if (j > 0 && j <= steps) {
+          v = landing(order.values(s, j - 1));
+          sm100::wait_or_abort(&weights[s], done++ & 1, s_abort, status);
         }
-        if (j < steps[1]) {
-          sm100::wait_or_abort(&weights[1], done[1]++ & 1, s_abort, status);
-          if (w.split) v = take();
-          product_o(1, v, j > 0);
-          if (j + 1 < steps[1]) {
-            if (w.split) k = take();
-            product_s(1, k);
+        if (j < steps) k = landing(order.keys(s, j));
+        sm100::wait_or_abort(&turn[s], (turns++ + 1 - s) & 1, s_abort, status);   // (the first group's first is given)
+        if (elect()) {
+          sm100::tc_fence_after();
+          if (j > 0 && j <= steps) {
+            const uint64_t b = sm100::desc_mnmajor_base(smem + v * kTileBytes, 128);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sm100::mma_bf16_tmem_a(t_o, t_s + 8 * i, b + sm100::mnmajor_step(i), kIdescO, j > 1 || i > 0);
+            sm100::mma_commit(&sums[s]);
+            free(v);
+          }
+          if (j < steps) {
+            const uint64_t b = sm100::desc_kmajor_base(smem + k * kTileBytes);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sm100::mma_bf16(t_s, q + sm100::kmajor_step(128, i), b + sm100::kmajor_step(128, i), kIdescS, i > 0);
+          }
+          sm100::mbar_arrive(&turn[1 - s]);
+          if (j < steps) {
+            sm100::mma_commit(&scores[s]);
+            free(k);
           }
         }
+        __syncwarp();
       }
+      n += 2 * tiles;
     }
     // (nothing is in flight behind this, after a timeout either)
-    if (lane == 0) sm100::mma_commit(drained);
+    if (elect()) sm100::mma_commit(&drained[s]);
     __syncwarp();
-    sm100::mbar_wait(drained, 0);
-  } else if (warp == 9 || (warp == 10 && !maps.box)) {
-    // ------------------------------------------------------------------ loads
-    const int half = warp - 9, box = maps.box;
-    uint32_t n = 0, fixes = 0, ring = 0;
-    uint32_t pending = 0;   // copies whose arrival is due, at most two
+    sm100::mbar_wait(&drained[s], 0);
+  } else {
+    // ------------------------------------------------------------------ loads: a warp for the keys, one for the values
+    const bool values = warp == kSoftWarps + 3;
+    const int box = maps.box, boxes = box ? kTile / box : 0, lots = box ? 1 : 4;
+    const CUtensorMap *map = values ? &maps.v : &maps.k;
+    const int64_t page_stride = values ? p.a.v_page_stride : p.a.k_page_stride, token_stride = values ? p.a.v_token_stride : p.a.k_token_stride;
+    const int page = p.a.page, page_step = kTile / page, row_step = kTile - page_step * page;   // from a tile to the next
+    uint32_t n = 0, fixes = 0, ring = 0, last = 0;   // tiles of the blocks before; cleared tiles; keys' tiles; the last one asked for
+    bool any = false;
+    // copies whose arrival is due, at most two
+    uint32_t pending = 0, due0 = 0, due1 = 0;
     const auto arrive_copies = [&](uint32_t most) {   // of all but the last `most`
       if (pending <= most) return;
-      if (most) asm volatile("cp.async.wait_group 2;" ::: "memory");
+      if (most) asm volatile("cp.async.wait_group 1;" ::: "memory");
       else asm volatile("cp.async.wait_group 0;" ::: "memory");
       sm100::fence_async_smem();
       __syncwarp();
-      for (; pending > most; --pending)
-        if (lane == 0) sm100::mbar_arrive(&landed[(n - pending) % kSlots]);
+      for (; pending > most; --pending) {
+        if (lane == 0) sm100::mbar_arrive(&landed[due0]);
+        due0 = due1;
+      }
       __syncwarp();
     };
-    struct Ids {
-      int id[2];          // pages of the lane's box (TMA) or of its two rows
-      int tile;
-    };
-    const auto ask = [&](int tile) {
-      Ids x;
-      x.tile = tile;
-      const int32_t *row = p.a.table + static_cast<int64_t>(w.table_row) * p.a.table_stride;
-      if (box) {
-        const int pos = tile * kTile + lane * box;
-        x.id[0] = lane * box < kTile && pos < w.len ? row[pos / p.a.page] : INT_MIN;
-        x.id[1] = INT_MIN;
-      } else {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int pos = tile * kTile + 64 * half + 32 * i + lane;
-          x.id[i] = pos < w.len ? row[pos / p.a.page] : INT_MIN;
-        }
-      }
-      return x;
-    };
     bool stop = false;
-    const auto load = [&](const Ids &x, bool values) {
-      if (stop) return;
-      const uint32_t slot = n % kSlots, dst = smem + slot * kTileBytes;
-      const int pos0 = x.tile * kTile, count = min(kTile, w.len - pos0);
-      const bool ok0 = x.id[0] >= 0 && x.id[0] < p.a.num_pages, ok1 = x.id[1] >= 0 && x.id[1] < p.a.num_pages;
-      if (!values && ((x.id[0] != INT_MIN && !ok0) || (x.id[1] != INT_MIN && !ok1))) atomicOr(status, KDA_DEVICE_BAD_PAGE);
-      const uint32_t on0 = __ballot_sync(0xffffffffu, ok0), on1 = __ballot_sync(0xffffffffu, ok1);
-      if (n >= kSlots) sm100::wait_or_abort(&freed[slot], (n / kSlots - 1) & 1, s_abort, status);
-      if (__any_sync(0xffffffffu, *s_abort != 0)) {
-        stop = true;
-        return;
+    while (!stop && uniform(static_cast<int>(walk(p, w)))) {
+      const bool split = uniform(static_cast<int>(w.split));
+      const int tiles = uniform(w.tiles), first = uniform(w.tile), len = uniform(w.len), head = uniform(w.h);
+      const Order order(split, tiles);
+      const int32_t *table = p.a.table + static_cast<int64_t>(w.table_row) * p.a.table_stride;
+      const uint16_t *base = (values ? p.a.v : p.a.k) + head * (values ? p.a.v_head_stride : p.a.k_head_stride);
+      // page (the place in the table's row) and row in it of the lane's box, or of its four tokens; ids are looked up a tile earlier
+      int at[4], row[4], id[4], next[4] = {INT_MIN, INT_MIN, INT_MIN, INT_MIN};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (i >= lots) break;
+        const int pos = first * kTile + (box ? lane * box : 32 * i + lane);
+        at[i] = pos / page;
+        row[i] = pos - at[i] * page;
       }
-      if (box) {
-        const int boxes = kTile / box;
-        const bool full = on0 == first_bits(boxes) && count == kTile;
-        if (!values && lane < 4) {
-          uint32_t word = 0;
-          for (int t = 0; t < 32; t += 8)
-            if (on0 >> ((32 * lane + t) / box) & 1) word |= 0xFFu << t;
-          reinterpret_cast<uint32_t *>(&s_mask[ring % kRing])[lane] = word & first_bits(count - 32 * lane);
-        }
-        __syncwarp();
-        uint64_t *bar = values && !full ? cleared : &landed[slot];
-        if (lane == 0) sm100::mbar_arrive_expect_tx(bar, __popc(on0) * box * 256);
-        __syncwarp();
-        if (ok0) {
-          const CUtensorMap *map = values ? &maps.v : &maps.k;
-          const int tok = (pos0 + lane * box) % p.a.page;
-          const uint32_t to = dst + lane * box * 128;
-          tma_load_4d(to, map, 0, w.h, tok, x.id[0], bar);
-          tma_load_4d(to + kTileBytes / 2, map, 64, w.h, tok, x.id[0], bar);
-        }
-        __syncwarp();
-        if (bar == cleared) {
-          // weights of 0 do not hide what lies where nothing is: NaN and infinities
-          sm100::wait_or_abort(cleared, fixes++ & 1, s_abort, status);
-          for (int row = lane; row < kTile; row += 32)
-            if (row >= count || !(on0 >> (row / box) & 1))
+      const auto look = [&](int tile) {
 #pragma unroll
-              for (int c = 0; c < 8; ++c) {
-                st_zero16(dst + row * 128 + 16 * c);
-                st_zero16(dst + kTileBytes / 2 + row * 128 + 16 * c);
-              }
-          sm100::fence_async_smem();
-          __syncwarp();
-          if (lane == 0) sm100::mbar_arrive(&landed[slot]);
-          __syncwarp();
+        for (int i = 0; i < 4; ++i) {
+          if (i >= lots) break;
+          const int in_tile = box ? lane * box : 32 * i + lane;
+          next[i] = in_tile < kTile && tile * kTile + in_tile < len ? table[at[i]] : INT_MIN;
         }
-      } else {
-        if (!values && lane < 2)
-          reinterpret_cast<uint32_t *>(&s_mask[ring % kRing])[2 * half + lane] = lane ? on1 : on0;
-        const int64_t ps = values ? p.a.v_page_stride : p.a.k_page_stride, ts = values ? p.a.v_token_stride : p.a.k_token_stride;
-        const uint16_t *base = (values ? p.a.v : p.a.k) + w.h * (values ? p.a.v_head_stride : p.a.k_head_stride);
-        const int chunk = lane & 15;
+      };
+      look(first);
+      for (int x = 0; x < tiles; ++x) {
+        const int tile = first + x, count = min(kTile, len - tile * kTile);
+        int from[4];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const bool ok = i ? ok1 : ok0;
-          const int64_t tok = (pos0 + 64 * half + 32 * i + lane) % p.a.page;
-          const int64_t at = ok ? x.id[i] * ps + tok * ts : -1;
-#pragma unroll 4
-          for (int r = 0; r < 32; r += 2) {
-            const int from = r + (lane >> 4), row = 64 * half + 32 * i + from;
-            const int64_t a = __shfl_sync(0xffffffffu, at, from);
-            const uint32_t to = dst + (chunk >> 3) * (kTileBytes / 2) + row * 128 + (((chunk ^ row) & 7) << 4);
-            if (a >= 0) cp16(to, base + a + 8 * chunk);
-            else if (values) st_zero16(to);
+        for (int i = 0; i < 4; ++i) {
+          if (i >= lots) break;
+          id[i] = next[i];
+          from[i] = row[i];
+          at[i] += page_step;
+          row[i] += row_step;
+          if (row[i] >= page) {
+            row[i] -= page;
+            ++at[i];
           }
         }
-        asm volatile("cp.async.commit_group;" ::: "memory");
-      }
-      ++n;
-      if (!box) {
-        ++pending;
-        arrive_copies(2);
-      }
-      if (!values) ++ring;
-    };
-    while (!stop && walk(p, w)) {
-      if (!w.split) {
-        Ids x = ask(w.tile);
-        for (int j = 0; j < w.tiles; ++j) {
-          load(x, false);
-          const Ids next = j + 1 < w.tiles ? ask(w.tile + j + 1) : x;
-          load(x, true);
-          x = next;
+        if (x + 1 < tiles) look(tile + 1);
+        const int s = split ? x & 1 : 0, j = split ? x >> 1 : x;
+        const uint32_t i = n + (values ? order.values(s, j) : order.keys(s, j)), slot = i % kSlots, dst = smem + slot * kTileBytes;
+        uint32_t on[4] = {0, 0, 0, 0};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          if (k >= lots) break;
+          const bool ok = id[k] >= 0 && id[k] < p.a.num_pages;
+          if (!values && !ok && id[k] != INT_MIN) atomicOr(status, KDA_DEVICE_BAD_PAGE);
+          on[k] = __ballot_sync(0xffffffffu, ok);
         }
-      } else {
-        // as the products take them: keys of both groups, then a group's values and its next keys in turn
-        Ids x = ask(w.tile), y = w.tiles > 1 ? ask(w.tile + 1) : x;
-        load(x, false);
-        if (w.tiles > 1) load(y, false);
-        for (int j = 0; j < w.tiles; j += 2) {
-          const Ids x2 = j + 2 < w.tiles ? ask(w.tile + j + 2) : x, y2 = j + 3 < w.tiles ? ask(w.tile + j + 3) : y;
-          load(x, true);
-          if (j + 2 < w.tiles) load(x2, false);
-          if (j + 1 < w.tiles) load(y, true);
-          if (j + 3 < w.tiles) load(y2, false);
-          x = x2;
-          y = y2;
+        if (i >= kSlots) sm100::wait_or_abort(&freed[slot], (i / kSlots - 1) & 1, s_abort, status);
+        if (__any_sync(0xffffffffu, *s_abort != 0)) {
+          stop = true;
+          break;
+        }
+        any = true;
+        last = i;
+        const bool full = count == kTile && (box ? on[0] == first_bits(boxes) : (on[0] & on[1] & on[2] & on[3]) == ~0u);
+        if (!values) {
+          if (full) {
+            if (lane == 0) s_mask[ring % kRing] = make_uint4(~0u, ~0u, ~0u, ~0u);
+          } else if (lane < 4) {
+            uint32_t word = on[0];
+            if (box) {
+              word = 0;
+              for (int t = 0; t < 32; t += 8)
+                if (on[0] >> ((32 * lane + t) / box) & 1) word |= 0xFFu << t;
+            } else {
+#pragma unroll
+              for (int k = 1; k < 4; ++k)
+                if (lane == k) word = on[k];
+            }
+            reinterpret_cast<uint32_t *>(&s_mask[ring % kRing])[lane] = word & first_bits(count - 32 * lane);
+          }
+          ++ring;
+          __syncwarp();
+        }
+        if (box) {
+          uint64_t *bar = values && !full ? cleared : &landed[slot];
+          // one lane brings all boxes: lanes that each bring their own are served one after another, 150 cycles each
+          const uint32_t there = uniform(on[0]);
+          if (elect()) sm100::mbar_arrive_expect_tx(bar, __popc(there) * box * 256);
+          for (int k = 0; k < boxes; ++k) {
+            const int pg = __shfl_sync(0xffffffffu, id[0], k), r = __shfl_sync(0xffffffffu, from[0], k);
+            if ((there >> k & 1) && elect()) {
+              const uint32_t to = dst + k * box * 128;
+              tma_load_4d(to, map, 0, head, r, pg, bar);
+              tma_load_4d(to + kTileBytes / 2, map, 64, head, r, pg, bar);
+            }
+            __syncwarp();
+          }
+          if (values && !full) {
+            // weights of 0 do not hide what lies where nothing is: NaN and infinities
+            sm100::wait_or_abort(cleared, fixes++ & 1, s_abort, status);
+            for (int k = lane; k < kTile; k += 32)
+              if (k >= count || !(there >> (k / box) & 1))
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                  st_zero16(dst + k * 128 + 16 * c);
+                  st_zero16(dst + kTileBytes / 2 + k * 128 + 16 * c);
+                }
+            sm100::fence_async_smem();
+            __syncwarp();
+            if (lane == 0) sm100::mbar_arrive(&landed[slot]);
+            __syncwarp();
+          }
+        } else {
+          const int chunk = lane & 15;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int64_t mine = on[k] >> lane & 1 ? id[k] * page_stride + from[k] * token_stride : -1;
+#pragma unroll 4
+            for (int r = 0; r < 32; r += 2) {
+              const int lane_of = r + (lane >> 4), to_row = 32 * k + lane_of;
+              const int64_t a = __shfl_sync(0xffffffffu, mine, lane_of);
+              const uint32_t to = dst + (chunk >> 3) * (kTileBytes / 2) + to_row * 128 + (((chunk ^ to_row) & 7) << 4);
+              if (a >= 0) cp16(to, base + a + 8 * chunk);
+              else if (values) st_zero16(to);
+            }
+          }
+          asm volatile("cp.async.commit_group;" ::: "memory");
+          if (pending++) due1 = slot;
+          else due0 = slot;
+          arrive_copies(1);
         }
       }
+      n += 2 * tiles;
     }
     arrive_copies(0);
-    asm volatile("cp.async.wait_all;" ::: "memory");
-    if (*s_abort && box) {   // (what was asked for lands before the CTA ends)
-      for (uint32_t i = n > kSlots ? n - kSlots : 0; i < n; ++i) sm100::mbar_wait(&landed[i % kSlots], i / kSlots & 1);
+    if (*s_abort && box && any) {   // (what was asked for lands before the CTA ends)
+      for (uint32_t i = last >= kSlots ? last - kSlots + 1 : 0; i <= last; ++i) sm100::mbar_wait(&landed[i % kSlots], i / kSlots & 1);
       if (fixes) sm100::mbar_wait(cleared, (fixes - 1) & 1);
     }
     __syncwarp();
   }
   __syncthreads();
-  if (warp == 8) {
+  if (warp == kSoftWarps) {
     sm100::tc_fence_after();
     sm100::tmem_dealloc(tmem, 512);
   }
@@ -701,7 +787,8 @@ __global__ void __launch_bounds__(kJoinThreads, 2) shared_prefix_join_kernel(Pre
         const bool end = mb == y.count - 1;
         const int64_t first = g.unit + h * y.units + static_cast<int64_t>(mb) * (g.tiles + kCost) + kCost;
         const int64_t last = first + (end ? y.last_steps : g.tiles) - 1;
-        const int c0 = static_cast<int>(((first + 1) * stretches - 1) / units), c1 = static_cast<int>(((last + 1) * stretches - 1) / units);
+        const int c0 = static_cast<int>(quotient((first + 1) * stretches - 1, units)),
+                  c1 = static_cast<int>(quotient((last + 1) * stretches - 1, units));
         twice = end && y.split ? 2 : 1;
         second = y.last_rows;
         pieces = (c1 - c0 + 1) * twice;
@@ -710,7 +797,7 @@ __global__ void __launch_bounds__(kJoinThreads, 2) shared_prefix_join_kernel(Pre
       const auto part = [&](int n) -> const float * {
         if (n < pieces) {
           const int c = twice == 2 ? n >> 1 : n;
-          return p.pieces + (base + static_cast<int64_t>(c) * kBlock + (twice == 2 && (n & 1) ? second : 0)) * kPagedPartFloats;
+          return p.pieces + (base + static_cast<int64_t>(c) * kBlock + (twice == 2 && (n & 1) ? second : 0)) * kPieceFloats;
         }
         n -= pieces;
         if (!j.x) return a.rows + at * kPagedPartFloats;
@@ -781,7 +868,7 @@ size_t shared_prefix_bytes(int B, int T, int Hq, int Hk, int groups, uint8_t *ba
   // blocks whose tiles are taken in turn have two pieces a row: one block of at most 128 rows for each group and key head
   const size_t twice = std::min(rows, static_cast<size_t>(std::min(groups, B)) * Hk * (kBlock / 2));
   const size_t sizes[] = {sizeof(PrefixPlan), static_cast<size_t>(groups) * sizeof(PrefixGroup), B * sizeof(int2), rows * row,
-                          (rows + twice + static_cast<size_t>(kMostCtas) * kBlock) * row};
+                          (rows + twice + static_cast<size_t>(kMostCtas) * kBlock) * kPieceFloats * sizeof(float)};
   size_t at[5], end = 0;
   for (int i = 0; i < 5; ++i) {
     at[i] = end;

@@ -6,11 +6,12 @@
 // rows of its own forks.  Bound by latency: lengths, counts, rows.
 //
 // Ending and compacting.  One cluster of CTAs has a bit for each page in each of its CTAs' shared memory (in windows of the ids
-// where there are more).  Its warps take the rows in pieces of 512 places and set the bits of what they hold, each in its own
+// where there are more).  Its warps take the rows in pieces of 256 places and set the bits of what they hold, each in its own
 // CTA's bits (where a prompt's pages are held by many rows, most find their bit set).  Then each CTA joins an equal part of the
-// words through the cluster, counts, and after the counts have gone round writes its part of the lists: places in a list are
-// sums of bits, so the lists are in ascending order whatever came first.  With n pages in use, the i-th one of id n or above goes
-// to the i-th free id below n.  A place of the table finds the number of its id in the list of ids that move, which is sorted.
+// words through the cluster, every CTA fetches all parts and sums the bits before each word, and writes its part of the lists:
+// places in a list are such sums, so the lists are in ascending order whatever came first.  With n pages in use, the i-th one of id
+// n or above goes to the i-th free id below n; a place of the table finds both by the same sums (in windows: in the lists).
+// Bound by latency: lengths, ids, three meetings of the cluster.
 //
 // Copying.  Bound by HBM.  Every CTA lists the pairs of a window that are copies; pieces of 8 KB of them all stand in one line, of
 // which each warp takes every so-manieth.
@@ -122,11 +123,12 @@ __global__ void __launch_bounds__(kForkThreads) fork_requests_kernel(ForkArgs p)
 
 // ---------------------------------------------------------------- pages in use
 constexpr int kThreads = 1024, kWarps = kThreads / 32;
-constexpr int kRanks = 8;                   // CTAs of the cluster
-constexpr int kMostWords = 48 * 1024;       // words of bits (192 KB): windows of 1.5 M ids
-constexpr int kPiece = 512;                 // places of a row that a warp takes
+constexpr int kRanks = 16;                  // CTAs of the cluster (of 8, with half the loads under way: 100 of 512 requests 46 us)
+constexpr int kMostWords = 28 * 1024;       // words of bits: windows of 896 K ids (224 KB with their sums)
+constexpr int kPiece = 256;                 // places of a row that a warp takes: 8 loads a lane, all under way together
 
 __device__ __forceinline__ void cluster_sync() {
+  __syncthreads();   // (whole warps come to the cluster's barrier)
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -134,140 +136,157 @@ __device__ __forceinline__ uint32_t cluster_rank() {
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
   return r;
 }
-// A word of the shared memory of the cluster's CTA `rank`, at this CTA's address of it.
-__device__ __forceinline__ uint32_t peer_word(const uint32_t *p, uint32_t rank) {
-  uint32_t at, v;
+// Four words of the shared memory of the cluster's CTA `rank`, at this CTA's address of them.
+__device__ __forceinline__ uint4 peer_words(const uint32_t *p, uint32_t rank) {
+  uint32_t at;
+  uint4 v;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(sm100::smem_u32(p)), "r"(rank));
-  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+  asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
   return v;
 }
 
-// The table's pieces in turn: f(place of the table's row, its row, places) of each by a warp of the cluster.
+// The table's pieces in turn, by the warps of the cluster: f(row, first place, places, the lane's ids; none of a bad length).
 template <typename F>
 __device__ __forceinline__ void pieces_of(const TableArgs &t, const int32_t *seq_lens, uint32_t rank, bool record, F f) {
-  const int lane = threadIdx.x & 31, w = rank * kWarps + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
   const int per_row = max(1, (t.width + kPiece - 1) / kPiece);
   const int64_t units = static_cast<int64_t>(per_row) * t.B;
-  for (int64_t u = w; u < units; u += kRanks * kWarps) {
-    const int piece = static_cast<int>(u / t.B), b = static_cast<int>(u - static_cast<int64_t>(piece) * t.B);
-    const int pages = pages_of(t, __ldcg(seq_lens + b), record && piece == 0 && lane == 0);
-    const int first = piece * kPiece, n = min(kPiece, pages - first);
-    if (n > 0) f(b, first, n, lane);
+  int64_t u = (threadIdx.x >> 5) * kRanks + rank;   // (few pieces go to all CTAs)
+  const auto row_of = [&](int64_t x, int &piece) {
+    piece = units >> 31 ? static_cast<int>(x / t.B) : static_cast<int>(static_cast<uint32_t>(x) / static_cast<uint32_t>(t.B));
+    // (a long row's pieces go to different warps: each round of pieces begins some rows later)
+    return static_cast<int>((x - static_cast<int64_t>(piece) * t.B + 37ll * piece) % t.B);
+  };
+  int piece = 0, b = 0, len = 0;
+  if (u < units) {
+    b = row_of(u, piece);
+    len = __ldcg(seq_lens + b);
   }
-}
-
-// Sets the bits of the window's ids that the rows hold, joined over the cluster: afterwards words w0 .. w1 of `bits` hold the
-// whole cluster's.  Bits behind the window's last id are set, so that they are no free pages.
-__device__ __forceinline__ void mark(const TableArgs &t, const int32_t *seq_lens, int num_pages, int window, int words, uint32_t *bits,
-                                     uint32_t rank, bool record, int w0, int w1) {
-  const int tid = threadIdx.x;
-  for (int i = tid; i < words; i += kThreads) bits[i] = 0;
-  __syncthreads();
-  const uint32_t span = min(words * 32, num_pages - window);
-  pieces_of(t, seq_lens, rank, record, [&](int b, int first, int n, int lane) {
-    const int32_t *row = t.table + b * t.stride + first;
-#pragma unroll 1
-    for (int e0 = 0; e0 < n; e0 += 128) {
-      int id[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int e = e0 + 32 * j + lane;
-        id[j] = e < n ? row[e] : -2;
-      }
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if (id[j] == -2 && e0 + 32 * j + lane >= n) continue;
-        if (id[j] < 0 || id[j] >= num_pages) {
-          if (record) atomicOr(t.status, KDA_DEVICE_BAD_PAGE);
-          continue;
-        }
-        const uint32_t at = static_cast<uint32_t>(id[j] - window);
-        if (id[j] < window || at >= span) continue;
-        const uint32_t bit = 1u << (at & 31);
-        volatile uint32_t *word = bits + (at >> 5);
-        if (!(*word & bit)) atomicOr(bits + (at >> 5), bit);
-      }
+  while (u < units) {
+    const int pages = pages_of(t, len, record && piece == 0 && lane == 0), first = piece * kPiece, n = min(kPiece, pages - first), row = b;
+    u += kRanks * kWarps;
+    if (u < units) {   // (the next one's length comes beside this one's ids)
+      b = row_of(u, piece);
+      len = __ldcg(seq_lens + b);
     }
-  });
-  cluster_sync();
-  for (int i = w0 + tid; i < w1; i += kThreads) {
-    uint32_t x[kRanks];
+    if (n <= 0) continue;
+    const int32_t *from = t.table + row * t.stride + first;
+    int id[kPiece / 32];
 #pragma unroll
-    for (uint32_t r = 0; r < kRanks; ++r) x[r] = peer_word(bits + i, r);
-#pragma unroll
-    for (uint32_t r = 1; r < kRanks; ++r) x[0] |= x[r];
-    const int valid = static_cast<int>(span) - 32 * i;
-    if (valid < 32) x[0] |= valid <= 0 ? ~0u : ~0u << valid;
-    bits[i] = x[0];   // (no other CTA reads these words of this CTA's)
-  }
-  __syncthreads();
-}
-
-// Ids of the window that `pick(word, its first id)` has bits for, among this CTA's words: counted, or (Emit) written in order
-// from out[base] on.
-template <bool kEmit, typename P>
-__device__ __forceinline__ int pick_ids(const uint32_t *bits, int w0, int w1, int window, int *s_warp, int32_t *out, int64_t base, P pick) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  int total = 0;
-  for (int i0 = w0; i0 < w1; i0 += kThreads) {
-    const int i = i0 + tid;
-    const uint32_t x = i < w1 ? pick(bits[i], window + 32 * i) : 0;
-    const int n = __popc(x), inc = warp_scan(n, lane);
-    if (lane == 31) s_warp[warp] = inc;
-    __syncthreads();
-    int mine = 0, all = 0;
-#pragma unroll 8
-    for (int w = 0; w < kWarps; ++w) {
-      const int c = s_warp[w];
-      mine += w < warp ? c : 0;
-      all += c;
-    }
-    if (kEmit && __any_sync(0xffffffffu, n)) {
-      const int at = mine + inc - n;
-#pragma unroll 1
-      for (int j = 0; j < 32; ++j) {
-        const uint32_t y = __shfl_sync(0xffffffffu, x, j);
-        const int before = __shfl_sync(0xffffffffu, at, j);
-        if (y >> lane & 1)
-          out[base + total + before + __popc(y & ((1u << lane) - 1))] = window + 32 * (i0 + 32 * warp + j) + lane;
-      }
-    }
-    total += all;
-    __syncthreads();
-  }
-  return total;
-}
-
-// Sums of every CTA's counts before this one's, and of all.  (Counts are written by one thread; the caller synchronises before
-// they are written again.)
-__device__ __forceinline__ void exchange(uint32_t *s_count, int count, uint32_t rank, int64_t &before, int64_t &all) {
-  if (threadIdx.x == 0) *s_count = count;
-  cluster_sync();
-  before = all = 0;
-#pragma unroll
-  for (uint32_t r = 0; r < kRanks; ++r) {
-    const uint32_t c = peer_word(s_count, r);
-    before += r < rank ? c : 0;
-    all += c;
+    for (int i = 0; i < kPiece / 32; ++i) id[i] = 32 * i + lane < n ? from[32 * i + lane] : 0;
+    f(row, first, n, id);
   }
 }
 
-struct Part {   // of the bits: this CTA's words of a window
-  int words, w0, w1;
+// The pages in use among the ids of a window: for every word of 32 its bits and how many bits are set before it.  Bits behind the
+// window's last id are clear.
+struct Window {
+  uint32_t *own, *bits;   // what this CTA's warps found; the cluster's
+  uint32_t *before;       // (in the place of own, which is done with by then)
+  int from, words, span;
+  int w0, w1;             // the words whose lists this CTA writes
+  int set;                // bits set in all
 };
-__device__ __forceinline__ Part part_of(int num_pages, int window, int most, uint32_t rank) {
-  Part x;
-  x.words = min(most, (num_pages - window + 31) / 32);
-  const int per = (x.words + kRanks - 1) / kRanks;
+__device__ __forceinline__ Window mark(const TableArgs &t, const int32_t *seq_lens, int num_pages, int from, int most, uint32_t *smem,
+                                       uint32_t *s_warp, uint32_t rank, bool record) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  Window x;
+  x.own = smem;
+  x.bits = smem + most;
+  x.before = smem;
+  x.from = from;
+  x.span = min(32 * most, num_pages - from);
+  x.words = (x.span + 31) / 32;
+  const int per = (x.words + 4 * kRanks - 1) / (4 * kRanks) * 4;   // (16 bytes at a time)
   x.w0 = min(x.words, static_cast<int>(rank) * per);
   x.w1 = min(x.words, x.w0 + per);
+  for (int i = tid; i < ((x.words + 3) & ~3); i += kThreads) x.own[i] = 0;
+  __syncthreads();
+  pieces_of(t, seq_lens, rank, record, [&](int, int, int n, const int (&id)[kPiece / 32]) {
+    bool bad = false;
+    uint32_t at[kPiece / 32], old[kPiece / 32];
+#pragma unroll
+    for (int i = 0; i < kPiece / 32; ++i) {   // (words that are set meanwhile are set again)
+      const bool there = 32 * i + lane < n;
+      bad |= there && (id[i] < 0 || id[i] >= num_pages);
+      at[i] = static_cast<uint32_t>(id[i]) - static_cast<uint32_t>(from);
+      if (!there || id[i] < from || at[i] >= static_cast<uint32_t>(x.span)) at[i] = ~0u;
+      old[i] = at[i] == ~0u ? ~0u : x.own[at[i] >> 5];
+    }
+#pragma unroll
+    for (int i = 0; i < kPiece / 32; ++i) {
+      const uint32_t bit = 1u << (at[i] & 31);
+      if (!(old[i] & bit)) atomicOr(x.own + (at[i] >> 5), bit);
+    }
+    if (record && bad) atomicOr(t.status, KDA_DEVICE_BAD_PAGE);
+  });
+  cluster_sync();
+  // an equal part of the words joined by each CTA, then all parts to all
+  for (int i = x.w0 + 4 * tid; i < x.w1; i += 4 * kThreads) {
+    uint4 y = make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (uint32_t r = 0; r < kRanks; ++r) {
+      const uint4 z = peer_words(x.own + i, r);
+      y.x |= z.x; y.y |= z.y; y.z |= z.z; y.w |= z.w;
+    }
+    *reinterpret_cast<uint4 *>(x.bits + i) = y;
+  }
+  cluster_sync();
+#pragma unroll 4
+  for (int i = 4 * tid; i < x.words; i += 4 * kThreads)
+    if (i < x.w0 || i >= x.w1) *reinterpret_cast<uint4 *>(x.bits + i) = peer_words(x.bits + i, static_cast<uint32_t>(i / per));
+  __syncthreads();
+  // sums of bits: consecutive words a thread
+  const int chunk = (x.words + 4 * kThreads - 1) / (4 * kThreads) * 4, c0 = min(x.words, tid * chunk), c1 = min(x.words, c0 + chunk);
+  int n = 0;
+  for (int i = c0; i < c1; i += 4) {   // (words behind the last of them are clear)
+    const uint4 y = *reinterpret_cast<const uint4 *>(x.bits + i);
+    n += __popc(y.x) + __popc(y.y) + __popc(y.z) + __popc(y.w);
+  }
+  const int inc = warp_scan(n, lane);
+  if (lane == 31) s_warp[warp] = inc;
+  __syncthreads();
+  const int of_warp = s_warp[lane], up_to = warp_scan(of_warp, lane);   // (as many warps as lanes)
+  x.set = __shfl_sync(0xffffffffu, up_to, 31);
+  int sum = inc - n + __shfl_sync(0xffffffffu, up_to - of_warp, warp);
+  for (int i = c0; i < c1; i += 4) {
+    const uint4 y = *reinterpret_cast<const uint4 *>(x.bits + i);
+    const int a = sum + __popc(y.x), b = a + __popc(y.y), c = b + __popc(y.z);
+    *reinterpret_cast<int4 *>(x.before + i) = make_int4(sum, a, b, c);
+    sum = c + __popc(y.w);
+  }
+  __syncthreads();
   return x;
 }
 
-__global__ void __launch_bounds__(kThreads, 1) release_requests_kernel(ReleaseArgs p, int most_words) {
-  extern __shared__ uint32_t s_bits[];
-  __shared__ int s_warp[kWarps];
-  __shared__ uint32_t s_count;
+// Ids of this CTA's words that `pick(word's place)` has bits for, to out[place(word's place)] on: a warp writes a word's ids.
+template <typename P, typename O>
+__device__ __forceinline__ void write_ids(const Window &x, int32_t *out, P pick, O place) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll 4
+  for (int i = x.w0 + (threadIdx.x >> 5); i < x.w1; i += kWarps) {
+    const uint32_t bits = pick(i);
+    if (bits >> lane & 1) out[place(i) + __popc(bits & ((1u << lane) - 1))] = x.from + 32 * i + lane;
+  }
+}
+
+// out[at .. end) = from, from + step, .. by the whole cluster, 16 bytes a store where they are aligned
+__device__ __forceinline__ void fill(int32_t *out, int64_t at, int64_t end, int64_t from, int step, uint32_t rank) {
+  const int64_t head = min(end, at + static_cast<int64_t>((4 - (reinterpret_cast<uintptr_t>(out + at) >> 2 & 3)) & 3));
+  const int64_t quads = (end - head) / 4;
+  const auto value = [&](int64_t i) { return static_cast<int>(from + step * (i - at)); };
+  const int64_t tid = static_cast<int64_t>(rank) * kThreads + threadIdx.x;
+  for (int64_t q = tid; q < quads; q += kRanks * kThreads) {
+    const int64_t i = head + 4 * q;
+    *reinterpret_cast<int4 *>(out + i) = make_int4(value(i), value(i + 1), value(i + 2), value(i + 3));
+  }
+  for (int64_t i = at + tid; i < head; i += kRanks * kThreads) out[i] = value(i);
+  for (int64_t i = head + 4 * quads + tid; i < end; i += kRanks * kThreads) out[i] = value(i);
+}
+
+__global__ void __launch_bounds__(kThreads, 1) release_requests_kernel(ReleaseArgs p, int most) {
+  extern __shared__ uint32_t s_words[];
+  __shared__ uint32_t s_warp[kWarps];
   const int tid = threadIdx.x;
   const uint32_t rank = cluster_rank();
   sm100::grid_dependency_wait();
@@ -279,100 +298,123 @@ __global__ void __launch_bounds__(kThreads, 1) release_requests_kernel(ReleaseAr
   }
   cluster_sync();
   int64_t done = 0;
-  for (int64_t from = 0; from < p.num_pages; from += 32 * most_words) {
-    const int window = static_cast<int>(from);
-    const Part x = part_of(p.num_pages, window, most_words, rank);
-    mark(p.t, p.seq_lens, p.num_pages, window, x.words, s_bits, rank, window == 0, x.w0, x.w1);
-    const auto open = [](uint32_t word, int) { return ~word; };
-    const int mine = pick_ids<false>(s_bits, x.w0, x.w1, window, s_warp, nullptr, 0, open);
-    int64_t before, all;
-    exchange(&s_count, mine, rank, before, all);
-    pick_ids<true>(s_bits, x.w0, x.w1, window, s_warp, p.free_pages, done + before, open);
-    done += all;
-    cluster_sync();   // (counts and bits have been read)
+  for (int64_t from = 0; from < p.num_pages; from += 32 * most) {
+    const Window x = mark(p.t, p.seq_lens, p.num_pages, static_cast<int>(from), most, s_words, s_warp, rank, from == 0);
+    write_ids(
+        x, p.free_pages,
+        [&](int i) {
+          const int left = x.span - 32 * i;
+          return ~x.bits[i] & (left >= 32 ? ~0u : (1u << left) - 1);
+        },
+        [&](int i) { return done + 32 * i - x.before[i]; });
+    done += x.span - x.set;
+    cluster_sync();   // (the bits have been read)
   }
-  for (int64_t i = done + rank * kThreads + tid; i < p.num_pages; i += kRanks * kThreads) p.free_pages[i] = -1;
+  fill(p.free_pages, done, p.num_pages, -1, 0, rank);
   if (rank == 0 && tid == 0) *p.num_free = static_cast<int>(done);
 }
 
-__global__ void __launch_bounds__(kThreads, 1) compact_pages_kernel(CompactArgs p, int most_words) {
-  extern __shared__ uint32_t s_bits[];
-  __shared__ int s_warp[kWarps];
-  __shared__ uint32_t s_count[3];
-  const int tid = threadIdx.x;
+__global__ void __launch_bounds__(kThreads, 1) compact_pages_kernel(CompactArgs p, int most) {
+  extern __shared__ uint32_t s_words[];
+  __shared__ uint32_t s_warp[kWarps];
   const uint32_t rank = cluster_rank();
   sm100::grid_dependency_wait();
   sm100::grid_launch_dependents();
-  const bool once = p.num_pages <= 32 * most_words;
-  // pages in use
-  int64_t open = 0;
-  for (int64_t from = 0; from < p.num_pages; from += 32 * most_words) {
-    const int window = static_cast<int>(from);
-    const Part x = part_of(p.num_pages, window, most_words, rank);
-    mark(p.t, p.seq_lens, p.num_pages, window, x.words, s_bits, rank, window == 0, x.w0, x.w1);
-    const int mine = pick_ids<false>(s_bits, x.w0, x.w1, window, s_warp, nullptr, 0, [](uint32_t word, int) { return ~word; });
-    int64_t before, all;
-    exchange(s_count, mine, rank, before, all);
-    open += all;
+  const bool once = p.num_pages <= 32 * most;
+  Window x{};
+  int64_t set = 0;
+  for (int64_t from = 0; from < p.num_pages; from += 32 * most) {
+    x = mark(p.t, p.seq_lens, p.num_pages, static_cast<int>(from), most, s_words, s_warp, rank, from == 0);
+    set += x.set;
     if (!once) cluster_sync();
   }
-  const int used = static_cast<int>(p.num_pages - open);
-  // bits of a word whose first id is `id` that lie below the number of pages in use
+  const int used = static_cast<int>(set);   // pages in use: those of id `used` and above move
+  // bits of a word whose first id is `id` that lie below it
   const auto below = [&](int id) { return used - id >= 32 ? ~0u : used <= id ? 0u : (1u << (used - id)) - 1; };
-  const auto hole = [&](uint32_t word, int id) { return ~word & below(id); };
-  const auto moves = [&](uint32_t word, int id) {
-    const int left = p.num_pages - id;   // (bits behind the last id are set)
-    return word & ~below(id) & (left >= 32 ? ~0u : (1u << left) - 1);
-  };
-  int64_t holes = 0, moved = 0;
-  for (int64_t from = 0; from < p.num_pages; from += 32 * most_words) {
-    const int window = static_cast<int>(from);
-    const Part x = part_of(p.num_pages, window, most_words, rank);
-    if (!once) mark(p.t, p.seq_lens, p.num_pages, window, x.words, s_bits, rank, false, x.w0, x.w1);
-    const int h = pick_ids<false>(s_bits, x.w0, x.w1, window, s_warp, nullptr, 0, hole);
-    const int m = pick_ids<false>(s_bits, x.w0, x.w1, window, s_warp, nullptr, 0, moves);
-    int64_t h0, h1, m0, m1;
-    exchange(s_count + 1, h, rank, h0, h1);
-    exchange(s_count + 2, m, rank, m0, m1);
-    pick_ids<true>(s_bits, x.w0, x.w1, window, s_warp, p.copy_dst, holes + h0, hole);
-    pick_ids<true>(s_bits, x.w0, x.w1, window, s_warp, p.copy_src, moved + m0, moves);
-    holes += h1;
-    moved += m1;
-    cluster_sync();   // counts and bits have been read, and the lists are there for all
+  int64_t ones = 0, stay = 0, holes = 0;    // set before the window; set below `used`, and clear, as far as the windows went
+  for (int64_t from = 0; from < p.num_pages; from += 32 * most) {
+    if (!once) x = mark(p.t, p.seq_lens, p.num_pages, static_cast<int>(from), most, s_words, s_warp, rank, false);
+    const int in = min(max(used - x.from, 0), x.span);   // ids of the window below `used`
+    const int64_t first_hole = holes, first_one = ones;
+    if (in > 0) {
+      const int w = in >> 5;
+      const int kept = w < x.words ? static_cast<int>(x.before[w]) + __popc(x.bits[w] & ((1u << (in & 31)) - 1)) : x.set;
+      stay += kept;
+      holes += in - kept;
+    }
+    write_ids(
+        x, p.copy_dst, [&](int i) { return ~x.bits[i] & below(x.from + 32 * i); },
+        [&](int i) { return first_hole + 32 * i - x.before[i]; });
+    write_ids(
+        x, p.copy_src, [&](int i) { return x.bits[i] & ~below(x.from + 32 * i); },
+        [&](int i) {   // (a word across `used` counts its own bits below it)
+          return first_one + x.before[i] + __popc(x.bits[i] & below(x.from + 32 * i)) - stay;
+        });
+    ones += x.set;
+    if (!once) cluster_sync();   // the bits have been read, and the lists are there for all
   }
-  const int copies = static_cast<int>(moved);
-  const int at = rank * kThreads + tid, step = kRanks * kThreads;
-  pieces_of(p.t, p.seq_lens, rank, false, [&](int b, int first, int n, int lane) {
-    const int32_t *row = p.t.table + b * p.t.stride + first;
-    int32_t *to = p.new_table + b * p.new_stride + first;
-#pragma unroll 4
-    for (int e = lane; e < n; e += 32) {
-      int id = row[e];
-      if (id >= used && id < p.num_pages) {
-        int lo = 0, hi = copies - 1;   // its number among the ids that move
-        while (lo < hi) {
-          const int mid = (lo + hi) >> 1;
-          if (__ldcg(p.copy_src + mid) < id) lo = mid + 1; else hi = mid;
+  const int copies = static_cast<int>(holes);
+  pieces_of(p.t, p.seq_lens, rank, false, [&](int row, int first, int n, const int (&id)[kPiece / 32]) {
+    const int lane = threadIdx.x & 31;
+    int32_t *to = p.new_table + row * p.new_stride + first;
+#pragma unroll
+    for (int i = 0; i < kPiece / 32; ++i) {
+      if (32 * i + lane >= n) break;
+      int y = id[i];
+      if (y >= used && y < p.num_pages) {
+        if (once) {
+          // its number among the ids that move, then the hole of that number: the last word with no more holes before it
+          int r = static_cast<int>(x.before[y >> 5]) + __popc(x.bits[y >> 5] & ((1u << (y & 31)) - 1)) - static_cast<int>(stay);
+          int lo = 0, hi = (used - 1) >> 5;
+          while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (32 * mid - static_cast<int>(x.before[mid]) <= r) lo = mid; else hi = mid - 1;
+          }
+          r -= 32 * lo - static_cast<int>(x.before[lo]);
+          uint32_t open = ~x.bits[lo];
+          int at = 0;
+#pragma unroll
+          for (int half = 16; half; half >>= 1) {   // the r-th bit set
+            const int c = __popc(open & ((1u << half) - 1));
+            if (c <= r) {
+              r -= c;
+              open >>= half;
+              at += half;
+            }
+          }
+          y = 32 * lo + at;
+        } else {
+          int lo = 0, hi = copies - 1;
+          while (lo < hi) {
+            const int mid = (lo + hi) >> 1;
+            if (__ldcg(p.copy_src + mid) < y) lo = mid + 1; else hi = mid;
+          }
+          if (lo < copies) y = __ldcg(p.copy_dst + lo);
         }
-        if (lo < copies) id = __ldcg(p.copy_dst + lo);
       }
-      to[e] = id;
+      to[32 * i + lane] = y;
     }
   });
-  for (int i = copies + at; i < p.room; i += step) p.copy_src[i] = p.copy_dst[i] = -1;
-  for (int i = at; i < p.num_pages; i += step) p.free_pages[i] = i < open ? used + i : -1;
-  if (at == 0) *p.num_free = static_cast<int>(open);
+  fill(p.copy_src, copies, p.room, -1, 0, rank);
+  fill(p.copy_dst, copies, p.room, -1, 0, rank);
+  const int64_t open = p.num_pages - set;
+  fill(p.free_pages, 0, open, used, 1, rank);
+  fill(p.free_pages, open, p.num_pages, -1, 0, rank);
+  if (rank == 0 && threadIdx.x == 0) *p.num_free = static_cast<int>(open);
+  if (once) cluster_sync();   // (a CTA's bits stay while others read them)
 }
 
 template <typename K, typename A>
 cudaError_t launch_marks(K kernel, std::mutex &mu, uint64_t &done, const A &a, cudaStream_t stream) {
   if (const cudaError_t e = set_attributes_once(mu, done, [&] {
-        return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 4 * kMostWords);
+        cudaError_t r = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 2 * 4 * kMostWords);
+        if (r == cudaSuccess) r = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        return r;
       }))
     return e;
   const int words = static_cast<int>((static_cast<int64_t>(a.num_pages) + 31) / 32);
-  const int most = words < kMostWords ? (words > 0 ? words : 1) : kMostWords;
-  return launch_dependent_clusters(kernel, kRanks, kRanks, kThreads, 4 * most, stream, a, most);
+  const int most = words < kMostWords ? (words > 0 ? (words + 3) & ~3 : 4) : kMostWords;
+  return launch_dependent_clusters(kernel, kRanks, kRanks, kThreads, 2 * 4 * most, stream, a, most);
 }
 
 // ---------------------------------------------------------------- copying

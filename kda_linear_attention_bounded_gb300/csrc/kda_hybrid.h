@@ -99,7 +99,7 @@ bool make_page_map(CUtensorMap *map, const uint16_t *pages, int64_t page_stride,
 // Rows (query heads x new tokens of a key head) that one CTA takes, for `rows` of them.
 int paged_rows_per_item(int rows);
 cudaError_t launch_paged_attention(const PagedArgs &args, cudaStream_t stream);
-// The same over the requests' own tokens; places: CTAs whose joins are written (0: none).
+// The same over the requests' own tokens; places: CTAs whose joins are written.
 cudaError_t launch_paged_own(const PagedArgs &args, int *places, cudaStream_t stream);
 // Checks what kda_paged_attention is given and fills its arguments (with B == 0 it leaves them without the tensors).
 int check_paged(const uint16_t *q, int64_t q_token_stride, const uint16_t *k_pages, int64_t k_page_stride, int64_t k_token_stride,

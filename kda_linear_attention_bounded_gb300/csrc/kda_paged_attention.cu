@@ -134,7 +134,7 @@ __device__ __forceinline__ int request_len(const PagedArgs &p, int b, bool recor
 // The first own token of request b; tiles begin at multiples of their size all the same.
 template <bool kOwn>
 __device__ __forceinline__ int request_start(const PagedArgs &p, int b) {
-  return kOwn ? p.own[b].x : 0;
+  return kOwn ? __ldcg(&p.own[b]).x : 0;
 }
 // Tiles of an item: an empty request keeps one (its rows are written as empty)
 __device__ __forceinline__ int tile_count(int len, int start = 0) { return max(1, (len + kTile - 1) / kTile - start / kTile); }
@@ -204,7 +204,9 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attention_kernel(PagedArgs 
     *s_abort = 0;
     sm100::fence_mbar_init();
   }
-  sm100::grid_dependency_wait();
+  // (The grid before one of own tokens is the prefixes', of which this one reads nothing: it began behind all that this one
+  // does read.  It is waited for at the end, so that the join comes behind both.)
+  if (!kOwn) sm100::grid_dependency_wait();
   sm100::grid_launch_dependents();
 
   // ---- this CTA's stretch of the line of tiles
@@ -333,8 +335,12 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attention_kernel(PagedArgs 
     }
     cluster_sync();   // (a CTA's shared memory stays while others read it)
   };
+  const auto leave = [] {
+    if (kOwn) sm100::grid_dependency_wait();
+  };
   if (none) {
     finish();
+    leave();
     return;
   }
 
@@ -344,6 +350,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attention_kernel(PagedArgs 
     const int half = warp - kComputeWarps;   // copies: rows 32 half + lane; TMA: the first warp's lanes have a box each
     if (half && maps.box) {
       finish();
+      leave();
       return;
     }
     cur.next = cur.b + 1 < p.B ? request_len(p, cur.b + 1) : 0;
@@ -426,6 +433,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attention_kernel(PagedArgs 
       }
     __syncwarp();
     finish();
+    leave();
     return;
   }
 
@@ -677,6 +685,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attention_kernel(PagedArgs 
   }
   __syncwarp();
   finish();
+  leave();
 }
 
 // Joins the parts of the items that the stretches cut.  Every CTA lists the joins (few places hold one) and takes rows of
@@ -792,8 +801,8 @@ cudaError_t launch_paged(PagedArgs a, cudaStream_t stream, int *places = nullptr
   static uint64_t done = 0;
   if (const cudaError_t e = set_attributes_once(mu, done, [] {
         cudaError_t r = cudaFuncSetAttribute(paged_attention_kernel<WR, false, kOwn>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
-        if (r == cudaSuccess)
-          r = cudaFuncSetAttribute(paged_attention_kernel<WR, true, kOwn>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+        if (r == cudaSuccess && !kOwn)
+          r = cudaFuncSetAttribute(paged_attention_kernel<WR, true, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
         return r;
       }))
     return e;
@@ -808,7 +817,8 @@ cudaError_t launch_paged(PagedArgs a, cudaStream_t stream, int *places = nullptr
   // join kernel cost more than the tiles.
   int ranks = kMostRanks;
   while (ranks > 1 && items * ranks > ctas) ranks >>= 1;
-  const bool whole = items * ranks <= ctas && most <= items * ranks * kWholeTiles;
+  // (never of own tokens: where items are so few and short nothing is shared)
+  const bool whole = !kOwn && items * ranks <= ctas && most <= items * ranks * kWholeTiles;
   while (ranks > 1 && most <= items * (ranks >> 1)) ranks >>= 1;   // no more of them than tiles
   a.cluster = ranks;
   const unsigned grid = static_cast<unsigned>(whole ? items * ranks : std::min(most, ctas));
@@ -818,9 +828,9 @@ cudaError_t launch_paged(PagedArgs a, cudaStream_t stream, int *places = nullptr
   if (maps.box < kLeastBox || !make_page_map(&maps.k, a.k, a.k_page_stride, a.k_token_stride, a.k_head_stride, a, maps.box) ||
       !make_page_map(&maps.v, a.v, a.v_page_stride, a.v_token_stride, a.v_head_stride, a, maps.box))
     maps.box = 0;
-  if (kOwn) *places = whole ? 0 : static_cast<int>(grid);
+  if (kOwn) *places = static_cast<int>(grid);
   if (whole)
-    return launch_dependent_clusters(paged_attention_kernel<WR, true, kOwn>, a.cluster, grid, kThreads, kSmemBytes, stream, a, maps);
+    return launch_dependent_clusters(paged_attention_kernel<WR, true, false>, a.cluster, grid, kThreads, kSmemBytes, stream, a, maps);
   const cudaError_t e = launch_dependent(paged_attention_kernel<WR, false, kOwn>, grid, kThreads, kSmemBytes, stream, a, maps);
   if (e != cudaSuccess || kOwn) return e;
   return launch_dependent(paged_join_kernel, std::min(grid * 16 * WR, static_cast<unsigned>(kJoinCtas)), kJoinThreads, 0, stream, a,

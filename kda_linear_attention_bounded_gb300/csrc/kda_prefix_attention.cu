@@ -164,6 +164,7 @@ struct Order {
 
 constexpr int kPlanThreads = 1024;
 __global__ void __launch_bounds__(kPlanThreads) shared_prefix_plan_kernel(PrefixArgs p, int ctas) {
+  __shared__ int4 s_group[kPlanThreads];   // first request, rows of a key head, shared tokens, the request whose table row is read
   __shared__ int64_t s_sum[2][32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   sm100::grid_dependency_wait();
@@ -173,78 +174,83 @@ __global__ void __launch_bounds__(kPlanThreads) shared_prefix_plan_kernel(Prefix
     const int from = p.group_starts[g], to = p.group_starts[g + 1];
     bad |= from < 0 || to < from || to > p.a.B || p.prefix_lens[g] < 0;
   }
-  for (int b = tid; b < p.a.B; b += kPlanThreads) p.own[b] = make_int2(0, -1);
+  // (requests before the first group and behind the last; if the groups are none, all)
+  const int from0 = p.group_starts[0], to0 = p.group_starts[p.groups];
   bad = __syncthreads_or(bad);
   if (bad && tid == 0) atomicOr(p.a.status, KDA_DEVICE_BAD_INDEX);
-  for (int g = warp; g < p.groups; g += kPlanThreads / 32) {
-    const int from = bad ? 0 : p.group_starts[g], to = bad ? 0 : p.group_starts[g + 1];
-    int least = p.a.max_len, count = 0, first = to;
-    for (int b = from + lane; b < to; b += 32) {
-      const int len = length_of(p.a, b);
-      if (len == 0) continue;
-      least = min(least, max(0, len - p.a.T + 1));
-      first = min(first, b);
-      ++count;
-    }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) {
-      least = min(least, __shfl_xor_sync(0xffffffffu, least, o));
-      first = min(first, __shfl_xor_sync(0xffffffffu, first, o));
-      count += __shfl_xor_sync(0xffffffffu, count, o);
-    }
-    const int len = count < 2 ? 0 : min(least, p.prefix_lens[g]);   // (one request alone shares nothing)
-    if (len > 0)
-      for (int b = from + lane; b < to; b += 32)
-        if (length_of(p.a, b) > 0) p.own[b] = make_int2(len, g);
-    if (lane == 0) {
-      PrefixGroup &x = p.group[g];
-      x.b0 = from;
-      x.rows = (to - from) * p.a.T * p.a.G;
-      x.len = len;
-      x.tiles = (len + kTile - 1) / kTile;
-      x.table_row = first;
-    }
-  }
-  __syncthreads();
+  for (int b = tid; b < p.a.B; b += kPlanThreads)
+    if (bad || b < from0 || b >= to0) p.own[b] = make_int2(0, -1);
   int64_t units = 0, rows = 0;   // of the groups before
   for (int g0 = 0; g0 < p.groups; g0 += kPlanThreads) {
+    for (int g = g0 + warp; g < min(p.groups, g0 + kPlanThreads); g += 32) {
+      const int from = bad ? 0 : p.group_starts[g], to = bad ? 0 : p.group_starts[g + 1];
+      int least = p.a.max_len, count = 0, first = to;
+#pragma unroll 4
+      for (int b = from + lane; b < to; b += 32) {
+        const int len = length_of(p.a, b);
+        if (len == 0) continue;
+        least = min(least, max(0, len - p.a.T + 1));
+        first = min(first, b);
+        ++count;
+      }
+#pragma unroll
+      for (int o = 16; o; o >>= 1) {
+        least = min(least, __shfl_xor_sync(0xffffffffu, least, o));
+        first = min(first, __shfl_xor_sync(0xffffffffu, first, o));
+        count += __shfl_xor_sync(0xffffffffu, count, o);
+      }
+      const int len = count < 2 ? 0 : min(least, p.prefix_lens[g]);   // (one request alone shares nothing)
+      for (int b = from + lane; b < to; b += 32)
+        p.own[b] = len > 0 && length_of(p.a, b) > 0 ? make_int2(len, g) : make_int2(0, -1);
+      if (lane == 0) s_group[g - g0] = make_int4(from, (to - from) * p.a.T * p.a.G, len, first);
+    }
+    __syncthreads();
     const int g = g0 + tid;
+    PrefixGroup x{};
     int64_t u = 0, r = 0;
-    if (g < p.groups && p.group[g].len > 0) {
-      const Blocks x = blocks_of(p.group[g].rows, p.group[g].tiles);
-      u = x.units * p.a.Hk;
-      r = x.rows * p.a.Hk;
+    if (g < p.groups) {
+      const int4 y = s_group[tid];
+      x.b0 = y.x;
+      x.rows = y.y;
+      x.len = y.z;
+      x.tiles = (y.z + kTile - 1) / kTile;
+      x.table_row = y.w;
+      if (x.len > 0) {
+        const Blocks z = blocks_of(x.rows, x.tiles);
+        u = z.units * p.a.Hk;
+        r = z.rows * p.a.Hk;
+      }
     }
     int64_t ui = u, ri = r;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int64_t x = __shfl_up_sync(0xffffffffu, ui, o), y = __shfl_up_sync(0xffffffffu, ri, o);
+      const int64_t a = __shfl_up_sync(0xffffffffu, ui, o), b = __shfl_up_sync(0xffffffffu, ri, o);
       if (lane >= o) {
-        ui += x;
-        ri += y;
+        ui += a;
+        ri += b;
       }
     }
-    __syncthreads();
     if (lane == 31) {
       s_sum[0][warp] = ui;
       s_sum[1][warp] = ri;
     }
     __syncthreads();
-    int64_t ub = units + ui - u, rb = rows + ri - r;
-#pragma unroll 8
-    for (int w = 0; w < 32; ++w) {
-      const int64_t x = s_sum[0][w], y = s_sum[1][w];
-      if (w < warp) {
-        ub += x;
-        rb += y;
+    // (as many warps as lanes)
+    const int64_t wu = s_sum[0][lane], wr = s_sum[1][lane];
+    int64_t su = wu, sr = wr;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t a = __shfl_up_sync(0xffffffffu, su, o), b = __shfl_up_sync(0xffffffffu, sr, o);
+      if (lane >= o) {
+        su += a;
+        sr += b;
       }
-      units += x;
-      rows += y;
     }
-    if (g < p.groups) {
-      p.group[g].unit = ub;
-      p.group[g].piece = rb;
-    }
+    x.unit = units + __shfl_sync(0xffffffffu, su - wu, warp) + ui - u;
+    x.piece = rows + __shfl_sync(0xffffffffu, sr - wr, warp) + ri - r;
+    if (g < p.groups) p.group[g] = x;
+    units += __shfl_sync(0xffffffffu, su, 31);
+    rows += __shfl_sync(0xffffffffu, sr, 31);
   }
   if (tid == 0) {
     p.plan->units = units;
@@ -860,6 +866,9 @@ __global__ void __launch_bounds__(kJoinThreads, 2) shared_prefix_join_kernel(Pre
   }
 }
 
+// Measured: see launch_shared_prefix.
+constexpr int64_t kLeastAgain = 64 << 20;
+
 }  // namespace
 
 size_t shared_prefix_bytes(int B, int T, int Hq, int Hk, int groups, uint8_t *base, PrefixArgs *args) {
@@ -887,7 +896,10 @@ size_t shared_prefix_bytes(int B, int T, int Hq, int Hk, int groups, uint8_t *ba
 
 cudaError_t launch_shared_prefix(const PrefixArgs &args, cudaStream_t stream) {
   if (args.a.B <= 0) return cudaSuccess;
-  if (args.groups == 0 || args.a.B == 1 || args.a.num_pages == 0) return launch_paged_attention(args.a, stream);   // nothing is shared
+  // Nothing is shared, or so little that the plan and the join cost more than reading it again: the bytes that the requests
+  // of all groups but one each could read at most.
+  const int64_t again = static_cast<int64_t>(args.a.B - std::min(args.groups, args.a.B)) * args.a.max_len * args.a.Hk * 4 * kD;
+  if (args.groups == 0 || args.a.num_pages == 0 || again < kLeastAgain) return launch_paged_attention(args.a, stream);
   static std::mutex mu;
   static uint64_t done = 0;
   if (const cudaError_t e = set_attributes_once(mu, done, [] {

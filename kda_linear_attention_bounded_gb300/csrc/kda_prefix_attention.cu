@@ -382,7 +382,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(PrefixArgs p
       lot_sync(lot);
       return hf ? x : *told;
     };
-    uint32_t done = 0;    // steps
+    uint32_t done = 0, blocks = 0;   // steps; blocks with some
     int ring = 0;         // tiles of the blocks before
     while (walk(p, w)) {
       const int row = (w.split ? 0 : 128 * s) + r;   // of the block
@@ -457,9 +457,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(PrefixArgs p
         if (lot_any(lot, high > m + kFollow)) {
           const float top = both(high, [](float a, float b) { return fmaxf(a, b); });
           const float to = top > m + kFollow ? top : m, f = m == to ? 1.f : fast_exp2(m - to);
-          sm100::wait_or_abort(&sums[s], (done - 1) & 1, s_abort, status);
-          sm100::tc_fence_after();
-          l *= f;
+          l *= f;   // (the sums are complete: their products come before those of the scores)
           m = to;
 #pragma unroll 1
           for (int c = 0; c < 64; c += 16) {
@@ -485,7 +483,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(PrefixArgs p
       l = both(l, [](float a, float b) { return a + b; });
       float *to = p.pieces + (w.piece + (w.split ? s * w.rows : 0) + row) * kPieceFloats;
       if (steps > 0) {
-        sm100::wait_or_abort(&sums[s], (done - 1) & 1, s_abort, status);
+        sm100::wait_or_abort(&sums[s], blocks++ & 1, s_abort, status);
         sm100::tc_fence_after();
       }
 #pragma unroll
@@ -533,32 +531,30 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(PrefixArgs p
       // into the other's products.  (Issued side by side both groups wait for their products and for their softmax at once.)
 #pragma unroll 1
       for (int j = 0; j <= (split ? order.first : tiles); ++j) {
+        // the weights come last: all else is waited for while they are made
+        const bool sum = j > 0 && j <= steps, next = j < steps;
         uint32_t k = 0, v = 0;
-        if (j > 0 && j <= steps) {
-          v = landing(order.values(s, j - 1));
-          sm100::wait_or_abort(&weights[s], done++ & 1, s_abort, status);
-        }
-        if (j < steps) k = landing(order.keys(s, j));
+        if (sum) v = landing(order.values(s, j - 1));
+        if (next) k = landing(order.keys(s, j));
         sm100::wait_or_abort(&turn[s], (turns++ + 1 - s) & 1, s_abort, status);   // (the first group's first is given)
+        if (sum) sm100::wait_or_abort(&weights[s], done++ & 1, s_abort, status);
         if (elect()) {
           sm100::tc_fence_after();
-          if (j > 0 && j <= steps) {
+          if (sum) {
             const uint64_t b = sm100::desc_mnmajor_base(smem + v * kTileBytes, 128);
 #pragma unroll
             for (int i = 0; i < 8; ++i) sm100::mma_bf16_tmem_a(t_o, t_s + 8 * i, b + sm100::mnmajor_step(i), kIdescO, j > 1 || i > 0);
-            sm100::mma_commit(&sums[s]);
-            free(v);
           }
-          if (j < steps) {
+          if (next) {
             const uint64_t b = sm100::desc_kmajor_base(smem + k * kTileBytes);
 #pragma unroll
             for (int i = 0; i < 8; ++i) sm100::mma_bf16(t_s, q + sm100::kmajor_step(128, i), b + sm100::kmajor_step(128, i), kIdescS, i > 0);
+            sm100::mma_commit(&scores[s]);
           }
           sm100::mbar_arrive(&turn[1 - s]);
-          if (j < steps) {
-            sm100::mma_commit(&scores[s]);
-            free(k);
-          }
+          if (sum && !next) sm100::mma_commit(&sums[s]);   // (else the scores behind them say that the sums are there)
+          if (sum) free(v);
+          if (next) free(k);
         }
         __syncwarp();
       }
@@ -840,10 +836,12 @@ __global__ void __launch_bounds__(kJoinThreads, 2) shared_prefix_join_kernel(Pre
           acc.x += c * x[i].x; acc.y += c * x[i].y; acc.z += c * x[i].z; acc.w += c * x[i].w;
         }
       }
-      s_acc[warp][lane] = acc;
-      if (lane == 0) s_ml[warp] = make_float2(m, l);
+      if (split > 1) {
+        s_acc[warp][lane] = acc;
+        if (lane == 0) s_ml[warp] = make_float2(m, l);
+      }
     }
-    __syncthreads();
+    if (split > 1) __syncthreads();
     if (there && w == 0) {
       float top = m;
       for (int i = 1; i < split; ++i) top = fmaxf(top, s_ml[warp + i].x);
@@ -862,7 +860,7 @@ __global__ void __launch_bounds__(kJoinThreads, 2) shared_prefix_join_kernel(Pre
           make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
       if (a.lse && lane == 0) a.lse[at] = l == 0.f ? -INFINITY : (top + log2f(l)) * 0.6931471805599453f;
     }
-    __syncthreads();
+    if (split > 1) __syncthreads();
   }
 }
 
@@ -923,7 +921,7 @@ cudaError_t launch_shared_prefix(const PrefixArgs &args, cudaStream_t stream) {
   if (const cudaError_t e = launch_paged_own(a, &places, stream)) return e;
   const int64_t rows = static_cast<int64_t>(a.B) * a.T * a.Hk * a.G;
   int split = kJoinWarps;
-  while (split > 2 && rows * split > static_cast<int64_t>(kJoinCtas) * kJoinWarps) split >>= 1;
+  while (split > 1 && rows * split > static_cast<int64_t>(kJoinCtas) * kJoinWarps) split >>= 1;
   const int64_t want = (rows * split + kJoinWarps - 1) / kJoinWarps;
   const int per = paged_rows_per_item(a.T * a.G);
   return launch_dependent(shared_prefix_join_kernel, static_cast<unsigned>(std::min<int64_t>(want, kJoinCtas)), kJoinThreads, 0, stream, args,

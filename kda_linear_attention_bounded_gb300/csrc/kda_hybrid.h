@@ -88,7 +88,8 @@ struct PagedArgs {
   int cluster;                                             // CTAs of an item's cluster (clusters)
   uint32_t *status;
   // own tokens alone (attention over shared prefixes; else null): request b's begin at own[b].x, and what its rows sum up to
-  // is left for a join: rows [B T, Hk G, kPagedPartFloats] of items in one piece, parts of the others
+  // is left for a join: rows [B T, Hk G, kPagedPartFloats], each its sums, maximum and sum of weights, or, of a cut item, behind
+  // them how many parts there are and the first CTA behind the cut
   const int2 *own;
   float *rows;
 };
@@ -99,8 +100,8 @@ bool make_page_map(CUtensorMap *map, const uint16_t *pages, int64_t page_stride,
 // Rows (query heads x new tokens of a key head) that one CTA takes, for `rows` of them.
 int paged_rows_per_item(int rows);
 cudaError_t launch_paged_attention(const PagedArgs &args, cudaStream_t stream);
-// The same over the requests' own tokens; places: CTAs whose joins are written.
-cudaError_t launch_paged_own(const PagedArgs &args, int *places, cudaStream_t stream);
+// The same over the requests' own tokens, without the join.
+cudaError_t launch_paged_own(const PagedArgs &args, cudaStream_t stream);
 // Checks what kda_paged_attention is given and fills its arguments (with B == 0 it leaves them without the tensors).
 int check_paged(const uint16_t *q, int64_t q_token_stride, const uint16_t *k_pages, int64_t k_page_stride, int64_t k_token_stride,
                 int64_t k_head_stride, const uint16_t *v_pages, int64_t v_page_stride, int64_t v_token_stride,

@@ -165,7 +165,7 @@ __device__ __forceinline__ void paged_store_row(const PagedArgs &p, int b, int t
   if constexpr (kOwn) {   // (for the join with what is shared)
     float *part = p.rows + (row * p.Hk * p.G + head) * kPagedPartFloats;
     *reinterpret_cast<float4 *>(part + lane * 4) = acc;
-    if (lane == 0) *reinterpret_cast<float2 *>(part + kD) = make_float2(m, l);
+    if (lane == 0) *reinterpret_cast<float4 *>(part + kD) = make_float4(m, l, 0.f, 0.f);   // (no parts: the row is whole)
     return;
   }
   const float inv = l == 0.f ? 0.f : 1.0f / l;   // a row that sees nothing: zeros
@@ -285,7 +285,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attention_kernel(PagedArgs 
     none = cur.unit >= last;   // (a stretch of an item's first units alone)
   }
   // an item that an earlier CTA began: the CTA at the first cut inside it describes the join
-  if (!kCluster && tid == 0) {
+  if (!kCluster && (kOwn || tid == 0)) {
     int4 j = make_int4(0, 0, 0, 0);
     if (!none && cur.tile > 0) {
       const int64_t begin = cur.unit - cur.tile, end = begin + cur.ntiles;   // the units of the item's tiles
@@ -295,7 +295,18 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attention_kernel(PagedArgs 
         j = make_int4(n + 1, cur.b, cur.hr, 0);
       }
     }
-    p.joins[blockIdx.x] = j;
+    if (!kOwn) {
+      p.joins[blockIdx.x] = j;
+    } else if (j.x) {
+      // each of the item's rows says how many parts it has, and where the cut is
+      const int rb = j.z % p.row_blocks, h = j.z / p.row_blocks;
+      for (int r = tid; r < kRows; r += kThreads) {
+        const int row = rb * kRows + r, t = row / p.G;
+        if (t >= p.T) break;
+        const int64_t at = (static_cast<int64_t>(j.y) * p.T + t) * p.Hk * p.G + h * p.G + row % p.G;
+        *reinterpret_cast<float2 *>(p.rows + at * kPagedPartFloats + kD + 2) = make_float2(__int_as_float(j.x), __int_as_float(blockIdx.x));
+      }
+    }
   }
   // A cluster's end: its CTAs' rows (channels in stage 0, maximum and weights beside) are joined in the order of their
   // tokens, each CTA taking every ranks-th row.  All threads of the cluster come here.
@@ -794,9 +805,8 @@ constexpr int kWholeTiles = 4;
 // 109 us against 95 us by asynchronous copies, of 16 and more 90 to 92 us (copies by one warp instead of two: 133 us).
 constexpr int kLeastBox = 16;
 
-// places: of the joins that the caller has to make (kOwn)
 template <int WR, bool kOwn>
-cudaError_t launch_paged(PagedArgs a, cudaStream_t stream, int *places = nullptr) {
+cudaError_t launch_paged(PagedArgs a, cudaStream_t stream) {
   static std::mutex mu;
   static uint64_t done = 0;
   if (const cudaError_t e = set_attributes_once(mu, done, [] {
@@ -828,7 +838,6 @@ cudaError_t launch_paged(PagedArgs a, cudaStream_t stream, int *places = nullptr
   if (maps.box < kLeastBox || !make_page_map(&maps.k, a.k, a.k_page_stride, a.k_token_stride, a.k_head_stride, a, maps.box) ||
       !make_page_map(&maps.v, a.v, a.v_page_stride, a.v_token_stride, a.v_head_stride, a, maps.box))
     maps.box = 0;
-  if (kOwn) *places = static_cast<int>(grid);
   if (whole)
     return launch_dependent_clusters(paged_attention_kernel<WR, true, false>, a.cluster, grid, kThreads, kSmemBytes, stream, a, maps);
   const cudaError_t e = launch_dependent(paged_attention_kernel<WR, false, kOwn>, grid, kThreads, kSmemBytes, stream, a, maps);
@@ -865,11 +874,11 @@ cudaError_t launch_paged_attention(const PagedArgs &a, cudaStream_t stream) {
   }
 }
 
-cudaError_t launch_paged_own(const PagedArgs &a, int *places, cudaStream_t stream) {
+cudaError_t launch_paged_own(const PagedArgs &a, cudaStream_t stream) {
   switch (paged_rows_per_item(a.T * a.G)) {
-    case 16: return launch_paged<1, true>(a, stream, places);
-    case 32: return launch_paged<2, true>(a, stream, places);
-    default: return launch_paged<4, true>(a, stream, places);
+    case 16: return launch_paged<1, true>(a, stream);
+    case 32: return launch_paged<2, true>(a, stream);
+    default: return launch_paged<4, true>(a, stream);
   }
 }
 

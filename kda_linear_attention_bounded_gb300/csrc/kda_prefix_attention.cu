@@ -731,67 +731,48 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(PrefixArgs p
 }
 
 // ---------------------------------------------------------------- the join
-// The parts of a row: its own tokens' (one, or those of the stretches that cut its item), and the pieces of its group's prefix.
-// split warps take a row's parts in turn, four under way together, and meet in shared memory.
-constexpr int kJoinThreads = 512, kJoinWarps = kJoinThreads / 32, kJoinCtas = 304;
-static_assert(kPagedMaxCtas <= kJoinThreads, "a place a thread");
-__global__ void __launch_bounds__(kJoinThreads, 2) shared_prefix_join_kernel(PrefixArgs p, int rows_per_item, int row_blocks, int places,
-                                                                             int split) {
-  __shared__ int4 s_join[kPagedMaxCtas];
-  __shared__ int s_count[kJoinWarps];
-  __shared__ float4 s_acc[kJoinWarps][32];
-  __shared__ float2 s_ml[kJoinWarps];
+// The parts of a row: the pieces of its group's prefix, then its own tokens' (one, or those of the stretches that cut its item).
+// 16 lanes take a row, eight channels each, four parts under way together; where rows are few, split lots of 16 lanes a row, which
+// meet in shared memory.  Bound by the latency of the request, its group, the parts and the row, so as many rows as can be go at
+// once.
+constexpr int kJoinThreads = 256, kJoinLots = kJoinThreads / 16, kJoinCtas = 3 * kMostCtas;
+__device__ __forceinline__ void add_part(float (&acc)[8], float c, const float4 (&x)[2]) {
+  acc[0] += c * x[0].x; acc[1] += c * x[0].y; acc[2] += c * x[0].z; acc[3] += c * x[0].w;
+  acc[4] += c * x[1].x; acc[5] += c * x[1].y; acc[6] += c * x[1].z; acc[7] += c * x[1].w;
+}
+__global__ void __launch_bounds__(kJoinThreads, 3) shared_prefix_join_kernel(PrefixArgs p, int rows_per_item, int split) {
+  __shared__ float4 s_acc[kJoinLots][16][2];
+  __shared__ float2 s_ml[kJoinLots];
   const PagedArgs &a = p.a;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int tid = threadIdx.x, lane = tid & 15, lot = tid >> 4;
   sm100::grid_dependency_wait();
   sm100::grid_launch_dependents();
-  int4 cut = static_cast<int>(threadIdx.x) < places ? a.joins[threadIdx.x] : make_int4(0, 0, 0, 0);
-  cut.w = threadIdx.x;
-  const uint32_t on = __ballot_sync(0xffffffffu, cut.x != 0);
-  if (lane == 0) s_count[warp] = __popc(on);
-  __syncthreads();
-  int joins = 0;
-#pragma unroll
-  for (int i = 0; i < kJoinWarps; ++i) {
-    if (i == warp && cut.x != 0) s_join[joins + __popc(on & ((1u << lane) - 1))] = cut;
-    joins += s_count[i];
-  }
-  __syncthreads();
-  const int Hq = a.Hk * a.G;
+  const int Hq = a.Hk * a.G, per_cta = kJoinLots / split, w = lot & (split - 1);
   const int64_t rows = static_cast<int64_t>(a.B) * a.T * Hq, units = p.plan->units, stretches = p.plan->stretches;
-  const int per_cta = kJoinWarps / split, w = warp & (split - 1);
   for (int64_t at0 = static_cast<int64_t>(per_cta) * blockIdx.x; at0 < rows; at0 += static_cast<int64_t>(per_cta) * gridDim.x) {
-    const int64_t at = at0 + warp / split;
+    const int64_t at = at0 + lot / split;
     const bool there = at < rows;
+    const int64_t tok = quotient(there ? at : 0, Hq);
+    const int head = static_cast<int>((there ? at : 0) - tok * Hq), b = static_cast<int>(tok) / a.T, t = static_cast<int>(tok) - b * a.T;
     float m = -INFINITY, l = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    const int64_t tok = at / Hq;
-    const int head = static_cast<int>(at - tok * Hq), b = static_cast<int>(tok / a.T), t = static_cast<int>(tok - static_cast<int64_t>(b) * a.T);
+    float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     if (there) {
-      const int h = head / a.G, row = t * a.G + head % a.G;
       const int2 own = p.own[b];
-      // own tokens: the item's stretches, if it was cut
-      const int hr = h * row_blocks + row / rows_per_item, r = row % rows_per_item;
-      int4 j = make_int4(0, 0, 0, 0);
-      for (int i0 = 0; i0 < joins; i0 += 32) {
-        const int4 x = i0 + lane < joins ? s_join[i0 + lane] : make_int4(0, -1, 0, 0);
-        const uint32_t hit = __ballot_sync(0xffffffffu, x.y == b && x.z == hr);
-        if (hit) j = s_join[i0 + __ffs(hit) - 1];
-      }
-      const int mine = j.x ? j.x : 1;
+      const float4 end = *reinterpret_cast<const float4 *>(a.rows + at * kPagedPartFloats + kD);
+      const int h = head / a.G, row = t * a.G + head - h * a.G, parts = __float_as_int(end.z), cut = __float_as_int(end.w);
       // the prefix: the stretches that hold steps of the block, two pieces each where the groups of threads took its tiles in turn
       int64_t base = 0;
       int pieces = 0, twice = 1, second = 0;
       if (own.y >= 0) {
         const PrefixGroup &g = p.group[own.y];
         const Blocks y = blocks_of(g.rows, g.tiles);
-        const int rr = static_cast<int>((tok - static_cast<int64_t>(g.b0) * a.T) * a.G) + head % a.G, mb = rr / kBlock;
-        const bool end = mb == y.count - 1;
+        const int rr = (b - g.b0) * a.T * a.G + row, mb = rr / kBlock;
+        const bool last_block = mb == y.count - 1;
         const int64_t first = g.unit + h * y.units + static_cast<int64_t>(mb) * (g.tiles + kCost) + kCost;
-        const int64_t last = first + (end ? y.last_steps : g.tiles) - 1;
+        const int64_t last = first + (last_block ? y.last_steps : g.tiles) - 1;
         const int c0 = static_cast<int>(quotient((first + 1) * stretches - 1, units)),
                   c1 = static_cast<int>(quotient((last + 1) * stretches - 1, units));
-        twice = end && y.split ? 2 : 1;
+        twice = last_block && y.split ? 2 : 1;
         second = y.last_rows;
         pieces = (c1 - c0 + 1) * twice;
         base = g.piece + h * y.rows + mb * kBlock + static_cast<int64_t>(c0) * kBlock + rr % kBlock;
@@ -802,24 +783,25 @@ __global__ void __launch_bounds__(kJoinThreads, 2) shared_prefix_join_kernel(Pre
           return p.pieces + (base + static_cast<int64_t>(c) * kBlock + (twice == 2 && (n & 1) ? second : 0)) * kPieceFloats;
         }
         n -= pieces;
-        if (!j.x) return a.rows + at * kPagedPartFloats;
+        if (!parts) return a.rows + at * kPagedPartFloats;
         // part 0: the stretch before the cut, in its last slot; part n: the n-th stretch from the cut on, in its first
-        const int slot = n == 0 ? 2 * (j.w - 1) + 1 : 2 * (j.w + n - 1);
-        return a.parts + (static_cast<size_t>(slot) * rows_per_item + r) * kPagedPartFloats;
+        const int slot = n == 0 ? 2 * (cut - 1) + 1 : 2 * (cut + n - 1);
+        return a.parts + (static_cast<size_t>(slot) * rows_per_item + row % rows_per_item) * kPagedPartFloats;
       };
-      const int count = pieces + mine;
+      const int count = pieces + (parts ? parts : 1);
       for (int n0 = w; n0 < count; n0 += 4 * split) {
         float2 ml[4];
-        float4 x[4];
+        float4 x[4][2];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int n = n0 + i * split;
           ml[i] = make_float2(-INFINITY, 0.f);
-          x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+          x[i][0] = x[i][1] = make_float4(0.f, 0.f, 0.f, 0.f);
           if (n < count) {
-            const float *q = part(n);
-            ml[i] = *reinterpret_cast<const float2 *>(q + kD);
-            x[i] = *reinterpret_cast<const float4 *>(q + lane * 4);
+            const float *from = part(n);
+            ml[i] = *reinterpret_cast<const float2 *>(from + kD);
+            x[i][0] = *reinterpret_cast<const float4 *>(from + lane * 4);
+            x[i][1] = *reinterpret_cast<const float4 *>(from + 64 + lane * 4);
           }
         }
         float top = m;
@@ -827,37 +809,40 @@ __global__ void __launch_bounds__(kJoinThreads, 2) shared_prefix_join_kernel(Pre
         for (int i = 0; i < 4; ++i) top = fmaxf(top, ml[i].x);
         const float from = top == -INFINITY ? 0.f : top, c0 = fast_exp2(m - from);
         l *= c0;
-        acc = make_float4(c0 * acc.x, c0 * acc.y, c0 * acc.z, c0 * acc.w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc[i] *= c0;
         m = top;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const float c = fast_exp2(ml[i].x - from);
           l += c * ml[i].y;
-          acc.x += c * x[i].x; acc.y += c * x[i].y; acc.z += c * x[i].z; acc.w += c * x[i].w;
+          add_part(acc, c, x[i]);
         }
       }
       if (split > 1) {
-        s_acc[warp][lane] = acc;
-        if (lane == 0) s_ml[warp] = make_float2(m, l);
+        s_acc[lot][lane][0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+        s_acc[lot][lane][1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
+        if (lane == 0) s_ml[lot] = make_float2(m, l);
       }
     }
     if (split > 1) __syncthreads();
     if (there && w == 0) {
       float top = m;
-      for (int i = 1; i < split; ++i) top = fmaxf(top, s_ml[warp + i].x);
+      for (int i = 1; i < split; ++i) top = fmaxf(top, s_ml[lot + i].x);
       const float from = top == -INFINITY ? 0.f : top, c0 = fast_exp2(m - from);
       l *= c0;
-      acc = make_float4(c0 * acc.x, c0 * acc.y, c0 * acc.z, c0 * acc.w);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) acc[i] *= c0;
       for (int i = 1; i < split; ++i) {
-        const float2 ml = s_ml[warp + i];
-        const float4 x = s_acc[warp + i][lane];
+        const float2 ml = s_ml[lot + i];
         const float c = fast_exp2(ml.x - from);
         l += c * ml.y;
-        acc.x += c * x.x; acc.y += c * x.y; acc.z += c * x.z; acc.w += c * x.w;
+        add_part(acc, c, s_acc[lot + i][lane]);
       }
       const float inv = l == 0.f ? 0.f : 1.0f / l;   // a row that sees nothing: zeros
-      *reinterpret_cast<uint2 *>(a.out + tok * a.out_stride + static_cast<int64_t>(head) * kD + lane * 4) =
-          make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+      uint16_t *to = a.out + tok * a.out_stride + static_cast<int64_t>(head) * kD + lane * 4;
+      *reinterpret_cast<uint2 *>(to) = make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv));
+      *reinterpret_cast<uint2 *>(to + 64) = make_uint2(pack_bf16x2(acc[4] * inv, acc[5] * inv), pack_bf16x2(acc[6] * inv, acc[7] * inv));
       if (a.lse && lane == 0) a.lse[at] = l == 0.f ? -INFINITY : (top + log2f(l)) * 0.6931471805599453f;
     }
     if (split > 1) __syncthreads();
@@ -917,15 +902,13 @@ cudaError_t launch_shared_prefix(const PrefixArgs &args, cudaStream_t stream) {
       !make_page_map(&maps.v, a.v, a.v_page_stride, a.v_token_stride, a.v_head_stride, a, maps.box))
     maps.box = 0;
   if (const cudaError_t e = launch_dependent(shared_prefix_kernel, ctas, kThreads, kSmemBytes, stream, args, maps)) return e;
-  int places = 0;
-  if (const cudaError_t e = launch_paged_own(a, &places, stream)) return e;
+  if (const cudaError_t e = launch_paged_own(a, stream)) return e;
   const int64_t rows = static_cast<int64_t>(a.B) * a.T * a.Hk * a.G;
-  int split = kJoinWarps;
-  while (split > 1 && rows * split > static_cast<int64_t>(kJoinCtas) * kJoinWarps) split >>= 1;
-  const int64_t want = (rows * split + kJoinWarps - 1) / kJoinWarps;
-  const int per = paged_rows_per_item(a.T * a.G);
+  int split = kJoinLots;
+  while (split > 1 && rows * split > static_cast<int64_t>(kJoinCtas) * kJoinLots) split >>= 1;
+  const int64_t want = (rows * split + kJoinLots - 1) / kJoinLots;
   return launch_dependent(shared_prefix_join_kernel, static_cast<unsigned>(std::min<int64_t>(want, kJoinCtas)), kJoinThreads, 0, stream, args,
-                          per, (a.T * a.G + per - 1) / per, places, split);
+                          paged_rows_per_item(a.T * a.G), split);
 }
 
 }  // namespace kda

@@ -849,8 +849,11 @@ __global__ void __launch_bounds__(kJoinThreads, 3) shared_prefix_join_kernel(Pre
   }
 }
 
-// Measured: see launch_shared_prefix.
-constexpr int64_t kLeastAgain = 64 << 20;
+// Bytes of prefixes that requests could read again, from which on they are shared.  The table's width bounds them; the host knows
+// no lengths.  Measured, alone against shared (one group, own tokens to 200): 16 requests x 4096 tokens (64 MB) 17.9 and 20.8 us, 16 x
+// 16384 (122 MB) 23.6 and 23.4, 64 x 4096 (134 MB) 24.5 and 22.3, 4 x 16384 (195 MB) 36 and 28, 64 x 4096 (268 MB) 38 and 29, 64 x
+// 16384 (1 GB) 111 and 34; more requests with shorter prefixes cross later (64 x 256, 126 MB: 22 and 32; 192 x 1024, 239 MB: 35 and 33).
+constexpr int64_t kLeastAgain = 128 << 20;
 
 }  // namespace
 

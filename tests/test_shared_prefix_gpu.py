@@ -55,8 +55,12 @@ def make(groups, T, hq, hk, page, seed, alone=0, share_pages=True, std=1.5, widt
     for a, b, n in copies:
         k[a, :n], v[a, :n] = k[b, :n], v[b, :n]
     # (a table as wide as a long context's, so that the call is not taken for one with next to nothing to share)
-    width = width or max([len(x) for x in rows] + [150000 // page])
-    table = i32([x + [-5] * (width - len(x)) for x in rows])
+    tokens = (1 << 28) // (512 * hk * max(1, len(rows) - len(groups)))
+    width = width or max([len(x) for x in rows] + [tokens // page + 1])
+    table = torch.full((len(rows), width), -5, dtype=torch.int32)
+    for b, x in enumerate(rows):
+        table[b, :len(x)] = torch.tensor(x, dtype=torch.int32)
+    table = table.cuda()
     q = (std * torch.randn((len(rows) * T, hq, D), generator=g)).bfloat16().cuda()
     return [q, k.cuda(), v.cuda(), table, i32(lens), i32(prefix), i32(starts)]
 

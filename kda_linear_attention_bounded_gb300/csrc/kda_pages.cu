@@ -10,7 +10,7 @@
 // CTA's bits (where a prompt's pages are held by many rows, most find their bit set).  Then each CTA joins an equal part of the
 // words through the cluster, every CTA fetches all parts and sums the bits before each word, and writes its part of the lists:
 // places in a list are such sums, so the lists are in ascending order whatever came first.  With n pages in use, the i-th one of id
-// n or above goes to the i-th free id below n; a place of the table finds both by the same sums (in windows: in the lists).
+// n or above goes to the i-th free id below n; a place of the table finds its number by the same sums (in windows: in the list).
 // Bound by latency: lengths, ids, three meetings of the cluster.
 //
 // Copying.  Bound by HBM.  Every CTA lists the pairs of a window that are copies; pieces of 8 KB of them all stand in one line, of
@@ -123,7 +123,7 @@ __global__ void __launch_bounds__(kForkThreads) fork_requests_kernel(ForkArgs p)
 
 // ---------------------------------------------------------------- pages in use
 constexpr int kThreads = 1024, kWarps = kThreads / 32;
-constexpr int kRanks = 16;                  // CTAs of the cluster (of 8, with half the loads under way: 100 of 512 requests 46 us)
+constexpr int kMostRanks = 16;              // CTAs of the cluster
 constexpr int kMostWords = 28 * 1024;       // words of bits: windows of 896 K ids (224 KB with their sums)
 constexpr int kPiece = 256;                 // places of a row that a warp takes: 8 loads a lane, all under way together
 
@@ -134,6 +134,11 @@ __device__ __forceinline__ void cluster_sync() {
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
   return r;
 }
 // Four words of the shared memory of the cluster's CTA `rank`, at this CTA's address of them.
@@ -148,10 +153,10 @@ __device__ __forceinline__ uint4 peer_words(const uint32_t *p, uint32_t rank) {
 // The table's pieces in turn, by the warps of the cluster: f(row, first place, places, the lane's ids; none of a bad length).
 template <typename F>
 __device__ __forceinline__ void pieces_of(const TableArgs &t, const int32_t *seq_lens, uint32_t rank, bool record, F f) {
-  const int lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31, ranks = cluster_size();
   const int per_row = max(1, (t.width + kPiece - 1) / kPiece);
   const int64_t units = static_cast<int64_t>(per_row) * t.B;
-  int64_t u = (threadIdx.x >> 5) * kRanks + rank;   // (few pieces go to all CTAs)
+  int64_t u = (threadIdx.x >> 5) * ranks + rank;   // (few pieces go to all CTAs)
   const auto row_of = [&](int64_t x, int &piece) {
     piece = units >> 31 ? static_cast<int>(x / t.B) : static_cast<int>(static_cast<uint32_t>(x) / static_cast<uint32_t>(t.B));
     // (a long row's pieces go to different warps: each round of pieces begins some rows later)
@@ -164,7 +169,7 @@ __device__ __forceinline__ void pieces_of(const TableArgs &t, const int32_t *seq
   }
   while (u < units) {
     const int pages = pages_of(t, len, record && piece == 0 && lane == 0), first = piece * kPiece, n = min(kPiece, pages - first), row = b;
-    u += kRanks * kWarps;
+    u += ranks * kWarps;
     if (u < units) {   // (the next one's length comes beside this one's ids)
       b = row_of(u, piece);
       len = __ldcg(seq_lens + b);
@@ -189,7 +194,7 @@ struct Window {
 };
 __device__ __forceinline__ Window mark(const TableArgs &t, const int32_t *seq_lens, int num_pages, int from, int most, uint32_t *smem,
                                        uint32_t *s_warp, uint32_t rank, bool record) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, ranks = cluster_size();
   Window x;
   x.own = smem;
   x.bits = smem + most;
@@ -197,7 +202,7 @@ __device__ __forceinline__ Window mark(const TableArgs &t, const int32_t *seq_le
   x.from = from;
   x.span = min(32 * most, num_pages - from);
   x.words = (x.span + 31) / 32;
-  const int per = (x.words + 4 * kRanks - 1) / (4 * kRanks) * 4;   // (16 bytes at a time)
+  const int per = (x.words + 4 * ranks - 1) / (4 * ranks) * 4;   // (16 bytes at a time)
   x.w0 = min(x.words, static_cast<int>(rank) * per);
   x.w1 = min(x.words, x.w0 + per);
   for (int i = tid; i < ((x.words + 3) & ~3); i += kThreads) x.own[i] = 0;
@@ -225,8 +230,8 @@ __device__ __forceinline__ Window mark(const TableArgs &t, const int32_t *seq_le
   for (int i = x.w0 + 4 * tid; i < x.w1; i += 4 * kThreads) {
     uint4 y = make_uint4(0, 0, 0, 0);
 #pragma unroll
-    for (uint32_t r = 0; r < kRanks; ++r) {
-      const uint4 z = peer_words(x.own + i, r);
+    for (uint32_t r = 0; r < kMostRanks; ++r) {
+      const uint4 z = peer_words(x.own + i, min(r, static_cast<uint32_t>(ranks) - 1));   // (all under way together)
       y.x |= z.x; y.y |= z.y; y.z |= z.z; y.w |= z.w;
     }
     *reinterpret_cast<uint4 *>(x.bits + i) = y;
@@ -272,16 +277,17 @@ __device__ __forceinline__ void write_ids(const Window &x, int32_t *out, P pick,
 
 // out[at .. end) = from, from + step, .. by the whole cluster, 16 bytes a store where they are aligned
 __device__ __forceinline__ void fill(int32_t *out, int64_t at, int64_t end, int64_t from, int step, uint32_t rank) {
+  const int64_t threads = static_cast<int64_t>(cluster_size()) * kThreads;
   const int64_t head = min(end, at + static_cast<int64_t>((4 - (reinterpret_cast<uintptr_t>(out + at) >> 2 & 3)) & 3));
   const int64_t quads = (end - head) / 4;
   const auto value = [&](int64_t i) { return static_cast<int>(from + step * (i - at)); };
   const int64_t tid = static_cast<int64_t>(rank) * kThreads + threadIdx.x;
-  for (int64_t q = tid; q < quads; q += kRanks * kThreads) {
+  for (int64_t q = tid; q < quads; q += threads) {
     const int64_t i = head + 4 * q;
     *reinterpret_cast<int4 *>(out + i) = make_int4(value(i), value(i + 1), value(i + 2), value(i + 3));
   }
-  for (int64_t i = at + tid; i < head; i += kRanks * kThreads) out[i] = value(i);
-  for (int64_t i = head + 4 * quads + tid; i < end; i += kRanks * kThreads) out[i] = value(i);
+  for (int64_t i = at + tid; i < head; i += threads) out[i] = value(i);
+  for (int64_t i = head + 4 * quads + tid; i < end; i += threads) out[i] = value(i);
 }
 
 __global__ void __launch_bounds__(kThreads, 1) release_requests_kernel(ReleaseArgs p, int most) {
@@ -291,7 +297,7 @@ __global__ void __launch_bounds__(kThreads, 1) release_requests_kernel(ReleaseAr
   const uint32_t rank = cluster_rank();
   sm100::grid_dependency_wait();
   sm100::grid_launch_dependents();
-  for (int i = rank * kThreads + tid; i < p.num_rows; i += kRanks * kThreads) {
+  for (int i = rank * kThreads + tid; i < p.num_rows; i += cluster_size() * kThreads) {
     const int row = p.rows[i];
     if (row >= p.t.B) atomicOr(p.t.status, KDA_DEVICE_BAD_INDEX);
     else if (row >= 0) p.seq_lens[row] = 0;
@@ -351,49 +357,33 @@ __global__ void __launch_bounds__(kThreads, 1) compact_pages_kernel(CompactArgs 
           return first_one + x.before[i] + __popc(x.bits[i] & below(x.from + 32 * i)) - stay;
         });
     ones += x.set;
-    if (!once) cluster_sync();   // the bits have been read, and the lists are there for all
+    cluster_sync();   // the bits have been read, and the lists are there for all
   }
   const int copies = static_cast<int>(holes);
   pieces_of(p.t, p.seq_lens, rank, false, [&](int row, int first, int n, const int (&id)[kPiece / 32]) {
     const int lane = threadIdx.x & 31;
     int32_t *to = p.new_table + row * p.new_stride + first;
+    int y[kPiece / 32];
 #pragma unroll
     for (int i = 0; i < kPiece / 32; ++i) {
-      if (32 * i + lane >= n) break;
-      int y = id[i];
-      if (y >= used && y < p.num_pages) {
-        if (once) {
-          // its number among the ids that move, then the hole of that number: the last word with no more holes before it
-          int r = static_cast<int>(x.before[y >> 5]) + __popc(x.bits[y >> 5] & ((1u << (y & 31)) - 1)) - static_cast<int>(stay);
-          int lo = 0, hi = (used - 1) >> 5;
-          while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (32 * mid - static_cast<int>(x.before[mid]) <= r) lo = mid; else hi = mid - 1;
-          }
-          r -= 32 * lo - static_cast<int>(x.before[lo]);
-          uint32_t open = ~x.bits[lo];
-          int at = 0;
-#pragma unroll
-          for (int half = 16; half; half >>= 1) {   // the r-th bit set
-            const int c = __popc(open & ((1u << half) - 1));
-            if (c <= r) {
-              r -= c;
-              open >>= half;
-              at += half;
-            }
-          }
-          y = 32 * lo + at;
-        } else {
-          int lo = 0, hi = copies - 1;
-          while (lo < hi) {
-            const int mid = (lo + hi) >> 1;
-            if (__ldcg(p.copy_src + mid) < y) lo = mid + 1; else hi = mid;
-          }
-          if (lo < copies) y = __ldcg(p.copy_dst + lo);
+      y[i] = id[i];
+      if (32 * i + lane >= n || id[i] < used || id[i] >= p.num_pages) continue;
+      int at = 0;   // its number among the ids that move
+      if (once) {
+        const int w = id[i] >> 5;
+        at = static_cast<int>(x.before[w]) + __popc(x.bits[w] & ((1u << (id[i] & 31)) - 1)) - static_cast<int>(stay);
+      } else {
+        int hi = copies - 1;
+        while (at < hi) {
+          const int mid = (at + hi) >> 1;
+          if (__ldcg(p.copy_src + mid) < id[i]) at = mid + 1; else hi = mid;
         }
       }
-      to[32 * i + lane] = y;
+      if (at < copies) y[i] = __ldcg(p.copy_dst + at);
     }
+#pragma unroll
+    for (int i = 0; i < kPiece / 32; ++i)
+      if (32 * i + lane < n) to[32 * i + lane] = y[i];
   });
   fill(p.copy_src, copies, p.room, -1, 0, rank);
   fill(p.copy_dst, copies, p.room, -1, 0, rank);
@@ -401,8 +391,11 @@ __global__ void __launch_bounds__(kThreads, 1) compact_pages_kernel(CompactArgs 
   fill(p.free_pages, 0, open, used, 1, rank);
   fill(p.free_pages, open, p.num_pages, -1, 0, rank);
   if (rank == 0 && threadIdx.x == 0) *p.num_free = static_cast<int>(open);
-  if (once) cluster_sync();   // (a CTA's bits stay while others read them)
 }
+
+// Places of the table up to which one CTA, or four, have fewer meetings to pay for than loads.  Measured (release; tables of 2048,
+// 8192, 32960 and 961536 places): one CTA 6.4, 9.5, 16.8 and 271 us, four 7.5, 8.3, 10.0 and 83, sixteen 8.9, 9.2, 10.0 and 35.
+constexpr int64_t kPlacesOfOne = 1 << 12, kPlacesOfFour = 1 << 14;
 
 template <typename K, typename A>
 cudaError_t launch_marks(K kernel, std::mutex &mu, uint64_t &done, const A &a, cudaStream_t stream) {
@@ -414,7 +407,9 @@ cudaError_t launch_marks(K kernel, std::mutex &mu, uint64_t &done, const A &a, c
     return e;
   const int words = static_cast<int>((static_cast<int64_t>(a.num_pages) + 31) / 32);
   const int most = words < kMostWords ? (words > 0 ? (words + 3) & ~3 : 4) : kMostWords;
-  return launch_dependent_clusters(kernel, kRanks, kRanks, kThreads, 2 * 4 * most, stream, a, most);
+  const int64_t places = static_cast<int64_t>(a.t.B) * a.t.width;
+  const unsigned ranks = places <= kPlacesOfOne ? 1 : places <= kPlacesOfFour ? 4 : kMostRanks;
+  return launch_dependent_clusters(kernel, ranks, ranks, kThreads, 2 * 4 * most, stream, a, most);
 }
 
 // ---------------------------------------------------------------- copying

@@ -148,10 +148,12 @@ __global__ void __launch_bounds__(32 * kWarps) rotary_to_pages_kernel(RotaryArgs
 
 cudaError_t launch_rotary_to_pages(const RotaryArgs &a, cudaStream_t stream) {
   if (a.tokens <= 0) return cudaSuccess;
-  // a token is split until there are 16 warps for each SM or one turn is left for each
+  // A token's rows are split until there are 64 warps for each SM or one turn of rows is left for each.  (Measured, 9001 tokens of
+  // 48 rows: up to 16, 64, 128 and 256 warps 39.7, 38.7, 41.5 and 51.4 us: at first the last wave counts, then the functions, which
+  // every warp of a token computes for itself.)
   const int turns = (a.Hq + 2 * a.Hk + 3) / 4;
   int parts = 1;
-  while (parts < turns && static_cast<int64_t>(a.tokens) * parts < 152 * 16) parts *= 2;
+  while (parts < turns && static_cast<int64_t>(a.tokens) * parts < 152 * 64) parts *= 2;
   parts = parts < turns ? parts : turns;
   const int64_t items = static_cast<int64_t>(a.tokens) * parts;
   return launch_dependent(rotary_to_pages_kernel, static_cast<unsigned>((items + kWarps - 1) / kWarps), 32 * kWarps, 0, stream, a,

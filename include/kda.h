@@ -736,9 +736,15 @@ KDA_API int kda_copy_pages(const kda_page_buffer *buffers, int num_buffers, int 
  *  workspace     kda_shared_prefix_workspace_size(B, T, Hq, Hk, num_groups) bytes; no
  *                part of it needs clearing.  Concurrent calls need separate ones.
  *
- * Device-side findings as in kda_paged_attention; starts that do not ascend or
- * leave 0 .. B, or a negative prefix length, make every request attend alone
- * (KDA_DEVICE_BAD_INDEX).  Results do not depend on timing.
+ * Calls that could read less than 128 MB of prefixes again (by B, num_groups and
+ * the table's width) let every request attend alone, which is faster there, and
+ * do not look at the groups.
+ *
+ * Device-side findings as in kda_paged_attention; where the groups are looked at,
+ * starts that do not ascend or leave 0 .. B, or a negative prefix length, make
+ * every request attend alone (KDA_DEVICE_BAD_INDEX).  Results do not depend on
+ * timing.  What a row joins (the prefix in pieces, its own tokens) depends on the
+ * batch, so its last bits do, too.
  */
 KDA_API size_t kda_shared_prefix_workspace_size(int B, int T, int Hq, int Hk, int num_groups);
 

@@ -121,10 +121,17 @@ constexpr uint32_t kMostRanks = 8;   // CTAs of a cluster
 constexpr int kItemCost = 4;   // (0 where there is a CTA for every tile)
 constexpr int kLastTile = 1 << 30;   // with the head and row block: the stretch ends here
 
+// What the grid before may not have waited for on this SM comes from L2 (kOwn, see the kernel's beginning).
+template <bool kOwn, typename T>
+__device__ __forceinline__ T fresh_of(const T *p) {
+  if constexpr (kOwn) return __ldcg(p);
+  else return *p;
+}
 // Tokens of request b; a length that is none, or that its table row cannot hold, counts as 0 (and is recorded, by the
 // thread whose part it is).
+template <bool kOwn>
 __device__ __forceinline__ int request_len(const PagedArgs &p, int b, bool record = false) {
-  const int len = p.seq_lens[b];
+  const int len = fresh_of<kOwn>(p.seq_lens + b);
   if (len < 0 || len > p.max_len) {
     if (record) atomicOr(p.status, KDA_DEVICE_BAD_COUNT);
     return 0;
@@ -152,7 +159,7 @@ __device__ __forceinline__ void advance(const PagedArgs &p, Cursor &c, int items
   c.start = c.next_start;
   c.ntiles = tile_count(c.len, c.start);
   if (c.b + 1 < p.B) {
-    c.next = request_len(p, c.b + 1);
+    c.next = request_len<kOwn>(p, c.b + 1);
     c.next_start = request_start<kOwn>(p, c.b + 1);
   }
 }
@@ -219,7 +226,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attention_kernel(PagedArgs 
     const int item = blockIdx.x / ranks;
     cur.b = item / ipr;
     cur.hr = item % ipr;
-    cur.len = request_len(p, cur.b, tid == 0);
+    cur.len = request_len<kOwn>(p, cur.b, tid == 0);
     cur.start = request_start<kOwn>(p, cur.b);
     cur.ntiles = tile_count(cur.len, cur.start);
     cur.cost = 0;
@@ -232,7 +239,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attention_kernel(PagedArgs 
     const int per = (p.B + kThreads - 1) / kThreads;
     const int b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
     int64_t sum = 0;
-    for (int b = b0; b < b1; ++b) sum += tile_count(request_len(p, b, true), request_start<kOwn>(p, b));
+    for (int b = b0; b < b1; ++b) sum += tile_count(request_len<kOwn>(p, b, true), request_start<kOwn>(p, b));
     int64_t inc = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -261,7 +268,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attention_kernel(PagedArgs 
       int b = b0;
       int64_t at = before;
       while (true) {
-        const int64_t n = static_cast<int64_t>(cur.cost + tile_count(request_len(p, b), request_start<kOwn>(p, b))) * ipr;
+        const int64_t n = static_cast<int64_t>(cur.cost + tile_count(request_len<kOwn>(p, b), request_start<kOwn>(p, b))) * ipr;
         if (first < at + n) break;
         at += n;
         ++b;
@@ -274,7 +281,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attention_kernel(PagedArgs 
   bool none = first >= last;
   if (!kCluster && !none) {
     cur.b = static_cast<int>(s_scan[6]);
-    cur.len = request_len(p, cur.b);
+    cur.len = request_len<kOwn>(p, cur.b);
     cur.start = request_start<kOwn>(p, cur.b);
     cur.ntiles = tile_count(cur.len, cur.start);
     const int per_item = cur.cost + cur.ntiles;
@@ -364,7 +371,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attention_kernel(PagedArgs 
       leave();
       return;
     }
-    cur.next = cur.b + 1 < p.B ? request_len(p, cur.b + 1) : 0;
+    cur.next = cur.b + 1 < p.B ? request_len<kOwn>(p, cur.b + 1) : 0;
     cur.next_start = cur.b + 1 < p.B ? request_start<kOwn>(p, cur.b + 1) : 0;
     const int at = lane + 32 * half;
     int id = 0;
@@ -372,7 +379,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attention_kernel(PagedArgs 
     auto ask = [&] {   // the pages of the tile at the cursor
       const int pos = (cur.start / kTile + cur.tile) * kTile + at * box;
       there = at < boxes && pos < cur.len;
-      id = there ? p.table[static_cast<int64_t>(cur.b) * p.table_stride + pos / p.page] : 0;
+      id = there ? fresh_of<kOwn>(p.table + static_cast<int64_t>(cur.b) * p.table_stride + pos / p.page) : 0;
     };
     ask();
     for (int i = 0; ; ++i) {
@@ -474,8 +481,8 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attention_kernel(PagedArgs 
       const uint16_t *src = p.q + (static_cast<int64_t>(cur.b) * p.T + t) * p.q_stride + (h * p.G + row % p.G) * kD + t4 * 2;
 #pragma unroll
       for (int kk = 0; kk < 8; ++kk) {
-        qf[kk][s] = t < p.T ? *reinterpret_cast<const uint32_t *>(src + kk * 16) : 0u;
-        qf[kk][s + 2] = t < p.T ? *reinterpret_cast<const uint32_t *>(src + kk * 16 + 8) : 0u;
+        qf[kk][s] = t < p.T ? fresh_of<kOwn>(reinterpret_cast<const uint32_t *>(src + kk * 16)) : 0u;
+        qf[kk][s + 2] = t < p.T ? fresh_of<kOwn>(reinterpret_cast<const uint32_t *>(src + kk * 16 + 8)) : 0u;
       }
       m2[s] = -INFINITY;
       l2[s] = 0.f;

@@ -736,7 +736,7 @@ KDA_API int kda_copy_pages(const kda_page_buffer *buffers, int num_buffers, int 
  *  workspace     kda_shared_prefix_workspace_size(B, T, Hq, Hk, num_groups) bytes; no
  *                part of it needs clearing.  Concurrent calls need separate ones.
  *
- * Calls that could read less than 128 MB of prefixes again (by B, num_groups and
+ * Calls that could read less than 160 MB of prefixes again (by B, num_groups and
  * the table's width) let every request attend alone, which is faster there, and
  * do not look at the groups.
  *

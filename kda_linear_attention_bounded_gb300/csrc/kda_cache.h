@@ -74,7 +74,8 @@ struct PrefixGroup {         // of the plan: a group's place in the line of work
 };
 struct PrefixPlan {
   int64_t units;
-  int stretches, pad;
+  int stretches;
+  int ticket;                // of the own tokens' stretches
 };
 struct PrefixArgs {
   PagedArgs a;               // own, rows: for the requests' own tokens

@@ -92,6 +92,7 @@ struct PagedArgs {
   // them how many parts there are and the first CTA behind the cut
   const int2 *own;
   float *rows;
+  int *ticket;                                             // 0 at the beginning: stretches taken
 };
 // The cache's pages as [page, token, head, 128], boxes of 64 channels x `box` tokens; false: the strides or sizes are none that
 // a tensor map takes.

@@ -121,17 +121,10 @@ constexpr uint32_t kMostRanks = 8;   // CTAs of a cluster
 constexpr int kItemCost = 4;   // (0 where there is a CTA for every tile)
 constexpr int kLastTile = 1 << 30;   // with the head and row block: the stretch ends here
 
-// What the grid before may not have waited for on this SM comes from L2 (kOwn, see the kernel's beginning).
-template <bool kOwn, typename T>
-__device__ __forceinline__ T fresh_of(const T *p) {
-  if constexpr (kOwn) return __ldcg(p);
-  else return *p;
-}
 // Tokens of request b; a length that is none, or that its table row cannot hold, counts as 0 (and is recorded, by the
 // thread whose part it is).
-template <bool kOwn>
 __device__ __forceinline__ int request_len(const PagedArgs &p, int b, bool record = false) {
-  const int len = fresh_of<kOwn>(p.seq_lens + b);
+  const int len = p.seq_lens[b];
   if (len < 0 || len > p.max_len) {
     if (record) atomicOr(p.status, KDA_DEVICE_BAD_COUNT);
     return 0;
@@ -141,7 +134,7 @@ __device__ __forceinline__ int request_len(const PagedArgs &p, int b, bool recor
 // The first own token of request b; tiles begin at multiples of their size all the same.
 template <bool kOwn>
 __device__ __forceinline__ int request_start(const PagedArgs &p, int b) {
-  return kOwn ? __ldcg(&p.own[b]).x : 0;
+  return kOwn ? p.own[b].x : 0;
 }
 // Tiles of an item: an empty request keeps one (its rows are written as empty)
 __device__ __forceinline__ int tile_count(int len, int start = 0) { return max(1, (len + kTile - 1) / kTile - start / kTile); }
@@ -159,7 +152,7 @@ __device__ __forceinline__ void advance(const PagedArgs &p, Cursor &c, int items
   c.start = c.next_start;
   c.ntiles = tile_count(c.len, c.start);
   if (c.b + 1 < p.B) {
-    c.next = request_len<kOwn>(p, c.b + 1);
+    c.next = request_len(p, c.b + 1);
     c.next_start = request_start<kOwn>(p, c.b + 1);
   }
 }
@@ -214,19 +207,22 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attention_kernel(PagedArgs 
   // (The grid before one of own tokens is the prefixes', of which this one reads nothing: it began behind all that this one
   // does read.  It is waited for at the end, so that the join comes behind both.)
   if (!kOwn) sm100::grid_dependency_wait();
+  else __threadfence();   // (nothing that this SM has read before those)
   sm100::grid_launch_dependents();
 
   // ---- this CTA's stretch of the line of tiles
   int64_t *s_scan = reinterpret_cast<int64_t *>(sm + OFF_SCAN);   // [6] warp sums, then the start's request and tile
   int64_t first = 0, last = 0, total = 0;
   int stretches = 0;   // CTAs with units: every one of them has at least one
+  int b0 = 0;          // this thread's requests begin there, and their units
+  int64_t before = 0, sum = 0;
   Cursor cur;
   const uint32_t ranks = kCluster ? p.cluster : 1, rank = blockIdx.x % ranks;
   if constexpr (kCluster) {
     const int item = blockIdx.x / ranks;
     cur.b = item / ipr;
     cur.hr = item % ipr;
-    cur.len = request_len<kOwn>(p, cur.b, tid == 0);
+    cur.len = request_len(p, cur.b, tid == 0);
     cur.start = request_start<kOwn>(p, cur.b);
     cur.ntiles = tile_count(cur.len, cur.start);
     cur.cost = 0;
@@ -237,9 +233,9 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attention_kernel(PagedArgs 
     __syncthreads();
   } else {
     const int per = (p.B + kThreads - 1) / kThreads;
-    const int b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
-    int64_t sum = 0;
-    for (int b = b0; b < b1; ++b) sum += tile_count(request_len<kOwn>(p, b, true), request_start<kOwn>(p, b));
+    b0 = min(p.B, tid * per);
+    const int b1 = min(p.B, b0 + per);
+    for (int b = b0; b < b1; ++b) sum += tile_count(request_len(p, b, true), request_start<kOwn>(p, b));
     int64_t inc = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -248,7 +244,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attention_kernel(PagedArgs 
     }
     if (lane == 31) s_scan[warp] = inc;
     __syncthreads();
-    int64_t before = inc - sum;
+    before = inc - sum;
 #pragma unroll
     for (int w = 0; w < kThreads / 32; ++w) {
       if (w < warp) before += s_scan[w];
@@ -259,16 +255,21 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attention_kernel(PagedArgs 
     before = (before + static_cast<int64_t>(cur.cost) * b0) * ipr;
     sum = (sum + static_cast<int64_t>(cur.cost) * (b1 - b0)) * ipr;
     stretches = static_cast<int>(min(total, static_cast<int64_t>(gridDim.x)));
-    if (blockIdx.x < stretches) {
-      first = total * blockIdx.x / stretches;
-      last = total * (blockIdx.x + 1) / stretches;
+  }
+  int tiles_done = 0;       // of the stretches before this one
+  uint32_t meetings = 0;
+  const auto run = [&](int64_t stretch) {
+  if constexpr (!kCluster) {
+    if (stretch < stretches) {
+      first = total * stretch / stretches;
+      last = total * (stretch + 1) / stretches;
     }
     // the thread whose requests hold the first tile walks to it
     if (first < last && first >= before && first < before + sum) {
       int b = b0;
       int64_t at = before;
       while (true) {
-        const int64_t n = static_cast<int64_t>(cur.cost + tile_count(request_len<kOwn>(p, b), request_start<kOwn>(p, b))) * ipr;
+        const int64_t n = static_cast<int64_t>(cur.cost + tile_count(request_len(p, b), request_start<kOwn>(p, b))) * ipr;
         if (first < at + n) break;
         at += n;
         ++b;
@@ -281,7 +282,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attention_kernel(PagedArgs 
   bool none = first >= last;
   if (!kCluster && !none) {
     cur.b = static_cast<int>(s_scan[6]);
-    cur.len = request_len<kOwn>(p, cur.b);
+    cur.len = request_len(p, cur.b);
     cur.start = request_start<kOwn>(p, cur.b);
     cur.ntiles = tile_count(cur.len, cur.start);
     const int per_item = cur.cost + cur.ntiles;
@@ -296,14 +297,14 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attention_kernel(PagedArgs 
     int4 j = make_int4(0, 0, 0, 0);
     if (!none && cur.tile > 0) {
       const int64_t begin = cur.unit - cur.tile, end = begin + cur.ntiles;   // the units of the item's tiles
-      if (total * (blockIdx.x - 1) / stretches <= begin) {
+      if (total * (stretch - 1) / stretches <= begin) {
         int n = 1;   // stretches behind the first that begin before the item's end
-        while (blockIdx.x + n < stretches && total * (blockIdx.x + n) / stretches < end) ++n;
+        while (stretch + n < stretches && total * (stretch + n) / stretches < end) ++n;
         j = make_int4(n + 1, cur.b, cur.hr, 0);
       }
     }
     if (!kOwn) {
-      p.joins[blockIdx.x] = j;
+      p.joins[stretch] = j;
     } else if (j.x) {
       // each of the item's rows says how many parts it has, and where the cut is
       const int rb = j.z % p.row_blocks, h = j.z / p.row_blocks;
@@ -311,7 +312,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attention_kernel(PagedArgs 
         const int row = rb * kRows + r, t = row / p.G;
         if (t >= p.T) break;
         const int64_t at = (static_cast<int64_t>(j.y) * p.T + t) * p.Hk * p.G + h * p.G + row % p.G;
-        *reinterpret_cast<float2 *>(p.rows + at * kPagedPartFloats + kD + 2) = make_float2(__int_as_float(j.x), __int_as_float(blockIdx.x));
+        *reinterpret_cast<float2 *>(p.rows + at * kPagedPartFloats + kD + 2) = make_float2(__int_as_float(j.x), __int_as_float(static_cast<int>(stretch)));
       }
     }
   }
@@ -353,12 +354,8 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attention_kernel(PagedArgs 
     }
     cluster_sync();   // (a CTA's shared memory stays while others read it)
   };
-  const auto leave = [] {
-    if (kOwn) sm100::grid_dependency_wait();
-  };
   if (none) {
     finish();
-    leave();
     return;
   }
 
@@ -368,10 +365,9 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attention_kernel(PagedArgs 
     const int half = warp - kComputeWarps;   // copies: rows 32 half + lane; TMA: the first warp's lanes have a box each
     if (half && maps.box) {
       finish();
-      leave();
       return;
     }
-    cur.next = cur.b + 1 < p.B ? request_len<kOwn>(p, cur.b + 1) : 0;
+    cur.next = cur.b + 1 < p.B ? request_len(p, cur.b + 1) : 0;
     cur.next_start = cur.b + 1 < p.B ? request_start<kOwn>(p, cur.b + 1) : 0;
     const int at = lane + 32 * half;
     int id = 0;
@@ -379,10 +375,11 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attention_kernel(PagedArgs 
     auto ask = [&] {   // the pages of the tile at the cursor
       const int pos = (cur.start / kTile + cur.tile) * kTile + at * box;
       there = at < boxes && pos < cur.len;
-      id = there ? fresh_of<kOwn>(p.table + static_cast<int64_t>(cur.b) * p.table_stride + pos / p.page) : 0;
+      id = there ? p.table[static_cast<int64_t>(cur.b) * p.table_stride + pos / p.page] : 0;
     };
     ask();
-    for (int i = 0; ; ++i) {
+    int i = tiles_done;
+    for (;; ++i) {
       const int st = i % kStages, pos0 = (cur.start / kTile + cur.tile) * kTile, h = cur.hr / p.row_blocks;
       const uint64_t before = kOwn ? first_tokens(cur.start - pos0) : 0;   // tokens of the tile that are not own
       const uint32_t dst = smem + st * kStageBytes;
@@ -442,16 +439,16 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attention_kernel(PagedArgs 
       }
       if (!more) break;
     }
+    tiles_done = i + 1;
     // (after a timeout the copies in flight are waited for here; otherwise the readers have waited for them)
     asm volatile("cp.async.wait_all;" ::: "memory");
     if (*s_abort)
-      for (int i = 0; i < kStages; ++i) {
-        sm100::mbar_wait(&landed[i], 0);
-        sm100::mbar_wait(&landed[i], 1);
+      for (int k = 0; k < kStages; ++k) {
+        sm100::mbar_wait(&landed[k], 0);
+        sm100::mbar_wait(&landed[k], 1);
       }
     __syncwarp();
     finish();
-    leave();
     return;
   }
 
@@ -463,7 +460,6 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attention_kernel(PagedArgs 
   const int g = lane >> 2, t4 = lane & 3;
   bool fresh = true;              // an item begins
   int begun = 0;                  // the stretch's first tile of the item
-  uint32_t meetings = 0;
   // the readers wait for each other (bounded like every wait: after a timeout nobody is waited for)
   const auto meet = [&] {
     __syncwarp();
@@ -481,8 +477,8 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attention_kernel(PagedArgs 
       const uint16_t *src = p.q + (static_cast<int64_t>(cur.b) * p.T + t) * p.q_stride + (h * p.G + row % p.G) * kD + t4 * 2;
 #pragma unroll
       for (int kk = 0; kk < 8; ++kk) {
-        qf[kk][s] = t < p.T ? fresh_of<kOwn>(reinterpret_cast<const uint32_t *>(src + kk * 16)) : 0u;
-        qf[kk][s + 2] = t < p.T ? fresh_of<kOwn>(reinterpret_cast<const uint32_t *>(src + kk * 16 + 8)) : 0u;
+        qf[kk][s] = t < p.T ? *reinterpret_cast<const uint32_t *>(src + kk * 16) : 0u;
+        qf[kk][s + 2] = t < p.T ? *reinterpret_cast<const uint32_t *>(src + kk * 16 + 8) : 0u;
       }
       m2[s] = -INFINITY;
       l2[s] = 0.f;
@@ -493,7 +489,8 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attention_kernel(PagedArgs 
       for (int e = 0; e < 4; ++e) o[n][e] = 0.f;
   };
   begin_item();   // (the first one's queries come beside its first tile)
-  for (int i = 0;; ++i) {
+  int i = tiles_done;
+  for (;; ++i) {
     const int st = i % kStages;
     sm100::wait_or_abort(&landed[st], (i / kStages) & 1, s_abort, p.status);
     const int4 info = s_info[st];
@@ -503,7 +500,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attention_kernel(PagedArgs 
     if (fresh) {
       fresh = false;
       begun = i;
-      if (i > 0) begin_item();
+      if (i > tiles_done) begin_item();
     }
     const uint32_t kt = smem + st * kStageBytes, vt = kt + 2 * kHalf;
     const int tok0 = wt * kTok;   // the warp's tokens of the tile
@@ -664,7 +661,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attention_kernel(PagedArgs 
       }
       meet();
       const int rb = cur.hr % p.row_blocks, h = cur.hr / p.row_blocks;
-      const int slot = 2 * blockIdx.x + (from_start ? 1 : 0);
+      const int slot = 2 * static_cast<int>(stretch) + (from_start ? 1 : 0);
       for (int r = warp; r < kRows; r += kComputeWarps) {
         const int row = rb * kRows + r, t = row / p.G;
         if (t >= p.T) break;
@@ -701,9 +698,25 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attention_kernel(PagedArgs 
     if (lane == 0) sm100::mbar_arrive(&freed[st]);
     if (stretch_ends) break;
   }
+  tiles_done = i + 1;
   __syncwarp();
   finish();
-  leave();
+  };
+  if constexpr (!kOwn) {
+    run(blockIdx.x);
+  } else {
+    // Stretches go to the CTAs as these come: where the prefixes are done early, or have no work, a CTA takes several.
+    volatile int *s_ticket = reinterpret_cast<volatile int *>(sm + OFF_BAR + 60);
+    while (true) {
+      if (tid == 0) *s_ticket = *s_abort ? stretches : atomicAdd(p.ticket, 1);
+      __syncthreads();
+      const int stretch = *s_ticket;
+      if (stretch >= stretches) break;
+      run(stretch);
+      __syncthreads();
+    }
+    sm100::grid_dependency_wait();
+  }
 }
 
 // Joins the parts of the items that the stretches cut.  Every CTA lists the joins (few places hold one) and takes rows of

@@ -49,6 +49,9 @@ constexpr uint32_t kSmemBytes = OFF_ABORT + 4 + 1024;
 static_assert(kSmemBytes <= 227 * 1024, "one CTA's shared memory");
 constexpr int kMostCtas = 152;
 constexpr int kCost = 2;                           // units of a block besides its steps': queries and sums
+// Units of a stretch at least: CTAs without one leave their SM to the requests' own tokens.  (64 x 8192: of 1, 3, 4, 6 and 8 units 35.3, 34.2,
+// 29.2, 29.1 and 34 us.)
+constexpr int kLeastUnits = 4;
 constexpr int kPieceFloats = 136;                  // a row of a piece: 128 sums, the maximum, the sum of weights, padding to 32 bytes
 constexpr float kFollow = 8.f;                     // powers of two that the maximum may be too low
 constexpr int kLeastBox = 8;
@@ -254,7 +257,8 @@ __global__ void __launch_bounds__(kPlanThreads) shared_prefix_plan_kernel(Prefix
   }
   if (tid == 0) {
     p.plan->units = units;
-    p.plan->stretches = static_cast<int>(min(units, static_cast<int64_t>(ctas)));
+    p.plan->ticket = 0;
+    p.plan->stretches = static_cast<int>(min((units + kLeastUnits - 1) / kLeastUnits, static_cast<int64_t>(ctas)));
   }
 }
 
@@ -850,10 +854,10 @@ __global__ void __launch_bounds__(kJoinThreads, 3) shared_prefix_join_kernel(Pre
 }
 
 // Bytes of prefixes that requests could read again, from which on they are shared.  The table's width bounds them; the host knows
-// no lengths.  Measured, alone against shared (one group, own tokens to 200): 16 requests x 4096 tokens (64 MB) 17.9 and 20.8 us, 16 x
-// 16384 (122 MB) 23.6 and 23.4, 64 x 4096 (134 MB) 24.5 and 22.3, 4 x 16384 (195 MB) 36 and 28, 64 x 4096 (268 MB) 38 and 29, 64 x
-// 16384 (1 GB) 111 and 34; more requests with shorter prefixes cross later (64 x 256, 126 MB: 22 and 32; 192 x 1024, 239 MB: 35 and 33).
-constexpr int64_t kLeastAgain = 128 << 20;
+// no lengths.  Measured, alone against shared (one group, own tokens to 200): 16 requests x 4096 tokens (64 MB) 17.7 and 26.5 us, 16 x
+// 16384 (122 MB) 23.4 and 27.1, 64 x 4096 (134 MB) 24.3 and 26.3, 4 x 16384 (195 MB) 36 and 27, 16 x 16384 (244 MB) 36 and 28, 64 x
+// 16384 (1 GB) 111 and 30; more requests with shorter prefixes cross later (192 x 1024, 239 MB: 35 and 28; 192 x 256, 382 MB: 49 and 56).
+constexpr int64_t kLeastAgain = 160 << 20;
 
 }  // namespace
 
@@ -871,6 +875,7 @@ size_t shared_prefix_bytes(int B, int T, int Hq, int Hk, int groups, uint8_t *ba
   }
   if (args) {
     args->plan = reinterpret_cast<PrefixPlan *>(base + at[0]);
+    args->a.ticket = &args->plan->ticket;
     args->group = reinterpret_cast<PrefixGroup *>(base + at[1]);
     args->own = reinterpret_cast<int2 *>(base + at[2]);
     args->a.own = args->own;

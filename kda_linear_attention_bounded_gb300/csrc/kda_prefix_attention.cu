@@ -82,8 +82,9 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map
       ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(sm100::smem_u32(bar))
       : "memory");
 }
-__device__ __forceinline__ void cp16(uint32_t dst, const void *src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+// 16 bytes, or zeros where they are not there
+__device__ __forceinline__ void cp16_or_zero(uint32_t dst, const void *src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
 }
 __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   float2 d;
@@ -642,6 +643,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(PrefixArgs p
           if (!values && !ok && id[k] != INT_MIN) atomicOr(status, KDA_DEVICE_BAD_PAGE);
           on[k] = __ballot_sync(0xffffffffu, ok);
         }
+        arrive_copies(1);   // (the one before this has to be told of: the slot may wait for its products)
         if (i >= kSlots) sm100::wait_or_abort(&freed[slot], (i / kSlots - 1) & 1, s_abort, status);
         if (__any_sync(0xffffffffu, *s_abort != 0)) {
           stop = true;
@@ -699,23 +701,22 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(PrefixArgs p
             __syncwarp();
           }
         } else {
-          const int chunk = lane & 15;
+          // two rows at a time, 16 lanes each; rows that are not there are zeros (weights of 0 do not hide NaN and infinities)
+          const int chunk = lane & 15, half = lane >> 4;
+          const uint32_t panel = dst + (chunk >> 3) * (kTileBytes / 2) + half * 128;
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const int64_t mine = on[k] >> lane & 1 ? id[k] * page_stride + from[k] * token_stride : -1;
-#pragma unroll 4
+            const bool ok = on[k] >> lane & 1;
+            const int64_t mine = ok ? id[k] * page_stride + from[k] * token_stride : -1;
+#pragma unroll
             for (int r = 0; r < 32; r += 2) {
-              const int lane_of = r + (lane >> 4), to_row = 32 * k + lane_of;
-              const int64_t a = __shfl_sync(0xffffffffu, mine, lane_of);
-              const uint32_t to = dst + (chunk >> 3) * (kTileBytes / 2) + to_row * 128 + (((chunk ^ to_row) & 7) << 4);
-              if (a >= 0) cp16(to, base + a + 8 * chunk);
-              else if (values) st_zero16(to);
+              const int64_t a = __shfl_sync(0xffffffffu, mine, r + half);
+              cp16_or_zero(panel + (32 * k + r) * 128 + (((chunk ^ (r + half)) & 7) << 4), base + (a >= 0 ? a : 0) + 8 * chunk, a >= 0);
             }
           }
           asm volatile("cp.async.commit_group;" ::: "memory");
           if (pending++) due1 = slot;
           else due0 = slot;
-          arrive_copies(1);
         }
       }
       n += 2 * tiles;

@@ -52,6 +52,12 @@ constexpr int kCost = 2;                           // units of a block besides i
 // Units of a stretch at least: CTAs without one leave their SM to the requests' own tokens.  (64 x 8192: of 1, 3, 4, 6 and 8 units 35.3, 34.2,
 // 29.2, 29.1 and 34 us.)
 constexpr int kLeastUnits = 4;
+// What the requests' own tokens cost on an SM, in units of the prefixes' line: a tile of 64 tokens of a key head, with an item's queries and
+// end as four tiles.  As many SMs as their share of the work are theirs from the start: one kernel's start and end lie beside the other's
+// work.  (7 groups x 4 / 192 x 40000: of 0, 0.1, 0.2, 0.3, 0.5 and 0.8 units 67.4, 65.2, 64.5, 65.3, 68.5, 74.6 / 121.7, 119.0, 119.3, 119.4,
+// 123.7, 131.7 us.)
+constexpr int kOwnTile = 64, kOwnCost = 4;
+constexpr float kOwnUnits = 0.2f;
 constexpr int kPieceFloats = 136;                  // a row of a piece: 128 sums, the maximum, the sum of weights, padding to 32 bytes
 constexpr float kFollow = 8.f;                     // powers of two that the maximum may be too low
 constexpr int kLeastBox = 8;
@@ -182,8 +188,13 @@ __global__ void __launch_bounds__(kPlanThreads) shared_prefix_plan_kernel(Prefix
   const int from0 = p.group_starts[0], to0 = p.group_starts[p.groups];
   bad = __syncthreads_or(bad);
   if (bad && tid == 0) atomicOr(p.a.status, KDA_DEVICE_BAD_INDEX);
+  int64_t left = 0;              // own tokens' tiles of this thread's requests, and what every request costs besides
+  const auto count_own = [&](int b, int from) { left += (max(0, length_of(p.a, b) - from) + kOwnTile - 1) / kOwnTile + kOwnCost; };
   for (int b = tid; b < p.a.B; b += kPlanThreads)
-    if (bad || b < from0 || b >= to0) p.own[b] = make_int2(0, -1);
+    if (bad || b < from0 || b >= to0) {
+      p.own[b] = make_int2(0, -1);
+      count_own(b, 0);
+    }
   int64_t units = 0, rows = 0;   // of the groups before
   for (int g0 = 0; g0 < p.groups; g0 += kPlanThreads) {
     for (int g = g0 + warp; g < min(p.groups, g0 + kPlanThreads); g += 32) {
@@ -204,8 +215,10 @@ __global__ void __launch_bounds__(kPlanThreads) shared_prefix_plan_kernel(Prefix
         count += __shfl_xor_sync(0xffffffffu, count, o);
       }
       const int len = count < 2 ? 0 : min(least, p.prefix_lens[g]);   // (one request alone shares nothing)
-      for (int b = from + lane; b < to; b += 32)
+      for (int b = from + lane; b < to; b += 32) {
         p.own[b] = len > 0 && length_of(p.a, b) > 0 ? make_int2(len, g) : make_int2(0, -1);
+        count_own(b, len);
+      }
       if (lane == 0) s_group[g - g0] = make_int4(from, (to - from) * p.a.T * p.a.G, len, first);
     }
     __syncthreads();
@@ -256,10 +269,20 @@ __global__ void __launch_bounds__(kPlanThreads) shared_prefix_plan_kernel(Prefix
     units += __shfl_sync(0xffffffffu, su, 31);
     rows += __shfl_sync(0xffffffffu, sr, 31);
   }
+  // the sum of all threads'
+#pragma unroll
+  for (int o = 16; o; o >>= 1) left += __shfl_xor_sync(0xffffffffu, left, o);
+  __syncthreads();   // (the last sums have been read)
+  if (lane == 0) s_sum[0][warp] = left;
+  __syncthreads();
   if (tid == 0) {
+    left = 0;
+    for (int w = 0; w < kPlanThreads / 32; ++w) left += s_sum[0][w];
+    const float own = kOwnUnits * p.a.Hk * ((p.a.T * p.a.G + 63) / 64) * static_cast<float>(left);
+    const int share = ctas - static_cast<int>(ctas * own / (own + static_cast<float>(units) + 1.f));
     p.plan->units = units;
     p.plan->ticket = 0;
-    p.plan->stretches = static_cast<int>(min((units + kLeastUnits - 1) / kLeastUnits, static_cast<int64_t>(ctas)));
+    p.plan->stretches = static_cast<int>(min((units + kLeastUnits - 1) / kLeastUnits, static_cast<int64_t>(max(share, 1))));
   }
 }
 

@@ -12,10 +12,14 @@
 // places in a list are such sums, so the lists are in ascending order whatever came first.  With n pages in use, the i-th one of id
 // n or above goes to the i-th free id below n; a place of the table finds its number by the same sums (in windows: in the list).
 // Bound by latency: lengths, ids, three meetings of the cluster.
+// Large tables are marked by all SMs instead, with atomics on bits in the free list's own memory, which is written over once all have
+// read them; where requests end, all SMs write the list, too.  Bound by the latency of four launches in a row, and by the atomics.
 //
 // Copying.  Bound by HBM.  Every CTA lists the pairs of a window that are copies; pieces of 8 KB of them all stand in one line, of
 // which each warp takes every so-manieth.
+#include <algorithm>
 #include <climits>
+#include <type_traits>
 
 #include "kda_cache.h"
 #include "kda_hybrid.cuh"
@@ -150,13 +154,13 @@ __device__ __forceinline__ uint4 peer_words(const uint32_t *p, uint32_t rank) {
   return v;
 }
 
-// The table's pieces in turn, by the warps of the cluster: f(row, first place, places, the lane's ids; none of a bad length).
+// The table's pieces in turn, by the warps of so many CTAs: f(row, first place, places, the lane's ids; none of a bad length).
 template <typename F>
-__device__ __forceinline__ void pieces_of(const TableArgs &t, const int32_t *seq_lens, uint32_t rank, bool record, F f) {
-  const int lane = threadIdx.x & 31, ranks = cluster_size();
+__device__ __forceinline__ void pieces_of(const TableArgs &t, const int32_t *seq_lens, uint32_t rank, int ranks, bool record, F f) {
+  const int lane = threadIdx.x & 31;
   const int per_row = max(1, (t.width + kPiece - 1) / kPiece);
   const int64_t units = static_cast<int64_t>(per_row) * t.B;
-  int64_t u = (threadIdx.x >> 5) * ranks + rank;   // (few pieces go to all CTAs)
+  int64_t u = static_cast<int>(threadIdx.x >> 5) * ranks + static_cast<int>(rank);   // (few pieces go to all CTAs)
   const auto row_of = [&](int64_t x, int &piece) {
     piece = units >> 31 ? static_cast<int>(x / t.B) : static_cast<int>(static_cast<uint32_t>(x) / static_cast<uint32_t>(t.B));
     // (a long row's pieces go to different warps: each round of pieces begins some rows later)
@@ -183,6 +187,11 @@ __device__ __forceinline__ void pieces_of(const TableArgs &t, const int32_t *seq
   }
 }
 
+__device__ __forceinline__ void end_request(int32_t *seq_lens, int row, int B, uint32_t *status) {
+  if (row >= B) atomicOr(status, KDA_DEVICE_BAD_INDEX);
+  else if (row >= 0) seq_lens[row] = 0;
+}
+
 // The pages in use among the ids of a window: for every word of 32 its bits and how many bits are set before it.  Bits behind the
 // window's last id are clear.
 struct Window {
@@ -192,9 +201,8 @@ struct Window {
   int w0, w1;             // the words whose lists this CTA writes
   int set;                // bits set in all
 };
-__device__ __forceinline__ Window mark(const TableArgs &t, const int32_t *seq_lens, int num_pages, int from, int most, uint32_t *smem,
-                                       uint32_t *s_warp, uint32_t rank, bool record) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, ranks = cluster_size();
+__device__ __forceinline__ Window window_of(int num_pages, int from, int most, uint32_t *smem, uint32_t rank, int *per) {
+  const int ranks = cluster_size();
   Window x;
   x.own = smem;
   x.bits = smem + most;
@@ -202,12 +210,44 @@ __device__ __forceinline__ Window mark(const TableArgs &t, const int32_t *seq_le
   x.from = from;
   x.span = min(32 * most, num_pages - from);
   x.words = (x.span + 31) / 32;
-  const int per = (x.words + 4 * ranks - 1) / (4 * ranks) * 4;   // (16 bytes at a time)
-  x.w0 = min(x.words, static_cast<int>(rank) * per);
-  x.w1 = min(x.words, x.w0 + per);
+  *per = (x.words + 4 * ranks - 1) / (4 * ranks) * 4;   // (16 bytes at a time)
+  x.w0 = min(x.words, static_cast<int>(rank) * *per);
+  x.w1 = min(x.words, x.w0 + *per);
+  return x;
+}
+// The sums, with the bits there.
+__device__ __forceinline__ void sum_bits(Window &x, uint32_t *s_warp) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  // (consecutive words a thread)
+  const int chunk = (x.words + 4 * kThreads - 1) / (4 * kThreads) * 4, c0 = min(x.words, tid * chunk), c1 = min(x.words, c0 + chunk);
+  int n = 0;
+  for (int i = c0; i < c1; i += 4) {   // (words behind the last of them are clear)
+    const uint4 y = *reinterpret_cast<const uint4 *>(x.bits + i);
+    n += __popc(y.x) + __popc(y.y) + __popc(y.z) + __popc(y.w);
+  }
+  const int inc = warp_scan(n, lane);
+  if (lane == 31) s_warp[warp] = inc;
+  __syncthreads();
+  const int of_warp = s_warp[lane], up_to = warp_scan(of_warp, lane);   // (as many warps as lanes)
+  x.set = __shfl_sync(0xffffffffu, up_to, 31);
+  int sum = inc - n + __shfl_sync(0xffffffffu, up_to - of_warp, warp);
+  for (int i = c0; i < c1; i += 4) {
+    const uint4 y = *reinterpret_cast<const uint4 *>(x.bits + i);
+    const int a = sum + __popc(y.x), b = a + __popc(y.y), c = b + __popc(y.z);
+    *reinterpret_cast<int4 *>(x.before + i) = make_int4(sum, a, b, c);
+    sum = c + __popc(y.w);
+  }
+  __syncthreads();
+}
+__device__ __forceinline__ Window mark(const TableArgs &t, const int32_t *seq_lens, int num_pages, int from, int most, uint32_t *smem,
+                                       uint32_t *s_warp, uint32_t rank, bool record) {
+  const int tid = threadIdx.x, ranks = cluster_size();
+  int per;
+  Window x = window_of(num_pages, from, most, smem, rank, &per);
+  const int lane = tid & 31;
   for (int i = tid; i < ((x.words + 3) & ~3); i += kThreads) x.own[i] = 0;
   __syncthreads();
-  pieces_of(t, seq_lens, rank, record, [&](int, int, int n, const int (&id)[kPiece / 32]) {
+  pieces_of(t, seq_lens, rank, ranks, record, [&](int, int, int n, const int (&id)[kPiece / 32]) {
     bool bad = false;
     uint32_t at[kPiece / 32], old[kPiece / 32];
 #pragma unroll
@@ -241,43 +281,75 @@ __device__ __forceinline__ Window mark(const TableArgs &t, const int32_t *seq_le
   for (int i = 4 * tid; i < x.words; i += 4 * kThreads)
     if (i < x.w0 || i >= x.w1) *reinterpret_cast<uint4 *>(x.bits + i) = peer_words(x.bits + i, static_cast<uint32_t>(i / per));
   __syncthreads();
-  // sums of bits: consecutive words a thread
-  const int chunk = (x.words + 4 * kThreads - 1) / (4 * kThreads) * 4, c0 = min(x.words, tid * chunk), c1 = min(x.words, c0 + chunk);
-  int n = 0;
-  for (int i = c0; i < c1; i += 4) {   // (words behind the last of them are clear)
-    const uint4 y = *reinterpret_cast<const uint4 *>(x.bits + i);
-    n += __popc(y.x) + __popc(y.y) + __popc(y.z) + __popc(y.w);
-  }
-  const int inc = warp_scan(n, lane);
-  if (lane == 31) s_warp[warp] = inc;
-  __syncthreads();
-  const int of_warp = s_warp[lane], up_to = warp_scan(of_warp, lane);   // (as many warps as lanes)
-  x.set = __shfl_sync(0xffffffffu, up_to, 31);
-  int sum = inc - n + __shfl_sync(0xffffffffu, up_to - of_warp, warp);
-  for (int i = c0; i < c1; i += 4) {
-    const uint4 y = *reinterpret_cast<const uint4 *>(x.bits + i);
-    const int a = sum + __popc(y.x), b = a + __popc(y.y), c = b + __popc(y.z);
-    *reinterpret_cast<int4 *>(x.before + i) = make_int4(sum, a, b, c);
-    sum = c + __popc(y.w);
-  }
-  __syncthreads();
+  sum_bits(x, s_warp);
   return x;
 }
 
-// Ids of this CTA's words that `pick(word's place)` has bits for, to out[place(word's place)] on: a warp writes a word's ids.
+// ---- tables of many places: marked by the whole GPU, in words where the free list will be
+__global__ void __launch_bounds__(256) clear_marks_kernel(uint32_t *words, int count, int32_t *seq_lens, const int32_t *rows, int num_rows, int B,
+                                                          uint32_t *status) {
+  sm100::grid_dependency_wait();
+  sm100::grid_launch_dependents();
+  const int tid = blockIdx.x * 256 + threadIdx.x, threads = gridDim.x * 256;
+  for (int i = 4 * tid; i < count; i += 4 * threads) *reinterpret_cast<uint4 *>(words + i) = make_uint4(0, 0, 0, 0);
+  for (int i = tid; i < num_rows; i += threads) end_request(seq_lens, rows[i], B, status);
+}
+__global__ void __launch_bounds__(kThreads, 1) mark_pages_kernel(TableArgs t, const int32_t *seq_lens, int num_pages, uint32_t *words) {
+  sm100::grid_dependency_wait();
+  sm100::grid_launch_dependents();
+  const int lane = threadIdx.x & 31;
+  pieces_of(t, seq_lens, blockIdx.x, gridDim.x, true, [&](int, int, int n, const int (&id)[kPiece / 32]) {
+    bool bad = false;
+#pragma unroll
+    for (int i = 0; i < kPiece / 32; ++i) {
+      const bool there = 32 * i + lane < n, on = there && id[i] >= 0 && id[i] < num_pages;
+      bad |= there && !on;
+      const int w = on ? id[i] >> 5 : -1;
+      uint32_t bit = on ? 1u << (id[i] & 31) : 0u;
+      // Ids in a row have few words: one lane sets what the first lane's and the last lane's words get.  (512 rows of one prompt with such ids:
+      // 376 us without.)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const bool same = w == __shfl_sync(0xffffffffu, w, 31 * k);
+        if (__popc(__ballot_sync(0xffffffffu, same && bit)) < 2) continue;
+        const uint32_t bits = __reduce_or_sync(0xffffffffu, same ? bit : 0u);
+        if (same) bit = 0;
+        if (lane == 31 * k) bit = bits;   // (after its own word's round a lane has no bit but what it sets for all)
+      }
+      if (bit) atomicOr(words + w, bit);
+    }
+    if (bad) atomicOr(t.status, KDA_DEVICE_BAD_PAGE);
+  });
+}
+// The window of all ids from such words.  Behind it they may be written over.
+__device__ __forceinline__ Window marked(const uint32_t *words, int num_pages, int most, uint32_t *smem, uint32_t *s_warp, uint32_t rank) {
+  int per;
+  Window x = window_of(num_pages, 0, most, smem, rank, &per);
+#pragma unroll 4
+  for (int i = 4 * threadIdx.x; i < x.words; i += 4 * kThreads)
+    *reinterpret_cast<uint4 *>(x.bits + i) = __ldcg(reinterpret_cast<const uint4 *>(words + i));
+  cluster_sync();
+  sum_bits(x, s_warp);
+  return x;
+}
+
+// Ids of this CTA's words that `pick(word's place)` has bits for, to out[place(word's place)] on, from out[begin] on: a warp writes a
+// word's ids.
 template <typename P, typename O>
-__device__ __forceinline__ void write_ids(const Window &x, int32_t *out, P pick, O place) {
+__device__ __forceinline__ void write_ids(const Window &x, int32_t *out, P pick, O place, int begin = 0) {
   const int lane = threadIdx.x & 31;
 #pragma unroll 4
   for (int i = x.w0 + (threadIdx.x >> 5); i < x.w1; i += kWarps) {
     const uint32_t bits = pick(i);
-    if (bits >> lane & 1) out[place(i) + __popc(bits & ((1u << lane) - 1))] = x.from + 32 * i + lane;
+    const int64_t to = place(i) + __popc(bits & ((1u << lane) - 1));
+    if ((bits >> lane & 1) && to >= begin) out[to] = x.from + 32 * i + lane;
   }
 }
 
-// out[at .. end) = from, from + step, .. by the whole cluster, 16 bytes a store where they are aligned
-__device__ __forceinline__ void fill(int32_t *out, int64_t at, int64_t end, int64_t from, int step, uint32_t rank) {
-  const int64_t threads = static_cast<int64_t>(cluster_size()) * kThreads;
+// out[at .. end) = from, from + step, .. by so many CTAs, 16 bytes a store where they are aligned
+__device__ __forceinline__ void fill(int32_t *out, int64_t at, int64_t end, int64_t from, int step, uint32_t rank, uint32_t ranks) {
+  const int64_t threads = static_cast<int64_t>(ranks) * kThreads;
+  if (at >= end) return;
   const int64_t head = min(end, at + static_cast<int64_t>((4 - (reinterpret_cast<uintptr_t>(out + at) >> 2 & 3)) & 3));
   const int64_t quads = (end - head) / 4;
   const auto value = [&](int64_t i) { return static_cast<int>(from + step * (i - at)); };
@@ -290,37 +362,93 @@ __device__ __forceinline__ void fill(int32_t *out, int64_t at, int64_t end, int6
   for (int64_t i = head + 4 * quads + tid; i < end; i += threads) out[i] = value(i);
 }
 
-__global__ void __launch_bounds__(kThreads, 1) release_requests_kernel(ReleaseArgs p, int most) {
+// The free list from such words, as far as it does not lie over them: every CTA counts the bits before its own words for itself.
+__global__ void __launch_bounds__(kThreads, 1) list_free_kernel(ReleaseArgs p, const uint32_t *words, int count) {
+  __shared__ int s_sum[3][kWarps];
+  __shared__ uint2 s_word[kThreads];   // a word's open bits, and where its first goes
+  sm100::grid_dependency_wait();
+  sm100::grid_launch_dependents();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int per = ((count + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x) + 3) & ~3;   // at most kThreads (by the caller)
+  const int w0 = min(count, static_cast<int>(blockIdx.x) * per), w1 = min(count, w0 + per);
+  int before = 0, all = 0;
+#pragma unroll 4
+  for (int i = 4 * tid; i < count; i += 4 * kThreads) {   // (bits behind the last id are clear)
+    const uint4 y = __ldcg(reinterpret_cast<const uint4 *>(words + i));
+    const int n = __popc(y.x) + __popc(y.y) + __popc(y.z) + __popc(y.w);
+    all += n;
+    if (i < w0) before += n;
+  }
+  const int w = w0 + tid, left = p.num_pages - 32 * w;
+  const uint32_t open = w >= w1 ? 0u : ~__ldcg(words + w) & (left >= 32 ? ~0u : left > 0 ? (1u << left) - 1 : 0u);
+  const int n = __popc(open), inc = warp_scan(n, lane);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    before += __shfl_xor_sync(0xffffffffu, before, o);
+    all += __shfl_xor_sync(0xffffffffu, all, o);
+  }
+  if (lane == 31) {
+    s_sum[0][warp] = before;
+    s_sum[1][warp] = all;
+    s_sum[2][warp] = inc;
+  }
+  __syncthreads();
+  // (as many warps as lanes)
+  const int of_warp = s_sum[2][lane], up_to = warp_scan(of_warp, lane);
+  before = warp_scan(s_sum[0][lane], lane);
+  all = warp_scan(s_sum[1][lane], lane);
+  const int at = min(32 * w0, p.num_pages) - __shfl_sync(0xffffffffu, before, 31) + __shfl_sync(0xffffffffu, up_to - of_warp, warp) + inc - n;
+  const int free = p.num_pages - __shfl_sync(0xffffffffu, all, 31);
+  const int end = static_cast<int>(reinterpret_cast<const int32_t *>(words) - p.free_pages);
+  s_word[tid] = make_uint2(open, at);
+  __syncthreads();
+#pragma unroll 4
+  for (int i = warp; i < w1 - w0; i += kWarps) {   // a word's ids by a warp
+    const uint2 x = s_word[i];
+    const int to = static_cast<int>(x.y) + __popc(x.x & ((1u << lane) - 1));
+    if ((x.x >> lane & 1) && to < end) p.free_pages[to] = 32 * (w0 + i) + lane;
+  }
+  fill(p.free_pages, free, end, -1, 0, blockIdx.x, gridDim.x);
+  if (blockIdx.x == 0 && tid == 0) *p.num_free = free;
+}
+
+// `words`: the marks of all pages, where the whole GPU made them; the list lacks what lies over them
+__global__ void __launch_bounds__(kThreads, 1) release_requests_kernel(ReleaseArgs p, int most, const uint32_t *words) {
   extern __shared__ uint32_t s_words[];
   __shared__ uint32_t s_warp[kWarps];
   const int tid = threadIdx.x;
   const uint32_t rank = cluster_rank();
   sm100::grid_dependency_wait();
   sm100::grid_launch_dependents();
-  for (int i = rank * kThreads + tid; i < p.num_rows; i += cluster_size() * kThreads) {
-    const int row = p.rows[i];
-    if (row >= p.t.B) atomicOr(p.t.status, KDA_DEVICE_BAD_INDEX);
-    else if (row >= 0) p.seq_lens[row] = 0;
+  const int begin = words ? static_cast<int>(reinterpret_cast<const int32_t *>(words) - p.free_pages) : 0;
+  if (words && __ldcg(p.num_free) <= begin) {
+    fill(p.free_pages, begin, p.num_pages, -1, 0, rank, cluster_size());
+    return;
   }
-  cluster_sync();
+  if (!words) {
+    for (int i = rank * kThreads + tid; i < p.num_rows; i += cluster_size() * kThreads)
+      end_request(p.seq_lens, p.rows[i], p.t.B, p.t.status);
+    cluster_sync();
+  }
   int64_t done = 0;
   for (int64_t from = 0; from < p.num_pages; from += 32 * most) {
-    const Window x = mark(p.t, p.seq_lens, p.num_pages, static_cast<int>(from), most, s_words, s_warp, rank, from == 0);
+    const Window x = words ? marked(words, p.num_pages, most, s_words, s_warp, rank)
+                           : mark(p.t, p.seq_lens, p.num_pages, static_cast<int>(from), most, s_words, s_warp, rank, from == 0);
     write_ids(
         x, p.free_pages,
         [&](int i) {
           const int left = x.span - 32 * i;
           return ~x.bits[i] & (left >= 32 ? ~0u : (1u << left) - 1);
         },
-        [&](int i) { return done + 32 * i - x.before[i]; });
+        [&](int i) { return done + 32 * i - x.before[i]; }, begin);
     done += x.span - x.set;
     cluster_sync();   // (the bits have been read)
   }
-  fill(p.free_pages, done, p.num_pages, -1, 0, rank);
+  fill(p.free_pages, max(done, static_cast<int64_t>(begin)), p.num_pages, -1, 0, rank, cluster_size());
   if (rank == 0 && tid == 0) *p.num_free = static_cast<int>(done);
 }
 
-__global__ void __launch_bounds__(kThreads, 1) compact_pages_kernel(CompactArgs p, int most) {
+__global__ void __launch_bounds__(kThreads, 1) compact_pages_kernel(CompactArgs p, int most, const uint32_t *words) {
   extern __shared__ uint32_t s_words[];
   __shared__ uint32_t s_warp[kWarps];
   const uint32_t rank = cluster_rank();
@@ -330,7 +458,8 @@ __global__ void __launch_bounds__(kThreads, 1) compact_pages_kernel(CompactArgs 
   Window x{};
   int64_t set = 0;
   for (int64_t from = 0; from < p.num_pages; from += 32 * most) {
-    x = mark(p.t, p.seq_lens, p.num_pages, static_cast<int>(from), most, s_words, s_warp, rank, from == 0);
+    x = words ? marked(words, p.num_pages, most, s_words, s_warp, rank)
+              : mark(p.t, p.seq_lens, p.num_pages, static_cast<int>(from), most, s_words, s_warp, rank, from == 0);
     set += x.set;
     if (!once) cluster_sync();
   }
@@ -360,7 +489,7 @@ __global__ void __launch_bounds__(kThreads, 1) compact_pages_kernel(CompactArgs 
     cluster_sync();   // the bits have been read, and the lists are there for all
   }
   const int copies = static_cast<int>(holes);
-  pieces_of(p.t, p.seq_lens, rank, false, [&](int row, int first, int n, const int (&id)[kPiece / 32]) {
+  pieces_of(p.t, p.seq_lens, rank, cluster_size(), false, [&](int row, int first, int n, const int (&id)[kPiece / 32]) {
     const int lane = threadIdx.x & 31;
     int32_t *to = p.new_table + row * p.new_stride + first;
     int y[kPiece / 32];
@@ -385,20 +514,30 @@ __global__ void __launch_bounds__(kThreads, 1) compact_pages_kernel(CompactArgs 
     for (int i = 0; i < kPiece / 32; ++i)
       if (32 * i + lane < n) to[32 * i + lane] = y[i];
   });
-  fill(p.copy_src, copies, p.room, -1, 0, rank);
-  fill(p.copy_dst, copies, p.room, -1, 0, rank);
+  fill(p.copy_src, copies, p.room, -1, 0, rank, cluster_size());
+  fill(p.copy_dst, copies, p.room, -1, 0, rank, cluster_size());
   const int64_t open = p.num_pages - set;
-  fill(p.free_pages, 0, open, used, 1, rank);
-  fill(p.free_pages, open, p.num_pages, -1, 0, rank);
+  fill(p.free_pages, 0, open, used, 1, rank, cluster_size());
+  fill(p.free_pages, open, p.num_pages, -1, 0, rank, cluster_size());
   if (rank == 0 && threadIdx.x == 0) *p.num_free = static_cast<int>(open);
 }
 
 // Places of the table up to which one CTA, or four, have fewer meetings to pay for than loads.  Measured (release; tables of 2048,
 // 8192, 32960 and 961536 places): one CTA 6.4, 9.5, 16.8 and 271 us, four 7.5, 8.3, 10.0 and 83, sixteen 8.9, 9.2, 10.0 and 35.
 constexpr int64_t kPlacesOfOne = 1 << 12, kPlacesOfFour = 1 << 14;
+// Places from which on all SMs mark (where a window holds all ids).  Release, then compact, with a cluster against with all SMs: 64000 places
+// 9.5 and 10 (13.7 and 14.5) us, 131072 11.3 and 9.2 (17.1 and 16.3), 256000 16.7 and 11.2 (26 and 24), 512000 28 and 13 (45 and 37).
+constexpr int64_t kPlacesOfAll = 1 << 17;
 
+constexpr int kListCtas = 152;
+static_assert((kMostWords + kListCtas - 1) / kListCtas + 3 <= kThreads, "a word of a CTA's a thread");
+struct Ended {   // requests that end
+  int32_t *seq_lens;
+  const int32_t *rows;
+  int num_rows;
+};
 template <typename K, typename A>
-cudaError_t launch_marks(K kernel, std::mutex &mu, uint64_t &done, const A &a, cudaStream_t stream) {
+cudaError_t launch_marks(K kernel, std::mutex &mu, uint64_t &done, const A &a, const Ended &ended, cudaStream_t stream) {
   if (const cudaError_t e = set_attributes_once(mu, done, [&] {
         cudaError_t r = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 2 * 4 * kMostWords);
         if (r == cudaSuccess) r = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
@@ -409,7 +548,22 @@ cudaError_t launch_marks(K kernel, std::mutex &mu, uint64_t &done, const A &a, c
   const int most = words < kMostWords ? (words > 0 ? (words + 3) & ~3 : 4) : kMostWords;
   const int64_t places = static_cast<int64_t>(a.t.B) * a.t.width;
   const unsigned ranks = places <= kPlacesOfOne ? 1 : places <= kPlacesOfFour ? 4 : kMostRanks;
-  return launch_dependent_clusters(kernel, ranks, ranks, kThreads, 2 * 4 * most, stream, a, most);
+  uint32_t *marks = nullptr;
+  if (places >= kPlacesOfAll && words <= most && a.num_pages >= most + 4) {
+    // the last 16-byte words of the free list's memory, which is written behind their last use
+    marks = reinterpret_cast<uint32_t *>(reinterpret_cast<uintptr_t>(a.free_pages + a.num_pages - most) & ~uintptr_t(15));
+    const unsigned clears = static_cast<unsigned>(std::min<int64_t>(152, (std::max(most / 4, ended.num_rows) + 255) / 256));
+    if (const cudaError_t e = launch_dependent(clear_marks_kernel, clears, 256, 0, stream, marks, most, ended.seq_lens, ended.rows,
+                                               ended.num_rows, a.t.B, a.t.status))
+      return e;
+    if (const cudaError_t e = launch_dependent(mark_pages_kernel, 152, kThreads, 0, stream, a.t, static_cast<const int32_t *>(a.seq_lens),
+                                               a.num_pages, marks))
+      return e;
+    if constexpr (std::is_same_v<A, ReleaseArgs>)
+      if (const cudaError_t e = launch_dependent(list_free_kernel, kListCtas, kThreads, 0, stream, a, static_cast<const uint32_t *>(marks), words))
+        return e;
+  }
+  return launch_dependent_clusters(kernel, ranks, ranks, kThreads, 2 * 4 * most, stream, a, most, static_cast<const uint32_t *>(marks));
 }
 
 // ---------------------------------------------------------------- copying
@@ -505,13 +659,13 @@ cudaError_t launch_fork_requests(const ForkArgs &a, cudaStream_t stream) {
 cudaError_t launch_release_requests(const ReleaseArgs &a, cudaStream_t stream) {
   static std::mutex mu;
   static uint64_t done = 0;
-  return launch_marks(release_requests_kernel, mu, done, a, stream);
+  return launch_marks(release_requests_kernel, mu, done, a, Ended{a.seq_lens, a.rows, a.num_rows}, stream);
 }
 
 cudaError_t launch_compact_pages(const CompactArgs &a, cudaStream_t stream) {
   static std::mutex mu;
   static uint64_t done = 0;
-  return launch_marks(compact_pages_kernel, mu, done, a, stream);
+  return launch_marks(compact_pages_kernel, mu, done, a, Ended{nullptr, nullptr, 0}, stream);
 }
 
 cudaError_t launch_copy_pages(const kda_page_buffer *buffers, int num_buffers, int num_pages, const int32_t *src,

@@ -196,6 +196,61 @@ def test_compact_of_what_is_none():
     assert got == compact_reference(table, seen, 16, total, total, [[-6] * len(table[0])] * 12)
 
 
+# ---------------------------------------------------------------- tables that the whole GPU marks
+WIDE = [(700, 400, 1, 1, None), (700, 1600, 4, 8, None), (4, 5, 1, 1, 70000), (33, 90, 16, 1, 4000), (2, 100000, 1, 1, None)]
+
+
+@pytest.mark.parametrize("B,longest,page,shared,width", WIDE)
+def test_release_in_wide_tables(B, longest, page, shared, width):
+    table, lens, total = page_case(B, longest, page, seed=B + page, shared=shared, width=width)
+    rows = random.Random(B).sample(range(B), B // 3) + [-1]
+    after = [0 if b in rows else n for b, n in enumerate(lens)]
+    assert release(table, lens, rows, page, total, more=1) == (after, *free_reference(table, after, page, total), 0)
+
+
+@pytest.mark.parametrize("B,longest,page,shared,width", WIDE)
+def test_compact_in_wide_tables(B, longest, page, shared, width):
+    table, lens, total = page_case(B, longest, page, seed=B + page, shared=shared, width=width, extra=1.7)
+    room = total // 2 + 1
+    got, status = compact(table, lens, page, total, room, in_place=True, more=1)
+    assert status == 0 and got == compact_reference(table, lens, page, total, room, table)
+
+
+@pytest.mark.parametrize("off", [1, 2, 3])
+def test_wide_tables_with_lists_anywhere(off):
+    # the free list at any 4 bytes, ids and lengths that are none, again from a graph
+    table, lens, total = page_case(300, 700, 1, seed=off, width=800)
+    lens[5], lens[6], lens[7] = -1, 801, 30
+    table[7][3], table[7][29], table[7][30] = -2, total, total + 1
+    rows = [0, 300, 44]
+    buffer = torch.full((total + 8,), -5, dtype=torch.int32, device="cuda")
+    t, start, count, ws = i32(table), i32(lens), i32([0]), kda.make_workspace()
+    n, free = start.clone(), buffer[off:off + total]
+    call = lambda: kda.release_requests(t, n, i32_rows, 1, free_pages=free, num_free=count, workspace=ws)
+    i32_rows = i32(rows)
+    seen = [0 if b in (0, 44) or x < 0 or x > 800 else x for b, x in enumerate(lens)]
+    read = [list(r) for r in table]
+    read[7][3] = read[7][29] = read[7][0]
+    want = free_reference(read, seen, 1, total)
+    lens[0] = lens[44] = 0
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(stream):
+        call()
+    stream.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    for _ in range(2):
+        assert (free.tolist(), int(count)) == want and n.tolist() == lens
+        assert buffer[:off].tolist() == [-5] * off and buffer[off + total:].tolist() == [-5] * (8 - off)
+        assert kda.read_device_status(ws) == kda.KDA_DEVICE_BAD_COUNT | kda.KDA_DEVICE_BAD_INDEX | kda.KDA_DEVICE_BAD_PAGE
+        free.fill_(-5)
+        n.copy_(start)
+        graph.replay()
+        torch.cuda.synchronize()
+
+
 # ---------------------------------------------------------------- copying
 def buffers_of(total, seed):
     g = torch.Generator(device="cuda").manual_seed(seed)

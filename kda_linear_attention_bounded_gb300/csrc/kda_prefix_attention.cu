@@ -16,8 +16,8 @@
 // One warp issues the products, one brings tiles (K and V in turn, five of 32 KB, TMA boxes of as many rows as the page's size has
 // powers of two, 8 to 64; pages without a factor of 8: asynchronous copies by two warps).  Steps of all blocks stand in one line of
 // which each CTA takes an equal stretch; a stretch's part of a block is one piece.
-// Weights are relative to a maximum that follows the scores only when it is 2^8 too low: then O and l are multiplied, which
-// after the first tiles hardly ever happens; a weight up to 2^8 is rounded to bf16 as exactly as one below 1.
+// Weights are relative to a maximum that follows the scores only when 64 weights' sum says that it is far too low (2^14): then O and l
+// are multiplied, which after the first tiles hardly ever happens; a weight of 2^14 is rounded to bf16 as exactly as one below 1.
 #include <cuda.h>
 
 #include <algorithm>
@@ -59,7 +59,7 @@ constexpr int kLeastUnits = 4;
 constexpr int kOwnTile = 64, kOwnCost = 4;
 constexpr float kOwnUnits = 0.2f;
 constexpr int kPieceFloats = 136;                  // a row of a piece: 128 sums, the maximum, the sum of weights, padding to 32 bytes
-constexpr float kFollow = 8.f;                     // powers of two that the maximum may be too low
+constexpr float kFollow = 64 * 256.f;              // half a row's weights of a tile: their sum, up to which the maximum may be too low
 constexpr int kLeastBox = 8;
 
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t *r) {
@@ -470,8 +470,9 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(PrefixArgs p
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
               const float2 v = make_float2(__uint_as_float(y[2 * i]), __uint_as_float(y[2 * i + 1]));
-              top[i & 1] = fmaxf(top[i & 1], fmaxf(v.x, v.y));
-              if constexpr (kWeigh) {
+              if constexpr (!kWeigh) {
+                top[i & 1] = fmaxf(top[i & 1], fmaxf(v.x, v.y));
+              } else {
                 const float2 e = exp2_2(fma2(v, k2, b2));
                 sum = add2(sum, e);
                 w2[8 * c + i] = pack2(e);
@@ -481,10 +482,10 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(PrefixArgs p
           return fmaxf(top[0], top[1]) * sl2;
         };
         if (j == 0) m = both(pass(std::false_type{}), [](float a, float b) { return fmaxf(a, b); });
-        const float high = pass(std::true_type{});
-        if (lot_any(lot, high > m + kFollow)) {
-          const float top = both(high, [](float a, float b) { return fmaxf(a, b); });
-          const float to = top > m + kFollow ? top : m, f = m == to ? 1.f : fast_exp2(m - to);
+        pass(std::true_type{});
+        if (lot_any(lot, sum.x + sum.y > kFollow || m == -INFINITY)) {
+          const float top = both(pass(std::false_type{}), [](float a, float b) { return fmaxf(a, b); });
+          const float to = fmaxf(top, m), f = m == to ? 1.f : fast_exp2(m - to);
           l *= f;   // (the sums are complete: their products come before those of the scores)
           m = to;
 #pragma unroll 1

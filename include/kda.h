@@ -591,7 +591,8 @@ KDA_API int kda_step_tables(int32_t *block_table, int64_t table_row_stride, int 
  * Around the paged cache: rotary positions and the store of a step's keys   *
  * and values, attention over prefixes that requests share, and the pages'   *
  * own operations.  Pages in use are those the block table names: there are  *
- * no reference counts, and each call leaves the same result when run again. *
+ * no reference counts, and a call that is run again leaves the same result   *
+ * (but for a table that was compacted in place: it is compact then).        *
  * ======================================================================== */
 
 /*

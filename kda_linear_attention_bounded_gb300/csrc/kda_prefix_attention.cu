@@ -914,7 +914,7 @@ cudaError_t launch_shared_prefix(const PrefixArgs &args, cudaStream_t stream) {
   if (args.a.B <= 0) return cudaSuccess;
   // Nothing is shared, or so little that the plan and the join cost more than reading it again: the bytes that the requests
   // of all groups but one each could read at most.
-  const int64_t again = static_cast<int64_t>(args.a.B - std::min(args.groups, args.a.B)) * args.a.max_len * args.a.Hk * 4 * kD;
+  const double again = static_cast<double>(args.a.B - std::min(args.groups, args.a.B)) * args.a.max_len * args.a.Hk * 4 * kD;
   if (args.groups == 0 || args.a.num_pages == 0 || again < kLeastAgain) return launch_paged_attention(args.a, stream);
   static std::mutex mu;
   static uint64_t done = 0;

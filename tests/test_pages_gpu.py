@@ -216,6 +216,17 @@ def test_compact_in_wide_tables(B, longest, page, shared, width):
     assert status == 0 and got == compact_reference(table, lens, page, total, room, table)
 
 
+@pytest.mark.parametrize("total,lens", [(5000, [3, 2]), (5000, [0, 0]), (70001, [900, 1300]), (70001, [900, 1500]), (150, [3, 140])])
+def test_wide_tables_of_a_nearly_free_cache(total, lens):
+    # more free pages than the list's memory has room for before the marks
+    ids = random.Random(total).sample(range(total), sum(lens))
+    table = [ids[:lens[0]] + [-4] * (70000 - lens[0]), ids[lens[0]:] + [-4] * (70000 - lens[1])]
+    want = free_reference(table, lens, 1, total)
+    assert release(table, lens, [-1], 1, total) == (lens, *want, 0)
+    got, status = compact(table, lens, 1, total, total, in_place=True)
+    assert status == 0 and got == compact_reference(table, lens, 1, total, total, table)
+
+
 @pytest.mark.parametrize("off", [1, 2, 3])
 def test_wide_tables_with_lists_anywhere(off):
     # the free list at any 4 bytes, ids and lengths that are none, again from a graph

@@ -228,6 +228,39 @@ def test_scores_of_one_sign():
     check(x, 1)
 
 
+@pytest.mark.parametrize("rise", [0.05, 0.5, 3.0, 40.0])
+def test_scores_that_rise(rise):
+    # from tile to tile by `rise`, downwards and upwards: maxima that follow never, at times and at every tile
+    n = 1700
+    for sign in (1, -1):
+        x = make([(n, [9] * 5)], 1, 4, 1, 20, seed=19)
+        q, k, v, table, lens = x[:5]
+        q[:] = 1.0
+        k *= 0.1
+        at = torch.arange(n, device="cuda")
+        level = sign * rise / 128 * (at - n / 2) / math.sqrt(D)   # (a key of c throughout: a score of c sqrt(128))
+        for b in range(5):
+            page = table[b, at // 20].long()
+            k[page, at % 20] = (0.1 * torch.randn((n, 1, D), generator=torch.Generator().manual_seed(3)).cuda() + level[:, None, None]).bfloat16()
+            v[page, at % 20] = v[table[0, at // 20].long(), at % 20]
+        check(x, 1)
+
+
+def test_prefix_that_begins_with_bad_pages():
+    # tiles of nothing before the first tokens that count: for one page they are left out, for a prefix of them nothing is left
+    x = make([(700, [9] * 3), (256, [4, 4])], 1, 4, 1, 64, seed=20)
+    table, lens = x[3], x[4]
+    table[:3, :5] = -1
+    table[3:, :4] = x[1].shape[0]
+    out, lse, status = run(x, 1)
+    assert status == kda.KDA_DEVICE_BAD_PAGE
+    for b, first in ((0, 5), (1, 5), (2, 5), (3, 4), (4, 4)):
+        row = table[b:b + 1, first:].contiguous()
+        ref, ref_lse = paged_reference(x[0][b:b + 1], x[1], x[2], row, [int(lens[b]) - 64 * first], 1)
+        assert rel_l2(out[b], ref[0]) <= OUT_TOL
+        assert float((lse[b].cpu() - ref_lse[0]).abs().max()) <= LSE_TOL * (1 + float(ref_lse.abs().max()))
+
+
 @pytest.mark.parametrize("n", [200, 384, 500])
 def test_what_is_not_seen_does_not_matter(n):
     # NaN and infinities in other pages, behind the requests' ends and in the rest of the prefix's last page

@@ -617,7 +617,8 @@ KDA_API int kda_step_tables(int32_t *block_table, int64_t table_row_stride, int 
  *  R             a multiple of 16, 16 .. 128 (else KDA_ERR_UNSUPPORTED)
  *  mscale        finite (else KDA_ERR_UNSUPPORTED)
  *  k_pages, v_pages [num_pages, page_size, Hk, 128] bf16 with any page, token
- *                and head strides (elements, multiples of 8) that keep rows apart
+ *                and head strides (elements, multiples of 8) that keep rows apart; keys and
+ *                values may share a buffer, but no row
  *  out           [tokens, Hq, 128] bf16, token stride out_token_stride; may be
  *                q itself (same stride)
  * What is written may overlap no input (KDA_ERR_INVALID_ARG), except that out may

@@ -105,6 +105,9 @@ int kda_rotary_to_pages(const uint16_t *q, int64_t q_token_stride, const uint16_
   Range reach[2];
   if (!good_pages(kp, num_pages, page_size, Hk, &reach[0]) || !good_pages(vp, num_pages, page_size, Hk, &reach[1]))
     return KDA_ERR_INVALID_ARG;
+  // (keys and values may lie in one buffer, but not in the same places: their first rows tell)
+  const auto k_at = reinterpret_cast<uintptr_t>(k_pages), v_at = reinterpret_cast<uintptr_t>(v_pages);
+  if (num_pages > 0 && (k_at < v_at ? v_at - k_at : k_at - v_at) < 2 * kda::kD) return KDA_ERR_INVALID_ARG;
   // what is written: out (q itself, or apart from all that is read) and the pages
   const Span qs = {q, 2 * qrow, tokens, 2 * q_token_stride}, os = {out, 2 * qrow, tokens, 2 * out_token_stride},
              inputs[] = {{k, 2 * krow, tokens, 2 * k_token_stride}, {v, 2 * krow, tokens, 2 * v_token_stride},

@@ -70,6 +70,13 @@ def test_rotary_overlaps(lib):
     assert _rotary(lib, **one, out=a[0] - 256) == 1
 
 
+def test_rotary_keys_on_values(lib):
+    a = addresses(10)
+    for off in (0, 16, 240, -16, -240):
+        assert _rotary(lib, v_pages=a[6] + off) == 1, off
+        assert _rotary(lib, v_pages=a[6] + off, pages=0, tokens=0) == 0
+
+
 def _fork(lib, *, stride=8, width=8, B=4, forks=2, free=3, page=16, ws_bytes=1024, **at):
     names = ("table", "lens", "parents", "children", "free_pages", "src", "dst", "used", "ws")
     a = dict(zip(names, addresses(len(names))))

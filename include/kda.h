@@ -651,13 +651,16 @@ KDA_API int kda_rotary_to_pages(const uint16_t *q, int64_t q_token_stride, const
  *                entry; one of B and above, or a child that is its parent,
  *                skips the fork (KDA_DEVICE_BAD_INDEX).
  *  free_pages    [num_free] int32: pages are taken from its front, in the order
- *                of the forks; *pages_used (int32) receives how many
+ *                of the forks; *pages_used (int32) receives how many.  A negative id
+ *                ends the list: kda_release_requests' and kda_compact_pages' whole
+ *                lists are taken as they are, their length unread by the host
  *  copy_src, copy_dst [forks] int32: the page to copy and where to, -1 where
  *                there is none
  * A parent's length that is negative or that its row cannot hold skips the fork
  * (KDA_DEVICE_BAD_COUNT), and so does a free list used up by the forks before
  * (KDA_DEVICE_NO_PAGES).  A fork that is skipped leaves the child's row and length
- * as they were.  What is written may overlap neither another input nor each other.
+ * as they were.  A parent's last page of a negative id is not copied
+ * (KDA_DEVICE_BAD_PAGE); the child has its own all the same.  What is written may overlap neither another input nor each other.
  */
 KDA_API int kda_fork_requests(int32_t *block_table, int64_t table_row_stride, int table_width, int32_t *seq_lens, int B,
                       const int32_t *parents, const int32_t *children, int forks, const int32_t *free_pages,

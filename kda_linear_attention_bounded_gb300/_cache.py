@@ -51,7 +51,7 @@ def fork_requests(block_table, seq_lens, parents, children, free_pages, page_siz
                   workspace=None, stream=None):
     """``kda_fork_requests``: rows ``children`` of the table become copies of rows ``parents`` (int32 ``[forks]``; a
     negative one is padding).  Whole pages are shared, the rest of a page gets a page of its own from the front of
-    free_pages, with the copy to make in copy_src, copy_dst (int32 ``[forks]``, -1: none; :func:`copy_pages` takes them).
+    free_pages (which ends at its first negative id, as :func:`release_requests` leaves it), with the copy to make in copy_src, copy_dst (int32 ``[forks]``, -1: none; :func:`copy_pages` takes them).
     seq_lens of the children and pages_used (int32 ``[1]``) are written.  :func:`copy_pages` also copies the recurrent states
     of a hybrid model's forked requests, with slots for pages."""
     workspace = _workspace(workspace, block_table, "block_table", stream)

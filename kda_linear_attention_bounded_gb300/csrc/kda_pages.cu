@@ -3,7 +3,8 @@
 //
 // Forking.  Fork i needs a page where its parent's length n is no multiple of the page, and takes the free list's entry at the
 // number of forks before it that need one.  Every CTA counts them for itself, in windows of a fork a thread, and then copies the
-// rows of its own forks.  Bound by latency: lengths, counts, rows.
+// rows of its own forks.  The list ends with its length or at its first negative id: each thread reads its own fork's entry, and
+// the least place of a negative one is the end for this window and those behind it.  Bound by latency: lengths, counts, ids, rows.
 //
 // Ending and compacting.  One cluster of CTAs has a bit for each page in each of its CTAs' shared memory (in windows of the ids
 // where there are more).  Its warps take the rows in pieces of 256 places and set the bits of what they hold, each in its own
@@ -18,7 +19,6 @@
 // Copying.  Bound by HBM.  Every CTA lists the pairs of a window that are copies; pieces of 8 KB of them all stand in one line, of
 // which each warp takes every so-manieth.
 #include <algorithm>
-#include <climits>
 #include <type_traits>
 
 #include "kda_cache.h"
@@ -50,12 +50,13 @@ __device__ __forceinline__ int warp_scan(int x, int lane) {   // inclusive
 constexpr int kForkThreads = 256;
 __global__ void __launch_bounds__(kForkThreads) fork_requests_kernel(ForkArgs p) {
   constexpr int kWarps = kForkThreads / 32;
-  __shared__ int s_len[kForkThreads], s_parent[kForkThreads], s_child[kForkThreads], s_taken[kForkThreads];
-  __shared__ int s_warp[kWarps];
+  __shared__ int s_len[kForkThreads], s_parent[kForkThreads], s_child[kForkThreads], s_taken[kForkThreads], s_page[kForkThreads];
+  __shared__ int s_warp[kWarps], s_end;
   sm100::grid_dependency_wait();
   sm100::grid_launch_dependents();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  int64_t before = 0;   // pages that the forks before the window need
+  int before = 0;   // pages that the forks before the window need
+  if (tid == 0) s_end = p.num_free;   // the first place behind the list's ids, as far as it has been read
   for (int f0 = 0; f0 < p.forks; f0 += kForkThreads) {
     const int f = f0 + tid;
     int parent = -1, child = -1, len = 0, need = 0;
@@ -82,25 +83,26 @@ __global__ void __launch_bounds__(kForkThreads) fork_requests_kernel(ForkArgs p)
     __syncthreads();   // the last window's lists have been read
     if (lane == 0) s_warp[warp] = __popc(on);
     __syncthreads();
-    int64_t taken = before + __popc(on & ((1u << lane) - 1));
+    int taken = before + __popc(on & ((1u << lane) - 1));   // (below the number of forks)
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
       if (w < warp) taken += s_warp[w];
       before += s_warp[w];
     }
-    if (need && taken >= p.num_free) {
-      bad |= KDA_DEVICE_NO_PAGES;
-      child = -1;
-    }
-    if (bad && blockIdx.x == 0) atomicOr(p.t.status, bad);
+    const int page = need && taken < s_end ? p.free_pages[taken] : -1;
+    if (need && page < 0) atomicMin(&s_end, taken);
     s_len[tid] = len;
     s_parent[tid] = parent;
     s_child[tid] = child;
-    s_taken[tid] = need ? static_cast<int>(min(taken, static_cast<int64_t>(INT_MAX))) : -1;
+    s_taken[tid] = need ? taken : -1;
+    s_page[tid] = page;
     __syncthreads();
+    const int end = s_end;
+    if (need && taken >= end) bad |= KDA_DEVICE_NO_PAGES;
+    if (bad && blockIdx.x == 0) atomicOr(p.t.status, bad);
     for (int j = (blockIdx.x + gridDim.x - f0 % gridDim.x) % gridDim.x; j < kForkThreads && f0 + j < p.forks; j += gridDim.x) {
       const int c = s_child[j], n = s_len[j], at = s_taken[j];
-      if (c < 0) {
+      if (c < 0 || at >= end) {
         if (tid == 0) p.copy_src[f0 + j] = p.copy_dst[f0 + j] = -1;
         continue;
       }
@@ -112,9 +114,9 @@ __global__ void __launch_bounds__(kForkThreads) fork_requests_kernel(ForkArgs p)
         int src = -1, dst = -1;
         if (at >= 0) {
           src = from[whole];
-          dst = p.free_pages[at];
+          dst = s_page[j];
           to[whole] = dst;
-          if (src < 0 || dst < 0) atomicOr(p.t.status, KDA_DEVICE_BAD_PAGE);   // (no copy is made)
+          if (src < 0) atomicOr(p.t.status, KDA_DEVICE_BAD_PAGE);   // (no copy is made)
         }
         p.copy_src[f0 + j] = src;
         p.copy_dst[f0 + j] = dst;
@@ -122,7 +124,8 @@ __global__ void __launch_bounds__(kForkThreads) fork_requests_kernel(ForkArgs p)
       }
     }
   }
-  if (blockIdx.x == 0 && tid == 0) *p.pages_used = static_cast<int>(min(before, static_cast<int64_t>(p.num_free)));
+  __syncthreads();   // (without forks the end has just been set)
+  if (blockIdx.x == 0 && tid == 0) *p.pages_used = min(before, s_end);
 }
 
 // ---------------------------------------------------------------- pages in use

@@ -558,7 +558,9 @@ KDA_API int kda_paged_attention(const uint16_t *q, int64_t q_token_stride, const
  *                of each request.  The ids of the pages that the new tokens
  *                begin are written behind those in use; all else is kept.
  *  free_pages    [num_free] int32: pages are taken from its front, in request
- *                order; *pages_used (int32) receives how many.
+ *                order; *pages_used (int32) receives how many.  Negative ids behind
+ *                the others are not counted in (kda_release_requests' and
+ *                kda_compact_pages' whole lists are taken as they are)
  *  page_size     tokens per page, >= 1
  *  max_tokens    rows of positions and slot_map
  *  cu_seqlens    [B + 1] int32: request r's new tokens are rows

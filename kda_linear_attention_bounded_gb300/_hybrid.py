@@ -168,7 +168,7 @@ def step_tables(block_table, seq_lens, new_lens, free_pages, page_size, *, cu_se
     """``kda_step_tables``: page tables and slot maps of one step from the requests' lengths, all on the GPU.
 
     block_table: int32 ``[B, width]`` (rows may be strided), extended in place; seq_lens, new_lens: int32 ``[B]``;
-    free_pages: int32 ``[F]``, taken from the front.  Written: cu_seqlens int32 ``[B + 1]``, kv_lens int32 ``[B]``,
+    free_pages: int32 ``[F]``, taken from the front, negative ids behind the others not counted in.  Written: cu_seqlens int32 ``[B + 1]``, kv_lens int32 ``[B]``,
     positions int32 and slot_map int64 ``[rows]`` (padding rows: 0 and -1), pages_used int32 ``[1]``; none of them may overlap
     another or an input, but kv_lens may be seq_lens, which then moves forward in place."""
     if workspace is None:

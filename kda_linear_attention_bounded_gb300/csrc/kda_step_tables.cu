@@ -78,8 +78,10 @@ __global__ void __launch_bounds__(kThreads) step_tables_kernel(StepTablesArgs p)
       tb += xb;
     }
     const int64_t start = rows + wa + a - count, taken = pages + wb + b - grown;
-    // pages go out in request order, so once a request finds too few, so does every later one that needs any
-    const bool refused = (bad & KDA_DEVICE_NO_PAGES) || (grown > 0 && taken + grown > p.num_free);
+    // Pages go out in request order, so once a request finds too few, so does every later one that needs any: places behind the
+    // list, or of negative ids, which stand behind the others.
+    const bool refused = (bad & KDA_DEVICE_NO_PAGES) ||
+                         (grown > 0 && (taken + grown > p.num_free || p.free_pages[taken + grown - 1] < 0));
     s_start[tid] = start;
     s_taken[tid] = taken;
     s_old[tid] = old;

@@ -620,7 +620,8 @@ KDA_API int kda_step_tables(int32_t *block_table, int64_t table_row_stride, int 
  *  mscale        finite (else KDA_ERR_UNSUPPORTED)
  *  k_pages, v_pages [num_pages, page_size, Hk, 128] bf16 with any page, token
  *                and head strides (elements, multiples of 8) that keep rows apart; keys and
- *                values may share a buffer, but no row
+ *                values may share a buffer, but no row.  Rows that meet, of one tensor
+ *                or of both, are refused (KDA_ERR_INVALID_ARG)
  *  out           [tokens, Hq, 128] bf16, token stride out_token_stride; may be
  *                q itself (same stride)
  * What is written may overlap no input (KDA_ERR_INVALID_ARG), except that out may

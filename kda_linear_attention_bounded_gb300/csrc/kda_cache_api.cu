@@ -10,6 +10,7 @@
 #include "kda_cache.h"
 #include "kda_checks.h"
 #include "kda_common.cuh"
+#include "kda_layout.h"
 
 namespace {
 
@@ -17,6 +18,7 @@ using kda::aligned16;
 using kda::aligned_to;
 using kda::check_workspace;
 using kda::good_stride;
+using kda::Pages;
 using kda::Span;
 
 Span ints(const int32_t *at, int64_t n) { return {at, 4 * n}; }
@@ -53,22 +55,19 @@ kda::TableArgs table_args(const int32_t *table, int64_t stride, int width, int B
 int status_of(cudaError_t e) { return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA; }
 
 // Pages that are written: strides that keep rows of 128 channels apart, and what they reach.
-struct Pages {
-  const uint16_t *at;
-  int64_t page, token, head;
-};
 bool good_pages(const Pages &p, int num_pages, int page_size, int Hk, Range *reach) {
   if (!aligned16(p.at) || (num_pages > 0 && !p.at)) return false;
   int64_t bytes = 256;
   const auto dim = [&](int64_t stride, int64_t n) {
     if (!good_stride(stride, 0) || (n > 1 && stride < kda::kD)) return false;
+    if (n > 1 && stride > (int64_t(1) << 46) / (n - 1)) return false;   // (behind all memory)
     if (n > 1) bytes += 2 * stride * (n - 1);
     return true;
   };
   if (!dim(p.page, num_pages) || !dim(p.token, page_size) || !dim(p.head, Hk)) return false;
   const auto at = reinterpret_cast<uintptr_t>(p.at);
   *reach = {at, num_pages > 0 ? at + static_cast<uintptr_t>(bytes) : at};
-  return true;
+  return kda::rows_apart(p, num_pages, page_size, Hk);
 }
 
 }  // namespace
@@ -105,9 +104,8 @@ int kda_rotary_to_pages(const uint16_t *q, int64_t q_token_stride, const uint16_
   Range reach[2];
   if (!good_pages(kp, num_pages, page_size, Hk, &reach[0]) || !good_pages(vp, num_pages, page_size, Hk, &reach[1]))
     return KDA_ERR_INVALID_ARG;
-  // (keys and values may lie in one buffer, but not in the same places: their first rows tell)
-  const auto k_at = reinterpret_cast<uintptr_t>(k_pages), v_at = reinterpret_cast<uintptr_t>(v_pages);
-  if (num_pages > 0 && (k_at < v_at ? v_at - k_at : k_at - v_at) < 2 * kda::kD) return KDA_ERR_INVALID_ARG;
+  // (keys and values may lie in one buffer, but not in the same places)
+  if (reach[0].meets(reach[1]) && kda::pages_meet(kp, vp, num_pages, page_size, Hk)) return KDA_ERR_INVALID_ARG;
   // what is written: out (q itself, or apart from all that is read) and the pages
   const Span qs = {q, 2 * qrow, tokens, 2 * q_token_stride}, os = {out, 2 * qrow, tokens, 2 * out_token_stride},
              inputs[] = {{k, 2 * krow, tokens, 2 * k_token_stride}, {v, 2 * krow, tokens, 2 * v_token_stride},

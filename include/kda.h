@@ -722,8 +722,8 @@ typedef struct kda_page_buffer {
  * Copies pages copy_src[i] -> copy_dst[i] (i < count) of every buffer.  A negative
  * id marks an entry without a copy; an id of num_pages or above skips it
  * (KDA_DEVICE_BAD_PAGE), and a page is not copied onto itself.  The destinations
- * are distinct, and none is a source.  `buffers` is a HOST array; the buffers may
- * not overlap.
+ * are distinct, and none is a source.  `buffers` is a HOST array; no page of one may
+ * meet a page of another (KDA_ERR_INVALID_ARG; between its pages one may lie).
  */
 KDA_API int kda_copy_pages(const kda_page_buffer *buffers, int num_buffers, int num_pages, const int32_t *copy_src,
                    const int32_t *copy_dst, int count, void *workspace, size_t workspace_bytes, void *stream);

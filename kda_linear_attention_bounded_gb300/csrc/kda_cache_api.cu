@@ -1,11 +1,14 @@
 // C ABI of the calls around the paged cache (declared in include/kda.h): rotary positions with the store into the pages,
 // forking and ending requests, compacting and copying pages, attention over shared prefixes.  Host-side validation and launch
 // planning only, by the rules of kda_api.cu.
+#include <algorithm>
 #include <climits>
 #include <cmath>
 #include <cstdint>
 #include <initializer_list>
 #include <iterator>
+#include <memory>
+#include <new>
 
 #include "kda_cache.h"
 #include "kda_checks.h"
@@ -68,6 +71,72 @@ bool good_pages(const Pages &p, int num_pages, int page_size, int Hk, Range *rea
   const auto at = reinterpret_cast<uintptr_t>(p.at);
   *reach = {at, num_pages > 0 ? at + static_cast<uintptr_t>(bytes) : at};
   return kda::rows_apart(p, num_pages, page_size, Hk);
+}
+
+// Whether two buffers of as many pages each meet, page by page.
+bool buffers_meet(const Span &a, const Span &b) {
+  if (a.bytes <= 0 || b.bytes <= 0 || !range_of(a).meets(range_of(b))) return false;
+  if (a.rows == 1 || a.stride == b.stride) return rows_meet(a, b);
+  for (int64_t r = 0; r < b.rows; ++r)
+    if (a.meets({static_cast<const uint8_t *>(b.at) + r * b.stride, b.bytes})) return true;
+  return false;
+}
+Span pages_span(const kda_page_buffer &b, int num_pages) { return {b.base, b.bytes, num_pages, b.page_stride}; }
+// Whether any two do.  Buffers behind one another, in any order, are told apart by their ends; those that reach into each other with
+// one stride (layers of one tensor) by the places of their first pages within it; others pair by pair.
+bool any_buffers_meet(const kda_page_buffer *buffers, int n, int num_pages) {
+  struct Entry {
+    int64_t at;
+    int buffer;
+    bool operator<(const Entry &o) const { return at < o.at; }
+  };
+  const auto range = [&](int i) { return range_of(pages_span(buffers[i], num_pages)); };
+  uintptr_t end = 0;
+  int i = 0;
+  for (; i < n; ++i) {   // mostly they come in order
+    const Range r = range(i);
+    if (r.from == r.to) continue;
+    if (r.from < end) break;
+    end = r.to;
+  }
+  if (i == n) return false;
+  constexpr int kFew = 256;
+  Entry few[kFew];
+  const std::unique_ptr<Entry[]> many(n > kFew ? new (std::nothrow) Entry[n] : nullptr);
+  Entry *const list = n > kFew ? many.get() : few;
+  const auto pairs = [&](auto of, int count) {
+    for (int x = 0; x < count; ++x)
+      for (int y = 0; y < x; ++y)
+        if (buffers_meet(pages_span(buffers[of(x)], num_pages), pages_span(buffers[of(y)], num_pages))) return true;
+    return false;
+  };
+  if (!list) return pairs([](int x) { return x; }, n);
+  int live = 0;
+  for (i = 0; i < n; ++i)
+    if (buffers[i].bytes > 0) list[live++] = {static_cast<int64_t>(reinterpret_cast<uintptr_t>(buffers[i].base)), i};
+  std::sort(list, list + live);
+  for (int from = 0, to; from < live; from = to) {
+    Entry *const group = list + from;
+    end = range(group[0].buffer).to;
+    const int64_t stride = buffers[group[0].buffer].page_stride;
+    bool same = num_pages > 1;
+    for (to = from + 1; to < live && range(list[to].buffer).from < end; ++to) {
+      end = std::max(end, range(list[to].buffer).to);
+      same = same && buffers[list[to].buffer].page_stride == stride;
+    }
+    const int count = to - from;
+    if (count == 1) continue;
+    bool apart = same;
+    if (same) {
+      const int64_t first = group[0].at;
+      for (i = 0; i < count; ++i) group[i].at = (group[i].at - first) % stride;
+      std::sort(group, group + count);
+      for (i = 0; i < count && apart; ++i)
+        apart = group[i].at + buffers[group[i].buffer].bytes <= (i + 1 < count ? group[i + 1].at : group[0].at + stride);
+    }
+    if (!apart && pairs([&](int x) { return group[x].buffer; }, count)) return true;
+  }
+  return false;
 }
 
 }  // namespace
@@ -238,9 +307,10 @@ int kda_copy_pages(const kda_page_buffer *buffers, int num_buffers, int num_page
     if (b.bytes < 0 || b.bytes > INT_MAX || b.bytes % 16 || b.page_stride % 16 || !aligned16(b.base)) return KDA_ERR_INVALID_ARG;
     if (num_pages > 0 && b.bytes > 0 && (!b.base || (num_pages > 1 && b.page_stride < b.bytes))) return KDA_ERR_INVALID_ARG;
     // the lists are read by every CTA at its own time
-    const Span pages = {b.base, b.bytes, num_pages, b.page_stride};
+    const Span pages = pages_span(b, num_pages);
     if (num_pages > 0 && (pages.meets(ints(copy_src, count)) || pages.meets(ints(copy_dst, count)))) return KDA_ERR_INVALID_ARG;
   }
+  if (any_buffers_meet(buffers, num_buffers, num_pages)) return KDA_ERR_INVALID_ARG;
   if (count == 0 || num_pages == 0) return KDA_OK;
   return status_of(kda::launch_copy_pages(buffers, num_buffers, num_pages, copy_src, copy_dst, count,
                                           static_cast<uint32_t *>(workspace), static_cast<cudaStream_t>(stream)));

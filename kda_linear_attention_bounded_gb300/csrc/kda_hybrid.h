@@ -68,6 +68,13 @@ cudaError_t launch_gdn_prefill(const GdnRecurrentArgs &args, const int32_t *cu_h
 // ---------------------------------------------------------------- paged attention
 constexpr int kPagedMaxCtas = 304;      // stretches of work at most (two CTAs on each of 152 SMs)
 constexpr int kPagedPartFloats = 132;   // a part of a row: 128 sums, the maximum, the sum of weights, padding
+// Where part n of a row lies whose item is cut into `parts` at the beginning of stretch `cut` (the parts of the workspace: two of every
+// stretch): part 0 in the last of the stretch before the cut, part n in the first of the n-th stretch from the cut on.
+constexpr int paged_part_slot(int cut, int n) { return n == 0 ? 2 * (cut - 1) + 1 : 2 * (cut + n - 1); }
+// Whether a row's own words on its parts can be so.  Rows that a kernel left unwritten, after a wait that gave up, say anything.
+constexpr bool paged_parts_there(int parts, int cut) {
+  return parts >= 2 && cut >= 1 && parts <= kPagedMaxCtas && cut <= kPagedMaxCtas + 1 - parts;
+}
 struct PagedArgs {
   const uint16_t *q, *k, *v;
   int64_t q_stride;                                        // tokens of q (heads contiguous)

@@ -788,7 +788,8 @@ __global__ void __launch_bounds__(kJoinThreads, 3) shared_prefix_join_kernel(Pre
     if (there) {
       const int2 own = p.own[b];
       const float4 end = *reinterpret_cast<const float4 *>(a.rows + at * kPagedPartFloats + kD);
-      const int h = head / a.G, row = t * a.G + head - h * a.G, parts = __float_as_int(end.z), cut = __float_as_int(end.w);
+      const int h = head / a.G, row = t * a.G + head - h * a.G, cut = __float_as_int(end.w);
+      const int parts = paged_parts_there(__float_as_int(end.z), cut) ? __float_as_int(end.z) : 0;   // (0: the row is whole)
       // the prefix: the stretches that hold steps of the block, two pieces each where the groups of threads took its tiles in turn
       int64_t base = 0;
       int pieces = 0, twice = 1, second = 0;
@@ -813,9 +814,7 @@ __global__ void __launch_bounds__(kJoinThreads, 3) shared_prefix_join_kernel(Pre
         }
         n -= pieces;
         if (!parts) return a.rows + at * kPagedPartFloats;
-        // part 0: the stretch before the cut, in its last slot; part n: the n-th stretch from the cut on, in its first
-        const int slot = n == 0 ? 2 * (cut - 1) + 1 : 2 * (cut + n - 1);
-        return a.parts + (static_cast<size_t>(slot) * rows_per_item + row % rows_per_item) * kPagedPartFloats;
+        return a.parts + (static_cast<size_t>(paged_part_slot(cut, n)) * rows_per_item + row % rows_per_item) * kPagedPartFloats;
       };
       const int count = pieces + (parts ? parts : 1);
       for (int n0 = w; n0 < count; n0 += 4 * split) {

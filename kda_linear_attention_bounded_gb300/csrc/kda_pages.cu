@@ -434,7 +434,8 @@ __global__ void __launch_bounds__(kThreads, 1) release_requests_kernel(ReleaseAr
     cluster_sync();
   }
   int64_t done = 0;
-  for (int64_t from = 0; from < p.num_pages; from += 32 * most) {
+  // (one window at least: the table is looked at where there are no pages, too)
+  for (int64_t from = 0; from == 0 || from < p.num_pages; from += 32 * most) {
     const Window x = words ? marked(words, p.num_pages, most, s_words, s_warp, rank)
                            : mark(p.t, p.seq_lens, p.num_pages, static_cast<int>(from), most, s_words, s_warp, rank, from == 0);
     write_ids(
@@ -460,7 +461,7 @@ __global__ void __launch_bounds__(kThreads, 1) compact_pages_kernel(CompactArgs 
   const bool once = p.num_pages <= 32 * most;
   Window x{};
   int64_t set = 0;
-  for (int64_t from = 0; from < p.num_pages; from += 32 * most) {
+  for (int64_t from = 0; from == 0 || from < p.num_pages; from += 32 * most) {
     x = words ? marked(words, p.num_pages, most, s_words, s_warp, rank)
               : mark(p.t, p.seq_lens, p.num_pages, static_cast<int>(from), most, s_words, s_warp, rank, from == 0);
     set += x.set;
@@ -470,7 +471,7 @@ __global__ void __launch_bounds__(kThreads, 1) compact_pages_kernel(CompactArgs 
   // bits of a word whose first id is `id` that lie below it
   const auto below = [&](int id) { return used - id >= 32 ? ~0u : used <= id ? 0u : (1u << (used - id)) - 1; };
   int64_t ones = 0, stay = 0, holes = 0;    // set before the window; set below `used`, and clear, as far as the windows went
-  for (int64_t from = 0; from < p.num_pages; from += 32 * most) {
+  for (int64_t from = 0; from == 0 || from < p.num_pages; from += 32 * most) {
     if (!once) x = mark(p.t, p.seq_lens, p.num_pages, static_cast<int>(from), most, s_words, s_warp, rank, false);
     const int in = min(max(used - x.from, 0), x.span);   // ids of the window below `used`
     const int64_t first_hole = holes, first_one = ones;

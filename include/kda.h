@@ -595,6 +595,8 @@ KDA_API int kda_step_tables(int32_t *block_table, int64_t table_row_stride, int 
  * own operations.  Pages in use are those the block table names: there are  *
  * no reference counts, and a call that is run again leaves the same result   *
  * (but for a table that was compacted in place: it is compact then).        *
+ * Lists (forks, rows, copies, groups; a step table's requests) have at most *
+ * 2^31 - 65537 entries.                                                     *
  * ======================================================================== */
 
 /*

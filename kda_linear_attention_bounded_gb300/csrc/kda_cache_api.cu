@@ -214,7 +214,7 @@ int kda_fork_requests(int32_t *block_table, int64_t table_row_stride, int table_
                       size_t workspace_bytes, void *stream) {
   if (int rc = check_workspace(workspace, workspace_bytes)) return rc;
   if (int rc = check_table(block_table, table_row_stride, table_width, seq_lens, B, page_size)) return rc;
-  if (forks < 0 || num_free < 0 || !pages_used || (num_free > 0 && !free_pages)) return KDA_ERR_INVALID_ARG;
+  if (forks < 0 || forks > kda::kMostEntries || num_free < 0 || !pages_used || (num_free > 0 && !free_pages)) return KDA_ERR_INVALID_ARG;
   if (forks > 0 && (!parents || !children || !copy_src || !copy_dst)) return KDA_ERR_INVALID_ARG;
   for (const int32_t *p : {parents, children, free_pages, static_cast<const int32_t *>(copy_src),
                            static_cast<const int32_t *>(copy_dst), static_cast<const int32_t *>(pages_used)})
@@ -244,7 +244,7 @@ int kda_release_requests(const int32_t *block_table, int64_t table_row_stride, i
                          int32_t *num_free, void *workspace, size_t workspace_bytes, void *stream) {
   if (int rc = check_workspace(workspace, workspace_bytes)) return rc;
   if (int rc = check_table(block_table, table_row_stride, table_width, seq_lens, B, page_size)) return rc;
-  if (num_rows < 0 || num_pages < 0 || !num_free || (num_rows > 0 && !rows) || (num_pages > 0 && !free_pages))
+  if (num_rows < 0 || num_rows > kda::kMostEntries || num_pages < 0 || !num_free || (num_rows > 0 && !rows) || (num_pages > 0 && !free_pages))
     return KDA_ERR_INVALID_ARG;
   if (!aligned_to(rows, 4) || !aligned_to(free_pages, 4) || !aligned_to(num_free, 4)) return KDA_ERR_INVALID_ARG;
   const Span inputs[] = {table_span(block_table, table_row_stride, table_width, B), ints(rows, num_rows)};
@@ -300,7 +300,7 @@ int kda_compact_pages(const int32_t *block_table, int64_t table_row_stride, int 
 int kda_copy_pages(const kda_page_buffer *buffers, int num_buffers, int num_pages, const int32_t *copy_src,
                    const int32_t *copy_dst, int count, void *workspace, size_t workspace_bytes, void *stream) {
   if (int rc = check_workspace(workspace, workspace_bytes)) return rc;
-  if (num_buffers < 0 || num_pages < 0 || count < 0 || (num_buffers > 0 && !buffers)) return KDA_ERR_INVALID_ARG;
+  if (num_buffers < 0 || num_pages < 0 || count < 0 || count > kda::kMostEntries || (num_buffers > 0 && !buffers)) return KDA_ERR_INVALID_ARG;
   if (count > 0 && (!copy_src || !copy_dst || !aligned_to(copy_src, 4) || !aligned_to(copy_dst, 4))) return KDA_ERR_INVALID_ARG;
   for (int i = 0; i < num_buffers; ++i) {
     const kda_page_buffer &b = buffers[i];
@@ -334,7 +334,7 @@ int kda_shared_prefix_attention(const uint16_t *q, int64_t q_token_stride, const
                                 v_token_stride, v_head_stride, num_pages, page_size, block_table, table_row_stride, table_width,
                                 seq_lens, B, T, Hq, Hk, scale, out, out_token_stride, lse, workspace, workspace_bytes, &p.a))
     return rc;
-  if (num_groups < 0 || !aligned_to(prefix_lens, 4) || !aligned_to(group_starts, 4)) return KDA_ERR_INVALID_ARG;
+  if (num_groups < 0 || num_groups > kda::kMostEntries || !aligned_to(prefix_lens, 4) || !aligned_to(group_starts, 4)) return KDA_ERR_INVALID_ARG;
   if (num_groups > 0 && (!prefix_lens || !group_starts)) return KDA_ERR_INVALID_ARG;
   if (B == 0) return KDA_OK;
   if (workspace_bytes < kda_shared_prefix_workspace_size(B, T, Hq, Hk, num_groups)) return KDA_ERR_WORKSPACE;

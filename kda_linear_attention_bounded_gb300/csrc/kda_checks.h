@@ -24,6 +24,9 @@ inline bool aligned_to(const void *p, uintptr_t n) { return (reinterpret_cast<ui
 
 inline bool good_stride(int64_t stride, int64_t min_elems) { return stride >= min_elems && stride % 8 == 0; }
 
+// Entries at most of a list that a kernel goes through in steps of up to 65536, with 32-bit places.
+constexpr int kMostEntries = 0x7FFFFFFF - 65536;
+
 inline int check_workspace(const void *ws, size_t bytes) {
   if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u) != 0 || bytes < kWorkspaceBytes) return KDA_ERR_WORKSPACE;
   return KDA_OK;

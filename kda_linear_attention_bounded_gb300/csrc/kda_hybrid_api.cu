@@ -227,7 +227,7 @@ int kda_step_tables(int32_t *block_table, int64_t table_row_stride, int table_wi
                     int64_t max_tokens, int32_t *cu_seqlens, int32_t *kv_lens, int32_t *positions, int64_t *slot_map,
                     int32_t *pages_used, void *workspace, size_t workspace_bytes, void *stream) {
   if (int rc = check_workspace(workspace, workspace_bytes)) return rc;
-  if (B < 0 || num_free < 0 || page_size < 1 || max_tokens < 0 || max_tokens > INT_MAX || table_width < 0)
+  if (B < 0 || B > kda::kMostEntries || num_free < 0 || page_size < 1 || max_tokens < 0 || max_tokens > INT_MAX || table_width < 0)
     return KDA_ERR_INVALID_ARG;
   if (B > 0 && (!seq_lens || !new_lens || !kv_lens || (table_width > 0 && !block_table) || table_row_stride < table_width))
     return KDA_ERR_INVALID_ARG;

@@ -63,8 +63,9 @@ bool good_pages(const Pages &p, int num_pages, int page_size, int Hk, Range *rea
   int64_t bytes = 256;
   const auto dim = [&](int64_t stride, int64_t n) {
     if (!good_stride(stride, 0) || (n > 1 && stride < kda::kD)) return false;
-    if (n > 1 && stride > (int64_t(1) << 46) / (n - 1)) return false;   // (behind all memory)
-    if (n > 1) bytes += 2 * stride * (n - 1);
+    int64_t far = 0;
+    if (n > 1 && (__builtin_mul_overflow(stride, n - 1, &far) || far > int64_t(1) << 46)) return false;   // (behind all memory)
+    bytes += 2 * far;
     return true;
   };
   if (!dim(p.page, num_pages) || !dim(p.token, page_size) || !dim(p.head, Hk)) return false;

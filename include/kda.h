@@ -735,7 +735,10 @@ KDA_API int kda_copy_pages(const kda_page_buffer *buffers, int num_buffers, int 
  * prefix is read once for all its requests.  Group g is the requests
  * group_starts[g] .. group_starts[g + 1] - 1, whose first prefix_lens[g] tokens are
  * the same: they are read through the group's first request with a length above 0.
- * Requests in no group attend alone.  The result is that of kda_paged_attention.
+ * Requests in no group attend alone.  The result is that of kda_paged_attention,
+ * but for roundings: a weight is rounded to bf16 where it meets its value, and a
+ * prefix's largest need not be 1 (out is off by up to 2.3e-3 in the norm, where
+ * its own bf16 leaves 1.7e-3).
  *
  *  prefix_lens   [num_groups] int32, >= 0, any length (pages need not end with the
  *                prefix; the requests' own tables hold all of their tokens).  Tokens
@@ -748,7 +751,8 @@ KDA_API int kda_copy_pages(const kda_page_buffer *buffers, int num_buffers, int 
  *
  * Calls that could read less than 160 MB of prefixes again (by B, num_groups and
  * the table's width) let every request attend alone, which is faster there, and
- * do not look at the groups.
+ * do not look at the groups.  The width counts, not the lengths: short requests
+ * are faster in a table (a view of its first columns) that ends with the longest.
  *
  * Device-side findings as in kda_paged_attention; where the groups are looked at,
  * starts that do not ascend or leave 0 .. B, or a negative prefix length, make

@@ -81,7 +81,8 @@ def compact_pages(block_table, seq_lens, page_size, *, new_table, copy_src, copy
 def copy_pages(buffers, copy_src, copy_dst, *, workspace=None, stream=None):
     """``kda_copy_pages``: pages ``copy_src[i]`` -> ``copy_dst[i]`` (int32, a negative one: no copy) of every buffer: a list
     of tensors ``[pages, ...]`` of any types whose pages are contiguous, 16-byte aligned and a multiple of 16 bytes long:
-    the keys and values of every layer, or pools of states and windows."""
+    the keys and values of every layer, or pools of states and windows.  They may be slices of one tensor, but no page of one may
+    meet a page of another."""
     if workspace is None:
         workspace = _workspace(None, copy_src, "copy_src", stream)
     _done(_h._ext.copy_pages(buffers, copy_src, copy_dst, workspace, _raw(stream, copy_src)), "kda_copy_pages")

@@ -1,4 +1,4 @@
-// Host-side argument checks shared by the entry points (kda_api.cu, kda_hybrid_api.cu).
+// Host-side argument checks shared by the entry points (kda_api.cu, kda_hybrid_api.cu, kda_cache_api.cu).
 #pragma once
 
 #include <stddef.h>

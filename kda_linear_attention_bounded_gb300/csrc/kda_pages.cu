@@ -17,7 +17,9 @@
 // read them; where requests end, all SMs write the list, too.  Bound by the latency of four launches in a row, and by the atomics.
 //
 // Copying.  Bound by HBM.  Every CTA lists the pairs of a window that are copies; pieces of 8 KB of them all stand in one line, of
-// which each warp takes every so-manieth.
+// which each warp takes every so-manieth.  (Read and written, of 0.5 GB: pages of 1 MB 6170 GB/s, of 8 KB 5550, of 12 KB, whose last
+// pieces are a plain loop's, 4860, of 4 KB 4370.)  A list is gone through by every CTA, what is no copy, too: ten copies in one of
+// 100000 entries take 182 us, in one of 450000 827.
 #include <algorithm>
 #include <type_traits>
 

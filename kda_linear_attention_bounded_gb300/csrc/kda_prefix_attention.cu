@@ -13,11 +13,15 @@
 // threads with half a row each, against tiles of 128 tokens, or 128 rows (where there are no more) of which the groups take the
 // tiles in turn.  So either way a step is two S = Q K^T and two O += P V of 128 x 128 x 128, and while one group turns its S into P the tensor
 // cores work for the other: with P written over S in TMEM (S, O: 4 x 128 columns) nothing of them passes through shared memory.
-// One warp issues the products, one brings tiles (K and V in turn, five of 32 KB, TMA boxes of as many rows as the page's size has
-// powers of two, 8 to 64; pages without a factor of 8: asynchronous copies by two warps).  Steps of all blocks stand in one line of
+// Two warps issue the products, one for each group, which hand the turn to each other; two bring tiles, one the keys and one the
+// values (K and V in turn, five of 32 KB, TMA boxes of as many rows as the page's size has powers of two, 8 to 64; pages without a
+// factor of 8: asynchronous copies by the same two).  Steps of all blocks stand in one line of
 // which each CTA takes an equal stretch; a stretch's part of a block is one piece.
 // Weights are relative to a maximum that follows the scores only when 64 weights' sum says that it is far too low (2^14): then O and l
 // are multiplied, which after the first tiles hardly ever happens; a weight of 2^14 is rounded to bf16 as exactly as one below 1.
+// That rounding is the tensor cores' price (both operands of a product have one type, and V is the caller's bf16): independent of the
+// output's own, it is as large (1.65e-3 in the norm), so a row whose weight is spread is off by 2.3e-3.  m, l and O are fp32, and l
+// and lse sum the weights as they are before it.
 #include <cuda.h>
 
 #include <algorithm>
@@ -49,13 +53,13 @@ constexpr uint32_t kSmemBytes = OFF_ABORT + 4 + 1024;
 static_assert(kSmemBytes <= 227 * 1024, "one CTA's shared memory");
 constexpr int kMostCtas = 152;
 constexpr int kCost = 2;                           // units of a block besides its steps': queries and sums
-// Units of a stretch at least: CTAs without one leave their SM to the requests' own tokens.  (64 x 8192: of 1, 3, 4, 6 and 8 units 35.3, 34.2,
-// 29.2, 29.1 and 34 us.)
+// Units of a stretch at least: CTAs without one leave their SM to the requests' own tokens.  (64 x 8192, with the share below: of 1, 2, 3, 4, 6
+// and 8 units 33.9, 33.8, 34.0, 33.6, 31.3 and 36.6 us; 7 groups x 4 and 192 x 40000 the same with all of them.)
 constexpr int kLeastUnits = 4;
 // What the requests' own tokens cost on an SM, in units of the prefixes' line: a tile of 64 tokens of a key head, with an item's queries and
 // end as four tiles.  As many SMs as their share of the work are theirs from the start: one kernel's start and end lie beside the other's
-// work.  (7 groups x 4 / 192 x 40000: of 0, 0.1, 0.2, 0.3, 0.5 and 0.8 units 67.4, 65.2, 64.5, 65.3, 68.5, 74.6 / 121.7, 119.0, 119.3, 119.4,
-// 123.7, 131.7 us.)
+// work.  (7 groups x 4 / 192 x 40000: of 0, 0.1, 0.2, 0.3 and 0.5 units 68.7, 65.9, 65.3, 66.7, 70.2 / 121.4, 119.3, 120.1, 122.7, 126.0 us; 64 x
+// 8192 33.3 to 33.8 with all of them.)
 constexpr int kOwnTile = 64, kOwnCost = 4;
 constexpr float kOwnUnits = 0.2f;
 constexpr int kPieceFloats = 136;                  // a row of a piece: 128 sums, the maximum, the sum of weights, padding to 32 bytes
@@ -878,9 +882,12 @@ __global__ void __launch_bounds__(kJoinThreads, 3) shared_prefix_join_kernel(Pre
 }
 
 // Bytes of prefixes that requests could read again, from which on they are shared.  The table's width bounds them; the host knows
-// no lengths.  Measured, alone against shared (one group, own tokens to 200): 16 requests x 4096 tokens (64 MB) 17.7 and 26.5 us, 16 x
-// 16384 (122 MB) 23.4 and 27.1, 64 x 4096 (134 MB) 24.3 and 26.3, 4 x 16384 (195 MB) 36 and 27, 16 x 16384 (244 MB) 36 and 28, 64 x
-// 16384 (1 GB) 111 and 30; more requests with shorter prefixes cross later (192 x 1024, 239 MB: 35 and 28; 192 x 256, 382 MB: 49 and 56).
+// no lengths.  Measured, alone against shared (one group, own tokens to 200, tables to the longest request when alone; h: key heads): 16
+// requests x 4096 tokens (2 h, 64 MB) 17.6 and 24.5 us, 192 x 256 (2 h, 96 MB) 20.6 and 28.2, 16 x 16384 (1 h, 122 MB) 23.4 and 25.3, 64 x 256 (8 h,
+// 126 MB) 22.3 and 28.5, 64 x 4096 (1 h, 134 MB) 24.2 and 25.0; 4 x 16384 (8 h, 195 MB) 35.9 and 25.7, 16 x 16384 (2 h, 244 MB) 36.0 and 26.3, 192 x 1024
+// (2 h, 239 MB) 34.4 and 29.9, 64 x 16384 (2 h, 1 GB) 111 and 34; where many requests share little, sharing loses beyond it, too (192 x 256, 8 h,
+// 382 MB: 49.1 and 55.7).  A table wider than the requests counts as wide as it is: 4 x 500 tokens (2 h) take 8.2 us in a table of their length
+// and 20.9 in one for 131072 tokens, 16 x 4096 17.3 and 24.8, 192 x 256 20.8 and 29.7, 64 x 4096 26.3 and 26.5.
 constexpr int64_t kLeastAgain = 160 << 20;
 
 }  // namespace
